@@ -31,6 +31,9 @@ __all__ = [
     "EBC_MAX_CHUNKS", "ebc_compress_chunked_bound", "ebc_compress_chunked", "ebc_compress_chunked_bf16",
     "ebc_decompress_chunked", "EBC_RADIUS", "EBC_RADIUS_WIDE", "ebc_set_radius", "ebc_compress_bound_radius",
     "ebc_decompress_columns", "EbcConfig", "ebc_set_first_wait_polls",
+    "EBC_MAX_EXPERTS", "EBC_F32", "EBC_BF16", "EBC_F16", "ebc_moe_plan", "ebc_moe_dispatch", "ebc_moe_combine",
+    "ebc_moe_combine_grad", "ebc_mx4_quantize", "ebc_mx4_dequantize", "ebc_moe_dispatch_mx4", "ebc_mx4_product",
+    "Experts", "Plan", "Mx4",
 ]
 
 EBC_OK, EBC_ERR_INVALID_ARG, EBC_ERR_CAPACITY, EBC_ERR_CORRUPT = 0, 1, 2, 3
@@ -38,6 +41,8 @@ EBC_ERR_DEVICE_TIMEOUT, EBC_ERR_CUDA, EBC_ERR_NO_DEVICE, EBC_ERR_INTERNAL = 4, 5
 EBC_ERR_SCRATCH_LIMIT = 8
 EBC_MAX_CHUNKS = 256
 EBC_RADIUS, EBC_RADIUS_WIDE = 128, 512
+EBC_MAX_EXPERTS = 1024
+EBC_F32, EBC_BF16, EBC_F16 = 0, 1, 2
 EBC_MODE_DEDUP_HUFFMAN, EBC_MODE_HUFFMAN, EBC_MODE_DEDUP_RAW, EBC_MODE_RAW = 0, 1, 2, 3
 EBC_DECAY_NONE, EBC_DECAY_LINEAR, EBC_DECAY_STEPWISE, EBC_DECAY_DROP, EBC_DECAY_LOG = 0, 1, 2, 3, 4
 DECAY = {"none": 0, "linear": 1, "stepwise": 2, "drop": 3, "log": 4}
@@ -50,6 +55,8 @@ EXPORTED_SYMBOLS = (
     "ebc_select_modes", "ebc_select_table_modes", "ebc_table_homo_index", "ebc_set_window", "ebc_compress_bf16",
     "ebc_compress_chunked_bound", "ebc_compress_chunked", "ebc_compress_chunked_bf16", "ebc_decompress_chunked",
     "ebc_set_radius", "ebc_compress_bound_radius", "ebc_decompress_columns", "ebc_set_first_wait_polls",
+    "ebc_moe_plan", "ebc_moe_dispatch", "ebc_moe_combine", "ebc_moe_combine_grad", "ebc_mx4_quantize",
+    "ebc_mx4_dequantize", "ebc_moe_dispatch_mx4", "ebc_mx4_product",
 )
 
 
@@ -139,6 +146,14 @@ def lib():
                 "ebc_compress_chunked": (I, [P, P, I64, I, I, P, I, P, U64, P, P]),
                 "ebc_compress_chunked_bf16": (I, [P, P, I64, I, I, P, I, P, U64, P, P]),
                 "ebc_decompress_chunked": (I, [P, P, U64, P, I, P, I64, I, I, P]),
+                "ebc_moe_plan": (I, [P, P, I, I64, I, I, P, P, P, P]),
+                "ebc_moe_dispatch": (I, [P, P, I64, I, I64, I, I64, P, P, I, P, P]),
+                "ebc_moe_combine": (I, [P, P, I64, I, I64, I, I64, P, P, P, P]),
+                "ebc_moe_combine_grad": (I, [P, P, I64, P, I64, I, I64, I, I64, P, P, I, P, P, P, P]),
+                "ebc_mx4_quantize": (I, [P, P, I64, I, I64, I64, P, P, P]),
+                "ebc_mx4_dequantize": (I, [P, P, P, I64, I64, I, P, P]),
+                "ebc_moe_dispatch_mx4": (I, [P, P, I64, I, I64, I, I64, P, P, I, P, P, P]),
+                "ebc_mx4_product": (I, [P, P, P, I64, I64, P, P, I64, I, P, I, P, P]),
             }
             for name, (res, args) in sig.items():
                 f = getattr(L, name)
@@ -309,6 +324,40 @@ def ebc_get_profile(ctx, capacity: int = 32):
     return {arr[i].name.decode(): (int(arr[i].launches), float(arr[i].total_ms)) for i in range(n.value)}
 
 
+# The expert-parallel and 4-bit calls take their arguments in the C order, as
+# plain ints and pointers (ctypes checks them).
+def ebc_moe_plan(*args) -> int:
+    return lib().ebc_moe_plan(*args)
+
+
+def ebc_moe_dispatch(*args) -> int:
+    return lib().ebc_moe_dispatch(*args)
+
+
+def ebc_moe_combine(*args) -> int:
+    return lib().ebc_moe_combine(*args)
+
+
+def ebc_moe_combine_grad(*args) -> int:
+    return lib().ebc_moe_combine_grad(*args)
+
+
+def ebc_mx4_quantize(*args) -> int:
+    return lib().ebc_mx4_quantize(*args)
+
+
+def ebc_mx4_dequantize(*args) -> int:
+    return lib().ebc_mx4_dequantize(*args)
+
+
+def ebc_moe_dispatch_mx4(*args) -> int:
+    return lib().ebc_moe_dispatch_mx4(*args)
+
+
+def ebc_mx4_product(*args) -> int:
+    return lib().ebc_mx4_product(*args)
+
+
 # ---- torch-facing convenience layer (marshalling only) ----
 def _ptr(t):
     return ctypes.c_void_p(t.data_ptr()) if t is not None else None
@@ -327,6 +376,14 @@ def _f32_host(arr, T):
     if a.size != T:
         raise ValueError(f"expected {T} bounds, got {a.size}")
     return a
+
+
+def __getattr__(name):
+    # the operators on torch tensors; torch is imported with them, not with the package
+    if name in ("Experts", "Plan", "Mx4"):
+        from . import experts
+        return getattr(experts, name)
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
 
 
 class Codec:

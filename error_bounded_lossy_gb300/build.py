@@ -16,8 +16,9 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libebc_gb300.so")
-SOURCES = ["ebc_api.cu", "ebc_compress.cu", "ebc_decompress.cu"]
-HEADERS = ["ebc_internal.cuh", os.path.join("..", "..", "include", "ebc.h")]
+SOURCES = ["ebc_api.cu", "ebc_compress.cu", "ebc_decompress.cu", "ebc_experts.cu", "ebc_mx4.cu",
+           "ebc_mx4_product.cu"]
+HEADERS = ["ebc_internal.cuh", "ebc_types.cuh", "ebc_mx4.cuh", os.path.join("..", "..", "include", "ebc.h")]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-ffp-contract=off,-O2",

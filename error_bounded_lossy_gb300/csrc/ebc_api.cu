@@ -219,6 +219,16 @@ static int grow(void** buf, size_t* have, size_t need) {
   return EBC_OK;
 }
 
+int ebc::begin_call(ebc_ctx* c, cudaStream_t st, CallView* out) {
+  if (!c) return EBC_ERR_INVALID_ARG;
+  if (cudaSetDevice(c->device) != cudaSuccess) return EBC_ERR_CUDA;
+  c->last_stream = st;
+  out->nsm = c->nsm;
+  out->glob = c->glob;
+  out->prof = c->prof;
+  return EBC_OK;
+}
+
 // ---------------------------------------------------------------------------
 // C ABI
 // ---------------------------------------------------------------------------

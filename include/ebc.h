@@ -403,6 +403,122 @@ int ebc_table_homo_index(ebc_ctx* ctx, const float* d_x, int64_t B, int T, int D
 int ebc_decompress_noalloc(const void* d_in, uint64_t in_bytes, float* d_xhat, int64_t B, int T, int D,
                            void* stream);
 
+/* ---- Expert parallelism: tokens sorted by expert and back ----
+ *
+ * The all-to-all of a mixture of experts has the same place in a step as the
+ * embedding exchange ([EBLC] §III-A, stages 1 to 4): each rank sorts its
+ * tokens' rows by the expert that its router chose into one sending buffer,
+ * sends every rank the rows of that rank's experts (a contiguous piece, which
+ * ebc_compress takes as [rows, T, D] with T * D = the row's width, or which
+ * goes out in 4 bits), and on the way back sums each token's rows with the
+ * router's weights.  These calls make the buffer, the sum, and the gradients
+ * of both.
+ *
+ * A batch has `tokens` tokens of `top` choices each; choice j of token t is
+ * slot s = t * top + j.  n = tokens * top slots, n <= 2^31 - 1; experts are
+ * numbered 0 .. n_experts - 1, 1 <= n_experts <= EBC_MAX_EXPERTS, and top is
+ * at most EBC_MAX_EXPERTS.
+ *
+ * All pointers named d_ are device memory owned by the caller and aligned to
+ * their elements; a row of `width` elements is contiguous, and ld_ arguments
+ * are the elements between the starts of two rows of an input (>= width);
+ * outputs are dense.  Row addresses that are all multiples of 16 bytes are
+ * the fast case.  The calls are asynchronous on `stream`, take no scratch,
+ * and give the same bits in every run.  They return EBC_ERR_INVALID_ARG for
+ * bad shapes, types or pointers before any device work; an entry of a plan
+ * that points outside its buffer is skipped, and recorded as
+ * EBC_ERR_INVALID_ARG for ebc_last_device_error. */
+#define EBC_MAX_EXPERTS 1024
+
+/* Element types of these calls. */
+typedef enum {
+  EBC_F32 = 0,
+  EBC_BF16 = 1,
+  EBC_F16 = 2
+} ebc_type;
+
+/* The plan of a routed batch: slots sorted by expert, slots of one expert in
+ * ascending order.  d_ids[n] (id_bytes 4: int32, 8: int64): the experts; a
+ * negative id drops its slot; so does an id >= n_experts, which also records
+ * EBC_ERR_INVALID_ARG.  Writes
+ *   d_rows[n]                  the slot of each sorted row, -1 past the last
+ *   d_place[n]                 the row of each slot, -1 for a dropped one
+ *   d_offsets[n_experts + 1]   rows of expert e: [offsets[e], offsets[e+1]) */
+int ebc_moe_plan(ebc_ctx* ctx, const void* d_ids, int id_bytes, int64_t tokens, int top, int n_experts,
+                 int32_t* d_rows, int32_t* d_place, int32_t* d_offsets, void* stream);
+
+/* d_xs[place[t, j]] = d_x[t] for every kept slot; rows from offsets[n_experts]
+ * to n are zero.  d_x[tokens][width], d_xs[n][width] of `type`. */
+int ebc_moe_dispatch(ebc_ctx* ctx, const void* d_x, int64_t ld_x, int type, int64_t tokens, int top, int64_t width,
+                     const int32_t* d_place, const int32_t* d_offsets, int n_experts, void* d_xs, void* stream);
+
+/* d_y[t] = sum over j of d_weights[t, j] * d_ys[place[t, j]] over the kept
+ * slots, in fp32 and in the order of j, rounded once to `type`; a token with
+ * no kept slot is zero, and nothing of a dropped slot is read.  d_ys[n][width],
+ * d_weights fp32 [tokens][top].  With d_weights = NULL every weight is 1: the
+ * gradient of ebc_moe_dispatch, with d_ys the gradient of its rows. */
+int ebc_moe_combine(ebc_ctx* ctx, const void* d_ys, int64_t ld_ys, int type, int64_t tokens, int top, int64_t width,
+                    const int32_t* d_place, const float* d_weights, void* d_y, void* stream);
+
+/* The gradients of ebc_moe_combine for the gradient d_dy[tokens][width] of its
+ * result: d_dys[place[t, j]] = d_weights[t, j] * d_dy[t] (rows past the last
+ * expert's are zero), and d_dweights[t, j] = <d_dy[t], d_ys[place[t, j]]> in
+ * fp32 (0 for a dropped slot). */
+int ebc_moe_combine_grad(ebc_ctx* ctx, const void* d_dy, int64_t ld_dy, const void* d_ys, int64_t ld_ys, int type,
+                         int64_t tokens, int top, int64_t width, const int32_t* d_place, const int32_t* d_offsets,
+                         int n_experts, const float* d_weights, void* d_dys, float* d_dweights, void* stream);
+
+/* ---- 4-bit microscaled values ----
+ *
+ * The fixed-rate lossy form next to the containers: 4.25 bits a value, with an
+ * error bound that each block states.  A row is cut into blocks of 32 values
+ * (the last one filled up with zeros).  A block has the scale X = 2^e, e the
+ * least integer >= -127 with max |x| <= 6 X, kept as the byte e + 127; each
+ * value is kept as the nearest of X * {0, 1/2, 1, 3/2, 2, 3, 4, 6} and its
+ * sign, ties to the even code, in 4 bits (sign, 2 exponent bits, 1 fraction
+ * bit).  No value saturates, so |x - xhat| <= X/4 for |x| <= 2X, X/2 for
+ * |x| <= 4X, and X always.  (The open microscaling formats' MXFP4 elements and
+ * scales; their suggested scale rule, which takes e one lower for max |x| in
+ * (6 X, 8 X), would break the bound.)  A block that holds a NaN or an infinity
+ * gets the byte 255 and reads back as NaN.
+ *
+ * Layout, dense and row-major: codes, EBC_MX4_CODE_BYTES(width) bytes a row,
+ * value 2i in the low half of byte i; scales, EBC_MX4_SCALE_BYTES(width) bytes
+ * a row, one a block, filled up with zeros.  Both arrays are 16-byte
+ * aligned.  1 <= width <= 2^24. */
+#define EBC_MX4_BLOCK 32
+#define EBC_MX4_CODE_BYTES(width) ((((width) + 31) / 32) * 16)
+#define EBC_MX4_SCALE_BYTES(width) ((((width) + 511) / 512) * 16)
+
+/* d_x[rows][width] of `type` to 4 bits. */
+int ebc_mx4_quantize(ebc_ctx* ctx, const void* d_x, int64_t ld_x, int type, int64_t rows, int64_t width,
+                     uint8_t* d_codes, uint8_t* d_scales, void* stream);
+
+/* The values of d_codes and d_scales as `type`, into d_xhat[rows][width]
+ * (exact in fp32 and bf16; rounded to nearest in fp16, whose range is
+ * smaller). */
+int ebc_mx4_dequantize(ebc_ctx* ctx, const uint8_t* d_codes, const uint8_t* d_scales, int64_t rows, int64_t width,
+                       int type, void* d_xhat, void* stream);
+
+/* ebc_moe_dispatch with the rows quantized on the way: n rows of codes and
+ * scales, each token quantized once; rows past the last expert's are zero. */
+int ebc_moe_dispatch_mx4(ebc_ctx* ctx, const void* d_x, int64_t ld_x, int type, int64_t tokens, int top,
+                         int64_t width, const int32_t* d_place, const int32_t* d_offsets, int n_experts,
+                         uint8_t* d_codes, uint8_t* d_scales, void* stream);
+
+/* The experts' products: d_ys[r][o] = sum over k of x[r][k] * w[e][o][k] for
+ * the rows r of expert e, [d_offsets[e], d_offsets[e+1]); rows outside every
+ * expert's are zero.  x: `rows` rows of `width` values in 4 bits, w: n_experts
+ * times `outs` rows of `width` values in 4 bits; products are exact and summed
+ * in fp32, and the sum is rounded once to out_type.  Offsets must ascend from
+ * 0 to at most `rows`; others are clamped to that, and recorded as
+ * EBC_ERR_INVALID_ARG.  d_offsets = NULL: one expert takes every row (a plain
+ * matrix product; n_experts must be 1).  rows <= 2^31 - 1,
+ * n_experts * outs <= 2^31 - 1. */
+int ebc_mx4_product(ebc_ctx* ctx, const uint8_t* d_x_codes, const uint8_t* d_x_scales, int64_t rows, int64_t width,
+                    const uint8_t* d_w_codes, const uint8_t* d_w_scales, int64_t outs, int n_experts,
+                    const int32_t* d_offsets, int out_type, void* d_ys, void* stream);
+
 /* Counts of the last compress call of the context, read on `stream` (a
  * cudaStream_t; NULL = the stream of the context's last call) after that call
  * has completed; synchronises both streams.  Returns the recorded device error
