@@ -1,110 +1,495 @@
-// ebc_mx4_product.cu -- the experts' products on 4-bit microscaled operands.
+// ebc_mx4_product.cu -- the experts' products on 4-bit microscaled operands:
+// ys[r] = W[e(r)] x[r], block-scaled fp4 matrix instructions with the
+// accumulator in tensor memory.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
 #include "ebc_mx4.cuh"
 
 using namespace ebc;
 
 namespace {
 
-constexpr int kT = 16;   // rows and outputs of a tile
+// ---- geometry ----
+// A tile is 128 outputs of an expert (the M side: weights, one per tensor
+// memory lane) by kTN of its rows (the N side).  The rows are on the N side
+// because an expert's share of a batch is ragged and often small, and N may be
+// as small as 16 where M is fixed.  A stage holds 256 values of K: 128 bytes a
+// row, one span of the 128-byte swizzle, four matrix instructions of K = 64.
+constexpr int kM = 128;
+constexpr int kStageK = 256;
+constexpr int kRowBytes = kStageK / 2;
+constexpr int kScaleTile = 512;    // bytes of the scales of 128 rows x 4 blocks, as the matrix unit wants them
+constexpr int kThreads = 384;      // warp 0 loads, warp 1 multiplies, warps 4-7 store, warps 8-11 lay out scales
+constexpr int kScaleWarps = 4;
 
-// Offset i >= 1, clamped to the rows and to what ascends; an offset that had to be
-// clamped is the caller's error.
-__device__ __forceinline__ int64_t offset_at(const int32_t* offsets, int i, int64_t floor, int64_t rows, bool* bad) {
-  const int64_t v = offsets ? offsets[i] : rows;
-  const int64_t c = v < floor ? floor : v > rows ? rows : v;
-  if (c != v) *bad = true;
-  return c;
+template <int kTN>
+struct Geom {
+  static constexpr int kScaleB = (kTN + 127) / 128;                       // scale tiles of the rows per 4 blocks
+  static constexpr int kABytes = kM * kRowBytes;
+  static constexpr int kBBytes = kTN * kRowBytes;
+  static constexpr int kScaleBytes = 2 * (1 + kScaleB) * kScaleTile;      // per stage: 8 blocks a row
+  static constexpr int kStages = kTN == 256 ? 4 : kTN == 128 ? 6 : 8;
+  static constexpr int kAcc = kTN == 256 ? 1 : 2;                         // accumulators
+  static constexpr int kScaleCols = 2 * (1 + kScaleB) * 4;                // tensor memory columns per stage
+  static constexpr int kCols = 512;
+  static constexpr size_t kSmem = 1024 + (size_t)kStages * (kABytes + kBBytes + kScaleBytes);
+  static_assert(kAcc * (kTN < 32 ? 32 : kTN) + kStages * kScaleCols <= kCols, "tensor memory");
+  static_assert(kSmem <= 216 * 1024, "shared memory");
+};
+
+// ---- PTX ----
+__device__ __forceinline__ uint32_t smem_u32(const void* p) {
+  return static_cast<uint32_t>(__cvta_generic_to_shared(p));
+}
+__device__ __forceinline__ void mbar_init(uint64_t* bar, uint32_t count) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(count) : "memory");
+}
+__device__ __forceinline__ void mbar_expect_tx(uint64_t* bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(bar)), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ bool mbar_try_wait(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0u;
+}
+__device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map, uint64_t* bar, int c0, int c1) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
+          dst),
+      "l"(map), "r"(c0), "r"(c1), "r"(smem_u32(bar))
+      : "memory");
+}
+__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_commit(uint64_t* bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
+               : "memory");
+}
+// 32 rows x 16 bytes of scales to four columns of each quarter of tensor memory
+__device__ __forceinline__ void tc_copy_scales(uint32_t taddr, uint64_t desc) {
+  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+}
+__device__ __forceinline__ void tc_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sa, uint32_t sb,
+                                       uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.u32 p, %6, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void tc_load16(uint32_t taddr, uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+      "%15}, [%16];"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
+        "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tc_load_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+
+// Shared-memory operand descriptor: rows of 128 bytes in the 128-byte swizzle,
+// eight-row groups 1024 bytes apart.
+__device__ __forceinline__ uint64_t operand_desc(uint32_t addr) {
+  return (uint64_t)((addr >> 4) & 0x3FFFu) | (1ull << 16) | (64ull << 32) | (1ull << 46) | (2ull << 61);
+}
+// Scales: no swizzle, eight-row groups of 16-byte rows 128 bytes apart.
+__device__ __forceinline__ uint64_t scale_desc(uint32_t addr) {
+  return (uint64_t)((addr >> 4) & 0x3FFFu) | (1ull << 16) | (8ull << 32) | (1ull << 46);
+}
+// Instruction descriptor: both operands E2M1 along K, scales UE8M0, M = 128,
+// N = n; `id` (0 or 2) is the byte of a scale word where the instruction's two
+// blocks start.
+__host__ __device__ constexpr uint32_t instr_desc(int n, int id) {
+  return (1u << 7) | (1u << 10) | ((uint32_t)(n >> 3) << 17) | (1u << 23) | ((uint32_t)(kM >> 4) << 24) |
+         ((uint32_t)id << 4) | ((uint32_t)id << 29);
 }
 
-// The plain kernel: a CTA takes 16 rows of one expert and 16 outputs; both
-// blocks of 32 values a row go through shared memory as fp32 values, and a
-// thread sums its output in fp32.  Tiles past the last expert's rows write
-// zeros.
+struct Args {
+  const uint8_t* xs;        // scales of the rows
+  const uint8_t* ws;        // scales of the weights
+  const int32_t* offsets;   // null: one expert takes every row
+  void* ys;
+  Glob* glob;
+  int64_t rows, outs, scale_bytes;
+  int out_type, blocks, experts;   // blocks: scale blocks a row
+};
+
+// A wait that gives up: after kWaitLimit polls, or once another thread of the
+// CTA did.  The first to give up records the time-out.
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile int* abort, Glob* glob) {
+  for (int i = 0; i < kWaitLimit; ++i) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if (*abort) return false;
+  }
+  *abort = 1;
+  record_error(glob, EBC_ERR_DEVICE_TIMEOUT);
+  return false;
+}
+
+// Sixteen rows' values of one output a lane, to memory: a warp writes 32
+// consecutive outputs of a row.
 template <typename T>
-__global__ void __launch_bounds__(kT* kT) k_mx4_product(const uint8_t* __restrict__ xc, const uint8_t* __restrict__ xs,
-                                                        int64_t rows, int64_t width, const uint8_t* __restrict__ wc,
-                                                        const uint8_t* __restrict__ ws, int64_t outs, int E,
-                                                        const int32_t* __restrict__ offsets, T* __restrict__ ys,
-                                                        Glob* glob) {
+__device__ __forceinline__ void store16(T* y, int64_t ld, const uint32_t (&v)[16], int count, bool mine) {
+#pragma unroll
+  for (int c = 0; c < 16; ++c)
+    if (mine && c < count) y[c * ld] = from_f32<T>(__uint_as_float(v[c]));
+}
+
+// One persistent CTA an SM walks tiles blockIdx.x, + gridDim.x, ...; outputs
+// of a run of rows come one after the other, so that the CTAs working at the
+// same time share both operands in L2.
+//   warp 0      brings the codes of both operands in by TMA, a ring of stages
+//   warps 8-11  lay the scales out: the matrix unit reads the scales of 128
+//               rows x 4 blocks from tensor memory as 32 lanes x 4 words,
+//               row r in lane r % 32, word r / 32, so a row's four scale bytes
+//               are one 4-byte store.  Rows and blocks past the end get 1.
+//   warp 1      copies a stage's scales to tensor memory and issues its matrix
+//               instructions; each stage has its own scale columns, so they
+//               are written again only after the stage was given back
+//   warps 4-7   read the accumulator, round once, and store
+// Every wait is bounded (see wait()); a CTA that gives up waits for the copies
+// and instructions it has in flight, frees its tensor memory and returns.
+template <int kTN>
+__global__ void __launch_bounds__(kThreads, 1) k_mx4_product(const __grid_constant__ CUtensorMap wmap,
+                                                             const __grid_constant__ CUtensorMap xmap, Args a) {
+  using G = Geom<kTN>;
+  extern __shared__ uint8_t raw[];
+  __shared__ uint64_t full[G::kStages], scaled[G::kStages], empty[G::kStages];
+  __shared__ uint64_t acc_full[G::kAcc], acc_empty[G::kAcc], drained;
+  __shared__ uint32_t s_tmem;
+  __shared__ int s_abort;
+  __shared__ int s_begin[EBC_MAX_EXPERTS + 1];   // first row of each expert
+  __shared__ int s_tiles[EBC_MAX_EXPERTS + 1];   // runs of kTN rows of the experts before
+  const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
+  uint8_t* base = raw + (1024 - (smem_u32(raw) & 1023)) % 1024;
+  uint8_t* sA = base;
+  uint8_t* sB = sA + G::kStages * G::kABytes;
+  uint8_t* sS = sB + G::kStages * G::kBBytes;
+
+  if (w == 0 && lane == 0) {
+    for (int i = 0; i < G::kStages; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&scaled[i], kScaleWarps);
+      mbar_init(&empty[i], 1);
+    }
+    for (int i = 0; i < G::kAcc; ++i) {
+      mbar_init(&acc_full[i], 1);
+      mbar_init(&acc_empty[i], 4);
+    }
+    mbar_init(&drained, 1);
+    s_abort = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (w == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&s_tmem)),
+                 "r"(G::kCols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    tc_fence_before();
+  }
   pdl_enter();
-  __shared__ float sx[kT][33], sw[kT][33];
-  __shared__ int64_t s_r0, s_r1;
-  __shared__ int s_e;
-  const int tid = threadIdx.x;
-  const int64_t out_tiles = (outs + kT - 1) / kT, out0 = blockIdx.x % out_tiles * kT;
-  if (tid == 0) {
-    // the tile-th run of 16 rows, counted expert by expert; then the rows
-    // that no expert has
-    int64_t tile = blockIdx.x / out_tiles, begin = 0;
-    bool bad = false;
-    s_e = -2;
-    if (offsets && offsets[0] != 0) bad = true;
-    for (int e = 0; e < E; ++e) {
-      const int64_t end = offset_at(offsets, e + 1, begin, rows, &bad);
-      const int64_t tiles = (end - begin + kT - 1) / kT;
-      if (s_e == -2 && tile < tiles) {
-        s_e = e;
-        s_r0 = begin + tile * kT;
-        s_r1 = s_r0 + kT < end ? s_r0 + kT : end;
+  if (w == 2) {
+    // the experts' segments, made to ascend inside the rows, and their runs
+    bool bad = a.offsets && lane == 0 && a.offsets[0] != 0;
+    int before = 0, tiles = 0;
+    if (lane == 0) s_begin[0] = s_tiles[0] = 0;
+    for (int e0 = 0; e0 < a.experts; e0 += 32) {
+      const int e = e0 + lane;
+      int end = 0;
+      if (e < a.experts) {
+        const int v = a.offsets ? a.offsets[e + 1] : (int)a.rows;
+        end = v < 0 ? 0 : v > a.rows ? (int)a.rows : v;
+        bad |= end != v;
       }
-      if (s_e == -2) tile -= tiles;
-      begin = end;
+      int top = end > before ? end : before;
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, top, off);
+        if (lane >= off && v > top) top = v;
+      }
+      bad |= e < a.experts && top != end;
+      int prev = __shfl_up_sync(0xffffffffu, top, 1);
+      if (lane == 0) prev = before;
+      int run = (top - prev + kTN - 1) / kTN;
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, run, off);
+        if (lane >= off) run += v;
+      }
+      if (e < a.experts) {
+        s_begin[e + 1] = top;
+        s_tiles[e + 1] = tiles + run;
+      }
+      before = __shfl_sync(0xffffffffu, top, 31);
+      tiles += __shfl_sync(0xffffffffu, run, 31);
     }
-    if (s_e == -2 && begin + tile * kT < rows) {
-      s_e = -1;
-      s_r0 = begin + tile * kT;
-      s_r1 = s_r0 + kT < rows ? s_r0 + kT : rows;
-    }
-    if (bad) record_error(glob, EBC_ERR_INVALID_ARG);
+    if (bad && blockIdx.x == 0) record_error(a.glob, EBC_ERR_INVALID_ARG);
   }
   __syncthreads();
-  const int e = s_e;
-  if (e == -2) return;
-  const int64_t cb = EBC_MX4_CODE_BYTES(width), sb = EBC_MX4_SCALE_BYTES(width), blocks = (width + 31) / 32;
-  const int i = tid / kT, o = tid % kT;
-  const int64_t r = s_r0 + i, out = out0 + o;
-  float acc = 0.f;
-  if (e >= 0) {
-    for (int64_t b = 0; b < blocks; ++b) {
-      // thread (i, o) decodes byte o of row i's block, and of output i's
-      const int64_t wi = out0 + i;
-      float2 x2 = make_float2(0.f, 0.f), w2 = x2;
-      if (r < s_r1) {
-        x2 = __half22float2(mx4_values(xc[r * cb + b * 16 + o]));
-        const float unit = mx4_unit(xs[r * sb + b]);
-        x2.x *= unit;
-        x2.y *= unit;
+  tc_fence_after();
+  const uint32_t tmem = s_tmem;
+  const uint32_t tmem_scales = tmem + G::kAcc * (kTN < 32 ? 32 : kTN);
+  const int out_tiles = (int)((a.outs + kM - 1) / kM);
+  const int64_t n_tiles = (int64_t)s_tiles[a.experts] * out_tiles;
+  const int stages = (a.blocks + 7) / 8;   // stages of a tile
+
+  // tile -> expert, its first output, first row and row count
+  auto locate = [&](int64_t tile, int* e, int* out0, int* row0, int* count) {
+    const int run = (int)(tile / out_tiles);
+    *out0 = (int)(tile - (int64_t)run * out_tiles) * kM;
+    int lo = 0, hi = a.experts;   // s_tiles[lo] <= run < s_tiles[hi]
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (s_tiles[mid] <= run) lo = mid; else hi = mid;
+    }
+    *e = lo;
+    *row0 = s_begin[lo] + (run - s_tiles[lo]) * kTN;
+    const int left = s_begin[lo + 1] - *row0;
+    *count = left < kTN ? left : kTN;
+  };
+
+  uint32_t issued = 0;   // stages that warp 0 has asked for
+  if (w == 0) {
+    if (lane == 0) {
+      bool ok = true;
+      for (int64_t tile = blockIdx.x; ok && tile < n_tiles; tile += gridDim.x) {
+        int e, out0, row0, count;
+        locate(tile, &e, &out0, &row0, &count);
+        for (int k = 0; k < stages; ++k) {
+          const int s = issued % G::kStages;
+          if (!wait(&empty[s], ((issued / G::kStages) & 1) ^ 1, &s_abort, a.glob)) {
+            ok = false;
+            break;
+          }
+          mbar_expect_tx(&full[s], G::kABytes + G::kBBytes);
+          tma_load_2d(smem_u32(sA + s * G::kABytes), &wmap, &full[s], k * kRowBytes, (int)(e * a.outs) + out0);
+          tma_load_2d(smem_u32(sB + s * G::kBBytes), &xmap, &full[s], k * kRowBytes, row0);
+          ++issued;
+        }
       }
-      if (wi < outs) {
-        const int64_t row = (int64_t)e * outs + wi;
-        w2 = __half22float2(mx4_values(wc[row * cb + b * 16 + o]));
-        const float unit = mx4_unit(ws[row * sb + b]);
-        w2.x *= unit;
-        w2.y *= unit;
-      }
-      __syncthreads();
-      sx[i][2 * o] = x2.x;
-      sx[i][2 * o + 1] = x2.y;
-      sw[i][2 * o] = w2.x;
-      sw[i][2 * o + 1] = w2.y;
-      __syncthreads();
+      // every stage given back: no arrival is left on its way to this CTA's barriers
+      for (uint32_t i = issued > G::kStages ? issued - G::kStages : 0; ok && i < issued; ++i)
+        ok = wait(&empty[i % G::kStages], (i / G::kStages) & 1, &s_abort, a.glob);
+    }
+    __syncwarp();
+  } else if (w == 1) {
+    if (lane == 0) {
+      uint32_t it = 0, n_acc = 0;
+      bool ok = true;
+      for (int64_t tile = blockIdx.x; ok && tile < n_tiles; tile += gridDim.x, ++n_acc) {
+        const int buf = n_acc % G::kAcc;
+        if (!wait(&acc_empty[buf], ((n_acc / G::kAcc) & 1) ^ 1, &s_abort, a.glob)) break;
+        tc_fence_after();
+        const uint32_t d = tmem + buf * kTN;
+        for (int k = 0; k < stages; ++k, ++it) {
+          const int s = it % G::kStages;
+          const uint32_t parity = (it / G::kStages) & 1;
+          if (!wait(&full[s], parity, &s_abort, a.glob) || !wait(&scaled[s], parity, &s_abort, a.glob)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t sc = smem_u32(sS + s * G::kScaleBytes);
+          const uint32_t ta = tmem_scales + s * G::kScaleCols, tb = ta + 8;
 #pragma unroll
-      for (int k = 0; k < 32; ++k) acc = fmaf(sx[i][k], sw[o][k], acc);
+          for (int q = 0; q < 2; ++q) {
+            tc_copy_scales(ta + 4 * q, scale_desc(sc + q * kScaleTile));
+#pragma unroll
+            for (int j = 0; j < G::kScaleB; ++j)
+              tc_copy_scales(tb + 4 * (q * G::kScaleB + j), scale_desc(sc + (2 + q * G::kScaleB + j) * kScaleTile));
+          }
+          const int left = a.blocks - k * 8;   // scale blocks from here on
+          const uint64_t da = operand_desc(smem_u32(sA + s * G::kABytes));
+          const uint64_t db = operand_desc(smem_u32(sB + s * G::kBBytes));
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            if (2 * q < left)
+              tc_mma(d, da + 2 * q, db + 2 * q, instr_desc(kTN, (q & 1) * 2), ta + 4 * (q >> 1),
+                     tb + 4 * G::kScaleB * (q >> 1), k > 0 || q > 0);
+          tc_commit(&empty[s]);
+        }
+        if (ok) tc_commit(&acc_full[buf]);
+      }
+    }
+    __syncwarp();
+  } else if (w >= 8) {
+    // 16 scale bytes a row (512 values, two stages) at a time; the next 16 are
+    // on their way while these are stored
+    const int t = tid - 256;
+    uint32_t it = 0;
+    bool ok = true;
+    const int groups = (stages + 1) / 2;
+    const int64_t weights = (int64_t)a.experts * a.outs;
+    for (int64_t tile = blockIdx.x; ok && tile < n_tiles; tile += gridDim.x) {
+      int e, out0, row0, count;
+      locate(tile, &e, &out0, &row0, &count);
+      constexpr int kRows = 1 + G::kScaleB;   // rows of a thread: one output, one or two rows
+      const uint8_t* src[kRows];
+      const int64_t wr = (int64_t)e * a.outs + out0 + t;
+      src[0] = wr < weights ? a.ws + wr * a.scale_bytes : nullptr;
+#pragma unroll
+      for (int j = 0; j < G::kScaleB; ++j) {
+        const int c = j * 128 + t;
+        src[1 + j] = c < count ? a.xs + ((int64_t)row0 + c) * a.scale_bytes : nullptr;
+      }
+      const uint32_t one = 0x7F7F7F7Fu;
+      uint4 next[kRows];
+      auto fetch = [&](int g) {
+#pragma unroll
+        for (int j = 0; j < kRows; ++j) {
+          next[j] = make_uint4(one, one, one, one);
+          if (src[j] && g < groups) next[j] = __ldg(reinterpret_cast<const uint4*>(src[j]) + g);
+        }
+      };
+      fetch(0);
+      for (int g = 0; ok && g < groups; ++g) {
+        uint32_t word[kRows][4];
+#pragma unroll
+        for (int j = 0; j < kRows; ++j) {
+          word[j][0] = next[j].x;
+          word[j][1] = next[j].y;
+          word[j][2] = next[j].z;
+          word[j][3] = next[j].w;
+          if (g == groups - 1)   // blocks past the row's end
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const int left = a.blocks - (g * 16 + q * 4);
+              if (left < 4) {
+                const uint32_t keep = left <= 0 ? 0u : (1u << (8 * left)) - 1u;
+                word[j][q] = (word[j][q] & keep) | (one & ~keep);
+              }
+            }
+        }
+        fetch(g + 1);
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          if (2 * g + half >= stages) break;
+          const int s = it % G::kStages;
+          ok = __all_sync(0xffffffffu, wait(&empty[s], ((it / G::kStages) & 1) ^ 1, &s_abort, a.glob));
+          if (!ok) break;
+          uint8_t* sc = sS + s * G::kScaleBytes + (t & 31) * 16 + (t >> 5) * 4;
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            *reinterpret_cast<uint32_t*>(sc + q * kScaleTile) = word[0][2 * half + q];
+#pragma unroll
+            for (int j = 0; j < G::kScaleB; ++j)
+              *reinterpret_cast<uint32_t*>(sc + (2 + q * G::kScaleB + j) * kScaleTile) = word[1 + j][2 * half + q];
+          }
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&scaled[s]);
+          ++it;
+        }
+      }
+    }
+  } else if (w >= 4) {
+    uint32_t n_acc = 0;
+    for (int64_t tile = blockIdx.x; tile < n_tiles; tile += gridDim.x, ++n_acc) {
+      int e, out0, row0, count;
+      locate(tile, &e, &out0, &row0, &count);
+      const int buf = n_acc % G::kAcc;
+      const bool ok = wait(&acc_full[buf], (n_acc / G::kAcc) & 1, &s_abort, a.glob);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      tc_fence_after();
+      const int out = out0 + (w - 4) * 32 + lane;
+      const bool mine = out < a.outs;
+      const uint32_t d = tmem + buf * kTN + ((uint32_t)((w - 4) * 32) << 16);
+      for (int c0 = 0; c0 < count; c0 += 16) {
+        uint32_t v[16];
+        tc_load16(d + c0, v);
+        tc_load_wait();
+        const int64_t at = ((int64_t)row0 + c0) * a.outs + out;
+        if (a.out_type == EBC_BF16)
+          store16((__nv_bfloat16*)a.ys + at, a.outs, v, count - c0, mine);
+        else if (a.out_type == EBC_F16)
+          store16((__half*)a.ys + at, a.outs, v, count - c0, mine);
+        else
+          store16((float*)a.ys + at, a.outs, v, count - c0, mine);
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&acc_empty[buf]);
+    }
+    // rows that no expert has
+    const int es = a.out_type == EBC_F32 ? 4 : 2;
+    const int64_t words = (a.rows - s_begin[a.experts]) * a.outs;
+    uint8_t* y0 = (uint8_t*)a.ys + (int64_t)s_begin[a.experts] * a.outs * es;
+    for (int64_t i = (int64_t)blockIdx.x * 128 + (tid - 128); i < words; i += (int64_t)gridDim.x * 128) {
+      if (es == 4)
+        reinterpret_cast<uint32_t*>(y0)[i] = 0u;
+      else
+        reinterpret_cast<uint16_t*>(y0)[i] = 0;
     }
   }
-  if (r < s_r1 && out < outs) ys[r * outs + out] = from_f32<T>(acc);
+
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (s_abort) {
+    // nothing that was started may outlive the CTA
+    if (w == 0 && lane == 0) {
+      for (uint32_t i = issued > G::kStages ? issued - G::kStages : 0; i < issued; ++i)
+        for (int p = 0; p < kWaitLimit && !mbar_try_wait(&full[i % G::kStages], (i / G::kStages) & 1); ++p) {
+        }
+    }
+    if (w == 1 && lane == 0) {
+      tc_commit(&drained);
+      for (int p = 0; p < kWaitLimit && !mbar_try_wait(&drained, 0); ++p) {
+      }
+    }
+    __syncthreads();
+  }
+  if (w == 1)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(G::kCols) : "memory");
 }
 
 bool aligned(const void* p, int bytes) { return ((uintptr_t)p & (uintptr_t)(bytes - 1)) == 0; }
 
-template <typename T>
-cudaError_t product_t(const CallView& v, const uint8_t* xc, const uint8_t* xs, int64_t rows, int64_t width,
-                      const uint8_t* wc, const uint8_t* ws, int64_t outs, int E, const int32_t* offsets, void* ys,
+// codes [rows][code_bytes] in boxes of 128 bytes x box_rows
+cudaError_t make_map(CUtensorMap* map, const uint8_t* codes, int64_t rows, int64_t code_bytes, int box_rows) {
+  static PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
+  if (!encode) {
+    cudaDriverEntryPointQueryResult q;
+    void* fn = nullptr;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &q) !=
+            cudaSuccess ||
+        q != cudaDriverEntryPointSuccess || !fn)
+      return cudaErrorNotSupported;
+    encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
+  }
+  const cuuint64_t dims[2] = {(cuuint64_t)code_bytes, (cuuint64_t)rows};
+  const cuuint64_t strides[1] = {(cuuint64_t)code_bytes};
+  const cuuint32_t box[2] = {(cuuint32_t)kRowBytes, (cuuint32_t)box_rows};
+  const cuuint32_t estr[2] = {1u, 1u};
+  const CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(codes), dims, strides, box,
+                            estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+template <int kTN>
+cudaError_t product_t(const CallView& v, const uint8_t* xc, const uint8_t* wc, int64_t width, const Args& a,
                       cudaStream_t st) {
-  const int64_t tiles = rows / kT + (E < rows ? E : rows) + 1;
-  return launch_named(v, "k_mx4_product", st, k_mx4_product<T>,
-                      dim3((unsigned)((outs + kT - 1) / kT * tiles)), dim3(kT * kT), 0, 1, xc, xs, rows,
-                      width, wc, ws, outs, E, offsets, (T*)ys, v.glob);
+  using G = Geom<kTN>;
+  CUtensorMap wmap, xmap;
+  const int64_t cb = EBC_MX4_CODE_BYTES(width);
+  cudaError_t e = make_map(&wmap, wc, a.experts * a.outs, cb, kM);
+  if (e == cudaSuccess) e = make_map(&xmap, xc, a.rows, cb, kTN);
+  if (e != cudaSuccess) return e;
+  e = cudaFuncSetAttribute(k_mx4_product<kTN>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)G::kSmem);
+  if (e != cudaSuccess) return e;
+  const int64_t most = (a.rows / kTN + (a.experts < a.rows ? a.experts : a.rows)) * ((a.outs + kM - 1) / kM);
+  return launch_named(v, "k_mx4_product", st, k_mx4_product<kTN>, dim3((unsigned)(most < v.nsm ? most : v.nsm)),
+                      dim3(kThreads), G::kSmem, 1, wmap, xmap, a);
 }
 
 }  // namespace
@@ -126,17 +511,25 @@ int ebc_mx4_product(ebc_ctx* ctx, const uint8_t* d_x_codes, const uint8_t* d_x_s
   cudaStream_t st = (cudaStream_t)stream;
   const int rc = begin_call(ctx, st, &v);
   if (rc || rows == 0) return rc;
-  cudaError_t e;
-  if (out_type == EBC_F32)
-    e = product_t<float>(v, d_x_codes, d_x_scales, rows, width, d_w_codes, d_w_scales, outs, n_experts, d_offsets,
-                         d_ys, st);
-  else if (out_type == EBC_BF16)
-    e = product_t<__nv_bfloat16>(v, d_x_codes, d_x_scales, rows, width, d_w_codes, d_w_scales, outs, n_experts,
-                                 d_offsets, d_ys, st);
-  else
-    e = product_t<__half>(v, d_x_codes, d_x_scales, rows, width, d_w_codes, d_w_scales, outs, n_experts, d_offsets,
-                          d_ys, st);
-  return cuda_code(e);
+  Args a;
+  a.xs = d_x_scales;
+  a.ws = d_w_scales;
+  a.offsets = d_offsets;
+  a.ys = d_ys;
+  a.glob = v.glob;
+  a.rows = rows;
+  a.outs = outs;
+  a.scale_bytes = EBC_MX4_SCALE_BYTES(width);
+  a.out_type = out_type;
+  a.blocks = (int)((width + EBC_MX4_BLOCK - 1) / EBC_MX4_BLOCK);
+  a.experts = n_experts;
+  // the rows of a tile: an expert's share of the rows, spread evenly
+  const int64_t share = (rows + n_experts - 1) / n_experts;
+  if (share <= 16) return cuda_code(product_t<16>(v, d_x_codes, d_w_codes, width, a, st));
+  if (share <= 32) return cuda_code(product_t<32>(v, d_x_codes, d_w_codes, width, a, st));
+  if (share <= 64) return cuda_code(product_t<64>(v, d_x_codes, d_w_codes, width, a, st));
+  if (share <= 128) return cuda_code(product_t<128>(v, d_x_codes, d_w_codes, width, a, st));
+  return cuda_code(product_t<256>(v, d_x_codes, d_w_codes, width, a, st));
 }
 
 }  // extern "C"
