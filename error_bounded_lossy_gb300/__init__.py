@@ -382,7 +382,8 @@ def __getattr__(name):
     # the operators on torch tensors; torch is imported with them, not with the package
     if name in ("Experts", "Plan", "Mx4"):
         from . import experts
-        return getattr(experts, name)
+        globals()[name] = found = getattr(experts, name)
+        return found
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
 
 

@@ -2,7 +2,9 @@
 
 nvcc compiles each translation unit for sm_103a in parallel, then links one
 shared library with the CUDA runtime statically linked.  No torch types cross
-the C ABI, so the library is loaded with ctypes.
+the C ABI, so the library is loaded with ctypes.  A second, small module
+(_build/_torch_calls-<torch version>.so, g++ against torch's headers) makes the
+expert-parallel and 4-bit calls on torch tensors; it links the first.
 """
 from __future__ import annotations
 
@@ -10,6 +12,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -19,6 +22,8 @@ LIB = os.path.join(BUILD, "libebc_gb300.so")
 SOURCES = ["ebc_api.cu", "ebc_compress.cu", "ebc_decompress.cu", "ebc_experts.cu", "ebc_mx4.cu",
            "ebc_mx4_product.cu"]
 HEADERS = ["ebc_internal.cuh", "ebc_types.cuh", "ebc_mx4.cuh", os.path.join("..", "..", "include", "ebc.h")]
+
+TORCH_SOURCE = "ebc_torch.cpp"
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-ffp-contract=off,-O2",
@@ -30,6 +35,27 @@ def nvcc() -> str:
     if not os.path.exists(path):
         raise RuntimeError("nvcc not found: the codec needs the CUDA toolkit to build")
     return path
+
+
+def torch_module() -> str:
+    """The path of the torch module, one for each torch it may be built against."""
+    import torch
+    return os.path.join(BUILD, f"_torch_calls-{torch.__version__}.so")
+
+
+def _torch_commands(obj: str, out: str):
+    """(compile, link) of the torch module."""
+    import torch
+    root = os.path.dirname(torch.__file__)
+    cuda = os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")
+    inc = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"), cuda,
+           sysconfig.get_paths()["include"]]
+    libs = os.path.join(root, "lib")
+    return (["g++", "-O2", "-std=c++17", "-fPIC", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+             *(f"-I{i}" for i in inc), "-c", os.path.join(CSRC, TORCH_SOURCE), "-o", obj],
+            ["g++", "-shared", "-o", out, obj, f"-L{libs}", "-ltorch_python", "-ltorch_cuda", "-ltorch_cpu", "-ltorch",
+             "-lc10_cuda", "-lc10", f"-L{BUILD}", "-l:" + os.path.basename(LIB), f"-Wl,-rpath,{libs}",
+             "-Wl,-rpath,$ORIGIN"])
 
 
 def _stale(out: str, deps) -> bool:
@@ -52,16 +78,23 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
                 cmd += ["-Xptxas", "-v"]
             jobs.append(cmd)
 
+    module = torch_module()
+    module_obj = module[:-3] + ".o"
+    torch_deps = [os.path.join(CSRC, TORCH_SOURCE), os.path.join(CSRC, HEADERS[-1]), os.path.abspath(__file__)]
+    compile_torch, link_torch = _torch_commands(module_obj, module + f".{os.getpid()}.tmp")
+    if force or _stale(module_obj, torch_deps):
+        jobs.append(compile_torch)
+
     def run(cmd):
         r = subprocess.run(cmd, capture_output=True, text=True)
         return cmd, r
 
-    with ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    with ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
         for cmd, r in ex.map(run, jobs):
             if verbose or ptxas_info or r.returncode != 0:
                 sys.stderr.write(r.stdout + r.stderr)
             if r.returncode != 0:
-                raise RuntimeError("nvcc failed: " + " ".join(cmd))
+                raise RuntimeError("compilation failed: " + " ".join(cmd))
     objs = [os.path.join(BUILD, s.replace(".cu", ".o")) for s in SOURCES]
     if force or jobs or _stale(LIB, objs):
         tmp = LIB + f".{os.getpid()}.tmp"
@@ -71,6 +104,12 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
             sys.stderr.write(r.stdout + r.stderr)
             raise RuntimeError("nvcc link failed")
         os.replace(tmp, LIB)
+    if force or _stale(module, [module_obj]):
+        r = subprocess.run(link_torch, capture_output=True, text=True)
+        if r.returncode != 0:
+            sys.stderr.write(r.stdout + r.stderr)
+            raise RuntimeError("linking the torch module failed")
+        os.replace(link_torch[3], module)
     return LIB
 
 
