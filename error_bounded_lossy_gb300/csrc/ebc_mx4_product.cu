@@ -20,22 +20,28 @@ constexpr int kM = 128;
 constexpr int kStageK = 256;
 constexpr int kRowBytes = kStageK / 2;
 constexpr int kScaleTile = 512;    // bytes of the scales of 128 rows x 4 blocks, as the matrix unit wants them
-constexpr int kThreads = 384;      // warp 0 loads, warp 1 multiplies, warps 4-7 store, warps 8-11 lay out scales
+constexpr int kThreads = 512;      // warp 0 loads, warp 1 multiplies, warps 4-7 lay out scales, warps 8-15 store
 constexpr int kScaleWarps = 4;
+constexpr int kStoreWarps = 8;
+constexpr int kStoreRows = 16;     // rows that a storing warp turns over at a time
+constexpr int kStorePitch = 80;    // bytes of such a row of 32 outputs: 64, and 16 to spread the banks
 
 template <int kTN>
 struct Geom {
   static constexpr int kScaleB = (kTN + 127) / 128;                       // scale tiles of the rows per 4 blocks
+  static constexpr int kBox = kTN < 64 ? kTN : 64;                        // rows of one copy
   static constexpr int kABytes = kM * kRowBytes;
   static constexpr int kBBytes = kTN * kRowBytes;
   static constexpr int kScaleBytes = 2 * (1 + kScaleB) * kScaleTile;      // per stage: 8 blocks a row
-  static constexpr int kStages = kTN == 256 ? 4 : kTN == 128 ? 6 : 8;
+  static constexpr int kStages = kTN == 256 ? 4 : kTN == 128 ? 6 : kTN == 64 ? 7 : 8;
   static constexpr int kAcc = kTN == 256 ? 1 : 2;                         // accumulators
+  static constexpr int kAccCols = kTN < 32 ? 32 : kTN;
   static constexpr int kScaleCols = 2 * (1 + kScaleB) * 4;                // tensor memory columns per stage
   static constexpr int kCols = 512;
-  static constexpr size_t kSmem = 1024 + (size_t)kStages * (kABytes + kBBytes + kScaleBytes);
-  static_assert(kAcc * (kTN < 32 ? 32 : kTN) + kStages * kScaleCols <= kCols, "tensor memory");
-  static_assert(kSmem <= 216 * 1024, "shared memory");
+  static constexpr int kStoreBytes = kStoreWarps * kStoreRows * kStorePitch;
+  static constexpr size_t kSmem = 1024 + (size_t)kStages * (kABytes + kBBytes + kScaleBytes) + kStoreBytes;
+  static_assert(kAcc * kAccCols + kStages * kScaleCols <= kCols, "tensor memory");
+  static_assert(kSmem <= 217 * 1024, "shared memory");
 };
 
 // ---- PTX ----
@@ -85,6 +91,7 @@ __device__ __forceinline__ void tc_mma(uint32_t d, uint64_t a, uint64_t b, uint3
       "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(accumulate)
       : "memory");
 }
+// 32 lanes x 16 columns, a lane a thread
 __device__ __forceinline__ void tc_load16(uint32_t taddr, uint32_t (&v)[16]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
@@ -93,6 +100,28 @@ __device__ __forceinline__ void tc_load16(uint32_t taddr, uint32_t (&v)[16]) {
         "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
       : "r"(taddr)
       : "memory");
+}
+// 16 lanes x 16 columns as two 16x8 fragments: thread t has lanes t / 4 (the
+// first two words of a fragment) and t / 4 + 8, columns 2 (t % 4) and the next
+__device__ __forceinline__ void tc_load_fragments(uint32_t taddr, uint32_t (&v)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
+               : "r"(taddr)
+               : "memory");
+}
+// four 8x8 blocks of 16-bit values, transposed: thread t gives the address of
+// column t % 8 of block t / 8
+__device__ __forceinline__ void store_transposed(uint32_t addr, const uint32_t (&v)[4]) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v[0]),
+               "r"(v[1]), "r"(v[2]), "r"(v[3])
+               : "memory");
+}
+// one thread of the warp, known to the compiler as such: what it issues has
+// its operands in uniform registers
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
+  return p != 0u;
 }
 __device__ __forceinline__ void tc_load_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 
@@ -108,7 +137,7 @@ __device__ __forceinline__ uint64_t scale_desc(uint32_t addr) {
 // Instruction descriptor: both operands E2M1 along K, scales UE8M0, M = 128,
 // N = n; `id` (0 or 2) is the byte of a scale word where the instruction's two
 // blocks start.
-__host__ __device__ constexpr uint32_t instr_desc(int n, int id) {
+__device__ __forceinline__ uint32_t instr_desc(int n, int id) {
   return (1u << 7) | (1u << 10) | ((uint32_t)(n >> 3) << 17) | (1u << 23) | ((uint32_t)(kM >> 4) << 24) |
          ((uint32_t)id << 4) | ((uint32_t)id << 29);
 }
@@ -121,6 +150,7 @@ struct Args {
   Glob* glob;
   int64_t rows, outs, scale_bytes;
   int out_type, blocks, experts;   // blocks: scale blocks a row
+  bool wide;                       // 16-byte stores of rows
 };
 
 // A wait that gives up: after kWaitLimit polls, or once another thread of the
@@ -135,27 +165,85 @@ __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile in
   return false;
 }
 
-// Sixteen rows' values of one output a lane, to memory: a warp writes 32
-// consecutive outputs of a row.
 template <typename T>
-__device__ __forceinline__ void store16(T* y, int64_t ld, const uint32_t (&v)[16], int count, bool mine) {
+__device__ __forceinline__ uint32_t pack2(uint32_t lo, uint32_t hi);
+template <>
+__device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(uint32_t lo, uint32_t hi) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(__uint_as_float(lo), __uint_as_float(hi));
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+template <>
+__device__ __forceinline__ uint32_t pack2<__half>(uint32_t lo, uint32_t hi) {
+  const __half2 v = __floats2half2_rn(__uint_as_float(lo), __uint_as_float(hi));
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// 32 outputs x 16 rows of an accumulator to memory, 16-bit results: fragments
+// of outputs x rows, turned over on their way through the warp's own piece of
+// shared memory, so that a lane then stores eight outputs of a row (16 bytes;
+// four lanes a row).  y: the first row's first output; outputs >= n_out and
+// rows >= n_row are not written.
+template <typename T>
+__device__ __forceinline__ void store_half(uint32_t taddr, uint32_t stage, T* y, int64_t ld, int n_out, int n_row,
+                                           bool wide, int lane) {
+  uint32_t a[8], b[8];
+  tc_load_fragments(taddr, a);
+  tc_load_fragments(taddr + (16u << 16), b);
+  tc_load_wait();
+  __syncwarp();   // the piece has been read
 #pragma unroll
-  for (int c = 0; c < 16; ++c)
-    if (mine && c < count) y[c * ld] = from_f32<T>(__uint_as_float(v[c]));
+  for (int h = 0; h < 2; ++h) {
+    const uint32_t v[4] = {pack2<T>(a[4 * h], a[4 * h + 1]), pack2<T>(a[4 * h + 2], a[4 * h + 3]),
+                           pack2<T>(b[4 * h], b[4 * h + 1]), pack2<T>(b[4 * h + 2], b[4 * h + 3])};
+    store_transposed(stage + (h * 8 + (lane & 7)) * kStorePitch + (lane >> 3) * 16, v);
+  }
+  __syncwarp();
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int r = h * 8 + (lane >> 2), o = (lane & 3) * 8;
+    Vec<T, 16> v;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.raw.x), "=r"(v.raw.y), "=r"(v.raw.z), "=r"(v.raw.w)
+                 : "r"(stage + r * kStorePitch + o * 2)
+                 : "memory");
+    if (r >= n_row) continue;
+    T* dst = y + r * ld + o;
+    if (wide && o + 8 <= n_out) {
+      *reinterpret_cast<uint4*>(dst) = v.raw;
+    } else {
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (o + k < n_out) dst[k] = v.e[k];
+    }
+  }
+}
+
+// The same in fp32: a warp stores 32 consecutive outputs of a row at a time.
+__device__ __forceinline__ void store_full(uint32_t taddr, float* y, int64_t ld, int n_out, int n_row, int lane) {
+  uint32_t v[16];
+  tc_load16(taddr, v);
+  tc_load_wait();
+  if (lane < n_out) {
+#pragma unroll
+    for (int c = 0; c < 16; ++c)
+      if (c < n_row) y[c * ld + lane] = __uint_as_float(v[c]);
+  }
 }
 
 // One persistent CTA an SM walks tiles blockIdx.x, + gridDim.x, ...; outputs
 // of a run of rows come one after the other, so that the CTAs working at the
 // same time share both operands in L2.
 //   warp 0      brings the codes of both operands in by TMA, a ring of stages
-//   warps 8-11  lay the scales out: the matrix unit reads the scales of 128
+//   warps 4-7   lay the scales out: the matrix unit reads the scales of 128
 //               rows x 4 blocks from tensor memory as 32 lanes x 4 words,
 //               row r in lane r % 32, word r / 32, so a row's four scale bytes
 //               are one 4-byte store.  Rows and blocks past the end get 1.
 //   warp 1      copies a stage's scales to tensor memory and issues its matrix
 //               instructions; each stage has its own scale columns, so they
 //               are written again only after the stage was given back
-//   warps 4-7   read the accumulator, round once, and store
+//   warps 8-15  read the accumulator, round once, and store
+// The N of the instructions is the tile's row count rounded up to 16, so a
+// ragged segment's last tile costs what it holds.
 // Every wait is bounded (see wait()); a CTA that gives up waits for the copies
 // and instructions it has in flight, frees its tensor memory and returns.
 template <int kTN>
@@ -174,6 +262,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx4_product(const __grid_consta
   uint8_t* sA = base;
   uint8_t* sB = sA + G::kStages * G::kABytes;
   uint8_t* sS = sB + G::kStages * G::kBBytes;
+  uint8_t* sStore = sS + G::kStages * G::kScaleBytes;
 
   if (w == 0 && lane == 0) {
     for (int i = 0; i < G::kStages; ++i) {
@@ -183,7 +272,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx4_product(const __grid_consta
     }
     for (int i = 0; i < G::kAcc; ++i) {
       mbar_init(&acc_full[i], 1);
-      mbar_init(&acc_empty[i], 4);
+      mbar_init(&acc_empty[i], kStoreWarps);
     }
     mbar_init(&drained, 1);
     s_abort = 0;
@@ -237,7 +326,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx4_product(const __grid_consta
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = s_tmem;
-  const uint32_t tmem_scales = tmem + G::kAcc * (kTN < 32 ? 32 : kTN);
+  const uint32_t tmem_scales = tmem + G::kAcc * G::kAccCols;
   const int out_tiles = (int)((a.outs + kM - 1) / kM);
   const int64_t n_tiles = (int64_t)s_tiles[a.experts] * out_tiles;
   const int stages = (a.blocks + 7) / 8;   // stages of a tile
@@ -259,72 +348,88 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx4_product(const __grid_consta
 
   uint32_t issued = 0;   // stages that warp 0 has asked for
   if (w == 0) {
-    if (lane == 0) {
-      bool ok = true;
-      for (int64_t tile = blockIdx.x; ok && tile < n_tiles; tile += gridDim.x) {
-        int e, out0, row0, count;
-        locate(tile, &e, &out0, &row0, &count);
-        for (int k = 0; k < stages; ++k) {
-          const int s = issued % G::kStages;
-          if (!wait(&empty[s], ((issued / G::kStages) & 1) ^ 1, &s_abort, a.glob)) {
-            ok = false;
-            break;
-          }
-          mbar_expect_tx(&full[s], G::kABytes + G::kBBytes);
-          tma_load_2d(smem_u32(sA + s * G::kABytes), &wmap, &full[s], k * kRowBytes, (int)(e * a.outs) + out0);
-          tma_load_2d(smem_u32(sB + s * G::kBBytes), &xmap, &full[s], k * kRowBytes, row0);
-          ++issued;
+    int s = 0;
+    uint32_t phase = 1;   // of the barriers that stages are given back on
+    bool ok = true;
+    for (int64_t tile = blockIdx.x; ok && tile < n_tiles; tile += gridDim.x) {
+      int e, out0, row0, count;
+      locate(tile, &e, &out0, &row0, &count);
+      const int boxes = (count + G::kBox - 1) / G::kBox;
+      const int wrow = (int)(e * a.outs) + out0;
+      for (int k = 0; k < stages; ++k) {
+        ok = __all_sync(0xffffffffu, wait(&empty[s], phase, &s_abort, a.glob));
+        if (!ok) break;
+        if (elect_one()) {
+          mbar_expect_tx(&full[s], G::kABytes + boxes * G::kBox * kRowBytes);
+          tma_load_2d(smem_u32(sA) + s * G::kABytes, &wmap, &full[s], k * kRowBytes, wrow);
+          for (int i = 0; i < boxes; ++i)
+            tma_load_2d(smem_u32(sB) + s * G::kBBytes + i * G::kBox * kRowBytes, &xmap, &full[s], k * kRowBytes,
+                        row0 + i * G::kBox);
+        }
+        __syncwarp();
+        ++issued;
+        if (++s == G::kStages) {
+          s = 0;
+          phase ^= 1;
         }
       }
-      // every stage given back: no arrival is left on its way to this CTA's barriers
-      for (uint32_t i = issued > G::kStages ? issued - G::kStages : 0; ok && i < issued; ++i)
-        ok = wait(&empty[i % G::kStages], (i / G::kStages) & 1, &s_abort, a.glob);
     }
-    __syncwarp();
+    // every stage given back: no arrival is left on its way to this CTA's barriers
+    for (uint32_t i = issued > G::kStages ? issued - G::kStages : 0; ok && i < issued; ++i)
+      ok = __all_sync(0xffffffffu, wait(&empty[i % G::kStages], (i / G::kStages) & 1, &s_abort, a.glob));
   } else if (w == 1) {
-    if (lane == 0) {
-      uint32_t it = 0, n_acc = 0;
-      bool ok = true;
-      for (int64_t tile = blockIdx.x; ok && tile < n_tiles; tile += gridDim.x, ++n_acc) {
-        const int buf = n_acc % G::kAcc;
-        if (!wait(&acc_empty[buf], ((n_acc / G::kAcc) & 1) ^ 1, &s_abort, a.glob)) break;
+    int s = 0, buf = 0;
+    uint32_t phase = 0, acc_phase = 1;
+    bool ok = true;
+    for (int64_t tile = blockIdx.x; ok && tile < n_tiles; tile += gridDim.x) {
+      int e, out0, row0, count;
+      locate(tile, &e, &out0, &row0, &count);
+      const uint32_t id0 = instr_desc((count + 15) & ~15, 0), id2 = instr_desc((count + 15) & ~15, 2);
+      ok = __all_sync(0xffffffffu, wait(&acc_empty[buf], acc_phase, &s_abort, a.glob));
+      if (!ok) break;
+      tc_fence_after();
+      const uint32_t d = tmem + buf * G::kAccCols;
+      for (int k = 0; k < stages; ++k) {
+        // the lanes wait for the codes and for the scales at the same time
+        ok = __all_sync(0xffffffffu, wait(lane & 1 ? &scaled[s] : &full[s], phase, &s_abort, a.glob));
+        if (!ok) break;
         tc_fence_after();
-        const uint32_t d = tmem + buf * kTN;
-        for (int k = 0; k < stages; ++k, ++it) {
-          const int s = it % G::kStages;
-          const uint32_t parity = (it / G::kStages) & 1;
-          if (!wait(&full[s], parity, &s_abort, a.glob) || !wait(&scaled[s], parity, &s_abort, a.glob)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          const uint32_t sc = smem_u32(sS + s * G::kScaleBytes);
+        if (elect_one()) {
           const uint32_t ta = tmem_scales + s * G::kScaleCols, tb = ta + 8;
+          const uint64_t ds = scale_desc(smem_u32(sS) + s * G::kScaleBytes);
 #pragma unroll
           for (int q = 0; q < 2; ++q) {
-            tc_copy_scales(ta + 4 * q, scale_desc(sc + q * kScaleTile));
+            tc_copy_scales(ta + 4 * q, ds + q * (kScaleTile >> 4));
 #pragma unroll
             for (int j = 0; j < G::kScaleB; ++j)
-              tc_copy_scales(tb + 4 * (q * G::kScaleB + j), scale_desc(sc + (2 + q * G::kScaleB + j) * kScaleTile));
+              tc_copy_scales(tb + 4 * (q * G::kScaleB + j), ds + (2 + q * G::kScaleB + j) * (kScaleTile >> 4));
           }
           const int left = a.blocks - k * 8;   // scale blocks from here on
-          const uint64_t da = operand_desc(smem_u32(sA + s * G::kABytes));
-          const uint64_t db = operand_desc(smem_u32(sB + s * G::kBBytes));
+          const uint64_t da = operand_desc(smem_u32(sA) + s * G::kABytes);
+          const uint64_t db = operand_desc(smem_u32(sB) + s * G::kBBytes);
 #pragma unroll
           for (int q = 0; q < 4; ++q)
             if (2 * q < left)
-              tc_mma(d, da + 2 * q, db + 2 * q, instr_desc(kTN, (q & 1) * 2), ta + 4 * (q >> 1),
-                     tb + 4 * G::kScaleB * (q >> 1), k > 0 || q > 0);
+              tc_mma(d, da + 2 * q, db + 2 * q, q & 1 ? id2 : id0, ta + 4 * (q >> 1), tb + 4 * G::kScaleB * (q >> 1),
+                     k > 0 || q > 0);
           tc_commit(&empty[s]);
+          if (k == stages - 1) tc_commit(&acc_full[buf]);
         }
-        if (ok) tc_commit(&acc_full[buf]);
+        __syncwarp();
+        if (++s == G::kStages) {
+          s = 0;
+          phase ^= 1;
+        }
+      }
+      if (++buf == G::kAcc) {
+        buf = 0;
+        acc_phase ^= 1;
       }
     }
-    __syncwarp();
-  } else if (w >= 8) {
+  } else if (w >= 4 && w < 8) {
     // 16 scale bytes a row (512 values, two stages) at a time; the next 16 are
     // on their way while these are stored
-    const int t = tid - 256;
+    const int t = tid - 128;
     uint32_t it = 0;
     bool ok = true;
     const int groups = (stages + 1) / 2;
@@ -391,39 +496,42 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx4_product(const __grid_consta
         }
       }
     }
-  } else if (w >= 4) {
-    uint32_t n_acc = 0;
-    for (int64_t tile = blockIdx.x; tile < n_tiles; tile += gridDim.x, ++n_acc) {
+  } else if (w >= 8) {
+    // a warp has the outputs of its quarter of the lanes, and every other run of 16 rows
+    const int quarter = w & 3, odd = (w - 8) >> 2;
+    const uint32_t stage = smem_u32(sStore) + (w - 8) * kStoreRows * kStorePitch;
+    int buf = 0;
+    uint32_t phase = 0;
+    for (int64_t tile = blockIdx.x; tile < n_tiles; tile += gridDim.x) {
       int e, out0, row0, count;
       locate(tile, &e, &out0, &row0, &count);
-      const int buf = n_acc % G::kAcc;
-      const bool ok = wait(&acc_full[buf], (n_acc / G::kAcc) & 1, &s_abort, a.glob);
-      if (!__all_sync(0xffffffffu, ok)) break;
+      if (!__all_sync(0xffffffffu, wait(&acc_full[buf], phase, &s_abort, a.glob))) break;
       tc_fence_after();
-      const int out = out0 + (w - 4) * 32 + lane;
-      const bool mine = out < a.outs;
-      const uint32_t d = tmem + buf * kTN + ((uint32_t)((w - 4) * 32) << 16);
-      for (int c0 = 0; c0 < count; c0 += 16) {
-        uint32_t v[16];
-        tc_load16(d + c0, v);
-        tc_load_wait();
+      const int64_t out = out0 + quarter * 32;
+      const int n_out = a.outs - out < 32 ? (int)(a.outs - out) : 32;   // may be <= 0
+      const uint32_t d = tmem + buf * G::kAccCols + ((uint32_t)(quarter * 32) << 16);
+      for (int c0 = odd * kStoreRows; c0 < count; c0 += 2 * kStoreRows) {
         const int64_t at = ((int64_t)row0 + c0) * a.outs + out;
         if (a.out_type == EBC_BF16)
-          store16((__nv_bfloat16*)a.ys + at, a.outs, v, count - c0, mine);
+          store_half(d + c0, stage, (__nv_bfloat16*)a.ys + at, a.outs, n_out, count - c0, a.wide, lane);
         else if (a.out_type == EBC_F16)
-          store16((__half*)a.ys + at, a.outs, v, count - c0, mine);
+          store_half(d + c0, stage, (__half*)a.ys + at, a.outs, n_out, count - c0, a.wide, lane);
         else
-          store16((float*)a.ys + at, a.outs, v, count - c0, mine);
+          store_full(d + c0, (float*)a.ys + at, a.outs, n_out, count - c0, lane);
       }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&acc_empty[buf]);
+      if (++buf == G::kAcc) {
+        buf = 0;
+        phase ^= 1;
+      }
     }
     // rows that no expert has
     const int es = a.out_type == EBC_F32 ? 4 : 2;
     const int64_t words = (a.rows - s_begin[a.experts]) * a.outs;
     uint8_t* y0 = (uint8_t*)a.ys + (int64_t)s_begin[a.experts] * a.outs * es;
-    for (int64_t i = (int64_t)blockIdx.x * 128 + (tid - 128); i < words; i += (int64_t)gridDim.x * 128) {
+    for (int64_t i = (int64_t)blockIdx.x * 256 + (tid - 256); i < words; i += (int64_t)gridDim.x * 256) {
       if (es == 4)
         reinterpret_cast<uint32_t*>(y0)[i] = 0u;
       else
@@ -483,7 +591,7 @@ cudaError_t product_t(const CallView& v, const uint8_t* xc, const uint8_t* wc, i
   CUtensorMap wmap, xmap;
   const int64_t cb = EBC_MX4_CODE_BYTES(width);
   cudaError_t e = make_map(&wmap, wc, a.experts * a.outs, cb, kM);
-  if (e == cudaSuccess) e = make_map(&xmap, xc, a.rows, cb, kTN);
+  if (e == cudaSuccess) e = make_map(&xmap, xc, a.rows, cb, G::kBox);
   if (e != cudaSuccess) return e;
   e = cudaFuncSetAttribute(k_mx4_product<kTN>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)G::kSmem);
   if (e != cudaSuccess) return e;
@@ -523,6 +631,7 @@ int ebc_mx4_product(ebc_ctx* ctx, const uint8_t* d_x_codes, const uint8_t* d_x_s
   a.out_type = out_type;
   a.blocks = (int)((width + EBC_MX4_BLOCK - 1) / EBC_MX4_BLOCK);
   a.experts = n_experts;
+  a.wide = aligned(d_ys, 16) && outs * b % 16 == 0;
   // the rows of a tile: an expert's share of the rows, spread evenly
   const int64_t share = (rows + n_experts - 1) / n_experts;
   if (share <= 16) return cuda_code(product_t<16>(v, d_x_codes, d_w_codes, width, a, st));
