@@ -20,9 +20,12 @@ constexpr int kM = 128;
 constexpr int kStageK = 256;
 constexpr int kRowBytes = kStageK / 2;
 constexpr int kScaleTile = 512;    // bytes of the scales of 128 rows x 4 blocks, as the matrix unit wants them
-constexpr int kThreads = 512;      // warp 0 loads, warp 1 multiplies, warps 4-7 lay out scales, warps 8-15 store
-constexpr int kScaleWarps = 4;
-constexpr int kStoreWarps = 8;
+// warp 0 loads, warp 1 multiplies, warps 2-3 lay out scales, warps 4-11 store:
+// three warps a scheduler, so that a storing thread can hold its share of a
+// tile (64 words) in its 168 registers
+constexpr int kThreads = 384;
+constexpr int kScaleWarp0 = 2, kScaleWarps = 2;
+constexpr int kStoreWarp0 = 4, kStoreWarps = 8;
 constexpr int kStoreRows = 16;     // rows that a storing warp turns over at a time
 constexpr int kStorePitch = 80;    // bytes of such a row of 32 outputs: 64, and 16 to spread the banks
 
@@ -61,6 +64,16 @@ __device__ __forceinline__ bool mbar_try_wait(uint64_t* bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
       "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0u;
+}
+// whether the phase is over now: does not wait
+__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
       : "=r"(ok)
       : "r"(smem_u32(bar)), "r"(parity)
       : "memory");
@@ -178,48 +191,96 @@ __device__ __forceinline__ uint32_t pack2<__half>(uint32_t lo, uint32_t hi) {
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
-// 32 outputs x 16 rows of an accumulator to memory, 16-bit results: fragments
-// of outputs x rows, turned over on their way through the warp's own piece of
-// shared memory, so that a lane then stores eight outputs of a row (16 bytes;
-// four lanes a row).  y: the first row's first output; outputs >= n_out and
-// rows >= n_row are not written.
+// 32 outputs x 16 rows of an accumulator, rounded to 16 bits: fragments of
+// outputs x rows.  (Loads are in flight until tc_load_wait.)
+struct Fragments {
+  uint32_t lo[8], hi[8];
+};
+__device__ __forceinline__ void load_half(uint32_t taddr, Fragments* f) {
+  tc_load_fragments(taddr, f->lo);
+  tc_load_fragments(taddr + (16u << 16), f->hi);
+}
 template <typename T>
-__device__ __forceinline__ void store_half(uint32_t taddr, uint32_t stage, T* y, int64_t ld, int n_out, int n_row,
-                                           bool wide, int lane) {
-  uint32_t a[8], b[8];
-  tc_load_fragments(taddr, a);
-  tc_load_fragments(taddr + (16u << 16), b);
-  tc_load_wait();
+__device__ __forceinline__ void pack_half(const Fragments& f, uint32_t (&v)[8]) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    v[4 * h] = pack2<T>(f.lo[4 * h], f.lo[4 * h + 1]);
+    v[4 * h + 1] = pack2<T>(f.lo[4 * h + 2], f.lo[4 * h + 3]);
+    v[4 * h + 2] = pack2<T>(f.hi[4 * h], f.hi[4 * h + 1]);
+    v[4 * h + 3] = pack2<T>(f.hi[4 * h + 2], f.hi[4 * h + 3]);
+  }
+}
+
+// They are turned over on their way through the warp's own piece of shared
+// memory, so that a lane then stores eight outputs of a row (16 bytes; four
+// lanes a row).  y: where the lane's first row goes (the second is 8 further,
+// ld8 elements on); n_row rows from the first on are written, and n_out
+// outputs of each (8 = in one store).
+template <typename T>
+__device__ __forceinline__ void store_half(const uint32_t (&v)[8], uint32_t stage, T* y, int64_t ld8, int n_out,
+                                           int n_row, int lane) {
   __syncwarp();   // the piece has been read
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    const uint32_t v[4] = {pack2<T>(a[4 * h], a[4 * h + 1]), pack2<T>(a[4 * h + 2], a[4 * h + 3]),
-                           pack2<T>(b[4 * h], b[4 * h + 1]), pack2<T>(b[4 * h + 2], b[4 * h + 3])};
-    store_transposed(stage + (h * 8 + (lane & 7)) * kStorePitch + (lane >> 3) * 16, v);
+    const uint32_t q[4] = {v[4 * h], v[4 * h + 1], v[4 * h + 2], v[4 * h + 3]};
+    store_transposed(stage + (h * 8 + (lane & 7)) * kStorePitch + (lane >> 3) * 16, q);
   }
   __syncwarp();
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    const int r = h * 8 + (lane >> 2), o = (lane & 3) * 8;
-    Vec<T, 16> v;
+    Vec<T, 16> o;
     asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(v.raw.x), "=r"(v.raw.y), "=r"(v.raw.z), "=r"(v.raw.w)
-                 : "r"(stage + r * kStorePitch + o * 2)
+                 : "=r"(o.raw.x), "=r"(o.raw.y), "=r"(o.raw.z), "=r"(o.raw.w)
+                 : "r"(stage + (h * 8 + (lane >> 2)) * kStorePitch + (lane & 3) * 16)
                  : "memory");
-    if (r >= n_row) continue;
-    T* dst = y + r * ld + o;
-    if (wide && o + 8 <= n_out) {
-      *reinterpret_cast<uint4*>(dst) = v.raw;
+    if (8 * h >= n_row) continue;
+    T* dst = y + h * ld8;
+    if (n_out == 8) {
+      *reinterpret_cast<uint4*>(dst) = o.raw;
     } else {
 #pragma unroll
       for (int k = 0; k < 8; ++k)
-        if (o + k < n_out) dst[k] = v.e[k];
+        if (k < (n_out & 7)) dst[k] = o.e[k];
+      if (n_out & 8) dst[7] = o.e[7];
     }
   }
 }
 
+// A storing warp's share of a tile, 16-bit results: 32 outputs of every other
+// run of 16 rows.  All of it is read and rounded first and the accumulator
+// given back, then it is stored while the next tile is multiplied.
+template <typename T, int kTN>
+__device__ __forceinline__ void store_tile(uint32_t d, uint32_t stage, T* y, int64_t ld, int64_t n_out, int odd,
+                                           int count, bool wide, int lane, uint64_t* given_back) {
+  constexpr int kRuns = kTN < 32 ? 1 : kTN / 32;
+  uint32_t v[kRuns][8];
+#pragma unroll
+  for (int i = 0; i < kRuns; ++i) {
+    const int c0 = (i * 2 + odd) * kStoreRows;
+    if (c0 < count) {
+      Fragments f;
+      load_half(d + c0, &f);
+      tc_load_wait();
+      pack_half<T>(f, v[i]);
+    }
+  }
+  tc_fence_before();
+  __syncwarp();
+  if (lane == 0) mbar_arrive(given_back);
+  // the lane's eight outputs, and its first row
+  const int o = (lane & 3) * 8, r = odd * kStoreRows + (lane >> 2);
+  const int64_t have = n_out - o;
+  const int mine = have >= 8 ? (wide ? 8 : 15) : have > 0 ? (int)have : 0;
+  y += (int64_t)r * ld + o;
+#pragma unroll
+  for (int i = 0; i < kRuns; ++i) {
+    if ((i * 2 + odd) * kStoreRows < count) store_half(v[i], stage, y, 8 * ld, mine, count - r - i * 2 * kStoreRows, lane);
+    y += 2 * kStoreRows * ld;
+  }
+}
+
 // The same in fp32: a warp stores 32 consecutive outputs of a row at a time.
-__device__ __forceinline__ void store_full(uint32_t taddr, float* y, int64_t ld, int n_out, int n_row, int lane) {
+__device__ __forceinline__ void store_full(uint32_t taddr, float* y, int64_t ld, int64_t n_out, int n_row, int lane) {
   uint32_t v[16];
   tc_load16(taddr, v);
   tc_load_wait();
@@ -234,14 +295,14 @@ __device__ __forceinline__ void store_full(uint32_t taddr, float* y, int64_t ld,
 // of a run of rows come one after the other, so that the CTAs working at the
 // same time share both operands in L2.
 //   warp 0      brings the codes of both operands in by TMA, a ring of stages
-//   warps 4-7   lay the scales out: the matrix unit reads the scales of 128
+//   warps 2-3   lay the scales out: the matrix unit reads the scales of 128
 //               rows x 4 blocks from tensor memory as 32 lanes x 4 words,
 //               row r in lane r % 32, word r / 32, so a row's four scale bytes
 //               are one 4-byte store.  Rows and blocks past the end get 1.
 //   warp 1      copies a stage's scales to tensor memory and issues its matrix
 //               instructions; each stage has its own scale columns, so they
 //               are written again only after the stage was given back
-//   warps 8-15  read the accumulator, round once, and store
+//   warps 4-11  read the accumulator, round once, and store
 // The N of the instructions is the tile's row count rounded up to 16, so a
 // ragged segment's last tile costs what it holds.
 // Every wait is bounded (see wait()); a CTA that gives up waits for the copies
@@ -267,7 +328,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx4_product(const __grid_consta
   if (w == 0 && lane == 0) {
     for (int i = 0; i < G::kStages; ++i) {
       mbar_init(&full[i], 1);
-      mbar_init(&scaled[i], kScaleWarps);
+      mbar_init(&scaled[i], 1);
       mbar_init(&empty[i], 1);
     }
     for (int i = 0; i < G::kAcc; ++i) {
@@ -378,9 +439,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx4_product(const __grid_consta
     for (uint32_t i = issued > G::kStages ? issued - G::kStages : 0; ok && i < issued; ++i)
       ok = __all_sync(0xffffffffu, wait(&empty[i % G::kStages], (i / G::kStages) & 1, &s_abort, a.glob));
   } else if (w == 1) {
+    // the lanes watch a stage's codes (even lanes) and its scales (odd lanes)
+    // at the same time, and the next stage before this one's instructions are
+    // issued, so that a wait that is over costs nothing
     int s = 0, buf = 0;
     uint32_t phase = 0, acc_phase = 1;
-    bool ok = true;
+    bool ok = true, ready = false;
+    uint64_t* const watch = lane & 1 ? scaled : full;
     for (int64_t tile = blockIdx.x; ok && tile < n_tiles; tile += gridDim.x) {
       int e, out0, row0, count;
       locate(tile, &e, &out0, &row0, &count);
@@ -390,10 +455,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx4_product(const __grid_consta
       tc_fence_after();
       const uint32_t d = tmem + buf * G::kAccCols;
       for (int k = 0; k < stages; ++k) {
-        // the lanes wait for the codes and for the scales at the same time
-        ok = __all_sync(0xffffffffu, wait(lane & 1 ? &scaled[s] : &full[s], phase, &s_abort, a.glob));
-        if (!ok) break;
+        if (!ready) {
+          ok = __all_sync(0xffffffffu, wait(&watch[s], phase, &s_abort, a.glob));
+          if (!ok) break;
+        }
         tc_fence_after();
+        const int s_next = s + 1 == G::kStages ? 0 : s + 1;
+        const bool over = mbar_test(&watch[s_next], phase ^ (s_next == 0));
         if (elect_one()) {
           const uint32_t ta = tmem_scales + s * G::kScaleCols, tb = ta + 8;
           const uint64_t ds = scale_desc(smem_u32(sS) + s * G::kScaleBytes);
@@ -415,91 +483,92 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx4_product(const __grid_consta
           tc_commit(&empty[s]);
           if (k == stages - 1) tc_commit(&acc_full[buf]);
         }
-        __syncwarp();
-        if (++s == G::kStages) {
-          s = 0;
-          phase ^= 1;
-        }
+        ready = __all_sync(0xffffffffu, over);
+        phase ^= s_next == 0;
+        s = s_next;
       }
       if (++buf == G::kAcc) {
         buf = 0;
         acc_phase ^= 1;
       }
     }
-  } else if (w >= 4 && w < 8) {
-    // 16 scale bytes a row (512 values, two stages) at a time; the next 16 are
-    // on their way while these are stored
-    const int t = tid - 128;
-    uint32_t it = 0;
-    bool ok = true;
+  } else if (w < kStoreWarp0) {
+    // A warp takes every other group of 512 values (two stages), 16 scale bytes
+    // a row.  A lane has rows lane, + 32, + 64 and + 96 of each 128, whose words
+    // stand next to each other: one 16-byte store for 4 blocks of 4 rows.  The
+    // loads of a group are over before its fence, which would wait for them.
     const int groups = (stages + 1) / 2;
     const int64_t weights = (int64_t)a.experts * a.outs;
+    const uint32_t one = 0x7F7F7F7Fu;
+    uint32_t before = 0, turn = w - kScaleWarp0;   // stages of the tiles before; groups until the warp's next
+    bool ok = true;
     for (int64_t tile = blockIdx.x; ok && tile < n_tiles; tile += gridDim.x) {
       int e, out0, row0, count;
       locate(tile, &e, &out0, &row0, &count);
-      constexpr int kRows = 1 + G::kScaleB;   // rows of a thread: one output, one or two rows
-      const uint8_t* src[kRows];
-      const int64_t wr = (int64_t)e * a.outs + out0 + t;
-      src[0] = wr < weights ? a.ws + wr * a.scale_bytes : nullptr;
+      constexpr int kTiles = 1 + G::kScaleB;
+      const uint8_t* src[kTiles][4];
 #pragma unroll
-      for (int j = 0; j < G::kScaleB; ++j) {
-        const int c = j * 128 + t;
-        src[1 + j] = c < count ? a.xs + ((int64_t)row0 + c) * a.scale_bytes : nullptr;
+      for (int j = 0; j < 4; ++j) {
+        const int64_t wr = (int64_t)e * a.outs + out0 + j * 32 + lane;
+        src[0][j] = wr < weights ? a.ws + wr * a.scale_bytes : nullptr;
+#pragma unroll
+        for (int i = 1; i < kTiles; ++i) {
+          const int r = (i - 1) * 128 + j * 32 + lane;
+          src[i][j] = r < count ? a.xs + ((int64_t)row0 + r) * a.scale_bytes : nullptr;
+        }
       }
-      const uint32_t one = 0x7F7F7F7Fu;
-      uint4 next[kRows];
-      auto fetch = [&](int g) {
+      int g = turn;
+      for (; ok && g < groups; g += kScaleWarps) {
+        uint32_t word[kTiles][4][4];
 #pragma unroll
-        for (int j = 0; j < kRows; ++j) {
-          next[j] = make_uint4(one, one, one, one);
-          if (src[j] && g < groups) next[j] = __ldg(reinterpret_cast<const uint4*>(src[j]) + g);
+        for (int i = 0; i < kTiles; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            uint4 v = make_uint4(one, one, one, one);
+            if (src[i][j]) v = __ldg(reinterpret_cast<const uint4*>(src[i][j]) + g);
+            word[i][j][0] = v.x;
+            word[i][j][1] = v.y;
+            word[i][j][2] = v.z;
+            word[i][j][3] = v.w;
+          }
+        if (g == groups - 1) {   // blocks past the row's end
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const int left = a.blocks - (g * 16 + q * 4);
+            const uint32_t keep = left >= 4 ? ~0u : left <= 0 ? 0u : (1u << (8 * left)) - 1u;
+#pragma unroll
+            for (int i = 0; i < kTiles; ++i)
+#pragma unroll
+              for (int j = 0; j < 4; ++j) word[i][j][q] = (word[i][j][q] & keep) | (one & ~keep);
+          }
         }
-      };
-      fetch(0);
-      for (int g = 0; ok && g < groups; ++g) {
-        uint32_t word[kRows][4];
-#pragma unroll
-        for (int j = 0; j < kRows; ++j) {
-          word[j][0] = next[j].x;
-          word[j][1] = next[j].y;
-          word[j][2] = next[j].z;
-          word[j][3] = next[j].w;
-          if (g == groups - 1)   // blocks past the row's end
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              const int left = a.blocks - (g * 16 + q * 4);
-              if (left < 4) {
-                const uint32_t keep = left <= 0 ? 0u : (1u << (8 * left)) - 1u;
-                word[j][q] = (word[j][q] & keep) | (one & ~keep);
-              }
-            }
-        }
-        fetch(g + 1);
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
           if (2 * g + half >= stages) break;
-          const int s = it % G::kStages;
-          ok = __all_sync(0xffffffffu, wait(&empty[s], ((it / G::kStages) & 1) ^ 1, &s_abort, a.glob));
+          const uint32_t n = before + 2 * g + half;
+          const int s = n % G::kStages;
+          ok = __all_sync(0xffffffffu, wait(&empty[s], ((n / G::kStages) & 1) ^ 1, &s_abort, a.glob));
           if (!ok) break;
-          uint8_t* sc = sS + s * G::kScaleBytes + (t & 31) * 16 + (t >> 5) * 4;
+          uint8_t* sc = sS + s * G::kScaleBytes + lane * 16;
 #pragma unroll
-          for (int q = 0; q < 2; ++q) {
-            *reinterpret_cast<uint32_t*>(sc + q * kScaleTile) = word[0][2 * half + q];
+          for (int q = 0; q < 2; ++q)
 #pragma unroll
-            for (int j = 0; j < G::kScaleB; ++j)
-              *reinterpret_cast<uint32_t*>(sc + (2 + q * G::kScaleB + j) * kScaleTile) = word[1 + j][2 * half + q];
-          }
+            for (int i = 0; i < kTiles; ++i)
+              *reinterpret_cast<uint4*>(sc + (i == 0 ? q : 2 + q * G::kScaleB + i - 1) * kScaleTile) =
+                  make_uint4(word[i][0][2 * half + q], word[i][1][2 * half + q], word[i][2][2 * half + q],
+                             word[i][3][2 * half + q]);
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           __syncwarp();
           if (lane == 0) mbar_arrive(&scaled[s]);
-          ++it;
         }
       }
+      turn = g - groups;
+      before += stages;
     }
-  } else if (w >= 8) {
+  } else {
     // a warp has the outputs of its quarter of the lanes, and every other run of 16 rows
-    const int quarter = w & 3, odd = (w - 8) >> 2;
-    const uint32_t stage = smem_u32(sStore) + (w - 8) * kStoreRows * kStorePitch;
+    const int quarter = w & 3, odd = (w - kStoreWarp0) >> 2;
+    const uint32_t stage = smem_u32(sStore) + (w - kStoreWarp0) * kStoreRows * kStorePitch;
     int buf = 0;
     uint32_t phase = 0;
     for (int64_t tile = blockIdx.x; tile < n_tiles; tile += gridDim.x) {
@@ -508,20 +577,22 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx4_product(const __grid_consta
       if (!__all_sync(0xffffffffu, wait(&acc_full[buf], phase, &s_abort, a.glob))) break;
       tc_fence_after();
       const int64_t out = out0 + quarter * 32;
-      const int n_out = a.outs - out < 32 ? (int)(a.outs - out) : 32;   // may be <= 0
+      const int64_t n_out = a.outs - out;   // outputs from here on, maybe none
       const uint32_t d = tmem + buf * G::kAccCols + ((uint32_t)(quarter * 32) << 16);
-      for (int c0 = odd * kStoreRows; c0 < count; c0 += 2 * kStoreRows) {
-        const int64_t at = ((int64_t)row0 + c0) * a.outs + out;
-        if (a.out_type == EBC_BF16)
-          store_half(d + c0, stage, (__nv_bfloat16*)a.ys + at, a.outs, n_out, count - c0, a.wide, lane);
-        else if (a.out_type == EBC_F16)
-          store_half(d + c0, stage, (__half*)a.ys + at, a.outs, n_out, count - c0, a.wide, lane);
-        else
-          store_full(d + c0, (float*)a.ys + at, a.outs, n_out, count - c0, lane);
+      const int64_t at = (int64_t)row0 * a.outs + out;
+      if (a.out_type == EBC_BF16) {
+        store_tile<__nv_bfloat16, kTN>(d, stage, (__nv_bfloat16*)a.ys + at, a.outs, n_out, odd, count, a.wide, lane,
+                                       &acc_empty[buf]);
+      } else if (a.out_type == EBC_F16) {
+        store_tile<__half, kTN>(d, stage, (__half*)a.ys + at, a.outs, n_out, odd, count, a.wide, lane,
+                                &acc_empty[buf]);
+      } else {
+        for (int c0 = odd * kStoreRows; c0 < count; c0 += 2 * kStoreRows)
+          store_full(d + c0, (float*)a.ys + at + c0 * a.outs, a.outs, n_out, count - c0, lane);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&acc_empty[buf]);
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&acc_empty[buf]);
       if (++buf == G::kAcc) {
         buf = 0;
         phase ^= 1;
@@ -531,7 +602,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx4_product(const __grid_consta
     const int es = a.out_type == EBC_F32 ? 4 : 2;
     const int64_t words = (a.rows - s_begin[a.experts]) * a.outs;
     uint8_t* y0 = (uint8_t*)a.ys + (int64_t)s_begin[a.experts] * a.outs * es;
-    for (int64_t i = (int64_t)blockIdx.x * 256 + (tid - 256); i < words; i += (int64_t)gridDim.x * 256) {
+    for (int64_t i = (int64_t)blockIdx.x * (32 * kStoreWarps) + (tid - 32 * kStoreWarp0); i < words;
+         i += (int64_t)gridDim.x * (32 * kStoreWarps)) {
       if (es == 4)
         reinterpret_cast<uint32_t*>(y0)[i] = 0u;
       else
