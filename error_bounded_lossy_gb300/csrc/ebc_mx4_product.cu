@@ -155,6 +155,45 @@ __device__ __forceinline__ uint32_t instr_desc(int n, int id) {
          ((uint32_t)id << 4) | ((uint32_t)id << 29);
 }
 
+// The tiles of a CTA, one after the other: a run of rows, and a place among the
+// outputs.  Steps are additions; the run's expert is mostly the last tile's or
+// the next, else searched for.
+struct Walk {
+  int step_run, step_out, run, out, e;
+  __device__ __forceinline__ Walk(int out_tiles, unsigned first, unsigned step)
+      : step_run((int)(step / (unsigned)out_tiles)),
+        step_out((int)(step % (unsigned)out_tiles)),
+        run((int)(first / (unsigned)out_tiles)),
+        out((int)(first % (unsigned)out_tiles)),
+        e(0) {}
+  // Whether there is a tile; then its first row and row count (at most tn).
+  // begin, tiles: per expert, its first row and the runs of the experts before.
+  __device__ __forceinline__ bool at(const int* begin, const int* tiles, int experts, int tn, int* row0,
+                                     int* count) {
+    if (run >= tiles[experts]) return false;
+    if (tiles[e + 1] <= run) ++e;
+    if (tiles[e + 1] <= run) {
+      int hi = experts;   // tiles[e] <= run < tiles[hi]
+      while (hi - e > 1) {
+        const int mid = (e + hi) >> 1;
+        if (tiles[mid] <= run) e = mid; else hi = mid;
+      }
+    }
+    *row0 = begin[e] + (run - tiles[e]) * tn;
+    const int left = begin[e + 1] - *row0;
+    *count = left < tn ? left : tn;
+    return true;
+  }
+  __device__ __forceinline__ void next(int out_tiles) {
+    run += step_run;
+    out += step_out;
+    if (out >= out_tiles) {
+      out -= out_tiles;
+      ++run;
+    }
+  }
+};
+
 struct Args {
   const uint8_t* xs;        // scales of the rows
   const uint8_t* ws;        // scales of the weights
@@ -389,34 +428,18 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx4_product(const __grid_consta
   const uint32_t tmem = s_tmem;
   const uint32_t tmem_scales = tmem + G::kAcc * G::kAccCols;
   const int out_tiles = (int)((a.outs + kM - 1) / kM);
-  const int64_t n_tiles = (int64_t)s_tiles[a.experts] * out_tiles;
   const int stages = (a.blocks + 7) / 8;   // stages of a tile
 
-  // tile -> expert, its first output, first row and row count
-  auto locate = [&](int64_t tile, int* e, int* out0, int* row0, int* count) {
-    const int run = (int)(tile / out_tiles);
-    *out0 = (int)(tile - (int64_t)run * out_tiles) * kM;
-    int lo = 0, hi = a.experts;   // s_tiles[lo] <= run < s_tiles[hi]
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (s_tiles[mid] <= run) lo = mid; else hi = mid;
-    }
-    *e = lo;
-    *row0 = s_begin[lo] + (run - s_tiles[lo]) * kTN;
-    const int left = s_begin[lo + 1] - *row0;
-    *count = left < kTN ? left : kTN;
-  };
-
+  Walk walk(out_tiles, blockIdx.x, gridDim.x);
+  int row0, count;
   uint32_t issued = 0;   // stages that warp 0 has asked for
   if (w == 0) {
     int s = 0;
     uint32_t phase = 1;   // of the barriers that stages are given back on
     bool ok = true;
-    for (int64_t tile = blockIdx.x; ok && tile < n_tiles; tile += gridDim.x) {
-      int e, out0, row0, count;
-      locate(tile, &e, &out0, &row0, &count);
+    for (; ok && walk.at(s_begin, s_tiles, a.experts, kTN, &row0, &count); walk.next(out_tiles)) {
       const int boxes = (count + G::kBox - 1) / G::kBox;
-      const int wrow = (int)(e * a.outs) + out0;
+      const int wrow = (int)(walk.e * a.outs) + walk.out * kM;
       for (int k = 0; k < stages; ++k) {
         ok = __all_sync(0xffffffffu, wait(&empty[s], phase, &s_abort, a.glob));
         if (!ok) break;
@@ -446,9 +469,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx4_product(const __grid_consta
     uint32_t phase = 0, acc_phase = 1;
     bool ok = true, ready = false;
     uint64_t* const watch = lane & 1 ? scaled : full;
-    for (int64_t tile = blockIdx.x; ok && tile < n_tiles; tile += gridDim.x) {
-      int e, out0, row0, count;
-      locate(tile, &e, &out0, &row0, &count);
+    for (; ok && walk.at(s_begin, s_tiles, a.experts, kTN, &row0, &count); walk.next(out_tiles)) {
       const uint32_t id0 = instr_desc((count + 15) & ~15, 0), id2 = instr_desc((count + 15) & ~15, 2);
       ok = __all_sync(0xffffffffu, wait(&acc_empty[buf], acc_phase, &s_abort, a.glob));
       if (!ok) break;
@@ -502,14 +523,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx4_product(const __grid_consta
     const uint32_t one = 0x7F7F7F7Fu;
     uint32_t before = 0, turn = w - kScaleWarp0;   // stages of the tiles before; groups until the warp's next
     bool ok = true;
-    for (int64_t tile = blockIdx.x; ok && tile < n_tiles; tile += gridDim.x) {
-      int e, out0, row0, count;
-      locate(tile, &e, &out0, &row0, &count);
+    for (; ok && walk.at(s_begin, s_tiles, a.experts, kTN, &row0, &count); walk.next(out_tiles)) {
       constexpr int kTiles = 1 + G::kScaleB;
       const uint8_t* src[kTiles][4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const int64_t wr = (int64_t)e * a.outs + out0 + j * 32 + lane;
+        const int64_t wr = walk.e * a.outs + walk.out * kM + j * 32 + lane;
         src[0][j] = wr < weights ? a.ws + wr * a.scale_bytes : nullptr;
 #pragma unroll
         for (int i = 1; i < kTiles; ++i) {
@@ -571,12 +590,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx4_product(const __grid_consta
     const uint32_t stage = smem_u32(sStore) + (w - kStoreWarp0) * kStoreRows * kStorePitch;
     int buf = 0;
     uint32_t phase = 0;
-    for (int64_t tile = blockIdx.x; tile < n_tiles; tile += gridDim.x) {
-      int e, out0, row0, count;
-      locate(tile, &e, &out0, &row0, &count);
+    for (; walk.at(s_begin, s_tiles, a.experts, kTN, &row0, &count); walk.next(out_tiles)) {
       if (!__all_sync(0xffffffffu, wait(&acc_full[buf], phase, &s_abort, a.glob))) break;
       tc_fence_after();
-      const int64_t out = out0 + quarter * 32;
+      const int64_t out = (int64_t)walk.out * kM + quarter * 32;
       const int64_t n_out = a.outs - out;   // outputs from here on, maybe none
       const uint32_t d = tmem + buf * G::kAccCols + ((uint32_t)(quarter * 32) << 16);
       const int64_t at = (int64_t)row0 * a.outs + out;
