@@ -14,69 +14,103 @@ namespace {
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanWarps = kPlanThreads / 32;
 
+constexpr int kPlanBatch = 8;   // rounds of 32 slots whose ids a warp has in flight
+
+// Ids of up to kPlanBatch rounds from slot s on; -1 past the end and for what
+// is no expert.
 template <typename Id>
-__device__ __forceinline__ int read_id(const Id* ids, int64_t s, int64_t n, int E, bool* bad) {
-  if (s >= n) return -1;
-  const Id v = ids[s];
-  if (v >= (Id)E) *bad = true;
-  return v >= 0 && v < (Id)E ? (int)v : -1;
+__device__ __forceinline__ void read_ids(const Id* ids, int64_t s, int64_t last, int E, int (&e)[kPlanBatch],
+                                         bool* bad) {
+  Id v[kPlanBatch];
+#pragma unroll
+  for (int i = 0; i < kPlanBatch; ++i) v[i] = s + 32 * i < last ? ids[s + 32 * i] : (Id)-1;
+#pragma unroll
+  for (int i = 0; i < kPlanBatch; ++i) {
+    if (v[i] >= (Id)E) *bad = true;
+    e[i] = v[i] >= 0 && v[i] < (Id)E ? (int)v[i] : -1;
+  }
+}
+
+// The lanes of equal value, for values 0 .. 2^bits - 1: one vote a bit.  (The
+// match instruction has the same answer and took 53 cycles a warp here, which
+// made it most of the plan's time.)
+__device__ __forceinline__ unsigned equal_lanes(int v, int bits) {
+  unsigned same = 0xffffffffu;
+  for (int b = 0; b < bits; ++b) {
+    const unsigned set = __ballot_sync(0xffffffffu, (v >> b) & 1);
+    same &= (v >> b) & 1 ? set : ~set;
+  }
+  return same;
 }
 
 // Stable counting sort of the n slots by expert, in one launch of one cluster.
 //
 // The slots are split evenly among the cluster's warps, in order.  Each warp
-// counts its slots per expert (lanes of equal expert found with one match per
-// 32 slots); the counts become, per warp and expert, the first row of that
-// warp's slots (a scan over the warps of a CTA in shared memory, over the CTAs
-// through distributed shared memory, over the experts by one thread each);
-// then each warp walks its slots again and hands out rows.  No atomics on
-// shared counters decide an order, so the plan is the same in every run.
+// counts its slots per expert (lanes of equal expert found by votes); the counts become, per warp and expert, the warp's first place
+// among the expert's slots of its CTA (a scan over the warps), which the CTAs'
+// totals (read through distributed shared memory) and a scan over the experts
+// turn into rows; then each warp walks its slots again and hands out rows.  No
+// atomics on shared counters decide an order, so the plan is the same in every
+// run.
 //
-// Bound by latency: the ids are read twice (the second time from L1/L2) and
-// two ints a slot are written, far below a microsecond of bandwidth at
-// 65,536 slots.
+// Bound by latency: the ids are read once where a warp's share is one batch
+// (else twice) and two ints a slot are written, far below a microsecond of
+// bandwidth at 65,536 slots.
 template <typename Id>
 __global__ void __launch_bounds__(kPlanThreads) k_moe_plan(const Id* __restrict__ ids, int64_t n, int E,
                                                            int32_t* __restrict__ rows, int32_t* __restrict__ place,
                                                            int32_t* __restrict__ offsets, Glob* glob) {
   extern __shared__ uint32_t sm[];
-  uint32_t* hist = sm;                        // [warps][E]
-  uint32_t* total = sm + kPlanWarps * E;      // [E] this CTA's slots per expert
+  const int pitch = E | 1;                       // an odd stride: the warps' counts of an expert in 32 banks
+  uint32_t* hist = sm;                           // [warps][pitch]
+  uint32_t* total = sm + kPlanWarps * pitch;     // [E] this CTA's slots per expert
+  uint32_t* base = total + E;                    // [E] first row of this CTA's slots of each expert
   __shared__ uint32_t s_warp[kPlanWarps];
   __shared__ uint32_t s_live;
   cg::cluster_group cluster = cg::this_cluster();
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
   const int C = (int)cluster.num_blocks(), c = (int)cluster.block_rank();
-  for (int i = tid; i < kPlanWarps * E; i += kPlanThreads) hist[i] = 0u;
+  for (int i = tid; i < kPlanWarps * pitch; i += kPlanThreads) hist[i] = 0u;
   pdl_enter();
-  __syncthreads();
 
   const int64_t warps = (int64_t)C * kPlanWarps;
   const int64_t share = ((n + warps - 1) / warps + 31) & ~(int64_t)31;
   const int64_t first = ((int64_t)c * kPlanWarps + w) * share;
   const int64_t last = first + share < n ? first + share : n;
-  uint32_t* mine = hist + w * E;
+  constexpr int kStep = 32 * kPlanBatch;
+  const bool once = share <= kStep;
+  const int bits = 32 - __clz(E);   // of 0 (none) .. E
+  uint32_t* mine = hist + w * pitch;
   bool bad = false;
-  for (int64_t s = first; s < last; s += 32) {
-    const int e = read_id(ids, s + lane, n, E, &bad);
-    const unsigned same = __match_any_sync(0xffffffffu, e);
-    if (e >= 0 && lane == __ffs(same) - 1) mine[e] += (uint32_t)__popc(same);
-    __syncwarp();
+  int e[kPlanBatch];
+  read_ids(ids, first + lane, last, E, e, &bad);
+  __syncthreads();   // the counts are zero
+  for (int64_t s = first; s < last; s += kStep) {
+    if (s > first) read_ids(ids, s + lane, last, E, e, &bad);
+#pragma unroll
+    for (int i = 0; i < kPlanBatch; ++i) {
+      if (s + 32 * i >= last) break;
+      const unsigned same = equal_lanes(e[i] + 1, bits);
+      if (e[i] >= 0 && lane == __ffs(same) - 1) mine[e[i]] += (uint32_t)__popc(same);
+      __syncwarp();
+    }
   }
   if (__any_sync(0xffffffffu, bad) && lane == 0) record_error(glob, EBC_ERR_INVALID_ARG);
   __syncthreads();
-  // counts -> slots of the warps before, per expert
-  if (tid < E) {
-    uint32_t run = 0;
-    for (int i = 0; i < kPlanWarps; ++i) {
-      const uint32_t v = hist[i * E + tid];
-      hist[i * E + tid] = run;
-      run += v;
+  // counts -> slots of the warps before, a warp an expert and a lane a warp
+  for (int x = w; x < E; x += kPlanWarps) {
+    const uint32_t v = hist[lane * pitch + x];
+    uint32_t inc = v;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const uint32_t u = __shfl_up_sync(0xffffffffu, inc, off);
+      if (lane >= off) inc += u;
     }
-    total[tid] = run;
+    hist[lane * pitch + x] = inc - v;
+    if (lane == 31) total[x] = inc;
   }
   cluster.sync();
-  // over the CTAs, then over the experts
+  // over the CTAs, then over the experts, a thread each
   uint32_t before = 0, all = 0;
   if (tid < E)
     for (int i = 0; i < C; ++i) {
@@ -92,33 +126,37 @@ __global__ void __launch_bounds__(kPlanThreads) k_moe_plan(const Id* __restrict_
   }
   if (lane == 31) s_warp[w] = inc;
   __syncthreads();
-  uint32_t pre = 0;
-  for (int i = 0; i < w; ++i) pre += s_warp[i];
+  uint32_t pre = lane < w ? s_warp[lane] : 0u;
+  pre = __reduce_add_sync(0xffffffffu, pre);
   const uint32_t start = pre + inc - all;
   if (tid < E) {
     if (c == 0) offsets[tid] = (int32_t)start;
-    const uint32_t base = start + before;
-    for (int i = 0; i < kPlanWarps; ++i) hist[i * E + tid] += base;
+    base[tid] = start + before;
   }
   if (tid == E - 1) {
     s_live = start + all;
     if (c == 0) offsets[E] = (int32_t)(start + all);
   }
-  cluster.sync();   // the totals have been read; hist and s_live are complete
-  for (int64_t s = first; s < last; s += 32) {
+  cluster.sync();   // the totals have been read; base and s_live are complete
+  for (int64_t s = first; s < last; s += kStep) {
     bool ignore = false;
-    const int e = read_id(ids, s + lane, n, E, &ignore);
-    const unsigned same = __match_any_sync(0xffffffffu, e);
-    if (e >= 0) {
-      const uint32_t r = mine[e] + (uint32_t)__popc(same & ((1u << lane) - 1u));
-      place[s + lane] = (int32_t)r;
-      rows[r] = (int32_t)(s + lane);
-    } else if (s + lane < n) {
-      place[s + lane] = -1;
+    if (!once) read_ids(ids, s + lane, last, E, e, &ignore);
+#pragma unroll
+    for (int i = 0; i < kPlanBatch; ++i) {
+      const int64_t at = s + 32 * i + lane;
+      if (s + 32 * i >= last) break;
+      const unsigned same = equal_lanes(e[i] + 1, bits);
+      if (e[i] >= 0) {
+        const uint32_t r = base[e[i]] + mine[e[i]] + (uint32_t)__popc(same & ((1u << lane) - 1u));
+        place[at] = (int32_t)r;
+        rows[r] = (int32_t)at;
+      } else if (at < last) {
+        place[at] = -1;
+      }
+      __syncwarp();
+      if (e[i] >= 0 && lane == __ffs(same) - 1) mine[e[i]] += (uint32_t)__popc(same);
+      __syncwarp();
     }
-    __syncwarp();
-    if (e >= 0 && lane == __ffs(same) - 1) mine[e] += (uint32_t)__popc(same);
-    __syncwarp();
   }
   for (int64_t r = (int64_t)s_live + (int64_t)c * kPlanThreads + tid; r < n; r += (int64_t)C * kPlanThreads)
     rows[r] = -1;
@@ -138,10 +176,13 @@ __device__ __forceinline__ int64_t live_rows(const int32_t* offsets, int E, int6
 }
 
 constexpr int kRowWarps = 8;
-constexpr int kScatterU = 4;   // vectors a lane holds of one piece of a row
+// Vectors of V bytes a lane holds of one piece of a row.
+template <int V>
+constexpr int scatter_vectors() {
+  return V >= 8 ? 4 : 8;
+}
 
-// xs[place[t, j]] = x[t]: a warp takes a piece of a token's row (kScatterU
-// vectors a lane), reads it once and writes it to every choice's row, so x is
+// xs[place[t, j]] = x[t]: a warp takes a piece of a token's row, reads it once and writes it to every choice's row, so x is
 // read once from memory.  Rows past the last expert's become zero.
 // Bound by the bandwidth of the writes.
 template <typename T, int V>
@@ -152,7 +193,7 @@ __global__ void __launch_bounds__(32 * kRowWarps) k_moe_dispatch(const T* __rest
                                                                  T* __restrict__ xs, Glob* glob) {
   pdl_enter();
   using R = Vec<T, V>;
-  constexpr int kPiece = 32 * kScatterU * R::kN;   // elements of a piece
+  constexpr int kScatterU = scatter_vectors<V>(), kPiece = 32 * kScatterU * R::kN;   // elements of a piece
   const int lane = threadIdx.x & 31;
   const int64_t n = tokens * top, pieces = (width + kPiece - 1) / kPiece;
   const int64_t live = live_rows(offsets, E, n);
@@ -195,10 +236,22 @@ __global__ void __launch_bounds__(32 * kRowWarps) k_moe_dispatch(const T* __rest
   }
 }
 
+// Vectors of V bytes a lane takes of a row at a time (1 KB of a wide row a
+// warp), and rows in flight.  Longer pieces of fewer rows suit the memory
+// better than more rows at once: 8192 tokens x 8 choices x 4096 bf16 took
+// 95 us so; 112 with 512 bytes of two rows, 125 of four, 189 of eight, and 134
+// with 1 KB of four rows, 100 with 2 KB of one.
+template <typename T, int V>
+constexpr int gather_vectors() {
+  constexpr int kN = V / (int)sizeof(T);
+  return kN >= 4 ? 2 : 8 / kN;
+}
+constexpr int kGatherRows = 2;
+
 // y[t] = sum over j of w[t, j] * ys[place[t, j]] (weights null: 1), held in
 // fp32 and added in the order of j; a dropped choice adds nothing, whatever
-// its weight.  A warp takes one vector a lane of a token's row, four rows'
-// loads in flight.  Bound by the bandwidth of the reads.
+// its weight.  A warp takes a piece of a token's row, kGatherRows rows' loads
+// in flight.  Bound by the bandwidth of the reads.
 template <typename T, int V>
 __global__ void __launch_bounds__(32 * kRowWarps) k_moe_combine(const T* __restrict__ ys, int64_t ld, int64_t tokens,
                                                                 int top, int64_t width,
@@ -207,101 +260,135 @@ __global__ void __launch_bounds__(32 * kRowWarps) k_moe_combine(const T* __restr
                                                                 Glob* glob) {
   pdl_enter();
   using R = Vec<T, V>;
-  constexpr int kPiece = 32 * R::kN;
+  constexpr int kU = gather_vectors<T, V>(), kStep = 32 * R::kN, kPiece = kU * kStep;
   const int lane = threadIdx.x & 31;
-  const int64_t n = tokens * top, pieces = (width + kPiece - 1) / kPiece, units = tokens * pieces;
+  const int64_t n = tokens * top;
+  const unsigned pieces = (unsigned)((width + kPiece - 1) / kPiece);
+  const int64_t units = tokens * pieces;
   for (int64_t u = (int64_t)blockIdx.x * kRowWarps + (threadIdx.x >> 5); u < units;
        u += (int64_t)gridDim.x * kRowWarps) {
-    const int64_t t = u / pieces, h = (u - t * pieces) * kPiece + lane * R::kN;
-    float acc[R::kN];
+    const int64_t t = units <= UINT32_MAX ? (unsigned)u / pieces : u / pieces;
+    const int64_t h = (u - t * pieces) * kPiece + lane * R::kN;
+    const int left = (int)(width - h < kPiece ? width - h : kPiece);   // of the lane's values; may be <= 0
+    float acc[kU][R::kN];
 #pragma unroll
-    for (int k = 0; k < R::kN; ++k) acc[k] = 0.f;
+    for (int i = 0; i < kU; ++i)
+#pragma unroll
+      for (int k = 0; k < R::kN; ++k) acc[i][k] = 0.f;
     for (int j0 = 0; j0 < top; j0 += 32) {
       const int m = top - j0 < 32 ? top - j0 : 32;
       const int64_t s = t * top + j0 + lane;
       const int32_t p_lane = lane < m ? read_place(place, s, n, glob) : -1;
       const float w_lane = lane < m && weights ? weights[s] : 1.f;
-      for (int j = 0; j < m; j += 4) {
-        R v[4];
-        int32_t p[4];
-        float w[4];
+      for (int j = 0; j < m; j += kGatherRows) {
+        R v[kGatherRows][kU];
+        int32_t p[kGatherRows];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          p[i] = __shfl_sync(0xffffffffu, p_lane, (j + i) & 31);
-          w[i] = __shfl_sync(0xffffffffu, w_lane, (j + i) & 31);
-          if (j + i >= m) p[i] = -1;
-          if (p[i] >= 0 && h < width)
-            v[i].raw = *reinterpret_cast<const typename Raw<V>::T*>(ys + (int64_t)p[i] * ld + h);
+        for (int r = 0; r < kGatherRows; ++r) {
+          p[r] = __shfl_sync(0xffffffffu, p_lane, (j + r) & 31);
+          if (j + r >= m) p[r] = -1;
+          const T* src = ys + (int64_t)p[r] * ld + h;
+          if (p[r] >= 0)
+#pragma unroll
+            for (int i = 0; i < kU; ++i)
+              if (i * kStep < left) v[r][i].raw = *reinterpret_cast<const typename Raw<V>::T*>(src + i * kStep);
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (p[i] >= 0 && h < width)
+        for (int r = 0; r < kGatherRows; ++r) {
+          const float w = __shfl_sync(0xffffffffu, w_lane, (j + r) & 31);
+          if (p[r] >= 0)
 #pragma unroll
-            for (int k = 0; k < R::kN; ++k) acc[k] = fmaf(w[i], to_f32(v[i].e[k]), acc[k]);
+            for (int i = 0; i < kU; ++i)
+              if (i * kStep < left)
+#pragma unroll
+                for (int k = 0; k < R::kN; ++k) acc[i][k] = fmaf(w, to_f32(v[r][i].e[k]), acc[i][k]);
+        }
       }
     }
-    if (h < width) {
-      R o;
 #pragma unroll
-      for (int k = 0; k < R::kN; ++k) o.e[k] = from_f32<T>(acc[k]);
-      *reinterpret_cast<typename Raw<V>::T*>(y + t * width + h) = o.raw;
-    }
+    for (int i = 0; i < kU; ++i)
+      if (i * kStep < left) {
+        R o;
+#pragma unroll
+        for (int k = 0; k < R::kN; ++k) o.e[k] = from_f32<T>(acc[i][k]);
+        *reinterpret_cast<typename Raw<V>::T*>(y + t * width + h + i * kStep) = o.raw;
+      }
   }
 }
 
-// One slot a warp: dys[p] = w * dy[t] and dw = <dy[t], ys[p]> in one pass over
-// the two rows (dy[t] comes from L1 or L2 for all but the first of a token's
-// choices).  The dot product is held in fp32: per lane in the order of the
-// row, then over the lanes by a fixed tree.  Rows past the last expert's
-// become zero.  Bound by bandwidth.
+// dys[p] = w * dy[t] and dw = <dy[t], ys[p]> in one pass over the two rows of a
+// slot (dy[t] comes from L1 or L2 for all but the first of a token's choices).
+// `split` warps of a CTA share a slot, so that few slots still fill the
+// machine: 777 tokens x 3 choices x 1003 fp16 took 7.4 us with one warp each.
+// The dot product is held in fp32: per lane in the order of the row, over the
+// lanes by a fixed tree, then over the warps in order.  Rows past the last
+// expert's become zero.  Bound by bandwidth.
 template <typename T, int V>
 __global__ void __launch_bounds__(32 * kRowWarps) k_moe_combine_grad(
     const T* __restrict__ dy, int64_t ld_dy, const T* __restrict__ ys, int64_t ld_ys, int64_t tokens, int top,
     int64_t width, const int32_t* __restrict__ place, const int32_t* __restrict__ offsets, int E,
-    const float* __restrict__ weights, T* __restrict__ dys, float* __restrict__ dw, Glob* glob) {
+    const float* __restrict__ weights, T* __restrict__ dys, float* __restrict__ dw, int split, Glob* glob) {
+  __shared__ float s_dot[kRowWarps];
   pdl_enter();
   using R = Vec<T, V>;
-  constexpr int kStep = 32 * R::kN;
-  const int lane = threadIdx.x & 31;
+  constexpr int kStep = 32 * R::kN, kU = R::kN >= 4 ? 4 : 8;   // vectors of each row in flight
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  const int part = w & (split - 1), slots = kRowWarps / split;
   const int64_t n = tokens * top;
   const int64_t live = live_rows(offsets, E, n);
   const int64_t units = n + (n - live);
-  for (int64_t s = (int64_t)blockIdx.x * kRowWarps + (threadIdx.x >> 5); s < units;
-       s += (int64_t)gridDim.x * kRowWarps) {
-    if (s >= n) {
+  const int64_t h0 = (int64_t)part * kU * kStep + lane * R::kN, stride = (int64_t)split * kU * kStep;
+  for (int64_t s0 = (int64_t)blockIdx.x * slots; s0 < units; s0 += (int64_t)gridDim.x * slots) {
+    const int64_t s = s0 + w / split;
+    const int32_t p = s < n ? read_place(place, s, n, glob) : -1;
+    float dot = 0.f;
+    if (p >= 0) {
+      const float scale = weights[s];
+      const T* a = dy + (n <= UINT32_MAX ? (unsigned)s / (unsigned)top : s / top) * ld_dy + h0;
+      const T* b = ys + (int64_t)p * ld_ys + h0;
+      T* dst = dys + (int64_t)p * width + h0;
+      for (int64_t left = width - h0; left > 0; left -= stride) {
+        R va[kU], vb[kU];
+#pragma unroll
+        for (int i = 0; i < kU; ++i)
+          if (i * kStep < left) {
+            va[i].raw = *reinterpret_cast<const typename Raw<V>::T*>(a + i * kStep);
+            vb[i].raw = *reinterpret_cast<const typename Raw<V>::T*>(b + i * kStep);
+          }
+#pragma unroll
+        for (int i = 0; i < kU; ++i)
+          if (i * kStep < left) {
+            R o;
+#pragma unroll
+            for (int k = 0; k < R::kN; ++k) {
+              const float g = to_f32(va[i].e[k]);
+              dot = fmaf(g, to_f32(vb[i].e[k]), dot);
+              o.e[k] = from_f32<T>(scale * g);
+            }
+            *reinterpret_cast<typename Raw<V>::T*>(dst + i * kStep) = o.raw;
+          }
+        a += stride;
+        b += stride;
+        dst += stride;
+      }
+#pragma unroll
+      for (int off = 16; off; off >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, off);
+    } else if (s >= n && s < units) {
       T* dst = dys + (live + (s - n)) * width;
       R z;
 #pragma unroll
       for (int k = 0; k < R::kN; ++k) z.e[k] = from_f32<T>(0.f);
-      for (int64_t h = lane * R::kN; h < width; h += kStep) *reinterpret_cast<typename Raw<V>::T*>(dst + h) = z.raw;
-      continue;
+      for (int64_t h = (part * 32 + lane) * R::kN; h < width; h += split * kStep)
+        *reinterpret_cast<typename Raw<V>::T*>(dst + h) = z.raw;
     }
-    const int32_t p = read_place(place, s, n, glob);
-    if (p < 0) {
-      if (lane == 0) dw[s] = 0.f;
-      continue;
+    if (split > 1) {
+      __syncthreads();   // the sums of the slots before have been read
+      if (lane == 0) s_dot[w] = dot;
+      __syncthreads();
+      if (part == 0 && lane == 0)
+        for (int i = 1; i < split; ++i) dot += s_dot[w + i];
     }
-    const float w = weights[s];
-    const T* a = dy + (s / top) * ld_dy;
-    const T* b = ys + (int64_t)p * ld_ys;
-    T* dst = dys + (int64_t)p * width;
-    float dot = 0.f;
-#pragma unroll 4
-    for (int64_t h = lane * R::kN; h < width; h += kStep) {
-      R va, vb, o;
-      va.raw = *reinterpret_cast<const typename Raw<V>::T*>(a + h);
-      vb.raw = *reinterpret_cast<const typename Raw<V>::T*>(b + h);
-#pragma unroll
-      for (int k = 0; k < R::kN; ++k) {
-        const float g = to_f32(va.e[k]);
-        dot = fmaf(g, to_f32(vb.e[k]), dot);
-        o.e[k] = from_f32<T>(w * g);
-      }
-      *reinterpret_cast<typename Raw<V>::T*>(dst + h) = o.raw;
-    }
-#pragma unroll
-    for (int off = 16; off; off >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, off);
-    if (lane == 0) dw[s] = dot;
+    if (part == 0 && lane == 0 && s < n) dw[s] = dot;
   }
 }
 
@@ -326,13 +413,20 @@ bool aligned(const void* p, int bytes) { return ((uintptr_t)p & (uintptr_t)(byte
 template <typename Id>
 cudaError_t plan_t(const CallView& v, const Id* ids, int64_t n, int E, int32_t* rows, int32_t* place,
                    int32_t* offsets, cudaStream_t st) {
-  const size_t smem = sizeof(uint32_t) * (size_t)(kPlanWarps + 1) * E;
+  const size_t smem = sizeof(uint32_t) * ((size_t)kPlanWarps * (E | 1) + 2 * (size_t)E);
   if (smem > 48 * 1024) {
     const cudaError_t e =
         cudaFuncSetAttribute(k_moe_plan<Id>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
   }
-  const unsigned C = n <= 4096 ? 1 : 8;
+  // CTAs of the cluster: a round of 1024 slots a CTA takes about a microsecond,
+  // a larger cluster about as long to come together (1024 slots: 4.3 us with
+  // one CTA, 4.8 with 8; 8192: 11.3, 5.3, and 5.8 with 16; 65,536: 71, 12.5, 9.1)
+  const unsigned C = n <= 1024 ? 1 : n <= 8192 ? 8 : 16;
+  if (C > 8) {
+    const cudaError_t e = cudaFuncSetAttribute(k_moe_plan<Id>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) return e;
+  }
   return launch_named(v, "k_moe_plan", st, k_moe_plan<Id>, dim3(C), dim3(kPlanThreads), smem, C, ids, n, E, rows,
                       place, offsets, v.glob);
 }
@@ -374,7 +468,7 @@ int ebc_moe_dispatch(ebc_ctx* ctx, const void* d_x, int64_t ld_x, int type, int6
   return cuda_code(with_type(type, vb, [&](auto tag) {
     using T = typename decltype(tag)::T;
     constexpr int V = decltype(tag)::V;
-    const int64_t piece = 32 * kScatterU * (V / (int)sizeof(T));
+    const int64_t piece = 32 * scatter_vectors<V>() * (V / (int)sizeof(T));
     return launch_named(v, "k_moe_dispatch", st, k_moe_dispatch<T, V>,
                         dim3(row_grid(tokens * ((width + piece - 1) / piece), v.nsm)), dim3(32 * kRowWarps), 0, 1,
                         (const T*)d_x, ld_x, tokens, top, width, d_place, d_offsets, n_experts, (T*)d_xs, v.glob);
@@ -396,7 +490,7 @@ int ebc_moe_combine(ebc_ctx* ctx, const void* d_ys, int64_t ld_ys, int type, int
   return cuda_code(with_type(type, vb, [&](auto tag) {
     using T = typename decltype(tag)::T;
     constexpr int V = decltype(tag)::V;
-    const int64_t piece = 32 * (V / (int)sizeof(T));
+    const int64_t piece = 32 * (V / (int)sizeof(T)) * gather_vectors<T, V>();
     return launch_named(v, "k_moe_combine", st, k_moe_combine<T, V>,
                         dim3(row_grid(tokens * ((width + piece - 1) / piece), v.nsm)), dim3(32 * kRowWarps), 0, 1,
                         (const T*)d_ys, ld_ys, tokens, top, width, d_place, d_weights, (T*)d_y, v.glob);
@@ -424,10 +518,13 @@ int ebc_moe_combine_grad(ebc_ctx* ctx, const void* d_dy, int64_t ld_dy, const vo
   return cuda_code(with_type(type, vb, [&](auto tag) {
     using T = typename decltype(tag)::T;
     constexpr int V = decltype(tag)::V;
-    return launch_named(v, "k_moe_combine_grad", st, k_moe_combine_grad<T, V>,
-                        dim3(row_grid(tokens * top, v.nsm)), dim3(32 * kRowWarps), 0, 1, (const T*)d_dy, ld_dy,
-                        (const T*)d_ys, ld_ys, tokens, top, width, d_place, d_offsets, n_experts, d_weights,
-                        (T*)d_dys, d_dweights, v.glob);
+    // warps a slot: until there are 32 a SM, or until a warp's share is one round
+    const int64_t n = tokens * top, round = 32 * (V / (int)sizeof(T)) * (V / (int)sizeof(T) >= 4 ? 4 : 8);
+    int split = 1;
+    while (split < kRowWarps && n * split < 32 * (int64_t)v.nsm && split * round < width) split *= 2;
+    return launch_named(v, "k_moe_combine_grad", st, k_moe_combine_grad<T, V>, dim3(row_grid(n * split, v.nsm)),
+                        dim3(32 * kRowWarps), 0, 1, (const T*)d_dy, ld_dy, (const T*)d_ys, ld_ys, tokens, top, width,
+                        d_place, d_offsets, n_experts, d_weights, (T*)d_dys, d_dweights, split, v.glob);
   }));
 }
 

@@ -8,43 +8,68 @@ namespace {
 
 constexpr int kMxWarps = 8;
 constexpr int kSpan = 512;   // values of a warp's piece: one 16-byte group of scales
+// a / b; most often in 32 bits, a fifth of the instructions
+__device__ __forceinline__ int64_t divide(int64_t a, int64_t b) {
+  return a <= UINT32_MAX ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
+}
+
 constexpr int kLane = 8;     // consecutive values of a lane; a block is four lanes
 
-// Eight consecutive values of a row as fp32 (zeros past its end): 16-byte
-// loads where the row is aligned for them, else one by one.
+// Eight consecutive values of a row (zeros past its end) as they are in
+// memory: 16-byte loads where the row is aligned for them, else one by one.
+template <typename T>
+struct Eight {
+  static constexpr int kWords = kLane * (int)sizeof(T) / 4;
+  union {
+    uint4 raw[kWords / 4];
+    uint32_t word[kWords];
+    T e[kLane];
+  };
+  __device__ __forceinline__ Eight() {}
+};
 template <typename T, bool kAligned>
-__device__ __forceinline__ void load8(const T* row, int64_t h, int64_t width, float (&v)[kLane]) {
+__device__ __forceinline__ void load8(const T* row, int64_t h, int64_t width, Eight<T>* v) {
   if (kAligned && h + kLane <= width) {
-    constexpr int kN = 16 / (int)sizeof(T);
 #pragma unroll
-    for (int i = 0; i < kLane / kN; ++i) {
-      Vec<T, 16> r;
-      r.raw = *reinterpret_cast<const uint4*>(row + h + i * kN);
-#pragma unroll
-      for (int k = 0; k < kN; ++k) v[i * kN + k] = to_f32(r.e[k]);
-    }
+    for (int i = 0; i < Eight<T>::kWords / 4; ++i) v->raw[i] = reinterpret_cast<const uint4*>(row + h)[i];
   } else {
 #pragma unroll
-    for (int k = 0; k < kLane; ++k) v[k] = h + k < width ? to_f32(row[h + k]) : 0.f;
+    for (int k = 0; k < kLane; ++k) v->e[k] = h + k < width ? row[h + k] : from_f32<T>(0.f);
   }
 }
 
-// The lane's eight codes and its block's scale byte.
-__device__ __forceinline__ uint32_t encode8(const float (&v)[kLane], uint32_t* scale) {
-  // the largest magnitude by its bits: magnitudes order as integers do, and a
-  // NaN's bits are above an infinity's, so neither gets lost
+// The largest magnitude of a block, four lanes' values.  Magnitudes order as
+// their bits do, and a NaN's bits are above an infinity's, so neither gets
+// lost; 16-bit types are compared two at a time.
+__device__ __forceinline__ float block_max(const Eight<float>& v) {
   uint32_t top = 0;
 #pragma unroll
-  for (int k = 0; k < kLane; ++k) top = max(top, __float_as_uint(v[k]) & 0x7FFFFFFFu);
+  for (int k = 0; k < kLane; ++k) top = max(top, v.word[k] & 0x7FFFFFFFu);
   top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
   top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-  const uint32_t s = mx4_scale(__uint_as_float(top));
+  return __uint_as_float(top);
+}
+template <typename T>
+__device__ __forceinline__ float block_max(const Eight<T>& v) {
+  uint32_t top = 0;
+#pragma unroll
+  for (int k = 0; k < kLane / 2; ++k) top = __vmaxu2(top, v.word[k] & 0x7FFF7FFFu);
+  top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, 1));
+  top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, 2));
+  const uint16_t one = (uint16_t)max(top & 0xFFFFu, top >> 16);
+  return to_f32(*reinterpret_cast<const T*>(&one));
+}
+
+// The lane's eight codes and its block's scale byte.
+template <typename T>
+__device__ __forceinline__ uint32_t encode8(const Eight<T>& v, uint32_t* scale) {
+  const uint32_t s = mx4_scale(block_max(v));
   *scale = s;
   if (s == 255u) return 0u;
   const float inv = mx4_inverse(s);
   uint32_t c = 0;
 #pragma unroll
-  for (int k = 0; k < kLane; k += 2) c |= mx4_pair(v[k] * inv, v[k + 1] * inv) << (4 * k);
+  for (int k = 0; k < kLane; k += 2) c |= mx4_pair(to_f32(v.e[k]) * inv, to_f32(v.e[k + 1]) * inv) << (4 * k);
   return c;
 }
 
@@ -73,14 +98,16 @@ __global__ void __launch_bounds__(32 * kMxWarps) k_mx4_quantize(const T* __restr
   const int64_t units = (rows + (n - live)) * spans;
   for (int64_t u = (int64_t)blockIdx.x * kMxWarps + (threadIdx.x >> 5); u < units;
        u += (int64_t)gridDim.x * kMxWarps) {
-    const int64_t t = u / spans, span = u - t * spans;
+    const int64_t t = divide(u, spans), span = u - t * spans;
     uint32_t c[2] = {0u, 0u}, s[2] = {0u, 0u};
     if (!kRoute || t < rows) {
+      Eight<T> v[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        load8<T, kAligned>(x + t * ld, span * kSpan + i * 256 + lane * kLane, width, &v[i]);
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        float v[kLane];
-        load8<T, kAligned>(x + t * ld, span * kSpan + i * 256 + lane * kLane, width, v);
-        c[i] = encode8(v, &s[i]);
+        c[i] = encode8(v[i], &s[i]);
         if (span * 16 + i * 8 + lane / 4 >= blocks) s[i] = 0u;
       }
     }
@@ -119,7 +146,7 @@ __global__ void __launch_bounds__(32 * kMxWarps) k_mx4_dequantize(const uint8_t*
   const int64_t code_bytes = EBC_MX4_CODE_BYTES(width), scale_bytes = spans * 16;
   for (int64_t u = (int64_t)blockIdx.x * kMxWarps + (threadIdx.x >> 5); u < rows * spans;
        u += (int64_t)gridDim.x * kMxWarps) {
-    const int64_t t = u / spans, span = u - t * spans;
+    const int64_t t = divide(u, spans), span = u - t * spans;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int64_t h = span * kSpan + i * 256 + lane * kLane;

@@ -63,6 +63,20 @@ at::ScalarType scalar_of(int64_t type) {
 }
 
 // The context's handle and device: the first two arguments of every call.
+// Several outputs of one call in one allocation, each on a 16-byte boundary:
+// an allocation costs as much as half a launch.
+struct Parts {
+  at::Tensor whole;
+  at::Tensor take(int64_t at, at::IntArrayRef shape, at::ScalarType type) const {
+    auto impl = c10::make_intrusive<c10::TensorImpl>(c10::Storage(whole.storage()), whole.key_set(),
+                                                     c10::scalarTypeToTypeMeta(type));
+    impl->set_storage_offset(at / (int64_t)c10::elementSize(type));
+    impl->set_sizes_contiguous(shape);
+    return at::Tensor(std::move(impl));
+  }
+};
+int64_t pad16(int64_t n) { return (n + 15) & ~(int64_t)15; }
+
 struct Where {
   ebc_ctx* ctx;
   c10::DeviceIndex device;
@@ -165,6 +179,13 @@ Mx4Ref mx4_here(const Where& w, PyObject* const* a) {
   return m;
 }
 
+// codes and scales of n rows, one allocation
+std::pair<at::Tensor, at::Tensor> mx4_rows(const Where& w, int64_t n, int64_t width) {
+  const int64_t cb = EBC_MX4_CODE_BYTES(width), sb = EBC_MX4_SCALE_BYTES(width);
+  const Parts all{w.empty({n * (cb + sb)}, at::kByte)};
+  return {all.take(0, {n, cb}, at::kByte), all.take(n * cb, {n, sb}, at::kByte)};
+}
+
 PyObject* wrap(const at::Tensor& t) { return THPVariable_Wrap(t); }
 
 PyObject* tuple(std::initializer_list<at::Tensor> ts) {
@@ -221,8 +242,10 @@ PyObject* py_plan(PyObject*, PyObject* const* a, Py_ssize_t n) {
     w.here(ids);
     if (experts < 1 || experts > EBC_MAX_EXPERTS) checked(EBC_ERR_INVALID_ARG, "ebc_moe_plan");
     const int64_t tokens = ids.size(0), top = ids.size(1);
-    at::Tensor r = w.empty({tokens * top}, at::kInt), p = w.empty({tokens, top}, at::kInt),
-               o = w.empty({experts + 1}, at::kInt);
+    const int64_t each = pad16(4 * tokens * top);
+    const Parts all{w.empty({2 * each + 4 * (experts + 1)}, at::kByte)};
+    at::Tensor r = all.take(0, {tokens * top}, at::kInt), p = all.take(each, {tokens, top}, at::kInt),
+               o = all.take(2 * each, {experts + 1}, at::kInt);
     checked(ebc_moe_plan(w.ctx, ids.data_ptr(), (int)ids.element_size(), tokens, (int)std::min<int64_t>(top, INT32_MAX),
                          (int)experts, (int32_t*)r.data_ptr(), (int32_t*)p.data_ptr(), (int32_t*)o.data_ptr(),
                          w.stream()),
@@ -253,8 +276,7 @@ PyObject* py_dispatch_mx4(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const Rows x = rows(w, a[2]);
     const PlanRef p = plan_here(w, a + 3);
     if (x.n != p.tokens) bad("x has not as many rows as the plan has tokens");
-    at::Tensor c = w.empty({p.n, EBC_MX4_CODE_BYTES(x.width)}, at::kByte),
-               s = w.empty({p.n, EBC_MX4_SCALE_BYTES(x.width)}, at::kByte);
+    auto [c, s] = mx4_rows(w, p.n, x.width);
     checked(ebc_moe_dispatch_mx4(w.ctx, x.t.data_ptr(), x.ld, x.type, p.tokens, (int)p.top, x.width, p.place_ptr(),
                                  p.offsets_ptr(), (int)p.experts, (uint8_t*)c.data_ptr(), (uint8_t*)s.data_ptr(),
                                  w.stream()),
@@ -302,8 +324,7 @@ PyObject* py_quantize(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded(n, 3, [&] {
     const Where w = where(a);
     const Rows x = rows(w, a[2]);
-    at::Tensor c = w.empty({x.n, EBC_MX4_CODE_BYTES(x.width)}, at::kByte),
-               s = w.empty({x.n, EBC_MX4_SCALE_BYTES(x.width)}, at::kByte);
+    auto [c, s] = mx4_rows(w, x.n, x.width);
     checked(ebc_mx4_quantize(w.ctx, x.t.data_ptr(), x.ld, x.type, x.n, x.width, (uint8_t*)c.data_ptr(),
                              (uint8_t*)s.data_ptr(), w.stream()),
             "ebc_mx4_quantize");

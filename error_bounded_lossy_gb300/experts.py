@@ -129,7 +129,7 @@ class Experts:
     def plan(self, ids, n_experts: int, stream=None) -> Plan:
         """The plan of the router's choices ids [tokens, top] (int32 or int64;
         negative: dropped).  An id >= n_experts is dropped too, and check() raises."""
-        p = _new(Plan)
+        p = _new(Plan)   # (tensors that the calls have made need no check)
         if stream is None:
             p.rows, p.place, p.offsets = _calls.plan(self._h, self._index, ids, n_experts)
         else:
@@ -177,13 +177,14 @@ class Experts:
                 q = self.quantize(x)
             x.record_stream(stream)
             return q
-        lead, width = x.shape[:-1], x.shape[-1]
-        flat = x if len(lead) == 1 else x.reshape(-1, width)
         q = _new(Mx4)
-        q.codes, q.scales = _calls.quantize(self._h, self._index, flat)
-        if flat is not x:
+        q.width = width = x.shape[-1]
+        if x.dim() == 2:
+            q.codes, q.scales = _calls.quantize(self._h, self._index, x)
+        else:
+            lead = x.shape[:-1]
+            q.codes, q.scales = _calls.quantize(self._h, self._index, x.reshape(-1, width))
             q.codes, q.scales = q.codes.view(*lead, q.codes.shape[1]), q.scales.view(*lead, q.scales.shape[1])
-        q.width = width
         return q
 
     def dequantize(self, q: Mx4, dtype=torch.float32, stream=None):
@@ -218,9 +219,7 @@ class Experts:
         return ebc_get_profile(self._ctx)
 
 
-def _new(cls):
-    """An instance for tensors that the calls have made, which need no check."""
-    return object.__new__(cls)
+_new = object.__new__
 
 
 def _type(dtype) -> int:
