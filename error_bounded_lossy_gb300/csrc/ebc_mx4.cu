@@ -7,34 +7,64 @@ using namespace ebc;
 namespace {
 
 constexpr int kMxWarps = 8;
-constexpr int kSpan = 512;   // values of a warp's piece: one 16-byte group of scales
+constexpr int kLane = 8;            // consecutive values of a lane; a block is four lanes
+constexpr int kPiece = 32 * kLane;  // consecutive values of a warp
+
 // a / b; most often in 32 bits, a fifth of the instructions
 __device__ __forceinline__ int64_t divide(int64_t a, int64_t b) {
   return a <= UINT32_MAX ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
 }
 
-constexpr int kLane = 8;     // consecutive values of a lane; a block is four lanes
+// Chunks of a row, its scales' filling included.
+__host__ __device__ __forceinline__ int64_t scale_chunks(int64_t width, int chunk) {
+  return (EBC_MX4_SCALE_BYTES(width) * 32 + chunk - 1) / chunk;
+}
 
-// Eight consecutive values of a row (zeros past its end) as they are in
-// memory: 16-byte loads where the row is aligned for them, else one by one.
+// Eight values of a row as they are in memory.
 template <typename T>
 struct Eight {
   static constexpr int kWords = kLane * (int)sizeof(T) / 4;
   union {
-    uint4 raw[kWords / 4];
     uint32_t word[kWords];
     T e[kLane];
   };
   __device__ __forceinline__ Eight() {}
 };
+// One load or store of 16 or 32 bytes where the row is aligned for it, else
+// one by one; values past the row's end are zero, or not written.
 template <typename T, bool kAligned>
-__device__ __forceinline__ void load8(const T* row, int64_t h, int64_t width, Eight<T>* v) {
-  if (kAligned && h + kLane <= width) {
-#pragma unroll
-    for (int i = 0; i < Eight<T>::kWords / 4; ++i) v->raw[i] = reinterpret_cast<const uint4*>(row + h)[i];
+__device__ __forceinline__ void load8(const T* p, int64_t left, Eight<T>* v) {
+  if (kAligned && left >= kLane) {
+    if constexpr (sizeof(T) == 4)
+      asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                   : "=r"(v->word[0]), "=r"(v->word[1]), "=r"(v->word[2]), "=r"(v->word[3]), "=r"(v->word[4]),
+                     "=r"(v->word[5]), "=r"(v->word[6]), "=r"(v->word[7])
+                   : "l"(p));
+    else
+      asm volatile("ld.global.v4.b32 {%0, %1, %2, %3}, [%4];"
+                   : "=r"(v->word[0]), "=r"(v->word[1]), "=r"(v->word[2]), "=r"(v->word[3])
+                   : "l"(p));
   } else {
 #pragma unroll
-    for (int k = 0; k < kLane; ++k) v->e[k] = h + k < width ? row[h + k] : from_f32<T>(0.f);
+    for (int k = 0; k < kLane; ++k) v->e[k] = k < left ? p[k] : from_f32<T>(0.f);
+  }
+}
+template <typename T, bool kAligned>
+__device__ __forceinline__ void store8(T* p, int64_t left, const Eight<T>& v) {
+  if (kAligned && left >= kLane) {
+    if constexpr (sizeof(T) == 4)
+      asm volatile("st.global.v8.b32 [%8], {%0, %1, %2, %3, %4, %5, %6, %7};" ::"r"(v.word[0]), "r"(v.word[1]),
+                   "r"(v.word[2]), "r"(v.word[3]), "r"(v.word[4]), "r"(v.word[5]), "r"(v.word[6]), "r"(v.word[7]),
+                   "l"(p)
+                   : "memory");
+    else
+      asm volatile("st.global.v4.b32 [%4], {%0, %1, %2, %3};" ::"r"(v.word[0]), "r"(v.word[1]), "r"(v.word[2]),
+                   "r"(v.word[3]), "l"(p)
+                   : "memory");
+  } else {
+#pragma unroll
+    for (int k = 0; k < kLane; ++k)
+      if (k < left) p[k] = v.e[k];
   }
 }
 
@@ -65,20 +95,21 @@ template <typename T>
 __device__ __forceinline__ uint32_t encode8(const Eight<T>& v, uint32_t* scale) {
   const uint32_t s = mx4_scale(block_max(v));
   *scale = s;
-  if (s == 255u) return 0u;
   const float inv = mx4_inverse(s);
-  uint32_t c = 0;
+  float u[kLane];
 #pragma unroll
-  for (int k = 0; k < kLane; k += 2) c |= mx4_pair(to_f32(v.e[k]) * inv, to_f32(v.e[k + 1]) * inv) << (4 * k);
-  return c;
+  for (int k = 0; k < kLane; ++k) u[k] = to_f32(v.e[k]) * inv;
+  return s == 255u ? 0u : mx4_codes(u);
 }
 
-// A warp takes 512 values of a row (two times eight a lane), so that it owns a
-// whole 16-byte group of scales.  With kRoute each token's codes go to the
+// A warp takes kPieces runs of 256 consecutive values of a row, eight a lane,
+// all of them in flight at once.  With kRoute each token's codes go to the
 // rows of its choices: quantized once, written `top` times, and rows past the
-// last expert's are zero.  Bound by bandwidth: 16 or 32 bits read and 4.25
-// written a value.
-template <typename T, bool kAligned, bool kRoute>
+// last expert's are zero.
+// 16 or 32 bits are read and 4.25 written a value: bound by bandwidth, with
+// issue close behind for 16-bit types.  [16384, 4096] bf16: 29 us (5.9 TB/s);
+// [8192, 3328] fp32: 22 us (5.6 TB/s).
+template <typename T, bool kAligned, bool kRoute, int kPieces>
 __global__ void __launch_bounds__(32 * kMxWarps) k_mx4_quantize(const T* __restrict__ x, int64_t ld, int64_t rows,
                                                                 int64_t width, int top,
                                                                 const int32_t* __restrict__ place,
@@ -86,40 +117,54 @@ __global__ void __launch_bounds__(32 * kMxWarps) k_mx4_quantize(const T* __restr
                                                                 uint8_t* __restrict__ codes,
                                                                 uint8_t* __restrict__ scales, Glob* glob) {
   pdl_enter();
-  const int lane = threadIdx.x & 31;
-  const int64_t spans = (width + kSpan - 1) / kSpan;
-  const int64_t code_bytes = EBC_MX4_CODE_BYTES(width), scale_bytes = spans * 16, blocks = (width + 31) / 32;
+  constexpr int kChunk = kPieces * kPiece;
+  const int lane = threadIdx.x & 31, quad = lane >> 2, j4 = lane & 3;
+  const int64_t code_bytes = EBC_MX4_CODE_BYTES(width), scale_bytes = EBC_MX4_SCALE_BYTES(width);
+  const int64_t chunks = scale_chunks(width, kChunk);
   const int64_t n = rows * top;
   int64_t live = n;
   if (kRoute) {
     live = offsets[E];
     live = live < 0 ? 0 : live < n ? live : n;
   }
-  const int64_t units = (rows + (n - live)) * spans;
+  const int64_t units = (rows + (n - live)) * chunks;
   for (int64_t u = (int64_t)blockIdx.x * kMxWarps + (threadIdx.x >> 5); u < units;
        u += (int64_t)gridDim.x * kMxWarps) {
-    const int64_t t = divide(u, spans), span = u - t * spans;
-    uint32_t c[2] = {0u, 0u}, s[2] = {0u, 0u};
+    const int64_t t = divide(u, chunks), h0 = (u - t * chunks) * kChunk, left = width - h0 - lane * kLane;
+    uint32_t c[kPieces], s[kPieces];
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) c[i] = s[i] = 0u;
     if (!kRoute || t < rows) {
-      Eight<T> v[2];
+      const T* src = x + t * ld + h0 + lane * kLane;
+      Eight<T> v[kPieces];
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
-        load8<T, kAligned>(x + t * ld, span * kSpan + i * 256 + lane * kLane, width, &v[i]);
+      for (int i = 0; i < kPieces; ++i) load8<T, kAligned>(src + i * kPiece, left - i * kPiece, &v[i]);
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
+      for (int i = 0; i < kPieces; ++i) {
         c[i] = encode8(v[i], &s[i]);
-        if (span * 16 + i * 8 + lane / 4 >= blocks) s[i] = 0u;
+        // a block past the row's end; a block's lanes agree on that
+        if (left + j4 * kLane - i * kPiece <= 0) s[i] = 0u;
       }
     }
-    auto store = [&](int64_t r) {
-      uint8_t* cr = codes + r * code_bytes;
-      uint8_t* sr = scales + r * scale_bytes + span * 16;
+    // of four pieces' scale bytes a block's lanes store one each
+    uint32_t mine[(kPieces + 3) / 4];
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int64_t at = span * 256 + i * 128 + lane * 4;
-        if (at < code_bytes) *reinterpret_cast<uint32_t*>(cr + at) = c[i];
-        if ((lane & 3) == 0) sr[i * 8 + lane / 4] = (uint8_t)s[i];
-      }
+    for (int q = 0; q < (kPieces + 3) / 4; ++q) {
+      uint32_t all = 0;
+#pragma unroll
+      for (int i = 0; i < 4 && 4 * q + i < kPieces; ++i) all |= s[4 * q + i] << (8 * i);
+      mine[q] = all >> (8 * j4);
+    }
+    const int64_t code_left = code_bytes - h0 / 2 - lane * 4, scale_left = scale_bytes - h0 / 32 - j4 * 8 - quad;
+    auto store = [&](int64_t r) {
+      uint8_t* cr = codes + r * code_bytes + h0 / 2 + lane * 4;
+      uint8_t* sr = scales + r * scale_bytes + h0 / 32 + j4 * 8 + quad;
+#pragma unroll
+      for (int i = 0; i < kPieces; ++i)
+        if (i * (kPiece / 2) < code_left) *reinterpret_cast<uint32_t*>(cr + i * (kPiece / 2)) = c[i];
+#pragma unroll
+      for (int q = 0; q < (kPieces + 3) / 4; ++q)
+        if (4 * q + j4 < kPieces && q * 32 < scale_left) sr[q * 32] = (uint8_t)mine[q];
     };
     if (!kRoute) {
       store(t);
@@ -135,52 +180,65 @@ __global__ void __launch_bounds__(32 * kMxWarps) k_mx4_quantize(const T* __restr
   }
 }
 
-// A lane takes eight codes.  Bound by the bandwidth of the writes.
-template <typename T, bool kAligned>
+// The way back: eight codes a lane, kPieces runs of 256 values a warp.  Bound
+// by the bandwidth of the writes: [8192, 3328] to fp32 20 us (6.1 TB/s).
+template <typename T, bool kAligned, int kPieces>
 __global__ void __launch_bounds__(32 * kMxWarps) k_mx4_dequantize(const uint8_t* __restrict__ codes,
                                                                   const uint8_t* __restrict__ scales, int64_t rows,
                                                                   int64_t width, T* __restrict__ x) {
   pdl_enter();
+  constexpr int kChunk = kPieces * kPiece;
   const int lane = threadIdx.x & 31;
-  const int64_t spans = (width + kSpan - 1) / kSpan;
-  const int64_t code_bytes = EBC_MX4_CODE_BYTES(width), scale_bytes = spans * 16;
-  for (int64_t u = (int64_t)blockIdx.x * kMxWarps + (threadIdx.x >> 5); u < rows * spans;
+  const int64_t chunks = (width + kChunk - 1) / kChunk;
+  const int64_t code_bytes = EBC_MX4_CODE_BYTES(width), scale_bytes = EBC_MX4_SCALE_BYTES(width);
+  for (int64_t u = (int64_t)blockIdx.x * kMxWarps + (threadIdx.x >> 5); u < rows * chunks;
        u += (int64_t)gridDim.x * kMxWarps) {
-    const int64_t t = divide(u, spans), span = u - t * spans;
+    const int64_t t = divide(u, chunks), h0 = (u - t * chunks) * kChunk, left = width - h0 - lane * kLane;
+    const uint8_t* cr = codes + t * code_bytes + h0 / 2 + lane * 4;
+    const uint8_t* sr = scales + t * scale_bytes + h0 / 32 + (lane >> 2);
+    T* dst = x + t * width + h0 + lane * kLane;
+    uint32_t c[kPieces], s[kPieces];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int64_t h = span * kSpan + i * 256 + lane * kLane;
-      if (h >= width) continue;
-      const uint32_t c = *reinterpret_cast<const uint32_t*>(codes + t * code_bytes + h / 2);
-      const float unit = mx4_unit(scales[t * scale_bytes + h / 32]);
-      float v[kLane];
-#pragma unroll
-      for (int k = 0; k < kLane; k += 2) {
-        const float2 f = __half22float2(mx4_values((c >> (4 * k)) & 0xFFu));
-        v[k] = f.x * unit;
-        v[k + 1] = f.y * unit;
+    for (int i = 0; i < kPieces; ++i)
+      if (i * kPiece < left) {
+        c[i] = *reinterpret_cast<const uint32_t*>(cr + i * (kPiece / 2));
+        s[i] = sr[i * (kPiece / 32)];
       }
-      T* dst = x + t * width + h;
-      if (kAligned && h + kLane <= width) {
-        constexpr int kN = 16 / (int)sizeof(T);
 #pragma unroll
-        for (int q = 0; q < kLane / kN; ++q) {
-          Vec<T, 16> o;
+    for (int i = 0; i < kPieces; ++i)
+      if (i * kPiece < left) {
+        const float unit = mx4_unit(s[i]);
+        __half2 h[4];
+        mx4_values(c[i], h);
+        Eight<T> o;
 #pragma unroll
-          for (int k = 0; k < kN; ++k) o.e[k] = from_f32<T>(v[q * kN + k]);
-          *reinterpret_cast<uint4*>(dst + q * kN) = o.raw;
+        for (int k = 0; k < 4; ++k) {
+          const float2 f = __half22float2(h[k]);
+          o.e[2 * k] = from_f32<T>(f.x * unit);
+          o.e[2 * k + 1] = from_f32<T>(f.y * unit);
         }
-      } else {
-#pragma unroll
-        for (int k = 0; k < kLane; ++k)
-          if (h + k < width) dst[k] = from_f32<T>(v[k]);
+        store8<T, kAligned>(dst + i * kPiece, left - i * kPiece, o);
       }
-    }
   }
 }
 
+// Pieces of a warp: as many (up to `most`) as leave 24 warps for each SM.  A
+// warp's own cost (about 150 instructions) is spread over them, and their
+// loads overlap: [16384, 4096] bf16 takes 52 us with one, 40 with two, 32 with
+// four and 29 with eight; [1531, 1056] fp16 3.8 with one, 3.5 with two, 4.4
+// with four.
+int pieces(int64_t rows, int64_t width, int nsm, int most) {
+  int p = most;
+  while (p > 1 && rows * scale_chunks(width, p * kPiece) < (int64_t)nsm * 24) p /= 2;
+  return p;
+}
+
+bool aligned(const void* p, int bytes) { return ((uintptr_t)p & (uintptr_t)(bytes - 1)) == 0; }
+
+// CTAs for `units` warps of work, at most two full turns of the machine; the
+// kernels loop beyond that.
 unsigned mx_grid(int64_t units, int nsm) {
-  const int64_t want = (units + kMxWarps - 1) / kMxWarps, most = (int64_t)nsm * 8 * 8;
+  const int64_t want = (units + kMxWarps - 1) / kMxWarps, most = (int64_t)nsm * 8 * 2;
   return (unsigned)(want < 1 ? 1 : want < most ? want : most);
 }
 
@@ -188,19 +246,30 @@ bool mx_rows_ok(int64_t rows, int64_t width) {
   return rows >= 0 && rows <= INT32_MAX && width >= 1 && width <= (1 << 24);
 }
 
-bool aligned(const void* p, int bytes) { return ((uintptr_t)p & (uintptr_t)(bytes - 1)) == 0; }
+template <typename T, bool kAligned, bool kRoute, int kPieces>
+cudaError_t quantize_launch(const CallView& v, const void* x, int64_t ld, int64_t rows, int64_t width, int top,
+                            const int32_t* place, const int32_t* offsets, int E, uint8_t* codes, uint8_t* scales,
+                            cudaStream_t st) {
+  return launch_named(v, kRoute ? "k_mx4_dispatch" : "k_mx4_quantize", st,
+                      k_mx4_quantize<T, kAligned, kRoute, kPieces>,
+                      dim3(mx_grid(rows * scale_chunks(width, kPieces * kPiece), v.nsm)), dim3(32 * kMxWarps), 0, 1,
+                      (const T*)x, ld, rows, width, top, place, offsets, E, codes, scales, v.glob);
+}
 
 template <typename T, bool kRoute>
 cudaError_t quantize_t(const CallView& v, const void* x, int64_t ld, int64_t rows, int64_t width, int top,
                        const int32_t* place, const int32_t* offsets, int E, uint8_t* codes, uint8_t* scales,
                        cudaStream_t st) {
-  const bool al = aligned(x, 16) && (ld * (int64_t)sizeof(T)) % 16 == 0;
-  const dim3 grid(mx_grid(rows * ((width + kSpan - 1) / kSpan), v.nsm)), block(32 * kMxWarps);
-  const char* name = kRoute ? "k_mx4_dispatch" : "k_mx4_quantize";
-  return al ? launch_named(v, name, st, k_mx4_quantize<T, true, kRoute>, grid, block, 0, 1, (const T*)x, ld, rows,
-                           width, top, place, offsets, E, codes, scales, v.glob)
-            : launch_named(v, name, st, k_mx4_quantize<T, false, kRoute>, grid, block, 0, 1, (const T*)x, ld, rows,
-                           width, top, place, offsets, E, codes, scales, v.glob);
+  constexpr int kMost = sizeof(T) == 2 ? 8 : 4, kAlign = kLane * (int)sizeof(T);
+  if (!aligned(x, kAlign) || ld * (int64_t)sizeof(T) % kAlign != 0)
+    return quantize_launch<T, false, kRoute, 1>(v, x, ld, rows, width, top, place, offsets, E, codes, scales, st);
+  switch (pieces(rows, width, v.nsm, kMost)) {
+    case 1: return quantize_launch<T, true, kRoute, 1>(v, x, ld, rows, width, top, place, offsets, E, codes, scales, st);
+    case 2: return quantize_launch<T, true, kRoute, 2>(v, x, ld, rows, width, top, place, offsets, E, codes, scales, st);
+    case 4: return quantize_launch<T, true, kRoute, 4>(v, x, ld, rows, width, top, place, offsets, E, codes, scales, st);
+    default:
+      return quantize_launch<T, true, kRoute, kMost>(v, x, ld, rows, width, top, place, offsets, E, codes, scales, st);
+  }
 }
 
 template <bool kRoute>
@@ -228,15 +297,26 @@ int quantize_any(ebc_ctx* ctx, const void* x, int64_t ld, int type, int64_t rows
   return cuda_code(e);
 }
 
+template <typename T, bool kAligned, int kPieces>
+cudaError_t dequantize_launch(const CallView& v, const uint8_t* codes, const uint8_t* scales, int64_t rows,
+                              int64_t width, void* x, cudaStream_t st) {
+  const int64_t chunk = kPieces * kPiece;
+  return launch_named(v, "k_mx4_dequantize", st, k_mx4_dequantize<T, kAligned, kPieces>,
+                      dim3(mx_grid(rows * ((width + chunk - 1) / chunk), v.nsm)), dim3(32 * kMxWarps), 0, 1, codes,
+                      scales, rows, width, (T*)x);
+}
+
 template <typename T>
 cudaError_t dequantize_t(const CallView& v, const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t width,
                          void* x, cudaStream_t st) {
-  const bool al = aligned(x, 16) && (width * (int64_t)sizeof(T)) % 16 == 0;
-  const dim3 grid(mx_grid(rows * ((width + kSpan - 1) / kSpan), v.nsm)), block(32 * kMxWarps);
-  return al ? launch_named(v, "k_mx4_dequantize", st, k_mx4_dequantize<T, true>, grid, block, 0, 1, codes, scales,
-                           rows, width, (T*)x)
-            : launch_named(v, "k_mx4_dequantize", st, k_mx4_dequantize<T, false>, grid, block, 0, 1, codes, scales,
-                           rows, width, (T*)x);
+  constexpr int kAlign = kLane * (int)sizeof(T);
+  if (!aligned(x, kAlign) || width * (int64_t)sizeof(T) % kAlign != 0)
+    return dequantize_launch<T, false, 1>(v, codes, scales, rows, width, x, st);
+  switch (pieces(rows, width, v.nsm, 4)) {
+    case 1: return dequantize_launch<T, true, 1>(v, codes, scales, rows, width, x, st);
+    case 2: return dequantize_launch<T, true, 2>(v, codes, scales, rows, width, x, st);
+    default: return dequantize_launch<T, true, 4>(v, codes, scales, rows, width, x, st);
+  }
 }
 
 }  // namespace

@@ -25,19 +25,29 @@ __device__ __forceinline__ float mx4_unit(uint32_t s) {
   return s == 255u ? __uint_as_float(0x7FC00000u) : s == 0u ? __uint_as_float(0x00400000u) : __uint_as_float(s << 23);
 }
 
-// The codes of two values, `lo` in the low four bits: to nearest, ties to the
-// even code.
-__device__ __forceinline__ uint32_t mx4_pair(float lo, float hi) {
+// The codes of eight values, the first in the low four bits: to nearest, ties
+// to the even code.
+__device__ __forceinline__ uint32_t mx4_codes(const float (&v)[8]) {
   uint32_t r;
-  asm("{\n .reg .b8 t;\n cvt.rn.satfinite.e2m1x2.f32 t, %1, %2;\n cvt.u32.u8 %0, t;\n}\n" : "=r"(r) : "f"(hi), "f"(lo));
+  asm("{\n .reg .b8 a, b, c, d;\n"
+      " cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n"
+      " cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n"
+      " mov.b32 %0, {a, b, c, d};\n}\n"
+      : "=r"(r)
+      : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]));
   return r;
 }
 
-// The values of the two codes in the low byte of `pair`, as halves (exact).
-__device__ __forceinline__ __half2 mx4_values(uint32_t pair) {
-  uint32_t r;
-  asm("{\n .reg .b8 t;\n cvt.u8.u32 t, %1;\n cvt.rn.f16x2.e2m1x2 %0, t;\n}\n" : "=r"(r) : "r"(pair));
-  return *reinterpret_cast<__half2*>(&r);
+// The values of eight codes, as four pairs of halves (exact).
+__device__ __forceinline__ void mx4_values(uint32_t codes, __half2 (&v)[4]) {
+  uint32_t r[4];
+  asm("{\n .reg .b8 a, b, c, d;\n mov.b32 {a, b, c, d}, %4;\n"
+      " cvt.rn.f16x2.e2m1x2 %0, a;\n cvt.rn.f16x2.e2m1x2 %1, b;\n"
+      " cvt.rn.f16x2.e2m1x2 %2, c;\n cvt.rn.f16x2.e2m1x2 %3, d;\n}\n"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+      : "r"(codes));
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = *reinterpret_cast<__half2*>(&r[i]);
 }
 
 }  // namespace ebc
