@@ -29,14 +29,20 @@ constexpr int kStoreWarp0 = 4, kStoreWarps = 8;
 constexpr int kStoreRows = 16;     // rows that a storing warp turns over at a time
 constexpr int kStorePitch = 80;    // bytes of such a row of 32 outputs: 64, and 16 to spread the banks
 
-template <int kTN>
+// kCtas = 2: a pair of CTAs on one tile of 256 outputs.  Each brings in its own
+// 128 outputs and half of the rows; the pair's matrix instructions read both
+// halves, so a CTA moves and reads half as many of the rows' bytes.
+template <int kTN, int kCtas>
 struct Geom {
+  static constexpr int kOuts = kM * kCtas;                                // outputs of a tile
   static constexpr int kScaleB = (kTN + 127) / 128;                       // scale tiles of the rows per 4 blocks
-  static constexpr int kBox = kTN < 64 ? kTN : 64;                        // rows of one copy
+  static constexpr int kBRows = kTN / kCtas;                              // rows that a CTA brings in
+  static constexpr int kBox = kBRows < 64 ? kBRows : 64;                  // rows of one copy
+  static constexpr int kRound = 16 * kCtas;                               // N of the instructions is a multiple
   static constexpr int kABytes = kM * kRowBytes;
-  static constexpr int kBBytes = kTN * kRowBytes;
+  static constexpr int kBBytes = kBRows * kRowBytes;
   static constexpr int kScaleBytes = 2 * (1 + kScaleB) * kScaleTile;      // per stage: 8 blocks a row
-  static constexpr int kStages = kTN == 256 ? 4 : kTN == 128 ? 6 : kTN == 64 ? 7 : 8;
+  static constexpr int kStages = kTN == 256 ? 5 : kTN == 128 ? 6 : kTN == 64 ? 7 : 8;
   static constexpr int kAcc = kTN == 256 ? 1 : 2;                         // accumulators
   static constexpr int kAccCols = kTN < 32 ? 32 : kTN;
   static constexpr int kScaleCols = 2 * (1 + kScaleB) * 4;                // tensor memory columns per stage
@@ -57,8 +63,24 @@ __device__ __forceinline__ void mbar_init(uint64_t* bar, uint32_t count) {
 __device__ __forceinline__ void mbar_expect_tx(uint64_t* bar, uint32_t bytes) {
   asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(bar)), "r"(bytes) : "memory");
 }
-__device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
-  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
+// The address of a shared variable of the pair's first CTA (kCtas = 1: of this
+// one), as the pair's shared memory has it.
+template <int kCtas>
+__device__ __forceinline__ uint32_t in_first(const void* p) {
+  uint32_t r = smem_u32(p);
+  if constexpr (kCtas == 2) asm volatile("mapa.shared::cluster.u32 %0, %0, 0;" : "+r"(r));
+  return r;
+}
+// An arrival at such a barrier.  What it announces has been handed to the async
+// proxy of the thread's own SM (fence.proxy.async) or to nobody (a stage or an
+// accumulator given back), so it needs no release of the thread's memory to the
+// cluster: that, a round trip to L2, took 1250 cycles a stage.
+template <int kCtas>
+__device__ __forceinline__ void mbar_arrive(uint32_t bar) {
+  if constexpr (kCtas == 2)
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+  else
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 __device__ __forceinline__ bool mbar_try_wait(uint64_t* bar, uint32_t parity) {
   uint32_t ok;
@@ -79,30 +101,84 @@ __device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
       : "memory");
   return ok != 0u;
 }
-__device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map, uint64_t* bar, int c0, int c1) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
-          dst),
-      "l"(map), "r"(c0), "r"(c1), "r"(smem_u32(bar))
-      : "memory");
+// a box into this CTA's shared memory; its bytes are counted at `bar`, which
+// may be the other CTA's of the pair
+template <int kCtas>
+__device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int c0, int c1) {
+  if constexpr (kCtas == 2)
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], "
+        "[%4];" ::"r"(dst),
+        "l"(map), "r"(c0), "r"(c1), "r"(bar)
+        : "memory");
+  else
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
+            dst),
+        "l"(map), "r"(c0), "r"(c1), "r"(bar)
+        : "memory");
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+// an arrival at `bar` (of both CTAs of a pair) once what was issued is done
+template <int kCtas>
 __device__ __forceinline__ void tc_commit(uint64_t* bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
-               : "memory");
+  if constexpr (kCtas == 2)
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+            smem_u32(bar)),
+        "h"((uint16_t)3)
+        : "memory");
+  else
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
+                 : "memory");
 }
 // 32 rows x 16 bytes of scales to four columns of each quarter of tensor memory
+// (in both CTAs of a pair, each from its own shared memory)
+template <int kCtas>
 __device__ __forceinline__ void tc_copy_scales(uint32_t taddr, uint64_t desc) {
-  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+  if constexpr (kCtas == 2)
+    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+  else
+    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
 }
+template <int kCtas>
 __device__ __forceinline__ void tc_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sa, uint32_t sb,
                                        uint32_t accumulate) {
-  asm volatile(
-      "{\n .reg .pred p;\n setp.ne.u32 p, %6, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n}\n" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(accumulate)
-      : "memory");
+  if constexpr (kCtas == 2)
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.u32 p, %6, 0;\n"
+        " tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n}\n" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(accumulate)
+        : "memory");
+  else
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.u32 p, %6, 0;\n"
+        " tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n}\n" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(accumulate)
+        : "memory");
+}
+template <int kCtas>
+__device__ __forceinline__ void tc_alloc(uint32_t* where, uint32_t cols) {
+  if constexpr (kCtas == 2) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(where)), "r"(cols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  } else {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(where)), "r"(cols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+}
+template <int kCtas>
+__device__ __forceinline__ void tc_free(uint32_t tmem, uint32_t cols) {
+  if constexpr (kCtas == 2)
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(cols) : "memory");
+  else
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(cols) : "memory");
 }
 // 32 lanes x 16 columns, a lane a thread
 __device__ __forceinline__ void tc_load16(uint32_t taddr, uint32_t (&v)[16]) {
@@ -147,11 +223,11 @@ __device__ __forceinline__ uint64_t operand_desc(uint32_t addr) {
 __device__ __forceinline__ uint64_t scale_desc(uint32_t addr) {
   return (uint64_t)((addr >> 4) & 0x3FFFu) | (1ull << 16) | (8ull << 32) | (1ull << 46);
 }
-// Instruction descriptor: both operands E2M1 along K, scales UE8M0, M = 128,
+// Instruction descriptor: both operands E2M1 along K, scales UE8M0, M = m,
 // N = n; `id` (0 or 2) is the byte of a scale word where the instruction's two
 // blocks start.
-__device__ __forceinline__ uint32_t instr_desc(int n, int id) {
-  return (1u << 7) | (1u << 10) | ((uint32_t)(n >> 3) << 17) | (1u << 23) | ((uint32_t)(kM >> 4) << 24) |
+__device__ __forceinline__ uint32_t instr_desc(int m, int n, int id) {
+  return (1u << 7) | (1u << 10) | ((uint32_t)(n >> 3) << 17) | (1u << 23) | ((uint32_t)(m >> 4) << 24) |
          ((uint32_t)id << 4) | ((uint32_t)id << 29);
 }
 
@@ -288,9 +364,9 @@ __device__ __forceinline__ void store_half(const uint32_t (&v)[8], uint32_t stag
 // A storing warp's share of a tile, 16-bit results: 32 outputs of every other
 // run of 16 rows.  All of it is read and rounded first and the accumulator
 // given back, then it is stored while the next tile is multiplied.
-template <typename T, int kTN>
+template <typename T, int kTN, int kCtas>
 __device__ __forceinline__ void store_tile(uint32_t d, uint32_t stage, T* y, int64_t ld, int64_t n_out, int odd,
-                                           int count, bool wide, int lane, uint64_t* given_back) {
+                                           int count, bool wide, int lane, uint32_t given_back) {
   constexpr int kRuns = kTN < 32 ? 1 : kTN / 32;
   uint32_t v[kRuns][8];
 #pragma unroll
@@ -305,7 +381,7 @@ __device__ __forceinline__ void store_tile(uint32_t d, uint32_t stage, T* y, int
   }
   tc_fence_before();
   __syncwarp();
-  if (lane == 0) mbar_arrive(given_back);
+  if (lane == 0) mbar_arrive<kCtas>(given_back);
   // the lane's eight outputs, and its first row
   const int o = (lane & 3) * 8, r = odd * kStoreRows + (lane >> 2);
   const int64_t have = n_out - o;
@@ -344,12 +420,14 @@ __device__ __forceinline__ void store_full(uint32_t taddr, float* y, int64_t ld,
 //   warps 4-11  read the accumulator, round once, and store
 // The N of the instructions is the tile's row count rounded up to 16, so a
 // ragged segment's last tile costs what it holds.
+// In a pair the first CTA multiplies for both; stages, scales and accumulators
+// are announced at its barriers, and its instructions' ends at both CTAs'.
 // Every wait is bounded (see wait()); a CTA that gives up waits for the copies
 // and instructions it has in flight, frees its tensor memory and returns.
-template <int kTN>
+template <int kTN, int kCtas>
 __global__ void __launch_bounds__(kThreads, 1) k_mx4_product(const __grid_constant__ CUtensorMap wmap,
                                                              const __grid_constant__ CUtensorMap xmap, Args a) {
-  using G = Geom<kTN>;
+  using G = Geom<kTN, kCtas>;
   extern __shared__ uint8_t raw[];
   __shared__ uint64_t full[G::kStages], scaled[G::kStages], empty[G::kStages];
   __shared__ uint64_t acc_full[G::kAcc], acc_empty[G::kAcc], drained;
@@ -358,6 +436,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx4_product(const __grid_consta
   __shared__ int s_begin[EBC_MAX_EXPERTS + 1];   // first row of each expert
   __shared__ int s_tiles[EBC_MAX_EXPERTS + 1];   // runs of kTN rows of the experts before
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
+  const int rank = kCtas == 2 ? blockIdx.x & 1 : 0;   // in the pair
   uint8_t* base = raw + (1024 - (smem_u32(raw) & 1023)) % 1024;
   uint8_t* sA = base;
   uint8_t* sB = sA + G::kStages * G::kABytes;
@@ -367,22 +446,19 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx4_product(const __grid_consta
   if (w == 0 && lane == 0) {
     for (int i = 0; i < G::kStages; ++i) {
       mbar_init(&full[i], 1);
-      mbar_init(&scaled[i], 1);
+      mbar_init(&scaled[i], kCtas);
       mbar_init(&empty[i], 1);
     }
     for (int i = 0; i < G::kAcc; ++i) {
       mbar_init(&acc_full[i], 1);
-      mbar_init(&acc_empty[i], kStoreWarps);
+      mbar_init(&acc_empty[i], kStoreWarps * kCtas);
     }
     mbar_init(&drained, 1);
     s_abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (w == 1) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&s_tmem)),
-                 "r"(G::kCols)
-                 : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    tc_alloc<kCtas>(&s_tmem, G::kCols);
     tc_fence_before();
   }
   pdl_enter();
@@ -424,13 +500,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx4_product(const __grid_consta
     if (bad && blockIdx.x == 0) record_error(a.glob, EBC_ERR_INVALID_ARG);
   }
   __syncthreads();
+  if (kCtas == 2) cluster_sync();   // the barriers are set up in both CTAs
   tc_fence_after();
   const uint32_t tmem = s_tmem;
   const uint32_t tmem_scales = tmem + G::kAcc * G::kAccCols;
-  const int out_tiles = (int)((a.outs + kM - 1) / kM);
+  const int out_tiles = (int)((a.outs + G::kOuts - 1) / G::kOuts);
   const int stages = (a.blocks + 7) / 8;   // stages of a tile
 
-  Walk walk(out_tiles, blockIdx.x, gridDim.x);
+  Walk walk(out_tiles, blockIdx.x / kCtas, gridDim.x / kCtas);
   int row0, count;
   uint32_t issued = 0;   // stages that warp 0 has asked for
   if (w == 0) {
@@ -438,17 +515,20 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx4_product(const __grid_consta
     uint32_t phase = 1;   // of the barriers that stages are given back on
     bool ok = true;
     for (; ok && walk.at(s_begin, s_tiles, a.experts, kTN, &row0, &count); walk.next(out_tiles)) {
-      const int boxes = (count + G::kBox - 1) / G::kBox;
-      const int wrow = (int)(walk.e * a.outs) + walk.out * kM;
+      // a pair's first CTA has the first half of the instructions' N, the other the second
+      const int mine = (count + G::kRound - 1) / G::kRound * 16;
+      const int boxes = (mine + G::kBox - 1) / G::kBox, brow = row0 + rank * mine;
+      const int wrow = (int)(walk.e * a.outs) + walk.out * G::kOuts + rank * kM;
       for (int k = 0; k < stages; ++k) {
         ok = __all_sync(0xffffffffu, wait(&empty[s], phase, &s_abort, a.glob));
         if (!ok) break;
         if (elect_one()) {
-          mbar_expect_tx(&full[s], G::kABytes + boxes * G::kBox * kRowBytes);
-          tma_load_2d(smem_u32(sA) + s * G::kABytes, &wmap, &full[s], k * kRowBytes, wrow);
+          const uint32_t bar = in_first<kCtas>(&full[s]);
+          if (rank == 0) mbar_expect_tx(&full[s], kCtas * (G::kABytes + boxes * G::kBox * kRowBytes));
+          tma_load_2d<kCtas>(smem_u32(sA) + s * G::kABytes, &wmap, bar, k * kRowBytes, wrow);
           for (int i = 0; i < boxes; ++i)
-            tma_load_2d(smem_u32(sB) + s * G::kBBytes + i * G::kBox * kRowBytes, &xmap, &full[s], k * kRowBytes,
-                        row0 + i * G::kBox);
+            tma_load_2d<kCtas>(smem_u32(sB) + s * G::kBBytes + i * G::kBox * kRowBytes, &xmap, bar, k * kRowBytes,
+                               brow + i * G::kBox);
         }
         __syncwarp();
         ++issued;
@@ -462,6 +542,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx4_product(const __grid_consta
     for (uint32_t i = issued > G::kStages ? issued - G::kStages : 0; ok && i < issued; ++i)
       ok = __all_sync(0xffffffffu, wait(&empty[i % G::kStages], (i / G::kStages) & 1, &s_abort, a.glob));
   } else if (w == 1) {
+    if (rank == 0) {
     // the lanes watch a stage's codes (even lanes) and its scales (odd lanes)
     // at the same time, and the next stage before this one's instructions are
     // issued, so that a wait that is over costs nothing
@@ -470,7 +551,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx4_product(const __grid_consta
     bool ok = true, ready = false;
     uint64_t* const watch = lane & 1 ? scaled : full;
     for (; ok && walk.at(s_begin, s_tiles, a.experts, kTN, &row0, &count); walk.next(out_tiles)) {
-      const uint32_t id0 = instr_desc((count + 15) & ~15, 0), id2 = instr_desc((count + 15) & ~15, 2);
+      const int n = (count + G::kRound - 1) / G::kRound * G::kRound;
+      const uint32_t id0 = instr_desc(G::kOuts, n, 0), id2 = instr_desc(G::kOuts, n, 2);
       ok = __all_sync(0xffffffffu, wait(&acc_empty[buf], acc_phase, &s_abort, a.glob));
       if (!ok) break;
       tc_fence_after();
@@ -488,10 +570,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx4_product(const __grid_consta
           const uint64_t ds = scale_desc(smem_u32(sS) + s * G::kScaleBytes);
 #pragma unroll
           for (int q = 0; q < 2; ++q) {
-            tc_copy_scales(ta + 4 * q, ds + q * (kScaleTile >> 4));
+            tc_copy_scales<kCtas>(ta + 4 * q, ds + q * (kScaleTile >> 4));
 #pragma unroll
             for (int j = 0; j < G::kScaleB; ++j)
-              tc_copy_scales(tb + 4 * (q * G::kScaleB + j), ds + (2 + q * G::kScaleB + j) * (kScaleTile >> 4));
+              tc_copy_scales<kCtas>(tb + 4 * (q * G::kScaleB + j), ds + (2 + q * G::kScaleB + j) * (kScaleTile >> 4));
           }
           const int left = a.blocks - k * 8;   // scale blocks from here on
           const uint64_t da = operand_desc(smem_u32(sA) + s * G::kABytes);
@@ -499,10 +581,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx4_product(const __grid_consta
 #pragma unroll
           for (int q = 0; q < 4; ++q)
             if (2 * q < left)
-              tc_mma(d, da + 2 * q, db + 2 * q, q & 1 ? id2 : id0, ta + 4 * (q >> 1), tb + 4 * G::kScaleB * (q >> 1),
+              tc_mma<kCtas>(d, da + 2 * q, db + 2 * q, q & 1 ? id2 : id0, ta + 4 * (q >> 1), tb + 4 * G::kScaleB * (q >> 1),
                      k > 0 || q > 0);
-          tc_commit(&empty[s]);
-          if (k == stages - 1) tc_commit(&acc_full[buf]);
+          tc_commit<kCtas>(&empty[s]);
+          if (k == stages - 1) tc_commit<kCtas>(&acc_full[buf]);
         }
         ready = __all_sync(0xffffffffu, over);
         phase ^= s_next == 0;
@@ -512,6 +594,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx4_product(const __grid_consta
         buf = 0;
         acc_phase ^= 1;
       }
+    }
     }
   } else if (w < kStoreWarp0) {
     // A warp takes every other group of 512 values (two stages), 16 scale bytes
@@ -528,7 +611,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx4_product(const __grid_consta
       const uint8_t* src[kTiles][4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const int64_t wr = walk.e * a.outs + walk.out * kM + j * 32 + lane;
+        const int64_t wr = walk.e * a.outs + walk.out * G::kOuts + rank * kM + j * 32 + lane;
         src[0][j] = wr < weights ? a.ws + wr * a.scale_bytes : nullptr;
 #pragma unroll
         for (int i = 1; i < kTiles; ++i) {
@@ -578,7 +661,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx4_product(const __grid_consta
                              word[i][3][2 * half + q]);
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           __syncwarp();
-          if (lane == 0) mbar_arrive(&scaled[s]);
+          if (lane == 0) mbar_arrive<kCtas>(in_first<kCtas>(&scaled[s]));
         }
       }
       turn = g - groups;
@@ -593,22 +676,22 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx4_product(const __grid_consta
     for (; walk.at(s_begin, s_tiles, a.experts, kTN, &row0, &count); walk.next(out_tiles)) {
       if (!__all_sync(0xffffffffu, wait(&acc_full[buf], phase, &s_abort, a.glob))) break;
       tc_fence_after();
-      const int64_t out = (int64_t)walk.out * kM + quarter * 32;
+      const int64_t out = (int64_t)walk.out * G::kOuts + rank * kM + quarter * 32;
       const int64_t n_out = a.outs - out;   // outputs from here on, maybe none
       const uint32_t d = tmem + buf * G::kAccCols + ((uint32_t)(quarter * 32) << 16);
       const int64_t at = (int64_t)row0 * a.outs + out;
       if (a.out_type == EBC_BF16) {
-        store_tile<__nv_bfloat16, kTN>(d, stage, (__nv_bfloat16*)a.ys + at, a.outs, n_out, odd, count, a.wide, lane,
-                                       &acc_empty[buf]);
+        store_tile<__nv_bfloat16, kTN, kCtas>(d, stage, (__nv_bfloat16*)a.ys + at, a.outs, n_out, odd, count, a.wide, lane,
+                                              in_first<kCtas>(&acc_empty[buf]));
       } else if (a.out_type == EBC_F16) {
-        store_tile<__half, kTN>(d, stage, (__half*)a.ys + at, a.outs, n_out, odd, count, a.wide, lane,
-                                &acc_empty[buf]);
+        store_tile<__half, kTN, kCtas>(d, stage, (__half*)a.ys + at, a.outs, n_out, odd, count, a.wide, lane,
+                                       in_first<kCtas>(&acc_empty[buf]));
       } else {
         for (int c0 = odd * kStoreRows; c0 < count; c0 += 2 * kStoreRows)
           store_full(d + c0, (float*)a.ys + at + c0 * a.outs, a.outs, n_out, count - c0, lane);
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&acc_empty[buf]);
+        if (lane == 0) mbar_arrive<kCtas>(in_first<kCtas>(&acc_empty[buf]));
       }
       if (++buf == G::kAcc) {
         buf = 0;
@@ -632,21 +715,22 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx4_product(const __grid_consta
   __syncthreads();
   tc_fence_after();
   if (s_abort) {
-    // nothing that was started may outlive the CTA
-    if (w == 0 && lane == 0) {
+    // nothing that was started may outlive the CTA (a pair's copies are counted
+    // at its first CTA)
+    if (rank == 0 && w == 0 && lane == 0) {
       for (uint32_t i = issued > G::kStages ? issued - G::kStages : 0; i < issued; ++i)
         for (int p = 0; p < kWaitLimit && !mbar_try_wait(&full[i % G::kStages], (i / G::kStages) & 1); ++p) {
         }
     }
-    if (w == 1 && lane == 0) {
-      tc_commit(&drained);
+    if (rank == 0 && w == 1 && lane == 0) {
+      tc_commit<kCtas>(&drained);
       for (int p = 0; p < kWaitLimit && !mbar_try_wait(&drained, 0); ++p) {
       }
     }
     __syncthreads();
   }
-  if (w == 1)
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(G::kCols) : "memory");
+  if (kCtas == 2) cluster_sync();   // neither CTA reads the other's memory any more
+  if (w == 1) tc_free<kCtas>(tmem, G::kCols);
 }
 
 bool aligned(const void* p, int bytes) { return ((uintptr_t)p & (uintptr_t)(bytes - 1)) == 0; }
@@ -673,20 +757,36 @@ cudaError_t make_map(CUtensorMap* map, const uint8_t* codes, int64_t rows, int64
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-template <int kTN>
+template <int kTN, int kCtas>
 cudaError_t product_t(const CallView& v, const uint8_t* xc, const uint8_t* wc, int64_t width, const Args& a,
                       cudaStream_t st) {
-  using G = Geom<kTN>;
+  using G = Geom<kTN, kCtas>;
   CUtensorMap wmap, xmap;
   const int64_t cb = EBC_MX4_CODE_BYTES(width);
   cudaError_t e = make_map(&wmap, wc, a.experts * a.outs, cb, kM);
   if (e == cudaSuccess) e = make_map(&xmap, xc, a.rows, cb, G::kBox);
   if (e != cudaSuccess) return e;
-  e = cudaFuncSetAttribute(k_mx4_product<kTN>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)G::kSmem);
+  e = cudaFuncSetAttribute(k_mx4_product<kTN, kCtas>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)G::kSmem);
   if (e != cudaSuccess) return e;
-  const int64_t most = (a.rows / kTN + (a.experts < a.rows ? a.experts : a.rows)) * ((a.outs + kM - 1) / kM);
-  return launch_named(v, "k_mx4_product", st, k_mx4_product<kTN>, dim3((unsigned)(most < v.nsm ? most : v.nsm)),
-                      dim3(kThreads), G::kSmem, 1, wmap, xmap, a);
+  const int64_t most = (a.rows / kTN + (a.experts < a.rows ? a.experts : a.rows)) *
+                       ((a.outs + G::kOuts - 1) / G::kOuts), ctas = v.nsm / kCtas;
+  return launch_named(v, "k_mx4_product", st, k_mx4_product<kTN, kCtas>,
+                      dim3((unsigned)((most < ctas ? most : ctas) * kCtas)), dim3(kThreads), G::kSmem, kCtas, wmap,
+                      xmap, a);
+}
+
+// The rows of a tile.  An expert's share of the rows, spread evenly, fills it
+// ...; but smaller ones as long as some SMs would have no tile.
+int tile_rows(int64_t rows, int64_t outs, int experts, int nsm) {
+  const int64_t active = experts < rows ? experts : rows, share = (rows + active - 1) / active;
+  int tn = 16;
+  while (tn < 256 && tn < share) tn *= 2;
+  if (tn == 256 && outs <= kM) tn = 128;   // half of a pair would have no outputs
+  auto tiles = [&](int n) {
+    return (rows / n + active / 2 + 1) * ((outs + kM - 1) / kM);
+  };
+  while (tn > 16 && tiles(tn) < nsm) tn /= 2;
+  return tn;
 }
 
 }  // namespace
@@ -721,13 +821,13 @@ int ebc_mx4_product(ebc_ctx* ctx, const uint8_t* d_x_codes, const uint8_t* d_x_s
   a.blocks = (int)((width + EBC_MX4_BLOCK - 1) / EBC_MX4_BLOCK);
   a.experts = n_experts;
   a.wide = aligned(d_ys, 16) && outs * b % 16 == 0;
-  // the rows of a tile: an expert's share of the rows, spread evenly
-  const int64_t share = (rows + n_experts - 1) / n_experts;
-  if (share <= 16) return cuda_code(product_t<16>(v, d_x_codes, d_w_codes, width, a, st));
-  if (share <= 32) return cuda_code(product_t<32>(v, d_x_codes, d_w_codes, width, a, st));
-  if (share <= 64) return cuda_code(product_t<64>(v, d_x_codes, d_w_codes, width, a, st));
-  if (share <= 128) return cuda_code(product_t<128>(v, d_x_codes, d_w_codes, width, a, st));
-  return cuda_code(product_t<256>(v, d_x_codes, d_w_codes, width, a, st));
+  switch (tile_rows(rows, outs, n_experts, v.nsm)) {
+    case 16: return cuda_code(product_t<16, 1>(v, d_x_codes, d_w_codes, width, a, st));
+    case 32: return cuda_code(product_t<32, 1>(v, d_x_codes, d_w_codes, width, a, st));
+    case 64: return cuda_code(product_t<64, 1>(v, d_x_codes, d_w_codes, width, a, st));
+    case 128: return cuda_code(product_t<128, 1>(v, d_x_codes, d_w_codes, width, a, st));
+    default: return cuda_code(product_t<256, 2>(v, d_x_codes, d_w_codes, width, a, st));
+  }
 }
 
 }  // extern "C"
