@@ -170,6 +170,15 @@ def test_product(ex, rows, experts, outs, width, dtype):
     check_product(ex, x, w, offsets, dtype)
 
 
+@pytest.mark.parametrize("rows,experts,outs,width", [
+    (4000, 3, 4000, 800), (5000, 7, 2056, 2592), (3001, 1, 3999, 4192), (2500, 2, 2500, 8480), (9000, 40, 1300, 1056)])
+def test_product_of_many_tiles(ex, rows, experts, outs, width):
+    """Large tiles, several of them one after the other, long sums of every number of stages."""
+    x, w, offsets = case(ex, rows, experts, outs, width, rows + outs)
+    for dtype in TYPES:
+        check_product(ex, x, w, offsets, dtype)
+
+
 @pytest.mark.parametrize("rows,experts", [(5, 1024), (3000, 700), (40, 64)])
 def test_product_of_many_experts(ex, rows, experts):
     x, w, offsets = case(ex, rows, experts, 40, 64, rows)
