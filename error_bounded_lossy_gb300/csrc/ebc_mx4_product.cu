@@ -20,35 +20,30 @@ constexpr int kM = 128;
 constexpr int kStageK = 256;
 constexpr int kRowBytes = kStageK / 2;
 constexpr int kScaleTile = 512;    // bytes of the scales of 128 rows x 4 blocks, as the matrix unit wants them
-// warp 0 loads, warp 1 multiplies, warps 2-4 lay out scales, warps 5-12 store
-constexpr int kThreads = 416;
-constexpr int kScaleWarp0 = 2, kScaleWarps = 3;
-constexpr int kStoreWarp0 = 5, kStoreWarps = 8;
+// warp 0 loads, warp 1 multiplies, warps 2-3 lay out scales, warps 4-11 store:
+// three warps a scheduler, so that a storing thread can hold its share of a
+// tile (64 words) in its 168 registers
+constexpr int kThreads = 384;
+constexpr int kScaleWarp0 = 2, kScaleWarps = 2;
+constexpr int kStoreWarp0 = 4, kStoreWarps = 8;
 constexpr int kStoreRows = 16;     // rows that a storing warp turns over at a time
 constexpr int kStorePitch = 80;    // bytes of such a row of 32 outputs: 64, and 16 to spread the banks
 
-// kQuad: clusters of two pairs of CTAs.  A pair works on one tile of 256 outputs:
-// each CTA brings in its own 128 outputs, and the pair's matrix instructions
-// read half of the rows from either.  The two pairs have neighbouring outputs
-// of the same rows: each brings in half of them, for both.  So a CTA asks L2
-// for 128 + kTN / 4 rows a stage instead of 128 + kTN, which matters: with
-// pairs alone (128 + kTN / 2) L2's 13.6 TB/s bounded the large products.
-template <int kTN, bool kQuad>
+// kCtas = 2: a pair of CTAs on one tile of 256 outputs.  Each brings in its own
+// 128 outputs and half of the rows; the pair's matrix instructions read both
+// halves, so a CTA moves and reads half as many of the rows' bytes.
+template <int kTN, int kCtas>
 struct Geom {
-  static constexpr int kCtas = kQuad ? 2 : 1;                             // CTAs of a matrix instruction
-  static constexpr int kPairs = kQuad ? 2 : 1;
-  static constexpr int kCluster = kCtas * kPairs;
-  static constexpr int kOuts = kM * kCtas;                                // outputs of a matrix instruction
-  static constexpr int kWide = kM * kCluster;                             // outputs of a cluster
+  static constexpr int kOuts = kM * kCtas;                                // outputs of a tile
   static constexpr int kScaleB = (kTN + 127) / 128;                       // scale tiles of the rows per 4 blocks
-  static constexpr int kBRows = kTN / kCtas;                              // rows that a CTA holds
-  static constexpr int kBox = kQuad ? kBRows / kPairs : kBRows < 64 ? kBRows : 64;   // rows of one copy
+  static constexpr int kBRows = kTN / kCtas;                              // rows that a CTA brings in
+  static constexpr int kBox = kBRows < 64 ? kBRows : 64;                  // rows of one copy
   static constexpr int kRound = 16 * kCtas;                               // N of the instructions is a multiple
   static constexpr int kABytes = kM * kRowBytes;
   static constexpr int kBBytes = kBRows * kRowBytes;
   static constexpr int kScaleBytes = 2 * (1 + kScaleB) * kScaleTile;      // per stage: 8 blocks a row
-  static constexpr int kStages = kTN == 192 ? 5 : kTN == 128 ? 6 : kTN == 64 ? 7 : 8;
-  static constexpr int kAcc = 2;                                          // accumulators
+  static constexpr int kStages = kTN == 256 ? 5 : kTN == 128 ? 6 : kTN == 64 ? 7 : 8;
+  static constexpr int kAcc = kTN == 256 ? 1 : 2;                         // accumulators
   static constexpr int kAccCols = kTN < 32 ? 32 : kTN;
   static constexpr int kScaleCols = 2 * (1 + kScaleB) * 4;                // tensor memory columns per stage
   static constexpr int kCols = 512;
@@ -71,12 +66,12 @@ __device__ __forceinline__ void mbar_init(uint64_t* bar, uint32_t count) {
 __device__ __forceinline__ void mbar_expect_tx(uint64_t* bar, uint32_t bytes) {
   asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(bar)), "r"(bytes) : "memory");
 }
-// The address of a shared variable of CTA `rank` of the cluster (kCtas = 1: of
-// this one), as the cluster's shared memory has it.
+// The address of a shared variable of the pair's first CTA (kCtas = 1: of this
+// one), as the pair's shared memory has it.
 template <int kCtas>
-__device__ __forceinline__ uint32_t in_cta(const void* p, uint32_t rank) {
+__device__ __forceinline__ uint32_t in_first(const void* p) {
   uint32_t r = smem_u32(p);
-  if constexpr (kCtas == 2) asm volatile("mapa.shared::cluster.u32 %0, %0, %1;" : "+r"(r) : "r"(rank));
+  if constexpr (kCtas == 2) asm volatile("mapa.shared::cluster.u32 %0, %0, 0;" : "+r"(r));
   return r;
 }
 // An arrival at such a barrier.  What it announces has been handed to the async
@@ -126,29 +121,19 @@ __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map
         "l"(map), "r"(c0), "r"(c1), "r"(bar)
         : "memory");
 }
-// a box into the shared memory of the CTAs in `mask`, at the same place in each;
-// its bytes are counted at `bar`'s place in each one's pair
-__device__ __forceinline__ void tma_load_2d_all(uint32_t dst, const CUtensorMap* map, uint32_t bar, int c0, int c1,
-                                                uint16_t mask) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes.multicast::cluster "
-      "[%0], [%1, {%2, %3}], [%4], %5;" ::"r"(dst),
-      "l"(map), "r"(c0), "r"(c1), "r"(bar), "h"(mask)
-      : "memory");
-}
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-// an arrival at `bar` (kCtas = 2: of the CTAs in `mask`) once what was issued is done
+// an arrival at `bar` (of both CTAs of a pair) once what was issued is done
 template <int kCtas>
-__device__ __forceinline__ void tc_commit(uint64_t* bar, uint16_t mask) {
+__device__ __forceinline__ void tc_commit(uint64_t* bar) {
   if constexpr (kCtas == 2)
     asm volatile(
         "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
             smem_u32(bar)),
-        "h"(mask)
+        "h"((uint16_t)3)
         : "memory");
   else
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
@@ -233,11 +218,14 @@ __device__ __forceinline__ bool elect_one() {
 __device__ __forceinline__ void tc_load_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 
 // Shared-memory operand descriptor: rows of 128 bytes in the 128-byte swizzle,
-// eight-row groups 1024 bytes apart.  Steps of 16 bytes are added to it.
-constexpr uint64_t kOperandDesc = (1ull << 16) | (64ull << 32) | (1ull << 46) | (2ull << 61);
+// eight-row groups 1024 bytes apart.
+__device__ __forceinline__ uint64_t operand_desc(uint32_t addr) {
+  return (uint64_t)((addr >> 4) & 0x3FFFu) | (1ull << 16) | (64ull << 32) | (1ull << 46) | (2ull << 61);
+}
 // Scales: no swizzle, eight-row groups of 16-byte rows 128 bytes apart.
-constexpr uint64_t kScaleDesc = (1ull << 16) | (8ull << 32) | (1ull << 46);
-__device__ __forceinline__ uint32_t desc_addr(uint32_t addr) { return (addr >> 4) & 0x3FFFu; }
+__device__ __forceinline__ uint64_t scale_desc(uint32_t addr) {
+  return (uint64_t)((addr >> 4) & 0x3FFFu) | (1ull << 16) | (8ull << 32) | (1ull << 46);
+}
 // Instruction descriptor: both operands E2M1 along K, scales UE8M0, M = m,
 // N = n; `id` (0 or 2) is the byte of a scale word where the instruction's two
 // blocks start.
@@ -275,13 +263,6 @@ struct Walk {
     *count = left < tn ? left : tn;
     return true;
   }
-  __device__ __forceinline__ bool at_uniform(const int* begin, const int* tiles, int experts, int tn, int* row0,
-                                             int* count) {
-    const bool more = at(begin, tiles, experts, tn, row0, count);
-    *row0 = __shfl_sync(0xffffffffu, *row0, 0);
-    *count = __shfl_sync(0xffffffffu, *count, 0);
-    return __all_sync(0xffffffffu, more);
-  }
   __device__ __forceinline__ void next(int out_tiles) {
     run += step_run;
     out += step_out;
@@ -315,15 +296,12 @@ __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile in
   return false;
 }
 
-template <typename T>
-__device__ __forceinline__ uint32_t pack2(uint32_t lo, uint32_t hi);
-template <>
-__device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(uint32_t lo, uint32_t hi) {
-  const __nv_bfloat162 v = __floats2bfloat162_rn(__uint_as_float(lo), __uint_as_float(hi));
-  return *reinterpret_cast<const uint32_t*>(&v);
-}
-template <>
-__device__ __forceinline__ uint32_t pack2<__half>(uint32_t lo, uint32_t hi) {
+// two sums as bf16 or fp16, `lo` in the low half
+__device__ __forceinline__ uint32_t pack2(uint32_t lo, uint32_t hi, bool bf16) {
+  if (bf16) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(__uint_as_float(lo), __uint_as_float(hi));
+    return *reinterpret_cast<const uint32_t*>(&v);
+  }
   const __half2 v = __floats2half2_rn(__uint_as_float(lo), __uint_as_float(hi));
   return *reinterpret_cast<const uint32_t*>(&v);
 }
@@ -337,14 +315,13 @@ __device__ __forceinline__ void load_half(uint32_t taddr, Fragments* f) {
   tc_load_fragments(taddr, f->lo);
   tc_load_fragments(taddr + (16u << 16), f->hi);
 }
-template <typename T>
-__device__ __forceinline__ void pack_half(const Fragments& f, uint32_t (&v)[8]) {
+__device__ __forceinline__ void pack_half(const Fragments& f, bool bf16, uint32_t (&v)[8]) {
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    v[4 * h] = pack2<T>(f.lo[4 * h], f.lo[4 * h + 1]);
-    v[4 * h + 1] = pack2<T>(f.lo[4 * h + 2], f.lo[4 * h + 3]);
-    v[4 * h + 2] = pack2<T>(f.hi[4 * h], f.hi[4 * h + 1]);
-    v[4 * h + 3] = pack2<T>(f.hi[4 * h + 2], f.hi[4 * h + 3]);
+    v[4 * h] = pack2(f.lo[4 * h], f.lo[4 * h + 1], bf16);
+    v[4 * h + 1] = pack2(f.lo[4 * h + 2], f.lo[4 * h + 3], bf16);
+    v[4 * h + 2] = pack2(f.hi[4 * h], f.hi[4 * h + 1], bf16);
+    v[4 * h + 3] = pack2(f.hi[4 * h + 2], f.hi[4 * h + 3], bf16);
   }
 }
 
@@ -353,8 +330,7 @@ __device__ __forceinline__ void pack_half(const Fragments& f, uint32_t (&v)[8]) 
 // lanes a row).  y: where the lane's first row goes (the second is 8 further,
 // ld8 elements on); n_row rows from the first on are written, and n_out
 // outputs of each (8 = in one store).
-template <typename T>
-__device__ __forceinline__ void store_half(const uint32_t (&v)[8], uint32_t stage, T* y, int64_t ld8, int n_out,
+__device__ __forceinline__ void store_half(const uint32_t (&v)[8], uint32_t stage, uint16_t* y, int64_t ld8, int n_out,
                                            int n_row, int lane) {
   __syncwarp();   // the piece has been read
 #pragma unroll
@@ -365,13 +341,13 @@ __device__ __forceinline__ void store_half(const uint32_t (&v)[8], uint32_t stag
   __syncwarp();
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    Vec<T, 16> o;
+    Vec<uint16_t, 16> o;
     asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
                  : "=r"(o.raw.x), "=r"(o.raw.y), "=r"(o.raw.z), "=r"(o.raw.w)
                  : "r"(stage + (h * 8 + (lane >> 2)) * kStorePitch + (lane & 3) * 16)
                  : "memory");
     if (8 * h >= n_row) continue;
-    T* dst = y + h * ld8;
+    uint16_t* dst = y + h * ld8;
     if (n_out == 8) {
       *reinterpret_cast<uint4*>(dst) = o.raw;
     } else {
@@ -384,42 +360,37 @@ __device__ __forceinline__ void store_half(const uint32_t (&v)[8], uint32_t stag
 }
 
 // A storing warp's share of a tile, 16-bit results: 32 outputs of every other
-// run of 16 rows.  Up to kHold runs are read and rounded before they are
-// stored (as many as fit the registers), and the accumulator is given back
-// once the last have been read, while the next tile is multiplied.
-template <typename T, int kTN, int kCtas>
-__device__ __forceinline__ void store_tile(uint32_t d, uint32_t stage, T* y, int64_t ld, int64_t n_out, int odd,
+// run of 16 rows.  All of it is read and rounded first and the accumulator
+// given back, then it is stored while the next tile is multiplied.
+template <int kTN, int kCtas>
+__device__ __forceinline__ void store_tile(uint32_t d, uint32_t stage, bool bf16, uint16_t* y, int64_t ld, int64_t n_out, int odd,
                                            int count, bool wide, int lane, uint32_t given_back) {
-  constexpr int kRuns = kTN < 32 ? 1 : kTN / 32, kHold = kRuns < 4 ? kRuns : kRuns / 2;
+  constexpr int kRuns = kTN < 32 ? 1 : kTN / 32;
+  uint32_t v[kRuns][8];
+  constexpr int kBatch = kRuns < 2 ? kRuns : 2;   // runs whose loads are in flight
+#pragma unroll
+  for (int i0 = 0; i0 < kRuns; i0 += kBatch) {
+    Fragments f[kBatch];
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i)
+      if (((i0 + i) * 2 + odd) * kStoreRows < count) load_half(d + ((i0 + i) * 2 + odd) * kStoreRows, &f[i]);
+    tc_load_wait();
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i)
+      if (((i0 + i) * 2 + odd) * kStoreRows < count) pack_half(f[i], bf16, v[i0 + i]);
+  }
+  tc_fence_before();
+  __syncwarp();
+  if (lane == 0) mbar_arrive<kCtas>(given_back);
   // the lane's eight outputs, and its first row
   const int o = (lane & 3) * 8, r = odd * kStoreRows + (lane >> 2);
   const int64_t have = n_out - o;
   const int mine = have >= 8 ? (wide ? 8 : 15) : have > 0 ? (int)have : 0;
   y += (int64_t)r * ld + o;
 #pragma unroll
-  for (int i0 = 0; i0 < kRuns; i0 += kHold) {
-    uint32_t v[kHold][8];
-#pragma unroll
-    for (int i = 0; i < kHold; ++i) {
-      const int c0 = ((i0 + i) * 2 + odd) * kStoreRows;
-      if (c0 < count) {
-        Fragments f;
-        load_half(d + c0, &f);
-        tc_load_wait();
-        pack_half<T>(f, v[i]);
-      }
-    }
-    if (i0 + kHold >= kRuns) {
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive<kCtas>(given_back);
-    }
-#pragma unroll
-    for (int i = 0; i < kHold; ++i) {
-      const int c0 = ((i0 + i) * 2 + odd) * kStoreRows;
-      if (c0 < count) store_half(v[i], stage, y, 8 * ld, mine, count - c0 - (lane >> 2), lane);
-      y += 2 * kStoreRows * ld;
-    }
+  for (int i = 0; i < kRuns; ++i) {
+    if ((i * 2 + odd) * kStoreRows < count) store_half(v[i], stage, y, 8 * ld, mine, count - r - i * 2 * kStoreRows, lane);
+    y += 2 * kStoreRows * ld;
   }
 }
 
@@ -439,26 +410,24 @@ __device__ __forceinline__ void store_full(uint32_t taddr, float* y, int64_t ld,
 // of a run of rows come one after the other, so that the CTAs working at the
 // same time share both operands in L2.
 //   warp 0      brings the codes of both operands in by TMA, a ring of stages
-//   warps 2-4   lay the scales out: the matrix unit reads the scales of 128
+//   warps 2-3   lay the scales out: the matrix unit reads the scales of 128
 //               rows x 4 blocks from tensor memory as 32 lanes x 4 words,
 //               row r in lane r % 32, word r / 32, so a row's four scale bytes
 //               are one 4-byte store.  Rows and blocks past the end get 1.
 //   warp 1      copies a stage's scales to tensor memory and issues its matrix
 //               instructions; each stage has its own scale columns, so they
 //               are written again only after the stage was given back
-//   warps 5-12  read the accumulator, round once, and store
+//   warps 4-11  read the accumulator, round once, and store
 // The N of the instructions is the tile's row count rounded up to 16, so a
 // ragged segment's last tile costs what it holds.
 // In a pair the first CTA multiplies for both; stages, scales and accumulators
-// are announced at its barriers, and its instructions' ends at both CTAs' (a
-// stage's at all four, as all four wait for it before they write to it).
+// are announced at its barriers, and its instructions' ends at both CTAs'.
 // Every wait is bounded (see wait()); a CTA that gives up waits for the copies
 // and instructions it has in flight, frees its tensor memory and returns.
-template <int kTN, bool kQuad>
+template <int kTN, int kCtas>
 __global__ void __launch_bounds__(kThreads, 1) k_mx4_product(const __grid_constant__ CUtensorMap wmap,
                                                              const __grid_constant__ CUtensorMap xmap, Args a) {
-  using G = Geom<kTN, kQuad>;
-  constexpr int kCtas = G::kCtas;
+  using G = Geom<kTN, kCtas>;
   extern __shared__ uint8_t raw[];
   __shared__ uint64_t full[G::kStages], scaled[G::kStages], empty[G::kStages];
   __shared__ uint64_t acc_full[G::kAcc], acc_empty[G::kAcc], drained;
@@ -467,9 +436,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx4_product(const __grid_consta
   __shared__ int s_begin[EBC_MAX_EXPERTS + 1];   // first row of each expert
   __shared__ int s_tiles[EBC_MAX_EXPERTS + 1];   // runs of kTN rows of the experts before
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
-  const int rank = kQuad ? blockIdx.x & 1 : 0, pair = kQuad ? (blockIdx.x >> 1) & 1 : 0;   // the CTA's place in the cluster
-  const uint32_t first = 2 * pair;                       // the pair's first CTA
-  const uint16_t of_pair = 3u << first, of_all = 15;
+  const int rank = kCtas == 2 ? blockIdx.x & 1 : 0;   // in the pair
   uint8_t* base = raw + (1024 - (smem_u32(raw) & 1023)) % 1024;
   uint8_t* sA = base;
   uint8_t* sB = sA + G::kStages * G::kABytes;
@@ -480,7 +447,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx4_product(const __grid_consta
     for (int i = 0; i < G::kStages; ++i) {
       mbar_init(&full[i], 1);
       mbar_init(&scaled[i], kCtas);
-      mbar_init(&empty[i], G::kPairs);
+      mbar_init(&empty[i], 1);
     }
     for (int i = 0; i < G::kAcc; ++i) {
       mbar_init(&acc_full[i], 1);
@@ -533,44 +500,35 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx4_product(const __grid_consta
     if (bad && blockIdx.x == 0) record_error(a.glob, EBC_ERR_INVALID_ARG);
   }
   __syncthreads();
-  if (kQuad) cluster_sync();   // the barriers are set up in both CTAs
+  if (kCtas == 2) cluster_sync();   // the barriers are set up in both CTAs
   tc_fence_after();
-  // (broadcast values are known to be the same in all lanes, and what they decide
-  // and address stays in uniform registers)
-  const uint32_t tmem = __shfl_sync(0xffffffffu, s_tmem, 0);
+  const uint32_t tmem = s_tmem;
   const uint32_t tmem_scales = tmem + G::kAcc * G::kAccCols;
-  const int out_tiles = (int)((a.outs + G::kWide - 1) / G::kWide);
+  const int out_tiles = (int)((a.outs + G::kOuts - 1) / G::kOuts);
   const int stages = (a.blocks + 7) / 8;   // stages of a tile
 
-  Walk walk(out_tiles, blockIdx.x / G::kCluster, gridDim.x / G::kCluster);
-  const int out_first = pair * G::kOuts + rank * kM;   // of the cluster's outputs
-  int row0 = 0, count = 0;
+  Walk walk(out_tiles, blockIdx.x / kCtas, gridDim.x / kCtas);
+  int row0, count;
   uint32_t issued = 0;   // stages that warp 0 has asked for
   if (w == 0) {
     int s = 0;
     uint32_t phase = 1;   // of the barriers that stages are given back on
     bool ok = true;
-    for (; ok && walk.at_uniform(s_begin, s_tiles, a.experts, kTN, &row0, &count); walk.next(out_tiles)) {
-      // a pair's first CTA has the first half of the instructions' N, the other
-      // the second; either pair's brings in half of that, for both (whole boxes,
-      // which overlap with the same rows where there are fewer)
-      const int mine = (count + G::kRound - 1) / G::kRound * 16, part = mine / G::kPairs;
-      const int boxes = kQuad ? G::kPairs : (mine + G::kBox - 1) / G::kBox;   // that a CTA gets
-      const int brow = row0 + rank * mine + pair * part;
-      const int wrow = (int)(walk.e * a.outs) + walk.out * G::kWide + out_first;
+    for (; ok && walk.at(s_begin, s_tiles, a.experts, kTN, &row0, &count); walk.next(out_tiles)) {
+      // a pair's first CTA has the first half of the instructions' N, the other the second
+      const int mine = (count + G::kRound - 1) / G::kRound * 16;
+      const int boxes = (mine + G::kBox - 1) / G::kBox, brow = row0 + rank * mine;
+      const int wrow = (int)(walk.e * a.outs) + walk.out * G::kOuts + rank * kM;
       for (int k = 0; k < stages; ++k) {
         ok = __all_sync(0xffffffffu, wait(&empty[s], phase, &s_abort, a.glob));
         if (!ok) break;
         if (elect_one()) {
-          const uint32_t bar = in_cta<kCtas>(&full[s], first), to = smem_u32(sB) + s * G::kBBytes;
+          const uint32_t bar = in_first<kCtas>(&full[s]);
           if (rank == 0) mbar_expect_tx(&full[s], kCtas * (G::kABytes + boxes * G::kBox * kRowBytes));
           tma_load_2d<kCtas>(smem_u32(sA) + s * G::kABytes, &wmap, bar, k * kRowBytes, wrow);
-          if constexpr (kQuad) {
-            tma_load_2d_all(to + pair * part * kRowBytes, &xmap, bar, k * kRowBytes, brow, 5u << rank);
-          } else {
-            for (int i = 0; i < boxes; ++i)
-              tma_load_2d<kCtas>(to + i * G::kBox * kRowBytes, &xmap, bar, k * kRowBytes, brow + i * G::kBox);
-          }
+          for (int i = 0; i < boxes; ++i)
+            tma_load_2d<kCtas>(smem_u32(sB) + s * G::kBBytes + i * G::kBox * kRowBytes, &xmap, bar, k * kRowBytes,
+                               brow + i * G::kBox);
         }
         __syncwarp();
         ++issued;
@@ -592,9 +550,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx4_product(const __grid_consta
     uint32_t phase = 0, acc_phase = 1;
     bool ok = true, ready = false;
     uint64_t* const watch = lane & 1 ? scaled : full;
-    const int full_stages = (a.blocks + 1) / 8;   // stages of four instructions
-    const uint32_t desc_a = desc_addr(smem_u32(sA)), desc_b = desc_addr(smem_u32(sB)), desc_s = desc_addr(smem_u32(sS));
-    for (; ok && walk.at_uniform(s_begin, s_tiles, a.experts, kTN, &row0, &count); walk.next(out_tiles)) {
+    for (; ok && walk.at(s_begin, s_tiles, a.experts, kTN, &row0, &count); walk.next(out_tiles)) {
       const int n = (count + G::kRound - 1) / G::kRound * G::kRound;
       const uint32_t id0 = instr_desc(G::kOuts, n, 0), id2 = instr_desc(G::kOuts, n, 2);
       ok = __all_sync(0xffffffffu, wait(&acc_empty[buf], acc_phase, &s_abort, a.glob));
@@ -611,9 +567,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx4_product(const __grid_consta
         const bool over = mbar_test(&watch[s_next], phase ^ (s_next == 0));
         if (elect_one()) {
           const uint32_t ta = tmem_scales + s * G::kScaleCols, tb = ta + 8;
-          const uint64_t ds = kScaleDesc + (desc_s + s * (G::kScaleBytes >> 4));
-          const uint64_t da = kOperandDesc + (desc_a + s * (G::kABytes >> 4));
-          const uint64_t db = kOperandDesc + (desc_b + s * (G::kBBytes >> 4));
+          const uint64_t ds = scale_desc(smem_u32(sS) + s * G::kScaleBytes);
 #pragma unroll
           for (int q = 0; q < 2; ++q) {
             tc_copy_scales<kCtas>(ta + 4 * q, ds + q * (kScaleTile >> 4));
@@ -621,21 +575,16 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx4_product(const __grid_consta
             for (int j = 0; j < G::kScaleB; ++j)
               tc_copy_scales<kCtas>(tb + 4 * (q * G::kScaleB + j), ds + (2 + q * G::kScaleB + j) * (kScaleTile >> 4));
           }
-          tc_mma<kCtas>(d, da, db, id0, ta, tb, k > 0);
-          if (k < full_stages) {
+          const int left = a.blocks - k * 8;   // scale blocks from here on
+          const uint64_t da = operand_desc(smem_u32(sA) + s * G::kABytes);
+          const uint64_t db = operand_desc(smem_u32(sB) + s * G::kBBytes);
 #pragma unroll
-            for (int q = 1; q < 4; ++q)
-              tc_mma<kCtas>(d, da + 2 * q, db + 2 * q, q & 1 ? id2 : id0, ta + 4 * (q >> 1),
-                            tb + 4 * G::kScaleB * (q >> 1), 1);
-          } else {   // the last stage, where it ends early
-#pragma unroll
-            for (int q = 1; q < 4; ++q)
-              if (2 * q < a.blocks - k * 8)
-                tc_mma<kCtas>(d, da + 2 * q, db + 2 * q, q & 1 ? id2 : id0, ta + 4 * (q >> 1),
-                              tb + 4 * G::kScaleB * (q >> 1), 1);
-          }
-          tc_commit<kCtas>(&empty[s], of_all);
-          if (k == stages - 1) tc_commit<kCtas>(&acc_full[buf], of_pair);
+          for (int q = 0; q < 4; ++q)
+            if (2 * q < left)
+              tc_mma<kCtas>(d, da + 2 * q, db + 2 * q, q & 1 ? id2 : id0, ta + 4 * (q >> 1), tb + 4 * G::kScaleB * (q >> 1),
+                     k > 0 || q > 0);
+          tc_commit<kCtas>(&empty[s]);
+          if (k == stages - 1) tc_commit<kCtas>(&acc_full[buf]);
         }
         ready = __all_sync(0xffffffffu, over);
         phase ^= s_next == 0;
@@ -648,7 +597,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx4_product(const __grid_consta
     }
     }
   } else if (w < kStoreWarp0) {
-    // A warp takes every third group of 512 values (two stages), 16 scale bytes
+    // A warp takes every other group of 512 values (two stages), 16 scale bytes
     // a row.  A lane has rows lane, + 32, + 64 and + 96 of each 128, whose words
     // stand next to each other: one 16-byte store for 4 blocks of 4 rows.  The
     // loads of a group are over before its fence, which would wait for them.
@@ -662,7 +611,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx4_product(const __grid_consta
       const uint8_t* src[kTiles][4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const int64_t wr = walk.e * a.outs + walk.out * G::kWide + out_first + j * 32 + lane;
+        const int64_t wr = walk.e * a.outs + walk.out * G::kOuts + rank * kM + j * 32 + lane;
         src[0][j] = wr < weights ? a.ws + wr * a.scale_bytes : nullptr;
 #pragma unroll
         for (int i = 1; i < kTiles; ++i) {
@@ -712,7 +661,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx4_product(const __grid_consta
                              word[i][3][2 * half + q]);
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           __syncwarp();
-          if (lane == 0) mbar_arrive<kCtas>(in_cta<kCtas>(&scaled[s], first));
+          if (lane == 0) mbar_arrive<kCtas>(in_first<kCtas>(&scaled[s]));
         }
       }
       turn = g - groups;
@@ -727,22 +676,19 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx4_product(const __grid_consta
     for (; walk.at(s_begin, s_tiles, a.experts, kTN, &row0, &count); walk.next(out_tiles)) {
       if (!__all_sync(0xffffffffu, wait(&acc_full[buf], phase, &s_abort, a.glob))) break;
       tc_fence_after();
-      const int64_t out = (int64_t)walk.out * G::kWide + out_first + quarter * 32;
+      const int64_t out = (int64_t)walk.out * G::kOuts + rank * kM + quarter * 32;
       const int64_t n_out = a.outs - out;   // outputs from here on, maybe none
       const uint32_t d = tmem + buf * G::kAccCols + ((uint32_t)(quarter * 32) << 16);
       const int64_t at = (int64_t)row0 * a.outs + out;
-      if (a.out_type == EBC_BF16) {
-        store_tile<__nv_bfloat16, kTN, kCtas>(d, stage, (__nv_bfloat16*)a.ys + at, a.outs, n_out, odd, count, a.wide, lane,
-                                              in_cta<kCtas>(&acc_empty[buf], first));
-      } else if (a.out_type == EBC_F16) {
-        store_tile<__half, kTN, kCtas>(d, stage, (__half*)a.ys + at, a.outs, n_out, odd, count, a.wide, lane,
-                                       in_cta<kCtas>(&acc_empty[buf], first));
+      if (a.out_type != EBC_F32) {
+        store_tile<kTN, kCtas>(d, stage, a.out_type == EBC_BF16, (uint16_t*)a.ys + at, a.outs, n_out, odd, count, a.wide,
+                               lane, in_first<kCtas>(&acc_empty[buf]));
       } else {
         for (int c0 = odd * kStoreRows; c0 < count; c0 += 2 * kStoreRows)
           store_full(d + c0, (float*)a.ys + at + c0 * a.outs, a.outs, n_out, count - c0, lane);
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive<kCtas>(in_cta<kCtas>(&acc_empty[buf], first));
+        if (lane == 0) mbar_arrive<kCtas>(in_first<kCtas>(&acc_empty[buf]));
       }
       if (++buf == G::kAcc) {
         buf = 0;
@@ -774,13 +720,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx4_product(const __grid_consta
         }
     }
     if (rank == 0 && w == 1 && lane == 0) {
-      tc_commit<kCtas>(&drained, of_pair);
+      tc_commit<kCtas>(&drained);
       for (int p = 0; p < kWaitLimit && !mbar_try_wait(&drained, 0); ++p) {
       }
     }
     __syncthreads();
   }
-  if (kQuad) cluster_sync();   // no CTA reads or writes another's memory any more
+  if (kCtas == 2) cluster_sync();   // neither CTA reads the other's memory any more
   if (w == 1) tc_free<kCtas>(tmem, G::kCols);
 }
 
@@ -808,43 +754,22 @@ cudaError_t make_map(CUtensorMap* map, const uint8_t* codes, int64_t rows, int64
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-template <int kTN, bool kQuad>
+template <int kTN, int kCtas>
 cudaError_t product_t(const CallView& v, const uint8_t* xc, const uint8_t* wc, int64_t width, const Args& a,
                       cudaStream_t st) {
-  using G = Geom<kTN, kQuad>;
+  using G = Geom<kTN, kCtas>;
   CUtensorMap wmap, xmap;
   const int64_t cb = EBC_MX4_CODE_BYTES(width);
   cudaError_t e = make_map(&wmap, wc, a.experts * a.outs, cb, kM);
   if (e == cudaSuccess) e = make_map(&xmap, xc, a.rows, cb, G::kBox);
   if (e != cudaSuccess) return e;
-  e = cudaFuncSetAttribute(k_mx4_product<kTN, kQuad>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)G::kSmem);
+  e = cudaFuncSetAttribute(k_mx4_product<kTN, kCtas>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)G::kSmem);
   if (e != cudaSuccess) return e;
-  int64_t clusters = v.nsm;
-  if (kQuad) {
-    // the clusters that fit at once: the SMs of a part of the device may not
-    // divide by four (36 of them on 152 SMs); the same for every call
-    static const int fit = [] {
-      cudaLaunchConfig_t cfg = {};
-      cfg.gridDim = dim3(G::kCluster);
-      cfg.blockDim = dim3(kThreads);
-      cfg.dynamicSmemBytes = G::kSmem;
-      cudaLaunchAttribute attr;
-      attr.id = cudaLaunchAttributeClusterDimension;
-      attr.val.clusterDim.x = G::kCluster;
-      attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-      cfg.attrs = &attr;
-      cfg.numAttrs = 1;
-      int n = 0;
-      return cudaOccupancyMaxActiveClusters(&n, k_mx4_product<kTN, kQuad>, &cfg) == cudaSuccess ? n : 0;
-    }();
-    if (fit <= 0) return cudaErrorInvalidConfiguration;
-    clusters = fit;
-  }
   const int64_t most = (a.rows / kTN + (a.experts < a.rows ? a.experts : a.rows)) *
-                       ((a.outs + G::kWide - 1) / G::kWide);
-  return launch_named(v, "k_mx4_product", st, k_mx4_product<kTN, kQuad>,
-                      dim3((unsigned)((most < clusters ? most : clusters) * G::kCluster)), dim3(kThreads), G::kSmem,
-                      G::kCluster, wmap, xmap, a);
+                       ((a.outs + G::kOuts - 1) / G::kOuts), ctas = v.nsm / kCtas;
+  return launch_named(v, "k_mx4_product", st, k_mx4_product<kTN, kCtas>,
+                      dim3((unsigned)((most < ctas ? most : ctas) * kCtas)), dim3(kThreads), G::kSmem, kCtas, wmap,
+                      xmap, a);
 }
 
 // The rows of a tile.  An expert's share of the rows, spread evenly, fills it
@@ -852,12 +777,12 @@ cudaError_t product_t(const CallView& v, const uint8_t* xc, const uint8_t* wc, i
 int tile_rows(int64_t rows, int64_t outs, int experts, int nsm) {
   const int64_t active = experts < rows ? experts : rows, share = (rows + active - 1) / active;
   int tn = 16;
-  while (tn < 128 && tn < share) tn *= 2;
-  if (share > 128 && outs > 2 * kM) tn = 192;   // four CTAs' tile; with fewer outputs half of it would have none
+  while (tn < 256 && tn < share) tn *= 2;
+  if (tn == 256 && outs <= kM) tn = 128;   // half of a pair would have no outputs
   auto tiles = [&](int n) {
     return (rows / n + active / 2 + 1) * ((outs + kM - 1) / kM);
   };
-  while (tn > 16 && tiles(tn) < nsm) tn = tn == 192 ? 128 : tn / 2;
+  while (tn > 16 && tiles(tn) < nsm) tn /= 2;
   return tn;
 }
 
@@ -894,11 +819,11 @@ int ebc_mx4_product(ebc_ctx* ctx, const uint8_t* d_x_codes, const uint8_t* d_x_s
   a.experts = n_experts;
   a.wide = aligned(d_ys, 16) && outs * b % 16 == 0;
   switch (tile_rows(rows, outs, n_experts, v.nsm)) {
-    case 16: return cuda_code(product_t<16, false>(v, d_x_codes, d_w_codes, width, a, st));
-    case 32: return cuda_code(product_t<32, false>(v, d_x_codes, d_w_codes, width, a, st));
-    case 64: return cuda_code(product_t<64, false>(v, d_x_codes, d_w_codes, width, a, st));
-    case 128: return cuda_code(product_t<128, false>(v, d_x_codes, d_w_codes, width, a, st));
-    default: return cuda_code(product_t<192, true>(v, d_x_codes, d_w_codes, width, a, st));
+    case 16: return cuda_code(product_t<16, 1>(v, d_x_codes, d_w_codes, width, a, st));
+    case 32: return cuda_code(product_t<32, 1>(v, d_x_codes, d_w_codes, width, a, st));
+    case 64: return cuda_code(product_t<64, 1>(v, d_x_codes, d_w_codes, width, a, st));
+    case 128: return cuda_code(product_t<128, 1>(v, d_x_codes, d_w_codes, width, a, st));
+    default: return cuda_code(product_t<256, 2>(v, d_x_codes, d_w_codes, width, a, st));
   }
 }
 
