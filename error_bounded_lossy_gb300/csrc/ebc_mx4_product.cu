@@ -772,18 +772,25 @@ cudaError_t product_t(const CallView& v, const uint8_t* xc, const uint8_t* wc, i
                       xmap, a);
 }
 
-// The rows of a tile.  An expert's share of the rows, spread evenly, fills it
-// ...; but smaller ones as long as some SMs would have no tile.
+// The rows of a tile: what makes the fewest turns of the machine, and the
+// smaller of two that make as many.  A tile of 16 rows costs a stage about as
+// much as one of 128 (the instructions of a stage take 450 cycles to issue
+// either way, and 512 to run at 256 rows).
 int tile_rows(int64_t rows, int64_t outs, int experts, int nsm) {
-  const int64_t active = experts < rows ? experts : rows, share = (rows + active - 1) / active;
-  int tn = 16;
-  while (tn < 256 && tn < share) tn *= 2;
-  if (tn == 256 && outs <= kM) tn = 128;   // half of a pair would have no outputs
-  auto tiles = [&](int n) {
-    return (rows / n + active / 2 + 1) * ((outs + kM - 1) / kM);
-  };
-  while (tn > 16 && tiles(tn) < nsm) tn /= 2;
-  return tn;
+  const int64_t active = experts < rows ? experts : rows;
+  int best = 16;
+  int64_t least = INT64_MAX;
+  for (int tn = 16; tn <= 256; tn *= 2) {
+    const int64_t wide = tn == 256 ? 2 * kM : kM, units = tn == 256 ? nsm / 2 : nsm;   // (256: pairs of CTAs)
+    // each expert's last run is half full on average, and a run at least
+    const int64_t runs = rows / tn + active / 2 > active ? rows / tn + active / 2 : active;
+    const int64_t turns = (runs * ((outs + wide - 1) / wide) + units - 1) / units;
+    if (turns < least) {
+      least = turns;
+      best = tn;
+    }
+  }
+  return best;
 }
 
 }  // namespace
