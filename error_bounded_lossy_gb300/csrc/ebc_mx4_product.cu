@@ -281,6 +281,7 @@ struct Args {
   Glob* glob;
   int64_t rows, outs, scale_bytes;
   int out_type, blocks, experts;   // blocks: scale blocks a row
+  int split_log2;                  // CTAs (a cluster) that share a tile's K; more than one only with a tile a cluster
   bool wide;                       // 16-byte stores of rows
 };
 
@@ -420,6 +421,9 @@ __device__ __forceinline__ void store_full(uint32_t taddr, float* y, int64_t ld,
 //   warps 4-11  read the accumulator, round once, and store
 // The N of the instructions is the tile's row count rounded up to 16, so a
 // ragged segment's last tile costs what it holds.
+// With few tiles a cluster of CTAs takes one: each the sum over its share
+// of K, which it leaves in shared memory; then each adds up the cluster's sums
+// of every split-th row, in the order of the CTAs.
 // In a pair the first CTA multiplies for both; stages, scales and accumulators
 // are announced at its barriers, and its instructions' ends at both CTAs'.
 // Every wait is bounded (see wait()); a CTA that gives up waits for the copies
@@ -507,7 +511,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx4_product(const __grid_consta
   const int out_tiles = (int)((a.outs + G::kOuts - 1) / G::kOuts);
   const int stages = (a.blocks + 7) / 8;   // stages of a tile
 
-  Walk walk(out_tiles, blockIdx.x / kCtas, gridDim.x / kCtas);
+  const int shift = kCtas == 2 ? 0 : a.split_log2, split = 1 << shift, part = (int)blockIdx.x & (split - 1);
+  // the groups of two stages, and the stages, that are this CTA's
+  const int groups = (stages + 1) / 2, group0 = groups * (kCtas == 2 ? 0 : part) >> shift,
+            group1 = groups * (kCtas == 2 ? 1 : part + 1) >> shift;
+  const int k0 = 2 * group0, k1 = 2 * group1 < stages ? 2 * group1 : stages;
+  const Walk start(out_tiles, blockIdx.x / kCtas >> shift, gridDim.x / kCtas >> shift);
+  Walk walk = start;
   int row0, count;
   uint32_t issued = 0;   // stages that warp 0 has asked for
   if (w == 0) {
@@ -519,7 +529,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx4_product(const __grid_consta
       const int mine = (count + G::kRound - 1) / G::kRound * 16;
       const int boxes = (mine + G::kBox - 1) / G::kBox, brow = row0 + rank * mine;
       const int wrow = (int)(walk.e * a.outs) + walk.out * G::kOuts + rank * kM;
-      for (int k = 0; k < stages; ++k) {
+      for (int k = k0; k < k1; ++k) {
         ok = __all_sync(0xffffffffu, wait(&empty[s], phase, &s_abort, a.glob));
         if (!ok) break;
         if (elect_one()) {
@@ -557,7 +567,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx4_product(const __grid_consta
       if (!ok) break;
       tc_fence_after();
       const uint32_t d = tmem + buf * G::kAccCols;
-      for (int k = 0; k < stages; ++k) {
+      for (int k = k0; k < k1; ++k) {
         if (!ready) {
           ok = __all_sync(0xffffffffu, wait(&watch[s], phase, &s_abort, a.glob));
           if (!ok) break;
@@ -582,9 +592,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx4_product(const __grid_consta
           for (int q = 0; q < 4; ++q)
             if (2 * q < left)
               tc_mma<kCtas>(d, da + 2 * q, db + 2 * q, q & 1 ? id2 : id0, ta + 4 * (q >> 1), tb + 4 * G::kScaleB * (q >> 1),
-                     k > 0 || q > 0);
+                     k > k0 || q > 0);
           tc_commit<kCtas>(&empty[s]);
-          if (k == stages - 1) tc_commit<kCtas>(&acc_full[buf]);
+          if (k == k1 - 1) tc_commit<kCtas>(&acc_full[buf]);
         }
         ready = __all_sync(0xffffffffu, over);
         phase ^= s_next == 0;
@@ -601,7 +611,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx4_product(const __grid_consta
     // a row.  A lane has rows lane, + 32, + 64 and + 96 of each 128, whose words
     // stand next to each other: one 16-byte store for 4 blocks of 4 rows.  The
     // loads of a group are over before its fence, which would wait for them.
-    const int groups = (stages + 1) / 2;
     const int64_t weights = (int64_t)a.experts * a.outs;
     const uint32_t one = 0x7F7F7F7Fu;
     uint32_t before = 0, turn = w - kScaleWarp0;   // stages of the tiles before; groups until the warp's next
@@ -620,23 +629,24 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx4_product(const __grid_consta
         }
       }
       int g = turn;
-      for (; ok && g < groups; g += kScaleWarps) {
+      for (; ok && g < group1 - group0; g += kScaleWarps) {
+        const int at = group0 + g;
         uint32_t word[kTiles][4][4];
 #pragma unroll
         for (int i = 0; i < kTiles; ++i)
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             uint4 v = make_uint4(one, one, one, one);
-            if (src[i][j]) v = __ldg(reinterpret_cast<const uint4*>(src[i][j]) + g);
+            if (src[i][j]) v = __ldg(reinterpret_cast<const uint4*>(src[i][j]) + at);
             word[i][j][0] = v.x;
             word[i][j][1] = v.y;
             word[i][j][2] = v.z;
             word[i][j][3] = v.w;
           }
-        if (g == groups - 1) {   // blocks past the row's end
+        if (at == groups - 1) {   // blocks past the row's end
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
-            const int left = a.blocks - (g * 16 + q * 4);
+            const int left = a.blocks - (at * 16 + q * 4);
             const uint32_t keep = left >= 4 ? ~0u : left <= 0 ? 0u : (1u << (8 * left)) - 1u;
 #pragma unroll
             for (int i = 0; i < kTiles; ++i)
@@ -646,7 +656,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx4_product(const __grid_consta
         }
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
-          if (2 * g + half >= stages) break;
+          if (2 * at + half >= stages) break;
           const uint32_t n = before + 2 * g + half;
           const int s = n % G::kStages;
           ok = __all_sync(0xffffffffu, wait(&empty[s], ((n / G::kStages) & 1) ^ 1, &s_abort, a.glob));
@@ -664,8 +674,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx4_product(const __grid_consta
           if (lane == 0) mbar_arrive<kCtas>(in_first<kCtas>(&scaled[s]));
         }
       }
-      turn = g - groups;
-      before += stages;
+      turn = g - (group1 - group0);
+      before += k1 - k0;
     }
   } else {
     // a warp has the outputs of its quarter of the lanes, and every other run of 16 rows
@@ -680,7 +690,20 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx4_product(const __grid_consta
       const int64_t n_out = a.outs - out;   // outputs from here on, maybe none
       const uint32_t d = tmem + buf * G::kAccCols + ((uint32_t)(quarter * 32) << 16);
       const int64_t at = (int64_t)row0 * a.outs + out;
-      if (a.out_type != EBC_F32) {
+      if (split > 1) {
+        // the sums of the CTA's share, [row][output], where the stages were
+        float* sums = reinterpret_cast<float*>(base) + quarter * 32 + lane;
+        for (int c0 = odd * kStoreRows; c0 < count; c0 += 2 * kStoreRows) {
+          uint32_t v[16];
+          tc_load16(d + c0, v);
+          tc_load_wait();
+#pragma unroll
+          for (int c = 0; c < 16; ++c) sums[(c0 + c) * kM] = __uint_as_float(v[c]);
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive<kCtas>(in_first<kCtas>(&acc_empty[buf]));
+      } else if (a.out_type != EBC_F32) {
         store_tile<kTN, kCtas>(d, stage, a.out_type == EBC_BF16, (uint16_t*)a.ys + at, a.outs, n_out, odd, count, a.wide,
                                lane, in_first<kCtas>(&acc_empty[buf]));
       } else {
@@ -726,6 +749,36 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx4_product(const __grid_consta
     }
     __syncthreads();
   }
+  if (split > 1) {
+    cluster_sync();   // every CTA's sums are there
+    Walk tile = start;
+    if (tile.at(s_begin, s_tiles, a.experts, kTN, &row0, &count)) {
+      const int out0 = tile.out * kM, n_out = a.outs - out0 < kM ? (int)(a.outs - out0) : kM;
+      for (int i = tid; i < ((count - part + split - 1) >> shift) * kM; i += kThreads) {
+        const int c = i / kM * split + part, n = i % kM;
+        if (n >= n_out) continue;
+        float sum = 0.f;
+        for (int q = 0; q < split; ++q) {
+          uint32_t from = smem_u32(base) + (c * kM + n) * 4;
+          float v;
+          asm volatile("mapa.shared::cluster.u32 %1, %1, %2;\n ld.shared::cluster.f32 %0, [%1];"
+                       : "=f"(v), "+r"(from)
+                       : "r"(q)
+                       : "memory");
+          sum += v;
+        }
+        const int64_t at = ((int64_t)row0 + c) * a.outs + out0 + n;
+        if (a.out_type == EBC_BF16)
+          ((__nv_bfloat16*)a.ys)[at] = from_f32<__nv_bfloat16>(sum);
+        else if (a.out_type == EBC_F16)
+          ((__half*)a.ys)[at] = from_f32<__half>(sum);
+        else
+          ((float*)a.ys)[at] = sum;
+      }
+    }
+    __syncthreads();
+    cluster_sync();   // and have been read
+  }
   if (kCtas == 2) cluster_sync();   // neither CTA reads the other's memory any more
   if (w == 1) tc_free<kCtas>(tmem, G::kCols);
 }
@@ -755,7 +808,7 @@ cudaError_t make_map(CUtensorMap* map, const uint8_t* codes, int64_t rows, int64
 }
 
 template <int kTN, int kCtas>
-cudaError_t product_t(const CallView& v, const uint8_t* xc, const uint8_t* wc, int64_t width, const Args& a,
+cudaError_t product_t(const CallView& v, const uint8_t* xc, const uint8_t* wc, int64_t width, Args a,
                       cudaStream_t st) {
   using G = Geom<kTN, kCtas>;
   CUtensorMap wmap, xmap;
@@ -767,8 +820,20 @@ cudaError_t product_t(const CallView& v, const uint8_t* xc, const uint8_t* wc, i
   if (e != cudaSuccess) return e;
   const int64_t most = (a.rows / kTN + (a.experts < a.rows ? a.experts : a.rows)) *
                        ((a.outs + G::kOuts - 1) / G::kOuts), ctas = v.nsm / kCtas;
+  // Share a tile's K among up to eight CTAs where all tiles still run at once
+  // (a cluster's SMs come from one of the device's eight parts, each of which
+  // may have up to split - 1 too few for another): one row x 1024 outputs x
+  // 16384 took 20 us in 8 CTAs.
+  int split = 1;
+  a.split_log2 = 0;
+  if (kCtas == 1)
+    while (split < 8 && most * split * 2 <= v.nsm - 8 * (split * 2 - 1) && split * 2 <= (a.blocks + 15) / 16) {
+      split *= 2;
+      ++a.split_log2;
+    }
+  const unsigned cluster = kCtas * split;
   return launch_named(v, "k_mx4_product", st, k_mx4_product<kTN, kCtas>,
-                      dim3((unsigned)((most < ctas ? most : ctas) * kCtas)), dim3(kThreads), G::kSmem, kCtas, wmap,
+                      dim3((unsigned)(most < ctas ? most : ctas) * cluster), dim3(kThreads), G::kSmem, cluster, wmap,
                       xmap, a);
 }
 

@@ -179,6 +179,18 @@ def test_product_of_many_tiles(ex, rows, experts, outs, width):
         check_product(ex, x, w, offsets, dtype)
 
 
+@pytest.mark.parametrize("rows,experts,outs,width", [
+    (1, 1, 1024, 16384), (3, 1, 130, 1024), (1, 2, 500, 2080), (17, 1, 1024, 4096), (40, 2, 300, 3104), (100, 1, 200, 1568),
+    (5, 3, 128, 544), (128, 1, 64, 9000)])
+def test_product_of_few_tiles(ex, rows, experts, outs, width):
+    """Few tiles and long sums, which several CTAs share."""
+    for cut in (None, [0] * experts + [rows], [0] * experts + [rows // 2]):
+        x, w, offsets = case(ex, rows, experts, outs, width, rows + outs, cut)
+        for dtype in TYPES:
+            check_product(ex, x, w, offsets, dtype)
+        assert torch.equal(ex.product(x, w, offsets), ex.product(x, w, offsets))
+
+
 @pytest.mark.parametrize("rows,experts", [(5, 1024), (3000, 700), (40, 64)])
 def test_product_of_many_experts(ex, rows, experts):
     x, w, offsets = case(ex, rows, experts, 40, 64, rows)
