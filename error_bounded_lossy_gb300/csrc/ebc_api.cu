@@ -7,7 +7,7 @@
 #include <mutex>
 #include <new>
 
-#include "ebc_internal.cuh"
+#include "ebc_types.cuh"
 
 
 using namespace ebc;

@@ -109,12 +109,12 @@ __global__ void __launch_bounds__(kPlanThreads) k_moe_plan(const Id* __restrict_
     hist[lane * pitch + x] = inc - v;
     if (lane == 31) total[x] = inc;
   }
-  cluster.sync();
+  if (C > 1) cluster.sync(); else __syncthreads();
   // over the CTAs, then over the experts, a thread each
   uint32_t before = 0, all = 0;
   if (tid < E)
     for (int i = 0; i < C; ++i) {
-      const uint32_t v = cluster.map_shared_rank(total, i)[tid];
+      const uint32_t v = (C > 1 ? cluster.map_shared_rank(total, i) : total)[tid];
       if (i < c) before += v;
       all += v;
     }
@@ -137,7 +137,7 @@ __global__ void __launch_bounds__(kPlanThreads) k_moe_plan(const Id* __restrict_
     s_live = start + all;
     if (c == 0) offsets[E] = (int32_t)(start + all);
   }
-  cluster.sync();   // the totals have been read; base and s_live are complete
+  if (C > 1) cluster.sync(); else __syncthreads();   // the totals have been read; base and s_live are complete
   for (int64_t s = first; s < last; s += kStep) {
     bool ignore = false;
     if (!once) read_ids(ids, s + lane, last, E, e, &ignore);
@@ -176,6 +176,11 @@ __device__ __forceinline__ int64_t live_rows(const int32_t* offsets, int E, int6
 }
 
 constexpr int kRowWarps = 8;
+
+// a / b; most often in 32 bits, a fifth of the instructions
+__device__ __forceinline__ int64_t divide(int64_t a, int64_t b) {
+  return a <= UINT32_MAX ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
+}
 // Vectors of V bytes a lane holds of one piece of a row.
 template <int V>
 constexpr int scatter_vectors() {
@@ -200,7 +205,7 @@ __global__ void __launch_bounds__(32 * kRowWarps) k_moe_dispatch(const T* __rest
   const int64_t units = (tokens + (n - live)) * pieces;
   for (int64_t u = (int64_t)blockIdx.x * kRowWarps + (threadIdx.x >> 5); u < units;
        u += (int64_t)gridDim.x * kRowWarps) {
-    const int64_t t = u / pieces, h0 = (u - t * pieces) * kPiece + lane * R::kN;
+    const int64_t t = divide(u, pieces), h0 = (u - t * pieces) * kPiece + lane * R::kN;
     R v[kScatterU];
     if (t < tokens) {
       const T* src = x + t * ld;
@@ -263,11 +268,10 @@ __global__ void __launch_bounds__(32 * kRowWarps) k_moe_combine(const T* __restr
   constexpr int kU = gather_vectors<T, V>(), kStep = 32 * R::kN, kPiece = kU * kStep;
   const int lane = threadIdx.x & 31;
   const int64_t n = tokens * top;
-  const unsigned pieces = (unsigned)((width + kPiece - 1) / kPiece);
-  const int64_t units = tokens * pieces;
+  const int64_t pieces = (width + kPiece - 1) / kPiece, units = tokens * pieces;
   for (int64_t u = (int64_t)blockIdx.x * kRowWarps + (threadIdx.x >> 5); u < units;
        u += (int64_t)gridDim.x * kRowWarps) {
-    const int64_t t = units <= UINT32_MAX ? (unsigned)u / pieces : u / pieces;
+    const int64_t t = divide(u, pieces);
     const int64_t h = (u - t * pieces) * kPiece + lane * R::kN;
     const int left = (int)(width - h < kPiece ? width - h : kPiece);   // of the lane's values; may be <= 0
     float acc[kU][R::kN];
@@ -344,7 +348,7 @@ __global__ void __launch_bounds__(32 * kRowWarps) k_moe_combine_grad(
     float dot = 0.f;
     if (p >= 0) {
       const float scale = weights[s];
-      const T* a = dy + (n <= UINT32_MAX ? (unsigned)s / (unsigned)top : s / top) * ld_dy + h0;
+      const T* a = dy + divide(s, top) * ld_dy + h0;
       const T* b = ys + (int64_t)p * ld_ys + h0;
       T* dst = dys + (int64_t)p * width + h0;
       for (int64_t left = width - h0; left > 0; left -= stride) {

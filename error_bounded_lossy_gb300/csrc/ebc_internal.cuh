@@ -410,17 +410,6 @@ struct Prof;
 void prof_begin(Prof* p, const char* name, cudaStream_t st);
 void prof_end(Prof* p, cudaStream_t st);
 
-// What the expert-parallel and 4-bit entry points need of a context: its
-// device, the device's SMs, the error word that the kernels record into, and
-// the profiler.  begin_call checks the context, makes its device current and
-// notes the stream as that of the last call (defined with the C ABI).
-struct CallView {
-  int nsm;
-  Glob* glob;
-  Prof* prof;
-};
-int begin_call(ebc_ctx* ctx, cudaStream_t st, CallView* out);
-
 // ---- launchers (one per direction; D is dispatched to the templated kernels) ----
 // out_bytes: the total size; chunk_off: null, or [R] the first byte of each container.
 cudaError_t launch_compress(const void* x, bool bf16, const Shape& sh, const EbParams& ep, const Work& w,

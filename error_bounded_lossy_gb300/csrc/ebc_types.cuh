@@ -1,5 +1,6 @@
-// ebc_types.cuh -- element types and row vectors of the expert-parallel and
-// 4-bit kernels: loads and stores of V bytes, converted from and to fp32.
+// ebc_types.cuh -- what the expert-parallel and 4-bit calls share: a context as
+// they see it, element types, and row vectors (loads and stores of V bytes,
+// converted from and to fp32).
 #pragma once
 
 #include <cuda_bf16.h>
@@ -8,6 +9,17 @@
 #include "ebc_internal.cuh"
 
 namespace ebc {
+
+// What the expert-parallel and 4-bit entry points need of a context: its
+// device, the device's SMs, the error word that the kernels record into, and
+// the profiler.  begin_call checks the context, makes its device current and
+// notes the stream as that of the last call (defined with the C ABI).
+struct CallView {
+  int nsm;
+  Glob* glob;
+  Prof* prof;
+};
+int begin_call(ebc_ctx* ctx, cudaStream_t st, CallView* out);
 
 inline int type_bytes(int type) { return type == EBC_F32 ? 4 : type == EBC_BF16 || type == EBC_F16 ? 2 : 0; }
 
