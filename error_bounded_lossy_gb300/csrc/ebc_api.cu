@@ -224,6 +224,7 @@ int ebc::begin_call(ebc_ctx* c, cudaStream_t st, CallView* out) {
   if (cudaSetDevice(c->device) != cudaSuccess) return EBC_ERR_CUDA;
   c->last_stream = st;
   out->nsm = c->nsm;
+  out->first_wait = c->first_wait;
   out->glob = c->glob;
   out->prof = c->prof;
   return EBC_OK;

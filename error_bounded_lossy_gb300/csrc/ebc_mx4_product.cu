@@ -281,20 +281,39 @@ struct Args {
   Glob* glob;
   int64_t rows, outs, scale_bytes;
   int out_type, blocks, experts;   // blocks: scale blocks a row
+  int first_wait;                  // polls of the multiplying warp's first wait for a stage (normally the full limit)
   int split_log2;                  // CTAs (a cluster) that share a tile's K; more than one only with a tile a cluster
   bool wide;                       // 16-byte stores of rows
 };
 
-// A wait that gives up: after kWaitLimit polls, or once another thread of the
-// CTA did.  The first to give up records the time-out.
-__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile int* abort, Glob* glob) {
-  for (int i = 0; i < kWaitLimit; ++i) {
+// A wait that gives up: after `limit` polls or kWaitCycles, or once another
+// thread of the cluster did.  The first to give up records the time-out and
+// tells the cluster's CTAs (which all stay until the last has ended).
+constexpr long long kWaitCycles = 1ll << 32;   // about two seconds
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile int* abort, Glob* glob,
+                                     int limit = kWaitLimit) {
+  if (limit > 0 && mbar_try_wait(bar, parity)) return true;
+  const long long begin = clock64();
+  for (int i = 1; i < limit && clock64() - begin < kWaitCycles; ++i) {
     if (mbar_try_wait(bar, parity)) return true;
     if (*abort) return false;
   }
-  *abort = 1;
   record_error(glob, EBC_ERR_DEVICE_TIMEOUT);
+  uint32_t ctas;
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(ctas));
+  for (uint32_t q = 0; q < ctas; ++q) {
+    uint32_t at = smem_u32(const_cast<int*>(abort));
+    asm volatile("mapa.shared::cluster.u32 %0, %0, %1;\n st.shared::cluster.u32 [%0], %2;" : "+r"(at) : "r"(q), "r"(1)
+                 : "memory");
+  }
   return false;
+}
+
+// A wait for what is in flight, with the same limits and nobody to tell.
+__device__ __forceinline__ void drain(uint64_t* bar, uint32_t parity) {
+  const long long begin = clock64();
+  for (int i = 0; i < kWaitLimit && clock64() - begin < kWaitCycles; ++i)
+    if (mbar_try_wait(bar, parity)) return;
 }
 
 // two sums as bf16 or fp16, `lo` in the low half
@@ -504,7 +523,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx4_product(const __grid_consta
     if (bad && blockIdx.x == 0) record_error(a.glob, EBC_ERR_INVALID_ARG);
   }
   __syncthreads();
-  if (kCtas == 2) cluster_sync();   // the barriers are set up in both CTAs
+  if (kCtas == 2 || a.split_log2 > 0) cluster_sync();   // the cluster's CTAs have started and set up their barriers
   tc_fence_after();
   const uint32_t tmem = s_tmem;
   const uint32_t tmem_scales = tmem + G::kAcc * G::kAccCols;
@@ -559,6 +578,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx4_product(const __grid_consta
     int s = 0, buf = 0;
     uint32_t phase = 0, acc_phase = 1;
     bool ok = true, ready = false;
+    int limit = a.first_wait;
     uint64_t* const watch = lane & 1 ? scaled : full;
     for (; ok && walk.at(s_begin, s_tiles, a.experts, kTN, &row0, &count); walk.next(out_tiles)) {
       const int n = (count + G::kRound - 1) / G::kRound * G::kRound;
@@ -569,9 +589,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx4_product(const __grid_consta
       const uint32_t d = tmem + buf * G::kAccCols;
       for (int k = k0; k < k1; ++k) {
         if (!ready) {
-          ok = __all_sync(0xffffffffu, wait(&watch[s], phase, &s_abort, a.glob));
+          ok = __all_sync(0xffffffffu, wait(&watch[s], phase, &s_abort, a.glob, limit));
           if (!ok) break;
         }
+        limit = kWaitLimit;
         tc_fence_after();
         const int s_next = s + 1 == G::kStages ? 0 : s + 1;
         const bool over = mbar_test(&watch[s_next], phase ^ (s_next == 0));
@@ -732,20 +753,19 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx4_product(const __grid_consta
   }
 
   tc_fence_before();
-  __syncthreads();
+  const bool gave_up = __syncthreads_or(s_abort) != 0;   // the same for all threads: another CTA may set it now
   tc_fence_after();
-  if (s_abort) {
+  if (gave_up) {
     // nothing that was started may outlive the CTA (a pair's copies are counted
     // at its first CTA)
-    if (rank == 0 && w == 0 && lane == 0) {
+    if (rank == 0 && w == 0) {
       for (uint32_t i = issued > G::kStages ? issued - G::kStages : 0; i < issued; ++i)
-        for (int p = 0; p < kWaitLimit && !mbar_try_wait(&full[i % G::kStages], (i / G::kStages) & 1); ++p) {
-        }
+        drain(&full[i % G::kStages], (i / G::kStages) & 1);
     }
-    if (rank == 0 && w == 1 && lane == 0) {
-      tc_commit<kCtas>(&drained);
-      for (int p = 0; p < kWaitLimit && !mbar_try_wait(&drained, 0); ++p) {
-      }
+    if (rank == 0 && w == 1) {
+      if (elect_one()) tc_commit<kCtas>(&drained);
+      __syncwarp();
+      drain(&drained, 0);
     }
     __syncthreads();
   }
@@ -889,6 +909,7 @@ int ebc_mx4_product(ebc_ctx* ctx, const uint8_t* d_x_codes, const uint8_t* d_x_s
   a.out_type = out_type;
   a.blocks = (int)((width + EBC_MX4_BLOCK - 1) / EBC_MX4_BLOCK);
   a.experts = n_experts;
+  a.first_wait = v.first_wait;
   a.wide = aligned(d_ys, 16) && outs * b % 16 == 0;
   switch (tile_rows(rows, outs, n_experts, v.nsm)) {
     case 16: return cuda_code(product_t<16, 1>(v, d_x_codes, d_w_codes, width, a, st));

@@ -11,11 +11,11 @@
 namespace ebc {
 
 // What the expert-parallel and 4-bit entry points need of a context: its
-// device, the device's SMs, the error word that the kernels record into, and
-// the profiler.  begin_call checks the context, makes its device current and
+// device, the device's SMs, the polls of a kernel's first wait (a test aid), the
+// error word that the kernels record into, and the profiler.  begin_call checks the context, makes its device current and
 // notes the stream as that of the last call (defined with the C ABI).
 struct CallView {
-  int nsm;
+  int nsm, first_wait;
   Glob* glob;
   Prof* prof;
 };

@@ -540,7 +540,9 @@ int ebc_last_device_error(ebc_ctx* ctx);
  * (0 <= polls <= 2^22; a negative value restores the full limit, which is the
  * default).  With 0 the first wait gives up before looking, so a test can run
  * the time-out path without hanging anything; later waits keep the full
- * limit.  Host-only; EBC_ERR_INVALID_ARG for a null context or polls > 2^22. */
+ * limit.  It sets the same for the first stage that each multiplying warp of
+ * the following ebc_mx4_product calls waits for; a product that gives up leaves
+ * d_ys unspecified.  Host-only; EBC_ERR_INVALID_ARG for a null context or polls > 2^22. */
 int ebc_set_first_wait_polls(ebc_ctx* ctx, int polls);
 
 /* Per-kernel timing (tracing aid).  While enabled, every kernel launch of the

@@ -282,6 +282,23 @@ def test_offsets_that_do_not_ascend_inside_the_rows_are_recorded(cut):
     e.close()
 
 
+@pytest.mark.parametrize("rows,experts,outs,width", [(16, 8, 2000, 2048), (6000, 4, 4000, 1024), (2, 1, 600, 8192)])
+def test_a_wait_that_runs_out_is_recorded_and_the_context_recovers(rows, experts, outs, width):
+    """Single CTAs, pairs and clusters that share K: the first stage's wait gives up at once; every CTA ends, the
+    status says so, and the next product is right."""
+    e = ebc.Experts(0)
+    x, w, offsets = case(e, rows, experts, outs, width, 3)
+    assert ebc.ebc_set_first_wait_polls(e.handle, 0) == 0
+    e.product(x, w, offsets)
+    with pytest.raises(ebc.EbcError) as err:
+        e.check()
+    assert err.value.code == ebc.EBC_ERR_DEVICE_TIMEOUT
+    assert ebc.ebc_set_first_wait_polls(e.handle, -1) == 0
+    check_product(e, x, w, offsets, torch.bfloat16)
+    e.check()
+    e.close()
+
+
 def test_refusals(ex):
     x, w, offsets = case(ex, 8, 2, 16, 64, 1)
     with pytest.raises(ValueError):
