@@ -30,43 +30,86 @@ struct Eight {
   };
   __device__ __forceinline__ Eight() {}
 };
-// One load or store of 16 or 32 bytes where the row is aligned for it, else
-// one by one; values past the row's end are zero, or not written.
-template <typename T, bool kAligned>
-__device__ __forceinline__ void load8(const T* p, int64_t left, Eight<T>* v) {
-  if (kAligned && left >= kLane) {
-    if constexpr (sizeof(T) == 4)
-      asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-                   : "=r"(v->word[0]), "=r"(v->word[1]), "=r"(v->word[2]), "=r"(v->word[3]), "=r"(v->word[4]),
-                     "=r"(v->word[5]), "=r"(v->word[6]), "=r"(v->word[7])
-                   : "l"(p));
-    else
-      asm volatile("ld.global.v4.b32 {%0, %1, %2, %3}, [%4];"
-                   : "=r"(v->word[0]), "=r"(v->word[1]), "=r"(v->word[2]), "=r"(v->word[3])
-                   : "l"(p));
-  } else {
+// A warp's piece between memory and its lanes' eights; `left`: the row's values
+// from the lane's first on (values past the row's end are zero, or not written).
+// kV = 8 * sizeof(T): rows whose eights are aligned, one load or store a lane.
+// Other rows go through the warp's own piece of shared memory in vectors of kV
+// bytes, the lanes next to each other: a lane that took its eight values one by
+// one touched 16 sectors an access ([8192, 1501] bf16: 49 us to quantize and
+// read back).
+template <typename T, int kV>
+struct Piece {
+  static constexpr bool kDirect = kV == kLane * (int)sizeof(T);
+  [[maybe_unused]] static constexpr int kN = kV / (int)sizeof(T);
+  [[maybe_unused]] static constexpr int kSteps = kDirect ? 1 : kLane / kN;
+  using Raw_ = typename Raw<kDirect ? 16 : kV>::T;
+
+  // row: the piece's first value; left0: the row's values from there on
+  static __device__ __forceinline__ void load(const T* row, int64_t left0, int lane, T* stage, Eight<T>* v) {
+    if constexpr (kDirect) {
+      const T* p = row + lane * kLane;
+      const int64_t left = left0 - lane * kLane;
+      if (left >= kLane) {
+        if constexpr (sizeof(T) == 4)
+          asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                       : "=r"(v->word[0]), "=r"(v->word[1]), "=r"(v->word[2]), "=r"(v->word[3]), "=r"(v->word[4]),
+                         "=r"(v->word[5]), "=r"(v->word[6]), "=r"(v->word[7])
+                       : "l"(p));
+        else
+          asm volatile("ld.global.v4.b32 {%0, %1, %2, %3}, [%4];"
+                       : "=r"(v->word[0]), "=r"(v->word[1]), "=r"(v->word[2]), "=r"(v->word[3])
+                       : "l"(p));
+      } else {
 #pragma unroll
-    for (int k = 0; k < kLane; ++k) v->e[k] = k < left ? p[k] : from_f32<T>(0.f);
-  }
-}
-template <typename T, bool kAligned>
-__device__ __forceinline__ void store8(T* p, int64_t left, const Eight<T>& v) {
-  if (kAligned && left >= kLane) {
-    if constexpr (sizeof(T) == 4)
-      asm volatile("st.global.v8.b32 [%8], {%0, %1, %2, %3, %4, %5, %6, %7};" ::"r"(v.word[0]), "r"(v.word[1]),
-                   "r"(v.word[2]), "r"(v.word[3]), "r"(v.word[4]), "r"(v.word[5]), "r"(v.word[6]), "r"(v.word[7]),
-                   "l"(p)
-                   : "memory");
-    else
-      asm volatile("st.global.v4.b32 [%4], {%0, %1, %2, %3};" ::"r"(v.word[0]), "r"(v.word[1]), "r"(v.word[2]),
-                   "r"(v.word[3]), "l"(p)
-                   : "memory");
-  } else {
+        for (int k = 0; k < kLane; ++k) v->e[k] = k < left ? p[k] : from_f32<T>(0.f);
+      }
+    } else {
+      Raw_ r[kSteps];
 #pragma unroll
-    for (int k = 0; k < kLane; ++k)
-      if (k < left) p[k] = v.e[k];
+      for (int i = 0; i < kSteps; ++i) {
+        const int at = (i * 32 + lane) * kN;
+        r[i] = at < left0 ? *reinterpret_cast<const Raw_*>(row + at) : Raw_{};
+      }
+      __syncwarp();   // the last piece has been taken
+#pragma unroll
+      for (int i = 0; i < kSteps; ++i) *reinterpret_cast<Raw_*>(stage + (i * 32 + lane) * kN) = r[i];
+      __syncwarp();
+#pragma unroll
+      for (int k = 0; k < Eight<T>::kWords; ++k) v->word[k] = reinterpret_cast<const uint32_t*>(stage + lane * kLane)[k];
+    }
   }
-}
+  static __device__ __forceinline__ void store(T* row, int64_t left0, int lane, T* stage, const Eight<T>& v) {
+    if constexpr (kDirect) {
+      T* p = row + lane * kLane;
+      const int64_t left = left0 - lane * kLane;
+      if (left >= kLane) {
+        if constexpr (sizeof(T) == 4)
+          asm volatile("st.global.v8.b32 [%8], {%0, %1, %2, %3, %4, %5, %6, %7};" ::"r"(v.word[0]), "r"(v.word[1]),
+                       "r"(v.word[2]), "r"(v.word[3]), "r"(v.word[4]), "r"(v.word[5]), "r"(v.word[6]), "r"(v.word[7]),
+                       "l"(p)
+                       : "memory");
+        else
+          asm volatile("st.global.v4.b32 [%4], {%0, %1, %2, %3};" ::"r"(v.word[0]), "r"(v.word[1]), "r"(v.word[2]),
+                       "r"(v.word[3]), "l"(p)
+                       : "memory");
+      } else {
+#pragma unroll
+        for (int k = 0; k < kLane; ++k)
+          if (k < left) p[k] = v.e[k];
+      }
+    } else {
+      __syncwarp();
+#pragma unroll
+      for (int k = 0; k < Eight<T>::kWords; ++k) reinterpret_cast<uint32_t*>(stage + lane * kLane)[k] = v.word[k];
+      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < kSteps; ++i) {
+        const int at = (i * 32 + lane) * kN;
+        if (at < left0) *reinterpret_cast<Raw_*>(row + at) = *reinterpret_cast<const Raw_*>(stage + at);
+      }
+    }
+  }
+};
 
 // The largest magnitude of a block, four lanes' values.  Magnitudes order as
 // their bits do, and a NaN's bits are above an infinity's, so neither gets
@@ -109,13 +152,16 @@ __device__ __forceinline__ uint32_t encode8(const Eight<T>& v, uint32_t* scale) 
 // 16 or 32 bits are read and 4.25 written a value: bound by bandwidth, with
 // issue close behind for 16-bit types.  [16384, 4096] bf16: 29 us (5.9 TB/s);
 // [8192, 3328] fp32: 22 us (5.6 TB/s).
-template <typename T, bool kAligned, bool kRoute, int kPieces>
+template <typename T, int kV, bool kRoute, int kPieces>
 __global__ void __launch_bounds__(32 * kMxWarps) k_mx4_quantize(const T* __restrict__ x, int64_t ld, int64_t rows,
                                                                 int64_t width, int top,
                                                                 const int32_t* __restrict__ place,
                                                                 const int32_t* __restrict__ offsets, int E,
                                                                 uint8_t* __restrict__ codes,
                                                                 uint8_t* __restrict__ scales, Glob* glob) {
+  using P = Piece<T, kV>;
+  __shared__ uint4 s_stage[P::kDirect ? 1 : kMxWarps * kPiece * sizeof(T) / 16];
+  T* stage = reinterpret_cast<T*>(s_stage) + (P::kDirect ? 0 : (threadIdx.x >> 5) * kPiece);
   pdl_enter();
   constexpr int kChunk = kPieces * kPiece;
   const int lane = threadIdx.x & 31, quad = lane >> 2, j4 = lane & 3;
@@ -135,10 +181,10 @@ __global__ void __launch_bounds__(32 * kMxWarps) k_mx4_quantize(const T* __restr
 #pragma unroll
     for (int i = 0; i < kPieces; ++i) c[i] = s[i] = 0u;
     if (!kRoute || t < rows) {
-      const T* src = x + t * ld + h0 + lane * kLane;
+      const T* src = x + t * ld + h0;
       Eight<T> v[kPieces];
 #pragma unroll
-      for (int i = 0; i < kPieces; ++i) load8<T, kAligned>(src + i * kPiece, left - i * kPiece, &v[i]);
+      for (int i = 0; i < kPieces; ++i) P::load(src + i * kPiece, width - h0 - i * kPiece, lane, stage, &v[i]);
 #pragma unroll
       for (int i = 0; i < kPieces; ++i) {
         c[i] = encode8(v[i], &s[i]);
@@ -182,10 +228,13 @@ __global__ void __launch_bounds__(32 * kMxWarps) k_mx4_quantize(const T* __restr
 
 // The way back: eight codes a lane, kPieces runs of 256 values a warp.  Bound
 // by the bandwidth of the writes: [8192, 3328] to fp32 20 us (6.1 TB/s).
-template <typename T, bool kAligned, int kPieces>
+template <typename T, int kV, int kPieces>
 __global__ void __launch_bounds__(32 * kMxWarps) k_mx4_dequantize(const uint8_t* __restrict__ codes,
                                                                   const uint8_t* __restrict__ scales, int64_t rows,
                                                                   int64_t width, T* __restrict__ x) {
+  using P = Piece<T, kV>;
+  __shared__ uint4 s_stage[P::kDirect ? 1 : kMxWarps * kPiece * sizeof(T) / 16];
+  T* stage = reinterpret_cast<T*>(s_stage) + (P::kDirect ? 0 : (threadIdx.x >> 5) * kPiece);
   pdl_enter();
   constexpr int kChunk = kPieces * kPiece;
   const int lane = threadIdx.x & 31;
@@ -196,7 +245,7 @@ __global__ void __launch_bounds__(32 * kMxWarps) k_mx4_dequantize(const uint8_t*
     const int64_t t = divide(u, chunks), h0 = (u - t * chunks) * kChunk, left = width - h0 - lane * kLane;
     const uint8_t* cr = codes + t * code_bytes + h0 / 2 + lane * 4;
     const uint8_t* sr = scales + t * scale_bytes + h0 / 32 + (lane >> 2);
-    T* dst = x + t * width + h0 + lane * kLane;
+    T* dst = x + t * width + h0;
     uint32_t c[kPieces], s[kPieces];
 #pragma unroll
     for (int i = 0; i < kPieces; ++i)
@@ -205,20 +254,22 @@ __global__ void __launch_bounds__(32 * kMxWarps) k_mx4_dequantize(const uint8_t*
         s[i] = sr[i * (kPiece / 32)];
       }
 #pragma unroll
-    for (int i = 0; i < kPieces; ++i)
+    for (int i = 0; i < kPieces; ++i) {
+      if (i * kPiece >= width - h0) break;
+      Eight<T> o;
       if (i * kPiece < left) {
         const float unit = mx4_unit(s[i]);
         __half2 h[4];
         mx4_values(c[i], h);
-        Eight<T> o;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           const float2 f = __half22float2(h[k]);
           o.e[2 * k] = from_f32<T>(f.x * unit);
           o.e[2 * k + 1] = from_f32<T>(f.y * unit);
         }
-        store8<T, kAligned>(dst + i * kPiece, left - i * kPiece, o);
       }
+      P::store(dst + i * kPiece, width - h0 - i * kPiece, lane, stage, o);
+    }
   }
 }
 
@@ -246,12 +297,12 @@ bool mx_rows_ok(int64_t rows, int64_t width) {
   return rows >= 0 && rows <= INT32_MAX && width >= 1 && width <= (1 << 24);
 }
 
-template <typename T, bool kAligned, bool kRoute, int kPieces>
+template <typename T, int kV, bool kRoute, int kPieces>
 cudaError_t quantize_launch(const CallView& v, const void* x, int64_t ld, int64_t rows, int64_t width, int top,
                             const int32_t* place, const int32_t* offsets, int E, uint8_t* codes, uint8_t* scales,
                             cudaStream_t st) {
   return launch_named(v, kRoute ? "k_mx4_dispatch" : "k_mx4_quantize", st,
-                      k_mx4_quantize<T, kAligned, kRoute, kPieces>,
+                      k_mx4_quantize<T, kV, kRoute, kPieces>,
                       dim3(mx_grid(rows * scale_chunks(width, kPieces * kPiece), v.nsm)), dim3(32 * kMxWarps), 0, 1,
                       (const T*)x, ld, rows, width, top, place, offsets, E, codes, scales, v.glob);
 }
@@ -260,15 +311,21 @@ template <typename T, bool kRoute>
 cudaError_t quantize_t(const CallView& v, const void* x, int64_t ld, int64_t rows, int64_t width, int top,
                        const int32_t* place, const int32_t* offsets, int E, uint8_t* codes, uint8_t* scales,
                        cudaStream_t st) {
-  constexpr int kMost = sizeof(T) == 2 ? 8 : 4, kAlign = kLane * (int)sizeof(T);
-  if (!aligned(x, kAlign) || ld * (int64_t)sizeof(T) % kAlign != 0)
-    return quantize_launch<T, false, kRoute, 1>(v, x, ld, rows, width, top, place, offsets, E, codes, scales, st);
+  constexpr int kMost = sizeof(T) == 2 ? 8 : 4, kV = kLane * (int)sizeof(T);
+  const uintptr_t rows_at = (uintptr_t)x | (uintptr_t)(ld * (int64_t)sizeof(T));
+  if (rows_at % kV != 0) {
+    // vectors of two 16-bit values where a row is whole vectors, else single values
+    if (sizeof(T) == 2 && (rows_at | (uintptr_t)(width * (int64_t)sizeof(T))) % 4 == 0)
+      return quantize_launch<T, 4, kRoute, 2>(v, x, ld, rows, width, top, place, offsets, E, codes, scales, st);
+    return quantize_launch<T, (int)sizeof(T), kRoute, 2>(v, x, ld, rows, width, top, place, offsets, E, codes, scales,
+                                                         st);
+  }
   switch (pieces(rows, width, v.nsm, kMost)) {
-    case 1: return quantize_launch<T, true, kRoute, 1>(v, x, ld, rows, width, top, place, offsets, E, codes, scales, st);
-    case 2: return quantize_launch<T, true, kRoute, 2>(v, x, ld, rows, width, top, place, offsets, E, codes, scales, st);
-    case 4: return quantize_launch<T, true, kRoute, 4>(v, x, ld, rows, width, top, place, offsets, E, codes, scales, st);
+    case 1: return quantize_launch<T, kV, kRoute, 1>(v, x, ld, rows, width, top, place, offsets, E, codes, scales, st);
+    case 2: return quantize_launch<T, kV, kRoute, 2>(v, x, ld, rows, width, top, place, offsets, E, codes, scales, st);
+    case 4: return quantize_launch<T, kV, kRoute, 4>(v, x, ld, rows, width, top, place, offsets, E, codes, scales, st);
     default:
-      return quantize_launch<T, true, kRoute, kMost>(v, x, ld, rows, width, top, place, offsets, E, codes, scales, st);
+      return quantize_launch<T, kV, kRoute, kMost>(v, x, ld, rows, width, top, place, offsets, E, codes, scales, st);
   }
 }
 
@@ -297,11 +354,11 @@ int quantize_any(ebc_ctx* ctx, const void* x, int64_t ld, int type, int64_t rows
   return cuda_code(e);
 }
 
-template <typename T, bool kAligned, int kPieces>
+template <typename T, int kV, int kPieces>
 cudaError_t dequantize_launch(const CallView& v, const uint8_t* codes, const uint8_t* scales, int64_t rows,
                               int64_t width, void* x, cudaStream_t st) {
   const int64_t chunk = kPieces * kPiece;
-  return launch_named(v, "k_mx4_dequantize", st, k_mx4_dequantize<T, kAligned, kPieces>,
+  return launch_named(v, "k_mx4_dequantize", st, k_mx4_dequantize<T, kV, kPieces>,
                       dim3(mx_grid(rows * ((width + chunk - 1) / chunk), v.nsm)), dim3(32 * kMxWarps), 0, 1, codes,
                       scales, rows, width, (T*)x);
 }
@@ -309,13 +366,16 @@ cudaError_t dequantize_launch(const CallView& v, const uint8_t* codes, const uin
 template <typename T>
 cudaError_t dequantize_t(const CallView& v, const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t width,
                          void* x, cudaStream_t st) {
-  constexpr int kAlign = kLane * (int)sizeof(T);
-  if (!aligned(x, kAlign) || width * (int64_t)sizeof(T) % kAlign != 0)
-    return dequantize_launch<T, false, 1>(v, codes, scales, rows, width, x, st);
+  constexpr int kV = kLane * (int)sizeof(T);
+  const uintptr_t rows_at = (uintptr_t)x | (uintptr_t)(width * (int64_t)sizeof(T));
+  if (rows_at % kV != 0) {
+    if (sizeof(T) == 2 && rows_at % 4 == 0) return dequantize_launch<T, 4, 2>(v, codes, scales, rows, width, x, st);
+    return dequantize_launch<T, (int)sizeof(T), 2>(v, codes, scales, rows, width, x, st);
+  }
   switch (pieces(rows, width, v.nsm, 4)) {
-    case 1: return dequantize_launch<T, true, 1>(v, codes, scales, rows, width, x, st);
-    case 2: return dequantize_launch<T, true, 2>(v, codes, scales, rows, width, x, st);
-    default: return dequantize_launch<T, true, 4>(v, codes, scales, rows, width, x, st);
+    case 1: return dequantize_launch<T, kV, 1>(v, codes, scales, rows, width, x, st);
+    case 2: return dequantize_launch<T, kV, 2>(v, codes, scales, rows, width, x, st);
+    default: return dequantize_launch<T, kV, 4>(v, codes, scales, rows, width, x, st);
   }
 }
 
