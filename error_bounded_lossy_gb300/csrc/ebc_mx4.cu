@@ -40,8 +40,6 @@ struct Eight {
 template <typename T, int kV>
 struct Piece {
   static constexpr bool kDirect = kV == kLane * (int)sizeof(T);
-  [[maybe_unused]] static constexpr int kN = kV / (int)sizeof(T);
-  [[maybe_unused]] static constexpr int kSteps = kDirect ? 1 : kLane / kN;
   using Raw_ = typename Raw<kDirect ? 16 : kV>::T;
 
   // row: the piece's first value; left0: the row's values from there on
@@ -64,6 +62,7 @@ struct Piece {
         for (int k = 0; k < kLane; ++k) v->e[k] = k < left ? p[k] : from_f32<T>(0.f);
       }
     } else {
+      constexpr int kN = kV / (int)sizeof(T), kSteps = kLane / kN;
       Raw_ r[kSteps];
 #pragma unroll
       for (int i = 0; i < kSteps; ++i) {
@@ -98,6 +97,7 @@ struct Piece {
           if (k < left) p[k] = v.e[k];
       }
     } else {
+      constexpr int kN = kV / (int)sizeof(T), kSteps = kLane / kN;
       __syncwarp();
 #pragma unroll
       for (int k = 0; k < Eight<T>::kWords; ++k) reinterpret_cast<uint32_t*>(stage + lane * kLane)[k] = v.word[k];

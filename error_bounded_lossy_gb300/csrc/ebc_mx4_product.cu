@@ -280,7 +280,7 @@ struct Args {
   int out_type, blocks, experts;   // blocks: scale blocks a row
   int first_wait;                  // polls of the multiplying warp's first wait for a stage (normally the full limit)
   int split_log2;                  // CTAs (a cluster) that share a tile's K; more than one only with a tile a cluster
-  bool wide;                       // 16-byte stores of rows
+  int unit;                        // 16-bit outputs of a store: 8, 2 or 1, as the rows are aligned
 };
 
 // A wait that gives up: after `limit` polls or kWaitCycles, or once another
@@ -343,12 +343,13 @@ __device__ __forceinline__ void pack_half(const Fragments& f, bool bf16, uint32_
 }
 
 // They are turned over on their way through the warp's own piece of shared
-// memory, so that a lane then stores eight outputs of a row (16 bytes; four
-// lanes a row).  y: where the lane's first row goes (the second is 8 further,
-// ld8 elements on); n_row rows from the first on are written, and n_out
-// outputs of each (8 = in one store).
-__device__ __forceinline__ void store_half(const uint32_t (&v)[8], uint32_t stage, uint16_t* y, int64_t ld8, int n_out,
-                                           int n_row, int lane) {
+// memory, and stored kUnit outputs a lane, lanes next to each other in a row:
+// 8 (16 bytes, four lanes a row) where all rows are aligned for it, 2 where
+// rows have even lengths, else 1 (the whole warp a row).  y: the first row's
+// first output; rows >= n_row and outputs >= n_out are not written.
+template <int kUnit>
+__device__ __forceinline__ void store_half(const uint32_t (&v)[8], uint32_t stage, uint16_t* y, int64_t ld,
+                                           int n_out, int n_row, int lane) {
   __syncwarp();   // the piece has been read
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
@@ -356,23 +357,31 @@ __device__ __forceinline__ void store_half(const uint32_t (&v)[8], uint32_t stag
     store_transposed(stage + (h * 8 + (lane & 7)) * kStorePitch + (lane >> 3) * 16, q);
   }
   __syncwarp();
+  constexpr int kLanes = 32 / kUnit, kRows = 32 / kLanes;   // lanes of a row, rows at a time
+  const int row = lane / kLanes, out = lane % kLanes * kUnit;
+  const uint32_t from = stage + row * kStorePitch + out * 2;
+  y += row * ld + out;
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    Vec<uint16_t, 16> o;
-    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(o.raw.x), "=r"(o.raw.y), "=r"(o.raw.z), "=r"(o.raw.w)
-                 : "r"(stage + (h * 8 + (lane >> 2)) * kStorePitch + (lane & 3) * 16)
-                 : "memory");
-    if (8 * h >= n_row) continue;
-    uint16_t* dst = y + h * ld8;
-    if (n_out == 8) {
-      *reinterpret_cast<uint4*>(dst) = o.raw;
-    } else {
-#pragma unroll
-      for (int k = 0; k < 8; ++k)
-        if (k < (n_out & 7)) dst[k] = o.e[k];
-      if (n_out & 8) dst[7] = o.e[7];
+  for (int r = 0; r < kStoreRows; r += kRows) {
+    if (row + r < n_row && out < n_out) {   // (whole units: rows of 8 or 2 outputs are whole units long)
+      if constexpr (kUnit == 8) {
+        uint4 o;
+        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(o.x), "=r"(o.y), "=r"(o.z), "=r"(o.w)
+                     : "r"(from + r * kStorePitch)
+                     : "memory");
+        *reinterpret_cast<uint4*>(y) = o;
+      } else if constexpr (kUnit == 2) {
+        uint32_t o;
+        asm volatile("ld.shared.b32 %0, [%1];" : "=r"(o) : "r"(from + r * kStorePitch) : "memory");
+        *reinterpret_cast<uint32_t*>(y) = o;
+      } else {
+        uint16_t o;
+        asm volatile("ld.shared.b16 %0, [%1];" : "=h"(o) : "r"(from + r * kStorePitch) : "memory");
+        *y = o;
+      }
     }
+    y += kRows * ld;
   }
 }
 
@@ -380,11 +389,11 @@ __device__ __forceinline__ void store_half(const uint32_t (&v)[8], uint32_t stag
 // run of 16 rows.  All of it is read and rounded first and the accumulator
 // given back, then it is stored while the next tile is multiplied.
 template <int kTN, int kCtas>
-__device__ __forceinline__ void store_tile(uint32_t d, uint32_t stage, bool bf16, uint16_t* y, int64_t ld, int64_t n_out, int odd,
-                                           int count, bool wide, int lane, uint32_t given_back) {
+__device__ __forceinline__ void store_tile(uint32_t d, uint32_t stage, bool bf16, uint16_t* y, int64_t ld, int n_out,
+                                           int odd, int count, int unit, int lane, uint32_t given_back) {
   constexpr int kRuns = kTN < 32 ? 1 : kTN / 32;
-  uint32_t v[kRuns][8];
   constexpr int kBatch = kRuns < 2 ? kRuns : 2;   // runs whose loads are in flight
+  uint32_t v[kRuns][8];
 #pragma unroll
   for (int i0 = 0; i0 < kRuns; i0 += kBatch) {
     Fragments f[kBatch];
@@ -399,20 +408,25 @@ __device__ __forceinline__ void store_tile(uint32_t d, uint32_t stage, bool bf16
   tc_fence_before();
   __syncwarp();
   if (lane == 0) mbar_arrive<kCtas>(given_back);
-  // the lane's eight outputs, and its first row
-  const int o = (lane & 3) * 8, r = odd * kStoreRows + (lane >> 2);
-  const int64_t have = n_out - o;
-  const int mine = have >= 8 ? (wide ? 8 : 15) : have > 0 ? (int)have : 0;
-  y += (int64_t)r * ld + o;
+  int left = count - odd * kStoreRows;
+  y += odd * kStoreRows * ld;
 #pragma unroll
   for (int i = 0; i < kRuns; ++i) {
-    if ((i * 2 + odd) * kStoreRows < count) store_half(v[i], stage, y, 8 * ld, mine, count - r - i * 2 * kStoreRows, lane);
+    if (left > 0) {
+      if (unit == 8)
+        store_half<8>(v[i], stage, y, ld, n_out, left, lane);
+      else if (unit == 2)
+        store_half<2>(v[i], stage, y, ld, n_out, left, lane);
+      else
+        store_half<1>(v[i], stage, y, ld, n_out, left, lane);
+    }
     y += 2 * kStoreRows * ld;
+    left -= 2 * kStoreRows;
   }
 }
 
 // The same in fp32: a warp stores 32 consecutive outputs of a row at a time.
-__device__ __forceinline__ void store_full(uint32_t taddr, float* y, int64_t ld, int64_t n_out, int n_row, int lane) {
+__device__ __forceinline__ void store_full(uint32_t taddr, float* y, int64_t ld, int n_out, int n_row, int lane) {
   uint32_t v[16];
   tc_load16(taddr, v);
   tc_load_wait();
@@ -722,7 +736,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx4_product(const __grid_consta
       if (!__all_sync(0xffffffffu, wait(&acc_full[buf], phase, &s_abort, a.glob))) break;
       tc_fence_after();
       const int64_t out = (int64_t)walk.out * G::kOuts + rank * kM + quarter * 32;
-      const int64_t n_out = a.outs - out;   // outputs from here on, maybe none
+      const int n_out = a.outs - out < 32 ? (int)(a.outs - out) : 32;   // of the warp's outputs, maybe none
       const uint32_t d = tmem + buf * G::kAccCols + ((uint32_t)(quarter * 32) << 16);
       const int64_t at = (int64_t)row0 * a.outs + out;
       if (split > 1) {
@@ -739,7 +753,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx4_product(const __grid_consta
         __syncwarp();
         if (lane == 0) mbar_arrive<kCtas>(in_first<kCtas>(&acc_empty[buf]));
       } else if (a.out_type != EBC_F32) {
-        store_tile<kTN, kCtas>(d, stage, a.out_type == EBC_BF16, (uint16_t*)a.ys + at, a.outs, n_out, odd, count, a.wide,
+        store_tile<kTN, kCtas>(d, stage, a.out_type == EBC_BF16, (uint16_t*)a.ys + at, a.outs, n_out, odd, count, a.unit,
                                lane, in_first<kCtas>(&acc_empty[buf]));
       } else {
         for (int c0 = odd * kStoreRows; c0 < count; c0 += 2 * kStoreRows)
@@ -924,7 +938,7 @@ int ebc_mx4_product(ebc_ctx* ctx, const uint8_t* d_x_codes, const uint8_t* d_x_s
   a.blocks = (int)((width + EBC_MX4_BLOCK - 1) / EBC_MX4_BLOCK);
   a.experts = n_experts;
   a.first_wait = v.first_wait;
-  a.wide = aligned(d_ys, 16) && outs * b % 16 == 0;
+  a.unit = aligned(d_ys, 16) && outs % 8 == 0 ? 8 : aligned(d_ys, 4) && outs % 2 == 0 ? 2 : 1;
   switch (tile_rows(rows, outs, n_experts, v.nsm)) {
     case 16: return cuda_code(product_t<16, 1>(v, d_x_codes, d_w_codes, width, a, st));
     case 32: return cuda_code(product_t<32, 1>(v, d_x_codes, d_w_codes, width, a, st));
