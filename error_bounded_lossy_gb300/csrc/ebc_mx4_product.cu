@@ -26,8 +26,7 @@ constexpr int kScaleTile = 512;    // bytes of the scales of 128 rows x 4 blocks
 constexpr int kThreads = 384;
 constexpr int kScaleWarp0 = 2, kScaleWarps = 2;
 constexpr int kStoreWarp0 = 4, kStoreWarps = 8;
-constexpr int kStoreRows = 16;     // rows that a storing warp turns over at a time
-constexpr int kStorePitch = 80;    // bytes of such a row of 32 outputs: 64, and 16 to spread the banks
+constexpr int kStoreRows = 16;     // rows that a storing warp reads at a time
 
 // kCtas = 2: a pair of CTAs on one tile of 256 outputs.  Each brings in its own
 // 128 outputs and half of the rows; the pair's matrix instructions read both
@@ -42,13 +41,14 @@ struct Geom {
   static constexpr int kABytes = kM * kRowBytes;
   static constexpr int kBBytes = kBRows * kRowBytes;
   static constexpr int kScaleBytes = 2 * (1 + kScaleB) * kScaleTile;      // per stage: 8 blocks a row
-  static constexpr int kStages = kTN == 256 ? 5 : kTN == 128 ? 6 : kTN == 64 ? 7 : 8;
+  // (more stages were slower: 256 rows a tile with 5 / 6, 299 / 309 us of 8192 x
+  // 8192; 16 rows with 5 / 6 / 8 / 10, 12.9 / 12.6 / 13.1 / 13.5 us of a decode step)
+  static constexpr int kStages = kTN == 256 ? 5 : kTN == 64 ? 7 : 6;
   static constexpr int kAcc = kTN == 256 ? 1 : 2;                         // accumulators
   static constexpr int kAccCols = kTN < 32 ? 32 : kTN;
   static constexpr int kScaleCols = 2 * (1 + kScaleB) * 4;                // tensor memory columns per stage
   static constexpr int kCols = 512;
-  static constexpr int kStoreBytes = kStoreWarps * kStoreRows * kStorePitch;
-  static constexpr size_t kSmem = 1024 + (size_t)kStages * (kABytes + kBBytes + kScaleBytes) + kStoreBytes;
+  static constexpr size_t kSmem = 1024 + (size_t)kStages * (kABytes + kBBytes + kScaleBytes);
   // A scale warp's next stages must not be two rounds of the ring past what it
   // knows to be given back: a barrier's phase is told by its parity alone.
   static_assert(2 * kScaleWarps <= kStages + 1, "scale warps");
@@ -193,21 +193,6 @@ __device__ __forceinline__ void tc_load16(uint32_t taddr, uint32_t (&v)[16]) {
       : "r"(taddr)
       : "memory");
 }
-// 16 lanes x 16 columns as two 16x8 fragments: thread t has lanes t / 4 (the
-// first two words of a fragment) and t / 4 + 8, columns 2 (t % 4) and the next
-__device__ __forceinline__ void tc_load_fragments(uint32_t taddr, uint32_t (&v)[8]) {
-  asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-               : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
-               : "r"(taddr)
-               : "memory");
-}
-// four 8x8 blocks of 16-bit values, transposed: thread t gives the address of
-// column t % 8 of block t / 8
-__device__ __forceinline__ void store_transposed(uint32_t addr, const uint32_t (&v)[4]) {
-  asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v[0]),
-               "r"(v[1]), "r"(v[2]), "r"(v[3])
-               : "memory");
-}
 // one thread of the warp, known to the compiler as such: what it issues has
 // its operands in uniform registers
 __device__ __forceinline__ bool elect_one() {
@@ -280,7 +265,6 @@ struct Args {
   int out_type, blocks, experts;   // blocks: scale blocks a row
   int first_wait;                  // polls of the multiplying warp's first wait for a stage (normally the full limit)
   int split_log2;                  // CTAs (a cluster) that share a tile's K; more than one only with a tile a cluster
-  int unit;                        // 16-bit outputs of a store: 8, 2 or 1, as the rows are aligned
 };
 
 // A wait that gives up: after `limit` polls or kWaitCycles, or once another
@@ -323,117 +307,68 @@ __device__ __forceinline__ uint32_t pack2(uint32_t lo, uint32_t hi, bool bf16) {
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
-// 32 outputs x 16 rows of an accumulator, rounded to 16 bits: fragments of
-// outputs x rows.  (Loads are in flight until tc_load_wait.)
-struct Fragments {
-  uint32_t lo[8], hi[8];
-};
-__device__ __forceinline__ void load_half(uint32_t taddr, Fragments* f) {
-  tc_load_fragments(taddr, f->lo);
-  tc_load_fragments(taddr + (16u << 16), f->hi);
-}
-__device__ __forceinline__ void pack_half(const Fragments& f, bool bf16, uint32_t (&v)[8]) {
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    v[4 * h] = pack2(f.lo[4 * h], f.lo[4 * h + 1], bf16);
-    v[4 * h + 1] = pack2(f.lo[4 * h + 2], f.lo[4 * h + 3], bf16);
-    v[4 * h + 2] = pack2(f.hi[4 * h], f.hi[4 * h + 1], bf16);
-    v[4 * h + 3] = pack2(f.hi[4 * h + 2], f.hi[4 * h + 3], bf16);
-  }
-}
-
-// They are turned over on their way through the warp's own piece of shared
-// memory, and stored kUnit outputs a lane, lanes next to each other in a row:
-// 8 (16 bytes, four lanes a row) where all rows are aligned for it, 2 where
-// rows have even lengths, else 1 (the whole warp a row).  y: the first row's
-// first output; rows >= n_row and outputs >= n_out are not written.
-template <int kUnit>
-__device__ __forceinline__ void store_half(const uint32_t (&v)[8], uint32_t stage, uint16_t* y, int64_t ld,
-                                           int n_out, int n_row, int lane) {
-  __syncwarp();   // the piece has been read
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const uint32_t q[4] = {v[4 * h], v[4 * h + 1], v[4 * h + 2], v[4 * h + 3]};
-    store_transposed(stage + (h * 8 + (lane & 7)) * kStorePitch + (lane >> 3) * 16, q);
-  }
-  __syncwarp();
-  constexpr int kLanes = 32 / kUnit, kRows = 32 / kLanes;   // lanes of a row, rows at a time
-  const int row = lane / kLanes, out = lane % kLanes * kUnit;
-  const uint32_t from = stage + row * kStorePitch + out * 2;
-  y += row * ld + out;
-#pragma unroll
-  for (int r = 0; r < kStoreRows; r += kRows) {
-    if (row + r < n_row && out < n_out) {   // (whole units: rows of 8 or 2 outputs are whole units long)
-      if constexpr (kUnit == 8) {
-        uint4 o;
-        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                     : "=r"(o.x), "=r"(o.y), "=r"(o.z), "=r"(o.w)
-                     : "r"(from + r * kStorePitch)
-                     : "memory");
-        *reinterpret_cast<uint4*>(y) = o;
-      } else if constexpr (kUnit == 2) {
-        uint32_t o;
-        asm volatile("ld.shared.b32 %0, [%1];" : "=r"(o) : "r"(from + r * kStorePitch) : "memory");
-        *reinterpret_cast<uint32_t*>(y) = o;
-      } else {
-        uint16_t o;
-        asm volatile("ld.shared.b16 %0, [%1];" : "=h"(o) : "r"(from + r * kStorePitch) : "memory");
-        *y = o;
-      }
-    }
-    y += kRows * ld;
-  }
-}
-
-// A storing warp's share of a tile, 16-bit results: 32 outputs of every other
-// run of 16 rows.  All of it is read and rounded first and the accumulator
-// given back, then it is stored while the next tile is multiplied.
+// A storing warp's share of a tile, 16-bit results: 32 outputs, one a lane, of
+// every other run of 16 rows.  All of it is read and rounded first and the
+// accumulator given back, then it is stored while the next tile is multiplied.
+// A store is 64 bytes of one row: turning the values over in shared memory to
+// 16 bytes a lane took 2 to 3% longer in all (shared memory is what the
+// multiplying waits for) and 30% with rows of odd length.
 template <int kTN, int kCtas>
-__device__ __forceinline__ void store_tile(uint32_t d, uint32_t stage, bool bf16, uint16_t* y, int64_t ld, int n_out,
-                                           int odd, int count, int unit, int lane, uint32_t given_back) {
+__device__ __forceinline__ void store_tile(uint32_t d, bool bf16, uint16_t* y, int64_t ld, bool mine, int odd,
+                                           int count, int lane, uint32_t given_back) {
   constexpr int kRuns = kTN < 32 ? 1 : kTN / 32;
   constexpr int kBatch = kRuns < 2 ? kRuns : 2;   // runs whose loads are in flight
   uint32_t v[kRuns][8];
 #pragma unroll
   for (int i0 = 0; i0 < kRuns; i0 += kBatch) {
-    Fragments f[kBatch];
+    uint32_t f[kBatch][16];
 #pragma unroll
     for (int i = 0; i < kBatch; ++i)
-      if (((i0 + i) * 2 + odd) * kStoreRows < count) load_half(d + ((i0 + i) * 2 + odd) * kStoreRows, &f[i]);
+      if (((i0 + i) * 2 + odd) * kStoreRows < count) tc_load16(d + ((i0 + i) * 2 + odd) * kStoreRows, f[i]);
     tc_load_wait();
 #pragma unroll
     for (int i = 0; i < kBatch; ++i)
-      if (((i0 + i) * 2 + odd) * kStoreRows < count) pack_half(f[i], bf16, v[i0 + i]);
+      if (((i0 + i) * 2 + odd) * kStoreRows < count)
+#pragma unroll
+        for (int c = 0; c < 8; ++c) v[i0 + i][c] = pack2(f[i][2 * c], f[i][2 * c + 1], bf16);
   }
   tc_fence_before();
   __syncwarp();
   if (lane == 0) mbar_arrive<kCtas>(given_back);
   int left = count - odd * kStoreRows;
-  y += odd * kStoreRows * ld;
+  y += odd * kStoreRows * ld + lane;
 #pragma unroll
   for (int i = 0; i < kRuns; ++i) {
-    if (left > 0) {
-      if (unit == 8)
-        store_half<8>(v[i], stage, y, ld, n_out, left, lane);
-      else if (unit == 2)
-        store_half<2>(v[i], stage, y, ld, n_out, left, lane);
-      else
-        store_half<1>(v[i], stage, y, ld, n_out, left, lane);
+    uint16_t* p = y;
+    if (left >= kStoreRows) {
+      if (mine)
+#pragma unroll
+        for (int c = 0; c < kStoreRows; ++c) {
+          *p = (uint16_t)(c & 1 ? v[i][c / 2] >> 16 : v[i][c / 2]);
+          p += ld;
+        }
+    } else if (left > 0) {
+#pragma unroll
+      for (int c = 0; c < kStoreRows; ++c) {
+        if (mine && c < left) *p = (uint16_t)(c & 1 ? v[i][c / 2] >> 16 : v[i][c / 2]);
+        p += ld;
+      }
     }
     y += 2 * kStoreRows * ld;
     left -= 2 * kStoreRows;
   }
 }
 
-// The same in fp32: a warp stores 32 consecutive outputs of a row at a time.
-__device__ __forceinline__ void store_full(uint32_t taddr, float* y, int64_t ld, int n_out, int n_row, int lane) {
+// The same in fp32, 16 rows at a time.
+__device__ __forceinline__ void store_full(uint32_t taddr, float* y, int64_t ld, bool mine, int n_row, int lane) {
   uint32_t v[16];
   tc_load16(taddr, v);
   tc_load_wait();
-  if (lane < n_out) {
+  y += lane;
 #pragma unroll
-    for (int c = 0; c < 16; ++c)
-      if (c < n_row) y[c * ld + lane] = __uint_as_float(v[c]);
+  for (int c = 0; c < kStoreRows; ++c) {
+    if (mine && c < n_row) *y = __uint_as_float(v[c]);
+    y += ld;
   }
 }
 
@@ -475,7 +410,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx4_product(const __grid_consta
   uint8_t* sA = base;
   uint8_t* sB = sA + G::kStages * G::kABytes;
   uint8_t* sS = sB + G::kStages * G::kBBytes;
-  uint8_t* sStore = sS + G::kStages * G::kScaleBytes;
 
   if (w == 0 && lane == 0) {
     for (int i = 0; i < G::kStages; ++i) {
@@ -729,14 +663,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx4_product(const __grid_consta
   } else {
     // a warp has the outputs of its quarter of the lanes, and every other run of 16 rows
     const int quarter = w & 3, odd = (w - kStoreWarp0) >> 2;
-    const uint32_t stage = smem_u32(sStore) + (w - kStoreWarp0) * kStoreRows * kStorePitch;
     int buf = 0;
     uint32_t phase = 0;
     for (; walk.at(s_begin, s_tiles, a.experts, kTN, &row0, &count); walk.next(out_tiles)) {
       if (!__all_sync(0xffffffffu, wait(&acc_full[buf], phase, &s_abort, a.glob))) break;
       tc_fence_after();
       const int64_t out = (int64_t)walk.out * G::kOuts + rank * kM + quarter * 32;
-      const int n_out = a.outs - out < 32 ? (int)(a.outs - out) : 32;   // of the warp's outputs, maybe none
+      const bool mine = out + lane < a.outs;
       const uint32_t d = tmem + buf * G::kAccCols + ((uint32_t)(quarter * 32) << 16);
       const int64_t at = (int64_t)row0 * a.outs + out;
       if (split > 1) {
@@ -753,11 +686,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx4_product(const __grid_consta
         __syncwarp();
         if (lane == 0) mbar_arrive<kCtas>(in_first<kCtas>(&acc_empty[buf]));
       } else if (a.out_type != EBC_F32) {
-        store_tile<kTN, kCtas>(d, stage, a.out_type == EBC_BF16, (uint16_t*)a.ys + at, a.outs, n_out, odd, count, a.unit,
-                               lane, in_first<kCtas>(&acc_empty[buf]));
+        store_tile<kTN, kCtas>(d, a.out_type == EBC_BF16, (uint16_t*)a.ys + at, a.outs, mine, odd, count, lane,
+                               in_first<kCtas>(&acc_empty[buf]));
       } else {
         for (int c0 = odd * kStoreRows; c0 < count; c0 += 2 * kStoreRows)
-          store_full(d + c0, (float*)a.ys + at + c0 * a.outs, a.outs, n_out, count - c0, lane);
+          store_full(d + c0, (float*)a.ys + at + c0 * a.outs, a.outs, mine, count - c0, lane);
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive<kCtas>(in_first<kCtas>(&acc_empty[buf]));
@@ -938,7 +871,6 @@ int ebc_mx4_product(ebc_ctx* ctx, const uint8_t* d_x_codes, const uint8_t* d_x_s
   a.blocks = (int)((width + EBC_MX4_BLOCK - 1) / EBC_MX4_BLOCK);
   a.experts = n_experts;
   a.first_wait = v.first_wait;
-  a.unit = aligned(d_ys, 16) && outs % 8 == 0 ? 8 : aligned(d_ys, 4) && outs % 2 == 0 ? 2 : 1;
   switch (tile_rows(rows, outs, n_experts, v.nsm)) {
     case 16: return cuda_code(product_t<16, 1>(v, d_x_codes, d_w_codes, width, a, st));
     case 32: return cuda_code(product_t<32, 1>(v, d_x_codes, d_w_codes, width, a, st));
