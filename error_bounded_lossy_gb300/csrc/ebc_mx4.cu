@@ -273,6 +273,140 @@ __global__ void __launch_bounds__(32 * kMxWarps) k_mx4_dequantize(const uint8_t*
   }
 }
 
+// Rows of at most 128 values, which would leave most lanes of a piece idle:
+// 4, 8 or 16 lanes a row (1 << lanes_log2), kNarrow runs of rows a warp.  In
+// pieces, 16384 bf16 rows of 64 or of 128 took 18.9 us to quantize and 5.4 to
+// read back; so they take less than 4.9 and 3.8, the call's time on the host.
+constexpr int kNarrowWidth = 128, kNarrow = 4;
+
+// A lane's eight values of a short row, in 16-byte loads where `wide`.
+template <typename T>
+__device__ __forceinline__ void load_narrow(const T* p, int64_t left, bool wide, Eight<T>* v) {
+  if (wide && left >= kLane) {
+#pragma unroll
+    for (int i = 0; i < Eight<T>::kWords / 4; ++i) {
+      const uint4 r = reinterpret_cast<const uint4*>(p)[i];
+      v->word[4 * i] = r.x;
+      v->word[4 * i + 1] = r.y;
+      v->word[4 * i + 2] = r.z;
+      v->word[4 * i + 3] = r.w;
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < kLane; ++k) v->e[k] = k < left ? p[k] : from_f32<T>(0.f);
+  }
+}
+
+template <typename T, bool kRoute>
+__global__ void __launch_bounds__(32 * kMxWarps) k_mx4_quantize_narrow(const T* __restrict__ x, int64_t ld,
+                                                                       int64_t rows, int width, int lanes_log2,
+                                                                       bool wide, int top,
+                                                                       const int32_t* __restrict__ place,
+                                                                       const int32_t* __restrict__ offsets, int E,
+                                                                       uint8_t* __restrict__ codes,
+                                                                       uint8_t* __restrict__ scales, Glob* glob) {
+  pdl_enter();
+  const int lane = threadIdx.x & 31, lanes = 1 << lanes_log2, at = lane & (lanes - 1), each = 32 >> lanes_log2;
+  const int code_bytes = EBC_MX4_CODE_BYTES(width);
+  const int64_t n = rows * top;
+  int64_t live = n;
+  if (kRoute) {
+    live = offsets[E];
+    live = live < 0 ? 0 : live < n ? live : n;
+  }
+  const int64_t total = rows + (n - live), units = (total + each * kNarrow - 1) / (each * kNarrow);
+  for (int64_t u = (int64_t)blockIdx.x * kMxWarps + (threadIdx.x >> 5); u < units;
+       u += (int64_t)gridDim.x * kMxWarps) {
+    Eight<T> v[kNarrow];
+#pragma unroll
+    for (int i = 0; i < kNarrow; ++i) {
+      const int64_t t = (u * kNarrow + i) * each + (lane >> lanes_log2);
+      load_narrow(x + t * ld + at * kLane, t < rows ? width - at * kLane : 0, wide, &v[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < kNarrow; ++i) {
+      const int64_t t = (u * kNarrow + i) * each + (lane >> lanes_log2);
+      uint32_t s;
+      const uint32_t c = encode8(v[i], &s);
+      if (t >= rows || (at & ~3) * kLane >= width) s = 0u;
+      uint32_t word = 0;   // the row's scale bytes
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const uint32_t b = __shfl_sync(0xffffffffu, s, (lane - at + 4 * k) & 31);
+        if (4 * k < lanes) word |= b << (8 * k);
+      }
+      auto store = [&](int64_t r) {
+        if (at * 4 < code_bytes) *reinterpret_cast<uint32_t*>(codes + r * code_bytes + at * 4) = c;
+        if (at == 0) *reinterpret_cast<uint4*>(scales + r * 16) = make_uint4(word, 0u, 0u, 0u);
+      };
+      if (t >= total) continue;
+      if (!kRoute) {
+        store(t);
+      } else if (t < rows) {
+        for (int j = 0; j < top; ++j) {
+          const int32_t p = place[t * top + j];
+          if (p >= n && at == 0) record_error(glob, EBC_ERR_INVALID_ARG);
+          if (p >= 0 && p < n) store(p);
+        }
+      } else {
+        store(live + (t - rows));
+      }
+    }
+  }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(32 * kMxWarps) k_mx4_dequantize_narrow(const uint8_t* __restrict__ codes,
+                                                                         const uint8_t* __restrict__ scales,
+                                                                         int64_t rows, int width, int lanes_log2,
+                                                                         bool wide, T* __restrict__ x) {
+  pdl_enter();
+  const int lane = threadIdx.x & 31, lanes = 1 << lanes_log2, at = lane & (lanes - 1), each = 32 >> lanes_log2;
+  const int code_bytes = EBC_MX4_CODE_BYTES(width), left = width - at * kLane;
+  const int64_t units = (rows + each * kNarrow - 1) / (each * kNarrow);
+  for (int64_t u = (int64_t)blockIdx.x * kMxWarps + (threadIdx.x >> 5); u < units;
+       u += (int64_t)gridDim.x * kMxWarps) {
+    uint32_t c[kNarrow], s[kNarrow];
+#pragma unroll
+    for (int i = 0; i < kNarrow; ++i) {
+      const int64_t t = (u * kNarrow + i) * each + (lane >> lanes_log2);
+      if (t < rows && left > 0) {
+        c[i] = *reinterpret_cast<const uint32_t*>(codes + t * code_bytes + at * 4);
+        s[i] = scales[t * 16 + (at >> 2)];
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kNarrow; ++i) {
+      const int64_t t = (u * kNarrow + i) * each + (lane >> lanes_log2);
+      if (t >= rows || left <= 0) continue;
+      const float unit = mx4_unit(s[i]);
+      __half2 h[4];
+      mx4_values(c[i], h);
+      Eight<T> o;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float2 f = __half22float2(h[k]);
+        o.e[2 * k] = from_f32<T>(f.x * unit);
+        o.e[2 * k + 1] = from_f32<T>(f.y * unit);
+      }
+      T* dst = x + t * width + at * kLane;
+      if (wide && left >= kLane) {
+#pragma unroll
+        for (int q = 0; q < Eight<T>::kWords / 4; ++q)
+          reinterpret_cast<uint4*>(dst)[q] =
+              make_uint4(o.word[4 * q], o.word[4 * q + 1], o.word[4 * q + 2], o.word[4 * q + 3]);
+      } else {
+#pragma unroll
+        for (int k = 0; k < kLane; ++k)
+          if (k < left) dst[k] = o.e[k];
+      }
+    }
+  }
+}
+
+// Lanes of a short row: its blocks', four each.
+int narrow_lanes_log2(int64_t width) { return width <= 32 ? 2 : width <= 64 ? 3 : 4; }
+
 // Pieces of a warp: as many (up to `most`) as leave 24 warps for each SM.  A
 // warp's own cost (about 150 instructions) is spread over them, and their
 // loads overlap: [16384, 4096] bf16 takes 52 us with one, 40 with two, 32 with
@@ -313,6 +447,13 @@ cudaError_t quantize_t(const CallView& v, const void* x, int64_t ld, int64_t row
                        cudaStream_t st) {
   constexpr int kMost = sizeof(T) == 2 ? 8 : 4, kV = kLane * (int)sizeof(T);
   const uintptr_t rows_at = (uintptr_t)x | (uintptr_t)(ld * (int64_t)sizeof(T));
+  if (width <= kNarrowWidth) {
+    const int lanes = narrow_lanes_log2(width);
+    const int64_t units = (rows + (32 >> lanes) * kNarrow - 1) / ((32 >> lanes) * kNarrow);
+    return launch_named(v, kRoute ? "k_mx4_dispatch" : "k_mx4_quantize", st, k_mx4_quantize_narrow<T, kRoute>,
+                        dim3(mx_grid(units, v.nsm)), dim3(32 * kMxWarps), 0, 1, (const T*)x, ld, rows, (int)width,
+                        lanes, rows_at % 16 == 0, top, place, offsets, E, codes, scales, v.glob);
+  }
   if (rows_at % kV != 0) {
     // vectors of two 16-bit values where a row is whole vectors, else single values
     if (sizeof(T) == 2 && (rows_at | (uintptr_t)(width * (int64_t)sizeof(T))) % 4 == 0)
@@ -368,6 +509,12 @@ cudaError_t dequantize_t(const CallView& v, const uint8_t* codes, const uint8_t*
                          void* x, cudaStream_t st) {
   constexpr int kV = kLane * (int)sizeof(T);
   const uintptr_t rows_at = (uintptr_t)x | (uintptr_t)(width * (int64_t)sizeof(T));
+  if (width <= kNarrowWidth) {
+    const int lanes = narrow_lanes_log2(width);
+    const int64_t units = (rows + (32 >> lanes) * kNarrow - 1) / ((32 >> lanes) * kNarrow);
+    return launch_named(v, "k_mx4_dequantize", st, k_mx4_dequantize_narrow<T>, dim3(mx_grid(units, v.nsm)),
+                        dim3(32 * kMxWarps), 0, 1, codes, scales, rows, (int)width, lanes, rows_at % 16 == 0, (T*)x);
+  }
   if (rows_at % kV != 0) {
     if (sizeof(T) == 2 && rows_at % 4 == 0) return dequantize_launch<T, 4, 2>(v, codes, scales, rows, width, x, st);
     return dequantize_launch<T, (int)sizeof(T), 2>(v, codes, scales, rows, width, x, st);

@@ -86,7 +86,7 @@ def special(width, seed, dtype):
 
 
 @pytest.mark.parametrize("dtype", TYPES)
-@pytest.mark.parametrize("width", [1, 31, 32, 40, 264, 512, 1000, 1056])
+@pytest.mark.parametrize("width", [1, 31, 32, 40, 64, 100, 128, 129, 264, 301, 512, 1000, 1056])
 def test_codes_scales_and_values(ex, width, dtype):
     x = special(width, width, dtype)
     code, scale, values = encode(x.double().cpu().numpy())
@@ -121,7 +121,7 @@ def test_leading_shapes_strides_and_nothing(ex):
 
 
 @pytest.mark.parametrize("dtype", TYPES)
-@pytest.mark.parametrize("tokens,top,experts,width,drop", [(1, 8, 64, 512, 0.0), (37, 3, 5, 1000, 0.3), (6, 2, 3, 40, 1.0)])
+@pytest.mark.parametrize("tokens,top,experts,width,drop", [(1, 8, 64, 512, 0.0), (37, 3, 5, 1000, 0.3), (6, 2, 3, 40, 1.0), (500, 3, 7, 96, 0.2), (77, 2, 7, 31, 0.5), (300, 2, 4, 333, 0.1)])
 def test_dispatch_in_4_bits(ex, tokens, top, experts, width, drop, dtype):
     rng = np.random.default_rng(1)
     ids = rng.integers(0, experts, (tokens, top))
