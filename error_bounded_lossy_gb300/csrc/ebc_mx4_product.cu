@@ -383,7 +383,8 @@ __device__ __forceinline__ void store_full(uint32_t taddr, float* y, int64_t ld,
 //   warp 1      copies a stage's scales to tensor memory and issues its matrix
 //               instructions; each stage has its own scale columns, so they
 //               are written again only after the stage was given back
-//   warps 4-11  read the accumulator, round once, and store
+//   warps 4-11  read the accumulator, round once, to the type that the caller
+//               asked for, and store
 // The N of the instructions is the tile's row count rounded up to 16, so a
 // ragged segment's last tile costs what it holds.
 // With few tiles a cluster of CTAs takes one: each the sum over its share
@@ -393,6 +394,12 @@ __device__ __forceinline__ void store_full(uint32_t taddr, float* y, int64_t ld,
 // are announced at its barriers, and its instructions' ends at both CTAs'.
 // Every wait is bounded (see wait()); a CTA that gives up waits for the copies
 // and instructions it has in flight, frees its tensor memory and returns.
+// 17/32 of a byte is read a value of rows and weights, and outs * rows results
+// are written; one expert, 16384 rows x 8192 x 8192: 299 us (7.4 PFLOP/s), where
+// a pair's stage takes 521 cycles to 512 of its instructions; 32 experts of 4096
+// x 4096: 115 us (4.8 PFLOP/s), a quarter of it the accumulator's reading, which
+// the next tile's instructions wait for; one turn of small tiles: 7 to 9 us of
+// latency, from the first stage's arrival to the last result's store.
 template <int kTN, int kCtas>
 __global__ void __launch_bounds__(kThreads, 1) k_mx4_product(const __grid_constant__ CUtensorMap wmap,
                                                              const __grid_constant__ CUtensorMap xmap, Args a) {
@@ -804,7 +811,7 @@ cudaError_t product_t(const CallView& v, const uint8_t* xc, const uint8_t* wc, i
   // Share a tile's K among up to eight CTAs where all tiles still run at once
   // (a cluster's SMs come from one of the device's eight parts, each of which
   // may have up to split - 1 too few for another): one row x 1024 outputs x
-  // 16384 took 20 us in 8 CTAs.
+  // 16384 takes 17.3 us in 8 CTAs and 8.2 in 64.
   int split = 1;
   a.split_log2 = 0;
   if (kCtas == 1)
@@ -818,21 +825,30 @@ cudaError_t product_t(const CallView& v, const uint8_t* xc, const uint8_t* wc, i
                       xmap, a);
 }
 
-// The rows of a tile: what makes the fewest turns of the machine, and the
-// smaller of two that make as many.  A tile of 16 rows costs a stage about as
-// much as one of 128 (the instructions of a stage take 450 cycles to issue
-// either way, and 512 to run at 256 rows).
-int tile_rows(int64_t rows, int64_t outs, int experts, int nsm) {
+// The rows of a tile: what takes the fewest cycles, and the smaller of two that
+// take as many.  Cycles are turns of the machine times a tile's: 450 a stage
+// with single CTAs whatever the rows (the instructions take that to issue, less
+// to run) and 520 with pairs, and about 2000 a tile for the results with single
+// CTAs, 3800 with pairs, which have one accumulator.
+// us with 16 / 32 / 64 / 128 / 256 rows a tile (the chosen one in brackets):
+//      16 rows x 32 experts x 4096 x 2048   [11.2] 11.4  14.5  15.3   14.6
+//     256 rows x  1 expert  x 4096 x 4096    18.5  11.9  [8.9] 10.0   12.0
+//    2048 rows x 32 experts x 2048 x 2048    38    25    17.2 [15.7]  19.4
+//    2228 rows x  5 experts x 2541 x  192    15.7  10.9   9.3  [9.4]  11.2
+//   16384 rows x 32 experts x 4096 x 4096   805   425   222   155   [118]
+int tile_rows(int64_t rows, int64_t outs, int64_t stages, int experts, int nsm) {
   const int64_t active = experts < rows ? experts : rows;
   int best = 16;
   int64_t least = INT64_MAX;
   for (int tn = 16; tn <= 256; tn *= 2) {
-    const int64_t wide = tn == 256 ? 2 * kM : kM, units = tn == 256 ? nsm / 2 : nsm;   // (256: pairs of CTAs)
+    const bool pair = tn == 256;
+    const int64_t wide = pair ? 2 * kM : kM, units = pair ? nsm / 2 : nsm;
     // each expert's last run is half full on average, and a run at least
     const int64_t runs = rows / tn + active / 2 > active ? rows / tn + active / 2 : active;
     const int64_t turns = (runs * ((outs + wide - 1) / wide) + units - 1) / units;
-    if (turns < least) {
-      least = turns;
+    const int64_t cycles = turns * (pair ? 520 * stages + 3800 : 450 * stages + 2000);
+    if (cycles < least) {
+      least = cycles;
       best = tn;
     }
   }
@@ -871,7 +887,7 @@ int ebc_mx4_product(ebc_ctx* ctx, const uint8_t* d_x_codes, const uint8_t* d_x_s
   a.blocks = (int)((width + EBC_MX4_BLOCK - 1) / EBC_MX4_BLOCK);
   a.experts = n_experts;
   a.first_wait = v.first_wait;
-  switch (tile_rows(rows, outs, n_experts, v.nsm)) {
+  switch (tile_rows(rows, outs, (width + kStageK - 1) / kStageK, n_experts, v.nsm)) {
     case 16: return cuda_code(product_t<16, 1>(v, d_x_codes, d_w_codes, width, a, st));
     case 32: return cuda_code(product_t<32, 1>(v, d_x_codes, d_w_codes, width, a, st));
     case 64: return cuda_code(product_t<64, 1>(v, d_x_codes, d_w_codes, width, a, st));
