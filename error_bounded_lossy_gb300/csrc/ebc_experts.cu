@@ -414,13 +414,19 @@ bool rows_ok(int type, int64_t width, int64_t ld) {
 
 bool aligned(const void* p, int bytes) { return ((uintptr_t)p & (uintptr_t)(bytes - 1)) == 0; }
 
+// Bytes of the plan's counts for E experts.
+constexpr size_t plan_shared(int E) { return sizeof(uint32_t) * ((size_t)kPlanWarps * (E | 1) + 2 * (size_t)E); }
+
 template <typename Id>
 cudaError_t plan_t(const CallView& v, const Id* ids, int64_t n, int E, int32_t* rows, int32_t* place,
                    int32_t* offsets, cudaStream_t st) {
-  const size_t smem = sizeof(uint32_t) * ((size_t)kPlanWarps * (E | 1) + 2 * (size_t)E);
-  if (smem > 48 * 1024) {
-    const cudaError_t e =
-        cudaFuncSetAttribute(k_moe_plan<Id>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  const size_t smem = plan_shared(E);
+  // More than 48 KB, with the kernel's own variables (some hundred bytes), has
+  // to be allowed.  Always the most: the limit is the kernel's, not the call's,
+  // and another host thread may be about to launch a plan of more experts.
+  if (smem > 47 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(k_moe_plan<Id>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               (int)plan_shared(EBC_MAX_EXPERTS));
     if (e != cudaSuccess) return e;
   }
   // CTAs of the cluster: a round of 1024 slots a CTA takes about a microsecond,

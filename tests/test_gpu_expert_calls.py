@@ -1,0 +1,64 @@
+"""The expert-parallel and 4-bit calls where what matters is not a kernel's
+arithmetic but how a program makes them: processes, threads, streams, graphs."""
+import os
+import subprocess
+import sys
+import threading
+
+import numpy as np
+import pytest
+import torch
+
+import error_bounded_lossy_gb300 as ebc
+
+pytestmark = [pytest.mark.gpu, pytest.mark.skipif(not torch.cuda.is_available(), reason="needs a CUDA device")]
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
+
+def run(program):
+    """A program in a process of its own, from the repository's root."""
+    r = subprocess.run([sys.executable, "-c", program], cwd=ROOT, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stdout + r.stderr
+
+
+@pytest.mark.parametrize("experts", [359, 360, 361, 362])
+def test_a_plan_whose_counts_just_fill_48_kb_in_a_fresh_process(experts):
+    run(f"""
+import torch
+import error_bounded_lossy_gb300 as ebc
+for kind in (torch.int32, torch.int64):
+    ex = ebc.Experts(0)
+    ids = torch.arange({experts}, device="cuda", dtype=kind)[:, None]
+    plan = ex.plan(ids.flip(0).contiguous(), {experts})
+    ex.check()
+    assert torch.equal(plan.rows.cpu(), torch.arange({experts}, dtype=torch.int32).flip(0))
+    assert torch.equal(plan.offsets.cpu(), torch.arange({experts} + 1, dtype=torch.int32))
+    ex.close()
+""")
+
+
+def test_plans_of_different_sizes_in_two_threads():
+    """Each thread has a context of its own; the C calls run without the interpreter's lock."""
+    ids = torch.from_numpy(np.random.default_rng(0).integers(0, 400, (512, 2)).astype(np.int32)).cuda()
+    torch.cuda.synchronize()
+    failed = []
+
+    def plans(experts):
+        h = ebc.ebc_create(0)
+        out = [torch.empty(n, dtype=torch.int32, device="cuda") for n in (1024, 1024, experts + 1)]
+        stream = torch.cuda.Stream()
+        for _ in range(3000):
+            rc = ebc.ebc_moe_plan(h, ids.data_ptr(), 4, 512, 2, experts, *(t.data_ptr() for t in out), stream.cuda_stream)
+            if rc:
+                failed.append((experts, rc))
+                break
+        stream.synchronize()
+        ebc.ebc_destroy(h)
+
+    threads = [threading.Thread(target=plans, args=(e,)) for e in (400, ebc.EBC_MAX_EXPERTS)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed

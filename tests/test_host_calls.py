@@ -1,0 +1,93 @@
+"""What the expert-parallel and 4-bit calls do on the host: the library's
+objects linked with a CUDA runtime without a device (fake_cudart.cpp), which
+writes down the calls that reach it."""
+import ctypes
+import os
+import re
+import subprocess
+
+import pytest
+
+import error_bounded_lossy_gb300 as ebc
+from error_bounded_lossy_gb300 import build as ebc_build
+
+HERE = os.path.dirname(os.path.abspath(__file__))
+A = 1 << 20   # an address that is aligned to anything; nothing reads it
+
+
+class Fake:
+    """The library on the runtime without a device."""
+
+    def __init__(self, path):
+        self.lib = L = ctypes.CDLL(path)
+        P, I, I64 = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64
+        for name, args in {
+            "ebc_create": [P, P, I], "ebc_last_device_error": [P],
+            "ebc_moe_plan": [P, P, I, I64, I, I, P, P, P, P],
+            "ebc_moe_dispatch": [P, P, I64, I, I64, I, I64, P, P, I, P, P],
+            "ebc_moe_combine": [P, P, I64, I, I64, I, I64, P, P, P, P],
+            "ebc_moe_combine_grad": [P, P, I64, P, I64, I, I64, I, I64, P, P, I, P, P, P, P],
+            "ebc_mx4_quantize": [P, P, I64, I, I64, I64, P, P, P],
+            "ebc_mx4_dequantize": [P, P, P, I64, I64, I, P, P],
+            "ebc_moe_dispatch_mx4": [P, P, I64, I, I64, I, I64, P, P, I, P, P, P],
+            "ebc_mx4_product": [P, P, P, I64, I64, P, P, I64, I, P, I, P, P],
+            "ebc_compress": [P, P, I64, I, I, P, P, ctypes.c_uint64, P, P],
+            "cudaSetDevice": [I], "cudaGetDevice": [P], "fake_max_clusters": [I],
+        }.items():
+            getattr(L, name).argtypes = args
+        L.ebc_destroy.argtypes = [P]
+        L.ebc_destroy.restype = None
+        L.fake_log.restype = ctypes.c_char_p
+
+    def context(self, device=0):
+        h = ctypes.c_void_p()
+        assert self.lib.ebc_create(ctypes.byref(h), None, device) == 0
+        self.log()
+        return h
+
+    def log(self):
+        """The calls since the last look."""
+        lines = self.lib.fake_log().decode().splitlines()
+        self.lib.fake_clear()
+        return lines
+
+    def launches(self):
+        return [m.groupdict() for m in (re.match(
+            r"launch (?P<name>\S+) grid (?P<grid>\d+) cluster (?P<cluster>\d+) shared (?P<shared>\d+) "
+            r"stream (?P<stream>\S+) device (?P<device>\d+)(?P<refused> refused)?", s) for s in self.log()) if m]
+
+    def plan(self, ctx, experts, tokens=64, top=2, id_bytes=4, stream=None):
+        return self.lib.ebc_moe_plan(ctx, A, id_bytes, tokens, top, experts, A, A, A, stream)
+
+
+@pytest.fixture(scope="module")
+def path(tmp_path_factory):
+    ebc_build.build()
+    d = tmp_path_factory.mktemp("fake")
+    out = str(d / "libebc_fake.so")
+    cuda = os.path.join(os.path.dirname(os.path.dirname(ebc_build.nvcc())), "include")
+    objs = [os.path.join(ebc_build.BUILD, s.replace(".cu", ".o")) for s in ebc_build.SOURCES]
+    subprocess.run(["g++", "-O1", "-std=c++17", "-fPIC", "-shared", "-Wl,-Bsymbolic", f"-I{cuda}", "-o", out,
+                    os.path.join(HERE, "fake_cudart.cpp"), *objs], check=True)
+    return out
+
+
+@pytest.fixture
+def fake(path):
+    f = Fake(path)
+    f.lib.cudaSetDevice(0)
+    f.log()
+    return f
+
+
+def test_a_plan_fits_its_shared_memory_whatever_was_planned_before(fake):
+    """The counts of 360 experts leave no room in 48 KB for the kernel's own variables; and what a plan of fewer
+    experts allows itself must not take from one of more that another thread is about to launch."""
+    ctx = fake.context()
+    for experts in (1, 359, 360, 361, 362, 400, ebc.EBC_MAX_EXPERTS, 400, ebc.EBC_MAX_EXPERTS):
+        for id_bytes in (4, 8):
+            assert fake.plan(ctx, experts, id_bytes=id_bytes) == 0, experts
+    most = 4 * (32 * (ebc.EBC_MAX_EXPERTS | 1) + 2 * ebc.EBC_MAX_EXPERTS)
+    allowed = [int(s.split()[-1]) for s in fake.log() if s.startswith("shared") and "plan" in s]
+    assert allowed and set(allowed) == {most}
+    fake.lib.ebc_destroy(ctx)
