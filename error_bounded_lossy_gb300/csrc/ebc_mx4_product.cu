@@ -263,7 +263,7 @@ struct Args {
   Glob* glob;
   int64_t rows, outs, scale_bytes;
   int out_type, blocks, experts;   // blocks: scale blocks a row
-  int first_wait;                  // polls of the multiplying warp's first wait for a stage (normally the full limit)
+  int first_wait;                  // (normally the full limit) polls of the multiplying warp's first wait for a stage, and of a pair's first loading warp
   int split_log2;                  // CTAs (a cluster) that share a tile's K; more than one only with a tile a cluster
 };
 
@@ -288,6 +288,23 @@ __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile in
                  : "memory");
   }
   return false;
+}
+
+// What the other CTA of a pair has asked for, told in both directions by the
+// loading warps (stages + 1; 0 is what a CTA that has not told leaves).
+__device__ __forceinline__ void tell_pair(volatile uint32_t* told, uint32_t rank, uint32_t stages) {
+  uint32_t at = smem_u32(const_cast<uint32_t*>(told));
+  asm volatile("mapa.shared::cluster.u32 %0, %0, %1;\n st.shared::cluster.u32 [%0], %2;" : "+r"(at)
+               : "r"(rank ^ 1u), "r"(stages + 1)
+               : "memory");
+}
+__device__ __forceinline__ uint32_t told_by_pair(volatile uint32_t* told) {
+  for (int i = 0; i < kWaitLimit; ++i) {
+    const uint32_t v = *told;
+    if (v) return v - 1;
+    __nanosleep(64);
+  }
+  return 0;
 }
 
 // A wait for what is in flight, with the same limits and nobody to tell.
@@ -393,7 +410,9 @@ __device__ __forceinline__ void store_full(uint32_t taddr, float* y, int64_t ld,
 // In a pair the first CTA multiplies for both; stages, scales and accumulators
 // are announced at its barriers, and its instructions' ends at both CTAs'.
 // Every wait is bounded (see wait()); a CTA that gives up waits for the copies
-// and instructions it has in flight, frees its tensor memory and returns.
+// and instructions it has in flight, frees its tensor memory and returns.  A
+// pair's copies are counted together, at the first CTA's barriers, so there the
+// loading warps first bring each other to the same stage.
 // 17/32 of a byte is read a value of rows and weights, and outs * rows results
 // are written; one expert, 16384 rows x 8192 x 8192: 299 us (7.4 PFLOP/s), where
 // a pair's stage takes 521 cycles to 512 of its instructions; 32 experts of 4096
@@ -409,6 +428,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx4_product(const __grid_consta
   __shared__ uint64_t acc_full[G::kAcc], acc_empty[G::kAcc], drained;
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
+  __shared__ uint32_t s_told;   // see tell_pair()
   __shared__ int s_begin[EBC_MAX_EXPERTS + 1];   // first row of each expert
   __shared__ int s_tiles[EBC_MAX_EXPERTS + 1];   // runs of kTN rows of the experts before
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
@@ -430,6 +450,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx4_product(const __grid_consta
     }
     mbar_init(&drained, 1);
     s_abort = 0;
+    s_told = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (w == 1) {
@@ -495,14 +516,28 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx4_product(const __grid_consta
     int s = 0;
     uint32_t phase = 1;   // of the barriers that stages are given back on
     bool ok = true;
-    for (; ok && walk.at(s_begin, s_tiles, a.experts, kTN, &row0, &count); walk.next(out_tiles)) {
+    uint32_t goal = ~0u;  // stages to ask for: all, until a wait gave up
+    int limit = kCtas == 2 && rank == 0 ? a.first_wait : kWaitLimit;
+    for (; issued < goal && walk.at(s_begin, s_tiles, a.experts, kTN, &row0, &count); walk.next(out_tiles)) {
       // a pair's first CTA has the first half of the instructions' N, the other the second
       const int mine = (count + G::kRound - 1) / G::kRound * 16;
       const int boxes = (mine + G::kBox - 1) / G::kBox, brow = row0 + rank * mine;
       const int wrow = (int)(walk.e * a.outs) + walk.out * G::kOuts + rank * kM;
-      for (int k = k0; k < k1; ++k) {
-        ok = __all_sync(0xffffffffu, wait(&empty[s], phase, &s_abort, a.glob));
-        if (!ok) break;
+      for (int k = k0; k < k1 && issued < goal; ++k) {
+        if (ok) ok = __all_sync(0xffffffffu, wait(&empty[s], phase, &s_abort, a.glob, limit));
+        limit = kWaitLimit;
+        if (!ok && goal == ~0u) {
+          // A stage that the other CTA has asked for has been given back to both
+          // (by one commit), so this CTA can ask for it too without a wait; then
+          // each stage's bytes are expected once and arrive in full.
+          goal = issued;
+          if constexpr (kCtas == 2) {
+            if (lane == 0) tell_pair(&s_told, rank, issued);
+            const uint32_t other = __shfl_sync(0xffffffffu, told_by_pair(&s_told), 0);
+            if (other > goal) goal = other;
+          }
+          if (issued == goal) break;
+        }
         if (elect_one()) {
           const uint32_t bar = in_first<kCtas>(&full[s]);
           if (rank == 0) mbar_expect_tx(&full[s], kCtas * (G::kABytes + boxes * G::kBox * kRowBytes));
@@ -522,6 +557,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx4_product(const __grid_consta
     // every stage given back: no arrival is left on its way to this CTA's barriers
     for (uint32_t i = issued > G::kStages ? issued - G::kStages : 0; ok && i < issued; ++i)
       ok = __all_sync(0xffffffffu, wait(&empty[i % G::kStages], (i / G::kStages) & 1, &s_abort, a.glob));
+    if (kCtas == 2 && goal == ~0u && lane == 0) tell_pair(&s_told, rank, issued);
   } else if (w == 1) {
     if (rank == 0) {
       // Two stages a step with single CTAs, so that the watching, which costs as
@@ -721,17 +757,21 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx4_product(const __grid_consta
   }
 
   tc_fence_before();
-  const bool gave_up = __syncthreads_or(s_abort) != 0;   // the same for all threads: another CTA may set it now
+  bool gave_up = __syncthreads_or(s_abort) != 0;   // the same for all threads: another CTA may set it now
+  if constexpr (kCtas == 2) {
+    cluster_sync();   // no wait of the pair is left: the same for both CTAs
+    gave_up = *const_cast<volatile int*>(&s_abort) != 0;
+  }
   tc_fence_after();
   if (gave_up) {
     // nothing that was started may outlive the CTA (a pair's copies are counted
-    // at its first CTA)
+    // at its first CTA, its instructions' ends at both)
     if (rank == 0 && w == 0) {
       for (uint32_t i = issued > G::kStages ? issued - G::kStages : 0; i < issued; ++i)
         drain(&full[i % G::kStages], (i / G::kStages) & 1);
     }
-    if (rank == 0 && w == 1) {
-      if (elect_one()) tc_commit<kCtas>(&drained);
+    if (w == 1) {
+      if (rank == 0 && elect_one()) tc_commit<kCtas>(&drained);
       __syncwarp();
       drain(&drained, 0);
     }

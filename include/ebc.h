@@ -541,7 +541,8 @@ int ebc_last_device_error(ebc_ctx* ctx);
  * default).  With 0 the first wait gives up before looking, so a test can run
  * the time-out path without hanging anything; later waits keep the full
  * limit.  It sets the same for the first stage that each multiplying warp of
- * the following ebc_mx4_product calls waits for; a product that gives up leaves
+ * the following ebc_mx4_product calls waits for, and for the first that the
+ * loading warp of a CTA pair's first CTA does; a product that gives up leaves
  * d_ys unspecified.  Host-only; EBC_ERR_INVALID_ARG for a null context or polls > 2^22. */
 int ebc_set_first_wait_polls(ebc_ctx* ctx, int polls);
 

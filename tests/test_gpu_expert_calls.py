@@ -62,3 +62,26 @@ def test_plans_of_different_sizes_in_two_threads():
     for t in threads:
         t.join()
     assert not failed
+
+
+@pytest.mark.parametrize("rows,experts,outs,width", [(6000, 4, 4000, 1024), (16384, 4, 4096, 32), (16384, 4, 4096, 288), (16384, 3, 4096, 4000)])
+def test_a_pair_that_gives_up_with_one_of_its_ctas_ahead(rows, experts, outs, width):
+    """The first CTA of each pair gives up before it has asked for anything, the second has asked for as many stages
+    as fit: both wait for what is in flight, the status says so, and what comes after on the stream is right."""
+    e = ebc.Experts(0)
+    g = torch.Generator("cuda").manual_seed(rows)
+    x = e.quantize(torch.randn(rows, width, generator=g, device="cuda"))
+    w = e.quantize(torch.randn(experts, outs, width, generator=g, device="cuda"))
+    cut = torch.tensor([rows * i // experts for i in range(experts + 1)], dtype=torch.int32, device="cuda")
+    want = e.product(x, w, cut)
+    e.check()
+    for _ in range(3):
+        assert ebc.ebc_set_first_wait_polls(e.handle, 0) == 0
+        e.product(x, w, cut)
+        assert ebc.ebc_set_first_wait_polls(e.handle, -1) == 0
+        again = e.product(x, w, cut)   # starts as soon as the CTAs that gave up have gone
+        with pytest.raises(ebc.EbcError) as err:
+            e.check()
+        assert err.value.code == ebc.EBC_ERR_DEVICE_TIMEOUT
+        assert torch.equal(again, want)
+    e.close()

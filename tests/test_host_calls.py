@@ -56,6 +56,13 @@ class Fake:
             r"launch (?P<name>\S+) grid (?P<grid>\d+) cluster (?P<cluster>\d+) shared (?P<shared>\d+) "
             r"stream (?P<stream>\S+) device (?P<device>\d+)(?P<refused> refused)?", s) for s in self.log()) if m]
 
+    def product(self, ctx, rows, experts, outs, width, out_type=ebc.EBC_BF16, stream=None):
+        rc = self.lib.ebc_mx4_product(ctx, A, A, rows, width, A, A, outs, experts, A, out_type, A, stream)
+        assert rc == 0
+        (launch,) = self.launches()
+        tile, ctas = re.search(r"k_mx4_productILi(\d+)ELi(\d)E", launch["name"]).groups()
+        return int(tile), int(ctas), int(launch["cluster"])
+
     def plan(self, ctx, experts, tokens=64, top=2, id_bytes=4, stream=None):
         return self.lib.ebc_moe_plan(ctx, A, id_bytes, tokens, top, experts, A, A, A, stream)
 
@@ -90,4 +97,13 @@ def test_a_plan_fits_its_shared_memory_whatever_was_planned_before(fake):
     most = 4 * (32 * (ebc.EBC_MAX_EXPERTS | 1) + 2 * ebc.EBC_MAX_EXPERTS)
     allowed = [int(s.split()[-1]) for s in fake.log() if s.startswith("shared") and "plan" in s]
     assert allowed and set(allowed) == {most}
+    fake.lib.ebc_destroy(ctx)
+
+
+def test_the_sizes_of_the_time_out_tests_reach_single_ctas_pairs_and_clusters(fake):
+    ctx = fake.context()
+    assert fake.product(ctx, 16, 8, 2000, 2048) == (16, 1, 1)
+    assert fake.product(ctx, 2, 1, 600, 8192)[1:] == (1, 8)
+    for rows, experts, outs, width in [(6000, 4, 4000, 1024), (16384, 4, 4096, 32), (16384, 4, 4096, 288), (16384, 3, 4096, 4000)]:
+        assert fake.product(ctx, rows, experts, outs, width) == (256, 2, 2)
     fake.lib.ebc_destroy(ctx)
