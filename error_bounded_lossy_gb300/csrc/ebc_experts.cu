@@ -57,7 +57,7 @@ __device__ __forceinline__ unsigned equal_lanes(int v, int bits) {
 // (else twice) and two ints a slot are written, far below a microsecond of
 // bandwidth at 65,536 slots.
 template <typename Id>
-__global__ void __launch_bounds__(kPlanThreads) k_moe_plan(const Id* __restrict__ ids, int64_t n, int E,
+__global__ void __launch_bounds__(kPlanThreads) k_moe_plan(const Id* ids, int64_t n, int E,
                                                            int32_t* __restrict__ rows, int32_t* __restrict__ place,
                                                            int32_t* __restrict__ offsets, Glob* glob) {
   extern __shared__ uint32_t sm[];
@@ -191,10 +191,10 @@ constexpr int scatter_vectors() {
 // read once from memory.  Rows past the last expert's become zero.
 // Bound by the bandwidth of the writes.
 template <typename T, int V>
-__global__ void __launch_bounds__(32 * kRowWarps) k_moe_dispatch(const T* __restrict__ x, int64_t ld, int64_t tokens,
+__global__ void __launch_bounds__(32 * kRowWarps) k_moe_dispatch(const T* x, int64_t ld, int64_t tokens,
                                                                  int top, int64_t width,
-                                                                 const int32_t* __restrict__ place,
-                                                                 const int32_t* __restrict__ offsets, int E,
+                                                                 const int32_t* place,
+                                                                 const int32_t* offsets, int E,
                                                                  T* __restrict__ xs, Glob* glob) {
   pdl_enter();
   using R = Vec<T, V>;
@@ -258,10 +258,10 @@ constexpr int kGatherRows = 2;
 // its weight.  A warp takes a piece of a token's row, kGatherRows rows' loads
 // in flight.  Bound by the bandwidth of the reads.
 template <typename T, int V>
-__global__ void __launch_bounds__(32 * kRowWarps) k_moe_combine(const T* __restrict__ ys, int64_t ld, int64_t tokens,
+__global__ void __launch_bounds__(32 * kRowWarps) k_moe_combine(const T* ys, int64_t ld, int64_t tokens,
                                                                 int top, int64_t width,
-                                                                const int32_t* __restrict__ place,
-                                                                const float* __restrict__ weights, T* __restrict__ y,
+                                                                const int32_t* place,
+                                                                const float* weights, T* __restrict__ y,
                                                                 Glob* glob) {
   pdl_enter();
   using R = Vec<T, V>;
@@ -329,9 +329,9 @@ __global__ void __launch_bounds__(32 * kRowWarps) k_moe_combine(const T* __restr
 // expert's become zero.  Bound by bandwidth.
 template <typename T, int V>
 __global__ void __launch_bounds__(32 * kRowWarps) k_moe_combine_grad(
-    const T* __restrict__ dy, int64_t ld_dy, const T* __restrict__ ys, int64_t ld_ys, int64_t tokens, int top,
-    int64_t width, const int32_t* __restrict__ place, const int32_t* __restrict__ offsets, int E,
-    const float* __restrict__ weights, T* __restrict__ dys, float* __restrict__ dw, int split, Glob* glob) {
+    const T* dy, int64_t ld_dy, const T* ys, int64_t ld_ys, int64_t tokens, int top,
+    int64_t width, const int32_t* place, const int32_t* offsets, int E,
+    const float* weights, T* __restrict__ dys, float* __restrict__ dw, int split, Glob* glob) {
   __shared__ float s_dot[kRowWarps];
   pdl_enter();
   using R = Vec<T, V>;

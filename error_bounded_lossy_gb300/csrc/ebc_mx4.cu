@@ -153,10 +153,10 @@ __device__ __forceinline__ uint32_t encode8(const Eight<T>& v, uint32_t* scale) 
 // issue close behind for 16-bit types.  [16384, 4096] bf16: 29 us (5.9 TB/s);
 // [8192, 3328] fp32: 22 us (5.6 TB/s).
 template <typename T, int kV, bool kRoute, int kPieces>
-__global__ void __launch_bounds__(32 * kMxWarps) k_mx4_quantize(const T* __restrict__ x, int64_t ld, int64_t rows,
+__global__ void __launch_bounds__(32 * kMxWarps) k_mx4_quantize(const T* x, int64_t ld, int64_t rows,
                                                                 int64_t width, int top,
-                                                                const int32_t* __restrict__ place,
-                                                                const int32_t* __restrict__ offsets, int E,
+                                                                const int32_t* place,
+                                                                const int32_t* offsets, int E,
                                                                 uint8_t* __restrict__ codes,
                                                                 uint8_t* __restrict__ scales, Glob* glob) {
   using P = Piece<T, kV>;
@@ -229,8 +229,8 @@ __global__ void __launch_bounds__(32 * kMxWarps) k_mx4_quantize(const T* __restr
 // The way back: eight codes a lane, kPieces runs of 256 values a warp.  Bound
 // by the bandwidth of the writes: [8192, 3328] to fp32 20 us (6.1 TB/s).
 template <typename T, int kV, int kPieces>
-__global__ void __launch_bounds__(32 * kMxWarps) k_mx4_dequantize(const uint8_t* __restrict__ codes,
-                                                                  const uint8_t* __restrict__ scales, int64_t rows,
+__global__ void __launch_bounds__(32 * kMxWarps) k_mx4_dequantize(const uint8_t* codes,
+                                                                  const uint8_t* scales, int64_t rows,
                                                                   int64_t width, T* __restrict__ x) {
   using P = Piece<T, kV>;
   __shared__ uint4 s_stage[P::kDirect ? 1 : kMxWarps * kPiece * sizeof(T) / 16];
@@ -298,11 +298,11 @@ __device__ __forceinline__ void load_narrow(const T* p, int64_t left, bool wide,
 }
 
 template <typename T, bool kRoute>
-__global__ void __launch_bounds__(32 * kMxWarps) k_mx4_quantize_narrow(const T* __restrict__ x, int64_t ld,
+__global__ void __launch_bounds__(32 * kMxWarps) k_mx4_quantize_narrow(const T* x, int64_t ld,
                                                                        int64_t rows, int width, int lanes_log2,
                                                                        bool wide, int top,
-                                                                       const int32_t* __restrict__ place,
-                                                                       const int32_t* __restrict__ offsets, int E,
+                                                                       const int32_t* place,
+                                                                       const int32_t* offsets, int E,
                                                                        uint8_t* __restrict__ codes,
                                                                        uint8_t* __restrict__ scales, Glob* glob) {
   pdl_enter();
@@ -356,8 +356,8 @@ __global__ void __launch_bounds__(32 * kMxWarps) k_mx4_quantize_narrow(const T* 
 }
 
 template <typename T>
-__global__ void __launch_bounds__(32 * kMxWarps) k_mx4_dequantize_narrow(const uint8_t* __restrict__ codes,
-                                                                         const uint8_t* __restrict__ scales,
+__global__ void __launch_bounds__(32 * kMxWarps) k_mx4_dequantize_narrow(const uint8_t* codes,
+                                                                         const uint8_t* scales,
                                                                          int64_t rows, int width, int lanes_log2,
                                                                          bool wide, T* __restrict__ x) {
   pdl_enter();

@@ -663,7 +663,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx4_product(const __grid_consta
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             uint4 v = make_uint4(one, one, one, one);
-            if (src[i][j]) v = __ldg(reinterpret_cast<const uint4*>(src[i][j]) + at);
+            if (src[i][j]) v = reinterpret_cast<const uint4*>(src[i][j])[at];
             word[i][j][0] = v.x;
             word[i][j][1] = v.y;
             word[i][j][2] = v.z;

@@ -104,6 +104,12 @@ cudaError_t with_type(int type, int v, F&& f) {
   return with_vec<__half>(v, f);
 }
 
+// The kernels start before those ahead of them on the stream have ended (see
+// pdl_enter), so what they read may still be written while they run.  Their
+// inputs are therefore ordinary pointers: `const __restrict__` and __ldg would
+// let the compiler use loads that take memory to be unchanged for the kernel's
+// whole life, and move them ahead of the wait.
+//
 // Launch with cluster dimension `cluster` (1 = none) and programmatic stream
 // serialization, bracketed by the profiler's events.
 template <typename... KArgs, typename... Args>

@@ -1,6 +1,9 @@
 """The expert-parallel and 4-bit calls on a machine without a GPU: declared and
 exported, refusing what is wrong before any device work; the torch layer checks
 its tensors."""
+import os
+import re
+
 import pytest
 import torch
 
@@ -46,3 +49,12 @@ def test_no_context_without_a_device():
         pytest.skip("a GPU is present")
     with pytest.raises(ebc.EbcError):
         ebc.Experts(0)
+
+
+@pytest.mark.parametrize("name", ["ebc_experts.cu", "ebc_mx4.cu", "ebc_mx4_product.cu"])
+def test_kernels_that_start_early_read_with_ordinary_loads(name):
+    """Read-only loads are for memory that nobody writes while the kernel runs; these kernels start before their
+    producers have ended."""
+    text = open(os.path.join(ebc_build.CSRC, name)).read()
+    assert "pdl_enter();" in text
+    assert not re.findall(r"const\s+\w+\s*\*\s*__restrict__|__ldg|ld\.global\.nc", text)
