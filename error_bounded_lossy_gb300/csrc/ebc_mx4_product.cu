@@ -903,8 +903,10 @@ int ebc_mx4_product(ebc_ctx* ctx, const uint8_t* d_x_codes, const uint8_t* d_x_s
                     const uint8_t* d_w_codes, const uint8_t* d_w_scales, int64_t outs, int n_experts,
                     const int32_t* d_offsets, int out_type, void* d_ys, void* stream) {
   const int b = type_bytes(out_type);
-  if (!ctx || !b || rows < 0 || rows > INT32_MAX || width < 1 || width > (1 << 24) || outs < 1 || n_experts < 1 ||
-      n_experts > EBC_MAX_EXPERTS || outs > (int64_t)INT32_MAX / n_experts || (!d_offsets && n_experts != 1) ||
+  // a tile that starts at the last row, or at the last output, still ends inside 31 bits
+  constexpr int64_t kMost = (1ll << 31) - 256;
+  if (!ctx || !b || rows < 0 || rows > kMost || width < 1 || width > (1 << 24) || outs < 1 || n_experts < 1 ||
+      n_experts > EBC_MAX_EXPERTS || outs > kMost / n_experts || (!d_offsets && n_experts != 1) ||
       !aligned(d_offsets, 4))
     return EBC_ERR_INVALID_ARG;
   if (rows > 0 && (!d_x_codes || !aligned(d_x_codes, 16) || !d_x_scales || !aligned(d_x_scales, 16) || !d_w_codes ||

@@ -513,8 +513,8 @@ int ebc_moe_dispatch_mx4(ebc_ctx* ctx, const void* d_x, int64_t ld_x, int type, 
  * in fp32, and the sum is rounded once to out_type.  Offsets must ascend from
  * 0 to at most `rows`; others are clamped to that, and recorded as
  * EBC_ERR_INVALID_ARG.  d_offsets = NULL: one expert takes every row (a plain
- * matrix product; n_experts must be 1).  rows <= 2^31 - 1,
- * n_experts * outs <= 2^31 - 1. */
+ * matrix product; n_experts must be 1).  rows <= 2^31 - 256,
+ * n_experts * outs <= 2^31 - 256. */
 int ebc_mx4_product(ebc_ctx* ctx, const uint8_t* d_x_codes, const uint8_t* d_x_scales, int64_t rows, int64_t width,
                     const uint8_t* d_w_codes, const uint8_t* d_w_scales, int64_t outs, int n_experts,
                     const int32_t* d_offsets, int out_type, void* d_ys, void* stream);

@@ -257,6 +257,27 @@ def test_rows_past_32_bits_of_outputs(ex):
         check_product(ex, part, w, torch.tensor([0, 300]), torch.bfloat16, ys[at])
 
 
+def test_as_many_rows_as_a_product_takes(ex):
+    """Segments that end at 2^31 - 256 rows: the first, the last and some in between."""
+    rows, width = 2 ** 31 - 256, 32
+    torch.cuda.empty_cache()
+    if torch.cuda.mem_get_info()[0] < 90 << 30:
+        pytest.skip("needs 90 GB")
+    x = ebc.Mx4(*(torch.zeros(rows, 16, dtype=torch.uint8, device="cuda") for _ in range(2)), width)
+    w = ex.quantize(torch.ones(2, 1, width, device="cuda") * torch.tensor([1.0, 2.0], device="cuda")[:, None, None])
+    x.scales[:, 0] = 127
+    at = torch.tensor([0, 1, 127, 255, 2 ** 30 - 1, 2 ** 30, 2 ** 31 - 513, 2 ** 31 - 512, 2 ** 31 - 258, 2 ** 31 - 257], device="cuda")
+    x.codes[at, 0] = 0x62   # 1 and 4
+    want = torch.zeros(rows, 1, dtype=torch.float16, device="cuda")
+    for cut in ([0, 0, rows], [0, rows, rows], [0, 2 ** 30, rows]):
+        offsets = torch.tensor(cut, dtype=torch.int32, device="cuda")
+        ys = ex.product(x, w, offsets, torch.float16)
+        ex.check()
+        want[at] = torch.where(at < cut[1], 5.0, 10.0).half()[:, None]
+        assert torch.equal(ys, want)
+        del ys
+
+
 def test_the_same_bits_in_every_run_and_on_another_stream(ex):
     x, w, offsets = case(ex, 700, 6, 520, 2080, 12)
     first = ex.product(x, w, offsets)

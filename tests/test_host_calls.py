@@ -107,3 +107,16 @@ def test_the_sizes_of_the_time_out_tests_reach_single_ctas_pairs_and_clusters(fa
     for rows, experts, outs, width in [(6000, 4, 4000, 1024), (16384, 4, 4096, 32), (16384, 4, 4096, 288), (16384, 3, 4096, 4000)]:
         assert fake.product(ctx, rows, experts, outs, width) == (256, 2, 2)
     fake.lib.ebc_destroy(ctx)
+
+
+def test_a_product_takes_no_more_rows_than_its_tiles_can_count(fake):
+    """A tile of 256 that starts at the last row or output must end inside 31 bits."""
+    ctx = fake.context()
+    most = 2 ** 31 - 256
+    call = lambda rows, outs, experts: fake.lib.ebc_mx4_product(  # noqa: E731
+        ctx, A, A, rows, 32, A, A, outs, experts, A, ebc.EBC_BF16, A, None)
+    for rows, outs, experts in [(most, 1, 1), (most, 4096, 32), (1, most, 1), (5, most // 2, 2), (5, most // 1024, 1024)]:
+        assert call(rows, outs, experts) == 0
+    for rows, outs, experts in [(most + 1, 1, 1), (2 ** 31 - 1, 1, 1), (1, most + 1, 1), (5, most // 2 + 1, 2)]:
+        assert call(rows, outs, experts) == ebc.EBC_ERR_INVALID_ARG
+    fake.lib.ebc_destroy(ctx)
