@@ -38,6 +38,7 @@ void ebc::prof_end(Prof* p, cudaStream_t st) {
 struct ebc_ctx {
   int device = 0;
   cudaStream_t last_stream = nullptr;
+  bool any_stream = false;             // has made calls that may be on other streams too, or in graphs
   Glob* glob = nullptr;                // device
   unsigned long long* h_pinned = nullptr;  // pinned scratch for the host-buffer calls
   // compress scratch
@@ -223,6 +224,7 @@ int ebc::begin_call(ebc_ctx* c, cudaStream_t st, CallView* out) {
   if (!c) return EBC_ERR_INVALID_ARG;
   if (cudaSetDevice(c->device) != cudaSuccess) return EBC_ERR_CUDA;
   c->last_stream = st;
+  c->any_stream = true;
   out->nsm = c->nsm;
   out->first_wait = c->first_wait;
   out->glob = c->glob;
@@ -649,7 +651,8 @@ int ebc_select_modes(const double* cr, const double* tc, const double* td, doubl
 int ebc_last_device_error(ebc_ctx* c) {
   if (!c) return EBC_ERR_INVALID_ARG;
   if (cudaSetDevice(c->device) != cudaSuccess) return EBC_ERR_CUDA;
-  if (cudaStreamSynchronize(c->last_stream) != cudaSuccess) return EBC_ERR_CUDA;
+  if ((c->any_stream ? cudaDeviceSynchronize() : cudaStreamSynchronize(c->last_stream)) != cudaSuccess)
+    return EBC_ERR_CUDA;
   unsigned int code = 0;
   if (cudaMemcpy(&code, &c->glob->sticky, 4, cudaMemcpyDeviceToHost) != cudaSuccess) return EBC_ERR_CUDA;
   if (code) {

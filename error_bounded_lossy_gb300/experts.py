@@ -205,7 +205,8 @@ class Experts:
                         _type(dtype))
 
     def check(self) -> None:
-        """Waits for the last call and raises what its kernels recorded."""
+        """Waits for the device (calls on every stream, and graphs that captured some) and raises the first error
+        that a kernel recorded since the last check."""
         rc = ebc_last_device_error(self._ctx)
         if rc:
             raise EbcError(rc, "device")

@@ -424,7 +424,8 @@ int ebc_decompress_noalloc(const void* d_in, uint64_t in_bytes, float* d_xhat, i
  * are the elements between the starts of two rows of an input (>= width);
  * outputs are dense.  Row addresses that are all multiples of 16 bytes are
  * the fast case.  The calls are asynchronous on `stream`, take no scratch,
- * and give the same bits in every run.  They return EBC_ERR_INVALID_ARG for
+ * and give the same bits in every run; a graph that captured them uses the
+ * context, which has to outlive it.  They return EBC_ERR_INVALID_ARG for
  * bad shapes, types or pointers before any device work; an entry of a plan
  * that points outside its buffer is skipped, and recorded as
  * EBC_ERR_INVALID_ARG for ebc_last_device_error. */
@@ -527,7 +528,11 @@ int ebc_get_stats(ebc_ctx* ctx, ebc_stats* out, void* stream);
 
 /* Synchronise the stream of the last call and return (and clear) the first
  * error the kernels recorded since the previous query: EBC_OK,
- * EBC_ERR_CAPACITY, EBC_ERR_CORRUPT, EBC_ERR_INVALID_ARG or EBC_ERR_INTERNAL. */
+ * EBC_ERR_CAPACITY, EBC_ERR_CORRUPT, EBC_ERR_INVALID_ARG,
+ * EBC_ERR_DEVICE_TIMEOUT or EBC_ERR_INTERNAL.  A context that has made an
+ * ebc_moe_* or ebc_mx4_* call synchronises its device instead: those calls need
+ * no scratch, so they may be on several streams at once, and in graphs that are
+ * replayed on others. */
 int ebc_last_device_error(ebc_ctx* ctx);
 
 /* Failure-detection test aid.  Every device-side wait of the codec is bounded:

@@ -85,3 +85,31 @@ def test_a_pair_that_gives_up_with_one_of_its_ctas_ahead(rows, experts, outs, wi
         assert err.value.code == ebc.EBC_ERR_DEVICE_TIMEOUT
         assert torch.equal(again, want)
     e.close()
+
+
+def test_a_check_finds_an_error_of_an_earlier_stream_and_of_a_replay():
+    e = ebc.Experts(0)
+    ids = {k: torch.full((4, 2), v, dtype=torch.int32, device="cuda") for k, v in (("good", 0), ("bad", 99))}
+    a, b = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(a):
+        torch.cuda._sleep(100_000_000)   # about 50 ms
+    e.plan(ids["bad"], 4, stream=a)
+    e.plan(ids["good"], 4, stream=b)
+    with pytest.raises(ebc.EbcError):
+        e.check()
+    e.check()
+    given = ids["good"].clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        e.plan(given, 4)
+    given.copy_(ids["bad"])
+    torch.cuda.synchronize()
+    for _ in range(2):
+        with torch.cuda.stream(a):
+            torch.cuda._sleep(100_000_000)
+            graph.replay()
+        with pytest.raises(ebc.EbcError):
+            e.check()
+    e.check()
+    e.close()

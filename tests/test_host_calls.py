@@ -120,3 +120,20 @@ def test_a_product_takes_no_more_rows_than_its_tiles_can_count(fake):
     for rows, outs, experts in [(most + 1, 1, 1), (2 ** 31 - 1, 1, 1), (1, most + 1, 1), (5, most // 2 + 1, 2)]:
         assert call(rows, outs, experts) == ebc.EBC_ERR_INVALID_ARG
     fake.lib.ebc_destroy(ctx)
+
+
+def test_a_check_waits_for_every_stream_of_the_experts_calls(fake):
+    """An error may come from any of the streams, or from a graph's replay."""
+    ctx = fake.context()
+    # the codec's calls share a scratch, so they are ordered: the last stream is enough
+    assert fake.lib.ebc_compress(ctx, A, 0, 1, 16, (ctypes.c_float * 1)(0.1), A, 1 << 20, A, 0x70) == 0
+    fake.log()
+    assert fake.lib.ebc_last_device_error(ctx) == 0
+    assert [s for s in fake.log() if s.startswith("sync")] == ["sync stream 0x70"]
+    for stream in (0x10, 0x20):
+        assert fake.plan(ctx, 4, stream=stream) == 0
+    for _ in range(2):   # a graph may be replayed after a check, too
+        fake.log()
+        assert fake.lib.ebc_last_device_error(ctx) == 0
+        assert "sync device 0" in fake.log()
+    fake.lib.ebc_destroy(ctx)
