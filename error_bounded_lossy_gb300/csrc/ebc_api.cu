@@ -222,7 +222,12 @@ static int grow(void** buf, size_t* have, size_t need) {
 
 int ebc::begin_call(ebc_ctx* c, cudaStream_t st, CallView* out) {
   if (!c) return EBC_ERR_INVALID_ARG;
-  if (cudaSetDevice(c->device) != cudaSuccess) return EBC_ERR_CUDA;
+  int now = -1;
+  if (cudaGetDevice(&now) != cudaSuccess) return EBC_ERR_CUDA;
+  if (now != c->device) {
+    if (cudaSetDevice(c->device) != cudaSuccess) return EBC_ERR_CUDA;
+    out->caller_device = now;
+  }
   c->last_stream = st;
   c->any_stream = true;
   out->nsm = c->nsm;

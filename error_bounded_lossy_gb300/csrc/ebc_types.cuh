@@ -10,14 +10,22 @@
 
 namespace ebc {
 
-// What the expert-parallel and 4-bit entry points need of a context: its
-// device, the device's SMs, the polls of a kernel's first wait (a test aid), the
-// error word that the kernels record into, and the profiler.  begin_call checks the context, makes its device current and
-// notes the stream as that of the last call (defined with the C ABI).
+// What the expert-parallel and 4-bit entry points need of a context: the
+// device's SMs, the polls of a kernel's first wait (a test aid), the error word
+// that the kernels record into, and the profiler.  begin_call checks the
+// context, makes its device current for as long as the view lives, and notes
+// the stream as that of the last call (defined with the C ABI).
 struct CallView {
   int nsm, first_wait;
   Glob* glob;
   Prof* prof;
+  int caller_device = -1;   // the host thread's device before, where it was another
+  CallView() = default;
+  CallView(const CallView&) = delete;
+  CallView& operator=(const CallView&) = delete;
+  ~CallView() {
+    if (caller_device >= 0) cudaSetDevice(caller_device);
+  }
 };
 int begin_call(ebc_ctx* ctx, cudaStream_t st, CallView* out);
 

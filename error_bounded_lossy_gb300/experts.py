@@ -15,6 +15,7 @@ experts' products on them (the ebc_moe_* and ebc_mx4_* calls of
 """
 from __future__ import annotations
 
+import contextlib
 import importlib.util
 import os
 
@@ -97,13 +98,19 @@ class Experts:
     def __init__(self, device: int = 0):
         self.device = torch.device("cuda", device)
         self._index = int(device)
-        self._ctx = ebc_create(device)
+        with self._here():
+            self._ctx = ebc_create(device)
         self._h = self._ctx.value
+
+    def _here(self):
+        """For the context's own calls, which leave its device current: the caller's is current again afterwards."""
+        return torch.cuda.device(self.device) if torch.cuda.is_available() else contextlib.nullcontext()
 
     def close(self):
         if self._ctx is not None:
             self._h = 0
-            ebc_destroy(self._ctx)
+            with self._here():
+                ebc_destroy(self._ctx)
             self._ctx = None
 
     def __del__(self):
@@ -207,12 +214,14 @@ class Experts:
     def check(self) -> None:
         """Waits for the device (calls on every stream, and graphs that captured some) and raises the first error
         that a kernel recorded since the last check."""
-        rc = ebc_last_device_error(self._ctx)
+        with self._here():
+            rc = ebc_last_device_error(self._ctx)
         if rc:
             raise EbcError(rc, "device")
 
     def set_profiling(self, enable: bool) -> None:
-        rc = ebc_set_profiling(self._ctx, enable)
+        with self._here():
+            rc = ebc_set_profiling(self._ctx, enable)
         if rc:
             raise EbcError(rc, "ebc_set_profiling")
 

@@ -424,6 +424,8 @@ int ebc_decompress_noalloc(const void* d_in, uint64_t in_bytes, float* d_xhat, i
  * are the elements between the starts of two rows of an input (>= width);
  * outputs are dense.  Row addresses that are all multiples of 16 bytes are
  * the fast case.  The calls are asynchronous on `stream`, take no scratch,
+ * leave the host thread's current device as it is (the other calls of a context
+ * make its device current),
  * and give the same bits in every run; a graph that captured them uses the
  * context, which has to outlive it.  They return EBC_ERR_INVALID_ARG for
  * bad shapes, types or pointers before any device work; an entry of a plan

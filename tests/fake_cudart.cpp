@@ -166,7 +166,7 @@ cudaError_t cudaLaunchKernelExC(const cudaLaunchConfig_t* c, const void* f, void
     if (c->attrs[i].id == cudaLaunchAttributeClusterDimension) cluster = c->attrs[i].val.clusterDim.x;
   auto it = g_shared_limit.find(f);
   const size_t allowed = it == g_shared_limit.end() ? 0 : (size_t)it->second;
-  const bool fits = c->dynamicSmemBytes + g_static_shared <= 48 * 1024 || c->dynamicSmemBytes <= allowed;
+  const bool fits = c->dynamicSmemBytes + g_static_shared <= (allowed > 48 * 1024 ? allowed + 1024 : 48 * 1024);
   logf("launch %s grid %u cluster %u shared %zu stream %p device %d%s", name_of(f), c->gridDim.x, cluster,
        c->dynamicSmemBytes, (void*)c->stream, g_device, fits ? "" : " refused");
   if (!fits) return cudaErrorInvalidValue;

@@ -32,7 +32,7 @@ class Fake:
             "ebc_moe_dispatch_mx4": [P, P, I64, I, I64, I, I64, P, P, I, P, P, P],
             "ebc_mx4_product": [P, P, P, I64, I64, P, P, I64, I, P, I, P, P],
             "ebc_compress": [P, P, I64, I, I, P, P, ctypes.c_uint64, P, P],
-            "cudaSetDevice": [I], "cudaGetDevice": [P], "fake_max_clusters": [I],
+            "cudaSetDevice": [I], "cudaGetDevice": [P], "fake_max_clusters": [I], "fake_static_shared": [I],
         }.items():
             getattr(L, name).argtypes = args
         L.ebc_destroy.argtypes = [P]
@@ -137,3 +137,61 @@ def test_a_check_waits_for_every_stream_of_the_experts_calls(fake):
         assert fake.lib.ebc_last_device_error(ctx) == 0
         assert "sync device 0" in fake.log()
     fake.lib.ebc_destroy(ctx)
+
+
+def test_the_callers_device_stays_current(fake):
+    """A context of another device than the thread's current one: kernels are launched there, and the thread's device
+    is what it was, also where a launch fails."""
+    lib, now = fake.lib, ctypes.c_int(-1)
+    ctx = fake.context(1)
+    calls = {
+        "plan": lambda: fake.plan(ctx, 4),
+        "dispatch": lambda: lib.ebc_moe_dispatch(ctx, A, 8, 0, 4, 2, 8, A, A, 3, A, None),
+        "combine": lambda: lib.ebc_moe_combine(ctx, A, 8, 0, 4, 2, 8, A, A, A, None),
+        "combine_grad": lambda: lib.ebc_moe_combine_grad(ctx, A, 8, A, 8, 0, 4, 2, 8, A, A, 3, A, A, A, None),
+        "quantize": lambda: lib.ebc_mx4_quantize(ctx, A, 64, 0, 4, 64, A, A, None),
+        "dequantize": lambda: lib.ebc_mx4_dequantize(ctx, A, A, 4, 64, 0, A, None),
+        "dispatch_mx4": lambda: lib.ebc_moe_dispatch_mx4(ctx, A, 64, 0, 4, 2, 64, A, A, 3, A, A, None),
+        "product": lambda: lib.ebc_mx4_product(ctx, A, A, 4, 64, A, A, 16, 2, A, 0, A, None),
+    }
+    for device in (0, 1):
+        lib.cudaSetDevice(device)
+        for name, call in calls.items():
+            assert call() == 0, name
+            assert lib.cudaGetDevice(ctypes.byref(now)) == 0 and now.value == device, name
+            assert [x["device"] for x in fake.launches()] == ["1"], name
+    lib.cudaSetDevice(0)
+    lib.fake_static_shared(1 << 20)   # no launch fits
+    for name, call in calls.items():
+        assert call() == ebc.EBC_ERR_CUDA, name
+        assert lib.cudaGetDevice(ctypes.byref(now)) == 0 and now.value == 0, name
+    lib.fake_static_shared(256)
+    lib.ebc_destroy(ctx)
+
+
+def test_the_torch_class_makes_its_contexts_own_calls_under_its_device(monkeypatch):
+    """Creating, checking and closing a context leave its device current; the class puts the caller's back."""
+    import contextlib
+    import torch
+    from error_bounded_lossy_gb300 import experts
+    inside, seen = [], []
+
+    @contextlib.contextmanager
+    def device(d):
+        inside.append(d)
+        yield
+        inside.pop()
+
+    def call(result):
+        return lambda *a: (seen.append(list(inside)), result)[1]
+
+    monkeypatch.setattr(torch.cuda, "is_available", lambda: True)
+    monkeypatch.setattr(torch.cuda, "device", device)
+    monkeypatch.setattr(experts, "ebc_create", call(ctypes.c_void_p(8)))
+    for name in ("ebc_last_device_error", "ebc_set_profiling", "ebc_destroy"):
+        monkeypatch.setattr(experts, name, call(0))
+    ex = experts.Experts(1)
+    ex.check()
+    ex.set_profiling(False)
+    ex.close()
+    assert seen == [[torch.device("cuda", 1)]] * 4
