@@ -815,16 +815,15 @@ bool aligned(const void* p, int bytes) { return ((uintptr_t)p & (uintptr_t)(byte
 
 // codes [rows][code_bytes] in boxes of 128 bytes x box_rows
 cudaError_t make_map(CUtensorMap* map, const uint8_t* codes, int64_t rows, int64_t code_bytes, int box_rows) {
-  static PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
-  if (!encode) {
+  // found once, whichever host thread comes first
+  static const PFN_cuTensorMapEncodeTiled_v12000 encode = [] {
     cudaDriverEntryPointQueryResult q;
     void* fn = nullptr;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &q) !=
-            cudaSuccess ||
-        q != cudaDriverEntryPointSuccess || !fn)
-      return cudaErrorNotSupported;
-    encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
-  }
+    const bool found = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault,
+                                                        &q) == cudaSuccess && q == cudaDriverEntryPointSuccess;
+    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(found ? fn : nullptr);
+  }();
+  if (!encode) return cudaErrorNotSupported;
   const cuuint64_t dims[2] = {(cuuint64_t)code_bytes, (cuuint64_t)rows};
   const cuuint64_t strides[1] = {(cuuint64_t)code_bytes};
   const cuuint32_t box[2] = {(cuuint32_t)kRowBytes, (cuuint32_t)box_rows};

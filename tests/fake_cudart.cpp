@@ -9,18 +9,22 @@
 // pass 48 KB and the kernel's attribute does not allow it.
 #include <cuda_runtime_api.h>
 
+#include <chrono>
 #include <cstdarg>
 #include <cstdio>
 #include <cstdlib>
 #include <cstring>
 #include <map>
+#include <mutex>
 #include <string>
+#include <thread>
 
 extern "C" {
 typedef void (*fake_launch_cb)(const char* name, void** args);
 }
 
 namespace {
+std::recursive_mutex g_lock;   // of the log and the maps
 std::string g_log;
 std::map<const void*, std::string> g_kernels;        // host function -> device name
 std::map<const void*, int> g_shared_limit;           // host function -> dynamic shared memory allowed
@@ -34,6 +38,7 @@ void logf(const char* format, ...) {
   va_start(v, format);
   vsnprintf(line, sizeof line, format, v);
   va_end(v);
+  std::lock_guard<std::recursive_mutex> hold(g_lock);
   g_log += line;
   g_log += '\n';
 }
@@ -146,6 +151,7 @@ cudaError_t cudaEventElapsedTime(float* ms, cudaEvent_t, cudaEvent_t) {
 
 // ---- kernels ----
 cudaError_t cudaFuncSetAttribute(const void* f, cudaFuncAttribute a, int v) {
+  std::lock_guard<std::recursive_mutex> hold(g_lock);
   if (a == cudaFuncAttributeMaxDynamicSharedMemorySize) {
     g_shared_limit[f] = v;
     logf("shared %s %d", name_of(f), v);
@@ -161,6 +167,7 @@ cudaError_t cudaOccupancyMaxActiveClusters(int* n, const void*, const cudaLaunch
   return cudaSuccess;
 }
 cudaError_t cudaLaunchKernelExC(const cudaLaunchConfig_t* c, const void* f, void** args) {
+  std::lock_guard<std::recursive_mutex> hold(g_lock);
   unsigned cluster = 1;
   for (unsigned i = 0; i < c->numAttrs; ++i)
     if (c->attrs[i].id == cudaLaunchAttributeClusterDimension) cluster = c->attrs[i].val.clusterDim.x;
@@ -180,6 +187,7 @@ static int fake_encode(void*, int, unsigned, void*, const void*, const void*, co
 cudaError_t cudaGetDriverEntryPointByVersion(const char* name, void** p, unsigned, unsigned long long,
                                              cudaDriverEntryPointQueryResult* q) {
   logf("entry point %s", name);
+  std::this_thread::sleep_for(std::chrono::milliseconds(50));   // other threads may ask meanwhile
   *p = (void*)fake_encode;
   *q = cudaDriverEntryPointSuccess;
   return cudaSuccess;

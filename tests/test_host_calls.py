@@ -4,7 +4,9 @@ writes down the calls that reach it."""
 import ctypes
 import os
 import re
+import shutil
 import subprocess
+import threading
 
 import pytest
 
@@ -195,3 +197,20 @@ def test_the_torch_class_makes_its_contexts_own_calls_under_its_device(monkeypat
     ex.set_profiling(False)
     ex.close()
     assert seen == [[torch.device("cuda", 1)]] * 4
+
+
+def test_the_first_products_of_several_threads(path, tmp_path):
+    """The driver's entry point is looked up once, by one of them."""
+    fake = Fake(shutil.copy(path, tmp_path / "libebc_first.so"))   # (nothing has been looked up in this copy)
+    ctxs = [fake.context() for _ in range(4)]
+    rcs = []
+    threads = [threading.Thread(target=lambda c=c: rcs.append(
+        fake.lib.ebc_mx4_product(c, A, A, 4, 64, A, A, 16, 2, A, 0, A, None))) for c in ctxs]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert rcs == [0] * 4
+    assert sum(s.startswith("entry point") for s in fake.log()) == 1
+    for c in ctxs:
+        fake.lib.ebc_destroy(c)
