@@ -57,6 +57,7 @@ struct ebc_ctx {
   unsigned long long* d_nbytes = nullptr;
   uint32_t cepoch = 0, depoch = 0;
   int nsm = 0;
+  unsigned plan_cluster = 0;           // CTAs that a plan's cluster may have, 0 = not asked yet
   // the compress layout whose dedup table and look-back flags are known clean
   const void* clean_buf = nullptr;
   int64_t cleanB = -1;
@@ -231,6 +232,7 @@ int ebc::begin_call(ebc_ctx* c, cudaStream_t st, CallView* out) {
   c->last_stream = st;
   c->any_stream = true;
   out->nsm = c->nsm;
+  out->plan_cluster = &c->plan_cluster;
   out->first_wait = c->first_wait;
   out->glob = c->glob;
   out->prof = c->prof;

@@ -417,6 +417,32 @@ bool aligned(const void* p, int bytes) { return ((uintptr_t)p & (uintptr_t)(byte
 // Bytes of the plan's counts for E experts.
 constexpr size_t plan_shared(int E) { return sizeof(uint32_t) * ((size_t)kPlanWarps * (E | 1) + 2 * (size_t)E); }
 
+// Whether the device (or what this process may use of it) has a cluster of 16
+// CTAs of the plan, whose size is not one that every device has.
+template <typename Id>
+cudaError_t ask_cluster(unsigned* most) {
+  const cudaError_t e = cudaFuncSetAttribute(k_moe_plan<Id>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             (int)plan_shared(EBC_MAX_EXPERTS));
+  if (e != cudaSuccess) return e;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = 16;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(16);
+  cfg.blockDim = dim3(kPlanThreads);
+  cfg.dynamicSmemBytes = plan_shared(EBC_MAX_EXPERTS);
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  int clusters = 0;
+  if (cudaOccupancyMaxActiveClusters(&clusters, k_moe_plan<Id>, &cfg) != cudaSuccess) {
+    cudaGetLastError();   // "none" may be said so
+    clusters = 0;
+  }
+  *most = clusters > 0 ? 16 : 8;
+  return cudaSuccess;
+}
+
 template <typename Id>
 cudaError_t plan_t(const CallView& v, const Id* ids, int64_t n, int E, int32_t* rows, int32_t* place,
                    int32_t* offsets, cudaStream_t st) {
@@ -432,10 +458,12 @@ cudaError_t plan_t(const CallView& v, const Id* ids, int64_t n, int E, int32_t* 
   // CTAs of the cluster: a round of 1024 slots a CTA takes about a microsecond,
   // a larger cluster about as long to come together (1024 slots: 4.3 us with
   // one CTA, 4.8 with 8; 8192: 11.3, 5.3, and 5.8 with 16; 65,536: 71, 12.5, 9.1)
-  const unsigned C = n <= 1024 ? 1 : n <= 8192 ? 8 : 16;
+  unsigned C = n <= 1024 ? 1 : n <= 8192 ? 8 : 16;
   if (C > 8) {
-    const cudaError_t e = cudaFuncSetAttribute(k_moe_plan<Id>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    cudaError_t e = cudaFuncSetAttribute(k_moe_plan<Id>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e == cudaSuccess && *v.plan_cluster == 0) e = ask_cluster<Id>(v.plan_cluster);
     if (e != cudaSuccess) return e;
+    C = *v.plan_cluster;
   }
   return launch_named(v, "k_moe_plan", st, k_moe_plan<Id>, dim3(C), dim3(kPlanThreads), smem, C, ids, n, E, rows,
                       place, offsets, v.glob);

@@ -11,12 +11,14 @@
 namespace ebc {
 
 // What the expert-parallel and 4-bit entry points need of a context: the
-// device's SMs, the polls of a kernel's first wait (a test aid), the error word
-// that the kernels record into, and the profiler.  begin_call checks the
+// device's SMs, the CTAs that a plan's cluster may have (0: not asked yet), the
+// polls of a kernel's first wait (a test aid), the error word that the kernels
+// record into, and the profiler.  begin_call checks the
 // context, makes its device current for as long as the view lives, and notes
 // the stream as that of the last call (defined with the C ABI).
 struct CallView {
   int nsm, first_wait;
+  unsigned* plan_cluster;
   Glob* glob;
   Prof* prof;
   int caller_device = -1;   // the host thread's device before, where it was another

@@ -5,7 +5,8 @@
 // reads, and a launch may be handed to the test, which can do the kernel's work.
 //
 // The rules of the runtime that the tests are about are kept: a current device
-// per host thread, and a launch fails when its dynamic and static shared memory
+// per host thread; a cluster of more than 8 has to be allowed and to fit; and a
+// launch fails when its dynamic and static shared memory
 // pass 48 KB and the kernel's attribute does not allow it.
 #include <cuda_runtime_api.h>
 
@@ -28,6 +29,7 @@ std::recursive_mutex g_lock;   // of the log and the maps
 std::string g_log;
 std::map<const void*, std::string> g_kernels;        // host function -> device name
 std::map<const void*, int> g_shared_limit;           // host function -> dynamic shared memory allowed
+std::map<const void*, int> g_large_cluster;          // host function -> clusters of more than 8 allowed
 fake_launch_cb g_on_launch = nullptr;
 int g_static_shared = 256, g_max_clusters = 8;
 thread_local int g_device = 0;
@@ -156,6 +158,7 @@ cudaError_t cudaFuncSetAttribute(const void* f, cudaFuncAttribute a, int v) {
     g_shared_limit[f] = v;
     logf("shared %s %d", name_of(f), v);
   }
+  if (a == cudaFuncAttributeNonPortableClusterSizeAllowed) g_large_cluster[f] = v;
   return cudaSuccess;
 }
 cudaError_t cudaOccupancyMaxActiveBlocksPerMultiprocessorWithFlags(int* n, const void*, int, size_t, unsigned) {
@@ -173,7 +176,8 @@ cudaError_t cudaLaunchKernelExC(const cudaLaunchConfig_t* c, const void* f, void
     if (c->attrs[i].id == cudaLaunchAttributeClusterDimension) cluster = c->attrs[i].val.clusterDim.x;
   auto it = g_shared_limit.find(f);
   const size_t allowed = it == g_shared_limit.end() ? 0 : (size_t)it->second;
-  const bool fits = c->dynamicSmemBytes + g_static_shared <= (allowed > 48 * 1024 ? allowed + 1024 : 48 * 1024);
+  const bool fits = c->dynamicSmemBytes + g_static_shared <= (allowed > 48 * 1024 ? allowed + 1024 : 48 * 1024) &&
+                    (cluster <= 8 || (g_large_cluster[f] && g_max_clusters > 0));
   logf("launch %s grid %u cluster %u shared %zu stream %p device %d%s", name_of(f), c->gridDim.x, cluster,
        c->dynamicSmemBytes, (void*)c->stream, g_device, fits ? "" : " refused");
   if (!fits) return cudaErrorInvalidValue;

@@ -214,3 +214,18 @@ def test_the_first_products_of_several_threads(path, tmp_path):
     assert sum(s.startswith("entry point") for s in fake.log()) == 1
     for c in ctxs:
         fake.lib.ebc_destroy(c)
+
+
+def test_a_large_plans_cluster_is_one_that_fits(fake):
+    """Sixteen CTAs are more than a cluster has everywhere: where none fits, eight."""
+    for fits, cluster in ((8, "16"), (0, "8")):
+        fake.lib.fake_max_clusters(fits)
+        ctx = fake.context()
+        for tokens in (8192, 100000):
+            for id_bytes in (4, 8):
+                assert fake.plan(ctx, 64, tokens=tokens, id_bytes=id_bytes) == 0
+                assert [x["cluster"] for x in fake.launches()] == [cluster]
+        assert fake.plan(ctx, 64, tokens=512) == 0
+        assert [x["cluster"] for x in fake.launches()] == ["1"]
+        fake.lib.ebc_destroy(ctx)
+    fake.lib.fake_max_clusters(8)
