@@ -4,7 +4,8 @@ nvcc compiles each translation unit for sm_103a in parallel, then links one
 shared library with the CUDA runtime statically linked.  No torch types cross
 the C ABI, so the library is loaded with ctypes.  A second, small module
 (_build/_torch_calls-<torch version>.so, g++ against torch's headers) makes the
-expert-parallel and 4-bit calls on torch tensors; it links the first.
+expert-parallel and 4-bit calls on torch tensors; it links the first, and is
+left out where torch is not installed.
 """
 from __future__ import annotations
 
@@ -78,19 +79,24 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
                 cmd += ["-Xptxas", "-v"]
             jobs.append(cmd)
 
-    module = torch_module()
-    module_obj = module[:-3] + ".o"
-    torch_deps = [os.path.join(CSRC, TORCH_SOURCE), os.path.join(CSRC, HEADERS[-1]), os.path.abspath(__file__)]
-    compile_torch, link_torch = _torch_commands(module_obj, module + f".{os.getpid()}.tmp")
-    if force or _stale(module_obj, torch_deps):
-        jobs.append(compile_torch)
-
     def run(cmd):
         r = subprocess.run(cmd, capture_output=True, text=True)
         return cmd, r
 
+    module = None
     with ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
-        for cmd, r in ex.map(run, jobs):
+        running = [ex.submit(run, cmd) for cmd in jobs]
+        try:
+            module = torch_module()   # (imports torch, while nvcc is at work)
+        except ImportError:
+            pass
+        if module:
+            module_obj = module[:-3] + ".o"
+            torch_deps = [os.path.join(CSRC, TORCH_SOURCE), os.path.join(CSRC, HEADERS[-1]), os.path.abspath(__file__)]
+            compile_torch, link_torch = _torch_commands(module_obj, module + f".{os.getpid()}.tmp")
+            if force or _stale(module_obj, torch_deps):
+                running.append(ex.submit(run, compile_torch))
+        for cmd, r in (f.result() for f in running):
             if verbose or ptxas_info or r.returncode != 0:
                 sys.stderr.write(r.stdout + r.stderr)
             if r.returncode != 0:
@@ -104,7 +110,7 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
             sys.stderr.write(r.stdout + r.stderr)
             raise RuntimeError("nvcc link failed")
         os.replace(tmp, LIB)
-    if force or _stale(module, [module_obj]):
+    if module and (force or _stale(module, [module_obj])):
         r = subprocess.run(link_torch, capture_output=True, text=True)
         if r.returncode != 0:
             sys.stderr.write(r.stdout + r.stderr)
