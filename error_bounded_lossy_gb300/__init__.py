@@ -17,7 +17,7 @@ import threading
 
 from . import build as _build
 
-__all__ = [
+_ALL = [
     "EBC_OK", "EBC_ERR_INVALID_ARG", "EBC_ERR_CAPACITY", "EBC_ERR_CORRUPT", "EBC_ERR_DEVICE_TIMEOUT",
     "EBC_ERR_CUDA", "EBC_ERR_NO_DEVICE", "EBC_ERR_INTERNAL", "EBC_DECAY_NONE", "EBC_DECAY_LINEAR",
     "EBC_DECAY_STEPWISE", "EBC_DECAY_DROP", "EBC_DECAY_LOG", "EbcStats", "EbcError", "lib", "library_path",
@@ -33,8 +33,8 @@ __all__ = [
     "ebc_decompress_columns", "EbcConfig", "ebc_set_first_wait_polls",
     "EBC_MAX_EXPERTS", "EBC_F32", "EBC_BF16", "EBC_F16", "ebc_moe_plan", "ebc_moe_dispatch", "ebc_moe_combine",
     "ebc_moe_combine_grad", "ebc_mx4_quantize", "ebc_mx4_dequantize", "ebc_moe_dispatch_mx4", "ebc_mx4_product",
-    "Experts", "Plan", "Mx4",
 ]
+_ON_TORCH = ["Experts", "Plan", "Mx4"]   # need torch and the compiled calls
 
 EBC_OK, EBC_ERR_INVALID_ARG, EBC_ERR_CAPACITY, EBC_ERR_CORRUPT = 0, 1, 2, 3
 EBC_ERR_DEVICE_TIMEOUT, EBC_ERR_CUDA, EBC_ERR_NO_DEVICE, EBC_ERR_INTERNAL = 4, 5, 6, 7
@@ -380,7 +380,13 @@ def _f32_host(arr, T):
 
 def __getattr__(name):
     # the operators on torch tensors; torch is imported with them, not with the package
-    if name in ("Experts", "Plan", "Mx4"):
+    if name == "__all__":   # of `import *`: what can be had here
+        try:
+            from . import experts  # noqa: F401
+        except (ImportError, OSError, RuntimeError):
+            return _ALL
+        return _ALL + _ON_TORCH
+    if name in _ON_TORCH:
         from . import experts
         globals()[name] = found = getattr(experts, name)
         return found

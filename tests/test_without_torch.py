@@ -34,3 +34,40 @@ ebc.lib()
 assert ebc.ebc_version() == 1
 assert ebc.ebc_moe_plan(None, None, 4, 0, 1, 1, None, None, None, None) == ebc.EBC_ERR_INVALID_ARG
 """)
+
+
+def test_everything_else_is_imported_by_star():
+    run(BLOCK + """
+from error_bounded_lossy_gb300 import *
+assert Codec and ebc_compress and EBC_OK == 0
+try:
+    Experts
+except NameError:
+    pass
+else:
+    raise AssertionError
+""")
+
+
+def test_everything_is_imported_by_star_where_torch_is():
+    run("""
+from error_bounded_lossy_gb300 import *
+import error_bounded_lossy_gb300 as ebc
+assert Codec and Experts is ebc.Experts and Plan is ebc.Plan and Mx4 is ebc.Mx4
+""")
+
+
+def test_everything_else_is_imported_by_star_where_the_calls_are_not_compiled():
+    run("""
+from error_bounded_lossy_gb300 import build
+build.torch_module = lambda: "/nowhere/calls.so"
+from error_bounded_lossy_gb300 import *
+assert Codec and "Experts" not in globals()
+import error_bounded_lossy_gb300 as ebc
+try:
+    ebc.Experts
+except RuntimeError as e:
+    assert "not built" in str(e)
+else:
+    raise AssertionError
+""")
