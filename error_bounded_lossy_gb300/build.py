@@ -3,7 +3,7 @@
 nvcc compiles each translation unit for sm_103a in parallel, then links one
 shared library with the CUDA runtime statically linked.  No torch types cross
 the C ABI, so the library is loaded with ctypes.  A second, small module
-(_build/_torch_calls-<torch version>.so, g++ against torch's headers) makes the
+(_build/_torch_calls-<torch version>-<python ABI>.so, g++ against torch's headers) makes the
 expert-parallel and 4-bit calls on torch tensors; it links the first, and is
 left out where torch is not installed.
 """
@@ -39,9 +39,9 @@ def nvcc() -> str:
 
 
 def torch_module() -> str:
-    """The path of the torch module, one for each torch it may be built against."""
+    """The path of the torch module, one for each torch and Python it may be built against."""
     import torch
-    return os.path.join(BUILD, f"_torch_calls-{torch.__version__}.so")
+    return os.path.join(BUILD, f"_torch_calls-{torch.__version__}-{sysconfig.get_config_var('SOABI')}.so")
 
 
 def _torch_commands(obj: str, out: str):

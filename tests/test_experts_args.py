@@ -58,3 +58,13 @@ def test_kernels_that_start_early_read_with_ordinary_loads(name):
     text = open(os.path.join(ebc_build.CSRC, name)).read()
     assert "pdl_enter();" in text
     assert not re.findall(r"const\s+\w+\s*\*\s*__restrict__|__ldg|ld\.global\.nc", text)
+
+
+def test_the_compiled_calls_are_kept_apart_by_torch_and_python(monkeypatch):
+    names = {ebc_build.torch_module()}
+    monkeypatch.setattr(torch, "__version__", "0.1")
+    names.add(ebc_build.torch_module())
+    config = ebc_build.sysconfig.get_config_var
+    monkeypatch.setattr(ebc_build.sysconfig, "get_config_var", lambda k: "cpython-00-none" if k == "SOABI" else config(k))
+    names.add(ebc_build.torch_module())
+    assert len(names) == 3
