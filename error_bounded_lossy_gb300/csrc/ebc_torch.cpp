@@ -9,6 +9,7 @@
 // itself was 2), more than the kernels.
 #include <ATen/core/Tensor.h>
 #include <ATen/cuda/EmptyTensor.h>
+#include <c10/core/GradMode.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -102,6 +103,11 @@ struct Rows {
   int64_t n, width, ld;
 };
 
+// The gradients are for the reverse mode (experts.py).
+void no_tangent(const at::Tensor& t) {
+  if (t._fw_grad(0).defined()) bad("forward-mode derivatives of these calls are not defined");
+}
+
 // A float tensor [rows, width] with contiguous rows; a single row, or none,
 // has no stride of its own.
 Rows rows(const Where& w, PyObject* o) {
@@ -149,6 +155,7 @@ const float* weights_of(const Where& w, PyObject* o, const PlanRef& p) {
   const at::Tensor& t = tensor(o, what);
   if (t.scalar_type() != at::kFloat || !t.is_contiguous() || t.sizes() != p.place.sizes()) bad(what);
   w.here(t);
+  no_tangent(t);
   return (const float*)t.data_ptr();
 }
 
@@ -254,11 +261,20 @@ PyObject* py_plan(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// Whether any of the objects is a tensor whose operations are to be recorded for gradients.
+PyObject* py_recorded(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (c10::GradMode::is_enabled())
+    for (Py_ssize_t i = 0; i < n; ++i)
+      if (THPVariable_Check(a[i]) && THPVariable_Unpack(a[i]).requires_grad()) Py_RETURN_TRUE;
+  Py_RETURN_FALSE;
+}
+
 // ctx, device, x, plan (3) -> xs
 PyObject* py_dispatch(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded(n, 6, [&] {
     const Where w = where(a);
     const Rows x = rows(w, a[2]);
+    no_tangent(x.t);
     const PlanRef p = plan_here(w, a + 3);
     if (x.n != p.tokens) bad("x has not as many rows as the plan has tokens");
     at::Tensor xs = w.empty({p.n, x.width}, x.t.scalar_type());
@@ -293,6 +309,7 @@ PyObject* py_combine(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const PlanRef p = plan_here(w, a + 4);
     if (ys.n != p.n) bad("ys has not as many rows as the plan");
     const float* weights = a[3] == Py_None ? nullptr : weights_of(w, a[3], p);
+    no_tangent(ys.t);
     at::Tensor y = w.empty({p.tokens, ys.width}, ys.t.scalar_type());
     checked(ebc_moe_combine(w.ctx, ys.t.data_ptr(), ys.ld, ys.type, p.tokens, (int)p.top, ys.width, p.place_ptr(),
                             weights, y.data_ptr(), w.stream()),
@@ -310,6 +327,8 @@ PyObject* py_combine_grad(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (dy.type != ys.type || dy.n != p.tokens || ys.n != p.n || dy.width != ys.width)
       bad("dy [tokens, width] and ys [n, width] of one type do not fit the plan");
     const float* weights = weights_of(w, a[4], p);
+    no_tangent(dy.t);
+    no_tangent(ys.t);
     at::Tensor dys = w.empty({p.n, ys.width}, ys.t.scalar_type()), dw = w.empty({p.tokens, p.top}, at::kFloat);
     checked(ebc_moe_combine_grad(w.ctx, dy.t.data_ptr(), dy.ld, ys.t.data_ptr(), ys.ld, ys.type, p.tokens, (int)p.top,
                                  ys.width, p.place_ptr(), p.offsets_ptr(), (int)p.experts, weights, dys.data_ptr(),
@@ -378,6 +397,7 @@ PyObject* py_product(PyObject*, PyObject* const* a, Py_ssize_t n) {
 PyMethodDef g_methods[] = {{"set_raise", py_set_raise, METH_O, nullptr},
                            CALL(check_plan),
                            CALL(check_mx4),
+                           CALL(recorded),
                            CALL(plan),
                            CALL(dispatch),
                            CALL(dispatch_mx4),

@@ -12,6 +12,10 @@ experts' products on them (the ebc_moe_* and ebc_mx4_* calls of
 
     w = ex.quantize(weight)                    # [n_experts, outs, width] in 4.25 bits a value
     ys = ex.product(ex.dispatch_mx4(x, plan), w, plan.offsets)
+
+dispatch, dispatch_grad and combine are recorded for gradients like torch's own
+operations (combine once: its gradients have none).  Values in 4 bits, and
+products of them, have no gradient.
 """
 from __future__ import annotations
 
@@ -128,10 +132,15 @@ class Experts:
         stream's, and the inputs' memory is not reused before it has passed the call."""
         with torch.cuda.stream(stream):
             out = call(self._h, self._index, *args)
-        for t in args:
-            if isinstance(t, torch.Tensor):
-                t.record_stream(stream)
-        return out
+        return _used(out, stream, args)
+
+    def _recorded(self, stream, function, *args):
+        """The function's call, recorded for gradients; they are taken on the same stream."""
+        if stream is None:
+            return function.apply(self, *args)
+        with torch.cuda.stream(stream):
+            out = function.apply(self, *args)
+        return _used(out, stream, args)
 
     def plan(self, ids, n_experts: int, stream=None) -> Plan:
         """The plan of the router's choices ids [tokens, top] (int32 or int64;
@@ -145,6 +154,8 @@ class Experts:
 
     def dispatch(self, x, plan: Plan, stream=None):
         """x [tokens, width] to rows sorted by expert [n, width]; rows past the last are zero."""
+        if _calls.recorded(x):
+            return self._recorded(stream, _Dispatch, x, plan.rows, plan.place, plan.offsets)
         if stream is None:
             return _calls.dispatch(self._h, self._index, x, plan.rows, plan.place, plan.offsets)
         return self._on(stream, _calls.dispatch, x, plan.rows, plan.place, plan.offsets)
@@ -162,17 +173,21 @@ class Experts:
     def combine(self, ys, weights, plan: Plan, stream=None):
         """y [tokens, width]: each token's rows of ys [n, width], times weights
         (fp32 [tokens, top]; None: 1), summed in fp32."""
+        if _calls.recorded(ys, weights):
+            if weights is None:
+                return self._recorded(stream, _Sum, ys, plan.rows, plan.place, plan.offsets)
+            return self._recorded(stream, _Combine, ys, weights, plan.rows, plan.place, plan.offsets)
         if stream is None:
             return _calls.combine(self._h, self._index, ys, weights, plan.rows, plan.place, plan.offsets)
         return self._on(stream, _calls.combine, ys, weights, plan.rows, plan.place, plan.offsets)
 
     def dispatch_grad(self, dxs, plan: Plan, stream=None):
-        """The gradient of dispatch's x for the gradient dxs [n, width] of its rows."""
+        """The gradient of dispatch's x for the gradient dxs [n, width] of its rows: combine without weights."""
         return self.combine(dxs, None, plan, stream)
 
     def combine_grad(self, dy, ys, weights, plan: Plan, stream=None):
         """The gradients of combine's ys and weights for the gradient dy [tokens, width]:
-        (dys [n, width], dweights fp32 [tokens, top])."""
+        (dys [n, width], dweights fp32 [tokens, top]).  They are not recorded for gradients of their own."""
         if stream is None:
             return _calls.combine_grad(self._h, self._index, dy, ys, weights, plan.rows, plan.place, plan.offsets)
         return self._on(stream, _calls.combine_grad, dy, ys, weights, plan.rows, plan.place, plan.offsets)
@@ -230,6 +245,60 @@ class Experts:
 
 
 _new = object.__new__
+
+
+def _used(out, stream, args):
+    for t in args:
+        if isinstance(t, torch.Tensor):
+            t.record_stream(stream)
+    return out
+
+
+def _plan(saved) -> Plan:
+    p = _new(Plan)
+    p.rows, p.place, p.offsets = saved
+    return p
+
+
+# The recorded forms.  A gradient may come with any strides (that of a sum is one
+# value expanded); the calls take contiguous rows.
+class _Dispatch(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, ex, x, *plan):
+        ctx.ex = ex
+        ctx.save_for_backward(*plan)
+        return _calls.dispatch(ex._h, ex._index, x, *plan)
+
+    @staticmethod
+    def backward(ctx, dxs):
+        return None, ctx.ex.combine(dxs.contiguous(), None, _plan(ctx.saved_tensors)), None, None, None
+
+
+class _Sum(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, ex, ys, *plan):
+        ctx.ex = ex
+        ctx.save_for_backward(*plan)
+        return _calls.combine(ex._h, ex._index, ys, None, *plan)
+
+    @staticmethod
+    def backward(ctx, dy):
+        return None, ctx.ex.dispatch(dy.contiguous(), _plan(ctx.saved_tensors)), None, None, None
+
+
+class _Combine(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, ex, ys, weights, *plan):
+        ctx.ex = ex
+        ctx.save_for_backward(ys, weights, *plan)
+        return _calls.combine(ex._h, ex._index, ys, weights, *plan)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dy):
+        ys, weights, *plan = ctx.saved_tensors
+        dys, dweights = ctx.ex.combine_grad(dy.contiguous(), ys, weights, _plan(plan))
+        return None, dys, dweights, None, None, None
 
 
 def _type(dtype) -> int:
