@@ -480,7 +480,9 @@ int ebc_moe_combine_grad(ebc_ctx* ctx, const void* d_dy, int64_t ld_dy, const vo
  * value is kept as the nearest of X * {0, 1/2, 1, 3/2, 2, 3, 4, 6} and its
  * sign, ties to the even code, in 4 bits (sign, 2 exponent bits, 1 fraction
  * bit).  No value saturates, so |x - xhat| <= X/4 for |x| <= 2X, X/2 for
- * |x| <= 4X, and X always.  (The open microscaling formats' MXFP4 elements and
+ * |x| <= 4X, and X always, for |x| < 3.5 * 2^126 (2.97e38): the nearest value
+ * of a larger one is 2^128, which a product takes as such and which reads back
+ * as infinity.  (The open microscaling formats' MXFP4 elements and
  * scales; their suggested scale rule, which takes e one lower for max |x| in
  * (6 X, 8 X), would break the bound.)  A block that holds a NaN or an infinity
  * gets the byte 255 and reads back as NaN.
@@ -498,8 +500,9 @@ int ebc_mx4_quantize(ebc_ctx* ctx, const void* d_x, int64_t ld_x, int type, int6
                      uint8_t* d_codes, uint8_t* d_scales, void* stream);
 
 /* The values of d_codes and d_scales as `type`, into d_xhat[rows][width]
- * (exact in fp32 and bf16; rounded to nearest in fp16, whose range is
- * smaller). */
+ * (exact in fp32 and bf16 but for 2^128, which is infinity there; rounded to
+ * nearest in fp16, whose range is smaller: a value of 65,536 and more is
+ * infinity, which of rows that were fp16 those from 57,344 on are). */
 int ebc_mx4_dequantize(ebc_ctx* ctx, const uint8_t* d_codes, const uint8_t* d_scales, int64_t rows, int64_t width,
                        int type, void* d_xhat, void* stream);
 

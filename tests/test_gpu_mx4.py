@@ -110,6 +110,26 @@ def test_the_error_bound(ex, dtype):
     assert bool((off <= unit * torch.where(v <= 2, 0.25, torch.where(v <= 4, 0.5, 1.0))).all())
 
 
+def test_the_top_of_the_range(ex):
+    """The bound holds up to the value whose nearest is the first past fp32's range, and the products take that one as
+    what it stands for."""
+    edge = np.float32(3.5 * 2.0 ** 126)
+    below = np.nextafter(edge, np.float32(0))
+    x = torch.zeros(4, 32, device="cuda")
+    x[:, 5] = torch.tensor([below, -below, edge, torch.finfo(torch.float32).max], device="cuda")
+    q = ex.quantize(x)
+    assert q.scales[:, 0].tolist() == [253] * 4
+    for dtype in (torch.float32, torch.bfloat16):
+        back = ex.dequantize(q, dtype)[:, 5].double().cpu()
+        assert back.tolist() == [3 * 2.0 ** 126, -3 * 2.0 ** 126, np.inf, np.inf]
+    assert abs(3 * 2.0 ** 126 - float(below)) <= 2.0 ** 126
+    w = ex.quantize(torch.full((1, 32), 2.0 ** -8, device="cuda"))
+    assert ex.product(q, w, dtype=torch.float32)[:, 0].tolist() == [3 * 2.0 ** 118, -3 * 2.0 ** 118, 2.0 ** 120, 2.0 ** 120]
+    half = torch.tensor([[57312.0] + [0.0] * 31, [57344.0] + [0.0] * 31, [65504.0] + [0.0] * 31], device="cuda").half()
+    assert ex.dequantize(ex.quantize(half), torch.float16)[:, 0].tolist() == [49152.0, np.inf, np.inf]
+    assert ex.dequantize(ex.quantize(half))[:, 0].tolist() == [49152.0, 65536.0, 65536.0]
+
+
 def test_leading_shapes_strides_and_nothing(ex):
     x = torch.randn(5, 6, 96, device="cuda").to(torch.bfloat16)
     q = ex.quantize(x)
