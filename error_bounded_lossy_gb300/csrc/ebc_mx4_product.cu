@@ -48,6 +48,10 @@ struct Geom {
   static constexpr int kAccCols = kTN < 32 ? 32 : kTN;
   static constexpr int kScaleCols = 2 * (1 + kScaleB) * 4;                // tensor memory columns per stage
   static constexpr int kCols = 512;
+  // Whether clusters of CTAs may share a tile's K.  They do where the tiles are
+  // so few that twice as many would still run at once, and then the smallest
+  // tiles, which the choice of a tile's rows falls on, are at most that many.
+  static constexpr bool kShares = kTN == 16;
   static constexpr size_t kSmem = 1024 + (size_t)kStages * (kABytes + kBBytes + kScaleBytes);
   // A scale warp's next stages must not be two rounds of the ring past what it
   // knows to be given back: a barrier's phase is told by its parity alone.
@@ -496,17 +500,16 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx4_product(const __grid_consta
     if (bad && blockIdx.x == 0) record_error(a.glob, EBC_ERR_INVALID_ARG);
   }
   __syncthreads();
-  if (kCtas == 2 || a.split_log2 > 0) cluster_sync();   // the cluster's CTAs have started and set up their barriers
+  if (kCtas == 2 || (G::kShares && a.split_log2 > 0)) cluster_sync();   // the cluster's CTAs have started and set up their barriers
   tc_fence_after();
   const uint32_t tmem = s_tmem;
   const uint32_t tmem_scales = tmem + G::kAcc * G::kAccCols;
   const int out_tiles = (int)((a.outs + G::kOuts - 1) / G::kOuts);
   const int stages = (a.blocks + 7) / 8;   // stages of a tile
 
-  const int shift = kCtas == 2 ? 0 : a.split_log2, split = 1 << shift, part = (int)blockIdx.x & (split - 1);
+  const int shift = G::kShares ? a.split_log2 : 0, split = 1 << shift, part = (int)blockIdx.x & (split - 1);
   // the groups of two stages, and the stages, that are this CTA's
-  const int groups = (stages + 1) / 2, group0 = groups * (kCtas == 2 ? 0 : part) >> shift,
-            group1 = groups * (kCtas == 2 ? 1 : part + 1) >> shift;
+  const int groups = (stages + 1) / 2, group0 = groups * part >> shift, group1 = groups * (part + 1) >> shift;
   const int k0 = 2 * group0, k1 = 2 * group1 < stages ? 2 * group1 : stages;
   const Walk start(out_tiles, blockIdx.x / kCtas >> shift, gridDim.x / kCtas >> shift);
   Walk walk = start;
@@ -715,7 +718,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx4_product(const __grid_consta
       const bool mine = out + lane < a.outs;
       const uint32_t d = tmem + buf * G::kAccCols + ((uint32_t)(quarter * 32) << 16);
       const int64_t at = (int64_t)row0 * a.outs + out;
-      if (split > 1) {
+      if (G::kShares && split > 1) {
         // the sums of the CTA's share, [row][output], where the stages were
         float* sums = reinterpret_cast<float*>(base) + quarter * 32 + lane;
         for (int c0 = odd * kStoreRows; c0 < count; c0 += 2 * kStoreRows) {
@@ -777,7 +780,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx4_product(const __grid_consta
     }
     __syncthreads();
   }
-  if (split > 1) {
+  if (G::kShares && split > 1) {
     cluster_sync();   // every CTA's sums are there
     Walk tile = start;
     if (tile.at(s_begin, s_tiles, a.experts, kTN, &row0, &count)) {
@@ -853,7 +856,7 @@ cudaError_t product_t(const CallView& v, const uint8_t* xc, const uint8_t* wc, i
   // 16384 takes 17.3 us in 8 CTAs and 8.2 in 64.
   int split = 1;
   a.split_log2 = 0;
-  if (kCtas == 1)
+  if (G::kShares)
     while (split < 8 && most * split * 2 <= v.nsm - 8 * (split * 2 - 1) && split * 2 <= (a.blocks + 15) / 16) {
       split *= 2;
       ++a.split_log2;

@@ -3,6 +3,7 @@ objects linked with a CUDA runtime without a device (fake_cudart.cpp), which
 writes down the calls that reach it."""
 import ctypes
 import os
+import random
 import re
 import shutil
 import subprocess
@@ -229,3 +230,18 @@ def test_a_large_plans_cluster_is_one_that_fits(fake):
         assert [x["cluster"] for x in fake.launches()] == ["1"]
         fake.lib.ebc_destroy(ctx)
     fake.lib.fake_max_clusters(8)
+
+
+def test_only_the_smallest_tiles_share_their_sums(fake):
+    """The kernels of larger tiles have no code for it."""
+    ctx = fake.context()
+    rng = random.Random(0)
+    shared = 0
+    for _ in range(4000):
+        rows, experts = int(2 ** rng.uniform(0, 14)), int(2 ** rng.uniform(0, 8))
+        outs, width = int(2 ** rng.uniform(0, 14)), int(2 ** rng.uniform(0, 15))
+        tile, ctas, cluster = fake.product(ctx, rows, experts, outs, width)
+        assert cluster == ctas or tile == 16, (rows, experts, outs, width)
+        shared += cluster > ctas
+    assert shared > 200
+    fake.lib.ebc_destroy(ctx)
