@@ -24,6 +24,7 @@ constexpr int kScaleTile = 512;    // bytes of the scales of 128 rows x 4 blocks
 // three warps a scheduler, so that a storing thread can hold its share of a
 // tile (64 words) in its 168 registers
 constexpr int kThreads = 384;
+// (in a pair's second CTA, which does not multiply, warp 1 announces the scales)
 constexpr int kScaleWarp0 = 2, kScaleWarps = 2;
 constexpr int kStoreWarp0 = 4, kStoreWarps = 8;
 constexpr int kStoreRows = 16;     // rows that a storing warp reads at a time
@@ -41,9 +42,16 @@ struct Geom {
   static constexpr int kABytes = kM * kRowBytes;
   static constexpr int kBBytes = kBRows * kRowBytes;
   static constexpr int kScaleBytes = 2 * (1 + kScaleB) * kScaleTile;      // per stage: 8 blocks a row
-  // (more stages were slower: 256 rows a tile with 5 / 6, 299 / 309 us of 8192 x
-  // 8192; 16 rows with 5 / 6 / 8 / 10, 12.9 / 12.6 / 13.1 / 13.5 us of a decode step)
+  // (256 rows a tile with 4 / 5 stages of codes: 329 / 320 us of 8192 x 8192, and
+  // more do not fit; 16 rows with 5 / 6 / 8 / 10: 12.9 / 12.6 / 13.1 / 13.5 us of a
+  // decode step)
   static constexpr int kStages = kTN == 256 ? 5 : kTN == 64 ? 7 : 6;
+  // A pair's scales have a ring of their own, a longer one: the second CTA's are
+  // known to the first only some 3600 cycles after they were laid out (see
+  // below).  The barriers on which stages are given back are as many, so that one
+  // instruction a stage gives back both.  8192 x 8192: 5 / 6 / 7 / 8 / 10 / 12 /
+  // 14 / 16 stages 483 / 426 / 396 / 360 / 342 / 328 / 325 / 322 us.
+  static constexpr int kScaleStages = kCtas == 2 ? 16 : kStages;
   static constexpr int kAcc = kTN == 256 ? 1 : 2;                         // accumulators
   static constexpr int kAccCols = kTN < 32 ? 32 : kTN;
   static constexpr int kScaleCols = 2 * (1 + kScaleB) * 4;                // tensor memory columns per stage
@@ -52,10 +60,11 @@ struct Geom {
   // so few that twice as many would still run at once, and then the smallest
   // tiles, which the choice of a tile's rows falls on, are at most that many.
   static constexpr bool kShares = kTN == 16;
-  static constexpr size_t kSmem = 1024 + (size_t)kStages * (kABytes + kBBytes + kScaleBytes);
+  static constexpr size_t kSmem =
+      1024 + (size_t)kStages * (kABytes + kBBytes) + (size_t)kScaleStages * kScaleBytes;
   // A scale warp's next stages must not be two rounds of the ring past what it
   // knows to be given back: a barrier's phase is told by its parity alone.
-  static_assert(2 * kScaleWarps <= kStages + 1, "scale warps");
+  static_assert(2 * kScaleWarps <= kScaleStages + 1, "scale warps");
   static_assert(kAcc * kAccCols + kStages * kScaleCols <= kCols, "tensor memory");
   static_assert(kSmem <= 217 * 1024, "shared memory");
 };
@@ -78,10 +87,8 @@ __device__ __forceinline__ uint32_t in_first(const void* p) {
   if constexpr (kCtas == 2) asm volatile("mapa.shared::cluster.u32 %0, %0, 0;" : "+r"(r));
   return r;
 }
-// An arrival at such a barrier.  What it announces has been handed to the async
-// proxy of the thread's own SM (fence.proxy.async) or to nobody (a stage or an
-// accumulator given back), so it needs no release of the thread's memory to the
-// cluster: that, a round trip to L2, took 1250 cycles a stage.
+// An arrival at such a barrier that announces no memory of another CTA: this
+// CTA's, or none (an accumulator given back).
 template <int kCtas>
 __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
   if constexpr (kCtas == 2)
@@ -89,23 +96,51 @@ __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
   else
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
+// An arrival at a barrier of the pair's first CTA that makes this CTA's memory
+// known to who waits there: a round trip to L2, 1200 cycles and more.  After it a
+// relaxed one is enough, for who waits for both in that order.
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void mbar_arrive_after(uint32_t bar) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+// kCtas = 2: what the pair's other CTA has announced is known after the wait, too
+template <int kCtas = 1>
 __device__ __forceinline__ bool mbar_try_wait(uint64_t* bar, uint32_t parity) {
   uint32_t ok;
-  asm volatile(
-      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
-      : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(parity)
-      : "memory");
+  if constexpr (kCtas == 2)
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
+        " selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+  else
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
   return ok != 0u;
 }
 // whether the phase is over now: does not wait
+template <int kCtas = 1>
 __device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
   uint32_t ok;
-  asm volatile(
-      "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
-      : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(parity)
-      : "memory");
+  if constexpr (kCtas == 2)
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
+        " selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+  else
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
   return ok != 0u;
 }
 // a box into this CTA's shared memory; its bytes are counted at `bar`, which
@@ -275,12 +310,13 @@ struct Args {
 // thread of the cluster did.  The first to give up records the time-out and
 // tells the cluster's CTAs (which all stay until the last has ended).
 constexpr long long kWaitCycles = 1ll << 32;   // about two seconds
+template <int kCtas = 1>
 __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile int* abort, Glob* glob,
                                      int limit = kWaitLimit) {
-  if (limit > 0 && mbar_try_wait(bar, parity)) return true;
+  if (limit > 0 && mbar_try_wait<kCtas>(bar, parity)) return true;
   const long long begin = clock64();
   for (int i = 1; i < limit && clock64() - begin < kWaitCycles; ++i) {
-    if (mbar_try_wait(bar, parity)) return true;
+    if (mbar_try_wait<kCtas>(bar, parity)) return true;
     if (*abort) return false;
   }
   record_error(glob, EBC_ERR_DEVICE_TIMEOUT);
@@ -403,7 +439,8 @@ __device__ __forceinline__ void store_full(uint32_t taddr, float* y, int64_t ld,
 //               are one 4-byte store.  Rows and blocks past the end get 1.
 //   warp 1      copies a stage's scales to tensor memory and issues its matrix
 //               instructions; each stage has its own scale columns, so they
-//               are written again only after the stage was given back
+//               are written again only after the stage was given back; in a
+//               pair's second CTA it announces that CTA's scales to the first
 //   warps 4-11  read the accumulator, round once, to the type that the caller
 //               asked for, and store
 // The N of the instructions is the tile's row count rounded up to 16, so a
@@ -418,9 +455,9 @@ __device__ __forceinline__ void store_full(uint32_t taddr, float* y, int64_t ld,
 // pair's copies are counted together, at the first CTA's barriers, so there the
 // loading warps first bring each other to the same stage.
 // 17/32 of a byte is read a value of rows and weights, and outs * rows results
-// are written; one expert, 16384 rows x 8192 x 8192: 299 us (7.4 PFLOP/s), where
-// a pair's stage takes 521 cycles to 512 of its instructions; 32 experts of 4096
-// x 4096: 115 us (4.8 PFLOP/s), a quarter of it the accumulator's reading, which
+// are written; one expert, 16384 rows x 8192 x 8192: 320 us (6.9 PFLOP/s), where
+// a pair's stage takes 550 cycles to 512 of its instructions; 32 experts of 4096
+// x 4096: 120 us (4.6 PFLOP/s), a quarter of it the accumulator's reading, which
 // the next tile's instructions wait for; one turn of small tiles: 7 to 9 us of
 // latency, from the first stage's arrival to the last result's store.
 template <int kTN, int kCtas>
@@ -428,7 +465,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx4_product(const __grid_consta
                                                              const __grid_constant__ CUtensorMap xmap, Args a) {
   using G = Geom<kTN, kCtas>;
   extern __shared__ uint8_t raw[];
-  __shared__ uint64_t full[G::kStages], scaled[G::kStages], empty[G::kStages];
+  __shared__ uint64_t full[G::kStages], scaled[G::kScaleStages], empty[G::kScaleStages];
+  __shared__ uint64_t laid[G::kScaleStages];   // of a pair's second CTA: scales laid out, not yet announced
   __shared__ uint64_t acc_full[G::kAcc], acc_empty[G::kAcc], drained;
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
@@ -443,9 +481,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx4_product(const __grid_consta
   uint8_t* sS = sB + G::kStages * G::kBBytes;
 
   if (w == 0 && lane == 0) {
-    for (int i = 0; i < G::kStages; ++i) {
-      mbar_init(&full[i], 1);
+    for (int i = 0; i < G::kStages; ++i) mbar_init(&full[i], 1);
+    for (int i = 0; i < G::kScaleStages; ++i) {
       mbar_init(&scaled[i], kCtas);
+      mbar_init(&laid[i], 1);
       mbar_init(&empty[i], 1);
     }
     for (int i = 0; i < G::kAcc; ++i) {
@@ -516,8 +555,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx4_product(const __grid_consta
   int row0, count;
   uint32_t issued = 0;   // stages that warp 0 has asked for
   if (w == 0) {
-    int s = 0;
-    uint32_t phase = 1;   // of the barriers that stages are given back on
+    int s = 0, back = G::kScaleStages - G::kStages;   // the barrier that a stage of kStages before was given back on
+    uint32_t phase = 1;                               // of that barrier
     bool ok = true;
     uint32_t goal = ~0u;  // stages to ask for: all, until a wait gave up
     int limit = kCtas == 2 && rank == 0 ? a.first_wait : kWaitLimit;
@@ -527,7 +566,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx4_product(const __grid_consta
       const int boxes = (mine + G::kBox - 1) / G::kBox, brow = row0 + rank * mine;
       const int wrow = (int)(walk.e * a.outs) + walk.out * G::kOuts + rank * kM;
       for (int k = k0; k < k1 && issued < goal; ++k) {
-        if (ok) ok = __all_sync(0xffffffffu, wait(&empty[s], phase, &s_abort, a.glob, limit));
+        if (ok) ok = __all_sync(0xffffffffu, wait(&empty[back], phase, &s_abort, a.glob, limit));
         limit = kWaitLimit;
         if (!ok && goal == ~0u) {
           // A stage that the other CTA has asked for has been given back to both
@@ -551,88 +590,121 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx4_product(const __grid_consta
         }
         __syncwarp();
         ++issued;
-        if (++s == G::kStages) {
-          s = 0;
+        if (++s == G::kStages) s = 0;
+        if (++back == G::kScaleStages) {
+          back = 0;
           phase ^= 1;
         }
       }
     }
     // every stage given back: no arrival is left on its way to this CTA's barriers
-    for (uint32_t i = issued > G::kStages ? issued - G::kStages : 0; ok && i < issued; ++i)
-      ok = __all_sync(0xffffffffu, wait(&empty[i % G::kStages], (i / G::kStages) & 1, &s_abort, a.glob));
+    for (uint32_t i = issued > G::kScaleStages ? issued - G::kScaleStages : 0; ok && i < issued; ++i)
+      ok = __all_sync(0xffffffffu, wait(&empty[i % G::kScaleStages], (i / G::kScaleStages) & 1, &s_abort, a.glob));
     if (kCtas == 2 && goal == ~0u && lane == 0) tell_pair(&s_told, rank, issued);
-  } else if (w == 1) {
-    if (rank == 0) {
-      // Two stages a step with single CTAs, so that the watching, which costs as
-      // much as issuing a stage's instructions, is shared (16 rows x 32 experts x
-      // 4096 x 2048: 11.9 -> 10.7 us); one with pairs, whose instructions take
-      // longer to run.  The lanes watch the stages' codes and scales at the same
-      // time, and the next step's before this one's instructions are issued, so
-      // that a wait that is over costs nothing.
-      const uint32_t desc_a = desc_addr(smem_u32(sA)), desc_b = desc_addr(smem_u32(sB)), desc_s = desc_addr(smem_u32(sS));
-      const int full_stages = (a.blocks + 1) / 8;   // stages of four instructions
-      uint64_t* const watch = lane & 1 ? scaled : full;
-      auto after = [](int s) { return s + 1 == G::kStages ? 0 : s + 1; };
-      int s = 0, buf = 0, limit = a.first_wait;
-      uint32_t phase = 0, acc_phase = 1;
-      bool ok = true, ready = false;
-      for (; ok && walk.at(s_begin, s_tiles, a.experts, kTN, &row0, &count); walk.next(out_tiles)) {
-        const int n = (count + G::kRound - 1) / G::kRound * G::kRound;
-        const uint32_t id0 = instr_desc(G::kOuts, n, 0), id2 = instr_desc(G::kOuts, n, 2);
-        ok = __all_sync(0xffffffffu, wait(&acc_empty[buf], acc_phase, &s_abort, a.glob));
-        if (!ok) break;
+  } else if (w == 1 && rank == 0) {
+    // Two stages a step with single CTAs, so that the watching, which costs as
+    // much as issuing a stage's instructions, is shared (16 rows x 32 experts x
+    // 4096 x 2048: 11.9 -> 10.7 us); one with pairs, whose instructions take
+    // longer to run.  The lanes watch the stages' codes and scales at the same
+    // time, and the next step's before this one's instructions are issued, so
+    // that a wait that is over costs nothing.
+    const uint32_t desc_a = desc_addr(smem_u32(sA)), desc_b = desc_addr(smem_u32(sB)), desc_s = desc_addr(smem_u32(sS));
+    const int full_stages = (a.blocks + 1) / 8;   // stages of four instructions
+    uint64_t* const watch = lane & 1 ? scaled : full;
+    const bool scales = kCtas == 2 && (lane & 1);   // the lane watches another ring
+    auto after = [](int s) { return s + 1 == G::kStages ? 0 : s + 1; };
+    auto after_r = [](int r) { return r + 1 == G::kScaleStages ? 0 : r + 1; };
+    int s = 0, r = 0, buf = 0, limit = a.first_wait;   // r: a pair's place in the scales' ring
+    uint32_t phase = 0, phase_r = 0, acc_phase = 1;
+    bool ok = true, ready = false;
+    for (; ok && walk.at(s_begin, s_tiles, a.experts, kTN, &row0, &count); walk.next(out_tiles)) {
+      const int n = (count + G::kRound - 1) / G::kRound * G::kRound;
+      const uint32_t id0 = instr_desc(G::kOuts, n, 0), id2 = instr_desc(G::kOuts, n, 2);
+      ok = __all_sync(0xffffffffu, wait(&acc_empty[buf], acc_phase, &s_abort, a.glob));
+      if (!ok) break;
+      tc_fence_after();
+      const uint32_t d = tmem + buf * G::kAccCols;
+      // a stage's scales to its columns, then its instructions (by one thread)
+      auto multiply = [&](int s, int r, int k) {
+        const uint32_t ta = tmem_scales + s * G::kScaleCols, tb = ta + 8;
+        const uint64_t ds = kScaleDesc + (desc_s + (kCtas == 2 ? r : s) * (G::kScaleBytes >> 4));
+        const uint64_t da = kOperandDesc + (desc_a + s * (G::kABytes >> 4));
+        const uint64_t db = kOperandDesc + (desc_b + s * (G::kBBytes >> 4));
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          tc_copy_scales<kCtas>(ta + 4 * q, ds + q * (kScaleTile >> 4));
+#pragma unroll
+          for (int j = 0; j < G::kScaleB; ++j)
+            tc_copy_scales<kCtas>(tb + 4 * (q * G::kScaleB + j), ds + (2 + q * G::kScaleB + j) * (kScaleTile >> 4));
+        }
+        const int left = k < full_stages ? 8 : a.blocks - k * 8;   // scale blocks from here on
+        tc_mma<kCtas>(d, da, db, id0, ta, tb, k > k0);
+#pragma unroll
+        for (int q = 1; q < 4; ++q)
+          if (2 * q < left)
+            tc_mma<kCtas>(d, da + 2 * q, db + 2 * q, q & 1 ? id2 : id0, ta + 4 * (q >> 1),
+                          tb + 4 * G::kScaleB * (q >> 1), 1);
+        tc_commit<kCtas>(&empty[kCtas == 2 ? r : s]);
+      };
+      for (int k = k0; k < k1;) {
+        const bool two = kCtas == 1 && k + 1 < k1;
+        const int s1 = after(s), r1 = after_r(r);
+        const uint32_t phase1 = phase ^ (s1 == 0), phase_r1 = phase_r ^ (r1 == 0);
+        if (!ready) {
+          const bool second = two && (lane & 2);
+          ok = __all_sync(0xffffffffu,
+                          wait<kCtas>(&watch[scales ? r : second ? s1 : s], scales ? phase_r : second ? phase1 : phase,
+                                      &s_abort, a.glob, limit));
+          if (!ok) break;
+        }
+        limit = kWaitLimit;
         tc_fence_after();
-        const uint32_t d = tmem + buf * G::kAccCols;
-        // a stage's scales to its columns, then its instructions (by one thread)
-        auto multiply = [&](int s, int k) {
-          const uint32_t ta = tmem_scales + s * G::kScaleCols, tb = ta + 8;
-          const uint64_t ds = kScaleDesc + (desc_s + s * (G::kScaleBytes >> 4));
-          const uint64_t da = kOperandDesc + (desc_a + s * (G::kABytes >> 4));
-          const uint64_t db = kOperandDesc + (desc_b + s * (G::kBBytes >> 4));
-#pragma unroll
-          for (int q = 0; q < 2; ++q) {
-            tc_copy_scales<kCtas>(ta + 4 * q, ds + q * (kScaleTile >> 4));
-#pragma unroll
-            for (int j = 0; j < G::kScaleB; ++j)
-              tc_copy_scales<kCtas>(tb + 4 * (q * G::kScaleB + j), ds + (2 + q * G::kScaleB + j) * (kScaleTile >> 4));
-          }
-          const int left = k < full_stages ? 8 : a.blocks - k * 8;   // scale blocks from here on
-          tc_mma<kCtas>(d, da, db, id0, ta, tb, k > k0);
-#pragma unroll
-          for (int q = 1; q < 4; ++q)
-            if (2 * q < left)
-              tc_mma<kCtas>(d, da + 2 * q, db + 2 * q, q & 1 ? id2 : id0, ta + 4 * (q >> 1),
-                            tb + 4 * G::kScaleB * (q >> 1), 1);
-          tc_commit<kCtas>(&empty[s]);
-        };
-        for (int k = k0; k < k1;) {
-          const bool two = kCtas == 1 && k + 1 < k1;
-          const int s1 = after(s);
-          const uint32_t phase1 = phase ^ (s1 == 0);
-          if (!ready) {
-            const bool second = two && (lane & 2);
-            ok = __all_sync(0xffffffffu, wait(&watch[second ? s1 : s], second ? phase1 : phase, &s_abort, a.glob, limit));
-            if (!ok) break;
-          }
-          limit = kWaitLimit;
-          tc_fence_after();
-          const int s2 = two ? after(s1) : s1, s3 = after(s2);
-          const uint32_t phase2 = two ? phase1 ^ (s2 == 0) : phase1, phase3 = phase2 ^ (s3 == 0);
-          const bool over = mbar_test(&watch[lane & 2 ? s3 : s2], lane & 2 ? phase3 : phase2);
-          if (elect_one()) {
-            multiply(s, k);
-            if (two) multiply(s1, k + 1);
-            if (k + 1 + two >= k1) tc_commit<kCtas>(&acc_full[buf]);
-          }
-          ready = __all_sync(0xffffffffu, over);
-          k += 1 + two;
-          s = s2;
-          phase = phase2;
+        const int s2 = two ? after(s1) : s1, s3 = after(s2);
+        const uint32_t phase2 = two ? phase1 ^ (s2 == 0) : phase1, phase3 = phase2 ^ (s3 == 0);
+        const int next = kCtas == 2 ? (scales ? r1 : s1) : lane & 2 ? s3 : s2;
+        const uint32_t next_phase = kCtas == 2 ? (scales ? phase_r1 : phase1) : lane & 2 ? phase3 : phase2;
+        const bool over = mbar_test<kCtas>(&watch[next], next_phase);
+        if (elect_one()) {
+          multiply(s, r, k);
+          if (two) multiply(s1, 0, k + 1);
+          if (k + 1 + two >= k1) tc_commit<kCtas>(&acc_full[buf]);
         }
-        if (++buf == G::kAcc) {
-          buf = 0;
-          acc_phase ^= 1;
+        ready = __all_sync(0xffffffffu, over);
+        k += 1 + two;
+        s = s2;
+        phase = phase2;
+        r = r1;
+        phase_r = phase_r1;
+      }
+      if (++buf == G::kAcc) {
+        buf = 0;
+        acc_phase ^= 1;
+      }
+    }
+  } else if (w == 1) {
+    // A pair's second CTA: announces to the first the stages whose scales are
+    // laid out, as many as there are at a time.  What the scale warps stored is
+    // ordinary memory of this CTA: to be known in the other it has to be released
+    // to the cluster, and a warp of its own does that, so that the next scales
+    // are read and laid out meanwhile.  (Released by the scale warps, 8192 x 8192
+    // takes 457 us, by three of them 352; single CTAs without any of this 484.)
+    uint32_t n = 0;   // stages announced
+    bool ok = true;
+    for (; ok && walk.at(s_begin, s_tiles, a.experts, kTN, &row0, &count); walk.next(out_tiles)) {
+      for (int left = k1 - k0; left > 0;) {
+        ok = __all_sync(0xffffffffu, wait(&laid[n % G::kScaleStages], (n / G::kScaleStages) & 1, &s_abort, a.glob));
+        if (!ok) break;
+        int more = 1;
+        while (more < left && more < G::kScaleStages &&
+               __all_sync(0xffffffffu, mbar_test(&laid[(n + more) % G::kScaleStages], ((n + more) / G::kScaleStages) & 1)))
+          ++more;
+        if (lane == 0) {
+          mbar_arrive_cluster(in_first<kCtas>(&scaled[n % G::kScaleStages]));
+          for (int i = 1; i < more; ++i) mbar_arrive_after(in_first<kCtas>(&scaled[(n + i) % G::kScaleStages]));
         }
+        __syncwarp();
+        n += more;
+        left -= more;
       }
     }
   } else if (w < kStoreWarp0) {
@@ -687,8 +759,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx4_product(const __grid_consta
         for (int half = 0; half < 2; ++half) {
           if (2 * at + half >= stages) break;
           const uint32_t n = before + 2 * g + half;
-          const int s = n % G::kStages;
-          ok = __all_sync(0xffffffffu, wait(&empty[s], ((n / G::kStages) & 1) ^ 1, &s_abort, a.glob));
+          const int s = n % G::kScaleStages;
+          ok = __all_sync(0xffffffffu, wait(&empty[s], ((n / G::kScaleStages) & 1) ^ 1, &s_abort, a.glob));
           if (!ok) break;
           uint8_t* sc = sS + s * G::kScaleBytes + lane * 16;
 #pragma unroll
@@ -700,7 +772,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx4_product(const __grid_consta
                              word[i][3][2 * half + q]);
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           __syncwarp();
-          if (lane == 0) mbar_arrive<kCtas>(in_first<kCtas>(&scaled[s]));
+          if (lane == 0) mbar_arrive<1>(smem_u32(rank == 1 ? &laid[s] : &scaled[s]));
         }
       }
       turn = g - (group1 - group0);
@@ -870,14 +942,14 @@ cudaError_t product_t(const CallView& v, const uint8_t* xc, const uint8_t* wc, i
 // The rows of a tile: what takes the fewest cycles, and the smaller of two that
 // take as many.  Cycles are turns of the machine times a tile's: 450 a stage
 // with single CTAs whatever the rows (the instructions take that to issue, less
-// to run) and 520 with pairs, and about 2000 a tile for the results with single
+// to run) and 550 with pairs, and about 2000 a tile for the results with single
 // CTAs, 3800 with pairs, which have one accumulator.
 // us with 16 / 32 / 64 / 128 / 256 rows a tile (the chosen one in brackets):
-//      16 rows x 32 experts x 4096 x 2048   [11.2] 11.4  14.5  15.3   14.6
-//     256 rows x  1 expert  x 4096 x 4096    18.5  11.9  [8.9] 10.0   12.0
-//    2048 rows x 32 experts x 2048 x 2048    38    25    17.2 [15.7]  19.4
-//    2228 rows x  5 experts x 2541 x  192    15.7  10.9   9.3  [9.4]  11.2
-//   16384 rows x 32 experts x 4096 x 4096   805   425   222   155   [118]
+//      16 rows x 32 experts x 4096 x 2048   [10.4] 10.6  12.4  12.7   15.3
+//     256 rows x  1 expert  x 4096 x 4096    18.9  11.7  [8.2]  9.2   13.5
+//    2048 rows x 32 experts x 2048 x 2048    39.5  25.8  19.0 [15.4]  19.8
+//    2228 rows x  5 experts x 2541 x  192    14.9  10.3   8.3  [8.8]  11.7
+//   16384 rows x 32 experts x 4096 x 4096   841   463   240   155   [120]
 int tile_rows(int64_t rows, int64_t outs, int64_t stages, int experts, int nsm) {
   const int64_t active = experts < rows ? experts : rows;
   int best = 16;
@@ -888,7 +960,7 @@ int tile_rows(int64_t rows, int64_t outs, int64_t stages, int experts, int nsm) 
     // each expert's last run is half full on average, and a run at least
     const int64_t runs = rows / tn + active / 2 > active ? rows / tn + active / 2 : active;
     const int64_t turns = (runs * ((outs + wide - 1) / wide) + units - 1) / units;
-    const int64_t cycles = turns * (pair ? 520 * stages + 3800 : 450 * stages + 2000);
+    const int64_t cycles = turns * (pair ? 550 * stages + 3800 : 450 * stages + 2000);
     if (cycles < least) {
       least = cycles;
       best = tn;
