@@ -153,7 +153,8 @@ class Experts:
         return p
 
     def dispatch(self, x, plan: Plan, stream=None):
-        """x [tokens, width] to rows sorted by expert [n, width]; rows past the last are zero."""
+        """x [tokens, width] to rows sorted by expert [n, width]; rows past the last are zero.  Copies bits: 4-bit
+        rows of several senders are sorted as fp32 views of their codes and scales, with a plan of one choice a row."""
         if _calls.recorded(x):
             return self._recorded(stream, _Dispatch, x, plan.rows, plan.place, plan.offsets)
         if stream is None:
@@ -219,7 +220,8 @@ class Experts:
         """ys [rows, outs]: each row of x [rows, width] times the weights of its
         expert, w [n_experts, outs, width]; expert e has the rows offsets[e] to
         offsets[e + 1], and other rows are zero.  Without offsets, w [outs, width]
-        takes every row."""
+        takes every row.  Sums are held in fp32 and rounded once, to dtype; rows that
+        combine sums up are rounded again there, which dtype=torch.float32 avoids."""
         if stream is None:
             return _calls.product(self._h, self._index, x.codes, x.scales, x.width, w.codes, w.scales, w.width,
                                   offsets, _type(dtype))

@@ -451,7 +451,10 @@ int ebc_moe_plan(ebc_ctx* ctx, const void* d_ids, int id_bytes, int64_t tokens, 
                  int32_t* d_rows, int32_t* d_place, int32_t* d_offsets, void* stream);
 
 /* d_xs[place[t, j]] = d_x[t] for every kept slot; rows from offsets[n_experts]
- * to n are zero.  d_x[tokens][width], d_xs[n][width] of `type`. */
+ * to n are zero.  d_x[tokens][width], d_xs[n][width] of `type`.  Bits are
+ * copied, so rows of anything may be given as a type of their size: the codes
+ * and scales of 4-bit rows that came from several ranks, each rank's sorted by
+ * expert, are sorted together as EBC_F32 rows with a plan of top = 1. */
 int ebc_moe_dispatch(ebc_ctx* ctx, const void* d_x, int64_t ld_x, int type, int64_t tokens, int top, int64_t width,
                      const int32_t* d_place, const int32_t* d_offsets, int n_experts, void* d_xs, void* stream);
 

@@ -113,3 +113,39 @@ def test_a_check_finds_an_error_of_an_earlier_stream_and_of_a_replay():
             e.check()
     e.check()
     e.close()
+
+
+@pytest.mark.parametrize("width", [96, 1000])
+def test_4_bit_rows_of_several_ranks_to_one_product(width):
+    """What a rank receives is one piece a sender, each sorted by expert: a plan of one choice a row sorts the pieces
+    together (dispatch copies bits, so codes and scales go through it as fp32 rows), and combine without weights
+    brings the results back into the order of arrival."""
+    ex = ebc.Experts(0)
+    ranks, experts, outs, top = 3, 8, 70, 2
+    g = torch.Generator("cuda").manual_seed(width)
+    w = ex.quantize(torch.randn(experts, outs, width, generator=g, device="cuda"))
+    pieces, ids, values = [], [], []
+    for r in range(ranks):
+        x = torch.randn(50 + r, width, generator=g, device="cuda")
+        x[3, 5] = float("inf")   # a block of NaN: the byte 255
+        plan = ex.plan(torch.randint(0, experts, (50 + r, top), generator=g, device="cuda"), experts)
+        pieces.append(ex.dispatch_mx4(x, plan))
+        ids.append(torch.repeat_interleave(torch.arange(experts, device="cuda"), plan.offsets.diff()))
+    codes, scales, e = torch.cat([q.codes for q in pieces]), torch.cat([q.scales for q in pieces]), torch.cat(ids)
+    # the receiving rank
+    plan = ex.plan(e[:, None], experts)
+    rows = lambda t: ex.dispatch(t.view(torch.float32), plan).view(torch.uint8)  # noqa: E731
+    q = ebc.Mx4(rows(codes), rows(scales), width)
+    order = torch.sort(e, stable=True).indices
+    assert torch.equal(q.codes, codes[order]) and torch.equal(q.scales, scales[order])
+    back = ex.combine(ex.product(q, w, plan.offsets, torch.float32), None, plan)
+    ex.check()
+    x64 = ex.dequantize(ebc.Mx4(codes, scales, width)).double()
+    w64 = ex.dequantize(w).double()
+    want = torch.einsum("rk,rok->ro", x64, w64[e])
+    size = torch.einsum("rk,rok->ro", x64.abs(), w64[e].abs())
+    assert torch.equal(back.isnan(), want.isnan()) and want.isnan().any()
+    off = (back.double() - want).abs().nan_to_num(nan=0.0)
+    # width exact products summed in 32 bits, one unit in the last place an addition
+    assert bool((off <= (width + 1) * 2.0 ** -23 * size.nan_to_num(nan=1.0)).all())
+    ex.close()
