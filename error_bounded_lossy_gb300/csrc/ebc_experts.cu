@@ -46,12 +46,12 @@ __device__ __forceinline__ unsigned equal_lanes(int v, int bits) {
 // Stable counting sort of the n slots by expert, in one launch of one cluster.
 //
 // The slots are split evenly among the cluster's warps, in order.  Each warp
-// counts its slots per expert (lanes of equal expert found by votes); the counts become, per warp and expert, the warp's first place
-// among the expert's slots of its CTA (a scan over the warps), which the CTAs'
-// totals (read through distributed shared memory) and a scan over the experts
-// turn into rows; then each warp walks its slots again and hands out rows.  No
-// atomics on shared counters decide an order, so the plan is the same in every
-// run.
+// counts its slots per expert (lanes of equal expert found by votes); the counts
+// become, per warp and expert, the warp's first place among the expert's slots of
+// its CTA (a scan over the warps), which the CTAs' totals (read through
+// distributed shared memory) and a scan over the experts turn into rows; then
+// each warp walks its slots again and hands out rows.  No atomics on shared
+// counters decide an order, so the plan is the same in every run.
 //
 // Bound by latency: the ids are read once where a warp's share is one batch
 // (else twice) and two ints a slot are written, far below a microsecond of
@@ -396,10 +396,10 @@ __global__ void __launch_bounds__(32 * kRowWarps) k_moe_combine_grad(
   }
 }
 
-// CTAs for `units` warps of work: one warp each up to 16 resident CTAs a SM in
-// 8 turns; the kernels loop beyond that.
+// CTAs for `units` warps of work: a warp each, up to 128 CTAs a SM (16 turns of
+// the 8 that are resident at once); the kernels loop beyond that.
 unsigned row_grid(int64_t units, int nsm) {
-  const int64_t want = (units + kRowWarps - 1) / kRowWarps, most = (int64_t)nsm * 16 * 8;
+  const int64_t want = (units + kRowWarps - 1) / kRowWarps, most = (int64_t)nsm * 8 * 16;
   return (unsigned)(want < 1 ? 1 : want < most ? want : most);
 }
 

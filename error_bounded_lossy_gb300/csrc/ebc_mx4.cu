@@ -149,8 +149,8 @@ __device__ __forceinline__ uint32_t encode8(const Eight<T>& v, uint32_t* scale) 
 // all of them in flight at once.  With kRoute each token's codes go to the
 // rows of its choices: quantized once, written `top` times, and rows past the
 // last expert's are zero.
-// 16 or 32 bits are read and 4.25 written a value: bound by bandwidth, with
-// issue close behind for 16-bit types.  [16384, 4096] bf16: 29 us (5.9 TB/s);
+// 16 or 32 bits are read and 4.25 written a value: bound by bandwidth, for 16-bit
+// types by issue as much (71% of the cycles issue, 60% of DRAM's rate).  [16384, 4096] bf16: 29 us (5.9 TB/s);
 // [8192, 3328] fp32: 22 us (5.6 TB/s).
 template <typename T, int kV, bool kRoute, int kPieces>
 __global__ void __launch_bounds__(32 * kMxWarps) k_mx4_quantize(const T* x, int64_t ld, int64_t rows,
@@ -227,7 +227,7 @@ __global__ void __launch_bounds__(32 * kMxWarps) k_mx4_quantize(const T* x, int6
 }
 
 // The way back: eight codes a lane, kPieces runs of 256 values a warp.  Bound
-// by the bandwidth of the writes: [8192, 3328] to fp32 20 us (6.1 TB/s).
+// by the bandwidth of the writes, to 16-bit types by issue more (69% to 49%): [8192, 3328] to fp32 20 us (6.1 TB/s).
 template <typename T, int kV, int kPieces>
 __global__ void __launch_bounds__(32 * kMxWarps) k_mx4_dequantize(const uint8_t* codes,
                                                                   const uint8_t* scales, int64_t rows,

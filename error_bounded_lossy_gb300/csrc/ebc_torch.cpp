@@ -63,9 +63,9 @@ at::ScalarType scalar_of(int64_t type) {
   bad("the type must be float32, bfloat16 or float16");
 }
 
-// The context's handle and device: the first two arguments of every call.
 // Several outputs of one call in one allocation, each on a 16-byte boundary:
-// an allocation costs as much as half a launch.
+// an allocation costs as much as half a launch.  (So one of them keeps the
+// memory of all.)
 struct Parts {
   at::Tensor whole;
   at::Tensor take(int64_t at, at::IntArrayRef shape, at::ScalarType type) const {
@@ -78,6 +78,7 @@ struct Parts {
 };
 int64_t pad16(int64_t n) { return (n + 15) & ~(int64_t)15; }
 
+// The context's handle and device: the first two arguments of every call.
 struct Where {
   ebc_ctx* ctx;
   c10::DeviceIndex device;
