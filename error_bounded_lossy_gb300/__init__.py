@@ -33,8 +33,11 @@ _ALL = [
     "ebc_decompress_columns", "EbcConfig", "ebc_set_first_wait_polls",
     "EBC_MAX_EXPERTS", "EBC_F32", "EBC_BF16", "EBC_F16", "ebc_moe_plan", "ebc_moe_dispatch", "ebc_moe_combine",
     "ebc_moe_combine_grad", "ebc_mx4_quantize", "ebc_mx4_dequantize", "ebc_moe_dispatch_mx4", "ebc_mx4_product",
+    "EBC_SOFTMAX", "EBC_SIGMOID", "EBC_MAX_TOP", "EBC_MAX_GROUPS", "EBC_MAX_NORM_WIDTH",
+    "ebc_mx8_quantize", "ebc_mx8_dequantize", "ebc_mx8_product", "ebc_moe_dispatch_mx", "ebc_moe_route",
+    "ebc_moe_route_grad", "ebc_norm", "ebc_norm_grad",
 ]
-_ON_TORCH = ["Experts", "Plan", "Mx4"]   # need torch and the compiled calls
+_ON_TORCH = ["Experts", "Plan", "Mx4", "Mx8"]   # need torch and the compiled calls
 
 EBC_OK, EBC_ERR_INVALID_ARG, EBC_ERR_CAPACITY, EBC_ERR_CORRUPT = 0, 1, 2, 3
 EBC_ERR_DEVICE_TIMEOUT, EBC_ERR_CUDA, EBC_ERR_NO_DEVICE, EBC_ERR_INTERNAL = 4, 5, 6, 7
@@ -43,6 +46,8 @@ EBC_MAX_CHUNKS = 256
 EBC_RADIUS, EBC_RADIUS_WIDE = 128, 512
 EBC_MAX_EXPERTS = 1024
 EBC_F32, EBC_BF16, EBC_F16 = 0, 1, 2
+EBC_SOFTMAX, EBC_SIGMOID = 0, 1
+EBC_MAX_TOP, EBC_MAX_GROUPS, EBC_MAX_NORM_WIDTH = 32, 32, 16384
 EBC_MODE_DEDUP_HUFFMAN, EBC_MODE_HUFFMAN, EBC_MODE_DEDUP_RAW, EBC_MODE_RAW = 0, 1, 2, 3
 EBC_DECAY_NONE, EBC_DECAY_LINEAR, EBC_DECAY_STEPWISE, EBC_DECAY_DROP, EBC_DECAY_LOG = 0, 1, 2, 3, 4
 DECAY = {"none": 0, "linear": 1, "stepwise": 2, "drop": 3, "log": 4}
@@ -57,6 +62,8 @@ EXPORTED_SYMBOLS = (
     "ebc_set_radius", "ebc_compress_bound_radius", "ebc_decompress_columns", "ebc_set_first_wait_polls",
     "ebc_moe_plan", "ebc_moe_dispatch", "ebc_moe_combine", "ebc_moe_combine_grad", "ebc_mx4_quantize",
     "ebc_mx4_dequantize", "ebc_moe_dispatch_mx4", "ebc_mx4_product",
+    "ebc_mx8_quantize", "ebc_mx8_dequantize", "ebc_mx8_product", "ebc_moe_dispatch_mx", "ebc_moe_route",
+    "ebc_moe_route_grad", "ebc_norm", "ebc_norm_grad",
 )
 
 
@@ -112,6 +119,7 @@ def lib():
                                    "`python -c 'import __graft_entry__ as g; g.build()'` first")
             L = ctypes.CDLL(path)
             P, I, I64, U64, D = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_uint64, ctypes.c_double
+            F = ctypes.c_float
             sig = {
                 "ebc_version": (I, []),
                 "ebc_strerror": (ctypes.c_char_p, [I]),
@@ -154,6 +162,14 @@ def lib():
                 "ebc_mx4_dequantize": (I, [P, P, P, I64, I64, I, P, P]),
                 "ebc_moe_dispatch_mx4": (I, [P, P, I64, I, I64, I, I64, P, P, I, P, P, P]),
                 "ebc_mx4_product": (I, [P, P, P, I64, I64, P, P, I64, I, P, I, P, P]),
+                "ebc_mx8_quantize": (I, [P, P, I64, I, I64, I64, P, P, P]),
+                "ebc_mx8_dequantize": (I, [P, P, P, I64, I64, I, P, P]),
+                "ebc_mx8_product": (I, [P, P, P, I64, I64, P, P, I64, I, P, I, P, P]),
+                "ebc_moe_dispatch_mx": (I, [P, P, I64, P, I64, I64, I, P, P, I, P, P, P]),
+                "ebc_moe_route": (I, [P, P, I64, I, I64, I, I, I, P, I, I, I, I, F, P, P, P]),
+                "ebc_moe_route_grad": (I, [P, P, P, I64, I, I64, I, I, P, I, I, F, P, P]),
+                "ebc_norm": (I, [P, P, I64, P, I64, I, P, I, I64, I64, F, P, P, P, P, P]),
+                "ebc_norm_grad": (I, [P, P, I64, P, I64, P, I64, I, P, I, I64, I64, F, P, P, P, P]),
             }
             for name, (res, args) in sig.items():
                 f = getattr(L, name)
@@ -324,7 +340,7 @@ def ebc_get_profile(ctx, capacity: int = 32):
     return {arr[i].name.decode(): (int(arr[i].launches), float(arr[i].total_ms)) for i in range(n.value)}
 
 
-# The expert-parallel and 4-bit calls take their arguments in the C order, as
+# The expert-parallel, 4- and 8-bit, router and norm calls take their arguments in the C order, as
 # plain ints and pointers (ctypes checks them).
 def ebc_moe_plan(*args) -> int:
     return lib().ebc_moe_plan(*args)
@@ -356,6 +372,38 @@ def ebc_moe_dispatch_mx4(*args) -> int:
 
 def ebc_mx4_product(*args) -> int:
     return lib().ebc_mx4_product(*args)
+
+
+def ebc_mx8_quantize(*args) -> int:
+    return lib().ebc_mx8_quantize(*args)
+
+
+def ebc_mx8_dequantize(*args) -> int:
+    return lib().ebc_mx8_dequantize(*args)
+
+
+def ebc_mx8_product(*args) -> int:
+    return lib().ebc_mx8_product(*args)
+
+
+def ebc_moe_dispatch_mx(*args) -> int:
+    return lib().ebc_moe_dispatch_mx(*args)
+
+
+def ebc_moe_route(*args) -> int:
+    return lib().ebc_moe_route(*args)
+
+
+def ebc_moe_route_grad(*args) -> int:
+    return lib().ebc_moe_route_grad(*args)
+
+
+def ebc_norm(*args) -> int:
+    return lib().ebc_norm(*args)
+
+
+def ebc_norm_grad(*args) -> int:
+    return lib().ebc_norm_grad(*args)
 
 
 # ---- torch-facing convenience layer (marshalling only) ----

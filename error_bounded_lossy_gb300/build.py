@@ -21,8 +21,8 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libebc_gb300.so")
 SOURCES = ["ebc_api.cu", "ebc_compress.cu", "ebc_decompress.cu", "ebc_experts.cu", "ebc_mx4.cu",
-           "ebc_mx4_product.cu"]
-HEADERS = ["ebc_internal.cuh", "ebc_types.cuh", "ebc_mx4.cuh", os.path.join("..", "..", "include", "ebc.h")]
+           "ebc_mx4_product.cu", "ebc_mx8.cu", "ebc_mx8_product.cu", "ebc_norm.cu", "ebc_route.cu"]
+HEADERS = ["ebc_internal.cuh", "ebc_types.cuh", "ebc_mx4.cuh", "ebc_mx8.cuh", "ebc_mx_product.cuh", os.path.join("..", "..", "include", "ebc.h")]
 
 TORCH_SOURCE = "ebc_torch.cpp"
 

@@ -241,6 +241,56 @@ __global__ void __launch_bounds__(32 * kRowWarps) k_moe_dispatch(const T* x, int
   }
 }
 
+// The same for rows that are codes and scales: a row is code_vecs and scale_vecs
+// vectors of 16 bytes, in two arrays.
+__global__ void __launch_bounds__(32 * kRowWarps) k_moe_dispatch_mx(const uint4* codes, int64_t code_vecs,
+                                                                    const uint4* scales, int64_t scale_vecs,
+                                                                    int64_t tokens, int top, const int32_t* place,
+                                                                    const int32_t* offsets, int E,
+                                                                    uint4* __restrict__ xs_codes,
+                                                                    uint4* __restrict__ xs_scales, Glob* glob) {
+  pdl_enter();
+  constexpr int kU = scatter_vectors<16>(), kPiece = 32 * kU;
+  const int lane = threadIdx.x & 31;
+  const int64_t n = tokens * top, vecs = code_vecs + scale_vecs, pieces = (vecs + kPiece - 1) / kPiece;
+  const int64_t live = live_rows(offsets, E, n);
+  const int64_t units = (tokens + (n - live)) * pieces;
+  for (int64_t u = (int64_t)blockIdx.x * kRowWarps + (threadIdx.x >> 5); u < units;
+       u += (int64_t)gridDim.x * kRowWarps) {
+    const int64_t t = divide(u, pieces), h0 = (u - t * pieces) * kPiece + lane;
+    uint4 v[kU];
+    auto store = [&](int64_t r) {
+#pragma unroll
+      for (int i = 0; i < kU; ++i) {
+        const int64_t h = h0 + i * 32;
+        if (h < code_vecs)
+          xs_codes[r * code_vecs + h] = v[i];
+        else if (h < vecs)
+          xs_scales[r * scale_vecs + (h - code_vecs)] = v[i];
+      }
+    };
+    if (t < tokens) {
+#pragma unroll
+      for (int i = 0; i < kU; ++i) {
+        const int64_t h = h0 + i * 32;
+        if (h < vecs) v[i] = h < code_vecs ? codes[t * code_vecs + h] : scales[t * scale_vecs + (h - code_vecs)];
+      }
+      for (int j0 = 0; j0 < top; j0 += 32) {
+        const int m = top - j0 < 32 ? top - j0 : 32;
+        const int32_t p_lane = lane < m ? read_place(place, t * top + j0 + lane, n, glob) : -1;
+        for (int j = 0; j < m; ++j) {
+          const int32_t p = __shfl_sync(0xffffffffu, p_lane, j);
+          if (p >= 0) store(p);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < kU; ++i) v[i] = make_uint4(0u, 0u, 0u, 0u);
+      store(live + (t - tokens));
+    }
+  }
+}
+
 // Vectors of V bytes a lane takes of a row at a time (1 KB of a wide row a
 // warp), and rows in flight.  Longer pieces of fewer rows suit the memory
 // better than more rows at once: 8192 tokens x 8 choices x 4096 bf16 took
@@ -511,6 +561,30 @@ int ebc_moe_dispatch(ebc_ctx* ctx, const void* d_x, int64_t ld_x, int type, int6
                         dim3(row_grid(tokens * ((width + piece - 1) / piece), v.nsm)), dim3(32 * kRowWarps), 0, 1,
                         (const T*)d_x, ld_x, tokens, top, width, d_place, d_offsets, n_experts, (T*)d_xs, v.glob);
   }));
+}
+
+int ebc_moe_dispatch_mx(ebc_ctx* ctx, const uint8_t* d_codes, int64_t code_bytes, const uint8_t* d_scales,
+                        int64_t scale_bytes, int64_t tokens, int top, const int32_t* d_place,
+                        const int32_t* d_offsets, int n_experts, uint8_t* d_xs_codes, uint8_t* d_xs_scales,
+                        void* stream) {
+  constexpr int64_t kMost = (int64_t)1 << 24;   // a row of 2^24 values of 8 bits, and more than its scales
+  if (!ctx || !routed_ok(tokens, top, n_experts) || code_bytes < 16 || code_bytes > kMost || code_bytes % 16 != 0 ||
+      scale_bytes < 16 || scale_bytes > kMost || scale_bytes % 16 != 0 || !d_offsets || !aligned(d_offsets, 4))
+    return EBC_ERR_INVALID_ARG;
+  if (tokens > 0 && (!d_codes || !aligned(d_codes, 16) || !d_scales || !aligned(d_scales, 16) || !d_place ||
+                     !aligned(d_place, 4) || !d_xs_codes || !aligned(d_xs_codes, 16) || !d_xs_scales ||
+                     !aligned(d_xs_scales, 16)))
+    return EBC_ERR_INVALID_ARG;
+  CallView v;
+  cudaStream_t st = (cudaStream_t)stream;
+  const int rc = begin_call(ctx, st, &v);
+  if (rc || tokens == 0) return rc;
+  const int64_t piece = 32 * scatter_vectors<16>(), vecs = (code_bytes + scale_bytes) / 16;
+  return cuda_code(launch_named(v, "k_moe_dispatch_mx", st, k_moe_dispatch_mx,
+                                dim3(row_grid(tokens * ((vecs + piece - 1) / piece), v.nsm)), dim3(32 * kRowWarps), 0,
+                                1, (const uint4*)d_codes, code_bytes / 16, (const uint4*)d_scales, scale_bytes / 16,
+                                tokens, top, d_place, d_offsets, n_experts, (uint4*)d_xs_codes, (uint4*)d_xs_scales,
+                                v.glob));
 }
 
 int ebc_moe_combine(ebc_ctx* ctx, const void* d_ys, int64_t ld_ys, int type, int64_t tokens, int top, int64_t width,

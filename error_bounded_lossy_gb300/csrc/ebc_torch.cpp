@@ -1,4 +1,4 @@
-// ebc_torch.cpp -- the expert-parallel and 4-bit calls on torch tensors: checks
+// ebc_torch.cpp -- the expert-parallel, 4- and 8-bit, router and norm calls on torch tensors: checks
 // of the tensors, outputs from torch's allocator on the current stream, and the
 // C calls of include/ebc.h.  A module of plain functions, called from
 // experts.py.
@@ -160,36 +160,43 @@ const float* weights_of(const Where& w, PyObject* o, const PlanRef& p) {
   return (const float*)t.data_ptr();
 }
 
-struct Mx4Ref {
+// Rows in 4 or 8 bits.
+struct MxRef {
   const at::Tensor &codes, &scales;
   int64_t width;
   const uint8_t* codes_ptr() const { return (const uint8_t*)codes.data_ptr(); }
   const uint8_t* scales_ptr() const { return (const uint8_t*)scales.data_ptr(); }
 };
 
-// codes, scales and width of rows in 4 bits.
-Mx4Ref mx4_of(PyObject* const* a) {
+int64_t code_bytes(int bits, int64_t width) {
+  return bits == 4 ? EBC_MX4_CODE_BYTES(width) : EBC_MX8_CODE_BYTES(width);
+}
+
+// codes, scales and width of such rows.
+template <int kBits>
+MxRef mx_of(PyObject* const* a) {
   const char* what = "codes and scales must be contiguous uint8 CUDA tensors";
   const at::Tensor &c = tensor(a[0], what), &s = tensor(a[1], what);
   const int64_t width = integer(a[2]), d = c.dim();
-  if (width < 1 || d < 1 || s.dim() != d || c.size(-1) != EBC_MX4_CODE_BYTES(width) ||
+  if (width < 1 || d < 1 || s.dim() != d || c.size(-1) != code_bytes(kBits, width) ||
       s.size(-1) != EBC_MX4_SCALE_BYTES(width) || c.sizes().slice(0, d - 1) != s.sizes().slice(0, d - 1))
     bad("codes and scales do not hold rows of that width");
   for (const at::Tensor* t : {&c, &s})
     if (t->scalar_type() != at::kByte || !t->is_cuda() || !t->is_contiguous()) bad(what);
-  return Mx4Ref{c, s, width};
+  return MxRef{c, s, width};
 }
 
-Mx4Ref mx4_here(const Where& w, PyObject* const* a) {
-  const Mx4Ref m = mx4_of(a);
+template <int kBits>
+MxRef mx_here(const Where& w, PyObject* const* a) {
+  const MxRef m = mx_of<kBits>(a);
   w.here(m.codes);
   w.here(m.scales);
   return m;
 }
 
 // codes and scales of n rows, one allocation
-std::pair<at::Tensor, at::Tensor> mx4_rows(const Where& w, int64_t n, int64_t width) {
-  const int64_t cb = EBC_MX4_CODE_BYTES(width), sb = EBC_MX4_SCALE_BYTES(width);
+std::pair<at::Tensor, at::Tensor> mx_rows(const Where& w, int bits, int64_t n, int64_t width) {
+  const int64_t cb = code_bytes(bits, width), sb = EBC_MX4_SCALE_BYTES(width);
   const Parts all{w.empty({n * (cb + sb)}, at::kByte)};
   return {all.take(0, {n, cb}, at::kByte), all.take(n * cb, {n, sb}, at::kByte)};
 }
@@ -231,12 +238,15 @@ PyObject* py_check_plan(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
-PyObject* py_check_mx4(PyObject*, PyObject* const* a, Py_ssize_t n) {
+template <int kBits>
+PyObject* check_mx(PyObject* const* a, Py_ssize_t n) {
   return guarded(n, 3, [&]() -> PyObject* {
-    mx4_of(a);
+    mx_of<kBits>(a);
     Py_RETURN_NONE;
   });
 }
+PyObject* py_check_mx4(PyObject*, PyObject* const* a, Py_ssize_t n) { return check_mx<4>(a, n); }
+PyObject* py_check_mx8(PyObject*, PyObject* const* a, Py_ssize_t n) { return check_mx<8>(a, n); }
 
 // ctx, device, ids, n_experts -> rows, place, offsets
 PyObject* py_plan(PyObject*, PyObject* const* a, Py_ssize_t n) {
@@ -293,7 +303,7 @@ PyObject* py_dispatch_mx4(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const Rows x = rows(w, a[2]);
     const PlanRef p = plan_here(w, a + 3);
     if (x.n != p.tokens) bad("x has not as many rows as the plan has tokens");
-    auto [c, s] = mx4_rows(w, p.n, x.width);
+    auto [c, s] = mx_rows(w, 4, p.n, x.width);
     checked(ebc_moe_dispatch_mx4(w.ctx, x.t.data_ptr(), x.ld, x.type, p.tokens, (int)p.top, x.width, p.place_ptr(),
                                  p.offsets_ptr(), (int)p.experts, (uint8_t*)c.data_ptr(), (uint8_t*)s.data_ptr(),
                                  w.stream()),
@@ -340,39 +350,48 @@ PyObject* py_combine_grad(PyObject*, PyObject* const* a, Py_ssize_t n) {
 }
 
 // ctx, device, x [rows, width] -> codes, scales
-PyObject* py_quantize(PyObject*, PyObject* const* a, Py_ssize_t n) {
+template <int kBits>
+PyObject* quantize(PyObject* const* a, Py_ssize_t n) {
   return guarded(n, 3, [&] {
     const Where w = where(a);
     const Rows x = rows(w, a[2]);
-    auto [c, s] = mx4_rows(w, x.n, x.width);
-    checked(ebc_mx4_quantize(w.ctx, x.t.data_ptr(), x.ld, x.type, x.n, x.width, (uint8_t*)c.data_ptr(),
-                             (uint8_t*)s.data_ptr(), w.stream()),
-            "ebc_mx4_quantize");
+    auto [c, s] = mx_rows(w, kBits, x.n, x.width);
+    checked((kBits == 4 ? ebc_mx4_quantize : ebc_mx8_quantize)(w.ctx, x.t.data_ptr(), x.ld, x.type, x.n, x.width,
+                                                               (uint8_t*)c.data_ptr(), (uint8_t*)s.data_ptr(),
+                                                               w.stream()),
+            kBits == 4 ? "ebc_mx4_quantize" : "ebc_mx8_quantize");
     return tuple({c, s});
   });
 }
+PyObject* py_quantize(PyObject*, PyObject* const* a, Py_ssize_t n) { return quantize<4>(a, n); }
+PyObject* py_quantize_mx8(PyObject*, PyObject* const* a, Py_ssize_t n) { return quantize<8>(a, n); }
 
 // ctx, device, codes, scales, width, type -> values
-PyObject* py_dequantize(PyObject*, PyObject* const* a, Py_ssize_t n) {
+template <int kBits>
+PyObject* dequantize(PyObject* const* a, Py_ssize_t n) {
   return guarded(n, 6, [&] {
     const Where w = where(a);
-    const Mx4Ref m = mx4_here(w, a + 2);
+    const MxRef m = mx_here<kBits>(w, a + 2);
     const int64_t type = integer(a[5]);
     at::DimVector shape(m.codes.sizes().begin(), m.codes.sizes().end());
     shape.back() = m.width;
     at::Tensor x = w.empty(shape, scalar_of(type));
-    checked(ebc_mx4_dequantize(w.ctx, m.codes_ptr(), m.scales_ptr(), x.numel() / m.width, m.width, (int)type,
-                               x.data_ptr(), w.stream()),
-            "ebc_mx4_dequantize");
+    checked((kBits == 4 ? ebc_mx4_dequantize : ebc_mx8_dequantize)(w.ctx, m.codes_ptr(), m.scales_ptr(),
+                                                                   x.numel() / m.width, m.width, (int)type,
+                                                                   x.data_ptr(), w.stream()),
+            kBits == 4 ? "ebc_mx4_dequantize" : "ebc_mx8_dequantize");
     return wrap(x);
   });
 }
+PyObject* py_dequantize(PyObject*, PyObject* const* a, Py_ssize_t n) { return dequantize<4>(a, n); }
+PyObject* py_dequantize_mx8(PyObject*, PyObject* const* a, Py_ssize_t n) { return dequantize<8>(a, n); }
 
 // ctx, device, x (3), w (3), offsets or None, type -> ys
-PyObject* py_product(PyObject*, PyObject* const* a, Py_ssize_t n) {
+template <int kBits>
+PyObject* product(PyObject* const* a, Py_ssize_t n) {
   return guarded(n, 10, [&] {
     const Where at = where(a);
-    const Mx4Ref x = mx4_here(at, a + 2), w = mx4_here(at, a + 5);
+    const MxRef x = mx_here<kBits>(at, a + 2), w = mx_here<kBits>(at, a + 5);
     const bool one = a[8] == Py_None;
     if (x.codes.dim() != 2 || w.codes.dim() != (one ? 2 : 3) || x.width != w.width)
       bad("x [rows, width] and w [n_experts, outs, width] (or [outs, width] without offsets) do not multiply");
@@ -386,11 +405,157 @@ PyObject* py_product(PyObject*, PyObject* const* a, Py_ssize_t n) {
       offsets = (const int32_t*)o.data_ptr();
     }
     at::Tensor ys = at.empty({x.codes.size(0), outs}, scalar_of(type));
-    checked(ebc_mx4_product(at.ctx, x.codes_ptr(), x.scales_ptr(), x.codes.size(0), x.width, w.codes_ptr(),
-                            w.scales_ptr(), outs, (int)std::min<int64_t>(experts, INT32_MAX), offsets, (int)type,
-                            ys.data_ptr(), at.stream()),
-            "ebc_mx4_product");
+    checked((kBits == 4 ? ebc_mx4_product : ebc_mx8_product)(
+                at.ctx, x.codes_ptr(), x.scales_ptr(), x.codes.size(0), x.width, w.codes_ptr(), w.scales_ptr(), outs,
+                (int)std::min<int64_t>(experts, INT32_MAX), offsets, (int)type, ys.data_ptr(), at.stream()),
+            kBits == 4 ? "ebc_mx4_product" : "ebc_mx8_product");
     return wrap(ys);
+  });
+}
+PyObject* py_product(PyObject*, PyObject* const* a, Py_ssize_t n) { return product<4>(a, n); }
+PyObject* py_product_mx8(PyObject*, PyObject* const* a, Py_ssize_t n) { return product<8>(a, n); }
+
+// ctx, device, codes, scales, plan (3) -> codes, scales of the sorted rows
+PyObject* py_dispatch_mx(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 7, [&] {
+    const Where w = where(a);
+    const char* what = "rows in 4 or 8 bits must be codes and scales [tokens, bytes], contiguous uint8 CUDA tensors";
+    const at::Tensor &c = tensor(a[2], what), &s = tensor(a[3], what);
+    for (const at::Tensor* t : {&c, &s}) {
+      if (t->scalar_type() != at::kByte || !t->is_cuda() || !t->is_contiguous() || t->dim() != 2) bad(what);
+      w.here(*t);
+    }
+    const PlanRef p = plan_here(w, a + 4);
+    if (c.size(0) != p.tokens || s.size(0) != p.tokens) bad("x has not as many rows as the plan has tokens");
+    const int64_t cb = c.size(1), sb = s.size(1);
+    const Parts all{w.empty({p.n * (cb + sb)}, at::kByte)};
+    at::Tensor xc = all.take(0, {p.n, cb}, at::kByte), xs = all.take(p.n * cb, {p.n, sb}, at::kByte);
+    checked(ebc_moe_dispatch_mx(w.ctx, (const uint8_t*)c.data_ptr(), cb, (const uint8_t*)s.data_ptr(), sb, p.tokens,
+                                (int)p.top, p.place_ptr(), p.offsets_ptr(), (int)p.experts, (uint8_t*)xc.data_ptr(),
+                                (uint8_t*)xs.data_ptr(), w.stream()),
+            "ebc_moe_dispatch_mx");
+    return tuple({xc, xs});
+  });
+}
+
+double real(PyObject* o) {
+  const double v = PyFloat_AsDouble(o);
+  if (v == -1.0 && PyErr_Occurred()) throw Raised{};
+  return v;
+}
+
+int small(PyObject* o) {   // an int argument of the C call, which refuses what is out of its range
+  const int64_t v = integer(o);
+  return (int)std::max<int64_t>(INT32_MIN, std::min<int64_t>(v, INT32_MAX));
+}
+
+// ctx, device, logits, top, score, bias or None, groups, keep_groups, group_top, renormalize, scale -> ids, weights
+PyObject* py_route(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 11, [&] {
+    const Where w = where(a);
+    const Rows l = rows(w, a[2]);
+    no_tangent(l.t);
+    const int top = small(a[3]);
+    const float* bias = nullptr;
+    if (a[5] != Py_None) {
+      const char* what = "bias must be a contiguous float32 CUDA tensor [n_experts]";
+      const at::Tensor& b = tensor(a[5], what);
+      if (b.scalar_type() != at::kFloat || b.dim() != 1 || b.numel() != l.width || !b.is_contiguous()) bad(what);
+      w.here(b);
+      bias = (const float*)b.data_ptr();
+    }
+    if (top < 1 || top > EBC_MAX_TOP) checked(EBC_ERR_INVALID_ARG, "ebc_moe_route");
+    at::Tensor ids = w.empty({l.n, top}, at::kInt), weights = w.empty({l.n, top}, at::kFloat);
+    checked(ebc_moe_route(w.ctx, l.t.data_ptr(), l.ld, l.type, l.n, (int)std::min<int64_t>(l.width, INT32_MAX), top,
+                          small(a[4]), bias, small(a[6]), small(a[7]), small(a[8]), PyObject_IsTrue(a[9]),
+                          (float)real(a[10]), (int32_t*)ids.data_ptr(), (float*)weights.data_ptr(), w.stream()),
+            "ebc_moe_route");
+    return tuple({ids, weights});
+  });
+}
+
+// ctx, device, dweights, logits, ids, score, renormalize, scale -> dlogits
+PyObject* py_route_grad(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 8, [&] {
+    const Where w = where(a);
+    const Rows l = rows(w, a[3]);
+    no_tangent(l.t);
+    const char* what = "dweights and ids must be contiguous float32 and int32 CUDA tensors [tokens, top]";
+    const at::Tensor &g = tensor(a[2], what), &ids = tensor(a[4], what);
+    if (g.scalar_type() != at::kFloat || ids.scalar_type() != at::kInt || g.dim() != 2 || g.size(0) != l.n ||
+        g.sizes() != ids.sizes() || !g.is_contiguous() || !ids.is_contiguous())
+      bad(what);
+    w.here(g);
+    w.here(ids);
+    no_tangent(g);
+    at::Tensor d = w.empty({l.n, l.width}, l.t.scalar_type());
+    checked(ebc_moe_route_grad(w.ctx, (const float*)g.data_ptr(), l.t.data_ptr(), l.ld, l.type, l.n,
+                               (int)std::min<int64_t>(l.width, INT32_MAX),
+                               (int)std::min<int64_t>(g.size(1), INT32_MAX), (const int32_t*)ids.data_ptr(),
+                               small(a[5]), PyObject_IsTrue(a[6]), (float)real(a[7]), d.data_ptr(), w.stream()),
+            "ebc_moe_route_grad");
+    return wrap(d);
+  });
+}
+
+// The norm's weight [width].
+const at::Tensor& gain(const Where& w, PyObject* o, int64_t width) {
+  const char* what = "weight must be a contiguous float32, bfloat16 or float16 CUDA tensor [width]";
+  const at::Tensor& t = tensor(o, what);
+  if (type_of(t) < 0 || t.dim() != 1 || t.numel() != width || !t.is_contiguous()) bad(what);
+  w.here(t);
+  no_tangent(t);
+  return t;
+}
+
+// Rows of the same shape and type as others.
+Rows rows_like(const Where& w, PyObject* o, const Rows& like) {
+  const Rows r = rows(w, o);
+  if (r.type != like.type || r.n != like.n || r.width != like.width) bad("rows of one shape and type are needed");
+  no_tangent(r.t);
+  return r;
+}
+
+// ctx, device, x, weight, residual or None, eps, whether in 8 bits, whether in x's type
+//   -> codes, scales (or None), y (or None), h (None without a residual)
+PyObject* py_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 8, [&] {
+    const Where w = where(a);
+    const Rows x = rows(w, a[2]);
+    no_tangent(x.t);
+    const at::Tensor& g = gain(w, a[3], x.width);
+    const bool more = a[4] != Py_None, mx8 = PyObject_IsTrue(a[6]), wide = PyObject_IsTrue(a[7]);
+    const Rows r = more ? rows_like(w, a[4], x) : x;
+    at::Tensor y, h, c, s;
+    if (wide) y = w.empty({x.n, x.width}, x.t.scalar_type());
+    if (more) h = w.empty({x.n, x.width}, x.t.scalar_type());
+    if (mx8) std::tie(c, s) = mx_rows(w, 8, x.n, x.width);
+    auto at_ = [](const at::Tensor& t) { return t.defined() ? t.data_ptr() : nullptr; };
+    checked(ebc_norm(w.ctx, x.t.data_ptr(), x.ld, more ? r.t.data_ptr() : nullptr, r.ld, x.type, g.data_ptr(),
+                     type_of(g), x.n, x.width, (float)real(a[5]), at_(y), at_(h), (uint8_t*)at_(c),
+                     (uint8_t*)at_(s), w.stream()),
+            "ebc_norm");
+    return tuple({c, s, y, h});   // (an undefined tensor is None)
+  });
+}
+
+// ctx, device, dy, h, weight, dh or None, eps -> dx, dweight
+PyObject* py_norm_grad(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 7, [&] {
+    const Where w = where(a);
+    const Rows dy = rows(w, a[2]);
+    no_tangent(dy.t);
+    const Rows h = rows_like(w, a[3], dy);
+    const at::Tensor& g = gain(w, a[4], dy.width);
+    const bool more = a[5] != Py_None;
+    const Rows dh = more ? rows_like(w, a[5], dy) : dy;
+    at::Tensor dx = w.empty({dy.n, dy.width}, dy.t.scalar_type()), dg = w.empty({dy.width}, g.scalar_type()),
+               scratch = w.empty({(int64_t)EBC_NORM_GRAD_SCRATCH(dy.n, dy.width)}, at::kByte);
+    checked(ebc_norm_grad(w.ctx, dy.t.data_ptr(), dy.ld, h.t.data_ptr(), h.ld, more ? dh.t.data_ptr() : nullptr,
+                          dh.ld, dy.type, g.data_ptr(), type_of(g), dy.n, dy.width, (float)real(a[6]),
+                          dx.data_ptr(), dg.data_ptr(), (float*)scratch.data_ptr(), w.stream()),
+            "ebc_norm_grad");
+    return tuple({dx, dg});
   });
 }
 
@@ -398,6 +563,7 @@ PyObject* py_product(PyObject*, PyObject* const* a, Py_ssize_t n) {
 PyMethodDef g_methods[] = {{"set_raise", py_set_raise, METH_O, nullptr},
                            CALL(check_plan),
                            CALL(check_mx4),
+                           CALL(check_mx8),
                            CALL(recorded),
                            CALL(plan),
                            CALL(dispatch),
@@ -407,6 +573,14 @@ PyMethodDef g_methods[] = {{"set_raise", py_set_raise, METH_O, nullptr},
                            CALL(quantize),
                            CALL(dequantize),
                            CALL(product),
+                           CALL(quantize_mx8),
+                           CALL(dequantize_mx8),
+                           CALL(product_mx8),
+                           CALL(dispatch_mx),
+                           CALL(route),
+                           CALL(route_grad),
+                           CALL(norm),
+                           CALL(norm_grad),
                            {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_torch_calls", nullptr, -1, g_methods};
 

@@ -1,9 +1,12 @@
-"""Expert parallelism on torch tensors: the plan of a routed batch, its rows
-sorted by expert and back with their gradients, rows in 4 bits, and the
-experts' products on them (the ebc_moe_* and ebc_mx4_* calls of
-``include/ebc.h``; marshalling only, no CPU path).
+"""Expert parallelism on torch tensors: the norm and the router ahead of the
+experts, the plan of a routed batch, its rows sorted by expert and back with
+their gradients, rows in 4 and 8 bits, and the experts' products on them (the
+ebc_norm*, ebc_moe_*, ebc_mx4_* and ebc_mx8_* calls of ``include/ebc.h``;
+marshalling only, no CPU path).
 
     ex = Experts(0)
+    y, h = ex.norm(x, gain, residual)          # h = x + residual, y its root-mean-square norm
+    ids, weights = ex.route(logits, top)       # each token's experts and weights, from its scores
     plan = ex.plan(ids, n_experts)             # ids [tokens, top]: the router's choices, negative = dropped
     xs = ex.dispatch(x, plan)                  # [tokens * top, width]: expert e's rows at plan.offsets[e]
     y = ex.combine(ys, weights, plan)          # [tokens, outs]
@@ -13,9 +16,13 @@ experts' products on them (the ebc_moe_* and ebc_mx4_* calls of
     w = ex.quantize(weight)                    # [n_experts, outs, width] in 4.25 bits a value
     ys = ex.product(ex.dispatch_mx4(x, plan), w, plan.offsets)
 
-dispatch, dispatch_grad and combine are recorded for gradients like torch's own
-operations (combine once: its gradients have none).  Values in 4 bits, and
-products of them, have no gradient.
+    q, y, h = ex.norm_mx8(x, gain, residual, wide=True)   # y in 8 bits, and in x's type for the router
+    w = ex.quantize_mx8(weight)                # [n_experts, outs, width] in 8.25 bits a value
+    ys = ex.product(ex.dispatch(q, plan), w, plan.offsets)
+
+norm, route, dispatch, dispatch_grad and combine are recorded for gradients like
+torch's own operations (norm, route and combine once: their gradients have
+none).  Values in 4 and 8 bits, and products of them, have no gradient.
 """
 from __future__ import annotations
 
@@ -25,10 +32,11 @@ import os
 
 import torch
 
-from . import EBC_BF16, EBC_F16, EBC_F32, EbcError, ebc_create, ebc_destroy, ebc_get_profile, ebc_last_device_error
+from . import EBC_BF16, EBC_F16, EBC_F32, EBC_SIGMOID, EBC_SOFTMAX, EbcError, ebc_create, ebc_destroy, ebc_get_profile, ebc_last_device_error
 from . import ebc_set_profiling, lib
 from . import build as _build
 
+_SCORES = {"softmax": EBC_SOFTMAX, "sigmoid": EBC_SIGMOID}
 _TYPES = {torch.float32: EBC_F32, torch.bfloat16: EBC_BF16, torch.float16: EBC_F16}
 
 
@@ -93,8 +101,24 @@ class Mx4:
         return (*self.codes.shape[:-1], self.width)
 
 
+class Mx8:
+    """Rows in 8 bits: codes uint8 [..., 32 * ceil(width / 32)] and scales uint8
+    [..., 16 * ceil(width / 512)], contiguous CUDA tensors of the same leading
+    shape; `width` values a row."""
+
+    __slots__ = ("codes", "scales", "width")
+
+    def __init__(self, codes, scales, width: int):
+        _calls.check_mx8(codes, scales, width)
+        self.codes, self.scales, self.width = codes, scales, width
+
+    @property
+    def shape(self):
+        return (*self.codes.shape[:-1], self.width)
+
+
 class Experts:
-    """The expert-parallel and 4-bit operators on one CUDA device.  Calls are
+    """The expert-parallel, 4- and 8-bit, router and norm operators on one CUDA device.  Calls are
     asynchronous on `stream` (None: the device's current stream), take no
     scratch, and return new tensors of that stream; not thread safe, use one
     per host thread."""
@@ -152,9 +176,95 @@ class Experts:
             p.rows, p.place, p.offsets = self._on(stream, _calls.plan, ids, n_experts)
         return p
 
+    def norm(self, x, weight, residual=None, eps: float = 1e-6, stream=None):
+        """(y, h): h = x + residual and y = h / sqrt(mean of h^2 over a row + eps) * weight, of x [..., width] and its
+        type.  y is of the sum before h is rounded; without a residual h is x.  weight [width] may be of another type."""
+        y, h = self._norm(x, weight, residual, eps, False, True, stream)[2:]
+        return y, h
+
+    def norm_mx8(self, x, weight, residual=None, eps: float = 1e-6, wide: bool = False, stream=None):
+        """(q, y, h): norm with y in 8 bits as q (Mx8), rounded from fp32; y itself with `wide`, else None.  The
+        gradients are those of y and h: q has none."""
+        q = _new(Mx8)
+        q.codes, q.scales, y, h = self._norm(x, weight, residual, eps, True, wide, stream)
+        q.width = x.shape[-1]
+        return q, y, h
+
+    def _norm(self, x, weight, residual, eps, mx8, wide, stream):
+        """codes, scales, y, h; each None where there is none, but h is x without a residual."""
+        if x.dim() != 2:
+            lead, width = x.shape[:-1], x.shape[-1]
+            with _on_stream(stream):   # rows that have to be laid out first are laid out there too
+                flat = x.reshape(-1, width)
+                more = None if residual is None else residual.reshape(-1, width)
+                out = self._norm(flat, weight, more, eps, mx8, wide, None)
+            if stream is not None:
+                _used(None, stream, (x, weight, residual))
+            return (*(None if t is None else t.view(*lead, t.shape[-1]) for t in out[:3]),
+                    x if residual is None else out[3].view(x.shape))
+        args = (x, weight, residual, eps, mx8, wide)
+        if _calls.recorded(x, weight, residual):
+            out = self._recorded(stream, _Norm, *args)
+        elif stream is None:
+            out = _calls.norm(self._h, self._index, *args)
+        else:
+            out = self._on(stream, _calls.norm, *args)
+        return out if residual is not None else (*out[:3], x)
+
+    def norm_grad(self, dy, h, weight, dh=None, eps: float = 1e-6, stream=None):
+        """(dx, dweight) for the gradient dy [rows, width] of norm's y, at its h: dx is the gradient of x and of the
+        residual alike, dh (what else uses h has as its gradient) included.  They are not recorded for gradients of
+        their own."""
+        if stream is None:
+            return _calls.norm_grad(self._h, self._index, dy, h, weight, dh, eps)
+        return self._on(stream, _calls.norm_grad, dy, h, weight, dh, eps)
+
+    def route(self, logits, top: int, score: str = "softmax", bias=None, groups: int = 1, keep_groups=None,
+              group_top: int = 1, renormalize: bool = True, scale: float = 1.0, stream=None):
+        """(ids int32, weights fp32), both [tokens, top]: the experts of the largest scores of logits [tokens,
+        n_experts], the best first (ties: the lower expert), and their weights.
+
+        Scores are the softmax of a row or the sigmoid of each logit ("sigmoid").  bias (fp32 [n_experts]) is added to
+        them for the choice alone.  With groups, experts are chosen from the keep_groups (None: all) groups whose best
+        group_top (1 or 2) scores have the largest sum.  Weights are the scores without the bias, divided by their sum
+        over the choices with renormalize, times scale.  An expert whose logit or bias is -inf is not chosen; where a
+        token has too few, the rest are -1 (dropped, for plan) with weight 0."""
+        kind = _SCORES.get(score)
+        if kind is None:
+            raise ValueError('score must be "softmax" or "sigmoid"')
+        args = (logits, top, kind, bias, groups, groups if keep_groups is None else keep_groups, group_top,
+                renormalize, scale)
+        if _calls.recorded(logits):
+            return self._recorded(stream, _Route, *args)
+        if stream is None:
+            return _calls.route(self._h, self._index, *args)
+        return self._on(stream, _calls.route, *args)
+
+    def route_grad(self, dweights, logits, ids, score: str = "softmax", renormalize: bool = True, scale: float = 1.0,
+                   stream=None):
+        """The gradient of route's logits for the gradient dweights [tokens, top] of its weights, with the ids that it
+        chose.  It is not recorded for gradients of its own."""
+        kind = _SCORES.get(score)
+        if kind is None:
+            raise ValueError('score must be "softmax" or "sigmoid"')
+        if stream is None:
+            return _calls.route_grad(self._h, self._index, dweights, logits, ids, kind, renormalize, scale)
+        return self._on(stream, _calls.route_grad, dweights, logits, ids, kind, renormalize, scale)
+
     def dispatch(self, x, plan: Plan, stream=None):
-        """x [tokens, width] to rows sorted by expert [n, width]; rows past the last are zero.  Copies bits: 4-bit
-        rows of several senders are sorted as fp32 views of their codes and scales, with a plan of one choice a row."""
+        """x [tokens, width] to rows sorted by expert [n, width]; rows past the last are zero.  Copies bits: x may be
+        rows in 4 or 8 bits (Mx4, Mx8), and gives such; rows of several senders are sorted together with a plan of one
+        choice a row."""
+        if isinstance(x, (Mx4, Mx8)):
+            q = _new(type(x))
+            q.width = x.width
+            if stream is None:
+                q.codes, q.scales = _calls.dispatch_mx(self._h, self._index, x.codes, x.scales, plan.rows, plan.place,
+                                                       plan.offsets)
+            else:
+                q.codes, q.scales = self._on(stream, _calls.dispatch_mx, x.codes, x.scales, plan.rows, plan.place,
+                                             plan.offsets)
+            return q
         if _calls.recorded(x):
             return self._recorded(stream, _Dispatch, x, plan.rows, plan.place, plan.offsets)
         if stream is None:
@@ -195,38 +305,49 @@ class Experts:
 
     def quantize(self, x, stream=None) -> Mx4:
         """x [..., width] in 4 bits."""
+        return self._quantize(x, stream, Mx4, _calls.quantize)
+
+    def quantize_mx8(self, x, stream=None) -> Mx8:
+        """x [..., width] in 8 bits."""
+        return self._quantize(x, stream, Mx8, _calls.quantize_mx8)
+
+    def _quantize(self, x, stream, kind, call):
         if stream is not None:   # rows that have to be laid out first are laid out there too
             with torch.cuda.stream(stream):
-                q = self.quantize(x)
+                q = self._quantize(x, None, kind, call)
             x.record_stream(stream)
             return q
-        q = _new(Mx4)
+        q = _new(kind)
         q.width = width = x.shape[-1]
         if x.dim() == 2:
-            q.codes, q.scales = _calls.quantize(self._h, self._index, x)
+            q.codes, q.scales = call(self._h, self._index, x)
         else:
             lead = x.shape[:-1]
-            q.codes, q.scales = _calls.quantize(self._h, self._index, x.reshape(-1, width))
+            q.codes, q.scales = call(self._h, self._index, x.reshape(-1, width))
             q.codes, q.scales = q.codes.view(*lead, q.codes.shape[1]), q.scales.view(*lead, q.scales.shape[1])
         return q
 
-    def dequantize(self, q: Mx4, dtype=torch.float32, stream=None):
-        """The values of q as `dtype`."""
+    def dequantize(self, q, dtype=torch.float32, stream=None):
+        """The values of q (Mx4 or Mx8) as `dtype`."""
+        call = _calls.dequantize_mx8 if isinstance(q, Mx8) else _calls.dequantize
         if stream is None:
-            return _calls.dequantize(self._h, self._index, q.codes, q.scales, q.width, _type(dtype))
-        return self._on(stream, _calls.dequantize, q.codes, q.scales, q.width, _type(dtype))
+            return call(self._h, self._index, q.codes, q.scales, q.width, _type(dtype))
+        return self._on(stream, call, q.codes, q.scales, q.width, _type(dtype))
 
-    def product(self, x: Mx4, w: Mx4, offsets=None, dtype=torch.bfloat16, stream=None):
+    def product(self, x, w, offsets=None, dtype=torch.bfloat16, stream=None):
         """ys [rows, outs]: each row of x [rows, width] times the weights of its
-        expert, w [n_experts, outs, width]; expert e has the rows offsets[e] to
-        offsets[e + 1], and other rows are zero.  Without offsets, w [outs, width]
-        takes every row.  Sums are held in fp32 and rounded once, to dtype; rows that
-        combine sums up are rounded again there, which dtype=torch.float32 avoids."""
+        expert, w [n_experts, outs, width], both Mx4 or both Mx8; expert e has the
+        rows offsets[e] to offsets[e + 1], and other rows are zero.  Without offsets,
+        w [outs, width] takes every row.  Sums are held in fp32 and rounded once, to
+        dtype; rows that combine sums up are rounded again there, which
+        dtype=torch.float32 avoids."""
+        if isinstance(x, Mx8) != isinstance(w, Mx8):
+            raise ValueError("x and w must be of the same kind, Mx4 or Mx8")
+        call = _calls.product_mx8 if isinstance(x, Mx8) else _calls.product
         if stream is None:
-            return _calls.product(self._h, self._index, x.codes, x.scales, x.width, w.codes, w.scales, w.width,
-                                  offsets, _type(dtype))
-        return self._on(stream, _calls.product, x.codes, x.scales, x.width, w.codes, w.scales, w.width, offsets,
+            return call(self._h, self._index, x.codes, x.scales, x.width, w.codes, w.scales, w.width, offsets,
                         _type(dtype))
+        return self._on(stream, call, x.codes, x.scales, x.width, w.codes, w.scales, w.width, offsets, _type(dtype))
 
     def check(self) -> None:
         """Waits for the device (calls on every stream, and graphs that captured some) and raises the first error
@@ -247,6 +368,10 @@ class Experts:
 
 
 _new = object.__new__
+
+
+def _on_stream(stream):
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
 
 
 def _used(out, stream, args):
@@ -301,6 +426,51 @@ class _Combine(torch.autograd.Function):
         ys, weights, *plan = ctx.saved_tensors
         dys, dweights = ctx.ex.combine_grad(dy.contiguous(), ys, weights, _plan(plan))
         return None, dys, dweights, None, None, None
+
+
+class _Norm(torch.autograd.Function):
+    """norm and norm_mx8 on rows: codes, scales, y, h."""
+
+    @staticmethod
+    def forward(ctx, ex, x, weight, residual, eps, mx8, wide):
+        ctx.ex, ctx.eps = ex, eps
+        ctx.set_materialize_grads(False)
+        codes, scales, y, h = _calls.norm(ex._h, ex._index, x, weight, residual, eps, mx8, wide)
+        ctx.save_for_backward(x if residual is None else h, weight)
+        if mx8:
+            ctx.mark_non_differentiable(codes, scales)
+        return codes, scales, y, h
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dcodes, dscales, dy, dh):
+        h, weight = ctx.saved_tensors
+        dweight = None
+        dx = dh
+        if dy is not None:
+            dx, dweight = ctx.ex.norm_grad(dy.contiguous(), h, weight, None if dh is None else dh.contiguous(), ctx.eps)
+        need = ctx.needs_input_grad
+        return None, dx if need[1] else None, dweight if need[2] else None, dx if need[3] else None, None, None, None
+
+
+class _Route(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, ex, logits, top, kind, bias, groups, keep, group_top, renormalize, scale):
+        ctx.ex, ctx.how = ex, (kind, renormalize, scale)
+        ctx.set_materialize_grads(False)
+        ids, weights = _calls.route(ex._h, ex._index, logits, top, kind, bias, groups, keep, group_top, renormalize, scale)
+        ctx.save_for_backward(logits, ids)
+        ctx.mark_non_differentiable(ids)
+        return ids, weights
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dids, dweights):
+        dlogits = None
+        if dweights is not None:
+            logits, ids = ctx.saved_tensors
+            dlogits = _calls.route_grad(ctx.ex._h, ctx.ex._index, dweights.contiguous(), logits, ids, *ctx.how)
+        return (None, dlogits) + (None,) * 8
 
 
 def _type(dtype) -> int:

@@ -498,6 +498,34 @@ int ebc_moe_combine_grad(ebc_ctx* ctx, const void* d_dy, int64_t ld_dy, const vo
 #define EBC_MX4_CODE_BYTES(width) ((((width) + 31) / 32) * 16)
 #define EBC_MX4_SCALE_BYTES(width) ((((width) + 511) / 512) * 16)
 
+/* ---- 8-bit microscaled values ----
+ *
+ * The same with elements of 8 bits: 8.25 bits a value.  A block of 32 values has
+ * the scale X = 2^e, e the least integer >= -127 with max |x| <= 448 X, kept as
+ * the byte e + 127; each value is kept as the nearest E4M3 number times X, ties
+ * to even (sign, 4 exponent bits, 3 fraction bits).  No value saturates, so
+ * |x - xhat| <= max(|x| / 16, X / 1024), for |x| < 1.9375 * 2^127 (3.29e38); the
+ * nearest value of a larger one is 2^128.  (The open microscaling formats' MXFP8
+ * elements and scales; their suggested scale rule would saturate values in
+ * (448 X, 512 X).)  A block that holds a NaN or an infinity gets the byte 255
+ * and reads back as NaN.
+ *
+ * Layout, dense and row-major: codes, EBC_MX8_CODE_BYTES(width) bytes a row, a
+ * byte a value, filled up with zeros; scales as those of 4-bit rows,
+ * EBC_MX8_SCALE_BYTES(width) bytes a row.  Both arrays are 16-byte aligned.
+ * 1 <= width <= 2^24. */
+#define EBC_MX8_BLOCK 32
+#define EBC_MX8_CODE_BYTES(width) ((((width) + 31) / 32) * 32)
+#define EBC_MX8_SCALE_BYTES(width) EBC_MX4_SCALE_BYTES(width)
+
+/* d_x[rows][width] of `type` to 8 bits, and the values of d_codes and d_scales
+ * as `type` (exact in fp32 and bf16 but for 2^128; rounded to nearest in fp16),
+ * as ebc_mx4_quantize and ebc_mx4_dequantize. */
+int ebc_mx8_quantize(ebc_ctx* ctx, const void* d_x, int64_t ld_x, int type, int64_t rows, int64_t width,
+                     uint8_t* d_codes, uint8_t* d_scales, void* stream);
+int ebc_mx8_dequantize(ebc_ctx* ctx, const uint8_t* d_codes, const uint8_t* d_scales, int64_t rows, int64_t width,
+                       int type, void* d_xhat, void* stream);
+
 /* d_x[rows][width] of `type` to 4 bits. */
 int ebc_mx4_quantize(ebc_ctx* ctx, const void* d_x, int64_t ld_x, int type, int64_t rows, int64_t width,
                      uint8_t* d_codes, uint8_t* d_scales, void* stream);
@@ -527,6 +555,81 @@ int ebc_moe_dispatch_mx4(ebc_ctx* ctx, const void* d_x, int64_t ld_x, int type, 
 int ebc_mx4_product(ebc_ctx* ctx, const uint8_t* d_x_codes, const uint8_t* d_x_scales, int64_t rows, int64_t width,
                     const uint8_t* d_w_codes, const uint8_t* d_w_scales, int64_t outs, int n_experts,
                     const int32_t* d_offsets, int out_type, void* d_ys, void* stream);
+
+/* The same on rows and weights of 8 bits. */
+int ebc_mx8_product(ebc_ctx* ctx, const uint8_t* d_x_codes, const uint8_t* d_x_scales, int64_t rows, int64_t width,
+                    const uint8_t* d_w_codes, const uint8_t* d_w_scales, int64_t outs, int n_experts,
+                    const int32_t* d_offsets, int out_type, void* d_ys, void* stream);
+
+/* ebc_moe_dispatch of rows that are in 4 or 8 bits already: the codes and the
+ * scales of each token, code_bytes and scale_bytes a row (multiples of 16; both
+ * arrays dense and 16-byte aligned), to n rows; rows past the last expert's are
+ * zero. */
+int ebc_moe_dispatch_mx(ebc_ctx* ctx, const uint8_t* d_codes, int64_t code_bytes, const uint8_t* d_scales,
+                        int64_t scale_bytes, int64_t tokens, int top, const int32_t* d_place,
+                        const int32_t* d_offsets, int n_experts, uint8_t* d_xs_codes, uint8_t* d_xs_scales,
+                        void* stream);
+
+/* ---- The router ----
+ *
+ * Each token's experts and their weights from its scores, d_logits[tokens]
+ * [n_experts] of `type` (ld_logits elements between two rows):
+ *   s = softmax(l), or sigmoid(l) of each; c = s + d_bias (fp32 [n_experts],
+ *   NULL: none; it decides the choice alone).
+ * An expert whose logit or bias is -infinity is never chosen.  The experts are
+ * `groups` groups of the same size, one after the other; a group's score is the
+ * sum of its group_top (1 or 2) largest c (of those that it has), and only
+ * experts of the keep_groups best groups are chosen from.  d_ids[tokens][top] are
+ * the experts of the largest c, the largest first, ties to the lower expert
+ * (among groups: to the lower group); -1 (dropped, for ebc_moe_plan) where there
+ * are not enough.  Two c are compared as they are, not as fp32 has them: where
+ * that could not tell, they are computed in 64 bits.  A NaN counts as the largest
+ * value.  Without a bias c orders as l does, and is compared so.
+ *   d_weights[tokens][top], fp32: scale * s of the chosen, with `renormalize`
+ * divided by the sum of s over the chosen; 0 for -1.
+ * 1 <= top <= 32, 1 <= keep_groups <= groups <= 32, groups divides n_experts. */
+#define EBC_SOFTMAX 0
+#define EBC_SIGMOID 1
+#define EBC_MAX_TOP 32
+#define EBC_MAX_GROUPS 32
+int ebc_moe_route(ebc_ctx* ctx, const void* d_logits, int64_t ld_logits, int type, int64_t tokens, int n_experts,
+                  int top, int score, const float* d_bias, int groups, int keep_groups, int group_top,
+                  int renormalize, float scale, int32_t* d_ids, float* d_weights, void* stream);
+
+/* The gradient of d_logits, d_dlogits[tokens][n_experts] of `type`, for the
+ * gradient d_dweights[tokens][top] (fp32) of the weights and the ids that
+ * ebc_moe_route chose (the choice itself has no gradient, nor has the bias).
+ * Ids outside [0, n_experts) are dropped ones; those >= n_experts are also
+ * recorded as EBC_ERR_INVALID_ARG.  The ids of a token are distinct. */
+int ebc_moe_route_grad(ebc_ctx* ctx, const float* d_dweights, const void* d_logits, int64_t ld_logits, int type,
+                       int64_t tokens, int n_experts, int top, const int32_t* d_ids, int score, int renormalize,
+                       float scale, void* d_dlogits, void* stream);
+
+/* ---- The norm ahead of an expert layer ----
+ *
+ * h = x + residual (d_residual NULL: h = x), y = h / sqrt(mean(h^2) + eps) *
+ * weight, in fp32 with y of the sum before h is rounded.  d_x and d_residual
+ * [rows][width] of `type`, d_weight[width] of weight_type.  Written where not
+ * NULL, dense: d_y and d_h of `type`; d_codes and d_scales, y in 8 bits.  One of
+ * d_y and d_codes is asked for.  1 <= width <= EBC_MAX_NORM_WIDTH. */
+#define EBC_MAX_NORM_WIDTH 16384
+int ebc_norm(ebc_ctx* ctx, const void* d_x, int64_t ld_x, const void* d_residual, int64_t ld_residual, int type,
+             const void* d_weight, int weight_type, int64_t rows, int64_t width, float eps, void* d_y, void* d_h,
+             uint8_t* d_codes, uint8_t* d_scales, void* stream);
+
+/* The gradients for the gradient d_dy of y, at the sum d_h that ebc_norm kept (x,
+ * without a residual): d_dx[rows][width], that of x and of the residual alike,
+ * with d_dh (NULL: none), what h has of other uses, added to it; and
+ * d_dweight[width] of weight_type, its sums in fp32 and in the same order in every
+ * run.  d_scratch: EBC_NORM_GRAD_SCRATCH(rows, width) bytes of the caller's,
+ * 16-byte aligned, free again once the call's work is done; calls that may
+ * overlap, or graphs that may be replayed at the same time, have one each. */
+#define EBC_NORM_GRAD_PARTS 608
+#define EBC_NORM_GRAD_SCRATCH(rows, width) \
+  ((int64_t)4 * (width) * ((rows) < EBC_NORM_GRAD_PARTS ? (rows) : EBC_NORM_GRAD_PARTS))
+int ebc_norm_grad(ebc_ctx* ctx, const void* d_dy, int64_t ld_dy, const void* d_h, int64_t ld_h, const void* d_dh,
+                  int64_t ld_dh, int type, const void* d_weight, int weight_type, int64_t rows, int64_t width,
+                  float eps, void* d_dx, void* d_dweight, float* d_scratch, void* stream);
 
 /* Counts of the last compress call of the context, read on `stream` (a
  * cudaStream_t; NULL = the stream of the context's last call) after that call
