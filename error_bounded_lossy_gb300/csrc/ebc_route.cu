@@ -2,7 +2,7 @@
 // and the scores' gradient.  See include/ebc.h for the definitions.
 #include <math_constants.h>
 
-#include "ebc_types.cuh"
+#include "ebc_mx8.cuh"
 
 using namespace ebc;
 
@@ -12,16 +12,6 @@ constexpr unsigned kAll = 0xffffffffu;
 constexpr float kUlp = 1.1920929e-7f;   // 2^-23
 constexpr int kGradWarps = 4;
 
-// Values of 32 bits that order as floats do.  0 is what may not be chosen; a NaN
-// is above everything; the two zeros are one value.
-__device__ __forceinline__ uint32_t ordered(float v) {
-  const uint32_t b = __float_as_uint(v + 0.f);
-  return v != v ? ~0u : b & 0x80000000u ? ~b : b | 0x80000000u;
-}
-__device__ __forceinline__ float value_of(uint32_t k) {
-  return k == ~0u ? CUDART_NAN_F : __uint_as_float(k & 0x80000000u ? k & 0x7FFFFFFFu : ~k);
-}
-
 template <typename R>
 __device__ __forceinline__ R warp_sum(R v) {
 #pragma unroll
@@ -29,9 +19,14 @@ __device__ __forceinline__ R warp_sum(R v) {
   return v;
 }
 __device__ __forceinline__ float warp_max(float v) {   // (a NaN is ignored)
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) v = fmaxf(v, __shfl_xor_sync(kAll, v, off));
-  return v;
+  float r;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+  return r;
+}
+__device__ __forceinline__ float max_or_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
 }
 // What the largest exponent is taken from: nothing where there is none.
 __device__ __forceinline__ float shift_of(float most) { return most == -CUDART_INF_F ? 0.f : most; }
@@ -43,45 +38,57 @@ struct RouteArgs {
   float* weights;
   int64_t ld, tokens;
   int E, top, groups, keep;
+  uint32_t inverse;             // e / (E / groups) is e * inverse >> 20 for e < 1024
+  int group_lanes_log2;         // lanes of a group, where a group is whole lanes and a power of two of them; else -1
   float scale;
   bool sigmoid, renorm, sums;   // sums: a group's score is the sum of two
+  bool wide;                    // a lane's logits are whole vectors
 };
 
-// A warp's memory.
+// A warp's memory.  Values: a group starts at an odd distance from the next.
 template <int N>
 struct Room {
-  float l[32 * N];
-  float c[32 * N + 32];    // the choice's scores; a group starts at an odd distance from the next
-  double d[32 * N];
-  uint32_t key[34];        // the best, and one more
-  int id[34];
+  union {
+    float c[32 * N + 32];
+    double d[32 * N];
+  };
+  float value[36];   // the candidates, then the best of them in their order
+  int id[36];
 };
 
-// The choice in 64 bits, for tokens where 32 cannot tell two values apart: the
-// same steps, written to be short.  Scores are computed again where c is in
-// [lo, hi]; elsewhere what 32 bits say is enough.  Leaves the ids in room.id.
-template <int N>
-__device__ __noinline__ void choose_exactly(const RouteArgs& a, Room<N>& room, int pad, float most, double lo,
-                                            double hi, int lane) {
+// ---- scores in 64 bits, for values that 32 cannot tell apart ----
+// The sum of a softmax's exponentials.
+template <typename T>
+__device__ __noinline__ double exact_total(const T* row, int E, float most, int lane) {
+  double sum = 0.0;
+  for (int e = lane; e < E; e += 32) sum += exp((double)to_f32(row[e]) - (double)most);
+  return warp_sum(sum);
+}
+// The choice's value of an expert.
+template <typename T>
+__device__ __noinline__ double exact_value(const RouteArgs& a, const T* row, int e, float most, double total) {
+  const double l = (double)to_f32(row[e]);
+  return (a.sigmoid ? 1.0 / (1.0 + exp(-l)) : exp(l - (double)most) / total) + (a.bias ? (double)a.bias[e] : 0.0);
+}
+
+// The whole choice in 64 bits, for rows with a NaN and for ties of more values
+// than a warp has lanes: the same steps, written to be short.  A NaN is above
+// everything.  Leaves the ids in room.id.
+template <typename T, int N>
+__device__ __noinline__ void choose_exactly(const RouteArgs& a, Room<N>& room, const T* row, float most, bool scored,
+                                            int lane) {
   const int size = a.E / a.groups;
-  double total = 1.0;
-  if (!a.sigmoid) {
-    total = 0.0;
-    for (int e = lane; e < a.E; e += 32) total += exp((double)room.l[e] - (double)most);
-    total = warp_sum(total);
-  }
+  const double total = scored && !a.sigmoid ? exact_total(row, a.E, most, lane) : 1.0;
+  __syncwarp();
   for (int e = lane; e < a.E; e += 32) {
-    const float l = room.l[e], b = a.bias ? a.bias[e] : 0.f;
-    double c = (double)room.c[e + e / size * pad];
-    if (l == -CUDART_INF_F || b == -CUDART_INF_F)
-      c = -CUDART_INF;
-    else if (c >= lo && c <= hi)
-      c = (a.sigmoid ? 1.0 / (1.0 + exp(-(double)l)) : exp((double)l - (double)most) / total) + (double)b;
-    room.d[e] = c;
+    const float l = to_f32(row[e]);
+    room.d[e] = l == -CUDART_INF_F || (a.bias && a.bias[e] == -CUDART_INF_F) ? -CUDART_INF
+                : scored ? exact_value(a, row, e, most, total)
+                         : (double)l;
   }
   __syncwarp();
-  // a is better than b: larger, or a NaN
-  auto better = [](double a, double b) { return a > b || (a != a && b == b); };
+  // x is better than y: larger, or a NaN
+  auto better = [](double x, double y) { return x > y || (x != x && y == y); };
   unsigned kept = kAll;
   if (a.groups > 1) {
     double score = -CUDART_INF;
@@ -111,13 +118,13 @@ __device__ __noinline__ void choose_exactly(const RouteArgs& a, Room<N>& room, i
     for (int e = lane; e < a.E; e += 32) {
       if (a.groups > 1 && !(kept >> (e / size) & 1)) continue;
       // without a bias it is the logits that are compared
-      const double c = room.d[e], v = c == -CUDART_INF || a.bias ? c : (double)room.l[e];
+      const double c = room.d[e], v = c == -CUDART_INF || a.bias ? c : (double)to_f32(row[e]);
       if (better(v, best)) {
         best = v;
         at = e;
       }
     }
-#pragma unroll
+#pragma unroll 1
     for (int off = 16; off > 0; off >>= 1) {
       const double v = __shfl_xor_sync(kAll, best, off);
       const int o = __shfl_xor_sync(kAll, at, off);
@@ -134,235 +141,312 @@ __device__ __noinline__ void choose_exactly(const RouteArgs& a, Room<N>& room, i
   }
 }
 
-// A warp a token; lane i has the experts i * N to i * N + N - 1.
+// Puts the experts of the set bits (bit j of a lane: expert lane * N + j) into
+// room.id in their order, with their values; returns how many, and writes
+// nothing where they are more than a warp.
+template <int N>
+__device__ __forceinline__ int gather(Room<N>& room, uint32_t bits, const float (&v)[N], int lane) {
+  const int mine = __popc(bits);
+  int at = mine;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const int o = __shfl_up_sync(kAll, at, off);
+    if (lane >= off) at += o;
+  }
+  const int all = __shfl_sync(kAll, at, 31);
+  at -= mine;
+  __syncwarp();
+  if (all <= 32) {
+#pragma unroll
+    for (int j = 0; j < N; ++j)
+      if (bits >> j & 1) {
+        room.value[at] = v[j];
+        room.id[at++] = lane * N + j;
+      }
+  }
+  __syncwarp();
+  return all;
+}
+
+// A warp a token; lane i has the experts i * N to i * N + N - 1, whose values in
+// 32 bits are -infinity where they may not be chosen.
 //
-// The choice, in 32 bits: the (top + 1)-th largest of the lanes' largest values
-// is a bound that at least top + 1 values reach; those that do (few more) are
-// put into lanes by their order among the experts, and each counts how many
-// come before it.  Where more than a warp of values reach it (ties), the best
-// are taken one by one.
+// The choice: the (top + 1)-th largest of the lanes' largest values is a bound
+// that at least top + 1 values reach; those that do (few more) are put into
+// lanes in the experts' order, and each counts the ones before it.
 //
-// Whether the choice is the one that the scores themselves give: the logits, as
-// they are, order it where there is no bias; else a score in 32 bits is off by
-// at most `err`, and where two values that decide are nearer than both may be
-// off, the token is done again in 64 bits.
+// Whether that is the choice that the scores themselves give: the logits order
+// it, as they are, where there is no bias; else a value in 32 bits is off by at
+// most `err`, and where two that decide are nearer than both may be off, those
+// few are computed again in 64 bits, a lane each, and compared so (two equal
+// logits with equal biases are equal, and need none of it).  The same for the
+// groups at the border of the kept ones.  With 256 experts that is one token in
+// some hundreds.
 template <typename T, int N, int kWarps>
 __global__ void __launch_bounds__(32 * kWarps) k_moe_route(RouteArgs a) {
   __shared__ Room<N> rooms[kWarps];
   pdl_enter();
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   Room<N>& room = rooms[w];
-  const int size = a.E / a.groups, pad = a.groups > 1 && size % 2 == 0;
-  const uint32_t inverse = ((1u << 20) + size - 1) / size;   // e / size is e * inverse >> 20 for e < 1024
   const bool scored = a.bias || (a.sums && a.groups > 1);
-  float bias[N];
-  uint32_t allowed = 0;   // a bit a value: an expert, not ruled out by its bias
-  float bias_most = 0.f;
+  float bias[N], bias_most = 0.f;
 #pragma unroll
-  for (int j = 0; j < N; ++j) {
-    const int e = lane * N + j;
-    bias[j] = a.bias && e < a.E ? a.bias[e] : 0.f;
-    if (e < a.E && bias[j] != -CUDART_INF_F) allowed |= 1u << j;
-    if (fabsf(bias[j]) < CUDART_INF_F) bias_most = fmaxf(bias_most, fabsf(bias[j]));
-  }
-  bias_most = warp_max(bias_most);
-  for (int64_t t = (int64_t)blockIdx.x * kWarps + w; t < a.tokens; t += (int64_t)gridDim.x * kWarps) {
-    const T* row = (const T*)a.logits + t * a.ld;
-    float l[N], c[N];
-    uint32_t alive = allowed;
-    float most = -CUDART_INF_F;
+  for (int j = 0; j < N; ++j) bias[j] = 0.f;
+  if (a.bias) {
 #pragma unroll
     for (int j = 0; j < N; ++j) {
       const int e = lane * N + j;
-      l[j] = e < a.E ? to_f32(row[e]) : -CUDART_INF_F;
-      if (l[j] == -CUDART_INF_F) alive &= ~(1u << j);
-      most = fmaxf(most, l[j]);
+      if (e < a.E) bias[j] = a.bias[e];
+      if (fabsf(bias[j]) < CUDART_INF_F) bias_most = fmaxf(bias_most, fabsf(bias[j]));
     }
-    float total = 1.f;
+    bias_most = warp_max(bias_most);
+  }
+  for (int64_t t = (int64_t)blockIdx.x * kWarps + w; t < a.tokens; t += (int64_t)gridDim.x * kWarps) {
+    const T* row = (const T*)a.logits + t * a.ld;
+    float l[N], c[N];
+    if (a.wide) {
+      constexpr int kV = N < 8 ? N : 8;
+#pragma unroll
+      for (int i = 0; i < N / kV; ++i) {
+        Values<T, kV> v;
+        if (lane * N < a.E) v.load(row + lane * N + i * kV);
+#pragma unroll
+        for (int j = 0; j < kV; ++j) l[i * kV + j] = lane * N < a.E ? to_f32(v.e[j]) : -CUDART_INF_F;
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < N; ++j) l[j] = lane * N + j < a.E ? to_f32(row[lane * N + j]) : -CUDART_INF_F;
+    }
+    float most = 0.f, total = 1.f;
     if (!a.sigmoid && (scored || !a.renorm)) {
+      most = l[0];
+#pragma unroll
+      for (int j = 1; j < N; ++j) most = fmaxf(most, l[j]);
       most = shift_of(warp_max(most));
       total = 0.f;
 #pragma unroll
       for (int j = 0; j < N; ++j) {
-        c[j] = expf(l[j] - most);   // (of -infinity: 0)
+        c[j] = __expf(l[j] - most);   // (of -infinity: 0)
         total += c[j];
       }
       total = warp_sum(total);
     }
     // How far a value in 32 bits may be off, with a margin.  Of the largest score
-    // (1, or the softmax's 1 / total): for the sigmoid exp, the sum and the quotient
-    // lose less than 2^-21; for the softmax the exponent's difference 2^-25 (it
-    // grows as the score falls), exp and the quotient 2^-21, and the total's N + 5
-    // roundings.  And the rounding of the bias's addition.
-    const float err = a.sigmoid ? (9.f + bias_most) * kUlp : ((float)(N + 17) / total + bias_most) * kUlp;
+    // (1, or the softmax's 1 / total): for the sigmoid the exponential, which is off
+    // by 2 + 1.2 |l| units of which s (1 - s) counts, the sum and the quotient lose
+    // less than 2^-21; for the softmax the exponential and the quotient 2^-21 (more
+    // where the score is smaller by more), and the total's N + 5 roundings and its
+    // terms' errors 2^-19.  And the rounding of the bias's addition.
+    const float err = a.sigmoid ? (9.f + bias_most) * kUlp : ((float)(N + 48) / total + bias_most) * kUlp;
     if (scored) {
+      const float part = __fdividef(1.f, total);
 #pragma unroll
       for (int j = 0; j < N; ++j) {
-        const float s = a.sigmoid ? __fdividef(1.f, 1.f + expf(-l[j])) : __fdividef(c[j], total);
-        c[j] = s + bias[j];
+        const float s = a.sigmoid ? __fdividef(1.f, 1.f + __expf(-l[j])) : c[j] * part;
+        c[j] = l[j] == -CUDART_INF_F ? l[j] : s + bias[j];
       }
-    }
-    __syncwarp();   // the room is free
+    } else {
 #pragma unroll
-    for (int j = 0; j < N; ++j) {
-      const int e = lane * N + j;
-      if (e < a.E) {
-        room.l[e] = l[j];
-        if (scored || a.groups > 1)
-          room.c[e + (int)((uint32_t)e * inverse >> 20) * pad] =
-              !(alive >> j & 1) ? -CUDART_INF_F : scored ? c[j] : l[j];
-      }
+      for (int j = 0; j < N; ++j) c[j] = l[j];
     }
-    __syncwarp();
-    bool close = false;
-    double lo = CUDART_INF, hi = -CUDART_INF;   // of the values that are too close
-    if (a.groups > 1) {
-      // `lanes` lanes a group, each its best two of every lanes-th value
-      const int lanes_log2 = 31 - __clz(32 / a.groups), lanes = 1 << lanes_log2, g = lane >> lanes_log2;
-      uint32_t first = 0, second = 0;
-      if (g < a.groups)
-        for (int i = lane & (lanes - 1); i < size; i += lanes) {
-          const float v = room.c[g * (size + pad) + i];
-          const uint32_t k = v == -CUDART_INF_F ? 0u : ordered(v);
-          second = max(second, min(first, k));
-          first = max(first, k);
+    float top1 = c[0];
+#pragma unroll
+    for (int j = 1; j < N; ++j) top1 = max_or_nan(top1, c[j]);
+    bool generic = __any_sync(kAll, top1 != top1);   // a NaN
+    double total64 = 0.0;                            // 0: not summed yet
+    if (a.groups > 1 && !generic) {
+      // a group's largest two, in each of its lanes
+      float first = -CUDART_INF_F, second = -CUDART_INF_F;
+      int log2 = a.group_lanes_log2;
+      if (log2 >= 0) {
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+          second = fmaxf(second, fminf(first, c[j]));
+          first = fmaxf(first, c[j]);
         }
-      for (int off = 1; off < lanes; off <<= 1) {
-        const uint32_t f = __shfl_xor_sync(kAll, first, off), s = __shfl_xor_sync(kAll, second, off);
-        second = max(max(second, s), min(first, f));
-        first = max(first, f);
+      } else {
+        const int size = a.E / a.groups, pad = size % 2 == 0;
+        __syncwarp();
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+          const int e = lane * N + j;
+          if (e < a.E) room.c[e + (int)((uint32_t)e * a.inverse >> 20) * pad] = c[j];
+        }
+        __syncwarp();
+        log2 = 31 - __clz(32 / a.groups);
+        if (lane >> log2 < a.groups)
+          for (int i = lane & ((1 << log2) - 1); i < size; i += 1 << log2) {
+            const float v = room.c[(lane >> log2) * (size + pad) + i];
+            second = fmaxf(second, fminf(first, v));
+            first = fmaxf(first, v);
+          }
       }
-      const uint32_t score = a.sums && second ? ordered(value_of(first) + value_of(second)) : first;
+      const int g = lane >> log2;
+#pragma unroll 1
+      for (int off = 1; off < 1 << log2; off <<= 1) {
+        const float f = __shfl_xor_sync(kAll, first, off), s = __shfl_xor_sync(kAll, second, off);
+        second = fmaxf(fmaxf(second, s), fminf(first, f));
+        first = fmaxf(first, f);
+      }
+      const float score = a.sums && second > -CUDART_INF_F ? first + second : first;
       int rank = 0;
       for (int i = 0; i < a.groups; ++i) {
-        const uint32_t s = __shfl_sync(kAll, score, i << lanes_log2);
+        const float s = __shfl_sync(kAll, score, i << log2);
         rank += s > score || (s == score && i < g);
       }
-      const bool one = g < a.groups && (lane & (lanes - 1)) == 0;   // (a group's first lane speaks for it)
-      const unsigned kept = __ballot_sync(kAll, one && rank < a.keep);
+      const bool one = g < a.groups && (lane & ((1 << log2) - 1)) == 0;   // (a group's first lane speaks for it)
       if (scored && a.keep < a.groups) {
         const unsigned in = __ballot_sync(kAll, one && rank == a.keep - 1), out = __ballot_sync(kAll, one && rank == a.keep);
-        const uint32_t ki = __shfl_sync(kAll, score, __ffs(in) - 1), ko = __shfl_sync(kAll, score, __ffs(out) - 1);
-        const float vi = value_of(ki), vo = value_of(ko);
-        if (ki && ko && vi - vo <= 6.f * err) {   // (two values and a rounding each)
-          close = true;
-          lo = -CUDART_INF;
-          hi = CUDART_INF;
-        }
-      }
+        const float vi = __shfl_sync(kAll, score, __ffs(in) - 1), vo = __shfl_sync(kAll, score, __ffs(out) - 1);
+        if (vo > -CUDART_INF_F && vi - vo <= 6.f * err) {   // (two values and a rounding each)
+          // what decides: the largest of the groups that are that near
+          const bool near = score <= vi + 6.f * err && score >= vo - 6.f * err;
+          const float from = near ? (a.sums && second > -CUDART_INF_F ? second : first) - 2.f * err : CUDART_INF_F;
+          uint32_t bits = 0;
 #pragma unroll
-      for (int j = 0; j < N; ++j)
-        if (!(kept >> (((uint32_t)(lane * N + j) * inverse >> 20) << lanes_log2 & 31) & 1)) alive &= ~(1u << j);
-    }
-    // the best top + 1
-    uint32_t key[N], mine = 0;
-#pragma unroll
-    for (int j = 0; j < N; ++j) {
-      key[j] = alive >> j & 1 ? ordered(a.bias ? c[j] : l[j]) : 0u;
-      mine = max(mine, key[j]);
-    }
-    uint32_t bound = 1, left = mine;
-    for (int r = 0; r <= a.top; ++r) {
-      const uint32_t m = __reduce_max_sync(kAll, left);
-      bound = m ? m : 1u;
-      if (!m) break;
-      if (left == m) left = 0;
-    }
-    uint32_t reach = 0;
-#pragma unroll
-    for (int j = 0; j < N; ++j)
-      if (key[j] >= bound) reach |= 1u << j;
-    int before = __popc(reach);
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-      const int v = __shfl_up_sync(kAll, before, off);
-      if (lane >= off) before += v;
-    }
-    const int found = __shfl_sync(kAll, before, 31);
-    before -= __popc(reach);
-    // room.key and room.id: the best, the best first; zero and -1 behind them
-    if (found <= 32) {
-#pragma unroll
-      for (int j = 0; j < N; ++j)
-        if (reach >> j & 1) {
-          room.key[before] = key[j];
-          room.id[before] = lane * N + j;
-          ++before;
-        }
-      __syncwarp();
-      const uint32_t k = lane < found ? room.key[lane] : 0u;
-      const int e = lane < found ? room.id[lane] : -1;
-      int rank = 0;
-      for (int i = 0; i < found; ++i) {
-        const uint32_t o = __shfl_sync(kAll, k, i);
-        rank += o > k || (o == k && i < lane);
-      }
-      if (lane >= found) rank = lane;
-      __syncwarp();
-      room.key[rank] = k;
-      room.id[rank] = e;
-      if (lane < 2) room.key[32 + lane] = 0u;
-    } else {
-      for (int r = 0; r <= a.top; ++r) {
-        uint32_t best = 0;
-        int at = 0;
-#pragma unroll
-        for (int j = 0; j < N; ++j)
-          if (key[j] > best) {
-            best = key[j];
-            at = j;
+          for (int j = 0; j < N; ++j) {
+            const int eg = (int)((uint32_t)(lane * N + j) * a.inverse >> 20) & 31;
+            const float least = __shfl_sync(kAll, from, eg << log2 & 31);
+            if (c[j] >= least && c[j] > -CUDART_INF_F) bits |= 1u << j;
           }
-        const uint32_t m = __reduce_max_sync(kAll, best);
-        const unsigned who = __ballot_sync(kAll, best == m);
-        if (lane == __ffs(who) - 1) {
-          room.key[r] = m;
-          room.id[r] = m ? lane * N + at : -1;
+          const int found = gather(room, bits, c, lane);
+          generic = found > 32;
+          if (!generic) {
+            if (!a.sigmoid) total64 = exact_total(row, a.E, most, lane);
+            const int e = lane < found ? room.id[lane] : 0;
+            const double value = exact_value(a, row, e, most, total64);
+            const int eg = (int)((uint32_t)e * a.inverse >> 20);
+            double f = -CUDART_INF, s = -CUDART_INF;
+#pragma unroll 1
+            for (int i = 0; i < found; ++i) {
+              const double v = __shfl_sync(kAll, value, i);
+              if (__shfl_sync(kAll, eg, i) == g) {
+                s = fmax(s, fmin(f, v));
+                f = fmax(f, v);
+              }
+            }
+            const double sure = !near ? (double)score : a.sums && s > -CUDART_INF ? f + s : f;
+            rank = 0;
+#pragma unroll 1
+            for (int i = 0; i < a.groups; ++i) {
+              const double o = __shfl_sync(kAll, sure, i << log2);
+              rank += o > sure || (o == sure && i < g);
+            }
+          }
+        }
+      }
+      const unsigned kept = __ballot_sync(kAll, one && rank < a.keep);
+#pragma unroll
+      for (int j = 0; j < N; ++j) {
+        const uint32_t eg = a.group_lanes_log2 >= 0 ? (uint32_t)g : (uint32_t)(lane * N + j) * a.inverse >> 20;
+        const bool dead = c[j] == -CUDART_INF_F || !(kept >> (eg << log2 & 31) & 1);
+        c[j] = dead ? -CUDART_INF_F : a.bias ? c[j] : l[j];   // (now what the choice compares)
+      }
+      top1 = c[0];
+#pragma unroll
+      for (int j = 1; j < N; ++j) top1 = fmaxf(top1, c[j]);
+    }
+    int id = -1;
+    if (!generic) {
+      // the best top + 1, and whatever may be among the best top
+      float bound = -CUDART_INF_F, left = top1;
+#pragma unroll 1
+      for (int r = 0; r <= a.top; ++r) {
+        bound = warp_max(left);
+        if (bound == -CUDART_INF_F) break;
+        if (left == bound) left = -CUDART_INF_F;
+      }
+      if (a.bias) bound -= 2.f * err;
+      uint32_t bits = 0;
+#pragma unroll
+      for (int j = 0; j < N; ++j)
+        if (c[j] >= bound && c[j] > -CUDART_INF_F) bits |= 1u << j;
+      const int found = gather(room, bits, c, lane);
+      if (found <= 32) {
+        float v = lane < found ? room.value[lane] : -CUDART_INF_F;
+        int e = lane < found ? room.id[lane] : -1, rank = 0;
+#pragma unroll 4
+        for (int i = 0; i < found; ++i) {
+          const float o = room.value[i];
+          rank += o > v || (o == v && i < lane);
+        }
+        if (lane >= found) rank = lane;
+        __syncwarp();
+        room.value[rank] = v;
+        room.id[rank] = e;
+        __syncwarp();
+        if (a.bias) {
+          // is each of the best far enough from the next, or the same as it
+          v = room.value[lane];
+          e = room.id[lane];
+          const float x = e >= 0 ? to_f32(row[e]) : 0.f, b = e >= 0 ? a.bias[e] : 0.f;
+          const float o = __shfl_down_sync(kAll, v, 1), ox = __shfl_down_sync(kAll, x, 1), ob = __shfl_down_sync(kAll, b, 1);
+          const bool near = lane < a.top && lane < 31 && o > -CUDART_INF_F && v - o <= 2.f * err && !(x == ox && b == ob);
+          if (__any_sync(kAll, near)) {
+            if (!a.sigmoid && total64 == 0.0) total64 = exact_total(row, a.E, most, lane);
+            const double value = e >= 0 ? exact_value(a, row, e, most, total64) : -CUDART_INF;
+            rank = 0;
+#pragma unroll 1
+            for (int i = 0; i < found; ++i) {
+              const double u = __shfl_sync(kAll, value, i);
+              const int n = __shfl_sync(kAll, e, i);
+              rank += u > value || (u == value && n < e);
+            }
+            if (lane >= found) rank = lane;
+            __syncwarp();
+            room.id[rank] = e;
+            __syncwarp();
+          }
+        }
+        id = lane < a.top ? room.id[lane] : -1;
+      } else if (!a.bias) {
+        // ties of more than a warp of values: the best one by one
+#pragma unroll 1
+        for (int r = 0; r < a.top; ++r) {
+          float best = c[0];
+          int at = 0;
+#pragma unroll
+          for (int j = 1; j < N; ++j)
+            if (c[j] > best) {
+              best = c[j];
+              at = j;
+            }
+          const float m = warp_max(best);
+          if (m == -CUDART_INF_F) break;
+          const int winner = __ffs(__ballot_sync(kAll, best == m)) - 1;
+          const int e = __shfl_sync(kAll, lane * N + at, winner);
+          if (lane == r) id = e;
 #pragma unroll
           for (int j = 0; j < N; ++j)
-            if (j == at) key[j] = 0;
+            if (lane == winner && j == at) c[j] = -CUDART_INF_F;
         }
+      } else {
+        generic = true;
       }
     }
-    __syncwarp();
-    if (a.bias) {
-      const uint32_t k = lane < a.top ? room.key[lane] : 0u, o = lane < a.top ? room.key[lane + 1] : 0u;
-      const float v = value_of(k), u = value_of(o);
-      const bool near = k && o && v - u <= 2.f * err;
-      if (__any_sync(kAll, near)) {
-        close = true;
-        // whatever is within reach of a pair (and of a run of them) is computed again
-        double from = near ? (double)u - 4.0 * err : CUDART_INF, to = near ? (double)v + 4.0 * err : -CUDART_INF;
-#pragma unroll
-        for (int off = 16; off > 0; off >>= 1) {
-          from = fmin(from, __shfl_xor_sync(kAll, from, off));
-          to = fmax(to, __shfl_xor_sync(kAll, to, off));
-        }
-        lo = fmin(lo, from);
-        hi = fmax(hi, to);
-      }
-    }
-    if (close) {
-      choose_exactly<N>(a, room, pad, most, lo, hi, lane);
+    if (generic) {
+      choose_exactly<T, N>(a, room, row, most, scored, lane);
+      id = lane < a.top ? room.id[lane] : -1;
       __syncwarp();
     }
     // weights, a lane a choice
-    const int id = lane < a.top ? room.id[lane] : -1;
-    const float x = id >= 0 ? room.l[id] : -CUDART_INF_F;
-    float s;
+    const float x = id >= 0 ? to_f32(row[id]) : -CUDART_INF_F;
+    float s = 0.f;
     if (a.renorm) {
       // shifted by the largest chosen, so that no sum is zero: for the sigmoid
       // only below 0, exp(x - m) / (1 + exp(x)) with m = 0 from there on
-      const float m = shift_of(warp_max(x));
-      if (a.sigmoid)
-        s = x <= 0.f ? expf(x - fminf(m, 0.f)) / (1.f + expf(x)) : 1.f / (1.f + expf(-x));
-      else
-        s = expf(x - m);
+      float m = shift_of(warp_max(x));
+      if (a.sigmoid) m = fminf(m, 0.f);
+      const bool high = a.sigmoid && x > 0.f;
+      s = expf(high ? -x : x - m);
+      if (a.sigmoid) s = (high ? 1.f : s) / (1.f + (high ? s : expf(x)));
       if (id < 0) s = 0.f;
       const float sum = warp_sum(s);
       // (a softmax with a NaN or +infinity in its row is NaN, whatever was chosen)
       s = id < 0 ? 0.f : total == total ? s / sum : total;
-    } else {
-      s = id < 0 ? 0.f : a.sigmoid ? 1.f / (1.f + expf(-x)) : expf(x - most) / total;
+    } else if (id >= 0) {
+      s = expf(a.sigmoid ? -x : x - most);
+      s = a.sigmoid ? 1.f / (1.f + s) : s / total;
     }
     if (lane < a.top) {
       a.ids[t * a.top + lane] = id;
@@ -470,8 +554,13 @@ unsigned grid(int64_t tokens, int warps, int nsm, int turns) {
 }
 
 template <typename T, int N>
-cudaError_t route_n(const CallView& v, const RouteArgs& a, cudaStream_t st) {
-  constexpr int kWarps = N == 32 ? 2 : 4;
+cudaError_t route_n(const CallView& v, RouteArgs a, cudaStream_t st) {
+  constexpr int kWarps = N == 32 ? 2 : 4, kBytes = (N < 8 ? N : 8) * (int)sizeof(T);
+  a.wide = a.E % N == 0 && ((uintptr_t)a.logits | (uintptr_t)(a.ld * (int64_t)sizeof(T))) % kBytes == 0;
+  const int size = a.E / a.groups, lanes = size / N;
+  a.group_lanes_log2 = -1;
+  if (size % N == 0 && (lanes & (lanes - 1)) == 0)
+    for (a.group_lanes_log2 = 0; 1 << a.group_lanes_log2 < lanes;) ++a.group_lanes_log2;
   return launch_named(v, "k_moe_route", st, k_moe_route<T, N, kWarps>, dim3(grid(a.tokens, kWarps, v.nsm, 1)),
                       dim3(32 * kWarps), 0, 1, a);
 }
@@ -506,9 +595,23 @@ int ebc_moe_route(ebc_ctx* ctx, const void* d_logits, int64_t ld_logits, int typ
   const int rc = begin_call(ctx, st, &v);
   if (rc || tokens == 0) return rc;
   // (all groups kept: no group decides anything)
-  const RouteArgs a{d_logits, d_bias, d_ids, d_weights, ld_logits, tokens, n_experts, top,
-                    keep_groups == groups ? 1 : groups, keep_groups == groups ? 1 : keep_groups, scale,
-                    score == EBC_SIGMOID, renormalize != 0, group_top == 2};
+  RouteArgs a = {};
+  a.logits = d_logits;
+  a.bias = d_bias;
+  a.ids = d_ids;
+  a.weights = d_weights;
+  a.ld = ld_logits;
+  a.tokens = tokens;
+  a.E = n_experts;
+  a.top = top;
+  a.groups = keep_groups == groups ? 1 : groups;
+  a.keep = keep_groups == groups ? 1 : keep_groups;
+  const uint32_t size = (uint32_t)(a.E / a.groups);
+  a.inverse = ((1u << 20) + size - 1) / size;
+  a.scale = scale;
+  a.sigmoid = score == EBC_SIGMOID;
+  a.renorm = renormalize != 0;
+  a.sums = group_top == 2;
   if (type == EBC_F32) return cuda_code(route_t<float>(v, a, st));
   if (type == EBC_BF16) return cuda_code(route_t<__nv_bfloat16>(v, a, st));
   return cuda_code(route_t<__half>(v, a, st));
