@@ -140,6 +140,16 @@ __global__ void __launch_bounds__(kMaxThreads) k_norm(NormArgs a) {
   }
 }
 
+// A weight's gradient, rounded once.
+__device__ __forceinline__ void store_dweight(void* dw, int type, int64_t i, float v) {
+  if (type == EBC_F32)
+    ((float*)dw)[i] = v;
+  else if (type == EBC_BF16)
+    ((__nv_bfloat16*)dw)[i] = from_f32<__nv_bfloat16>(v);
+  else
+    ((__half*)dw)[i] = from_f32<__half>(v);
+}
+
 struct GradArgs {
   const void *dy, *h, *dh, *w;   // dh: null where nothing else uses h
   void *dx, *dw;
@@ -149,35 +159,115 @@ struct GradArgs {
   float eps;
 };
 
+// A thread's values of the rows to come, in shared memory: its own copies, which
+// it alone reads, so there is nothing to wait for but its own.  One row is 16
+// bytes a thread, the threads next to each other, for each 16 bytes that it has.
+template <typename T, int V, int N, int kStages>
+struct Ring {
+  static constexpr int kParts = V * (int)sizeof(T) / 16;          // 16-byte copies of a vector
+  static constexpr int kStreams = 3;                              // h, dy, dh
+  static __device__ __forceinline__ uint4* at(int stage, int stream, int n, int part) {
+    extern __shared__ uint4 ring[];
+    return ring + (((stage * kStreams + stream) * N + n) * kParts + part) * blockDim.x + threadIdx.x;
+  }
+  static __device__ __forceinline__ void copy(int stage, int stream, int n, const T* src) {
+#pragma unroll
+    for (int i = 0; i < kParts; ++i)
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                       (uint32_t)__cvta_generic_to_shared(at(stage, stream, n, i))),
+                   "l"(reinterpret_cast<const uint4*>(src) + i)
+                   : "memory");
+  }
+  static __device__ __forceinline__ void get(int stage, int stream, int n, Values<T, V>* v) {
+#pragma unroll
+    for (int i = 0; i < kParts; ++i) {
+      const uint4 r = *at(stage, stream, n, i);
+      v->word[4 * i] = r.x;
+      v->word[4 * i + 1] = r.y;
+      v->word[4 * i + 2] = r.z;
+      v->word[4 * i + 3] = r.w;
+    }
+  }
+  static __device__ __forceinline__ void commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+  static __device__ __forceinline__ void wait() {   // for all but the latest kStages - 1
+    asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
+  }
+  static size_t bytes(int threads) { return (size_t)kStages * kStreams * N * kParts * 16 * threads; }
+};
+
 // With u = h / sqrt(mean(h^2) + eps) and q = dy * w:
 //   dx = (q - u * mean(q * u)) / sqrt(mean(h^2) + eps) + dh,   dw = sum over rows of dy * u.
 // Both means of a row come out of one pass over it.  A thread keeps the same
 // columns in every row, and with them their part of dw, so dw takes one
 // partial row a CTA, which k_norm_dweight adds up in a fixed order.
-template <typename T, int V, int N, int kLanes>
+// Bound by bandwidth, if loads are in flight while a row's sums go around the
+// CTA: with kStages, the rows to come are copied to shared memory meanwhile.
+template <typename T, int V, int N, int kLanes, int kStages>
 __global__ void __launch_bounds__(kLanes ? kRowThreads : kMaxThreads) k_norm_grad(GradArgs a) {
+  using R = Ring<T, V, N, kStages>;
   __shared__ float part[2][2][kMaxThreads / 32];
   pdl_enter();
   const int lanes = kLanes ? kLanes : blockDim.x, at = threadIdx.x % lanes, groups = blockDim.x / lanes;
   const int64_t step = (int64_t)gridDim.x * groups;
   const float share = 1.f / (float)a.width;
-  float dw[N][V];
+  constexpr bool kKeep = N * V <= 16;   // the weights stay in registers
+  float dw[N][V], kept[kKeep ? N : 1][V];
 #pragma unroll
-  for (int n = 0; n < N; ++n)
+  for (int n = 0; n < N; ++n) {
 #pragma unroll
     for (int k = 0; k < V; ++k) dw[n][k] = 0.f;
-  int turn = 0;
+    if constexpr (kKeep) {
+      const int c = (n * lanes + at) * V;
+#pragma unroll
+      for (int k = 0; k < V; ++k) kept[n][k] = 0.f;
+      if (c < a.width) load_weights<V>(a.w, a.w_type, c, kept[n]);
+    }
+  }
+  auto weights = [&](int n, int c, float (&w)[V]) {
+    if constexpr (kKeep) {
+#pragma unroll
+      for (int k = 0; k < V; ++k) w[k] = kept[n][k];
+    } else {
+      load_weights<V>(a.w, a.w_type, c, w);
+    }
+  };
+  auto request = [&](int64_t row, int stage) {
+    if constexpr (kStages > 0) {
+      if (row < a.rows) {
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+          const int c = (n * lanes + at) * V;
+          if (c >= a.width) continue;
+          R::copy(stage, 0, n, (const T*)a.h + row * a.ld_h + c);
+          R::copy(stage, 1, n, (const T*)a.dy + row * a.ld_dy + c);
+          if (a.dh) R::copy(stage, 2, n, (const T*)a.dh + row * a.ld_dh + c);
+        }
+      }
+      R::commit();
+    }
+  };
+  int turn = 0, stage = 0;
+  for (int i = 0; i < kStages - 1; ++i) request((int64_t)blockIdx.x * groups + i * step, i);
   for (int64_t row0 = (int64_t)blockIdx.x * groups; row0 < a.rows; row0 += step, turn ^= 1) {
     const int64_t row = row0 + threadIdx.x / lanes;
     const bool live = row < a.rows;
     Values<T, V> hv[N], gv[N], ev[N];
+    if constexpr (kStages > 0) {
+      request(row0 + (kStages - 1) * step, stage == 0 ? kStages - 1 : stage - 1);
+      R::wait();
+    }
 #pragma unroll
     for (int n = 0; n < N; ++n) {
       const int c = (n * lanes + at) * V;
       if (live && c < a.width) {
-        hv[n].load((const T*)a.h + row * a.ld_h + c);
-        gv[n].load((const T*)a.dy + row * a.ld_dy + c);
-        if (a.dh) ev[n].load((const T*)a.dh + row * a.ld_dh + c);
+        if constexpr (kStages > 0) {
+          R::get(stage, 0, n, &hv[n]);
+          R::get(stage, 1, n, &gv[n]);
+        } else {
+          hv[n].load((const T*)a.h + row * a.ld_h + c);
+          gv[n].load((const T*)a.dy + row * a.ld_dy + c);
+          if (a.dh) ev[n].load((const T*)a.dh + row * a.ld_dh + c);
+        }
       } else {
         hv[n].zero();
         gv[n].zero();
@@ -187,35 +277,40 @@ __global__ void __launch_bounds__(kLanes ? kRowThreads : kMaxThreads) k_norm_gra
 #pragma unroll
     for (int n = 0; n < N; ++n) {
       const int c = (n * lanes + at) * V;
+      if (c >= a.width) continue;
       float w[V];
-      if (c < a.width) load_weights<V>(a.w, a.w_type, c, w);
+      weights(n, c, w);
 #pragma unroll
       for (int k = 0; k < V; ++k) {
         const float h = to_f32(hv[n].e[k]);
         sum[0] += h * h;
-        if (c < a.width) sum[1] += to_f32(gv[n].e[k]) * w[k] * h;
+        sum[1] += to_f32(gv[n].e[k]) * w[k] * h;
       }
     }
     group_sum<kLanes>(sum, part, turn);
     const float scale = rsqrtf(sum[0] * share + a.eps), mean = sum[1] * share * scale;
-    if (!live) continue;
+    if (live) {
 #pragma unroll
-    for (int n = 0; n < N; ++n) {
-      const int c = (n * lanes + at) * V;
-      if (c >= a.width) continue;
-      float w[V];
-      load_weights<V>(a.w, a.w_type, c, w);
-      Values<T, V> out;
+      for (int n = 0; n < N; ++n) {
+        const int c = (n * lanes + at) * V;
+        if (c >= a.width) continue;
+        float w[V];
+        weights(n, c, w);
+        Values<T, V> out;
+        if constexpr (kStages > 0)
+          if (a.dh) R::get(stage, 2, n, &ev[n]);
 #pragma unroll
-      for (int k = 0; k < V; ++k) {
-        const float u = to_f32(hv[n].e[k]) * scale, g = to_f32(gv[n].e[k]);
-        float d = scale * (g * w[k] - u * mean);
-        if (a.dh) d += to_f32(ev[n].e[k]);
-        out.e[k] = from_f32<T>(d);
-        dw[n][k] += g * u;
+        for (int k = 0; k < V; ++k) {
+          const float u = to_f32(hv[n].e[k]) * scale, g = to_f32(gv[n].e[k]);
+          float d = scale * (g * w[k] - u * mean);
+          if (a.dh) d += to_f32(ev[n].e[k]);
+          out.e[k] = from_f32<T>(d);
+          dw[n][k] += g * u;
+        }
+        out.store((T*)a.dx + row * a.width + c);
       }
-      out.store((T*)a.dx + row * a.width + c);
     }
+    if (++stage >= kStages) stage = 0;
   }
   float* mine = a.parts + (int64_t)blockIdx.x * a.width;
   if constexpr (kLanes == 0) {
@@ -223,6 +318,11 @@ __global__ void __launch_bounds__(kLanes ? kRowThreads : kMaxThreads) k_norm_gra
     for (int n = 0; n < N; ++n) {
       const int c = (n * lanes + at) * V;
       if (c >= a.width) continue;
+      if (gridDim.x == 1) {   // nothing to add up
+#pragma unroll
+        for (int k = 0; k < V; ++k) store_dweight(a.dw, a.w_type, c + k, dw[n][k]);
+        continue;
+      }
       Values<float, V> out;
 #pragma unroll
       for (int k = 0; k < V; ++k) out.e[k] = dw[n][k];
@@ -242,7 +342,11 @@ __global__ void __launch_bounds__(kLanes ? kRowThreads : kMaxThreads) k_norm_gra
           }
       __syncthreads();
     }
-    for (int c = threadIdx.x; c < a.width; c += blockDim.x) mine[c] = all[c];
+    for (int c = threadIdx.x; c < a.width; c += blockDim.x)
+      if (gridDim.x == 1)
+        store_dweight(a.dw, a.w_type, c, all[c]);
+      else
+        mine[c] = all[c];
   }
 }
 
@@ -260,13 +364,7 @@ __global__ void __launch_bounds__(1024) k_norm_dweight(const float* parts, int n
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
   const int mine = blockIdx.x * 32 + w;
-  if (lane != 0 || mine >= width) return;
-  if (type == EBC_F32)
-    ((float*)dw)[mine] = s;
-  else if (type == EBC_BF16)
-    ((__nv_bfloat16*)dw)[mine] = from_f32<__nv_bfloat16>(s);
-  else
-    ((__half*)dw)[mine] = from_f32<__half>(s);
+  if (lane == 0 && mine < width) store_dweight(dw, type, mine, s);
 }
 
 bool aligned(const void* p, int bytes) { return ((uintptr_t)p & (uintptr_t)(bytes - 1)) == 0; }
@@ -388,17 +486,33 @@ int ebc_norm_grad(ebc_ctx* ctx, const void* d_dy, int64_t ld_dy, const void* d_h
     e = with_type_of(type, [&](auto one) {
       return with_layout<decltype(one)>(vals < vals_s ? vals : vals_s, (int)width, [&](auto l, int threads) {
         using L = decltype(l);
+        // A row a CTA of whole vectors: rows to come in shared memory, as many as
+        // two CTAs an SM have room for.
+        constexpr int kBytes = 3 * L::N * L::V * (int)sizeof(typename L::T) * kMaxThreads;
+        constexpr int kStages = L::kLanes || L::V < 8 ? 0 : kBytes <= 48 * 1024 ? 4 : kBytes <= 96 * 1024 ? 2 : 0;
+        const auto kernel = k_norm_grad<typename L::T, L::V, L::N, L::kLanes, kStages>;
+        size_t smem = 0;
+        if constexpr (kStages > 0) {
+          using R = Ring<typename L::T, L::V, L::N, kStages>;
+          const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                     (int)R::bytes(kMaxThreads));
+          if (e != cudaSuccess) return e;
+          smem = R::bytes(threads);
+        }
         const int groups = L::kLanes ? threads / L::kLanes : 1;
         const int64_t want = (rows + groups - 1) / groups;
-        int64_t most = (int64_t)v.nsm * (1024 / threads < 1 ? 1 : 1024 / threads);
+        // all CTAs at once: by their registers (at most 128 a thread) and shared memory
+        constexpr int kFit = L::N * L::V <= 8 ? 1024 : 512;
+        int64_t each = kFit / threads < 1 ? 1 : kFit / threads;
+        if (smem && each > (int64_t)((220 * 1024) / (smem + 2048))) each = (int64_t)((220 * 1024) / (smem + 2048));
+        int64_t most = (int64_t)v.nsm * (each < 1 ? 1 : each);
         if (most > EBC_NORM_GRAD_PARTS) most = EBC_NORM_GRAD_PARTS;
         a.n_parts = (int)(want < most ? want : most);
-        return launch_named(v, "k_norm_grad", st, k_norm_grad<typename L::T, L::V, L::N, L::kLanes>,
-                            dim3((unsigned)a.n_parts), dim3(threads), 0, 1, a);
+        return launch_named(v, "k_norm_grad", st, kernel, dim3((unsigned)a.n_parts), dim3(threads), smem, 1, a);
       });
     });
   }
-  if (e == cudaSuccess)
+  if (e == cudaSuccess && a.n_parts != 1)
     e = launch_named(v, "k_norm_dweight", st, k_norm_dweight, dim3((unsigned)((width + 31) / 32)), dim3(1024), 0, 1,
                      d_scratch, a.n_parts, (int)width, weight_type, d_dweight);
   return cuda_code(e);

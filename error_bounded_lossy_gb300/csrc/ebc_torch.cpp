@@ -438,6 +438,14 @@ PyObject* py_dispatch_mx(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// Whether a call has to be recorded for gradients.
+bool recorded(std::initializer_list<PyObject*> os) {
+  if (c10::GradMode::is_enabled())
+    for (PyObject* o : os)
+      if (THPVariable_Check(o) && THPVariable_Unpack(o).requires_grad()) return true;
+  return false;
+}
+
 double real(PyObject* o) {
   const double v = PyFloat_AsDouble(o);
   if (v == -1.0 && PyErr_Occurred()) throw Raised{};
@@ -449,10 +457,12 @@ int small(PyObject* o) {   // an int argument of the C call, which refuses what 
   return (int)std::max<int64_t>(INT32_MIN, std::min<int64_t>(v, INT32_MAX));
 }
 
-// ctx, device, logits, top, score, bias or None, groups, keep_groups, group_top, renormalize, scale -> ids, weights
+// ctx, device, logits, top, score, bias or None, groups, keep_groups, group_top, renormalize, scale -> ids, weights;
+// None where the call has to be recorded for gradients
 PyObject* py_route(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  return guarded(n, 11, [&] {
+  return guarded(n, 11, [&]() -> PyObject* {
     const Where w = where(a);
+    if (recorded({a[2]})) Py_RETURN_NONE;
     const Rows l = rows(w, a[2]);
     no_tangent(l.t);
     const int top = small(a[3]);
@@ -465,7 +475,8 @@ PyObject* py_route(PyObject*, PyObject* const* a, Py_ssize_t n) {
       bias = (const float*)b.data_ptr();
     }
     if (top < 1 || top > EBC_MAX_TOP) checked(EBC_ERR_INVALID_ARG, "ebc_moe_route");
-    at::Tensor ids = w.empty({l.n, top}, at::kInt), weights = w.empty({l.n, top}, at::kFloat);
+    const Parts all{w.empty({2 * pad16(4 * l.n * top)}, at::kByte)};
+    at::Tensor ids = all.take(0, {l.n, top}, at::kInt), weights = all.take(pad16(4 * l.n * top), {l.n, top}, at::kFloat);
     checked(ebc_moe_route(w.ctx, l.t.data_ptr(), l.ld, l.type, l.n, (int)std::min<int64_t>(l.width, INT32_MAX), top,
                           small(a[4]), bias, small(a[6]), small(a[7]), small(a[8]), PyObject_IsTrue(a[9]),
                           (float)real(a[10]), (int32_t*)ids.data_ptr(), (float*)weights.data_ptr(), w.stream()),
@@ -516,26 +527,70 @@ Rows rows_like(const Where& w, PyObject* o, const Rows& like) {
   return r;
 }
 
-// ctx, device, x, weight, residual or None, eps, whether in 8 bits, whether in x's type
-//   -> codes, scales (or None), y (or None), h (None without a residual)
+// The norm's outputs: of few bytes in one allocation, which is most of a small
+// call's time; of more in their own, each as long-lived as its user.
+constexpr int64_t kFewBytes = 64 << 10;
+// (on 32-byte boundaries, where fp32 rows are read eight values at a time)
+int64_t pad32(int64_t n) { return (n + 31) & ~(int64_t)31; }
+
+// ctx, device, x, weight, residual or None, eps -> y, h (x without a residual); None where x is not rows, or where the
+// call has to be recorded for gradients
 PyObject* py_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  return guarded(n, 8, [&] {
+  return guarded(n, 6, [&]() -> PyObject* {
     const Where w = where(a);
+    if (recorded({a[2], a[3], a[4]}) || (THPVariable_Check(a[2]) && THPVariable_Unpack(a[2]).dim() != 2)) Py_RETURN_NONE;
     const Rows x = rows(w, a[2]);
     no_tangent(x.t);
     const at::Tensor& g = gain(w, a[3], x.width);
-    const bool more = a[4] != Py_None, mx8 = PyObject_IsTrue(a[6]), wide = PyObject_IsTrue(a[7]);
+    const bool more = a[4] != Py_None;
     const Rows r = more ? rows_like(w, a[4], x) : x;
-    at::Tensor y, h, c, s;
-    if (wide) y = w.empty({x.n, x.width}, x.t.scalar_type());
-    if (more) h = w.empty({x.n, x.width}, x.t.scalar_type());
-    if (mx8) std::tie(c, s) = mx_rows(w, 8, x.n, x.width);
-    auto at_ = [](const at::Tensor& t) { return t.defined() ? t.data_ptr() : nullptr; };
+    at::Tensor y, h;
+    const int64_t each = pad32(x.n * x.width * (int64_t)x.t.element_size());
+    if (more && each <= kFewBytes) {
+      const Parts all{w.empty({2 * each}, at::kByte)};
+      y = all.take(0, {x.n, x.width}, x.t.scalar_type());
+      h = all.take(each, {x.n, x.width}, x.t.scalar_type());
+    } else {
+      y = w.empty({x.n, x.width}, x.t.scalar_type());
+      if (more) h = w.empty({x.n, x.width}, x.t.scalar_type());
+    }
     checked(ebc_norm(w.ctx, x.t.data_ptr(), x.ld, more ? r.t.data_ptr() : nullptr, r.ld, x.type, g.data_ptr(),
-                     type_of(g), x.n, x.width, (float)real(a[5]), at_(y), at_(h), (uint8_t*)at_(c),
-                     (uint8_t*)at_(s), w.stream()),
+                     type_of(g), x.n, x.width, (float)real(a[5]), y.data_ptr(), more ? h.data_ptr() : nullptr, nullptr,
+                     nullptr, w.stream()),
             "ebc_norm");
-    return tuple({c, s, y, h});   // (an undefined tensor is None)
+    return tuple({y, more ? h : x.t});
+  });
+}
+
+// ctx, device, x, weight, residual or None, eps, wide -> codes, scales, y (None unless wide), h; or None, as py_norm
+PyObject* py_norm_mx8(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 7, [&]() -> PyObject* {
+    const Where w = where(a);
+    if (recorded({a[2], a[3], a[4]}) || (THPVariable_Check(a[2]) && THPVariable_Unpack(a[2]).dim() != 2)) Py_RETURN_NONE;
+    const Rows x = rows(w, a[2]);
+    no_tangent(x.t);
+    const at::Tensor& g = gain(w, a[3], x.width);
+    const bool more = a[4] != Py_None, wide = PyObject_IsTrue(a[6]);
+    const Rows r = more ? rows_like(w, a[4], x) : x;
+    const int64_t each = pad32(x.n * x.width * (int64_t)x.t.element_size()), cb = x.n * code_bytes(8, x.width),
+                  sb = pad32(x.n * EBC_MX8_SCALE_BYTES(x.width));
+    at::Tensor y, h, c, s;
+    if ((more || wide) && cb + sb + 2 * each <= kFewBytes) {
+      const Parts all{w.empty({cb + sb + (more + wide) * each}, at::kByte)};
+      c = all.take(0, {x.n, code_bytes(8, x.width)}, at::kByte);
+      s = all.take(cb, {x.n, EBC_MX8_SCALE_BYTES(x.width)}, at::kByte);
+      if (wide) y = all.take(cb + sb, {x.n, x.width}, x.t.scalar_type());
+      if (more) h = all.take(cb + sb + wide * each, {x.n, x.width}, x.t.scalar_type());
+    } else {
+      std::tie(c, s) = mx_rows(w, 8, x.n, x.width);
+      if (wide) y = w.empty({x.n, x.width}, x.t.scalar_type());
+      if (more) h = w.empty({x.n, x.width}, x.t.scalar_type());
+    }
+    checked(ebc_norm(w.ctx, x.t.data_ptr(), x.ld, more ? r.t.data_ptr() : nullptr, r.ld, x.type, g.data_ptr(),
+                     type_of(g), x.n, x.width, (float)real(a[5]), wide ? y.data_ptr() : nullptr,
+                     more ? h.data_ptr() : nullptr, (uint8_t*)c.data_ptr(), (uint8_t*)s.data_ptr(), w.stream()),
+            "ebc_norm");
+    return tuple({c, s, y, more ? h : x.t});   // (an undefined tensor is None)
   });
 }
 
@@ -549,8 +604,19 @@ PyObject* py_norm_grad(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const at::Tensor& g = gain(w, a[4], dy.width);
     const bool more = a[5] != Py_None;
     const Rows dh = more ? rows_like(w, a[5], dy) : dy;
-    at::Tensor dx = w.empty({dy.n, dy.width}, dy.t.scalar_type()), dg = w.empty({dy.width}, g.scalar_type()),
-               scratch = w.empty({(int64_t)EBC_NORM_GRAD_SCRATCH(dy.n, dy.width)}, at::kByte);
+    const int64_t xb = pad32(dy.n * dy.width * (int64_t)dy.t.element_size()), gb = pad32(dy.width * (int64_t)g.element_size()),
+                  sb = pad32(EBC_NORM_GRAD_SCRATCH(dy.n, dy.width));
+    at::Tensor dx, dg, scratch;
+    if (xb + gb + sb <= kFewBytes) {
+      const Parts all{w.empty({xb + gb + sb}, at::kByte)};
+      scratch = all.take(0, {sb}, at::kByte);
+      dx = all.take(sb, {dy.n, dy.width}, dy.t.scalar_type());
+      dg = all.take(sb + xb, {dy.width}, g.scalar_type());
+    } else {
+      dx = w.empty({dy.n, dy.width}, dy.t.scalar_type());
+      dg = w.empty({dy.width}, g.scalar_type());
+      scratch = w.empty({sb}, at::kByte);
+    }
     checked(ebc_norm_grad(w.ctx, dy.t.data_ptr(), dy.ld, h.t.data_ptr(), h.ld, more ? dh.t.data_ptr() : nullptr,
                           dh.ld, dy.type, g.data_ptr(), type_of(g), dy.n, dy.width, (float)real(a[6]),
                           dx.data_ptr(), dg.data_ptr(), (float*)scratch.data_ptr(), w.stream()),
@@ -580,6 +646,7 @@ PyMethodDef g_methods[] = {{"set_raise", py_set_raise, METH_O, nullptr},
                            CALL(route),
                            CALL(route_grad),
                            CALL(norm),
+                           CALL(norm_mx8),
                            CALL(norm_grad),
                            {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_torch_calls", nullptr, -1, g_methods};

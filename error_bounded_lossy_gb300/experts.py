@@ -179,37 +179,42 @@ class Experts:
     def norm(self, x, weight, residual=None, eps: float = 1e-6, stream=None):
         """(y, h): h = x + residual and y = h / sqrt(mean of h^2 over a row + eps) * weight, of x [..., width] and its
         type.  y is of the sum before h is rounded; without a residual h is x.  weight [width] may be of another type."""
-        y, h = self._norm(x, weight, residual, eps, False, True, stream)[2:]
-        return y, h
+        if stream is None:
+            out = _calls.norm(self._h, self._index, x, weight, residual, eps)
+            if out is not None:
+                return out
+        return self._norm(stream, _calls.norm, x, weight, residual, eps)
 
     def norm_mx8(self, x, weight, residual=None, eps: float = 1e-6, wide: bool = False, stream=None):
         """(q, y, h): norm with y in 8 bits as q (Mx8), rounded from fp32; y itself with `wide`, else None.  The
         gradients are those of y and h: q has none."""
+        out = None
+        if stream is None:
+            out = _calls.norm_mx8(self._h, self._index, x, weight, residual, eps, wide)
+        if out is None:
+            out = self._norm(stream, _calls.norm_mx8, x, weight, residual, eps, wide)
         q = _new(Mx8)
-        q.codes, q.scales, y, h = self._norm(x, weight, residual, eps, True, wide, stream)
+        q.codes, q.scales, y, h = out
         q.width = x.shape[-1]
         return q, y, h
 
-    def _norm(self, x, weight, residual, eps, mx8, wide, stream):
-        """codes, scales, y, h; each None where there is none, but h is x without a residual."""
-        if x.dim() != 2:
-            lead, width = x.shape[:-1], x.shape[-1]
-            with _on_stream(stream):   # rows that have to be laid out first are laid out there too
-                flat = x.reshape(-1, width)
-                more = None if residual is None else residual.reshape(-1, width)
-                out = self._norm(flat, weight, more, eps, mx8, wide, None)
-            if stream is not None:
-                _used(None, stream, (x, weight, residual))
-            return (*(None if t is None else t.view(*lead, t.shape[-1]) for t in out[:3]),
-                    x if residual is None else out[3].view(x.shape))
-        args = (x, weight, residual, eps, mx8, wide)
-        if _calls.recorded(x, weight, residual):
-            out = self._recorded(stream, _Norm, *args)
-        elif stream is None:
-            out = _calls.norm(self._h, self._index, *args)
-        else:
-            out = self._on(stream, _calls.norm, *args)
-        return out if residual is not None else (*out[:3], x)
+    def _norm(self, stream, call, x, weight, residual, *how):
+        """norm's or norm_mx8's call on any rows, recorded where it has to be."""
+        if residual is not None and residual.shape != x.shape:
+            raise ValueError("x and residual must have the same shape")
+        with _on_stream(stream):   # rows that have to be laid out first are laid out there too
+            flat = x if x.dim() == 2 else x.reshape(-1, x.shape[-1])
+            more = residual if residual is None or residual.dim() == 2 else residual.reshape(-1, residual.shape[-1])
+            if _calls.recorded(flat, weight, more):
+                out = _Norm.apply(self, call, flat, weight, more, *how)
+            else:
+                out = call(self._h, self._index, flat, weight, more, *how)
+            out = [None if t is None else t.view(*x.shape[:-1], t.shape[-1]) for t in out]
+            if residual is None:
+                out[-1] = x
+        if stream is not None:
+            _used(None, stream, (x, weight, residual))
+        return tuple(out)
 
     def norm_grad(self, dy, h, weight, dh=None, eps: float = 1e-6, stream=None):
         """(dx, dweight) for the gradient dy [rows, width] of norm's y, at its h: dx is the gradient of x and of the
@@ -232,12 +237,14 @@ class Experts:
         kind = _SCORES.get(score)
         if kind is None:
             raise ValueError('score must be "softmax" or "sigmoid"')
-        args = (logits, top, kind, bias, groups, groups if keep_groups is None else keep_groups, group_top,
-                renormalize, scale)
+        keep = groups if keep_groups is None else keep_groups
+        if stream is None:
+            out = _calls.route(self._h, self._index, logits, top, kind, bias, groups, keep, group_top, renormalize, scale)
+            if out is not None:
+                return out
+        args = (logits, top, kind, bias, groups, keep, group_top, renormalize, scale)
         if _calls.recorded(logits):
             return self._recorded(stream, _Route, *args)
-        if stream is None:
-            return _calls.route(self._h, self._index, *args)
         return self._on(stream, _calls.route, *args)
 
     def route_grad(self, dweights, logits, ids, score: str = "softmax", renormalize: bool = True, scale: float = 1.0,
@@ -318,11 +325,12 @@ class Experts:
             x.record_stream(stream)
             return q
         q = _new(kind)
-        q.width = width = x.shape[-1]
-        if x.dim() == 2:
+        shape = x.shape
+        q.width = width = shape[-1]
+        if len(shape) == 2:
             q.codes, q.scales = call(self._h, self._index, x)
         else:
-            lead = x.shape[:-1]
+            lead = shape[:-1]
             q.codes, q.scales = call(self._h, self._index, x.reshape(-1, width))
             q.codes, q.scales = q.codes.view(*lead, q.codes.shape[1]), q.scales.view(*lead, q.scales.shape[1])
         return q
@@ -429,28 +437,29 @@ class _Combine(torch.autograd.Function):
 
 
 class _Norm(torch.autograd.Function):
-    """norm and norm_mx8 on rows: codes, scales, y, h."""
+    """norm's and norm_mx8's calls on rows: what they return, h last (of no use without a residual: it is x)."""
 
     @staticmethod
-    def forward(ctx, ex, x, weight, residual, eps, mx8, wide):
-        ctx.ex, ctx.eps = ex, eps
+    def forward(ctx, ex, call, x, weight, residual, *how):
+        ctx.ex, ctx.eps, ctx.more = ex, how[0], residual is not None
         ctx.set_materialize_grads(False)
-        codes, scales, y, h = _calls.norm(ex._h, ex._index, x, weight, residual, eps, mx8, wide)
-        ctx.save_for_backward(x if residual is None else h, weight)
-        if mx8:
-            ctx.mark_non_differentiable(codes, scales)
-        return codes, scales, y, h
+        *out, h = call(ex._h, ex._index, x, weight, residual, *how)
+        ctx.save_for_backward(h, weight)
+        if len(out) == 3:
+            ctx.mark_non_differentiable(*out[:2])
+        return (*out, h if ctx.more else None)
 
     @staticmethod
     @torch.autograd.function.once_differentiable
-    def backward(ctx, dcodes, dscales, dy, dh):
+    def backward(ctx, *grads):
         h, weight = ctx.saved_tensors
-        dweight = None
-        dx = dh
-        if dy is not None:
-            dx, dweight = ctx.ex.norm_grad(dy.contiguous(), h, weight, None if dh is None else dh.contiguous(), ctx.eps)
+        dweight, dx = None, grads[-1]
+        if grads[-2] is not None:
+            dh = None if dx is None else dx.contiguous()
+            dx, dweight = ctx.ex.norm_grad(grads[-2].contiguous(), h, weight, dh, ctx.eps)
         need = ctx.needs_input_grad
-        return None, dx if need[1] else None, dweight if need[2] else None, dx if need[3] else None, None, None, None
+        return (None, None, dx if need[2] else None, dweight if need[3] else None, dx if need[4] else None,
+                *[None] * (len(need) - 5))
 
 
 class _Route(torch.autograd.Function):

@@ -65,7 +65,7 @@ def calls(lib, ctx, tokens=4, stream=None):
         "route": (lambda: lib.ebc_moe_route(ctx, A, 8, 0, tokens, 8, 2, 1, A, 4, 2, 2, 1, 1.0, A, A, stream), 1),
         "route_grad": (lambda: lib.ebc_moe_route_grad(ctx, A, A, 8, 0, tokens, 8, 2, A, 1, 1, 1.0, A, stream), 1),
         "norm": (lambda: lib.ebc_norm(ctx, A, 64, A, 64, 1, A, 0, tokens, 64, 1e-6, A, A, A, A, stream), 1),
-        "norm_grad": (lambda: lib.ebc_norm_grad(ctx, A, 64, A, 64, A, 64, 1, A, 0, tokens, 64, 1e-6, A, A, A, stream), 2),
+        "norm_grad": (lambda: lib.ebc_norm_grad(ctx, A, 4096, A, 4096, A, 4096, 1, A, 0, tokens, 4096, 1e-6, A, A, A, stream), 2),
     }
 
 
@@ -147,8 +147,9 @@ def test_the_norms_gradient_stays_inside_its_scratch(fake):
         rows, width = int(2 ** rng.uniform(0, 20)), int(2 ** rng.uniform(0, 14))
         for shift in (0, 2, 4, 8, 16):
             assert fake.ebc_norm_grad(ctx, A + shift, width, A, width, None, 0, 1, A, 0, rows, width, 1e-6, A, A, A + 16, None) == 0
-            first, second = launches(fake)
-            assert 1 <= int(first[1]) <= min(rows, 608) and int(second[1]) == -(-width // 32)
+            first, *second = launches(fake)
+            assert 1 <= int(first[1]) <= min(rows, 608)
+            assert [int(x[1]) for x in second] == ([-(-width // 32)] if int(first[1]) > 1 else [])   # one has nothing to add up
     fake.ebc_destroy(ctx)
 
 
