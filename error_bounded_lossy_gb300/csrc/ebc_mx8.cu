@@ -21,6 +21,15 @@ struct Rows {
   uint32_t scale_bytes;
 };
 
+// The row (past the unit's first) and the place in it of vector v, counted from
+// that row's start.  Mostly a unit ends before the second row does.
+template <int kPieces>
+__device__ __forceinline__ void place(const Rows& r, uint32_t v, uint32_t* row, uint32_t* vec) {
+  const uint32_t each = (uint32_t)r.each;
+  *row = each >= 32u * kPieces ? (v >= each ? 1u : 0u) : v / each;
+  *vec = v - *row * each;
+}
+
 // A warp takes kPieces runs of 32 vectors, all in flight at once; a block is
 // 32 / V lanes.  The lanes of a row's last block also fill up its scales.
 // 16 or 32 bits are read and 8.25 written a value: bound by bandwidth.
@@ -39,8 +48,7 @@ __global__ void __launch_bounds__(32 * kWarps) k_mx8_quantize(const T* x, Rows r
     uint32_t row[kPieces], vec[kPieces];
 #pragma unroll
     for (int i = 0; i < kPieces; ++i) {
-      row[i] = (v0 + 32 * i) / (uint32_t)r.each;
-      vec[i] = v0 + 32 * i - row[i] * (uint32_t)r.each;
+      place<kPieces>(r, v0 + 32 * i, &row[i], &vec[i]);
       const int64_t t = t0 + row[i], left = t < r.rows ? r.width - (int64_t)vec[i] * V : 0;
       const T* p = x + t * r.ld + (int64_t)vec[i] * V;
       if (left >= V) {
@@ -53,8 +61,7 @@ __global__ void __launch_bounds__(32 * kWarps) k_mx8_quantize(const T* x, Rows r
 #pragma unroll
     for (int i = 0; i < kPieces; ++i) {
       float f[V];
-#pragma unroll
-      for (int k = 0; k < V; ++k) f[k] = to_f32(in[i].e[k]);
+      in[i].get(f);
       const uint32_t s = mx8_scale(mx8_block_max<V>(f));
       const int64_t t = t0 + row[i];
       if (t >= r.rows) continue;
@@ -83,8 +90,7 @@ __global__ void __launch_bounds__(32 * kWarps) k_mx8_dequantize(const uint8_t* c
     uint32_t s[kPieces], row[kPieces], vec[kPieces];
 #pragma unroll
     for (int i = 0; i < kPieces; ++i) {
-      row[i] = (v0 + 32 * i) / (uint32_t)r.each;
-      vec[i] = v0 + 32 * i - row[i] * (uint32_t)r.each;
+      place<kPieces>(r, v0 + 32 * i, &row[i], &vec[i]);
       const int64_t t = t0 + row[i];
       if (t >= r.rows) continue;
       const uint8_t* p = codes + t * code_bytes + (int64_t)vec[i] * V;
@@ -103,12 +109,14 @@ __global__ void __launch_bounds__(32 * kWarps) k_mx8_dequantize(const uint8_t* c
       if (t >= r.rows) continue;
       const float unit = mx8_unit(s[i]);
       Values<T, V> out;
+      float f[V];
 #pragma unroll
       for (int k = 0; k < V; k += 2) {
-        const float2 f = mx8_values2((k < 4 ? c[i].x : c[i].y) >> (8 * (k & 3)));
-        out.e[k] = from_f32<T>(f.x * unit);
-        if constexpr (V > 1) out.e[k + 1] = from_f32<T>(f.y * unit);
+        const float2 v = mx8_values2((k < 4 ? c[i].x : c[i].y) >> (8 * (k & 3)));
+        f[k] = v.x * unit;
+        if constexpr (V > 1) f[k + 1] = v.y * unit;
       }
+      out.set(f);
       const int64_t left = r.width - (int64_t)vec[i] * V;
       T* p = x + t * r.width + (int64_t)vec[i] * V;
       if (left >= V) {

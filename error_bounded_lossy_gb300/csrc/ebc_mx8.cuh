@@ -2,6 +2,8 @@
 // scale, a value's code, and back; and a row's values between memory and lanes.
 #pragma once
 
+#include <type_traits>
+
 #include "ebc_types.cuh"
 
 namespace ebc {
@@ -83,7 +85,44 @@ struct Values {
   }
   __device__ __forceinline__ void zero() {
 #pragma unroll
-    for (int k = 0; k < V; ++k) e[k] = from_f32<T>(0.f);
+    for (int k = 0; k < kWords; ++k) word[k] = 0u;
+  }
+  // As fp32, and from fp32 to nearest: two 16-bit values at a time, which is half
+  // of the instructions that one at a time takes, and less.
+  __device__ __forceinline__ void get(float (&f)[V]) const {
+    if constexpr (sizeof(T) == 4 || V == 1) {
+#pragma unroll
+      for (int k = 0; k < V; ++k) f[k] = to_f32(e[k]);
+    } else {
+#pragma unroll
+      for (int k = 0; k < V / 2; ++k) {
+        if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+          f[2 * k] = __uint_as_float(word[k] << 16);
+          f[2 * k + 1] = __uint_as_float(word[k] & 0xFFFF0000u);
+        } else {
+          const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&word[k]));
+          f[2 * k] = v.x;
+          f[2 * k + 1] = v.y;
+        }
+      }
+    }
+  }
+  __device__ __forceinline__ void set(const float (&f)[V]) {
+    if constexpr (sizeof(T) == 4 || V == 1) {
+#pragma unroll
+      for (int k = 0; k < V; ++k) e[k] = from_f32<T>(f[k]);
+    } else {
+#pragma unroll
+      for (int k = 0; k < V / 2; ++k) {
+        if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+          const __nv_bfloat162 v = __floats2bfloat162_rn(f[2 * k], f[2 * k + 1]);
+          word[k] = *reinterpret_cast<const uint32_t*>(&v);
+        } else {
+          const __half2 v = __floats2half2_rn(f[2 * k], f[2 * k + 1]);
+          word[k] = *reinterpret_cast<const uint32_t*>(&v);
+        }
+      }
+    }
   }
 };
 
@@ -93,30 +132,34 @@ inline int row_values(uintptr_t addresses, int elem) {
   return addresses % (uintptr_t)(8 * elem) == 0 ? 8 : addresses % (uintptr_t)(2 * elem) == 0 ? 2 : 1;
 }
 
-// A block's largest magnitude (its bits: magnitudes order as their bits do, and
-// a NaN's are above an infinity's), of the 32 / V lanes that hold it.
+// A block's largest magnitude (its bits; of a NaN, all of them but the sign), of
+// the 32 / V lanes that hold it.
 template <int V>
 __device__ __forceinline__ uint32_t mx8_block_max(const float (&f)[V]) {
-  uint32_t top = 0;
+  float top = fabsf(f[0]);
 #pragma unroll
-  for (int k = 0; k < V; ++k) top = max(top, __float_as_uint(f[k]) & 0x7FFFFFFFu);
+  for (int k = 1; k < V; ++k) asm("max.NaN.f32 %0, %0, %1;" : "+f"(top) : "f"(fabsf(f[k])));
+  // (magnitudes order as their bits do, and a NaN's are above an infinity's)
   if constexpr (V == 1) {
-    return __reduce_max_sync(0xffffffffu, top);
+    return __reduce_max_sync(0xffffffffu, __float_as_uint(top));
   } else {
+    uint32_t bits = __float_as_uint(top);
 #pragma unroll
-    for (int off = 1; off < 32 / V; off <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, off));
-    return top;
+    for (int off = 1; off < 32 / V; off <<= 1) bits = max(bits, __shfl_xor_sync(0xffffffffu, bits, off));
+    return bits & 0x7FFFFFFFu;
   }
 }
 
 // The lane's codes of a block with that scale, to `codes` (aligned to V).
 template <int V>
 __device__ __forceinline__ void mx8_store(const float (&f)[V], uint32_t scale, uint8_t* codes) {
-  const float inv = scale == 255u ? 0.f : mx8_inverse(scale);
-  auto code2 = [&](float lo, float hi) { return scale == 255u ? 0u : mx8_codes2(lo * inv, hi * inv); };
+  const float inv = mx8_inverse(scale);   // (of 255: not used)
+  const uint32_t keep = scale == 255u ? 0u : ~0u;
+  auto code2 = [&](float lo, float hi) { return mx8_codes2(lo * inv, hi * inv) & keep; };
   if constexpr (V == 8) {
-    const uint32_t a = code2(f[0], f[1]) | code2(f[2], f[3]) << 16, b = code2(f[4], f[5]) | code2(f[6], f[7]) << 16;
-    *reinterpret_cast<uint2*>(codes) = make_uint2(a, b);
+    const uint32_t a = mx8_codes2(f[0] * inv, f[1] * inv) | mx8_codes2(f[2] * inv, f[3] * inv) << 16;
+    const uint32_t b = mx8_codes2(f[4] * inv, f[5] * inv) | mx8_codes2(f[6] * inv, f[7] * inv) << 16;
+    *reinterpret_cast<uint2*>(codes) = make_uint2(a & keep, b & keep);
   } else if constexpr (V == 2) {
     *reinterpret_cast<uint16_t*>(codes) = (uint16_t)code2(f[0], f[1]);
   } else {

@@ -38,15 +38,88 @@ __device__ __forceinline__ void group_sum(float (&v)[K], float (*part)[K][kMaxTh
   }
 }
 
-// V weights from the i-th on, of the type that the caller keeps them in.
+// ---- two fp32 numbers in one register pair, and arithmetic on both at once ----
+using Two = uint64_t;
+__device__ __forceinline__ Two two(float lo, float hi) {
+  Two r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ float2 parts_of(Two v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ Two add2(Two a, Two b) {
+  Two r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ Two mul2(Two a, Two b) {
+  Two r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ Two fma2(Two a, Two b, Two c) {
+  Two r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
+// A thread's values are taken in chunks: one vector, or two of a single value.
 template <int V>
-__device__ __forceinline__ void load_weights(const void* w, int type, int64_t i, float (&f)[V]) {
+struct Chunk {
+  static constexpr int kVecs = V == 1 ? 2 : 1, kTwos = V * kVecs / 2;
+};
+template <typename T, int V>
+__device__ __forceinline__ void widen(const Values<T, V>* v, Two (&p)[Chunk<V>::kTwos]) {
+  if constexpr (V == 1) {
+    p[0] = two(to_f32(v[0].e[0]), to_f32(v[1].e[0]));
+  } else {
+    float f[V];
+    v[0].get(f);
+#pragma unroll
+    for (int k = 0; k < V / 2; ++k) p[k] = two(f[2 * k], f[2 * k + 1]);
+  }
+}
+template <int V>
+__device__ __forceinline__ void split(const Two (&p)[Chunk<V>::kTwos], float (&f)[V * Chunk<V>::kVecs]) {
+#pragma unroll
+  for (int k = 0; k < Chunk<V>::kTwos; ++k) {
+    const float2 v = parts_of(p[k]);
+    f[2 * k] = v.x;
+    f[2 * k + 1] = v.y;
+  }
+}
+// To the vectors' type, rounded to nearest.
+template <typename T, int V>
+__device__ __forceinline__ void narrow(const Two (&p)[Chunk<V>::kTwos], Values<T, V>* v) {
+  float f[V * Chunk<V>::kVecs];
+  split<V>(p, f);
+  if constexpr (V == 1) {
+    v[0].e[0] = from_f32<T>(f[0]);
+    v[1].e[0] = from_f32<T>(f[1]);
+  } else {
+    v[0].set(f);
+  }
+}
+
+// A chunk's weights, of the type that the caller keeps them in; zero past the
+// row's end.
+template <int V>
+__device__ __forceinline__ void load_weights(const void* w, int type, int c, int hop, int width,
+                                             Two (&p)[Chunk<V>::kTwos]) {
   auto get = [&](auto one) {
     using W = decltype(one);
-    Values<W, V> v;
-    v.load((const W*)w + i);
+    Values<W, V> v[Chunk<V>::kVecs];
 #pragma unroll
-    for (int k = 0; k < V; ++k) f[k] = to_f32(v.e[k]);
+    for (int i = 0; i < Chunk<V>::kVecs; ++i) {
+      if (c + i * hop < width)
+        v[i].load((const W*)w + c + i * hop);
+      else
+        v[i].zero();
+    }
+    widen<W, V>(v, p);
   };
   if (type == EBC_F32)
     get(float());
@@ -74,63 +147,106 @@ template <typename T, int V, int N, int kLanes>
 __global__ void __launch_bounds__(kMaxThreads) k_norm(NormArgs a) {
   __shared__ float part[2][1][kMaxThreads / 32];
   pdl_enter();
+  using C = Chunk<V>;
+  constexpr int kChunks = N / C::kVecs;
   const int lanes = kLanes ? kLanes : blockDim.x, at = threadIdx.x % lanes, groups = blockDim.x / lanes;
   const int64_t step = (int64_t)gridDim.x * groups;
   const int padded = (a.width + 31) / 32 * 32;
   const float share = 1.f / (float)a.width;
+  // single weights stay in registers where there is room for them; vectors of them
+  // are read again (a wait for them ahead of the first row: 43 -> 49 us of 8192 x 4096 bf16)
+  constexpr bool kKeep = V < 8 && N * V <= 16;
+  const int c0 = at * V, hop = lanes * V;   // the thread's first column, and to the next
+  Two kept[kKeep ? kChunks : 1][C::kTwos];
+  if constexpr (kKeep)
+#pragma unroll
+    for (int q = 0; q < kChunks; ++q)
+      load_weights<V>(a.w, a.w_type, c0 + q * C::kVecs * hop, hop, a.width, kept[q]);
   int turn = 0;
   // the groups of a warp, and the warps of a CTA, go through the same rounds
   for (int64_t row0 = (int64_t)blockIdx.x * groups; row0 < a.rows; row0 += step, turn ^= 1) {
     const int64_t row = row0 + threadIdx.x / lanes;
     const bool live = row < a.rows;
-    Values<T, V> xv[N], rv[N];
+    Values<T, V> xv[N];
+    Two f[kChunks][C::kTwos];
+    auto load = [&](const void* rows, int64_t ld) {
+      const T* p = (const T*)rows + row * ld + c0;
 #pragma unroll
-    for (int n = 0; n < N; ++n) {
-      const int c = (n * lanes + at) * V;
-      if (live && c < a.width) {
-        xv[n].load((const T*)a.x + row * a.ld_x + c);
-        if (a.r) rv[n].load((const T*)a.r + row * a.ld_r + c);
-      } else {
-        xv[n].zero();
-        rv[n].zero();
+      for (int n = 0; n < N; ++n) {
+        if (live && c0 + n * hop < a.width)
+          xv[n].load(p + n * hop);
+        else
+          xv[n].zero();
       }
-    }
-    float f[N][V], sum[1] = {0.f};
+    };
+    auto store = [&](void* rows) {
+      T* p = (T*)rows + row * a.width + c0;
 #pragma unroll
-    for (int n = 0; n < N; ++n) {
-      const int c = (n * lanes + at) * V;
-      Values<T, V> hv;
+      for (int q = 0; q < kChunks; ++q) narrow<T, V>(f[q], xv + q * C::kVecs);
 #pragma unroll
-      for (int k = 0; k < V; ++k) {
-        f[n][k] = to_f32(xv[n].e[k]);
-        if (a.r) f[n][k] += to_f32(rv[n].e[k]);
-        hv.e[k] = from_f32<T>(f[n][k]);
-        sum[0] += f[n][k] * f[n][k];
+      for (int n = 0; n < N; ++n)
+        if (live && c0 + n * hop < a.width) xv[n].store(p + n * hop);
+    };
+    load(a.x, a.ld_x);
+    if (a.r) {
+      Values<T, V> rv[N];
+      const T* p = (const T*)a.r + row * a.ld_r + c0;
+#pragma unroll
+      for (int n = 0; n < N; ++n) {
+        if (live && c0 + n * hop < a.width)
+          rv[n].load(p + n * hop);
+        else
+          rv[n].zero();
       }
-      if (a.h && live && c < a.width) hv.store((T*)a.h + row * a.width + c);
+#pragma unroll
+      for (int q = 0; q < kChunks; ++q) {
+        Two g[C::kTwos];
+        widen<T, V>(xv + q * C::kVecs, f[q]);
+        widen<T, V>(rv + q * C::kVecs, g);
+#pragma unroll
+        for (int k = 0; k < C::kTwos; ++k) f[q][k] = add2(f[q][k], g[k]);
+      }
+    } else {
+#pragma unroll
+      for (int q = 0; q < kChunks; ++q) widen<T, V>(xv + q * C::kVecs, f[q]);
     }
+    if (a.h) store(a.h);
+    Two squares = 0;
+#pragma unroll
+    for (int q = 0; q < kChunks; ++q)
+#pragma unroll
+      for (int k = 0; k < C::kTwos; ++k) squares = fma2(f[q][k], f[q][k], squares);
+    float sum[1] = {parts_of(squares).x + parts_of(squares).y};
     group_sum<kLanes>(sum, part, turn);
     const float scale = rsqrtf(sum[0] * share + a.eps);
+    const Two scales2 = two(scale, scale);
 #pragma unroll
-    for (int n = 0; n < N; ++n) {
-      const int c = (n * lanes + at) * V;
-      if (c < a.width) {
-        float w[V];
-        load_weights<V>(a.w, a.w_type, c, w);
+    for (int q = 0; q < kChunks; ++q) {
+      Two w[C::kTwos];
+      if constexpr (!kKeep) load_weights<V>(a.w, a.w_type, c0 + q * C::kVecs * hop, hop, a.width, w);
 #pragma unroll
-        for (int k = 0; k < V; ++k) f[n][k] = f[n][k] * scale * w[k];
-      }
-      if (a.y && live && c < a.width) {
-        Values<T, V> yv;
+      for (int k = 0; k < C::kTwos; ++k) f[q][k] = mul2(mul2(f[q][k], scales2), kKeep ? kept[kKeep ? q : 0][k] : w[k]);
+    }
+    if (a.y) store(a.y);
+    if (a.codes) {
+      uint8_t* codes = a.codes + row * padded + c0;
+      uint8_t* scales = a.scales + row * EBC_MX8_SCALE_BYTES(a.width) + c0 / 32;
 #pragma unroll
-        for (int k = 0; k < V; ++k) yv.e[k] = from_f32<T>(f[n][k]);
-        yv.store((T*)a.y + row * a.width + c);
-      }
-      if (a.codes) {
-        const uint32_t s = mx8_scale(mx8_block_max<V>(f[n]));   // (values past the row's end are zero)
-        if (live && c < padded) {
-          mx8_store<V>(f[n], s, a.codes + row * padded + c);
-          if (c % 32 == 0) a.scales[row * EBC_MX8_SCALE_BYTES(a.width) + c / 32] = (uint8_t)s;
+      for (int q = 0; q < kChunks; ++q) {
+        float g[V * C::kVecs];
+        split<V>(f[q], g);
+        // (values past the row's end are zero, or NaN beside an infinite sum)
+#pragma unroll
+        for (int i = 0; i < C::kVecs; ++i) {
+          const int n = q * C::kVecs + i;
+          float v[V];
+#pragma unroll
+          for (int k = 0; k < V; ++k) v[k] = c0 + n * hop < a.width ? g[i * V + k] : 0.f;
+          const uint32_t s = mx8_scale(mx8_block_max<V>(v));
+          if (live && c0 + n * hop < padded) {
+            mx8_store<V>(v, s, codes + n * hop);
+            if (c0 % 32 == 0) scales[n * hop / 32] = (uint8_t)s;
+          }
         }
       }
     }
@@ -205,49 +321,45 @@ struct Ring {
 template <typename T, int V, int N, int kLanes, int kStages>
 __global__ void __launch_bounds__(kLanes ? kRowThreads : kMaxThreads) k_norm_grad(GradArgs a) {
   using R = Ring<T, V, N, kStages>;
+  using C = Chunk<V>;
+  constexpr int kChunks = N / C::kVecs;
   __shared__ float part[2][2][kMaxThreads / 32];
   pdl_enter();
   const int lanes = kLanes ? kLanes : blockDim.x, at = threadIdx.x % lanes, groups = blockDim.x / lanes;
   const int64_t step = (int64_t)gridDim.x * groups;
   const float share = 1.f / (float)a.width;
-  constexpr bool kKeep = N * V <= 16;   // the weights stay in registers
-  float dw[N][V], kept[kKeep ? N : 1][V];
-#pragma unroll
-  for (int n = 0; n < N; ++n) {
-#pragma unroll
-    for (int k = 0; k < V; ++k) dw[n][k] = 0.f;
-    if constexpr (kKeep) {
-      const int c = (n * lanes + at) * V;
-#pragma unroll
-      for (int k = 0; k < V; ++k) kept[n][k] = 0.f;
-      if (c < a.width) load_weights<V>(a.w, a.w_type, c, kept[n]);
-    }
-  }
-  auto weights = [&](int n, int c, float (&w)[V]) {
-    if constexpr (kKeep) {
-#pragma unroll
-      for (int k = 0; k < V; ++k) w[k] = kept[n][k];
-    } else {
-      load_weights<V>(a.w, a.w_type, c, w);
-    }
-  };
+  const int c0 = at * V, hop = lanes * V;   // the thread's first column, and to the next
   auto request = [&](int64_t row, int stage) {
     if constexpr (kStages > 0) {
       if (row < a.rows) {
+        const T* h = (const T*)a.h + row * a.ld_h + c0;
+        const T* g = (const T*)a.dy + row * a.ld_dy + c0;
 #pragma unroll
         for (int n = 0; n < N; ++n) {
-          const int c = (n * lanes + at) * V;
-          if (c >= a.width) continue;
-          R::copy(stage, 0, n, (const T*)a.h + row * a.ld_h + c);
-          R::copy(stage, 1, n, (const T*)a.dy + row * a.ld_dy + c);
-          if (a.dh) R::copy(stage, 2, n, (const T*)a.dh + row * a.ld_dh + c);
+          if (c0 + n * hop >= a.width) continue;
+          R::copy(stage, 0, n, h + n * hop);
+          R::copy(stage, 1, n, g + n * hop);
+        }
+        if (a.dh) {
+          const T* e = (const T*)a.dh + row * a.ld_dh + c0;
+#pragma unroll
+          for (int n = 0; n < N; ++n)
+            if (c0 + n * hop < a.width) R::copy(stage, 2, n, e + n * hop);
         }
       }
       R::commit();
     }
   };
-  int turn = 0, stage = 0;
   for (int i = 0; i < kStages - 1; ++i) request((int64_t)blockIdx.x * groups + i * step, i);
+  constexpr bool kKeep = N * V <= 16;   // the weights stay in registers
+  Two dw[kChunks][C::kTwos], kept[kKeep ? kChunks : 1][C::kTwos];
+#pragma unroll
+  for (int q = 0; q < kChunks; ++q) {
+#pragma unroll
+    for (int k = 0; k < C::kTwos; ++k) dw[q][k] = 0;
+    if constexpr (kKeep) load_weights<V>(a.w, a.w_type, c0 + q * C::kVecs * hop, hop, a.width, kept[q]);
+  }
+  int turn = 0, stage = 0;
   for (int64_t row0 = (int64_t)blockIdx.x * groups; row0 < a.rows; row0 += step, turn ^= 1) {
     const int64_t row = row0 + threadIdx.x / lanes;
     const bool live = row < a.rows;
@@ -256,76 +368,112 @@ __global__ void __launch_bounds__(kLanes ? kRowThreads : kMaxThreads) k_norm_gra
       request(row0 + (kStages - 1) * step, stage == 0 ? kStages - 1 : stage - 1);
       R::wait();
     }
+    if constexpr (kStages > 0) {
 #pragma unroll
-    for (int n = 0; n < N; ++n) {
-      const int c = (n * lanes + at) * V;
-      if (live && c < a.width) {
-        if constexpr (kStages > 0) {
+      for (int n = 0; n < N; ++n) {
+        if (c0 + n * hop < a.width) {
           R::get(stage, 0, n, &hv[n]);
           R::get(stage, 1, n, &gv[n]);
         } else {
-          hv[n].load((const T*)a.h + row * a.ld_h + c);
-          gv[n].load((const T*)a.dy + row * a.ld_dy + c);
-          if (a.dh) ev[n].load((const T*)a.dh + row * a.ld_dh + c);
+          hv[n].zero();
+          gv[n].zero();
         }
-      } else {
-        hv[n].zero();
-        gv[n].zero();
+      }
+    } else {
+      const T* h = (const T*)a.h + row * a.ld_h + c0;
+      const T* g = (const T*)a.dy + row * a.ld_dy + c0;
+#pragma unroll
+      for (int n = 0; n < N; ++n) {
+        if (live && c0 + n * hop < a.width) {
+          hv[n].load(h + n * hop);
+          gv[n].load(g + n * hop);
+        } else {
+          hv[n].zero();
+          gv[n].zero();
+        }
+      }
+      if (a.dh && live) {
+        const T* e = (const T*)a.dh + row * a.ld_dh + c0;
+#pragma unroll
+        for (int n = 0; n < N; ++n)
+          if (c0 + n * hop < a.width) ev[n].load(e + n * hop);
       }
     }
-    float sum[2] = {0.f, 0.f};
+    // (past the row's end everything is zero)
+    Two squares = 0, inner = 0;
 #pragma unroll
-    for (int n = 0; n < N; ++n) {
-      const int c = (n * lanes + at) * V;
-      if (c >= a.width) continue;
-      float w[V];
-      weights(n, c, w);
+    for (int q = 0; q < kChunks; ++q) {
+      Two w[C::kTwos], h[C::kTwos], g[C::kTwos];
+      if constexpr (!kKeep) load_weights<V>(a.w, a.w_type, c0 + q * C::kVecs * hop, hop, a.width, w);
+      widen<T, V>(hv + q * C::kVecs, h);
+      widen<T, V>(gv + q * C::kVecs, g);
 #pragma unroll
-      for (int k = 0; k < V; ++k) {
-        const float h = to_f32(hv[n].e[k]);
-        sum[0] += h * h;
-        sum[1] += to_f32(gv[n].e[k]) * w[k] * h;
+      for (int k = 0; k < C::kTwos; ++k) {
+        squares = fma2(h[k], h[k], squares);
+        inner = fma2(mul2(g[k], kKeep ? kept[kKeep ? q : 0][k] : w[k]), h[k], inner);
       }
     }
+    float sum[2] = {parts_of(squares).x + parts_of(squares).y, parts_of(inner).x + parts_of(inner).y};
     group_sum<kLanes>(sum, part, turn);
     const float scale = rsqrtf(sum[0] * share + a.eps), mean = sum[1] * share * scale;
     if (live) {
+      const Two scale2 = two(scale, scale), mean2 = two(-mean, -mean);
+      T* dx = (T*)a.dx + row * a.width + c0;
 #pragma unroll
-      for (int n = 0; n < N; ++n) {
-        const int c = (n * lanes + at) * V;
-        if (c >= a.width) continue;
-        float w[V];
-        weights(n, c, w);
-        Values<T, V> out;
-        if constexpr (kStages > 0)
-          if (a.dh) R::get(stage, 2, n, &ev[n]);
+      for (int q = 0; q < kChunks; ++q) {
+        Two w[C::kTwos], h[C::kTwos], g[C::kTwos], d[C::kTwos];
+        if constexpr (!kKeep) load_weights<V>(a.w, a.w_type, c0 + q * C::kVecs * hop, hop, a.width, w);
+        widen<T, V>(hv + q * C::kVecs, h);
+        widen<T, V>(gv + q * C::kVecs, g);
 #pragma unroll
-        for (int k = 0; k < V; ++k) {
-          const float u = to_f32(hv[n].e[k]) * scale, g = to_f32(gv[n].e[k]);
-          float d = scale * (g * w[k] - u * mean);
-          if (a.dh) d += to_f32(ev[n].e[k]);
-          out.e[k] = from_f32<T>(d);
-          dw[n][k] += g * u;
+        for (int k = 0; k < C::kTwos; ++k) {
+          const Two u = mul2(h[k], scale2);
+          d[k] = mul2(fma2(u, mean2, mul2(g[k], kKeep ? kept[kKeep ? q : 0][k] : w[k])), scale2);
+          dw[q][k] = fma2(g[k], u, dw[q][k]);
         }
-        out.store((T*)a.dx + row * a.width + c);
+        if (a.dh) {
+          Two e[C::kTwos];
+          if constexpr (kStages > 0) {
+#pragma unroll
+            for (int i = 0; i < C::kVecs; ++i)
+              if (c0 + (q * C::kVecs + i) * hop < a.width) R::get(stage, 2, q * C::kVecs + i, &ev[q * C::kVecs + i]);
+          }
+          widen<T, V>(ev + q * C::kVecs, e);
+#pragma unroll
+          for (int k = 0; k < C::kTwos; ++k) d[k] = add2(d[k], e[k]);
+        }
+        Values<T, V> out[C::kVecs];
+        narrow<T, V>(d, out);
+#pragma unroll
+        for (int i = 0; i < C::kVecs; ++i)
+          if (c0 + (q * C::kVecs + i) * hop < a.width) out[i].store(dx + (q * C::kVecs + i) * hop);
       }
     }
     if (++stage >= kStages) stage = 0;
   }
+  float sums[N * V];   // vector n's values from n * V on
+#pragma unroll
+  for (int q = 0; q < kChunks; ++q)
+#pragma unroll
+    for (int k = 0; k < C::kTwos; ++k) {
+      const float2 v = parts_of(dw[q][k]);
+      sums[2 * (q * C::kTwos + k)] = v.x;
+      sums[2 * (q * C::kTwos + k) + 1] = v.y;
+    }
   float* mine = a.parts + (int64_t)blockIdx.x * a.width;
   if constexpr (kLanes == 0) {
 #pragma unroll
     for (int n = 0; n < N; ++n) {
-      const int c = (n * lanes + at) * V;
+      const int c = c0 + n * hop;
       if (c >= a.width) continue;
       if (gridDim.x == 1) {   // nothing to add up
 #pragma unroll
-        for (int k = 0; k < V; ++k) store_dweight(a.dw, a.w_type, c + k, dw[n][k]);
+        for (int k = 0; k < V; ++k) store_dweight(a.dw, a.w_type, c + k, sums[n * V + k]);
         continue;
       }
       Values<float, V> out;
 #pragma unroll
-      for (int k = 0; k < V; ++k) out.e[k] = dw[n][k];
+      for (int k = 0; k < V; ++k) out.e[k] = sums[n * V + k];
       out.store(mine + c);
     }
   } else {
@@ -337,8 +485,8 @@ __global__ void __launch_bounds__(kLanes ? kRowThreads : kMaxThreads) k_norm_gra
         for (int n = 0; n < N; ++n)
 #pragma unroll
           for (int k = 0; k < V; ++k) {
-            float* p = all + (n * lanes + at) * V + k;
-            *p = g ? *p + dw[n][k] : dw[n][k];
+            float* p = all + c0 + n * hop + k;
+            *p = g ? *p + sums[n * V + k] : sums[n * V + k];
           }
       __syncthreads();
     }
@@ -390,7 +538,6 @@ cudaError_t with_layout(int v, int width, F&& f) {
     if (width <= 128) return f(Layout<T, 8, 1, 16>{}, kRowThreads);
     if (width <= 256) return f(Layout<T, 8, 1, 32>{}, kRowThreads);
     if (width <= 512) return f(Layout<T, 8, 2, 32>{}, kRowThreads);
-    if (width <= 2048) return cta(Layout<T, 8, 1, 0>{});
     if (width <= 8192) return cta(Layout<T, 8, 2, 0>{});
     return cta(Layout<T, 8, 4, 0>{});
   }
@@ -502,11 +649,11 @@ int ebc_norm_grad(ebc_ctx* ctx, const void* d_dy, int64_t ld_dy, const void* d_h
         const int groups = L::kLanes ? threads / L::kLanes : 1;
         const int64_t want = (rows + groups - 1) / groups;
         // all CTAs at once: by their registers (at most 128 a thread) and shared memory
-        constexpr int kFit = L::N * L::V <= 8 ? 1024 : 512;
+        constexpr int kFit = L::N * L::V <= 8 ? 1024 : L::N * L::V <= 16 ? 640 : 512;
         int64_t each = kFit / threads < 1 ? 1 : kFit / threads;
         if (smem && each > (int64_t)((220 * 1024) / (smem + 2048))) each = (int64_t)((220 * 1024) / (smem + 2048));
         int64_t most = (int64_t)v.nsm * (each < 1 ? 1 : each);
-        if (most > EBC_NORM_GRAD_PARTS) most = EBC_NORM_GRAD_PARTS;
+        if (most > EBC_NORM_GRAD_PARTS(width)) most = EBC_NORM_GRAD_PARTS(width);
         a.n_parts = (int)(want < most ? want : most);
         return launch_named(v, "k_norm_grad", st, kernel, dim3((unsigned)a.n_parts), dim3(threads), smem, 1, a);
       });
