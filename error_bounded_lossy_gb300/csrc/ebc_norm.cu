@@ -12,25 +12,27 @@ constexpr int kRowThreads = 256;   // of a CTA whose rows take a warp or less ea
 
 // ---- one row on a group of threads ----
 // A thread has N vectors of V consecutive values: vector n * lanes + its place
-// in the group.  kLanes: the lanes of a warp that a row takes; 0: the whole CTA.
+// in the group.  kLanes: the lanes of a warp that a row takes; 0: whole warps
+// (`lanes` threads), all of the CTA or one of several such groups.
 
 // The group's sums of K values a thread, the same in all its threads.  `part`
 // has room for two rows, so one barrier a row is enough.
 template <int kLanes, int K>
-__device__ __forceinline__ void group_sum(float (&v)[K], float (*part)[K][kMaxThreads / 32], int turn) {
+__device__ __forceinline__ void group_sum(float (&v)[K], float (*part)[K][kMaxThreads / 32], int turn, int lanes) {
 #pragma unroll
   for (int off = (kLanes ? kLanes : 32) / 2; off > 0; off >>= 1)
 #pragma unroll
     for (int k = 0; k < K; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], off);
   if constexpr (kLanes == 0) {
-    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, warps = lanes >> 5, group = w / warps;
     if (lane == 0)
 #pragma unroll
       for (int k = 0; k < K; ++k) part[turn][k][w] = v[k];
-    __syncthreads();
+    // (barrier 0 is __syncthreads')
+    asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(lanes) : "memory");
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      float s = lane < warps ? part[turn][k][lane] : 0.f;
+      float s = lane < warps ? part[turn][k][group * warps + lane] : 0.f;
 #pragma unroll
       for (int off = kMaxThreads / 64; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
       v[k] = __shfl_sync(0xffffffffu, s, 0);
@@ -217,7 +219,7 @@ __global__ void __launch_bounds__(kMaxThreads) k_norm(NormArgs a) {
 #pragma unroll
       for (int k = 0; k < C::kTwos; ++k) squares = fma2(f[q][k], f[q][k], squares);
     float sum[1] = {parts_of(squares).x + parts_of(squares).y};
-    group_sum<kLanes>(sum, part, turn);
+    group_sum<kLanes>(sum, part, turn, lanes);
     const float scale = rsqrtf(sum[0] * share + a.eps);
     const Two scales2 = two(scale, scale);
 #pragma unroll
@@ -319,18 +321,19 @@ struct Ring {
 // Bound by bandwidth, if loads are in flight while a row's sums go around the
 // CTA: with kStages, the rows to come are copied to shared memory meanwhile.
 template <typename T, int V, int N, int kLanes, int kStages>
-__global__ void __launch_bounds__(kLanes ? kRowThreads : kMaxThreads) k_norm_grad(GradArgs a) {
+__global__ void __launch_bounds__(kLanes ? kRowThreads : kMaxThreads) k_norm_grad(GradArgs a, int row_lanes) {
   using R = Ring<T, V, N, kStages>;
   using C = Chunk<V>;
   constexpr int kChunks = N / C::kVecs;
   __shared__ float part[2][2][kMaxThreads / 32];
   pdl_enter();
-  const int lanes = kLanes ? kLanes : blockDim.x, at = threadIdx.x % lanes, groups = blockDim.x / lanes;
+  const int lanes = kLanes ? kLanes : row_lanes, at = threadIdx.x % lanes, groups = blockDim.x / lanes;
   const int64_t step = (int64_t)gridDim.x * groups;
   const float share = 1.f / (float)a.width;
   const int c0 = at * V, hop = lanes * V;   // the thread's first column, and to the next
-  auto request = [&](int64_t row, int stage) {
+  auto request = [&](int64_t row, int stage) {   // row: of the CTA's first group
     if constexpr (kStages > 0) {
+      row += threadIdx.x / lanes;
       if (row < a.rows) {
         const T* h = (const T*)a.h + row * a.ld_h + c0;
         const T* g = (const T*)a.dy + row * a.ld_dy + c0;
@@ -414,7 +417,7 @@ __global__ void __launch_bounds__(kLanes ? kRowThreads : kMaxThreads) k_norm_gra
       }
     }
     float sum[2] = {parts_of(squares).x + parts_of(squares).y, parts_of(inner).x + parts_of(inner).y};
-    group_sum<kLanes>(sum, part, turn);
+    group_sum<kLanes>(sum, part, turn, lanes);
     const float scale = rsqrtf(sum[0] * share + a.eps), mean = sum[1] * share * scale;
     if (live) {
       const Two scale2 = two(scale, scale), mean2 = two(-mean, -mean);
@@ -461,7 +464,7 @@ __global__ void __launch_bounds__(kLanes ? kRowThreads : kMaxThreads) k_norm_gra
       sums[2 * (q * C::kTwos + k) + 1] = v.y;
     }
   float* mine = a.parts + (int64_t)blockIdx.x * a.width;
-  if constexpr (kLanes == 0) {
+  if (groups == 1) {
 #pragma unroll
     for (int n = 0; n < N; ++n) {
       const int c = c0 + n * hop;
@@ -478,7 +481,9 @@ __global__ void __launch_bounds__(kLanes ? kRowThreads : kMaxThreads) k_norm_gra
     }
   } else {
     // the CTA's groups one after the other, so that the order is the same in every run
-    __shared__ float all[N * V * kLanes];
+    extern __shared__ uint4 ring[];   // (rows to come: none any more)
+    float* all = reinterpret_cast<float*>(ring);
+    __syncthreads();
     for (int g = 0; g < groups; ++g) {
       if ((int)threadIdx.x / lanes == g)
 #pragma unroll
@@ -633,29 +638,37 @@ int ebc_norm_grad(ebc_ctx* ctx, const void* d_dy, int64_t ld_dy, const void* d_h
     e = with_type_of(type, [&](auto one) {
       return with_layout<decltype(one)>(vals < vals_s ? vals : vals_s, (int)width, [&](auto l, int threads) {
         using L = decltype(l);
-        // A row a CTA of whole vectors: rows to come in shared memory, as many as
-        // two CTAs an SM have room for.
-        constexpr int kBytes = 3 * L::N * L::V * (int)sizeof(typename L::T) * kMaxThreads;
-        constexpr int kStages = L::kLanes || L::V < 8 ? 0 : kBytes <= 48 * 1024 ? 4 : kBytes <= 96 * 1024 ? 2 : 0;
+        // A row a CTA of whole vectors: the rows to come in shared memory.  Three
+        // stages: with two CTAs of 256 threads an SM that is 98 KB in flight (8192 x
+        // 4096 bf16 with dh 45.0 us; 45.5 with two stages, 47.8 with four), and with
+        // one of 448 threads 86 KB (8192 x 7168: 73.4; 80.9, 72.7).
+        constexpr int kBytes = 3 * L::N * L::V * (int)sizeof(typename L::T) * kMaxThreads;   // of a stage
+        constexpr int kStages = L::kLanes || L::V < 8 ? 0 : kBytes <= 64 * 1024 ? 3 : kBytes <= 96 * 1024 ? 2 : 0;
         const auto kernel = k_norm_grad<typename L::T, L::V, L::N, L::kLanes, kStages>;
-        size_t smem = 0;
-        if constexpr (kStages > 0) {
-          using R = Ring<typename L::T, L::V, L::N, kStages>;
-          const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                     (int)R::bytes(kMaxThreads));
-          if (e != cudaSuccess) return e;
-          smem = R::bytes(threads);
-        }
-        const int groups = L::kLanes ? threads / L::kLanes : 1;
-        const int64_t want = (rows + groups - 1) / groups;
-        // all CTAs at once: by their registers (at most 128 a thread) and shared memory
-        constexpr int kFit = L::N * L::V <= 8 ? 1024 : L::N * L::V <= 16 ? 640 : 512;
+        // Rows that take less than 256 threads: several in a CTA.
+        const int lanes = L::kLanes ? L::kLanes : threads, groups = L::kLanes || threads <= 128 ? kRowThreads / lanes : 1;
+        threads = groups * lanes;
+        // All CTAs at once, as many on each SM: as registers (at most 128 a thread),
+        // shared memory and the scratch's rows allow.
+        constexpr int kFit = L::N * L::V <= 8 ? 1024 : 512;
         int64_t each = kFit / threads < 1 ? 1 : kFit / threads;
-        if (smem && each > (int64_t)((220 * 1024) / (smem + 2048))) each = (int64_t)((220 * 1024) / (smem + 2048));
-        int64_t most = (int64_t)v.nsm * (each < 1 ? 1 : each);
-        if (most > EBC_NORM_GRAD_PARTS(width)) most = EBC_NORM_GRAD_PARTS(width);
+        // where the groups' sums are added up
+        size_t smem = groups > 1 ? (size_t)4 * L::N * L::V * lanes : 0;
+        if constexpr (kStages > 0) {
+          const size_t ring = Ring<typename L::T, L::V, L::N, kStages>::bytes(threads);
+          constexpr int kMost = 226 * 1024;   // of an SM's 228 KB (each CTA has 1 KB of its own)
+          if (ring > smem) smem = ring;
+          if (each * (int64_t)(smem + 2048) > kMost) each = kMost / (int64_t)(smem + 2048);
+          // so much that no SM takes more: the kernel before may still fill some of them
+          smem = (size_t)(kMost / each - 2048) & ~(size_t)127;
+          const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost - 2048);
+          if (e != cudaSuccess) return e;
+        }
+        const int64_t want = (rows + groups - 1) / groups;
+        int64_t most = (int64_t)v.nsm * each;
+        if (most > EBC_NORM_GRAD_PARTS) most = EBC_NORM_GRAD_PARTS;
         a.n_parts = (int)(want < most ? want : most);
-        return launch_named(v, "k_norm_grad", st, kernel, dim3((unsigned)a.n_parts), dim3(threads), smem, 1, a);
+        return launch_named(v, "k_norm_grad", st, kernel, dim3((unsigned)a.n_parts), dim3(threads), smem, 1, a, lanes);
       });
     });
   }

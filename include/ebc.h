@@ -624,9 +624,9 @@ int ebc_norm(ebc_ctx* ctx, const void* d_x, int64_t ld_x, const void* d_residual
  * run.  d_scratch: EBC_NORM_GRAD_SCRATCH(rows, width) bytes of the caller's,
  * 16-byte aligned, free again once the call's work is done; calls that may
  * overlap, or graphs that may be replayed at the same time, have one each. */
-#define EBC_NORM_GRAD_PARTS(width) ((width) <= 2048 ? 1216 : 608)
+#define EBC_NORM_GRAD_PARTS 608
 #define EBC_NORM_GRAD_SCRATCH(rows, width) \
-  ((int64_t)4 * (width) * ((rows) < EBC_NORM_GRAD_PARTS(width) ? (rows) : EBC_NORM_GRAD_PARTS(width)))
+  ((int64_t)4 * (width) * ((rows) < EBC_NORM_GRAD_PARTS ? (rows) : EBC_NORM_GRAD_PARTS))
 int ebc_norm_grad(ebc_ctx* ctx, const void* d_dy, int64_t ld_dy, const void* d_h, int64_t ld_h, const void* d_dh,
                   int64_t ld_dh, int type, const void* d_weight, int weight_type, int64_t rows, int64_t width,
                   float eps, void* d_dx, void* d_dweight, float* d_scratch, void* stream);

@@ -148,7 +148,7 @@ def test_the_norms_gradient_stays_inside_its_scratch(fake):
         for shift in (0, 2, 4, 8, 16):
             assert fake.ebc_norm_grad(ctx, A + shift, width, A, width, None, 0, 1, A, 0, rows, width, 1e-6, A, A, A + 16, None) == 0
             first, *second = launches(fake)
-            assert 1 <= int(first[1]) <= min(rows, 1216 if width <= 2048 else 608)
+            assert 1 <= int(first[1]) <= min(rows, 608)
             assert [int(x[1]) for x in second] == ([-(-width // 32)] if int(first[1]) > 1 else [])   # one has nothing to add up
     fake.ebc_destroy(ctx)
 
