@@ -47,6 +47,7 @@ struct Values {
   static constexpr int kBytes = V * (int)sizeof(T), kWords = (kBytes + 3) / 4;
   union {
     uint32_t word[kWords];
+    uint16_t half[2 * kWords];
     T e[V];
   };
   __device__ __forceinline__ Values() {}
@@ -65,7 +66,7 @@ struct Values {
     else if constexpr (kBytes == 4)
       asm volatile("ld.global.b32 %0, [%1];" : "=r"(word[0]) : "l"(p));
     else
-      e[0] = *p;
+      asm volatile("ld.global.b16 %0, [%1];" : "=h"(half[0]) : "l"(p));
   }
   __device__ __forceinline__ void store(T* p) const {
     if constexpr (kBytes == 32)
@@ -81,7 +82,7 @@ struct Values {
     else if constexpr (kBytes == 4)
       asm volatile("st.global.b32 [%1], %0;" ::"r"(word[0]), "l"(p) : "memory");
     else
-      *p = e[0];
+      asm volatile("st.global.b16 [%1], %0;" ::"h"(half[0]), "l"(p) : "memory");
   }
   __device__ __forceinline__ void zero() {
 #pragma unroll

@@ -17,19 +17,23 @@ constexpr int kRowThreads = 256;   // of a CTA whose rows take a warp or less ea
 
 // The group's sums of K values a thread, the same in all its threads.  `part`
 // has room for two rows, so one barrier a row is enough.
-template <int kLanes, int K>
+// kWhole: a group is the CTA.  (Else a barrier is named by a register, for which
+// a CTA is given all sixteen.)
+template <int kLanes, bool kWhole, int K>
 __device__ __forceinline__ void group_sum(float (&v)[K], float (*part)[K][kMaxThreads / 32], int turn, int lanes) {
 #pragma unroll
   for (int off = (kLanes ? kLanes : 32) / 2; off > 0; off >>= 1)
 #pragma unroll
     for (int k = 0; k < K; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], off);
   if constexpr (kLanes == 0) {
-    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, warps = lanes >> 5, group = w / warps;
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, warps = lanes >> 5, group = kWhole ? 0 : w / warps;
     if (lane == 0)
 #pragma unroll
       for (int k = 0; k < K; ++k) part[turn][k][w] = v[k];
-    // (barrier 0 is __syncthreads')
-    asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(lanes) : "memory");
+    if constexpr (kWhole)
+      __syncthreads();
+    else
+      asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(lanes) : "memory");   // (0 is __syncthreads')
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       float s = lane < warps ? part[turn][k][group * warps + lane] : 0.f;
@@ -106,9 +110,82 @@ __device__ __forceinline__ void narrow(const Two (&p)[Chunk<V>::kTwos], Values<T
   }
 }
 
-// A chunk's weights, of the type that the caller keeps them in; zero past the
-// row's end.
+// ---- rows off a vector's boundary ----
+// Where all rows of a call (inputs and outputs alike) are off it by as much, they
+// are still taken in whole vectors, from the boundary before a row's start on:
+// kShift, with the thread's first column that much lower.  A group takes rows
+// that are off by the same (every eighth row is), so it keeps its columns, and
+// the weights of them.  A row's first and last vectors hold values of its
+// neighbours, which are read and dropped; those of the first and last rows, which
+// may have no neighbour, are read one by one.
 template <int V>
+__device__ __forceinline__ bool whole(int c, int width) { return c >= 0 && c + V <= width; }
+template <int V>
+__device__ __forceinline__ bool some(int c, int width) { return c > -V && c < width; }
+
+// A thread's vectors of a row: which of them have columns of it, and which are
+// cut by one of its ends.  (What few threads have to do is kept apart from the
+// loads and stores of all, which are then issued one after the other.)
+template <typename T, int V, int N, bool kShift>
+struct Span {
+  int c0, hop, width;   // the first vector's column, and to the next
+  uint32_t in, cut;     // a bit a vector
+  __device__ __forceinline__ Span(int c0, int hop, int width) : c0(c0), hop(hop), width(width), in(0), cut(0) {
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      const int c = c0 + n * hop;
+      if (kShift ? some<V>(c, width) : c < width) in |= 1u << n;
+      if (kShift && some<V>(c, width) && !whole<V>(c, width)) cut |= 1u << n;
+    }
+  }
+  __device__ __forceinline__ bool has(int n) const { return in >> n & 1; }
+  // Row `p` (the thread's first column's address); zeros where the row is not.
+  // Values beside the row stay until clip().  edge: a row without a neighbour.
+  __device__ __forceinline__ void load(Values<T, V> (&v)[N], const T* p, bool live, bool edge) const {
+    const uint32_t whole = live ? kShift && edge ? in & ~cut : in : 0u;
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      if (whole >> n & 1)
+        v[n].load(p + n * hop);
+      else
+        v[n].zero();
+    }
+    if constexpr (kShift)
+      if (live && edge && cut) ends([&](int n, int k) { v[n].e[k] = p[n * hop + k]; });
+  }
+  __device__ __forceinline__ void clip(Values<T, V> (&v)[N]) const {
+    if constexpr (kShift)
+      if (cut) {
+#pragma unroll
+        for (int n = 0; n < N; ++n)
+          if (cut >> n & 1)
+#pragma unroll
+            for (int k = 0; k < V; ++k)
+              if (c0 + n * hop + k < 0 || c0 + n * hop + k >= width) v[n].e[k] = from_f32<T>(0.f);
+      }
+  }
+  __device__ __forceinline__ void store(const Values<T, V> (&v)[N], T* p) const {
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+      if ((kShift ? in & ~cut : in) >> n & 1) v[n].store(p + n * hop);
+    if constexpr (kShift)
+      if (cut) ends([&](int n, int k) { p[n * hop + k] = v[n].e[k]; });
+  }
+  // f(n, k) for the row's values in vectors that are cut
+  template <typename F>
+  __device__ __forceinline__ void ends(F&& f) const {
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+      if (cut >> n & 1)
+#pragma unroll
+        for (int k = 0; k < V; ++k)
+          if (c0 + n * hop + k >= 0 && c0 + n * hop + k < width) f(n, k);
+  }
+};
+
+// A chunk's weights, of the type that the caller keeps them in; zero outside the
+// row.
+template <bool kShift, int V>
 __device__ __forceinline__ void load_weights(const void* w, int type, int c, int hop, int width,
                                              Two (&p)[Chunk<V>::kTwos]) {
   auto get = [&](auto one) {
@@ -116,10 +193,17 @@ __device__ __forceinline__ void load_weights(const void* w, int type, int c, int
     Values<W, V> v[Chunk<V>::kVecs];
 #pragma unroll
     for (int i = 0; i < Chunk<V>::kVecs; ++i) {
-      if (c + i * hop < width)
-        v[i].load((const W*)w + c + i * hop);
-      else
-        v[i].zero();
+      const int ci = c + i * hop;
+      if constexpr (kShift) {
+#pragma unroll
+        for (int k = 0; k < V; ++k)
+          v[i].e[k] = ci + k >= 0 && ci + k < width ? ((const W*)w)[ci + k] : from_f32<W>(0.f);
+      } else {
+        if (ci < width)
+          v[i].load((const W*)w + ci);
+        else
+          v[i].zero();
+      }
     }
     widen<W, V>(v, p);
   };
@@ -129,6 +213,35 @@ __device__ __forceinline__ void load_weights(const void* w, int type, int c, int
     get(__nv_bfloat16());
   else
     get(__half());
+}
+
+// A thread's weights in shared memory: its own, so there is nothing to wait for.
+// Four numbers a slot, the threads' slots next to each other.
+struct Slots {
+  static __device__ __forceinline__ ulonglong2* at(void* base, int slot) {
+    return reinterpret_cast<ulonglong2*>(base) + slot * blockDim.x + threadIdx.x;
+  }
+  template <int kTwos>
+  static __device__ __forceinline__ void put(void* base, int q, const Two (&p)[kTwos]) {
+#pragma unroll
+    for (int i = 0; i < kTwos / 2; ++i) *at(base, q * (kTwos / 2) + i) = make_ulonglong2(p[2 * i], p[2 * i + 1]);
+  }
+  template <int kTwos>
+  static __device__ __forceinline__ void get(void* base, int q, Two (&p)[kTwos]) {
+#pragma unroll
+    for (int i = 0; i < kTwos / 2; ++i) {
+      const ulonglong2 v = *at(base, q * (kTwos / 2) + i);
+      p[2 * i] = v.x;
+      p[2 * i + 1] = v.y;
+    }
+  }
+};
+
+// How far the group's rows start past a vector's boundary (row: one of them).
+template <typename T, int V, bool kShift>
+__device__ __forceinline__ int shift_of(const void* rows, int64_t ld, int64_t row) {
+  if constexpr (!kShift) return 0;
+  return (int)(((uintptr_t)rows / sizeof(T) + (uintptr_t)(row * ld)) % V);
 }
 
 struct NormArgs {
@@ -145,8 +258,9 @@ struct NormArgs {
 // be kept, and y is of the sum before that rounding, rounded once to its type
 // and once to 8 bits.
 // Every input is read once and every output written once; bound by bandwidth.
-template <typename T, int V, int N, int kLanes>
-__global__ void __launch_bounds__(kMaxThreads) k_norm(NormArgs a) {
+// (what rows off a boundary need beside must not cost them half of the warps)
+template <typename T, int V, int N, int kLanes, bool kShift>
+__global__ void __launch_bounds__(kMaxThreads, kShift && N * V <= 16 ? 2 : 1) k_norm(NormArgs a) {
   __shared__ float part[2][1][kMaxThreads / 32];
   pdl_enter();
   using C = Chunk<V>;
@@ -158,12 +272,22 @@ __global__ void __launch_bounds__(kMaxThreads) k_norm(NormArgs a) {
   // single weights stay in registers where there is room for them; vectors of them
   // are read again (a wait for them ahead of the first row: 43 -> 49 us of 8192 x 4096 bf16)
   constexpr bool kKeep = V < 8 && N * V <= 16;
-  const int c0 = at * V, hop = lanes * V;   // the thread's first column, and to the next
+  extern __shared__ ulonglong2 dynamic[];   // kShift: the weights, and what is rounded to 8 bits
+  const int c0 = at * V - shift_of<T, V, kShift>(a.x, a.ld_x, blockIdx.x * groups + threadIdx.x / lanes);
+  const int hop = lanes * V;   // from the thread's first column to the next
+  const Span<T, V, N, kShift> span(c0, hop, a.width);
   Two kept[kKeep ? kChunks : 1][C::kTwos];
   if constexpr (kKeep)
 #pragma unroll
     for (int q = 0; q < kChunks; ++q)
-      load_weights<V>(a.w, a.w_type, c0 + q * C::kVecs * hop, hop, a.width, kept[q]);
+      load_weights<kShift, V>(a.w, a.w_type, c0 + q * C::kVecs * hop, hop, a.width, kept[q]);
+  if constexpr (kShift)
+#pragma unroll
+    for (int q = 0; q < kChunks; ++q) {
+      Two w[C::kTwos];
+      load_weights<kShift, V>(a.w, a.w_type, c0 + q * C::kVecs * hop, hop, a.width, w);
+      Slots::put(dynamic, q, w);
+    }
   int turn = 0;
   // the groups of a warp, and the warps of a CTA, go through the same rounds
   for (int64_t row0 = (int64_t)blockIdx.x * groups; row0 < a.rows; row0 += step, turn ^= 1) {
@@ -171,35 +295,18 @@ __global__ void __launch_bounds__(kMaxThreads) k_norm(NormArgs a) {
     const bool live = row < a.rows;
     Values<T, V> xv[N];
     Two f[kChunks][C::kTwos];
-    auto load = [&](const void* rows, int64_t ld) {
-      const T* p = (const T*)rows + row * ld + c0;
-#pragma unroll
-      for (int n = 0; n < N; ++n) {
-        if (live && c0 + n * hop < a.width)
-          xv[n].load(p + n * hop);
-        else
-          xv[n].zero();
-      }
-    };
+    const bool edge = row == 0 || row == a.rows - 1;
     auto store = [&](void* rows) {
-      T* p = (T*)rows + row * a.width + c0;
 #pragma unroll
       for (int q = 0; q < kChunks; ++q) narrow<T, V>(f[q], xv + q * C::kVecs);
-#pragma unroll
-      for (int n = 0; n < N; ++n)
-        if (live && c0 + n * hop < a.width) xv[n].store(p + n * hop);
+      if (live) span.store(xv, (T*)rows + row * a.width + c0);
     };
-    load(a.x, a.ld_x);
+    span.load(xv, (const T*)a.x + row * a.ld_x + c0, live, edge);
     if (a.r) {
       Values<T, V> rv[N];
-      const T* p = (const T*)a.r + row * a.ld_r + c0;
-#pragma unroll
-      for (int n = 0; n < N; ++n) {
-        if (live && c0 + n * hop < a.width)
-          rv[n].load(p + n * hop);
-        else
-          rv[n].zero();
-      }
+      span.load(rv, (const T*)a.r + row * a.ld_r + c0, live, edge);
+      span.clip(xv);
+      span.clip(rv);
 #pragma unroll
       for (int q = 0; q < kChunks; ++q) {
         Two g[C::kTwos];
@@ -209,6 +316,7 @@ __global__ void __launch_bounds__(kMaxThreads) k_norm(NormArgs a) {
         for (int k = 0; k < C::kTwos; ++k) f[q][k] = add2(f[q][k], g[k]);
       }
     } else {
+      span.clip(xv);
 #pragma unroll
       for (int q = 0; q < kChunks; ++q) widen<T, V>(xv + q * C::kVecs, f[q]);
     }
@@ -219,18 +327,58 @@ __global__ void __launch_bounds__(kMaxThreads) k_norm(NormArgs a) {
 #pragma unroll
       for (int k = 0; k < C::kTwos; ++k) squares = fma2(f[q][k], f[q][k], squares);
     float sum[1] = {parts_of(squares).x + parts_of(squares).y};
-    group_sum<kLanes>(sum, part, turn, lanes);
+    group_sum<kLanes, true>(sum, part, turn, lanes);
     const float scale = rsqrtf(sum[0] * share + a.eps);
     const Two scales2 = two(scale, scale);
 #pragma unroll
     for (int q = 0; q < kChunks; ++q) {
       Two w[C::kTwos];
-      if constexpr (!kKeep) load_weights<V>(a.w, a.w_type, c0 + q * C::kVecs * hop, hop, a.width, w);
+      if constexpr (kShift)
+        Slots::get(dynamic, q, w);
+      else if constexpr (!kKeep)
+        load_weights<kShift, V>(a.w, a.w_type, c0 + q * C::kVecs * hop, hop, a.width, w);
 #pragma unroll
       for (int k = 0; k < C::kTwos; ++k) f[q][k] = mul2(mul2(f[q][k], scales2), kKeep ? kept[kKeep ? q : 0][k] : w[k]);
     }
     if (a.y) store(a.y);
-    if (a.codes) {
+    if constexpr (kShift) {
+      if (a.codes) {
+        // Blocks start at column 0, vectors do not: the row goes through shared
+        // memory, a word between each eight, so that neither way has lanes in the
+        // same bank.
+        float* y = reinterpret_cast<float*>(dynamic + kChunks * (C::kTwos / 2) * blockDim.x) +
+                   (threadIdx.x / lanes) * (lanes * N * V / 8 * 9);
+        if (kLanes) __syncwarp();
+#pragma unroll
+        for (int q = 0; q < kChunks; ++q) {
+          float g[V * C::kVecs];
+          split<V>(f[q], g);
+#pragma unroll
+          for (int k = 0; k < V; ++k) {
+            const int c = c0 + q * hop + k;
+            if (c >= 0) y[c + (c >> 3)] = g[k];
+          }
+        }
+        if (kLanes)
+          __syncwarp();
+        else
+          __syncthreads();   // (the next row's sum is between this reading and the next writing)
+        uint8_t* codes = a.codes + row * padded;
+        uint8_t* scales = a.scales + row * EBC_MX8_SCALE_BYTES(a.width);
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+          const int c = (n * lanes + at) * V;
+          float v[V];
+#pragma unroll
+          for (int k = 0; k < V; ++k) v[k] = c + k < a.width ? y[c + (c >> 3) + k] : 0.f;
+          const uint32_t s = mx8_scale(mx8_block_max<V>(v));
+          if (live && c < padded) {
+            mx8_store<V>(v, s, codes + c);
+            if (c % 32 == 0) scales[c / 32] = (uint8_t)s;
+          }
+        }
+      }
+    } else if (a.codes) {
       uint8_t* codes = a.codes + row * padded + c0;
       uint8_t* scales = a.scales + row * EBC_MX8_SCALE_BYTES(a.width) + c0 / 32;
 #pragma unroll
@@ -306,11 +454,15 @@ struct Ring {
       v->word[4 * i + 3] = r.w;
     }
   }
+  static __device__ __forceinline__ T* value(int stage, int stream, int n, int k) {
+    constexpr int kEach = 16 / (int)sizeof(T);
+    return reinterpret_cast<T*>(at(stage, stream, n, k / kEach)) + k % kEach;
+  }
   static __device__ __forceinline__ void commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
   static __device__ __forceinline__ void wait() {   // for all but the latest kStages - 1
     asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
   }
-  static size_t bytes(int threads) { return (size_t)kStages * kStreams * N * kParts * 16 * threads; }
+  static __host__ __device__ size_t bytes(int threads) { return (size_t)kStages * kStreams * N * kParts * 16 * threads; }
 };
 
 // With u = h / sqrt(mean(h^2) + eps) and q = dy * w:
@@ -320,8 +472,10 @@ struct Ring {
 // partial row a CTA, which k_norm_dweight adds up in a fixed order.
 // Bound by bandwidth, if loads are in flight while a row's sums go around the
 // CTA: with kStages, the rows to come are copied to shared memory meanwhile.
-template <typename T, int V, int N, int kLanes, int kStages>
-__global__ void __launch_bounds__(kLanes ? kRowThreads : kMaxThreads) k_norm_grad(GradArgs a, int row_lanes) {
+// (rows off a boundary take a warp more; two CTAs an SM still)
+constexpr int grad_threads(int lanes, bool shift) { return lanes ? kRowThreads : shift ? 576 : kMaxThreads; }
+template <typename T, int V, int N, int kLanes, int kStages, bool kShift>
+__global__ void __launch_bounds__(grad_threads(kLanes, kShift)) k_norm_grad(GradArgs a, int row_lanes) {
   using R = Ring<T, V, N, kStages>;
   using C = Chunk<V>;
   constexpr int kChunks = N / C::kVecs;
@@ -330,37 +484,48 @@ __global__ void __launch_bounds__(kLanes ? kRowThreads : kMaxThreads) k_norm_gra
   const int lanes = kLanes ? kLanes : row_lanes, at = threadIdx.x % lanes, groups = blockDim.x / lanes;
   const int64_t step = (int64_t)gridDim.x * groups;
   const float share = 1.f / (float)a.width;
-  const int c0 = at * V, hop = lanes * V;   // the thread's first column, and to the next
+  const int c0 = at * V - shift_of<T, V, kShift>(a.h, a.ld_h, blockIdx.x * groups + threadIdx.x / lanes);
+  const int hop = lanes * V;   // from the thread's first column to the next
+  const Span<T, V, N, kShift> span(c0, hop, a.width);
   auto request = [&](int64_t row, int stage) {   // row: of the CTA's first group
     if constexpr (kStages > 0) {
       row += threadIdx.x / lanes;
       if (row < a.rows) {
-        const T* h = (const T*)a.h + row * a.ld_h + c0;
-        const T* g = (const T*)a.dy + row * a.ld_dy + c0;
-#pragma unroll
-        for (int n = 0; n < N; ++n) {
-          if (c0 + n * hop >= a.width) continue;
-          R::copy(stage, 0, n, h + n * hop);
-          R::copy(stage, 1, n, g + n * hop);
-        }
-        if (a.dh) {
-          const T* e = (const T*)a.dh + row * a.ld_dh + c0;
+        const bool edge = row == 0 || row == a.rows - 1;
+        auto copy = [&](const void* rows, int64_t ld, int stream) {
+          const T* p = (const T*)rows + row * ld + c0;
 #pragma unroll
           for (int n = 0; n < N; ++n)
-            if (c0 + n * hop < a.width) R::copy(stage, 2, n, e + n * hop);
-        }
+            if ((kShift && edge ? span.in & ~span.cut : span.in) >> n & 1) R::copy(stage, stream, n, p + n * hop);
+          if constexpr (kShift)
+            if (edge && span.cut) span.ends([&](int n, int k) { *R::value(stage, stream, n, k) = p[n * hop + k]; });
+        };
+        copy(a.h, a.ld_h, 0);
+        copy(a.dy, a.ld_dy, 1);
+        if (a.dh) copy(a.dh, a.ld_dh, 2);
       }
       R::commit();
     }
   };
   for (int i = 0; i < kStages - 1; ++i) request((int64_t)blockIdx.x * groups + i * step, i);
-  constexpr bool kKeep = N * V <= 16;   // the weights stay in registers
+  // the weights stay in registers, or in shared memory behind the rows to come
+  constexpr bool kSlots = kShift && kStages > 0 && sizeof(T) == 2, kKeep = !kSlots && N * V <= 16;
+  ulonglong2* slots = nullptr;
+  if constexpr (kSlots) {
+    extern __shared__ uint4 ring[];
+    slots = reinterpret_cast<ulonglong2*>(reinterpret_cast<uint8_t*>(ring) + R::bytes(blockDim.x));
+  }
   Two dw[kChunks][C::kTwos], kept[kKeep ? kChunks : 1][C::kTwos];
 #pragma unroll
   for (int q = 0; q < kChunks; ++q) {
 #pragma unroll
     for (int k = 0; k < C::kTwos; ++k) dw[q][k] = 0;
-    if constexpr (kKeep) load_weights<V>(a.w, a.w_type, c0 + q * C::kVecs * hop, hop, a.width, kept[q]);
+    if constexpr (kKeep) load_weights<kShift, V>(a.w, a.w_type, c0 + q * C::kVecs * hop, hop, a.width, kept[q]);
+    if constexpr (kSlots) {
+      Two w[C::kTwos];
+      load_weights<kShift, V>(a.w, a.w_type, c0 + q * C::kVecs * hop, hop, a.width, w);
+      Slots::put(slots, q, w);
+    }
   }
   int turn = 0, stage = 0;
   for (int64_t row0 = (int64_t)blockIdx.x * groups; row0 < a.rows; row0 += step, turn ^= 1) {
@@ -374,7 +539,7 @@ __global__ void __launch_bounds__(kLanes ? kRowThreads : kMaxThreads) k_norm_gra
     if constexpr (kStages > 0) {
 #pragma unroll
       for (int n = 0; n < N; ++n) {
-        if (c0 + n * hop < a.width) {
+        if (span.has(n)) {
           R::get(stage, 0, n, &hv[n]);
           R::get(stage, 1, n, &gv[n]);
         } else {
@@ -383,31 +548,22 @@ __global__ void __launch_bounds__(kLanes ? kRowThreads : kMaxThreads) k_norm_gra
         }
       }
     } else {
-      const T* h = (const T*)a.h + row * a.ld_h + c0;
-      const T* g = (const T*)a.dy + row * a.ld_dy + c0;
-#pragma unroll
-      for (int n = 0; n < N; ++n) {
-        if (live && c0 + n * hop < a.width) {
-          hv[n].load(h + n * hop);
-          gv[n].load(g + n * hop);
-        } else {
-          hv[n].zero();
-          gv[n].zero();
-        }
-      }
-      if (a.dh && live) {
-        const T* e = (const T*)a.dh + row * a.ld_dh + c0;
-#pragma unroll
-        for (int n = 0; n < N; ++n)
-          if (c0 + n * hop < a.width) ev[n].load(e + n * hop);
-      }
+      const bool edge = row == 0 || row == a.rows - 1;
+      span.load(hv, (const T*)a.h + row * a.ld_h + c0, live, edge);
+      span.load(gv, (const T*)a.dy + row * a.ld_dy + c0, live, edge);
+      if (a.dh) span.load(ev, (const T*)a.dh + row * a.ld_dh + c0, live, edge);
     }
+    span.clip(hv);
+    span.clip(gv);
     // (past the row's end everything is zero)
     Two squares = 0, inner = 0;
 #pragma unroll
     for (int q = 0; q < kChunks; ++q) {
       Two w[C::kTwos], h[C::kTwos], g[C::kTwos];
-      if constexpr (!kKeep) load_weights<V>(a.w, a.w_type, c0 + q * C::kVecs * hop, hop, a.width, w);
+      if constexpr (kSlots)
+        Slots::get(slots, q, w);
+      else if constexpr (!kKeep)
+        load_weights<kShift, V>(a.w, a.w_type, c0 + q * C::kVecs * hop, hop, a.width, w);
       widen<T, V>(hv + q * C::kVecs, h);
       widen<T, V>(gv + q * C::kVecs, g);
 #pragma unroll
@@ -417,7 +573,7 @@ __global__ void __launch_bounds__(kLanes ? kRowThreads : kMaxThreads) k_norm_gra
       }
     }
     float sum[2] = {parts_of(squares).x + parts_of(squares).y, parts_of(inner).x + parts_of(inner).y};
-    group_sum<kLanes>(sum, part, turn, lanes);
+    group_sum<kLanes, false>(sum, part, turn, lanes);
     const float scale = rsqrtf(sum[0] * share + a.eps), mean = sum[1] * share * scale;
     if (live) {
       const Two scale2 = two(scale, scale), mean2 = two(-mean, -mean);
@@ -425,7 +581,10 @@ __global__ void __launch_bounds__(kLanes ? kRowThreads : kMaxThreads) k_norm_gra
 #pragma unroll
       for (int q = 0; q < kChunks; ++q) {
         Two w[C::kTwos], h[C::kTwos], g[C::kTwos], d[C::kTwos];
-        if constexpr (!kKeep) load_weights<V>(a.w, a.w_type, c0 + q * C::kVecs * hop, hop, a.width, w);
+        if constexpr (kSlots)
+        Slots::get(slots, q, w);
+      else if constexpr (!kKeep)
+        load_weights<kShift, V>(a.w, a.w_type, c0 + q * C::kVecs * hop, hop, a.width, w);
         widen<T, V>(hv + q * C::kVecs, h);
         widen<T, V>(gv + q * C::kVecs, g);
 #pragma unroll
@@ -438,19 +597,15 @@ __global__ void __launch_bounds__(kLanes ? kRowThreads : kMaxThreads) k_norm_gra
           Two e[C::kTwos];
           if constexpr (kStages > 0) {
 #pragma unroll
-            for (int i = 0; i < C::kVecs; ++i)
-              if (c0 + (q * C::kVecs + i) * hop < a.width) R::get(stage, 2, q * C::kVecs + i, &ev[q * C::kVecs + i]);
+            for (int i = 0; i < C::kVecs; ++i) R::get(stage, 2, q * C::kVecs + i, &ev[q * C::kVecs + i]);   // (stored where it is of the row)
           }
           widen<T, V>(ev + q * C::kVecs, e);
 #pragma unroll
           for (int k = 0; k < C::kTwos; ++k) d[k] = add2(d[k], e[k]);
         }
-        Values<T, V> out[C::kVecs];
-        narrow<T, V>(d, out);
-#pragma unroll
-        for (int i = 0; i < C::kVecs; ++i)
-          if (c0 + (q * C::kVecs + i) * hop < a.width) out[i].store(dx + (q * C::kVecs + i) * hop);
+        narrow<T, V>(d, gv + q * C::kVecs);
       }
+      span.store(gv, dx);
     }
     if (++stage >= kStages) stage = 0;
   }
@@ -471,13 +626,20 @@ __global__ void __launch_bounds__(kLanes ? kRowThreads : kMaxThreads) k_norm_gra
       if (c >= a.width) continue;
       if (gridDim.x == 1) {   // nothing to add up
 #pragma unroll
-        for (int k = 0; k < V; ++k) store_dweight(a.dw, a.w_type, c + k, sums[n * V + k]);
+        for (int k = 0; k < V; ++k)
+          if (!kShift || (c + k >= 0 && c + k < a.width)) store_dweight(a.dw, a.w_type, c + k, sums[n * V + k]);
         continue;
       }
       Values<float, V> out;
 #pragma unroll
       for (int k = 0; k < V; ++k) out.e[k] = sums[n * V + k];
-      out.store(mine + c);
+      if constexpr (kShift) {   // (the scratch's rows are off by another distance)
+#pragma unroll
+        for (int k = 0; k < V; ++k)
+          if (c + k >= 0 && c + k < a.width) mine[c + k] = out.e[k];
+      } else {
+        out.store(mine + c);
+      }
     }
   } else {
     // the CTA's groups one after the other, so that the order is the same in every run
@@ -490,8 +652,8 @@ __global__ void __launch_bounds__(kLanes ? kRowThreads : kMaxThreads) k_norm_gra
         for (int n = 0; n < N; ++n)
 #pragma unroll
           for (int k = 0; k < V; ++k) {
-            float* p = all + c0 + n * hop + k;
-            *p = g ? *p + sums[n * V + k] : sums[n * V + k];
+            const int c = c0 + n * hop + k;
+            if (c >= 0 && c < a.width) all[c] = g ? all[c] + sums[n * V + k] : sums[n * V + k];
           }
       __syncthreads();
     }
@@ -522,38 +684,42 @@ __global__ void __launch_bounds__(1024) k_norm_dweight(const float* parts, int n
 
 bool aligned(const void* p, int bytes) { return ((uintptr_t)p & (uintptr_t)(bytes - 1)) == 0; }
 
-// A row's layout: values of a vector, vectors of a thread, lanes of a row (0: a
-// CTA), threads of a CTA.
-template <typename T_, int V_, int N_, int kLanes_>
+// A row's layout: values of a vector, vectors of a thread, lanes of a row (0:
+// whole warps), and whether rows start off a vector's boundary.
+template <typename T_, int V_, int N_, int kLanes_, bool kShift_>
 struct Layout {
   using T = T_;
   static constexpr int V = V_, N = N_, kLanes = kLanes_;
+  static constexpr bool kShift = kShift_;
 };
 
 // Calls f with the layout and the CTA's threads: a row on as few lanes as hold
-// it with one vector each, then on more vectors a lane, then on a CTA.
+// it with one vector each, then on more vectors a lane, then on whole warps.
+template <typename T, typename F, int V, int N, bool kShift>
+cudaError_t on_warps(int width, F&& f, Layout<T, V, N, 0, kShift> layout) {
+  return f(layout, ((width + V * N - 1) / (V * N) + 31) / 32 * 32);
+}
+template <typename T, bool kShift, typename F>
+cudaError_t with_vectors(int width, F&& f) {
+  if (width <= 64) return f(Layout<T, 8, 1, 8, kShift>{}, kRowThreads);
+  if (width <= 128) return f(Layout<T, 8, 1, 16, kShift>{}, kRowThreads);
+  if (width <= 256) return f(Layout<T, 8, 1, 32, kShift>{}, kRowThreads);
+  if (width <= 512) return f(Layout<T, 8, 2, 32, kShift>{}, kRowThreads);
+  if (width <= 8192) return on_warps<T>(width, f, Layout<T, 8, 2, 0, kShift>{});
+  return on_warps<T>(width, f, Layout<T, 8, 4, 0, kShift>{});
+}
 template <typename T, typename F>
 cudaError_t with_layout(int v, int width, F&& f) {
-  auto cta = [&](auto layout) {
-    const int each = layout.V * layout.N;
-    return f(layout, ((width + each - 1) / each + 31) / 32 * 32);
-  };
-  if (v == 8) {
-    if (width <= 64) return f(Layout<T, 8, 1, 8>{}, kRowThreads);
-    if (width <= 128) return f(Layout<T, 8, 1, 16>{}, kRowThreads);
-    if (width <= 256) return f(Layout<T, 8, 1, 32>{}, kRowThreads);
-    if (width <= 512) return f(Layout<T, 8, 2, 32>{}, kRowThreads);
-    if (width <= 8192) return cta(Layout<T, 8, 2, 0>{});
-    return cta(Layout<T, 8, 4, 0>{});
-  }
+  if (v == 8) return with_vectors<T, false>(width, f);
+  if (v == 0) return with_vectors<T, true>(width + 7, f);   // as many as a shift may add
   if (v == 2) {
-    if (width <= 512) return f(Layout<T, 2, 8, 32>{}, kRowThreads);
-    if (width <= 4096) return cta(Layout<T, 2, 4, 0>{});
-    return cta(Layout<T, 2, 16, 0>{});
+    if (width <= 512) return f(Layout<T, 2, 8, 32, false>{}, kRowThreads);
+    if (width <= 4096) return on_warps<T>(width, f, Layout<T, 2, 4, 0, false>{});
+    return on_warps<T>(width, f, Layout<T, 2, 16, 0, false>{});
   }
-  if (width <= 256) return f(Layout<T, 1, 8, 32>{}, kRowThreads);
-  if (width <= 4096) return cta(Layout<T, 1, 8, 0>{});
-  return cta(Layout<T, 1, 32, 0>{});
+  if (width <= 256) return f(Layout<T, 1, 8, 32, false>{}, kRowThreads);
+  if (width <= 4096) return on_warps<T>(width, f, Layout<T, 1, 8, 0, false>{});
+  return on_warps<T>(width, f, Layout<T, 1, 32, 0, false>{});
 }
 
 template <typename F>
@@ -569,11 +735,31 @@ bool shape_ok(int type, int w_type, int64_t rows, int64_t width, float eps) {
 }
 bool ld_ok(int64_t ld, int64_t width) { return ld >= width && ld <= ((int64_t)1 << 40); }
 
-// 8, 2 or 1 values that one access takes everywhere
-int values_of(uintptr_t rows, int elem, const void* w, int w_elem) {
-  const int a = row_values(rows, elem), b = row_values((uintptr_t)w, w_elem);
-  return a < b ? a : b;
-}
+// What one access takes: 8 values where all rows and the weight allow it, 0 for
+// 8 off the boundary (where they are off by as much), else 2 or 1.  `strides`:
+// bytes between two rows' starts.
+struct Places {
+  uintptr_t all = 0, first = 0, stride = 0;
+  bool alike = true, any = false;
+  int elem;
+  explicit Places(int elem) : elem(elem) {}
+  void add(const void* p, int64_t ld) {
+    if (!p) return;
+    const uintptr_t a = (uintptr_t)p, s = (uintptr_t)(ld * elem), unit = (uintptr_t)(8 * elem);
+    if (any && ((a - first) % unit || (s - stride) % unit)) alike = false;
+    if (!any) {
+      first = a;
+      stride = s;
+    }
+    any = true;
+    all |= a | s;
+  }
+  int values(const void* w, int w_elem, int64_t width) const {
+    const int a = row_values(all, elem), b = row_values((uintptr_t)w, w_elem);
+    const int v = a < b ? a : b;
+    return v < 8 && alike && width >= 8 && width + 7 <= EBC_MAX_NORM_WIDTH ? 0 : v;
+  }
+};
 
 }  // namespace
 
@@ -596,16 +782,30 @@ int ebc_norm(ebc_ctx* ctx, const void* d_x, int64_t ld_x, const void* d_residual
   if (rc || rows == 0) return rc;
   const NormArgs a{d_x, d_residual, d_weight, d_y, d_h, d_codes, d_scales, v.glob, ld_x, ld_residual, rows,
                    (int)width, weight_type, eps};
-  const int vals = values_of((uintptr_t)d_x | (uintptr_t)(ld_x * b) | (uintptr_t)(width * b) | (uintptr_t)d_y |
-                                 (uintptr_t)d_h | (d_residual ? (uintptr_t)d_residual | (uintptr_t)(ld_residual * b) : 0),
-                             b, d_weight, wb);
+  Places at(b);
+  at.add(d_x, ld_x);
+  at.add(d_residual, ld_residual);
+  at.add(d_y, width);
+  at.add(d_h, width);
   return cuda_code(with_type_of(type, [&](auto one) {
-    return with_layout<decltype(one)>(vals, (int)width, [&](auto l, int threads) {
+    return with_layout<decltype(one)>(at.values(d_weight, wb, width), (int)width, [&](auto l, int threads) {
       using L = decltype(l);
       const int groups = L::kLanes ? threads / L::kLanes : 1;
-      const int64_t want = (rows + groups - 1) / groups, most = (int64_t)v.nsm * (2048 / threads) * 2;
-      return launch_named(v, "k_norm", st, k_norm<typename L::T, L::V, L::N, L::kLanes>,
-                          dim3((unsigned)(want < most ? want : most)), dim3(threads), 0, 1, a);
+      // (a multiple of eight, so that a group's rows are all off by as much; with
+      // weights in registers no more than are resident)
+      const int64_t want = (rows + groups - 1) / groups;
+      const int64_t most = ((int64_t)v.nsm * (L::kShift ? (1024 / threads ? 1024 / threads : 1) : 2048 / threads * 2)) & ~7ll;
+      const auto kernel = k_norm<typename L::T, L::V, L::N, L::kLanes, L::kShift>;
+      size_t smem = 0;
+      if constexpr (L::kShift) {
+        constexpr int kWeights = 4 * L::N * L::V, kRow = kWeights / 8 * 9;   // bytes a thread
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                   (kWeights + kRow) * kMaxThreads);
+        if (e != cudaSuccess) return e;
+        smem = (size_t)threads * (d_codes ? kWeights + kRow : kWeights);
+      }
+      return launch_named(v, "k_norm", st, kernel, dim3((unsigned)(want < most || most < 8 ? want : most)),
+                          dim3(threads), smem, 1, a);
     });
   }));
 }
@@ -629,14 +829,17 @@ int ebc_norm_grad(ebc_ctx* ctx, const void* d_dy, int64_t ld_dy, const void* d_h
              0, eps};
   cudaError_t e = cudaSuccess;
   if (rows > 0) {
-    const int vals = values_of((uintptr_t)d_dy | (uintptr_t)(ld_dy * b) | (uintptr_t)d_h | (uintptr_t)(ld_h * b) |
-                                   (uintptr_t)d_dx | (uintptr_t)(width * b) |
-                                   (d_dh ? (uintptr_t)d_dh | (uintptr_t)(ld_dh * b) : 0),
-                               b, d_weight, wb);
+    Places at(b);
+    at.add(d_dy, ld_dy);
+    at.add(d_h, ld_h);
+    at.add(d_dh, ld_dh);
+    at.add(d_dx, width);
+    int vals = at.values(d_weight, wb, width);
     // (fp32 partial rows start where the scratch's 16 bytes allow: whole vectors of 8 want 32)
     const int vals_s = row_values((uintptr_t)d_scratch | (uintptr_t)(width * 4), 4);
+    if (vals > vals_s) vals = vals == 8 && width >= 8 && width + 7 <= EBC_MAX_NORM_WIDTH ? 0 : vals_s;
     e = with_type_of(type, [&](auto one) {
-      return with_layout<decltype(one)>(vals < vals_s ? vals : vals_s, (int)width, [&](auto l, int threads) {
+      return with_layout<decltype(one)>(vals, (int)width, [&](auto l, int threads) {
         using L = decltype(l);
         // A row a CTA of whole vectors: the rows to come in shared memory.  Three
         // stages: with two CTAs of 256 threads an SM that is 98 KB in flight (8192 x
@@ -644,18 +847,19 @@ int ebc_norm_grad(ebc_ctx* ctx, const void* d_dy, int64_t ld_dy, const void* d_h
         // one of 448 threads 86 KB (8192 x 7168: 73.4; 80.9, 72.7).
         constexpr int kBytes = 3 * L::N * L::V * (int)sizeof(typename L::T) * kMaxThreads;   // of a stage
         constexpr int kStages = L::kLanes || L::V < 8 ? 0 : kBytes <= 64 * 1024 ? 3 : kBytes <= 96 * 1024 ? 2 : 0;
-        const auto kernel = k_norm_grad<typename L::T, L::V, L::N, L::kLanes, kStages>;
+        const auto kernel = k_norm_grad<typename L::T, L::V, L::N, L::kLanes, kStages, L::kShift>;
         // Rows that take less than 256 threads: several in a CTA.
         const int lanes = L::kLanes ? L::kLanes : threads, groups = L::kLanes || threads <= 128 ? kRowThreads / lanes : 1;
         threads = groups * lanes;
         // All CTAs at once, as many on each SM: as registers (at most 128 a thread),
         // shared memory and the scratch's rows allow.
-        constexpr int kFit = L::N * L::V <= 8 ? 1024 : 512;
+        constexpr int kFit = L::N * L::V <= 8 ? 1024 : L::kLanes ? kMaxThreads : grad_threads(0, L::kShift);
         int64_t each = kFit / threads < 1 ? 1 : kFit / threads;
         // where the groups' sums are added up
         size_t smem = groups > 1 ? (size_t)4 * L::N * L::V * lanes : 0;
         if constexpr (kStages > 0) {
-          const size_t ring = Ring<typename L::T, L::V, L::N, kStages>::bytes(threads);
+          const size_t ring = Ring<typename L::T, L::V, L::N, kStages>::bytes(threads) +
+                              (L::kShift && sizeof(typename L::T) == 2 ? 4 * L::N * L::V * threads : 0);
           constexpr int kMost = 226 * 1024;   // of an SM's 228 KB (each CTA has 1 KB of its own)
           if (ring > smem) smem = ring;
           if (each * (int64_t)(smem + 2048) > kMost) each = kMost / (int64_t)(smem + 2048);
@@ -667,6 +871,7 @@ int ebc_norm_grad(ebc_ctx* ctx, const void* d_dy, int64_t ld_dy, const void* d_h
         const int64_t want = (rows + groups - 1) / groups;
         int64_t most = (int64_t)v.nsm * each;
         if (most > EBC_NORM_GRAD_PARTS) most = EBC_NORM_GRAD_PARTS;
+        most = most < 8 ? 1 : most & ~7ll;   // (so that a group's rows are all off by as much)
         a.n_parts = (int)(want < most ? want : most);
         return launch_named(v, "k_norm_grad", st, kernel, dim3((unsigned)a.n_parts), dim3(threads), smem, 1, a, lanes);
       });

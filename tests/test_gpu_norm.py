@@ -160,6 +160,45 @@ def test_rows_with_strides(ex, at):
         check_backward(a[2], b[0], w, None, *ex.norm_grad(a[2], b[0], w))
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("rows,width", [(1, 9), (2, 9), (20, 9), (5, 57), (40, 63), (9, 121), (21, 203), (3, 249), (50, 505), (17, 1001), (33, 2047), (9, 5003), (12, 8185), (3, 8187), (700, 999)])
+def test_what_is_beside_a_row_stays_out_of_it(ex, rows, width, dtype):
+    """Rows off a vector's boundary are read in whole vectors: what stands between them, and NaN in the rows before
+    and after, do not get in, and nothing is written beside the results."""
+    g = torch.Generator("cuda").manual_seed(rows + width)
+    pitch = width + 8
+    x, r, dy, dh = (torch.full((rows * pitch,), float("nan"), dtype=dtype, device="cuda").as_strided((rows, width), (pitch, 1)) for _ in range(4))
+    for t in (x, r, dy, dh):
+        t.copy_(torch.randn(rows, width, generator=g, device="cuda"))
+    w = torch.randn(width, generator=g, device="cuda").to(dtype)
+    check_forward(x, r, w, *ex.norm(x, w, r))
+    check_forward(x, None, w, *ex.norm(x, w))
+    check_backward(dy, x, w, dh, *ex.norm_grad(dy, x, w, dh))
+    check_backward(dy, x, w, None, *ex.norm_grad(dy, x, w))
+    check_8_bit(ex, ex.norm_mx8(x, w, r)[0], x, r, w)
+    dense = [t.clone(memory_format=torch.contiguous_format) for t in (x, r, dy, dh)]
+    dense[0][::2] = float("nan")
+    y, h = ex.norm(dense[0], w, dense[1])
+    good = torch.arange(rows, device="cuda") % 2 == 1
+    assert bool(y[~good].isnan().all()) and bool(h[~good].isnan().all())
+    check_forward(x[good], r[good], w, y[good], h[good])
+    dx, dw = ex.norm_grad(dense[2], dense[0], w, dense[3])
+    assert bool(dx[~good].isnan().all()) and bool(dw.isnan().all())
+    if rows > 1:
+        check_backward(dy[good], x[good], w, dh[good], dx[good], ex.norm_grad(dy[good], x[good], w, dh[good])[1])
+    # through the C calls, into buffers with something behind their ends
+    out = torch.full((rows * width + 64,), 7.0, dtype=dtype, device="cuda")
+    type_ = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}[dtype]
+    d = [t.contiguous() for t in (x, r, dy)]
+    st = torch.cuda.current_stream().cuda_stream
+    for shift in (0, 32):
+        at = out.data_ptr() + shift * out.element_size()
+        assert ebc.ebc_norm(ex.handle, d[0].data_ptr(), width, None, 0, type_, w.data_ptr(), type_, rows, width, EPS, at, None, None, None, st) == 0
+        check_forward(d[0], None, w, out[shift:shift + rows * width].view(rows, width).clone(), d[0])
+        assert bool((out[:shift] == 7).all()) and bool((out[shift + rows * width:] == 7).all())
+        out.fill_(7.0)
+
+
 def test_leading_shapes_one_row_and_nothing(ex):
     x, r, w, _, _ = batch(30, 96, torch.bfloat16, 5)
     y, h = ex.norm(x, w, r)
