@@ -13,7 +13,7 @@ __device__ __forceinline__ int64_t divide(int64_t a, int64_t b) {
   return a <= UINT32_MAX ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
 }
 
-// Rows as one run of vectors of V values, filled up to whole blocks, so that
+// Rows as one run of vectors of eight values, filled up to whole blocks, so that
 // short rows leave no lane idle: vector v of row t is number t * each + v.
 struct Rows {
   int64_t rows, width, ld;
@@ -30,55 +30,156 @@ __device__ __forceinline__ void place(const Rows& r, uint32_t v, uint32_t* row, 
   *vec = v - *row * each;
 }
 
+// A warp's 32 vectors of eight values between memory and its lanes.  kV = 8: rows
+// whose vectors are aligned, one access a lane.  Other rows go through the warp's
+// piece of shared memory in accesses of kV values, the lanes next to each other,
+// where the vectors are of one row (they mostly are); else a lane takes its values
+// one by one, which touches as many sectors as there are lanes.
+template <typename T, int kV>
+struct Piece {
+  static constexpr int kSteps = 8 / kV;
+  static constexpr int kStage = kV == 8 ? 1 : 256;   // values
+  // p: the lane's vector; left: the row's values from there on (not above 0: none)
+  static __device__ __forceinline__ void load(const T* p, int64_t left, uint32_t row, T* stage, int lane,
+                                              Values<T, 8>* v) {
+    if constexpr (kV == 8) {
+      if (left >= 8) {
+        v->load(p);
+        return;
+      }
+    } else {
+      if (__all_sync(0xffffffffu, row == __shfl_sync(0xffffffffu, row, 0))) {
+        const T* q = p - lane * 8;
+        const int64_t left0 = left + lane * 8;
+        Values<T, kV> r[kSteps];
+#pragma unroll
+        for (int i = 0; i < kSteps; ++i) {
+          const int at = (i * 32 + lane) * kV;
+          if (at < left0)
+            r[i].load(q + at);
+          else
+            r[i].zero();
+        }
+        __syncwarp();   // the last piece has been taken
+#pragma unroll
+        for (int i = 0; i < kSteps; ++i) put(stage + (i * 32 + lane) * kV, r[i]);
+        __syncwarp();
+#pragma unroll
+        for (int k = 0; k < Values<T, 8>::kWords; k += 4) {
+          const uint4 w = reinterpret_cast<const uint4*>(stage + lane * 8)[k / 4];
+          v->word[k] = w.x;
+          v->word[k + 1] = w.y;
+          v->word[k + 2] = w.z;
+          v->word[k + 3] = w.w;
+        }
+        return;
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v->e[k] = k < left ? p[k] : from_f32<T>(0.f);
+  }
+  static __device__ __forceinline__ void store(T* p, int64_t left, uint32_t row, T* stage, int lane,
+                                               const Values<T, 8>& v) {
+    if constexpr (kV == 8) {
+      if (left >= 8) {
+        v.store(p);
+        return;
+      }
+    } else {
+      if (__all_sync(0xffffffffu, row == __shfl_sync(0xffffffffu, row, 0))) {
+        T* q = p - lane * 8;
+        const int64_t left0 = left + lane * 8;
+        __syncwarp();
+#pragma unroll
+        for (int k = 0; k < Values<T, 8>::kWords; k += 4)
+          reinterpret_cast<uint4*>(stage + lane * 8)[k / 4] =
+              make_uint4(v.word[k], v.word[k + 1], v.word[k + 2], v.word[k + 3]);
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < kSteps; ++i) {
+          const int at = (i * 32 + lane) * kV;
+          if (at < left0) {
+            Values<T, kV> r;
+            get(stage + at, &r);
+            r.store(q + at);
+          }
+        }
+        return;
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (k < left) p[k] = v.e[k];
+  }
+  static __device__ __forceinline__ void put(T* at, const Values<T, kV>& r) {
+    if constexpr (kV == 1)
+      *at = r.e[0];
+    else if constexpr (sizeof(T) == 2)
+      *reinterpret_cast<uint32_t*>(at) = r.word[0];
+    else
+      *reinterpret_cast<uint2*>(at) = make_uint2(r.word[0], r.word[1]);
+  }
+  static __device__ __forceinline__ void get(const T* at, Values<T, kV>* r) {
+    if constexpr (kV == 1) {
+      r->e[0] = *at;
+    } else if constexpr (sizeof(T) == 2) {
+      r->word[0] = *reinterpret_cast<const uint32_t*>(at);
+    } else {
+      const uint2 w = *reinterpret_cast<const uint2*>(at);
+      r->word[0] = w.x;
+      r->word[1] = w.y;
+    }
+  }
+};
+
 // A warp takes kPieces runs of 32 vectors, all in flight at once; a block is
-// 32 / V lanes.  The lanes of a row's last block also fill up its scales.
+// four lanes.  The lanes of a row's last block also fill up its scales.
 // 16 or 32 bits are read and 8.25 written a value: bound by bandwidth.
-template <typename T, int V, int kPieces>
+template <typename T, int kV, int kPieces>
 __global__ void __launch_bounds__(32 * kWarps) k_mx8_quantize(const T* x, Rows r, uint8_t* __restrict__ codes,
                                                               uint8_t* __restrict__ scales) {
+  using P = Piece<T, kV>;
+  __shared__ uint4 stages[kWarps][(P::kStage * sizeof(T) + 15) / 16];
+  T* stage = reinterpret_cast<T*>(stages[threadIdx.x >> 5]);
   pdl_enter();
-  constexpr int kLanes = 32 / V;   // of a block
-  const int lane = threadIdx.x & 31, at = lane & (kLanes - 1);
-  const int64_t code_bytes = (int64_t)r.each * V;
+  const int lane = threadIdx.x & 31, at = lane & 3;
+  const int64_t code_bytes = (int64_t)r.each * 8;
   const int64_t units = (r.rows * r.each + 32 * kPieces - 1) / (32 * kPieces);
   for (int64_t u = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5); u < units; u += (int64_t)gridDim.x * kWarps) {
     const int64_t first = u * (32 * kPieces), t0 = divide(first, r.each);
     const uint32_t v0 = (uint32_t)(first - t0 * r.each) + lane;
-    Values<T, V> in[kPieces];
+    Values<T, 8> in[kPieces];
     uint32_t row[kPieces], vec[kPieces];
 #pragma unroll
     for (int i = 0; i < kPieces; ++i) {
       place<kPieces>(r, v0 + 32 * i, &row[i], &vec[i]);
-      const int64_t t = t0 + row[i], left = t < r.rows ? r.width - (int64_t)vec[i] * V : 0;
-      const T* p = x + t * r.ld + (int64_t)vec[i] * V;
-      if (left >= V) {
-        in[i].load(p);
-      } else {
-#pragma unroll
-        for (int k = 0; k < V; ++k) in[i].e[k] = k < left ? p[k] : from_f32<T>(0.f);
-      }
+      const int64_t t = t0 + row[i], left = t < r.rows ? r.width - (int64_t)vec[i] * 8 : 0;
+      P::load(x + t * r.ld + (int64_t)vec[i] * 8, left, t < r.rows ? row[i] : ~0u - lane, stage, lane, &in[i]);
     }
 #pragma unroll
     for (int i = 0; i < kPieces; ++i) {
-      float f[V];
+      float f[8];
       in[i].get(f);
-      const uint32_t s = mx8_scale(mx8_block_max<V>(f));
+      const uint32_t s = mx8_scale(mx8_block_max<8>(f));
       const int64_t t = t0 + row[i];
       if (t >= r.rows) continue;
-      mx8_store<V>(f, s, codes + t * code_bytes + (int64_t)vec[i] * V);
+      mx8_store<8>(f, s, codes + t * code_bytes + (int64_t)vec[i] * 8);
       uint8_t* sr = scales + t * r.scale_bytes;
-      const uint32_t block = vec[i] / kLanes;
+      const uint32_t block = vec[i] / 4;
       if (at == 0) sr[block] = (uint8_t)s;
-      if (block == (uint32_t)r.each / kLanes - 1)
-        for (uint32_t b = block + 1 + at; b < r.scale_bytes; b += kLanes) sr[b] = 0;
+      if (block == (uint32_t)r.each / 4 - 1)
+        for (uint32_t b = block + 1 + at; b < r.scale_bytes; b += 4) sr[b] = 0;
     }
   }
 }
 
 // The way back, laid out the same (vectors of a row's values, no filling).
-template <typename T, int V, int kPieces>
+template <typename T, int kV, int kPieces>
 __global__ void __launch_bounds__(32 * kWarps) k_mx8_dequantize(const uint8_t* codes, const uint8_t* scales, Rows r,
                                                                 T* __restrict__ x) {
+  using P = Piece<T, kV>;
+  __shared__ uint4 stages[kWarps][(P::kStage * sizeof(T) + 15) / 16];
+  T* stage = reinterpret_cast<T*>(stages[threadIdx.x >> 5]);
   pdl_enter();
   const int lane = threadIdx.x & 31;
   const int64_t code_bytes = (r.width + 31) / 32 * 32;
@@ -93,39 +194,27 @@ __global__ void __launch_bounds__(32 * kWarps) k_mx8_dequantize(const uint8_t* c
       place<kPieces>(r, v0 + 32 * i, &row[i], &vec[i]);
       const int64_t t = t0 + row[i];
       if (t >= r.rows) continue;
-      const uint8_t* p = codes + t * code_bytes + (int64_t)vec[i] * V;
-      c[i].y = 0u;
-      if constexpr (V == 8)
-        c[i] = *reinterpret_cast<const uint2*>(p);
-      else if constexpr (V == 2)
-        c[i].x = *reinterpret_cast<const uint16_t*>(p);
-      else
-        c[i].x = *p;
-      s[i] = scales[t * r.scale_bytes + vec[i] / (32 / V)];
+      c[i] = *reinterpret_cast<const uint2*>(codes + t * code_bytes + (int64_t)vec[i] * 8);
+      s[i] = scales[t * r.scale_bytes + vec[i] / 4];
     }
 #pragma unroll
     for (int i = 0; i < kPieces; ++i) {
       const int64_t t = t0 + row[i];
-      if (t >= r.rows) continue;
-      const float unit = mx8_unit(s[i]);
-      Values<T, V> out;
-      float f[V];
+      const bool live = t < r.rows;
+      Values<T, 8> out;
+      if (live) {
+        const float unit = mx8_unit(s[i]);
+        float f[8];
 #pragma unroll
-      for (int k = 0; k < V; k += 2) {
-        const float2 v = mx8_values2((k < 4 ? c[i].x : c[i].y) >> (8 * (k & 3)));
-        f[k] = v.x * unit;
-        if constexpr (V > 1) f[k + 1] = v.y * unit;
+        for (int k = 0; k < 8; k += 2) {
+          const float2 v = mx8_values2((k < 4 ? c[i].x : c[i].y) >> (8 * (k & 3)));
+          f[k] = v.x * unit;
+          f[k + 1] = v.y * unit;
+        }
+        out.set(f);
       }
-      out.set(f);
-      const int64_t left = r.width - (int64_t)vec[i] * V;
-      T* p = x + t * r.width + (int64_t)vec[i] * V;
-      if (left >= V) {
-        out.store(p);
-      } else {
-#pragma unroll
-        for (int k = 0; k < V; ++k)
-          if (k < left) p[k] = out.e[k];
-      }
+      P::store(x + t * r.width + (int64_t)vec[i] * 8, live ? r.width - (int64_t)vec[i] * 8 : 0, live ? row[i] : ~0u - lane,
+               stage, lane, out);
     }
   }
 }
@@ -163,14 +252,20 @@ cudaError_t with_values(int v, F&& f) {
   return f(std::integral_constant<int, 1>{});
 }
 
+// Values of an access: eight, or two where rows are whole pairs, or one.
+template <typename T>
+int values_of(const void* x, int64_t ld, int64_t width) {
+  const uintptr_t rows = (uintptr_t)x | (uintptr_t)(ld * (int64_t)sizeof(T));
+  return row_values(rows, sizeof(T)) == 8 ? 8 : row_values(rows | (uintptr_t)(width * (int64_t)sizeof(T)), sizeof(T)) > 1 ? 2 : 1;
+}
+
 template <typename T>
 cudaError_t quantize_t(const CallView& v, const T* x, int64_t ld, int64_t rows, int64_t width, uint8_t* codes,
                        uint8_t* scales, cudaStream_t st) {
-  return with_values<T>(row_values((uintptr_t)x | (uintptr_t)(ld * (int64_t)sizeof(T)), sizeof(T)), [&](auto tv) {
-    constexpr int V = tv();
-    const Rows r{rows, width, ld, (int)((width + 31) / 32 * (32 / V)), (uint32_t)EBC_MX8_SCALE_BYTES(width)};
+  const Rows r{rows, width, ld, (int)((width + 31) / 32 * 4), (uint32_t)EBC_MX8_SCALE_BYTES(width)};
+  return with_values<T>(values_of<T>(x, ld, width), [&](auto tv) {
     return with_pieces(pieces(rows * r.each, v.nsm), [&](auto tp) {
-      return launch_named(v, "k_mx8_quantize", st, k_mx8_quantize<T, V, tp()>,
+      return launch_named(v, "k_mx8_quantize", st, k_mx8_quantize<T, tv(), tp()>,
                           dim3(grid(rows * r.each, tp(), v.nsm)), dim3(32 * kWarps), 0, 1, x, r, codes, scales);
     });
   });
@@ -179,11 +274,10 @@ cudaError_t quantize_t(const CallView& v, const T* x, int64_t ld, int64_t rows, 
 template <typename T>
 cudaError_t dequantize_t(const CallView& v, const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t width,
                          T* x, cudaStream_t st) {
-  return with_values<T>(row_values((uintptr_t)x | (uintptr_t)(width * (int64_t)sizeof(T)), sizeof(T)), [&](auto tv) {
-    constexpr int V = tv();
-    const Rows r{rows, width, width, (int)((width + V - 1) / V), (uint32_t)EBC_MX8_SCALE_BYTES(width)};
+  const Rows r{rows, width, width, (int)((width + 7) / 8), (uint32_t)EBC_MX8_SCALE_BYTES(width)};
+  return with_values<T>(values_of<T>(x, width, width), [&](auto tv) {
     return with_pieces(pieces(rows * r.each, v.nsm), [&](auto tp) {
-      return launch_named(v, "k_mx8_dequantize", st, k_mx8_dequantize<T, V, tp()>,
+      return launch_named(v, "k_mx8_dequantize", st, k_mx8_dequantize<T, tv(), tp()>,
                           dim3(grid(rows * r.each, tp(), v.nsm)), dim3(32 * kWarps), 0, 1, codes, scales, r, x);
     });
   });

@@ -700,18 +700,21 @@ cudaError_t on_warps(int width, F&& f, Layout<T, V, N, 0, kShift> layout) {
   return f(layout, ((width + V * N - 1) / (V * N) + 31) / 32 * 32);
 }
 template <typename T, bool kShift, typename F>
+cudaError_t on_wide(int width, F&& f) {   // more than 512 columns
+  if (width <= 8192) return on_warps<T>(width, f, Layout<T, 8, 2, 0, kShift>{});
+  return on_warps<T>(width, f, Layout<T, 8, 4, 0, kShift>{});
+}
+template <typename T, bool kShift, typename F>
 cudaError_t with_vectors(int width, F&& f) {
   if (width <= 64) return f(Layout<T, 8, 1, 8, kShift>{}, kRowThreads);
   if (width <= 128) return f(Layout<T, 8, 1, 16, kShift>{}, kRowThreads);
   if (width <= 256) return f(Layout<T, 8, 1, 32, kShift>{}, kRowThreads);
   if (width <= 512) return f(Layout<T, 8, 2, 32, kShift>{}, kRowThreads);
-  if (width <= 8192) return on_warps<T>(width, f, Layout<T, 8, 2, 0, kShift>{});
-  return on_warps<T>(width, f, Layout<T, 8, 4, 0, kShift>{});
+  return on_wide<T, kShift>(width, f);
 }
 template <typename T, typename F>
 cudaError_t with_layout(int v, int width, F&& f) {
   if (v == 8) return with_vectors<T, false>(width, f);
-  if (v == 0) return with_vectors<T, true>(width + 7, f);   // as many as a shift may add
   if (v == 2) {
     if (width <= 512) return f(Layout<T, 2, 8, 32, false>{}, kRowThreads);
     if (width <= 4096) return on_warps<T>(width, f, Layout<T, 2, 4, 0, false>{});
@@ -735,9 +738,8 @@ bool shape_ok(int type, int w_type, int64_t rows, int64_t width, float eps) {
 }
 bool ld_ok(int64_t ld, int64_t width) { return ld >= width && ld <= ((int64_t)1 << 40); }
 
-// What one access takes: 8 values where all rows and the weight allow it, 0 for
-// 8 off the boundary (where they are off by as much), else 2 or 1.  `strides`:
-// bytes between two rows' starts.
+// What one access takes: 8 values where all rows and the weight allow it, else 2
+// or 1; and whether all rows are off a vector's boundary by as much.
 struct Places {
   uintptr_t all = 0, first = 0, stride = 0;
   bool alike = true, any = false;
@@ -754,11 +756,13 @@ struct Places {
     any = true;
     all |= a | s;
   }
-  int values(const void* w, int w_elem, int64_t width) const {
+  int values(const void* w, int w_elem) const {
     const int a = row_values(all, elem), b = row_values((uintptr_t)w, w_elem);
-    const int v = a < b ? a : b;
-    return v < 8 && alike && width >= 8 && width + 7 <= EBC_MAX_NORM_WIDTH ? 0 : v;
+    return a < b ? a : b;
   }
+  // Whether such rows can be taken in whole vectors all the same (with up to 7
+  // columns more, and a row's neighbours no nearer than a vector).
+  bool shifts(int64_t width) const { return alike && width >= 8 && width + 7 <= EBC_MAX_NORM_WIDTH; }
 };
 
 }  // namespace
@@ -788,7 +792,8 @@ int ebc_norm(ebc_ctx* ctx, const void* d_x, int64_t ld_x, const void* d_residual
   at.add(d_y, width);
   at.add(d_h, width);
   return cuda_code(with_type_of(type, [&](auto one) {
-    return with_layout<decltype(one)>(at.values(d_weight, wb, width), (int)width, [&](auto l, int threads) {
+    using T = decltype(one);
+    auto launch = [&](auto l, int threads) {
       using L = decltype(l);
       const int groups = L::kLanes ? threads / L::kLanes : 1;
       // (a multiple of eight, so that a group's rows are all off by as much; with
@@ -806,7 +811,10 @@ int ebc_norm(ebc_ctx* ctx, const void* d_x, int64_t ld_x, const void* d_residual
       }
       return launch_named(v, "k_norm", st, kernel, dim3((unsigned)(want < most || most < 8 ? want : most)),
                           dim3(threads), smem, 1, a);
-    });
+    };
+    const int vals = at.values(d_weight, wb);
+    return vals < 8 && at.shifts(width) ? with_vectors<T, true>((int)width + 7, launch)
+                                        : with_layout<T>(vals, (int)width, launch);
   }));
 }
 
@@ -834,19 +842,25 @@ int ebc_norm_grad(ebc_ctx* ctx, const void* d_dy, int64_t ld_dy, const void* d_h
     at.add(d_h, ld_h);
     at.add(d_dh, ld_dh);
     at.add(d_dx, width);
-    int vals = at.values(d_weight, wb, width);
+    int vals = at.values(d_weight, wb);
     // (fp32 partial rows start where the scratch's 16 bytes allow: whole vectors of 8 want 32)
     const int vals_s = row_values((uintptr_t)d_scratch | (uintptr_t)(width * 4), 4);
-    if (vals > vals_s) vals = vals == 8 && width >= 8 && width + 7 <= EBC_MAX_NORM_WIDTH ? 0 : vals_s;
+    if (vals > vals_s) vals = vals_s;
+    // Rows off the boundary in whole vectors where it takes less time: many wide
+    // ones of 16-bit values (us, single values / so: 128 x 4095 6.2 / 9.6, 512 x 4095
+    // 12.7 / 13.0, 1531 x 1001 12.2 / 10.5, 16384 x 1001 66 / 32, 16384 x 101 12.7 /
+    // 21.9; in fp32 16384 x 1001 53 / 56).
+    const bool shift = vals < 8 && at.shifts(width) && b == 2 && width > 512 && rows * width >= 3 << 19;
     e = with_type_of(type, [&](auto one) {
-      return with_layout<decltype(one)>(vals, (int)width, [&](auto l, int threads) {
+      using T = decltype(one);
+      auto launch = [&](auto l, int threads) {
         using L = decltype(l);
         // A row a CTA of whole vectors: the rows to come in shared memory.  Three
         // stages: with two CTAs of 256 threads an SM that is 98 KB in flight (8192 x
         // 4096 bf16 with dh 45.0 us; 45.5 with two stages, 47.8 with four), and with
         // one of 448 threads 86 KB (8192 x 7168: 73.4; 80.9, 72.7).
         constexpr int kBytes = 3 * L::N * L::V * (int)sizeof(typename L::T) * kMaxThreads;   // of a stage
-        constexpr int kStages = L::kLanes || L::V < 8 ? 0 : kBytes <= 64 * 1024 ? 3 : kBytes <= 96 * 1024 ? 2 : 0;
+        constexpr int kStages = L::kLanes || L::V < 8 || (L::kShift && L::N > 2) ? 0 : kBytes <= 64 * 1024 ? 3 : kBytes <= 96 * 1024 ? 2 : 0;
         const auto kernel = k_norm_grad<typename L::T, L::V, L::N, L::kLanes, kStages, L::kShift>;
         // Rows that take less than 256 threads: several in a CTA.
         const int lanes = L::kLanes ? L::kLanes : threads, groups = L::kLanes || threads <= 128 ? kRowThreads / lanes : 1;
@@ -874,7 +888,10 @@ int ebc_norm_grad(ebc_ctx* ctx, const void* d_dy, int64_t ld_dy, const void* d_h
         most = most < 8 ? 1 : most & ~7ll;   // (so that a group's rows are all off by as much)
         a.n_parts = (int)(want < most ? want : most);
         return launch_named(v, "k_norm_grad", st, kernel, dim3((unsigned)a.n_parts), dim3(threads), smem, 1, a, lanes);
-      });
+      };
+      if constexpr (sizeof(T) == 2)
+        if (shift) return on_wide<T, true>((int)width + 7, launch);
+      return with_layout<T>(vals, (int)width, launch);
     });
   }
   if (e == cudaSuccess && a.n_parts != 1)
