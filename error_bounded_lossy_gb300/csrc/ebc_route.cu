@@ -42,7 +42,7 @@ struct RouteArgs {
   int group_lanes_log2;         // lanes of a group, where a group is whole lanes and a power of two of them; else -1
   float scale;
   bool sigmoid, renorm, sums;   // sums: a group's score is the sum of two
-  bool wide;                    // a lane's logits are whole vectors
+  bool wide, wide_bias;         // a lane's logits, and biases, are whole vectors
 };
 
 // A warp's memory.  Values: a group starts at an odd distance from the next.
@@ -141,6 +141,28 @@ __device__ __noinline__ void choose_exactly(const RouteArgs& a, Room<N>& room, c
   }
 }
 
+// A lane's N values from lane * N on (of E), `missing` past the end.
+template <typename T, int N>
+__device__ __forceinline__ void load_lane(const T* p, int E, int lane, bool wide, float missing, float (&v)[N]) {
+  if (wide) {
+    constexpr int kV = N < 8 ? N : 8;
+    Values<T, kV> r[N / kV];
+#pragma unroll
+    for (int i = 0; i < N / kV; ++i)
+      if (lane * N < E) r[i].load(p + lane * N + i * kV);
+#pragma unroll
+    for (int i = 0; i < N / kV; ++i) {
+      float f[kV];
+      r[i].get(f);
+#pragma unroll
+      for (int j = 0; j < kV; ++j) v[i * kV + j] = lane * N < E ? f[j] : missing;
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < N; ++j) v[j] = lane * N + j < E ? to_f32(p[lane * N + j]) : missing;
+  }
+}
+
 // Puts the experts of the set bits (bit j of a lane: expert lane * N + j) into
 // room.id in their order, with their values; returns how many, and writes
 // nothing where they are more than a warp.
@@ -183,52 +205,34 @@ __device__ __forceinline__ int gather(Room<N>& room, uint32_t bits, const float 
 // groups at the border of the kept ones.  With 256 experts that is one token in
 // some hundreds.
 template <typename T, int N, int kWarps>
-__global__ void __launch_bounds__(32 * kWarps) k_moe_route(RouteArgs a) {
+__global__ void __launch_bounds__(32 * kWarps, N <= 8 ? 8 : 4) k_moe_route(RouteArgs a) {
   __shared__ Room<N> rooms[kWarps];
   pdl_enter();
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   Room<N>& room = rooms[w];
   const bool scored = a.bias || (a.sums && a.groups > 1);
-  float bias[N], bias_most = 0.f;
-#pragma unroll
-  for (int j = 0; j < N; ++j) bias[j] = 0.f;
+  float bias_most = 0.f;
   if (a.bias) {
+    float b[N];
+    load_lane<float, N>(a.bias, a.E, lane, a.wide_bias, 0.f, b);
 #pragma unroll
-    for (int j = 0; j < N; ++j) {
-      const int e = lane * N + j;
-      if (e < a.E) bias[j] = a.bias[e];
-      if (fabsf(bias[j]) < CUDART_INF_F) bias_most = fmaxf(bias_most, fabsf(bias[j]));
-    }
+    for (int j = 0; j < N; ++j)
+      if (fabsf(b[j]) < CUDART_INF_F) bias_most = fmaxf(bias_most, fabsf(b[j]));
     bias_most = warp_max(bias_most);
   }
   for (int64_t t = (int64_t)blockIdx.x * kWarps + w; t < a.tokens; t += (int64_t)gridDim.x * kWarps) {
     const T* row = (const T*)a.logits + t * a.ld;
-    float l[N], c[N];
-    if (a.wide) {
-      constexpr int kV = N < 8 ? N : 8;
-#pragma unroll
-      for (int i = 0; i < N / kV; ++i) {
-        Values<T, kV> v;
-        if (lane * N < a.E) v.load(row + lane * N + i * kV);
-#pragma unroll
-        for (int j = 0; j < kV; ++j) l[i * kV + j] = lane * N < a.E ? to_f32(v.e[j]) : -CUDART_INF_F;
-      }
-    } else {
-#pragma unroll
-      for (int j = 0; j < N; ++j) l[j] = lane * N + j < a.E ? to_f32(row[lane * N + j]) : -CUDART_INF_F;
-    }
+    float c[N];   // first the logits
+    load_lane<T, N>(row, a.E, lane, a.wide, -CUDART_INF_F, c);
     float most = 0.f, total = 1.f;
     if (!a.sigmoid && (scored || !a.renorm)) {
-      most = l[0];
+      most = c[0];
 #pragma unroll
-      for (int j = 1; j < N; ++j) most = fmaxf(most, l[j]);
+      for (int j = 1; j < N; ++j) most = fmaxf(most, c[j]);
       most = shift_of(warp_max(most));
       total = 0.f;
 #pragma unroll
-      for (int j = 0; j < N; ++j) {
-        c[j] = __expf(l[j] - most);   // (of -infinity: 0)
-        total += c[j];
-      }
+      for (int j = 0; j < N; ++j) total += __expf(c[j] - most);   // (of -infinity: 0)
       total = warp_sum(total);
     }
     // How far a value in 32 bits may be off, with a margin.  Of the largest score
@@ -240,14 +244,18 @@ __global__ void __launch_bounds__(32 * kWarps) k_moe_route(RouteArgs a) {
     const float err = a.sigmoid ? (9.f + bias_most) * kUlp : ((float)(N + 48) / total + bias_most) * kUlp;
     if (scored) {
       const float part = __fdividef(1.f, total);
+      float b[N];
+      if (a.bias) {
+        load_lane<float, N>(a.bias, a.E, lane, a.wide_bias, 0.f, b);
+      } else {
+#pragma unroll
+        for (int j = 0; j < N; ++j) b[j] = 0.f;
+      }
 #pragma unroll
       for (int j = 0; j < N; ++j) {
-        const float s = a.sigmoid ? __fdividef(1.f, 1.f + __expf(-l[j])) : c[j] * part;
-        c[j] = l[j] == -CUDART_INF_F ? l[j] : s + bias[j];
+        const float s = a.sigmoid ? __fdividef(1.f, 1.f + __expf(-c[j])) : __expf(c[j] - most) * part;
+        c[j] = c[j] == -CUDART_INF_F ? c[j] : s + b[j];
       }
-    } else {
-#pragma unroll
-      for (int j = 0; j < N; ++j) c[j] = l[j];
     }
     float top1 = c[0];
 #pragma unroll
@@ -339,8 +347,14 @@ __global__ void __launch_bounds__(32 * kWarps) k_moe_route(RouteArgs a) {
 #pragma unroll
       for (int j = 0; j < N; ++j) {
         const uint32_t eg = a.group_lanes_log2 >= 0 ? (uint32_t)g : (uint32_t)(lane * N + j) * a.inverse >> 20;
-        const bool dead = c[j] == -CUDART_INF_F || !(kept >> (eg << log2 & 31) & 1);
-        c[j] = dead ? -CUDART_INF_F : a.bias ? c[j] : l[j];   // (now what the choice compares)
+        if (!(kept >> (eg << log2 & 31) & 1)) c[j] = -CUDART_INF_F;
+      }
+      if (scored && !a.bias) {   // the choice compares the logits
+        float l[N];
+        load_lane<T, N>(row, a.E, lane, a.wide, -CUDART_INF_F, l);
+#pragma unroll
+        for (int j = 0; j < N; ++j)
+          if (c[j] != -CUDART_INF_F) c[j] = l[j];
       }
       top1 = c[0];
 #pragma unroll
@@ -557,6 +571,7 @@ template <typename T, int N>
 cudaError_t route_n(const CallView& v, RouteArgs a, cudaStream_t st) {
   constexpr int kWarps = N == 32 ? 2 : 4, kBytes = (N < 8 ? N : 8) * (int)sizeof(T);
   a.wide = a.E % N == 0 && ((uintptr_t)a.logits | (uintptr_t)(a.ld * (int64_t)sizeof(T))) % kBytes == 0;
+  a.wide_bias = a.E % N == 0 && (uintptr_t)a.bias % ((N < 8 ? N : 8) * 4) == 0;
   const int size = a.E / a.groups, lanes = size / N;
   a.group_lanes_log2 = -1;
   if (size % N == 0 && (lanes & (lanes - 1)) == 0)
