@@ -1,5 +1,5 @@
 """A mixture-of-experts layer with experts on several ranks, the operators as
-they are used together: tokens sorted by expert, the rows of each rank as an
+they are used together: the router, tokens sorted by expert, the rows of each rank as an
 error-bounded container, the experts' products on the received rows in 4 bits,
 and the weighted sum on the way back; then a training step's gradients.
 
@@ -20,7 +20,7 @@ import error_bounded_lossy_gb300 as ebc  # noqa: E402
 
 
 def route(x, gate, top):
-    """The router: each token's experts and their weights."""
+    """The router's definition in torch's operations: each token's experts and their weights."""
     p, ids = (x.float() @ gate).softmax(1).topk(top, 1)
     return ids, (p / p.sum(1, keepdim=True)).contiguous()
 
@@ -43,7 +43,7 @@ def exchange(codec, rows, bound):
 
 def forward(ex, codec, x, gate, weights, top, ranks, bound):
     """The layer's result, and what its parts were."""
-    ids, w = route(x, gate, top)
+    ids, w = ex.route(x.float() @ gate, top)
     n_experts = gate.shape[1]
     plan = ex.plan(ids, n_experts)
     xs = ex.dispatch(x, plan)
