@@ -40,7 +40,7 @@ struct Piece {
   static constexpr int kSteps = 8 / kV;
   static constexpr int kStage = kV == 8 ? 1 : 256;   // values
   // p: the lane's vector; left: the row's values from there on (not above 0: none)
-  static __device__ __forceinline__ void load(const T* p, int64_t left, uint32_t row, T* stage, int lane,
+  static __device__ __forceinline__ void load(const T* p, int left, uint32_t row, T* stage, int lane,
                                               Values<T, 8>* v) {
     if constexpr (kV == 8) {
       if (left >= 8) {
@@ -50,7 +50,7 @@ struct Piece {
     } else {
       if (__all_sync(0xffffffffu, row == __shfl_sync(0xffffffffu, row, 0))) {
         const T* q = p - lane * 8;
-        const int64_t left0 = left + lane * 8;
+        const int left0 = left + lane * 8;
         Values<T, kV> r[kSteps];
 #pragma unroll
         for (int i = 0; i < kSteps; ++i) {
@@ -143,31 +143,37 @@ __global__ void __launch_bounds__(32 * kWarps) k_mx8_quantize(const T* x, Rows r
   T* stage = reinterpret_cast<T*>(stages[threadIdx.x >> 5]);
   pdl_enter();
   const int lane = threadIdx.x & 31, at = lane & 3;
-  const int64_t code_bytes = (int64_t)r.each * 8;
-  const int64_t units = (r.rows * r.each + 32 * kPieces - 1) / (32 * kPieces);
+  const int64_t total = r.rows * r.each, units = (total + 32 * kPieces - 1) / (32 * kPieces);
+  const int64_t next = r.ld - (int64_t)r.each * 8;   // from a row's last vector to the next row's first
+  const uint32_t blocks = (uint32_t)r.each / 4;
   for (int64_t u = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5); u < units; u += (int64_t)gridDim.x * kWarps) {
-    const int64_t first = u * (32 * kPieces), t0 = divide(first, r.each);
+    // The codes' vectors stand one after the other, whatever row they are of.
+    const int64_t first = u * (32 * kPieces), t0 = divide(first, r.each), rest = total - first;
     const uint32_t v0 = (uint32_t)(first - t0 * r.each) + lane;
+    const uint32_t there = rest < 32 * kPieces ? (uint32_t)rest : 32u * kPieces;
+    const T* xb = x + t0 * r.ld + (int64_t)v0 * 8;
+    uint8_t* cb = codes + (first + lane) * 8;
+    uint8_t* sb = scales + t0 * r.scale_bytes;
     Values<T, 8> in[kPieces];
     uint32_t row[kPieces], vec[kPieces];
 #pragma unroll
     for (int i = 0; i < kPieces; ++i) {
       place<kPieces>(r, v0 + 32 * i, &row[i], &vec[i]);
-      const int64_t t = t0 + row[i], left = t < r.rows ? r.width - (int64_t)vec[i] * 8 : 0;
-      P::load(x + t * r.ld + (int64_t)vec[i] * 8, left, t < r.rows ? row[i] : ~0u - lane, stage, lane, &in[i]);
+      const bool live = lane + 32 * i < there;
+      const int left = live ? (int)r.width - (int)vec[i] * 8 : 0;
+      P::load(xb + i * 256 + row[i] * next, left, live ? row[i] : ~0u - lane, stage, lane, &in[i]);
     }
 #pragma unroll
     for (int i = 0; i < kPieces; ++i) {
       float f[8];
       in[i].get(f);
       const uint32_t s = mx8_scale(mx8_block_max<8>(f));
-      const int64_t t = t0 + row[i];
-      if (t >= r.rows) continue;
-      mx8_store<8>(f, s, codes + t * code_bytes + (int64_t)vec[i] * 8);
-      uint8_t* sr = scales + t * r.scale_bytes;
+      if (lane + 32 * i >= there) continue;
+      mx8_store<8>(f, s, cb + i * 256);
       const uint32_t block = vec[i] / 4;
+      uint8_t* sr = sb + row[i] * r.scale_bytes;
       if (at == 0) sr[block] = (uint8_t)s;
-      if (block == (uint32_t)r.each / 4 - 1)
+      if (block == blocks - 1)
         for (uint32_t b = block + 1 + at; b < r.scale_bytes; b += 4) sr[b] = 0;
     }
   }

@@ -52,8 +52,13 @@ struct Room {
     float c[32 * N + 32];
     double d[32 * N];
   };
-  float value[36];   // the candidates, then the best of them in their order
-  int id[36];
+  // the candidates (a value and its expert each), then the best of them in their
+  // order, and one that nobody reads
+  float2 slot[36];
+  __device__ __forceinline__ float value(int i) const { return slot[i].x; }
+  __device__ __forceinline__ int id(int i) const { return __float_as_int(slot[i].y); }
+  __device__ __forceinline__ void put(int i, float v, int e) { slot[i] = make_float2(v, __int_as_float(e)); }
+  static constexpr int kNowhere = 35;
 };
 
 // ---- scores in 64 bits, for values that 32 cannot tell apart ----
@@ -73,7 +78,7 @@ __device__ __noinline__ double exact_value(const RouteArgs& a, const T* row, int
 
 // The whole choice in 64 bits, for rows with a NaN and for ties of more values
 // than a warp has lanes: the same steps, written to be short.  A NaN is above
-// everything.  Leaves the ids in room.id.
+// everything.  Leaves the ids in the slots.
 template <typename T, int N>
 __device__ __noinline__ void choose_exactly(const RouteArgs& a, Room<N>& room, const T* row, float most, bool scored,
                                             int lane) {
@@ -134,7 +139,7 @@ __device__ __noinline__ void choose_exactly(const RouteArgs& a, Room<N>& room, c
       }
     }
     if (lane == 0) {
-      room.id[r] = at == INT32_MAX ? -1 : at;
+      room.put(r, 0.f, at == INT32_MAX ? -1 : at);
       if (at != INT32_MAX) room.d[at] = -CUDART_INF;
     }
     __syncwarp();
@@ -163,9 +168,9 @@ __device__ __forceinline__ void load_lane(const T* p, int E, int lane, bool wide
   }
 }
 
-// Puts the experts of the set bits (bit j of a lane: expert lane * N + j) into
-// room.id in their order, with their values; returns how many, and writes
-// nothing where they are more than a warp.
+// Puts the experts of the set bits (bit j of a lane: expert lane * N + j) into the
+// slots in their order, with their values; returns how many, and writes nothing
+// where they are more than a warp.
 template <int N>
 __device__ __forceinline__ int gather(Room<N>& room, uint32_t bits, const float (&v)[N], int lane) {
   const int mine = __popc(bits);
@@ -179,15 +184,63 @@ __device__ __forceinline__ int gather(Room<N>& room, uint32_t bits, const float 
   at -= mine;
   __syncwarp();
   if (all <= 32) {
+    // (a store for each value, not a branch: most of them nowhere)
 #pragma unroll
-    for (int j = 0; j < N; ++j)
-      if (bits >> j & 1) {
-        room.value[at] = v[j];
-        room.id[at++] = lane * N + j;
-      }
+    for (int j = 0; j < N; ++j) {
+      const bool set = bits >> j & 1;
+      room.put(set ? at : Room<N>::kNowhere, v[j], lane * N + j);
+      at += set;
+    }
   }
   __syncwarp();
   return all;
+}
+
+// The groups' ranks from sums in 64 bits of the `near` ones' largest values, which
+// are among the `found` of room.id, and from the others' as they are.
+template <typename T, int N>
+__device__ __noinline__ int settle_groups(const RouteArgs& a, Room<N>& room, const T* row, float most, int found,
+                                          bool near, float score, int log2, int lane) {
+  const double total = a.sigmoid ? 1.0 : exact_total(row, a.E, most, lane);
+  const int e = lane < found ? room.id(lane) : 0, g = lane >> log2;
+  const double value = exact_value(a, row, e, most, total);
+  const int eg = (int)((uint32_t)e * a.inverse >> 20);
+  double first = -CUDART_INF, second = -CUDART_INF;
+#pragma unroll 1
+  for (int i = 0; i < found; ++i) {
+    const double v = __shfl_sync(kAll, value, i);
+    if (__shfl_sync(kAll, eg, i) == g) {
+      second = fmax(second, fmin(first, v));
+      first = fmax(first, v);
+    }
+  }
+  const double sure = !near ? (double)score : a.sums && second > -CUDART_INF ? first + second : first;
+  int rank = 0;
+#pragma unroll 1
+  for (int i = 0; i < a.groups; ++i) {
+    const double o = __shfl_sync(kAll, sure, i << log2);
+    rank += o > sure || (o == sure && i < g);
+  }
+  return rank;
+}
+
+// The order of the `found` best in room.id by their values in 64 bits.
+template <typename T, int N>
+__device__ __noinline__ void settle_order(const RouteArgs& a, Room<N>& room, const T* row, float most, int found,
+                                          int lane) {
+  const double total = a.sigmoid ? 1.0 : exact_total(row, a.E, most, lane);
+  const int e = lane < found ? room.id(lane) : -1;
+  const double value = e >= 0 ? exact_value(a, row, e, most, total) : -CUDART_INF;
+  int rank = 0;
+#pragma unroll 1
+  for (int i = 0; i < found; ++i) {
+    const double u = __shfl_sync(kAll, value, i);
+    const int n = __shfl_sync(kAll, e, i);
+    rank += u > value || (u == value && n < e);
+  }
+  __syncwarp();
+  if (lane < found) room.put(rank, 0.f, e);
+  __syncwarp();
 }
 
 // A warp a token; lane i has the experts i * N to i * N + N - 1, whose values in
@@ -205,25 +258,31 @@ __device__ __forceinline__ int gather(Room<N>& room, uint32_t bits, const float 
 // groups at the border of the kept ones.  With 256 experts that is one token in
 // some hundreds.
 template <typename T, int N, int kWarps>
-__global__ void __launch_bounds__(32 * kWarps, N <= 8 ? 8 : 4) k_moe_route(RouteArgs a) {
+__global__ void __launch_bounds__(32 * kWarps, N <= 8 ? 8 : 4) k_moe_route(const __grid_constant__ RouteArgs a) {
   __shared__ Room<N> rooms[kWarps];
   pdl_enter();
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   Room<N>& room = rooms[w];
   const bool scored = a.bias || (a.sums && a.groups > 1);
-  float bias_most = 0.f;
-  if (a.bias) {
-    float b[N];
-    load_lane<float, N>(a.bias, a.E, lane, a.wide_bias, 0.f, b);
-#pragma unroll
-    for (int j = 0; j < N; ++j)
-      if (fabsf(b[j]) < CUDART_INF_F) bias_most = fmaxf(bias_most, fabsf(b[j]));
-    bias_most = warp_max(bias_most);
-  }
+  float bias_most = -1.f;   // (not known yet)
   for (int64_t t = (int64_t)blockIdx.x * kWarps + w; t < a.tokens; t += (int64_t)gridDim.x * kWarps) {
     const T* row = (const T*)a.logits + t * a.ld;
-    float c[N];   // first the logits
+    float c[N], b[N];   // c: first the logits
     load_lane<T, N>(row, a.E, lane, a.wide, -CUDART_INF_F, c);
+    if (a.bias) {
+      load_lane<float, N>(a.bias, a.E, lane, a.wide_bias, 0.f, b);
+      if (bias_most < 0.f) {
+        bias_most = 0.f;
+#pragma unroll
+        for (int j = 0; j < N; ++j)
+          if (fabsf(b[j]) < CUDART_INF_F) bias_most = fmaxf(bias_most, fabsf(b[j]));
+        bias_most = warp_max(bias_most);
+      }
+    } else {
+      bias_most = 0.f;
+#pragma unroll
+      for (int j = 0; j < N; ++j) b[j] = 0.f;
+    }
     float most = 0.f, total = 1.f;
     if (!a.sigmoid && (scored || !a.renorm)) {
       most = c[0];
@@ -244,13 +303,6 @@ __global__ void __launch_bounds__(32 * kWarps, N <= 8 ? 8 : 4) k_moe_route(Route
     const float err = a.sigmoid ? (9.f + bias_most) * kUlp : ((float)(N + 48) / total + bias_most) * kUlp;
     if (scored) {
       const float part = __fdividef(1.f, total);
-      float b[N];
-      if (a.bias) {
-        load_lane<float, N>(a.bias, a.E, lane, a.wide_bias, 0.f, b);
-      } else {
-#pragma unroll
-        for (int j = 0; j < N; ++j) b[j] = 0.f;
-      }
 #pragma unroll
       for (int j = 0; j < N; ++j) {
         const float s = a.sigmoid ? __fdividef(1.f, 1.f + __expf(-c[j])) : __expf(c[j] - most) * part;
@@ -261,7 +313,6 @@ __global__ void __launch_bounds__(32 * kWarps, N <= 8 ? 8 : 4) k_moe_route(Route
 #pragma unroll
     for (int j = 1; j < N; ++j) top1 = max_or_nan(top1, c[j]);
     bool generic = __any_sync(kAll, top1 != top1);   // a NaN
-    double total64 = 0.0;                            // 0: not summed yet
     if (a.groups > 1 && !generic) {
       // a group's largest two, in each of its lanes
       float first = -CUDART_INF_F, second = -CUDART_INF_F;
@@ -319,28 +370,7 @@ __global__ void __launch_bounds__(32 * kWarps, N <= 8 ? 8 : 4) k_moe_route(Route
           }
           const int found = gather(room, bits, c, lane);
           generic = found > 32;
-          if (!generic) {
-            if (!a.sigmoid) total64 = exact_total(row, a.E, most, lane);
-            const int e = lane < found ? room.id[lane] : 0;
-            const double value = exact_value(a, row, e, most, total64);
-            const int eg = (int)((uint32_t)e * a.inverse >> 20);
-            double f = -CUDART_INF, s = -CUDART_INF;
-#pragma unroll 1
-            for (int i = 0; i < found; ++i) {
-              const double v = __shfl_sync(kAll, value, i);
-              if (__shfl_sync(kAll, eg, i) == g) {
-                s = fmax(s, fmin(f, v));
-                f = fmax(f, v);
-              }
-            }
-            const double sure = !near ? (double)score : a.sums && s > -CUDART_INF ? f + s : f;
-            rank = 0;
-#pragma unroll 1
-            for (int i = 0; i < a.groups; ++i) {
-              const double o = __shfl_sync(kAll, sure, i << log2);
-              rank += o > sure || (o == sure && i < g);
-            }
-          }
+          if (!generic) rank = settle_groups<T, N>(a, room, row, most, found, near, score, log2, lane);
         }
       }
       const unsigned kept = __ballot_sync(kAll, one && rank < a.keep);
@@ -377,42 +407,31 @@ __global__ void __launch_bounds__(32 * kWarps, N <= 8 ? 8 : 4) k_moe_route(Route
         if (c[j] >= bound && c[j] > -CUDART_INF_F) bits |= 1u << j;
       const int found = gather(room, bits, c, lane);
       if (found <= 32) {
-        float v = lane < found ? room.value[lane] : -CUDART_INF_F;
-        int e = lane < found ? room.id[lane] : -1, rank = 0;
+        float v = lane < found ? room.value(lane) : -CUDART_INF_F;
+        int e = lane < found ? room.id(lane) : -1, rank = 0;
 #pragma unroll 4
         for (int i = 0; i < found; ++i) {
-          const float o = room.value[i];
+          const float o = room.value(i);
           rank += o > v || (o == v && i < lane);
         }
         if (lane >= found) rank = lane;
         __syncwarp();
-        room.value[rank] = v;
-        room.id[rank] = e;
+        room.put(rank, v, e);
         __syncwarp();
         if (a.bias) {
           // is each of the best far enough from the next, or the same as it
-          v = room.value[lane];
-          e = room.id[lane];
-          const float x = e >= 0 ? to_f32(row[e]) : 0.f, b = e >= 0 ? a.bias[e] : 0.f;
-          const float o = __shfl_down_sync(kAll, v, 1), ox = __shfl_down_sync(kAll, x, 1), ob = __shfl_down_sync(kAll, b, 1);
-          const bool near = lane < a.top && lane < 31 && o > -CUDART_INF_F && v - o <= 2.f * err && !(x == ox && b == ob);
+          v = room.value(lane);
+          const float o = __shfl_down_sync(kAll, v, 1);
+          bool near = lane < a.top && lane < 31 && o > -CUDART_INF_F && v - o <= 2.f * err;
           if (__any_sync(kAll, near)) {
-            if (!a.sigmoid && total64 == 0.0) total64 = exact_total(row, a.E, most, lane);
-            const double value = e >= 0 ? exact_value(a, row, e, most, total64) : -CUDART_INF;
-            rank = 0;
-#pragma unroll 1
-            for (int i = 0; i < found; ++i) {
-              const double u = __shfl_sync(kAll, value, i);
-              const int n = __shfl_sync(kAll, e, i);
-              rank += u > value || (u == value && n < e);
-            }
-            if (lane >= found) rank = lane;
-            __syncwarp();
-            room.id[rank] = e;
-            __syncwarp();
+            e = room.id(lane);
+            const float x = e >= 0 ? to_f32(row[e]) : 0.f, b = e >= 0 ? a.bias[e] : 0.f;
+            const float ox = __shfl_down_sync(kAll, x, 1), ob = __shfl_down_sync(kAll, b, 1);
+            near = near && !(x == ox && b == ob);
+            if (__any_sync(kAll, near)) settle_order<T, N>(a, room, row, most, found, lane);
           }
         }
-        id = lane < a.top ? room.id[lane] : -1;
+        id = lane < a.top ? room.id(lane) : -1;
       } else if (!a.bias) {
         // ties of more than a warp of values: the best one by one
 #pragma unroll 1
@@ -440,7 +459,7 @@ __global__ void __launch_bounds__(32 * kWarps, N <= 8 ? 8 : 4) k_moe_route(Route
     }
     if (generic) {
       choose_exactly<T, N>(a, room, row, most, scored, lane);
-      id = lane < a.top ? room.id[lane] : -1;
+      id = lane < a.top ? room.id(lane) : -1;
       __syncwarp();
     }
     // weights, a lane a choice
