@@ -134,7 +134,10 @@ struct Piece {
 
 // A warp takes kPieces runs of 32 vectors, all in flight at once; a block is
 // four lanes.  The lanes of a row's last block also fill up its scales.
-// 16 or 32 bits are read and 8.25 written a value: bound by bandwidth.
+// 16 or 32 bits are read and 8.25 written a value: bound by bandwidth, for 16-bit
+// types by issue as much.  [16384, 4096] bf16 36.6 us (5.6 TB/s), [8192, 3328] fp32
+// 21.4 (6.4); off a boundary [16384, 1502] bf16 24 us, [16384, 1501] 38 (a lane's
+// values one by one took 45 and 69).
 template <typename T, int kV, int kPieces>
 __global__ void __launch_bounds__(32 * kWarps) k_mx8_quantize(const T* x, Rows r, uint8_t* __restrict__ codes,
                                                               uint8_t* __restrict__ scales) {
@@ -180,6 +183,7 @@ __global__ void __launch_bounds__(32 * kWarps) k_mx8_quantize(const T* x, Rows r
 }
 
 // The way back, laid out the same (vectors of a row's values, no filling).
+// [16384, 4096] to bf16 34 us (6.0 TB/s), [16384, 1501] 19.
 template <typename T, int kV, int kPieces>
 __global__ void __launch_bounds__(32 * kWarps) k_mx8_dequantize(const uint8_t* codes, const uint8_t* scales, Rows r,
                                                                 T* __restrict__ x) {

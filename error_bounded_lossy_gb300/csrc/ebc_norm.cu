@@ -248,7 +248,6 @@ struct NormArgs {
   const void *x, *r, *w;   // r: null without a residual
   void *y, *h;             // null where not asked for
   uint8_t *codes, *scales;
-  Glob* glob;
   int64_t ld_x, ld_r, rows;
   int width, w_type;
   float eps;
@@ -257,8 +256,13 @@ struct NormArgs {
 // h = x + r, y = h / sqrt(mean(h^2) + eps) * w, in 32 bits: h is rounded once, to
 // be kept, and y is of the sum before that rounding, rounded once to its type
 // and once to 8 bits.
-// Every input is read once and every output written once; bound by bandwidth.
-// (what rows off a boundary need beside must not cost them half of the warps)
+// Every input is read once and every output written once; bound by bandwidth:
+// 8192 x 4096 bf16 with a residual 42.5 us (6.3 TB/s), 16384 rows 81 us (6.6);
+// to 8 bits 41.5 and 78, both 48 and 93; off a boundary, x 4095, 51 us.  A row on
+// fewer threads with more values each takes fewer joins: 16384 x 1024 25.1 us with
+// eight values a thread, 22.1 with sixteen.
+// (What rows off a boundary need beside must not cost them half of the warps: two
+// CTAs of 512 threads an SM.)
 template <typename T, int V, int N, int kLanes, bool kShift>
 __global__ void __launch_bounds__(kMaxThreads, kShift && N * V <= 16 ? 2 : 1) k_norm(NormArgs a) {
   __shared__ float part[2][1][kMaxThreads / 32];
@@ -469,10 +473,14 @@ struct Ring {
 //   dx = (q - u * mean(q * u)) / sqrt(mean(h^2) + eps) + dh,   dw = sum over rows of dy * u.
 // Both means of a row come out of one pass over it.  A thread keeps the same
 // columns in every row, and with them their part of dw, so dw takes one
-// partial row a CTA, which k_norm_dweight adds up in a fixed order.
+// partial row a CTA, which k_norm_dweight adds up in a fixed order (4 to 5 us at
+// 304 CTAs; several narrow rows go to a CTA so that there are no more).
 // Bound by bandwidth, if loads are in flight while a row's sums go around the
-// CTA: with kStages, the rows to come are copied to shared memory meanwhile.
-// (rows off a boundary take a warp more; two CTAs an SM still)
+// CTA: with kStages, the rows to come are copied to shared memory meanwhile
+// (without: 73 us of 8192 x 4096 bf16 with dh, so: 44, 6.1 TB/s; 16384 rows 82, 6.5).
+// Rows off a boundary, one value an access: issue and latency (8192 x 1001 fp32 28 us).
+
+// (Rows off a boundary take a warp more; two CTAs an SM still.)
 constexpr int grad_threads(int lanes, bool shift) { return lanes ? kRowThreads : shift ? 576 : kMaxThreads; }
 template <typename T, int V, int N, int kLanes, int kStages, bool kShift>
 __global__ void __launch_bounds__(grad_threads(kLanes, kShift)) k_norm_grad(GradArgs a, int row_lanes) {
@@ -582,9 +590,9 @@ __global__ void __launch_bounds__(grad_threads(kLanes, kShift)) k_norm_grad(Grad
       for (int q = 0; q < kChunks; ++q) {
         Two w[C::kTwos], h[C::kTwos], g[C::kTwos], d[C::kTwos];
         if constexpr (kSlots)
-        Slots::get(slots, q, w);
-      else if constexpr (!kKeep)
-        load_weights<kShift, V>(a.w, a.w_type, c0 + q * C::kVecs * hop, hop, a.width, w);
+          Slots::get(slots, q, w);
+        else if constexpr (!kKeep)
+          load_weights<kShift, V>(a.w, a.w_type, c0 + q * C::kVecs * hop, hop, a.width, w);
         widen<T, V>(hv + q * C::kVecs, h);
         widen<T, V>(gv + q * C::kVecs, g);
 #pragma unroll
@@ -784,7 +792,7 @@ int ebc_norm(ebc_ctx* ctx, const void* d_x, int64_t ld_x, const void* d_residual
   cudaStream_t st = (cudaStream_t)stream;
   const int rc = begin_call(ctx, st, &v);
   if (rc || rows == 0) return rc;
-  const NormArgs a{d_x, d_residual, d_weight, d_y, d_h, d_codes, d_scales, v.glob, ld_x, ld_residual, rows,
+  const NormArgs a{d_x, d_residual, d_weight, d_y, d_h, d_codes, d_scales, ld_x, ld_residual, rows,
                    (int)width, weight_type, eps};
   Places at(b);
   at.add(d_x, ld_x);
