@@ -41,6 +41,7 @@ constexpr int kStoreRows = 16;     // rows that a storing warp reads at a time
 struct Mx4Format {
   static constexpr int kStageK = 256;
   static constexpr uint32_t kTypes = (1u << 7) | (1u << 10);   // E2M1
+  static constexpr int kPairStart = 0;      // cycles of a pair's launch, see tile_rows()
   static constexpr const char* kName = "k_mx4_product";
   static int64_t code_bytes(int64_t width) { return EBC_MX4_CODE_BYTES(width); }
   static int64_t scale_bytes(int64_t width) { return EBC_MX4_SCALE_BYTES(width); }
@@ -48,6 +49,7 @@ struct Mx4Format {
 struct Mx8Format {
   static constexpr int kStageK = 128;
   static constexpr uint32_t kTypes = 0u;                       // E4M3
+  static constexpr int kPairStart = 5000;
   static constexpr const char* kName = "k_mx8_product";
   static int64_t code_bytes(int64_t width) { return EBC_MX8_CODE_BYTES(width); }
   static int64_t scale_bytes(int64_t width) { return EBC_MX8_SCALE_BYTES(width); }
@@ -527,12 +529,15 @@ __device__ __forceinline__ void product_begin(Shared<Geom<F, kTN, kCtas>>& sh) {
 // and instructions it has in flight, frees its tensor memory and returns.  A
 // pair's copies are counted together, at the first CTA's barriers, so there the
 // loading warps first bring each other to the same stage.
-// 17/32 of a byte is read a value of rows and weights, and outs * rows results
-// are written; one expert, 16384 rows x 8192 x 8192: 320 us (6.9 PFLOP/s), where
+// 17/32 of a byte is read a value of rows and weights in 4 bits, 33/32 in 8, and
+// outs * rows results are written.  4 bits: one expert, 16384 rows x 8192 x 8192: 320 us (6.9 PFLOP/s), where
 // a pair's stage takes 550 cycles to 512 of its instructions; 32 experts of 4096
 // x 4096: 120 us (4.6 PFLOP/s), a quarter of it the accumulator's reading, which
 // the next tile's instructions wait for; one turn of small tiles: 7 to 9 us of
-// latency, from the first stage's arrival to the last result's store.
+// latency, from the first stage's arrival to the last result's store.  8 bits: one
+// expert, 16384 rows x 8192 x 8192: 680 us (3.2 PFLOP/s) at the board's power
+// limit, where the clock falls to 1.3 GHz and a stage takes 517 cycles of it (633 at
+// 2.07 GHz, with operands of zeros); 32 experts of 4096 x 4096: 203 us (2.7).
 template <typename F, int kTN, int kCtas>
 __device__ __forceinline__ void product_run(Shared<Geom<F, kTN, kCtas>>& sh, const CUtensorMap& wmap,
                                             const CUtensorMap& xmap, const Args& a) {
@@ -989,12 +994,22 @@ cudaError_t product_t(const CallView& v, const uint8_t* xc, const uint8_t* wc, i
 // with single CTAs whatever the rows (the instructions take that to issue, less
 // to run) and 550 with pairs, and about 2000 a tile for the results with single
 // CTAs, 3800 with pairs, which have one accumulator.
-// us with 16 / 32 / 64 / 128 / 256 rows a tile (the chosen one in brackets):
+// With 8 bits, whose stages are twice as many for the same K, pairs come out 5000
+// cycles worse a launch (the single CTAs' first stages overlap more of it).
+// us of 4 bits with 16 / 32 / 64 / 128 / 256 rows a tile (the chosen one in brackets):
 //      16 rows x 32 experts x 4096 x 2048   [10.4] 10.6  12.4  12.7   15.3
 //     256 rows x  1 expert  x 4096 x 4096    18.9  11.7  [8.2]  9.2   13.5
 //    2048 rows x 32 experts x 2048 x 2048    39.5  25.8  19.0 [15.4]  19.8
 //    2228 rows x  5 experts x 2541 x  192    14.9  10.3   8.3  [8.8]  11.7
 //   16384 rows x 32 experts x 4096 x 4096   841   463   240   155   [120]
+// and of 8 bits:
+//      16 rows x 32 experts x 4096 x 2048   [20.9] 21.2  25.5  26.3   26.0
+//     256 rows x  1 expert  x 4096 x 4096    30.0  17.5 [11.3] 12.5   17.9
+//    2048 rows x  8 experts x 1024 x 1024    17.1  11.8  [8.6]  8.9   11.5
+//    2048 rows x 32 experts x 2048 x 2048    62.9  40.3  30.1 [29.2]  34.7
+//   16384 rows x 32 experts x 1024 x 1024   109    62.3  37.6 [27.0]  29.1
+//    8192 rows x 32 experts x 2048 x 2048   201   113    66.0  48.4  [46.4]
+template <typename F>
 int tile_rows(int64_t rows, int64_t outs, int64_t stages, int experts, int nsm) {
   const int64_t active = experts < rows ? experts : rows;
   int best = 16;
@@ -1005,7 +1020,7 @@ int tile_rows(int64_t rows, int64_t outs, int64_t stages, int experts, int nsm) 
     // each expert's last run is half full on average, and a run at least
     const int64_t runs = rows / tn + active / 2 > active ? rows / tn + active / 2 : active;
     const int64_t turns = (runs * ((outs + wide - 1) / wide) + units - 1) / units;
-    const int64_t cycles = turns * (pair ? 550 * stages + 3800 : 450 * stages + 2000);
+    const int64_t cycles = turns * (pair ? 550 * stages + 3800 : 450 * stages + 2000) + (pair ? F::kPairStart : 0);
     if (cycles < least) {
       least = cycles;
       best = tn;
@@ -1048,7 +1063,7 @@ int product_any(ebc_ctx* ctx, const uint8_t* d_x_codes, const uint8_t* d_x_scale
   a.blocks = (int)((width + kBlock - 1) / kBlock);
   a.experts = n_experts;
   a.first_wait = v.first_wait;
-  switch (tile_rows(rows, outs, (width + F::kStageK - 1) / F::kStageK, n_experts, v.nsm)) {
+  switch (tile_rows<F>(rows, outs, (width + F::kStageK - 1) / F::kStageK, n_experts, v.nsm)) {
     case 16: return cuda_code(product_t<L, 16, 1>(v, d_x_codes, d_w_codes, width, a, st));
     case 32: return cuda_code(product_t<L, 32, 1>(v, d_x_codes, d_w_codes, width, a, st));
     case 64: return cuda_code(product_t<L, 64, 1>(v, d_x_codes, d_w_codes, width, a, st));

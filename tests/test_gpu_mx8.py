@@ -230,6 +230,18 @@ def test_product_of_few_tiles(ex, rows, experts, outs, width):
         assert torch.equal(ex.product(x, w, offsets), ex.product(x, w, offsets))
 
 
+@pytest.mark.parametrize("tiles", [39, 75, 76, 77, 151, 152, 153, 170, 227, 228, 229, 303, 304, 305, 380, 381, 456, 500])
+@pytest.mark.parametrize("width", [544, 1056])
+def test_product_of_a_few_rows_of_one_of_some_experts(ex, tiles, width):
+    """Counts of small tiles around whole and half turns of 152 CTAs; the host is told of four experts, any of which may
+    have rows."""
+    for cut in ([0, 0, 8, 8, 8], [0, 0, 0, 3, 3]):
+        x, w, offsets = case(ex, 8, 4, 128 * tiles - 60, width, tiles, cut)
+        check_product(ex, x, w, offsets, torch.float32)
+        check_product(ex, x, w, offsets, torch.bfloat16)
+        assert torch.equal(ex.product(x, w, offsets), ex.product(x, w, offsets))
+
+
 @pytest.mark.parametrize("rows,experts", [(5, 1024), (3000, 700), (40, 64)])
 def test_product_of_many_experts(ex, rows, experts):
     x, w, offsets = case(ex, rows, experts, 40, 64, rows)
@@ -324,7 +336,7 @@ def test_offsets_that_do_not_ascend_inside_the_rows_are_recorded(cut):
     e.close()
 
 
-@pytest.mark.parametrize("rows,experts,outs,width", [(16, 8, 2000, 2048), (6000, 4, 4000, 1024), (2, 1, 600, 8192), (16384, 3, 4096, 4000)])
+@pytest.mark.parametrize("rows,experts,outs,width", [(16, 8, 2000, 2048), (6000, 4, 4000, 1024), (2, 1, 600, 8192), (16384, 3, 4096, 4000), (16, 32, 4096, 2048), (13, 32, 4000, 1000)])
 def test_a_wait_that_runs_out_is_recorded_and_the_context_recovers(rows, experts, outs, width):
     """Single CTAs, pairs and clusters that share K: the first stage's wait gives up at once; every CTA ends, the
     status says so, and the next product is right."""

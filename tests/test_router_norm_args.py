@@ -164,6 +164,31 @@ def test_an_8_bit_product_takes_no_more_rows_than_its_tiles_can_count(fake):
     fake.ebc_destroy(ctx)
 
 
+def test_the_launches_of_8_bit_products(fake):
+    """Single CTAs, pairs and clusters that share K as those of 4 bits, by the sizes; only the smallest tiles share."""
+    ctx = context(fake)
+
+    def product(rows, experts, outs, width):
+        assert fake.ebc_mx8_product(ctx, A, A, rows, width, A, A, outs, experts, A, ebc.EBC_BF16, A, None) == 0
+        (found,) = launches(fake)
+        tile, ctas = re.search(r"k_mx8_productILi(\d+)ELi(\d)E", found[0]).groups()
+        return int(tile), int(ctas), int(found[1]), int(found[2])
+
+    assert product(16, 8, 2000, 2048) == (16, 1, 144, 1)
+    assert product(2, 1, 600, 8192) == (16, 1, 40, 8)
+    assert product(2048, 8, 1024, 1024)[:2] == (64, 1)
+    assert product(16384, 4, 4096, 4096) == (256, 2, 152, 2)
+    rng, seen = random.Random(0), set()
+    for _ in range(2000):
+        rows, experts = int(2 ** rng.uniform(0, 14)), int(2 ** rng.uniform(0, 8))
+        outs, width = int(2 ** rng.uniform(0, 14)), int(2 ** rng.uniform(0, 15))
+        tile, ctas, grid, cluster = product(rows, experts, outs, width)
+        assert grid % cluster == 0 and grid <= 152 and (cluster == ctas or tile == 16), (rows, experts, outs, width)
+        seen.add((tile, cluster))
+    assert {(16, 1), (16, 8), (64, 1), (256, 2)} <= seen
+    fake.ebc_destroy(ctx)
+
+
 def test_the_torch_types_refuse_other_tensors():
     b, s = torch.zeros(3, 64, dtype=torch.uint8), torch.zeros(3, 16, dtype=torch.uint8)
     with pytest.raises(ValueError, match="CUDA"):
