@@ -258,23 +258,28 @@ __global__ void __launch_bounds__(32 * kRowWarps) k_moe_dispatch_mx(const uint4*
   for (int64_t u = (int64_t)blockIdx.x * kRowWarps + (threadIdx.x >> 5); u < units;
        u += (int64_t)gridDim.x * kRowWarps) {
     const int64_t t = divide(u, pieces), h0 = (u - t * pieces) * kPiece + lane;
+    // a vector's place in both arrays' first rows, and from row to row
+    const uint4* src[kU];
+    uint4* dst[kU];
+    int64_t hop[kU];
     uint4 v[kU];
+#pragma unroll
+    for (int i = 0; i < kU; ++i) {
+      const int64_t h = h0 + i * 32;
+      const bool code = h < code_vecs;
+      hop[i] = h < vecs ? code ? code_vecs : scale_vecs : 0;   // 0: no vector
+      src[i] = code ? codes + h : scales + (h - code_vecs);
+      dst[i] = code ? xs_codes + h : xs_scales + (h - code_vecs);
+    }
     auto store = [&](int64_t r) {
 #pragma unroll
-      for (int i = 0; i < kU; ++i) {
-        const int64_t h = h0 + i * 32;
-        if (h < code_vecs)
-          xs_codes[r * code_vecs + h] = v[i];
-        else if (h < vecs)
-          xs_scales[r * scale_vecs + (h - code_vecs)] = v[i];
-      }
+      for (int i = 0; i < kU; ++i)
+        if (hop[i]) dst[i][r * hop[i]] = v[i];
     };
     if (t < tokens) {
 #pragma unroll
-      for (int i = 0; i < kU; ++i) {
-        const int64_t h = h0 + i * 32;
-        if (h < vecs) v[i] = h < code_vecs ? codes[t * code_vecs + h] : scales[t * scale_vecs + (h - code_vecs)];
-      }
+      for (int i = 0; i < kU; ++i)
+        if (hop[i]) v[i] = src[i][t * hop[i]];
       for (int j0 = 0; j0 < top; j0 += 32) {
         const int m = top - j0 < 32 ? top - j0 : 32;
         const int32_t p_lane = lane < m ? read_place(place, t * top + j0 + lane, n, glob) : -1;
