@@ -422,8 +422,10 @@ int ebc_decompress_noalloc(const void* d_in, uint64_t in_bytes, float* d_xhat, i
  * All pointers named d_ are device memory owned by the caller and aligned to
  * their elements; a row of `width` elements is contiguous, and ld_ arguments
  * are the elements between the starts of two rows of an input (>= width);
- * outputs are dense.  Row addresses that are all multiples of 16 bytes are
- * the fast case.  The calls are asynchronous on `stream`, take no scratch,
+ * outputs are dense.  Row addresses that are all multiples of 16 bytes (32 for
+ * fp32 rows) are the fast case, and where they are not, a row's sum may be taken in
+ * another order.  The calls are asynchronous on `stream`, take no scratch but what a
+ * caller passes,
  * leave the host thread's current device as it is (the other calls of a context
  * make its device current),
  * and give the same bits in every run; a graph that captured them uses the
@@ -641,9 +643,9 @@ int ebc_get_stats(ebc_ctx* ctx, ebc_stats* out, void* stream);
  * error the kernels recorded since the previous query: EBC_OK,
  * EBC_ERR_CAPACITY, EBC_ERR_CORRUPT, EBC_ERR_INVALID_ARG,
  * EBC_ERR_DEVICE_TIMEOUT or EBC_ERR_INTERNAL.  A context that has made an
- * ebc_moe_* or ebc_mx4_* call synchronises its device instead: those calls need
- * no scratch, so they may be on several streams at once, and in graphs that are
- * replayed on others. */
+ * ebc_moe_*, ebc_mx4_*, ebc_mx8_* or ebc_norm* call synchronises its device
+ * instead: those calls have no scratch of the context's, so they may be on several
+ * streams at once, and in graphs that are replayed on others. */
 int ebc_last_device_error(ebc_ctx* ctx);
 
 /* Failure-detection test aid.  Every device-side wait of the codec is bounded:
@@ -657,7 +659,7 @@ int ebc_last_device_error(ebc_ctx* ctx);
  * default).  With 0 the first wait gives up before looking, so a test can run
  * the time-out path without hanging anything; later waits keep the full
  * limit.  It sets the same for the first stage that each multiplying warp of
- * the following ebc_mx4_product calls waits for, and for the first that the
+ * the following ebc_mx4_product and ebc_mx8_product calls waits for, and for the first that the
  * loading warp of a CTA pair's first CTA does; a product that gives up leaves
  * d_ys unspecified.  Host-only; EBC_ERR_INVALID_ARG for a null context or polls > 2^22. */
 int ebc_set_first_wait_polls(ebc_ctx* ctx, int polls);
