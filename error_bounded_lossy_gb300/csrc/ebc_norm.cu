@@ -139,47 +139,53 @@ struct Span {
     }
   }
   __device__ __forceinline__ bool has(int n) const { return in >> n & 1; }
-  // Row `p` (the thread's first column's address); zeros where the row is not.
-  // Values beside the row stay until clip().  edge: a row without a neighbour.
-  __device__ __forceinline__ void load(Values<T, V> (&v)[N], const T* p, bool live, bool edge) const {
+  // Row `p` (the thread's first column's address), or M vectors of it from vector
+  // `first` on; zeros where the row is not.  Values beside the row stay until
+  // clip().  edge: a row without a neighbour.
+  template <int M>
+  __device__ __forceinline__ void load(Values<T, V> (&v)[M], const T* p, bool live, bool edge, int first = 0) const {
     const uint32_t whole = live ? kShift && edge ? in & ~cut : in : 0u;
 #pragma unroll
-    for (int n = 0; n < N; ++n) {
-      if (whole >> n & 1)
-        v[n].load(p + n * hop);
+    for (int n = 0; n < M; ++n) {
+      if (whole >> (first + n) & 1)
+        v[n].load(p + (first + n) * hop);
       else
         v[n].zero();
     }
     if constexpr (kShift)
-      if (live && edge && cut) ends([&](int n, int k) { v[n].e[k] = p[n * hop + k]; });
+      if (live && edge && cut) ends<M>(first, [&](int n, int k) { v[n].e[k] = p[(first + n) * hop + k]; });
   }
-  __device__ __forceinline__ void clip(Values<T, V> (&v)[N]) const {
+  template <int M>
+  __device__ __forceinline__ void clip(Values<T, V> (&v)[M], int first = 0) const {
     if constexpr (kShift)
       if (cut) {
 #pragma unroll
-        for (int n = 0; n < N; ++n)
-          if (cut >> n & 1)
+        for (int n = 0; n < M; ++n) {
+          const int c = c0 + (first + n) * hop;
+          if (cut >> (first + n) & 1)
 #pragma unroll
             for (int k = 0; k < V; ++k)
-              if (c0 + n * hop + k < 0 || c0 + n * hop + k >= width) v[n].e[k] = from_f32<T>(0.f);
+              if (c + k < 0 || c + k >= width) v[n].e[k] = from_f32<T>(0.f);
+        }
       }
   }
-  __device__ __forceinline__ void store(const Values<T, V> (&v)[N], T* p) const {
+  template <int M>
+  __device__ __forceinline__ void store(const Values<T, V> (&v)[M], T* p, int first = 0) const {
 #pragma unroll
-    for (int n = 0; n < N; ++n)
-      if ((kShift ? in & ~cut : in) >> n & 1) v[n].store(p + n * hop);
+    for (int n = 0; n < M; ++n)
+      if ((kShift ? in & ~cut : in) >> (first + n) & 1) v[n].store(p + (first + n) * hop);
     if constexpr (kShift)
-      if (cut) ends([&](int n, int k) { p[n * hop + k] = v[n].e[k]; });
+      if (cut) ends<M>(first, [&](int n, int k) { p[(first + n) * hop + k] = v[n].e[k]; });
   }
-  // f(n, k) for the row's values in vectors that are cut
-  template <typename F>
-  __device__ __forceinline__ void ends(F&& f) const {
+  // f(n, k) for the row's values in those of M vectors from `first` on that are cut
+  template <int M, typename F>
+  __device__ __forceinline__ void ends(int first, F&& f) const {
 #pragma unroll
-    for (int n = 0; n < N; ++n)
-      if (cut >> n & 1)
+    for (int n = 0; n < M; ++n)
+      if (cut >> (first + n) & 1)
 #pragma unroll
         for (int k = 0; k < V; ++k)
-          if (c0 + n * hop + k >= 0 && c0 + n * hop + k < width) f(n, k);
+          if (c0 + (first + n) * hop + k >= 0 && c0 + (first + n) * hop + k < width) f(n, k);
   }
 };
 
@@ -264,7 +270,7 @@ struct NormArgs {
 // (What rows off a boundary need beside must not cost them half of the warps: two
 // CTAs of 512 threads an SM.)
 template <typename T, int V, int N, int kLanes, bool kShift>
-__global__ void __launch_bounds__(kMaxThreads, kShift && N * V <= 16 ? 2 : 1) k_norm(NormArgs a) {
+__global__ void __launch_bounds__(kShift && N * V > 16 ? 576 : kMaxThreads, kShift && N * V <= 16 ? 2 : 1) k_norm(NormArgs a) {
   __shared__ float part[2][1][kMaxThreads / 32];
   pdl_enter();
   using C = Chunk<V>;
@@ -481,12 +487,19 @@ struct Ring {
 // Rows off a boundary, one value an access: issue and latency (8192 x 1001 fp32 28 us).
 
 // (Rows off a boundary take a warp more; two CTAs an SM still.)
-constexpr int grad_threads(int lanes, bool shift) { return lanes ? kRowThreads : shift ? 576 : kMaxThreads; }
+constexpr int grad_threads(int lanes, int values, bool shift) {
+  return lanes ? kRowThreads : shift && values <= 16 ? 576 : kMaxThreads;
+}
 template <typename T, int V, int N, int kLanes, int kStages, bool kShift>
-__global__ void __launch_bounds__(grad_threads(kLanes, kShift)) k_norm_grad(GradArgs a, int row_lanes) {
+__global__ void __launch_bounds__(grad_threads(kLanes, N * V, kShift)) k_norm_grad(GradArgs a, int row_lanes) {
   using R = Ring<T, V, N, kStages>;
   using C = Chunk<V>;
   constexpr int kChunks = N / C::kVecs;
+  // More values than registers hold beside dw: they are read twice, the second
+  // time mostly out of the L1 cache, a few at a time.
+  constexpr bool kAgain = kStages == 0 && N * V > 16;
+  constexpr int M = kAgain ? 8 / V : N;
+  static_assert(!kAgain || kLanes == 0);   // (a barrier between the two)
   __shared__ float part[2][2][kMaxThreads / 32];
   pdl_enter();
   const int lanes = kLanes ? kLanes : row_lanes, at = threadIdx.x % lanes, groups = blockDim.x / lanes;
@@ -506,7 +519,7 @@ __global__ void __launch_bounds__(grad_threads(kLanes, kShift)) k_norm_grad(Grad
           for (int n = 0; n < N; ++n)
             if ((kShift && edge ? span.in & ~span.cut : span.in) >> n & 1) R::copy(stage, stream, n, p + n * hop);
           if constexpr (kShift)
-            if (edge && span.cut) span.ends([&](int n, int k) { *R::value(stage, stream, n, k) = p[n * hop + k]; });
+            if (edge && span.cut) span.template ends<N>(0, [&](int n, int k) { *R::value(stage, stream, n, k) = p[n * hop + k]; });
         };
         copy(a.h, a.ld_h, 0);
         copy(a.dy, a.ld_dy, 1);
@@ -517,7 +530,7 @@ __global__ void __launch_bounds__(grad_threads(kLanes, kShift)) k_norm_grad(Grad
   };
   for (int i = 0; i < kStages - 1; ++i) request((int64_t)blockIdx.x * groups + i * step, i);
   // the weights stay in registers, or in shared memory behind the rows to come
-  constexpr bool kSlots = kShift && kStages > 0 && sizeof(T) == 2, kKeep = !kSlots && N * V <= 16;
+  constexpr bool kSlots = kShift, kKeep = !kSlots && N * V <= 16;
   ulonglong2* slots = nullptr;
   if constexpr (kSlots) {
     extern __shared__ uint4 ring[];
@@ -539,45 +552,58 @@ __global__ void __launch_bounds__(grad_threads(kLanes, kShift)) k_norm_grad(Grad
   for (int64_t row0 = (int64_t)blockIdx.x * groups; row0 < a.rows; row0 += step, turn ^= 1) {
     const int64_t row = row0 + threadIdx.x / lanes;
     const bool live = row < a.rows;
-    Values<T, V> hv[N], gv[N], ev[N];
+    const bool edge = row == 0 || row == a.rows - 1;
+    // M vectors of h and dy, or of dh, from vector `first` on
+    Values<T, V> hv[M], gv[M], ev[M];
+    auto get_hg = [&](int first) {
+      if constexpr (kStages > 0) {
+#pragma unroll
+        for (int n = 0; n < M; ++n) {
+          if (span.has(first + n)) {
+            R::get(stage, 0, first + n, &hv[n]);
+            R::get(stage, 1, first + n, &gv[n]);
+          } else {
+            hv[n].zero();
+            gv[n].zero();
+          }
+        }
+      } else {
+        span.load(hv, (const T*)a.h + row * a.ld_h + c0, live, edge, first);
+        span.load(gv, (const T*)a.dy + row * a.ld_dy + c0, live, edge, first);
+      }
+    };
+    auto get_e = [&](int first) { span.load(ev, (const T*)a.dh + row * a.ld_dh + c0, live, edge, first); };
+    auto clip = [&](int first) {
+      span.clip(hv, first);
+      span.clip(gv, first);
+    };
     if constexpr (kStages > 0) {
       request(row0 + (kStages - 1) * step, stage == 0 ? kStages - 1 : stage - 1);
       R::wait();
     }
-    if constexpr (kStages > 0) {
-#pragma unroll
-      for (int n = 0; n < N; ++n) {
-        if (span.has(n)) {
-          R::get(stage, 0, n, &hv[n]);
-          R::get(stage, 1, n, &gv[n]);
-        } else {
-          hv[n].zero();
-          gv[n].zero();
-        }
-      }
-    } else {
-      const bool edge = row == 0 || row == a.rows - 1;
-      span.load(hv, (const T*)a.h + row * a.ld_h + c0, live, edge);
-      span.load(gv, (const T*)a.dy + row * a.ld_dy + c0, live, edge);
-      if (a.dh) span.load(ev, (const T*)a.dh + row * a.ld_dh + c0, live, edge);
-    }
-    span.clip(hv);
-    span.clip(gv);
     // (past the row's end everything is zero)
     Two squares = 0, inner = 0;
 #pragma unroll
-    for (int q = 0; q < kChunks; ++q) {
-      Two w[C::kTwos], h[C::kTwos], g[C::kTwos];
-      if constexpr (kSlots)
-        Slots::get(slots, q, w);
-      else if constexpr (!kKeep)
-        load_weights<kShift, V>(a.w, a.w_type, c0 + q * C::kVecs * hop, hop, a.width, w);
-      widen<T, V>(hv + q * C::kVecs, h);
-      widen<T, V>(gv + q * C::kVecs, g);
+    for (int first = 0; first < N; first += M) {
+      get_hg(first);
+      if constexpr (kStages == 0 && !kAgain)
+        if (a.dh) get_e(first);
+      clip(first);
 #pragma unroll
-      for (int k = 0; k < C::kTwos; ++k) {
-        squares = fma2(h[k], h[k], squares);
-        inner = fma2(mul2(g[k], kKeep ? kept[kKeep ? q : 0][k] : w[k]), h[k], inner);
+      for (int i = 0; i < M / C::kVecs; ++i) {
+        const int q = first / C::kVecs + i;
+        Two w[C::kTwos], h[C::kTwos], g[C::kTwos];
+        if constexpr (kSlots)
+          Slots::get(slots, q, w);
+        else if constexpr (!kKeep)
+          load_weights<kShift, V>(a.w, a.w_type, c0 + q * C::kVecs * hop, hop, a.width, w);
+        widen<T, V>(hv + i * C::kVecs, h);
+        widen<T, V>(gv + i * C::kVecs, g);
+#pragma unroll
+        for (int k = 0; k < C::kTwos; ++k) {
+          squares = fma2(h[k], h[k], squares);
+          inner = fma2(mul2(g[k], kKeep ? kept[kKeep ? q : 0][k] : w[k]), h[k], inner);
+        }
       }
     }
     float sum[2] = {parts_of(squares).x + parts_of(squares).y, parts_of(inner).x + parts_of(inner).y};
@@ -587,33 +613,42 @@ __global__ void __launch_bounds__(grad_threads(kLanes, kShift)) k_norm_grad(Grad
       const Two scale2 = two(scale, scale), mean2 = two(-mean, -mean);
       T* dx = (T*)a.dx + row * a.width + c0;
 #pragma unroll
-      for (int q = 0; q < kChunks; ++q) {
-        Two w[C::kTwos], h[C::kTwos], g[C::kTwos], d[C::kTwos];
-        if constexpr (kSlots)
-          Slots::get(slots, q, w);
-        else if constexpr (!kKeep)
-          load_weights<kShift, V>(a.w, a.w_type, c0 + q * C::kVecs * hop, hop, a.width, w);
-        widen<T, V>(hv + q * C::kVecs, h);
-        widen<T, V>(gv + q * C::kVecs, g);
-#pragma unroll
-        for (int k = 0; k < C::kTwos; ++k) {
-          const Two u = mul2(h[k], scale2);
-          d[k] = mul2(fma2(u, mean2, mul2(g[k], kKeep ? kept[kKeep ? q : 0][k] : w[k])), scale2);
-          dw[q][k] = fma2(g[k], u, dw[q][k]);
+      for (int first = 0; first < N; first += M) {
+        if constexpr (kAgain) {
+          get_hg(first);
+          if (a.dh) get_e(first);
+          clip(first);
         }
-        if (a.dh) {
-          Two e[C::kTwos];
-          if constexpr (kStages > 0) {
 #pragma unroll
-            for (int i = 0; i < C::kVecs; ++i) R::get(stage, 2, q * C::kVecs + i, &ev[q * C::kVecs + i]);   // (stored where it is of the row)
+        for (int i = 0; i < M / C::kVecs; ++i) {
+          const int q = first / C::kVecs + i;
+          Two w[C::kTwos], h[C::kTwos], g[C::kTwos], d[C::kTwos];
+          if constexpr (kSlots)
+            Slots::get(slots, q, w);
+          else if constexpr (!kKeep)
+            load_weights<kShift, V>(a.w, a.w_type, c0 + q * C::kVecs * hop, hop, a.width, w);
+          widen<T, V>(hv + i * C::kVecs, h);
+          widen<T, V>(gv + i * C::kVecs, g);
+#pragma unroll
+          for (int k = 0; k < C::kTwos; ++k) {
+            const Two u = mul2(h[k], scale2);
+            d[k] = mul2(fma2(u, mean2, mul2(g[k], kKeep ? kept[kKeep ? q : 0][k] : w[k])), scale2);
+            dw[q][k] = fma2(g[k], u, dw[q][k]);
           }
-          widen<T, V>(ev + q * C::kVecs, e);
+          if (a.dh) {
+            Two e[C::kTwos];
+            if constexpr (kStages > 0) {
 #pragma unroll
-          for (int k = 0; k < C::kTwos; ++k) d[k] = add2(d[k], e[k]);
+              for (int j = 0; j < C::kVecs; ++j) R::get(stage, 2, q * C::kVecs + j, &ev[i * C::kVecs + j]);   // (stored where it is of the row)
+            }
+            widen<T, V>(ev + i * C::kVecs, e);
+#pragma unroll
+            for (int k = 0; k < C::kTwos; ++k) d[k] = add2(d[k], e[k]);
+          }
+          narrow<T, V>(d, gv + i * C::kVecs);
         }
-        narrow<T, V>(d, gv + q * C::kVecs);
+        span.store(gv, dx, first);
       }
-      span.store(gv, dx);
     }
     if (++stage >= kStages) stage = 0;
   }
@@ -875,13 +910,19 @@ int ebc_norm_grad(ebc_ctx* ctx, const void* d_dy, int64_t ld_dy, const void* d_h
         threads = groups * lanes;
         // All CTAs at once, as many on each SM: as registers (at most 128 a thread),
         // shared memory and the scratch's rows allow.
-        constexpr int kFit = L::N * L::V <= 8 ? 1024 : L::kLanes ? kMaxThreads : grad_threads(0, L::kShift);
+        constexpr int kFit = L::N * L::V <= 8 ? 1024 : L::kLanes ? kMaxThreads : grad_threads(0, L::N * L::V, L::kShift);
         int64_t each = kFit / threads < 1 ? 1 : kFit / threads;
         // where the groups' sums are added up
         size_t smem = groups > 1 ? (size_t)4 * L::N * L::V * lanes : 0;
+        if constexpr (L::kShift && kStages == 0) {   // the weights
+          static_assert(L::kLanes == 0 && L::N * L::V > 16);   // (a CTA is one group)
+          smem = (size_t)4 * L::N * L::V * threads;
+          const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 4 * L::N * L::V * kMaxThreads);
+          if (e != cudaSuccess) return e;
+        }
         if constexpr (kStages > 0) {
           const size_t ring = Ring<typename L::T, L::V, L::N, kStages>::bytes(threads) +
-                              (L::kShift && sizeof(typename L::T) == 2 ? 4 * L::N * L::V * threads : 0);
+                              (L::kShift ? 4 * L::N * L::V * threads : 0);
           constexpr int kMost = 226 * 1024;   // of an SM's 228 KB (each CTA has 1 KB of its own)
           if (ring > smem) smem = ring;
           if (each * (int64_t)(smem + 2048) > kMost) each = kMost / (int64_t)(smem + 2048);
