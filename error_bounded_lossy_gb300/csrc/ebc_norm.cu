@@ -7,7 +7,8 @@ using namespace ebc;
 
 namespace {
 
-constexpr int kMaxThreads = 512;
+constexpr int kMaxThreads = 1024;
+constexpr int kFewThreads = 512;   // of a row of the gradient
 constexpr int kRowThreads = 256;   // of a CTA whose rows take a warp or less each
 
 // ---- one row on a group of threads ----
@@ -38,8 +39,8 @@ __device__ __forceinline__ void group_sum(float (&v)[K], float (*part)[K][kMaxTh
     for (int k = 0; k < K; ++k) {
       float s = lane < warps ? part[turn][k][group * warps + lane] : 0.f;
 #pragma unroll
-      for (int off = kMaxThreads / 64; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
-      v[k] = __shfl_sync(0xffffffffu, s, 0);
+      for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
+      v[k] = s;
     }
   }
 }
@@ -267,10 +268,11 @@ struct NormArgs {
 // to 8 bits 41.5 and 78, both 48 and 93; off a boundary, x 4095, 51 us.  A row on
 // fewer threads with more values each takes fewer joins: 16384 x 1024 25.1 us with
 // eight values a thread, 22.1 with sixteen.
-// (What rows off a boundary need beside must not cost them half of the warps: two
-// CTAs of 512 threads an SM.)
+// An SM has 1024 threads of 16 values: left to take 68 registers the first two took
+// 47.8 and 91 us.  Wide rows: 2048 x 16384 bf16 38.4 us (on 512 threads of 32 values
+// 40.6), off a boundary 2731 x 12289 41.0 (45.5).
 template <typename T, int V, int N, int kLanes, bool kShift>
-__global__ void __launch_bounds__(kShift && N * V > 16 ? 576 : kMaxThreads, kShift && N * V <= 16 ? 2 : 1) k_norm(NormArgs a) {
+__global__ void __launch_bounds__(kMaxThreads) k_norm(NormArgs a) {
   __shared__ float part[2][1][kMaxThreads / 32];
   pdl_enter();
   using C = Chunk<V>;
@@ -281,7 +283,7 @@ __global__ void __launch_bounds__(kShift && N * V > 16 ? 576 : kMaxThreads, kShi
   const float share = 1.f / (float)a.width;
   // single weights stay in registers where there is room for them; vectors of them
   // are read again (a wait for them ahead of the first row: 43 -> 49 us of 8192 x 4096 bf16)
-  constexpr bool kKeep = V < 8 && N * V <= 16;
+  constexpr bool kKeep = N * V <= 8 && V < 8;
   extern __shared__ ulonglong2 dynamic[];   // kShift: the weights, and what is rounded to 8 bits
   const int c0 = at * V - shift_of<T, V, kShift>(a.x, a.ld_x, blockIdx.x * groups + threadIdx.x / lanes);
   const int hop = lanes * V;   // from the thread's first column to the next
@@ -488,7 +490,7 @@ struct Ring {
 
 // (Rows off a boundary take a warp more; two CTAs an SM still.)
 constexpr int grad_threads(int lanes, int values, bool shift) {
-  return lanes ? kRowThreads : shift && values <= 16 ? 576 : kMaxThreads;
+  return lanes ? kRowThreads : shift && values <= 16 ? 576 : kFewThreads;
 }
 template <typename T, int V, int N, int kLanes, int kStages, bool kShift>
 __global__ void __launch_bounds__(grad_threads(kLanes, N * V, kShift)) k_norm_grad(GradArgs a, int row_lanes) {
@@ -742,30 +744,34 @@ template <typename T, typename F, int V, int N, bool kShift>
 cudaError_t on_warps(int width, F&& f, Layout<T, V, N, 0, kShift> layout) {
   return f(layout, ((width + V * N - 1) / (V * N) + 31) / 32 * 32);
 }
-template <typename T, bool kShift, typename F>
+// kMost: the threads of a row with 16 values each; past them (a gradient's rows) it
+// takes 32 values on half of that.
+template <typename T, bool kShift, int kMost, typename F>
 cudaError_t on_wide(int width, F&& f) {   // more than 512 columns
-  if (width <= 8192) return on_warps<T>(width, f, Layout<T, 8, 2, 0, kShift>{});
-  return on_warps<T>(width, f, Layout<T, 8, 4, 0, kShift>{});
+  if constexpr (16 * kMost < EBC_MAX_NORM_WIDTH)
+    if (width > 16 * kMost) return on_warps<T>(width, f, Layout<T, 8, 4, 0, kShift>{});
+  return on_warps<T>(width, f, Layout<T, 8, 2, 0, kShift>{});
 }
-template <typename T, bool kShift, typename F>
+template <typename T, bool kShift, int kMost, typename F>
 cudaError_t with_vectors(int width, F&& f) {
   if (width <= 64) return f(Layout<T, 8, 1, 8, kShift>{}, kRowThreads);
   if (width <= 128) return f(Layout<T, 8, 1, 16, kShift>{}, kRowThreads);
   if (width <= 256) return f(Layout<T, 8, 1, 32, kShift>{}, kRowThreads);
   if (width <= 512) return f(Layout<T, 8, 2, 32, kShift>{}, kRowThreads);
-  return on_wide<T, kShift>(width, f);
+  return on_wide<T, kShift, kMost>(width, f);
 }
-template <typename T, typename F>
+template <typename T, int kMost, typename F>
 cudaError_t with_layout(int v, int width, F&& f) {
-  if (v == 8) return with_vectors<T, false>(width, f);
+  constexpr int kValues = EBC_MAX_NORM_WIDTH / kMost;   // of a thread, in the widest rows
+  if (v == 8) return with_vectors<T, false, kMost>(width, f);
   if (v == 2) {
     if (width <= 512) return f(Layout<T, 2, 8, 32, false>{}, kRowThreads);
     if (width <= 4096) return on_warps<T>(width, f, Layout<T, 2, 4, 0, false>{});
-    return on_warps<T>(width, f, Layout<T, 2, 16, 0, false>{});
+    return on_warps<T>(width, f, Layout<T, 2, kValues / 2, 0, false>{});
   }
   if (width <= 256) return f(Layout<T, 1, 8, 32, false>{}, kRowThreads);
   if (width <= 4096) return on_warps<T>(width, f, Layout<T, 1, 8, 0, false>{});
-  return on_warps<T>(width, f, Layout<T, 1, 32, 0, false>{});
+  return on_warps<T>(width, f, Layout<T, 1, kValues, 0, false>{});
 }
 
 template <typename F>
@@ -856,8 +862,8 @@ int ebc_norm(ebc_ctx* ctx, const void* d_x, int64_t ld_x, const void* d_residual
                           dim3(threads), smem, 1, a);
     };
     const int vals = at.values(d_weight, wb);
-    return vals < 8 && at.shifts(width) ? with_vectors<T, true>((int)width + 7, launch)
-                                        : with_layout<T>(vals, (int)width, launch);
+    return vals < 8 && at.shifts(width) ? with_vectors<T, true, kMaxThreads>((int)width + 7, launch)
+                                        : with_layout<T, kMaxThreads>(vals, (int)width, launch);
   }));
 }
 
@@ -902,7 +908,7 @@ int ebc_norm_grad(ebc_ctx* ctx, const void* d_dy, int64_t ld_dy, const void* d_h
         // stages: with two CTAs of 256 threads an SM that is 98 KB in flight (8192 x
         // 4096 bf16 with dh 45.0 us; 45.5 with two stages, 47.8 with four), and with
         // one of 448 threads 86 KB (8192 x 7168: 73.4; 80.9, 72.7).
-        constexpr int kBytes = 3 * L::N * L::V * (int)sizeof(typename L::T) * kMaxThreads;   // of a stage
+        constexpr int kBytes = 3 * L::N * L::V * (int)sizeof(typename L::T) * kFewThreads;   // of a stage
         constexpr int kStages = L::kLanes || L::V < 8 || (L::kShift && L::N > 2) ? 0 : kBytes <= 64 * 1024 ? 3 : kBytes <= 96 * 1024 ? 2 : 0;
         const auto kernel = k_norm_grad<typename L::T, L::V, L::N, L::kLanes, kStages, L::kShift>;
         // Rows that take less than 256 threads: several in a CTA.
@@ -910,14 +916,14 @@ int ebc_norm_grad(ebc_ctx* ctx, const void* d_dy, int64_t ld_dy, const void* d_h
         threads = groups * lanes;
         // All CTAs at once, as many on each SM: as registers (at most 128 a thread),
         // shared memory and the scratch's rows allow.
-        constexpr int kFit = L::N * L::V <= 8 ? 1024 : L::kLanes ? kMaxThreads : grad_threads(0, L::N * L::V, L::kShift);
+        constexpr int kFit = L::N * L::V <= 8 ? 1024 : L::kLanes ? kFewThreads : grad_threads(0, L::N * L::V, L::kShift);
         int64_t each = kFit / threads < 1 ? 1 : kFit / threads;
         // where the groups' sums are added up
         size_t smem = groups > 1 ? (size_t)4 * L::N * L::V * lanes : 0;
         if constexpr (L::kShift && kStages == 0) {   // the weights
           static_assert(L::kLanes == 0 && L::N * L::V > 16);   // (a CTA is one group)
           smem = (size_t)4 * L::N * L::V * threads;
-          const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 4 * L::N * L::V * kMaxThreads);
+          const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 4 * L::N * L::V * kFewThreads);
           if (e != cudaSuccess) return e;
         }
         if constexpr (kStages > 0) {
@@ -939,8 +945,8 @@ int ebc_norm_grad(ebc_ctx* ctx, const void* d_dy, int64_t ld_dy, const void* d_h
         return launch_named(v, "k_norm_grad", st, kernel, dim3((unsigned)a.n_parts), dim3(threads), smem, 1, a, lanes);
       };
       if constexpr (sizeof(T) == 2)
-        if (shift) return on_wide<T, true>((int)width + 7, launch);
-      return with_layout<T>(vals, (int)width, launch);
+        if (shift) return on_wide<T, true, kFewThreads>((int)width + 7, launch);
+      return with_layout<T, kFewThreads>(vals, (int)width, launch);
     });
   }
   if (e == cudaSuccess && a.n_parts != 1)
