@@ -896,10 +896,11 @@ int ebc_norm_grad(ebc_ctx* ctx, const void* d_dy, int64_t ld_dy, const void* d_h
     const int vals_s = row_values((uintptr_t)d_scratch | (uintptr_t)(width * 4), 4);
     if (vals > vals_s) vals = vals_s;
     // Rows off the boundary in whole vectors where it takes less time: many wide
-    // ones of 16-bit values (us, single values / so: 128 x 4095 6.2 / 9.6, 512 x 4095
-    // 12.7 / 13.0, 1531 x 1001 12.2 / 10.5, 16384 x 1001 66 / 32, 16384 x 101 12.7 /
-    // 21.9; in fp32 16384 x 1001 53 / 56).
-    const bool shift = vals < 8 && at.shifts(width) && b == 2 && width > 512 && rows * width >= 3 << 19;
+    // ones, of fp32 very wide ones (us, single values / so, bf16: 128 x 4095 6.2 / 9.6,
+    // 512 x 4095 12.7 / 13.0, 1531 x 1001 12.2 / 10.5, 16384 x 1001 66 / 32, 16384 x
+    // 101 12.7 / 21.9; fp32 with dh: 16384 x 1001 60 / 70, 8192 x 4095 132 / 141, 4096
+    // x 8191 284 / 192, 2048 x 12289 274 / 118).
+    const bool shift = vals < 8 && at.shifts(width) && width > (b == 2 ? 512 : 4096) && rows * width >= 3 << 19;
     e = with_type_of(type, [&](auto one) {
       using T = decltype(one);
       auto launch = [&](auto l, int threads) {
@@ -944,8 +945,7 @@ int ebc_norm_grad(ebc_ctx* ctx, const void* d_dy, int64_t ld_dy, const void* d_h
         a.n_parts = (int)(want < most ? want : most);
         return launch_named(v, "k_norm_grad", st, kernel, dim3((unsigned)a.n_parts), dim3(threads), smem, 1, a, lanes);
       };
-      if constexpr (sizeof(T) == 2)
-        if (shift) return on_wide<T, true, kFewThreads>((int)width + 7, launch);
+      if (shift) return on_wide<T, true, kFewThreads>((int)width + 7, launch);
       return with_layout<T, kFewThreads>(vals, (int)width, launch);
     });
   }
