@@ -485,8 +485,10 @@ struct Ring {
 // 304 CTAs; several narrow rows go to a CTA so that there are no more).
 // Bound by bandwidth, if loads are in flight while a row's sums go around the
 // CTA: with kStages, the rows to come are copied to shared memory meanwhile
-// (without: 73 us of 8192 x 4096 bf16 with dh, so: 44, 6.1 TB/s; 16384 rows 82, 6.5).
-// Rows off a boundary, one value an access: issue and latency (8192 x 1001 fp32 28 us).
+// (without: 73 us of 8192 x 4096 bf16 with dh, so: 44, 6.1 TB/s; 16384 rows 82, 6.6).
+// Not so for fp32, whose vectors are wider than such a copy (137 us with, 93
+// without: 5.8 TB/s).  Rows off a boundary: 8192 x 4095 bf16 70 us, fp32 103; one
+// value an access, issue and latency (1531 x 1001 fp32 11.4 us).
 
 // (Rows off a boundary take a warp more; two CTAs an SM still.)
 constexpr int grad_threads(int lanes, int values, bool shift) {
@@ -895,12 +897,13 @@ int ebc_norm_grad(ebc_ctx* ctx, const void* d_dy, int64_t ld_dy, const void* d_h
     // (fp32 partial rows start where the scratch's 16 bytes allow: whole vectors of 8 want 32)
     const int vals_s = row_values((uintptr_t)d_scratch | (uintptr_t)(width * 4), 4);
     if (vals > vals_s) vals = vals_s;
-    // Rows off the boundary in whole vectors where it takes less time: many wide
-    // ones, of fp32 very wide ones (us, single values / so, bf16: 128 x 4095 6.2 / 9.6,
-    // 512 x 4095 12.7 / 13.0, 1531 x 1001 12.2 / 10.5, 16384 x 1001 66 / 32, 16384 x
-    // 101 12.7 / 21.9; fp32 with dh: 16384 x 1001 60 / 70, 8192 x 4095 132 / 141, 4096
-    // x 8191 284 / 192, 2048 x 12289 274 / 118).
-    const bool shift = vals < 8 && at.shifts(width) && width > (b == 2 ? 512 : 4096) && rows * width >= 3 << 19;
+    // Rows off the boundary in whole vectors where it takes less time: very wide ones,
+    // and many of more than 512 values (us with dh, single values / so, bf16: 600 x
+    // 1001 7.9 / 8.6, 1024 x 1001 10.6 / 8.8, 128 x 4095 6.5 / 9.8, 512 x 4095 14.2 /
+    // 13.2, 64 x 8101 27.8 / 11.1, 16384 x 101 12.7 / 21.9; fp32: 2048 x 1001 13.5 /
+    // 12.7, 512 x 4095 13.9 / 15.2, 8192 x 4095 132 / 103, 64 x 8101 22.6 / 11.8).
+    const bool many = rows * width >= (b == 2 ? 3 << 18 : 1 << 22);
+    const bool shift = vals < 8 && at.shifts(width) && (width > 4096 || (width > 512 && many));
     e = with_type_of(type, [&](auto one) {
       using T = decltype(one);
       auto launch = [&](auto l, int threads) {
@@ -909,8 +912,7 @@ int ebc_norm_grad(ebc_ctx* ctx, const void* d_dy, int64_t ld_dy, const void* d_h
         // stages: with two CTAs of 256 threads an SM that is 98 KB in flight (8192 x
         // 4096 bf16 with dh 45.0 us; 45.5 with two stages, 47.8 with four), and with
         // one of 448 threads 86 KB (8192 x 7168: 73.4; 80.9, 72.7).
-        constexpr int kBytes = 3 * L::N * L::V * (int)sizeof(typename L::T) * kFewThreads;   // of a stage
-        constexpr int kStages = L::kLanes || L::V < 8 || (L::kShift && L::N > 2) ? 0 : kBytes <= 64 * 1024 ? 3 : kBytes <= 96 * 1024 ? 2 : 0;
+        constexpr int kStages = L::kLanes || L::V < 8 || sizeof(typename L::T) > 2 ? 0 : L::N == 2 ? 3 : L::kShift ? 0 : 2;
         const auto kernel = k_norm_grad<typename L::T, L::V, L::N, L::kLanes, kStages, L::kShift>;
         // Rows that take less than 256 threads: several in a CTA.
         const int lanes = L::kLanes ? L::kLanes : threads, groups = L::kLanes || threads <= 128 ? kRowThreads / lanes : 1;
@@ -921,10 +923,9 @@ int ebc_norm_grad(ebc_ctx* ctx, const void* d_dy, int64_t ld_dy, const void* d_h
         int64_t each = kFit / threads < 1 ? 1 : kFit / threads;
         // where the groups' sums are added up
         size_t smem = groups > 1 ? (size_t)4 * L::N * L::V * lanes : 0;
-        if constexpr (L::kShift && kStages == 0) {   // the weights
-          static_assert(L::kLanes == 0 && L::N * L::V > 16);   // (a CTA is one group)
+        if constexpr (L::kShift && kStages == 0) {   // the weights, before that
           smem = (size_t)4 * L::N * L::V * threads;
-          const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 4 * L::N * L::V * kFewThreads);
+          const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
           if (e != cudaSuccess) return e;
         }
         if constexpr (kStages > 0) {

@@ -23,7 +23,8 @@ EPS = 1e-6
 SIZES = [(1, 1), (3, 2), (1, 8), (5, 31), (40, 33), (9, 64), (1000, 64), (70, 65), (300, 128), (13, 136), (257, 256), (7, 258),
          (3, 301), (600, 512), (5, 520), (2, 1000), (3, 1001), (4, 1002), (400, 1024), (1, 2048), (3, 2050), (650, 4096), (3, 4098),
          (2, 5001), (700, 7168), (3, 8192), (2, 8200), (2, 12289), (2, 16384), (2, 16383), (2, 16382),
-         (300, 8199), (200, 12289), (97, 16377), (400, 16383), (400, 16382)]
+         (300, 8199), (200, 12289), (97, 16377), (400, 16383), (400, 16382),
+         (1100, 4099), (5000, 1001)]
 
 
 @pytest.fixture(scope="module")
