@@ -271,7 +271,10 @@ struct NormArgs {
 // An SM has 1024 threads of 16 values: left to take 68 registers the first two took
 // 47.8 and 91 us.  Wide rows: 2048 x 16384 bf16 38.4 us (on 512 threads of 32 values
 // 40.6), off a boundary 2731 x 12289 41.0 (45.5).
-template <typename T, int V, int N, int kLanes, bool kShift>
+// kAhead: without a residual there is room to load a row ahead (8192 x 4096 bf16 30.1
+// -> 24.8 us, x 4095 36.2 -> 27.2, 2048 x 16384 38.3 -> 26.1; in one kernel with the
+// residual's addition that loses 1 to 4%).
+template <typename T, int V, int N, int kLanes, bool kShift, bool kAhead>
 __global__ void __launch_bounds__(kMaxThreads) k_norm(NormArgs a) {
   __shared__ float part[2][1][kMaxThreads / 32];
   pdl_enter();
@@ -301,22 +304,26 @@ __global__ void __launch_bounds__(kMaxThreads) k_norm(NormArgs a) {
       Slots::put(dynamic, q, w);
     }
   int turn = 0;
+  Values<T, V> xv[N];
+  auto load_x = [&](int64_t row) {
+    span.load(xv, (const T*)a.x + row * a.ld_x + c0, row < a.rows, row == 0 || row == a.rows - 1);
+  };
+  if constexpr (kAhead) load_x((int64_t)blockIdx.x * groups + threadIdx.x / lanes);
   // the groups of a warp, and the warps of a CTA, go through the same rounds
   for (int64_t row0 = (int64_t)blockIdx.x * groups; row0 < a.rows; row0 += step, turn ^= 1) {
     const int64_t row = row0 + threadIdx.x / lanes;
     const bool live = row < a.rows;
-    Values<T, V> xv[N];
     Two f[kChunks][C::kTwos];
-    const bool edge = row == 0 || row == a.rows - 1;
     auto store = [&](void* rows) {
+      Values<T, V> out[N];
 #pragma unroll
-      for (int q = 0; q < kChunks; ++q) narrow<T, V>(f[q], xv + q * C::kVecs);
-      if (live) span.store(xv, (T*)rows + row * a.width + c0);
+      for (int q = 0; q < kChunks; ++q) narrow<T, V>(f[q], out + q * C::kVecs);
+      if (live) span.store(out, (T*)rows + row * a.width + c0);
     };
-    span.load(xv, (const T*)a.x + row * a.ld_x + c0, live, edge);
-    if (a.r) {
+    if constexpr (!kAhead) load_x(row);
+    if (!kAhead && a.r) {
       Values<T, V> rv[N];
-      span.load(rv, (const T*)a.r + row * a.ld_r + c0, live, edge);
+      span.load(rv, (const T*)a.r + row * a.ld_r + c0, live, row == 0 || row == a.rows - 1);
       span.clip(xv);
       span.clip(rv);
 #pragma unroll
@@ -331,6 +338,7 @@ __global__ void __launch_bounds__(kMaxThreads) k_norm(NormArgs a) {
       span.clip(xv);
 #pragma unroll
       for (int q = 0; q < kChunks; ++q) widen<T, V>(xv + q * C::kVecs, f[q]);
+      if constexpr (kAhead) load_x(row + step);
     }
     if (a.h) store(a.h);
     Two squares = 0;
@@ -844,14 +852,13 @@ int ebc_norm(ebc_ctx* ctx, const void* d_x, int64_t ld_x, const void* d_residual
   at.add(d_h, width);
   return cuda_code(with_type_of(type, [&](auto one) {
     using T = decltype(one);
-    auto launch = [&](auto l, int threads) {
+    auto run = [&](auto l, int threads, auto kernel, bool ahead) {
       using L = decltype(l);
       const int groups = L::kLanes ? threads / L::kLanes : 1;
       // (a multiple of eight, so that a group's rows are all off by as much; with
-      // weights in registers no more than are resident)
+      // weights kept, or a row ahead, no more than are resident)
       const int64_t want = (rows + groups - 1) / groups;
-      const int64_t most = ((int64_t)v.nsm * (L::kShift ? (1024 / threads ? 1024 / threads : 1) : 2048 / threads * 2)) & ~7ll;
-      const auto kernel = k_norm<typename L::T, L::V, L::N, L::kLanes, L::kShift>;
+      const int64_t most = ((int64_t)v.nsm * (L::kShift || ahead ? 1024 / threads : 2048 / threads * 2)) & ~7ll;
       size_t smem = 0;
       if constexpr (L::kShift) {
         constexpr int kWeights = 4 * L::N * L::V, kRow = kWeights / 8 * 9;   // bytes a thread
@@ -862,6 +869,12 @@ int ebc_norm(ebc_ctx* ctx, const void* d_x, int64_t ld_x, const void* d_residual
       }
       return launch_named(v, "k_norm", st, kernel, dim3((unsigned)(want < most || most < 8 ? want : most)),
                           dim3(threads), smem, 1, a);
+    };
+    auto launch = [&](auto l, int threads) {
+      using L = decltype(l);
+      if constexpr (L::V == 8)
+        if (!d_residual) return run(l, threads, k_norm<typename L::T, L::V, L::N, L::kLanes, L::kShift, true>, true);
+      return run(l, threads, k_norm<typename L::T, L::V, L::N, L::kLanes, L::kShift, false>, false);
     };
     const int vals = at.values(d_weight, wb);
     return vals < 8 && at.shifts(width) ? with_vectors<T, true, kMaxThreads>((int)width + 7, launch)
