@@ -246,9 +246,9 @@ __device__ __noinline__ void settle_order(const RouteArgs& a, Room<N>& room, con
 // A warp a token; lane i has the experts i * N to i * N + N - 1, whose values in
 // 32 bits are -infinity where they may not be chosen.
 //
-// The choice: the (top + 1)-th largest of the lanes' largest values is a bound
-// that at least top + 1 values reach; those that do (few more) are put into
-// lanes in the experts' order, and each counts the ones before it.
+// The choice: the top-th largest of the lanes' largest values is a bound that at
+// least `top` values reach; those that do (few more) are put into lanes in the
+// experts' order, and each counts the ones before it.
 //
 // Whether that is the choice that the scores themselves give: the logits order
 // it, as they are, where there is no bias; else a value in 32 bits is off by at
@@ -260,8 +260,8 @@ __device__ __noinline__ void settle_order(const RouteArgs& a, Room<N>& room, con
 // a lane each; its whole row so took 30).
 //
 // Bound by issue: some 600 instructions a token, 300 more for the scores of a
-// bias, 350 more for groups.  8192 tokens x 256 experts, 8 chosen: 7.6 us by the
-// logits, 11.7 with a bias, 14.4 with both; x 64: 6.1.  A search a choice took 15.8,
+// bias, 350 more for groups.  8192 tokens x 256 experts, 8 chosen: 7.4 us by the
+// logits, 11.6 with a bias, 14.4 with both; x 64: 6.0.  A search a choice took 15.8,
 // 46 and 58.  A token alone takes 2.5 to 4 us of latency.
 template <typename T, int N, int kWarps>
 __global__ void __launch_bounds__(32 * kWarps, N <= 8 ? 8 : 4) k_moe_route(const __grid_constant__ RouteArgs a) {
@@ -398,20 +398,41 @@ __global__ void __launch_bounds__(32 * kWarps, N <= 8 ? 8 : 4) k_moe_route(const
     }
     int id = -1;
     if (!generic) {
-      // the best top + 1, and whatever may be among the best top
+      // at least the best `top`, and whatever may be among them
+      auto from = [&](float bound) {
+        if (a.bias) bound -= 2.f * err;
+        uint32_t bits = 0;
+#pragma unroll
+        for (int j = 0; j < N; ++j)
+          if (c[j] >= bound && c[j] > -CUDART_INF_F) bits |= 1u << j;
+        return gather(room, bits, c, lane);
+      };
       float bound = -CUDART_INF_F, left = top1;
 #pragma unroll 1
-      for (int r = 0; r <= a.top; ++r) {
+      for (int r = 0; r < a.top; ++r) {
         bound = warp_max(left);
         if (bound == -CUDART_INF_F) break;
         if (left == bound) left = -CUDART_INF_F;
       }
-      if (a.bias) bound -= 2.f * err;
-      uint32_t bits = 0;
+      int found = from(bound);
+      if (found > 32 && a.bias) {
+        // many choices, or few lanes with what may be chosen: as many of the values
+        // themselves, equal ones of a lane once (8 of two groups of 32: 369 -> 16 us of
+        // 8192 tokens, 24 of 256: 818 -> 24; what was left to choose_exactly)
+        left = top1;
+#pragma unroll 1
+        for (int r = 0; r < a.top; ++r) {
+          bound = warp_max(left);
+          if (bound == -CUDART_INF_F) break;
+          if (left == bound) {
+            left = -CUDART_INF_F;
 #pragma unroll
-      for (int j = 0; j < N; ++j)
-        if (c[j] >= bound && c[j] > -CUDART_INF_F) bits |= 1u << j;
-      const int found = gather(room, bits, c, lane);
+            for (int j = 0; j < N; ++j)
+              if (c[j] < bound) left = fmaxf(left, c[j]);
+          }
+        }
+        found = from(bound);
+      }
       if (found <= 32) {
         float v = lane < found ? room.value(lane) : -CUDART_INF_F;
         int e = lane < found ? room.id(lane) : -1, rank = 0;

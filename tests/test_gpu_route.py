@@ -125,7 +125,7 @@ def logits_of(tokens, experts, dtype, seed, masked=0.0, spread=1.0):
 @pytest.mark.parametrize("kind", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("tokens,experts,top,masked", [
     (1, 1, 1, 0.0), (1, 64, 8, 0.0), (5, 2, 2, 0.3), (33, 10, 3, 0.2), (7, 32, 32, 0.0), (40, 33, 7, 0.1), (100, 64, 6, 0.0), (20, 100, 32, 0.5),
-    (50, 128, 8, 0.0), (300, 256, 8, 0.0), (30, 257, 16, 0.1), (9, 512, 1, 0.0), (6, 1000, 31, 0.0), (6, 1024, 32, 0.9), (3, 40, 9, 1.0)])
+    (50, 128, 8, 0.0), (300, 256, 8, 0.0), (30, 257, 16, 0.1), (9, 512, 1, 0.0), (6, 1000, 31, 0.0), (6, 1024, 32, 0.9), (40, 256, 24, 0.0), (40, 64, 31, 0.0), (3, 40, 9, 1.0)])
 def test_without_groups(ex, tokens, experts, top, masked, kind, dtype):
     l, b = logits_of(tokens, experts, dtype, tokens + experts, masked)
     check(ex, l, top, kind=kind)
@@ -137,7 +137,7 @@ def test_without_groups(ex, tokens, experts, top, masked, kind, dtype):
 @pytest.mark.parametrize("kind", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("tokens,experts,groups,keep,top,masked", [
     (1, 256, 8, 4, 8, 0.0), (300, 256, 8, 4, 8, 0.0), (50, 256, 8, 1, 6, 0.1), (40, 64, 32, 5, 8, 0.2), (20, 32, 32, 7, 7, 0.0), (60, 30, 3, 2, 4, 0.2),
-    (33, 35, 5, 2, 6, 0.1), (21, 1024, 16, 3, 20, 0.0), (15, 992, 31, 30, 32, 0.0), (10, 12, 2, 1, 9, 0.3), (10, 12, 2, 2, 9, 0.3), (8, 48, 24, 3, 2, 1.0)])
+    (33, 35, 5, 2, 6, 0.1), (21, 1024, 16, 3, 20, 0.0), (60, 256, 8, 2, 8, 0.0), (60, 256, 8, 2, 24, 0.1), (30, 512, 4, 1, 32, 0.0), (15, 992, 31, 30, 32, 0.0), (10, 12, 2, 1, 9, 0.3), (10, 12, 2, 2, 9, 0.3), (8, 48, 24, 3, 2, 1.0)])
 def test_groups(ex, tokens, experts, groups, keep, top, masked, kind):
     l, b = logits_of(tokens, experts, torch.float32, tokens + experts, masked)
     for group_top in (1, 2):
@@ -293,7 +293,7 @@ def check_grad(l, ids, dw, got, kind, renorm, scale):
 @pytest.mark.parametrize("renorm", [False, True])
 @pytest.mark.parametrize("tokens,experts,top,masked", [
     (1, 1, 1, 0.0), (1, 64, 8, 0.0), (5, 2, 2, 0.3), (33, 10, 3, 0.2), (7, 32, 32, 0.0), (40, 33, 7, 0.1), (20, 100, 32, 0.5), (300, 256, 8, 0.0),
-    (30, 257, 16, 0.1), (9, 512, 1, 0.0), (6, 1023, 31, 0.0), (6, 1024, 32, 0.9), (3, 40, 9, 1.0)])
+    (30, 257, 16, 0.1), (9, 512, 1, 0.0), (6, 1023, 31, 0.0), (6, 1024, 32, 0.9), (40, 256, 24, 0.0), (40, 64, 31, 0.0), (3, 40, 9, 1.0)])
 def test_the_gradient(ex, tokens, experts, top, masked, renorm, kind, dtype):
     l, b = logits_of(tokens, experts, dtype, tokens + experts, masked)
     dw = torch.randn(tokens, top, device="cuda")
