@@ -938,7 +938,8 @@ int ebc_norm_grad(ebc_ctx* ctx, const void* d_dy, int64_t ld_dy, const void* d_h
         size_t smem = groups > 1 ? (size_t)4 * L::N * L::V * lanes : 0;
         if constexpr (L::kShift && kStages == 0) {   // the weights, before that
           smem = (size_t)4 * L::N * L::V * threads;
-          const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+          const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                     4 * L::N * L::V * grad_threads(0, L::N * L::V, true));
           if (e != cudaSuccess) return e;
         }
         if constexpr (kStages > 0) {

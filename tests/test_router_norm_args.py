@@ -153,6 +153,28 @@ def test_the_norms_gradient_stays_inside_its_scratch(fake):
     fake.ebc_destroy(ctx)
 
 
+def test_a_kernel_is_allowed_the_same_shared_memory_by_every_call(fake):
+    """Contexts of two host threads then do not take it from each other; and every launch stays within it."""
+    ctx = context(fake)
+    rng = random.Random(1)
+    allowed = {}
+    fake.fake_static_shared(1024)
+    for i in range(600):
+        rows, width, kind = int(2 ** rng.uniform(0, 16)), int(2 ** rng.uniform(0, 14)) if i else 16377, rng.randrange(3)
+        for shift in (0, 4):
+            assert fake.ebc_norm(ctx, A + shift, width, None, 0, kind, A, 0, rows, width, 1e-6, A + shift, None, A, A, None) == 0, (rows, width)
+            assert fake.ebc_norm_grad(ctx, A + shift, width, A + shift, width, A + shift, width, kind, A, 0, rows, width, 1e-6,
+                                      A + shift, A, A, None) == 0, (rows, width)
+        log = fake.fake_log().decode()
+        fake.fake_clear()
+        assert "refused" not in log
+        for name, most in re.findall(r"shared (\S+) (\d+)", re.sub(r"launch.*", "", log)):
+            allowed.setdefault(name, set()).add(int(most))
+    fake.fake_static_shared(256)
+    fake.ebc_destroy(ctx)
+    assert len(allowed) > 10 and all(len(v) == 1 and max(v) <= 226 * 1024 for v in allowed.values()), allowed
+
+
 def test_an_8_bit_product_takes_no_more_rows_than_its_tiles_can_count(fake):
     ctx = context(fake)
     most = 2 ** 31 - 256
