@@ -121,7 +121,9 @@ class Experts:
     """The expert-parallel, 4- and 8-bit, router and norm operators on one CUDA device.  Calls are
     asynchronous on `stream` (None: the device's current stream), take no
     scratch, and return new tensors of that stream; not thread safe, use one
-    per host thread."""
+    per host thread.  A backward pass can be captured into a graph; as with
+    torch's own operations, outputs of eager passes over the same leaves are
+    released before."""
 
     def __init__(self, device: int = 0):
         self.device = torch.device("cuda", device)

@@ -170,6 +170,47 @@ def test_a_layer_is_trained(ex, score, renormalize):
     ex.check()
 
 
+def test_a_training_pass_in_a_graph(ex):
+    """Forward and backward captured together and replayed on other inputs: the bits of an eager pass.  (Outputs of
+    eager passes over the same leaves are gone by then, as torch asks.)"""
+    tokens, width, experts, top = 70, 200, 16, 4
+    g = torch.Generator("cuda").manual_seed(9)
+    make = lambda *s: torch.randn(*s, generator=g, device="cuda")  # noqa: E731
+    leaves = [t.requires_grad_() for t in (make(tokens, width), make(tokens, width), 1 + 0.1 * make(width), make(width, experts) / 10)]
+    inputs = [[make(tokens, width) for _ in range(4)] for _ in range(3)]   # x, residual, dy, dh
+    bias = 0.1 * make(experts)
+
+    def step(dy, dh):
+        x, r, gain, gate = leaves
+        y, h = ex.norm(x, gain, r)
+        ids, p = ex.route(y @ gate, top, bias=bias, **ROUTER)
+        plan = ex.plan(ids, experts)
+        out = ex.combine(ex.dispatch(y, plan), p, plan)
+        return torch.autograd.grad((out, h), leaves, (dy, dh))
+
+    def eager(x, r, dy, dh):
+        with torch.no_grad():
+            leaves[0].copy_(x)
+            leaves[1].copy_(r)
+        return step(dy, dh)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        want = [[t.clone() for t in eager(*i)] for i in inputs]
+    torch.cuda.synchronize()
+    graph, dy, dh = torch.cuda.CUDAGraph(), inputs[0][2].clone(), inputs[0][3].clone()
+    with torch.cuda.graph(graph):
+        got = step(dy, dh)
+    for k in (1, 0, 2, 1):
+        with torch.no_grad():
+            for t, i in zip((leaves[0], leaves[1], dy, dh), inputs[k]):
+                t.copy_(i)
+        graph.replay()
+        assert all(torch.equal(a, b) for a, b in zip(got, want[k])), k
+    ex.check()
+
+
 def test_8_bit_rows_of_several_ranks_to_one_product(ex):
     """Pieces of several senders, each sorted by expert, are sorted together by a plan of one choice a row."""
     width, experts, outs = 200, 6, 40
