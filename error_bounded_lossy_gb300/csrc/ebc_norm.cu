@@ -495,8 +495,10 @@ struct Ring {
 // CTA: with kStages, the rows to come are copied to shared memory meanwhile
 // (without: 73 us of 8192 x 4096 bf16 with dh, so: 44, 6.1 TB/s; 16384 rows 82, 6.6).
 // Not so for fp32, whose vectors are wider than such a copy (137 us with, 93
-// without: 5.8 TB/s).  Rows off a boundary: 8192 x 4095 bf16 70 us, fp32 103; one
-// value an access, issue and latency (1531 x 1001 fp32 11.4 us).
+// without: 5.8 TB/s).  Weights stay in registers: read again each row, 2048 x 16384
+// bf16 took 74 us, so 48 (5.6 TB/s).  Rows off a boundary: 8192 x 4095 bf16 70 us,
+// 2048 x 16377 66, 8192 x 4095 fp32 103; one value an access, issue and latency (1531
+// x 1001 fp32 11.4 us).
 
 // (Rows off a boundary take a warp more; two CTAs an SM still.)
 constexpr int grad_threads(int lanes, int values, bool shift) {
@@ -507,9 +509,9 @@ __global__ void __launch_bounds__(grad_threads(kLanes, N * V, kShift)) k_norm_gr
   using R = Ring<T, V, N, kStages>;
   using C = Chunk<V>;
   constexpr int kChunks = N / C::kVecs;
-  // More values than registers hold beside dw: they are read twice, the second
-  // time mostly out of the L1 cache, a few at a time.
-  constexpr bool kAgain = kStages == 0 && N * V > 16;
+  // More values than registers hold beside dw: they are read twice, a few at a time,
+  // the second time out of shared memory, or mostly of the L1 cache.
+  constexpr bool kAgain = N * V > 16;
   constexpr int M = kAgain ? 8 / V : N;
   static_assert(!kAgain || kLanes == 0);   // (a barrier between the two)
   __shared__ float part[2][2][kMaxThreads / 32];
@@ -542,7 +544,7 @@ __global__ void __launch_bounds__(grad_threads(kLanes, N * V, kShift)) k_norm_gr
   };
   for (int i = 0; i < kStages - 1; ++i) request((int64_t)blockIdx.x * groups + i * step, i);
   // the weights stay in registers, or in shared memory behind the rows to come
-  constexpr bool kSlots = kShift, kKeep = !kSlots && N * V <= 16;
+  constexpr bool kSlots = kShift && (N * V <= 16 || kStages == 0), kKeep = !kSlots && (N * V <= 16 || V == 8);
   ulonglong2* slots = nullptr;
   if constexpr (kSlots) {
     extern __shared__ uint4 ring[];
@@ -560,6 +562,16 @@ __global__ void __launch_bounds__(grad_threads(kLanes, N * V, kShift)) k_norm_gr
       Slots::put(slots, q, w);
     }
   }
+  auto weights = [&](int q, Two (&w)[C::kTwos]) {
+    if constexpr (kSlots) {
+      Slots::get(slots, q, w);
+    } else if constexpr (kKeep) {
+#pragma unroll
+      for (int k = 0; k < C::kTwos; ++k) w[k] = kept[q][k];
+    } else {
+      load_weights<kShift, V>(a.w, a.w_type, c0 + q * C::kVecs * hop, hop, a.width, w);
+    }
+  };
   int turn = 0, stage = 0;
   for (int64_t row0 = (int64_t)blockIdx.x * groups; row0 < a.rows; row0 += step, turn ^= 1) {
     const int64_t row = row0 + threadIdx.x / lanes;
@@ -605,16 +617,13 @@ __global__ void __launch_bounds__(grad_threads(kLanes, N * V, kShift)) k_norm_gr
       for (int i = 0; i < M / C::kVecs; ++i) {
         const int q = first / C::kVecs + i;
         Two w[C::kTwos], h[C::kTwos], g[C::kTwos];
-        if constexpr (kSlots)
-          Slots::get(slots, q, w);
-        else if constexpr (!kKeep)
-          load_weights<kShift, V>(a.w, a.w_type, c0 + q * C::kVecs * hop, hop, a.width, w);
+        weights(q, w);
         widen<T, V>(hv + i * C::kVecs, h);
         widen<T, V>(gv + i * C::kVecs, g);
 #pragma unroll
         for (int k = 0; k < C::kTwos; ++k) {
           squares = fma2(h[k], h[k], squares);
-          inner = fma2(mul2(g[k], kKeep ? kept[kKeep ? q : 0][k] : w[k]), h[k], inner);
+          inner = fma2(mul2(g[k], w[k]), h[k], inner);
         }
       }
     }
@@ -628,23 +637,21 @@ __global__ void __launch_bounds__(grad_threads(kLanes, N * V, kShift)) k_norm_gr
       for (int first = 0; first < N; first += M) {
         if constexpr (kAgain) {
           get_hg(first);
-          if (a.dh) get_e(first);
+          if constexpr (kStages == 0)
+            if (a.dh) get_e(first);
           clip(first);
         }
 #pragma unroll
         for (int i = 0; i < M / C::kVecs; ++i) {
           const int q = first / C::kVecs + i;
           Two w[C::kTwos], h[C::kTwos], g[C::kTwos], d[C::kTwos];
-          if constexpr (kSlots)
-            Slots::get(slots, q, w);
-          else if constexpr (!kKeep)
-            load_weights<kShift, V>(a.w, a.w_type, c0 + q * C::kVecs * hop, hop, a.width, w);
+          weights(q, w);
           widen<T, V>(hv + i * C::kVecs, h);
           widen<T, V>(gv + i * C::kVecs, g);
 #pragma unroll
           for (int k = 0; k < C::kTwos; ++k) {
             const Two u = mul2(h[k], scale2);
-            d[k] = mul2(fma2(u, mean2, mul2(g[k], kKeep ? kept[kKeep ? q : 0][k] : w[k])), scale2);
+            d[k] = mul2(fma2(u, mean2, mul2(g[k], w[k])), scale2);
             dw[q][k] = fma2(g[k], u, dw[q][k]);
           }
           if (a.dh) {
@@ -925,7 +932,7 @@ int ebc_norm_grad(ebc_ctx* ctx, const void* d_dy, int64_t ld_dy, const void* d_h
         // stages: with two CTAs of 256 threads an SM that is 98 KB in flight (8192 x
         // 4096 bf16 with dh 45.0 us; 45.5 with two stages, 47.8 with four), and with
         // one of 448 threads 86 KB (8192 x 7168: 73.4; 80.9, 72.7).
-        constexpr int kStages = L::kLanes || L::V < 8 || sizeof(typename L::T) > 2 ? 0 : L::N == 2 ? 3 : L::kShift ? 0 : 2;
+        constexpr int kStages = L::kLanes || L::V < 8 || sizeof(typename L::T) > 2 ? 0 : L::N == 2 ? 3 : 2;
         const auto kernel = k_norm_grad<typename L::T, L::V, L::N, L::kLanes, kStages, L::kShift>;
         // Rows that take less than 256 threads: several in a CTA.
         const int lanes = L::kLanes ? L::kLanes : threads, groups = L::kLanes || threads <= 128 ? kRowThreads / lanes : 1;
@@ -944,7 +951,7 @@ int ebc_norm_grad(ebc_ctx* ctx, const void* d_dy, int64_t ld_dy, const void* d_h
         }
         if constexpr (kStages > 0) {
           const size_t ring = Ring<typename L::T, L::V, L::N, kStages>::bytes(threads) +
-                              (L::kShift ? 4 * L::N * L::V * threads : 0);
+                              (L::kShift && L::N == 2 ? 4 * L::N * L::V * threads : 0);
           constexpr int kMost = 226 * 1024;   // of an SM's 228 KB (each CTA has 1 KB of its own)
           if (ring > smem) smem = ring;
           if (each * (int64_t)(smem + 2048) > kMost) each = kMost / (int64_t)(smem + 2048);
