@@ -496,7 +496,7 @@ struct Ring {
 // (without: 73 us of 8192 x 4096 bf16 with dh, so: 44, 6.1 TB/s; 16384 rows 82, 6.6).
 // Not so for fp32, whose vectors are wider than such a copy (137 us with, 93
 // without: 5.8 TB/s).  Weights stay in registers: read again each row, 2048 x 16384
-// bf16 took 74 us, so 48 (5.6 TB/s).  Rows off a boundary: 8192 x 4095 bf16 70 us,
+// bf16 took 74 us, so 48 (5.6 TB/s).  Rows off a boundary: 8192 x 4095 bf16 68 us,
 // 2048 x 16377 66, 8192 x 4095 fp32 103; one value an access, issue and latency (1531
 // x 1001 fp32 11.4 us).
 
@@ -509,9 +509,10 @@ __global__ void __launch_bounds__(grad_threads(kLanes, N * V, kShift)) k_norm_gr
   using R = Ring<T, V, N, kStages>;
   using C = Chunk<V>;
   constexpr int kChunks = N / C::kVecs;
-  // More values than registers hold beside dw: they are read twice, a few at a time,
-  // the second time out of shared memory, or mostly of the L1 cache.
-  constexpr bool kAgain = N * V > 16;
+  // More values than registers hold beside dw and the weights: they are read twice, a
+  // few at a time, the second time out of shared memory, or mostly of the L1 cache.
+  // (Where they fit, 8192 x 4096 bf16 takes 44 us, read twice 49.)
+  constexpr bool kAgain = N * V > 16 || (kShift && kStages > 0);
   constexpr int M = kAgain ? 8 / V : N;
   static_assert(!kAgain || kLanes == 0);   // (a barrier between the two)
   __shared__ float part[2][2][kMaxThreads / 32];
@@ -543,12 +544,12 @@ __global__ void __launch_bounds__(grad_threads(kLanes, N * V, kShift)) k_norm_gr
     }
   };
   for (int i = 0; i < kStages - 1; ++i) request((int64_t)blockIdx.x * groups + i * step, i);
-  // the weights stay in registers, or in shared memory behind the rows to come
-  constexpr bool kSlots = kShift && (N * V <= 16 || kStages == 0), kKeep = !kSlots && (N * V <= 16 || V == 8);
+  // the weights stay in registers, or in shared memory where no rows to come are
+  constexpr bool kSlots = kShift && kStages == 0, kKeep = !kSlots && (N * V <= 16 || V == 8);
   ulonglong2* slots = nullptr;
   if constexpr (kSlots) {
     extern __shared__ uint4 ring[];
-    slots = reinterpret_cast<ulonglong2*>(reinterpret_cast<uint8_t*>(ring) + R::bytes(blockDim.x));
+    slots = reinterpret_cast<ulonglong2*>(ring);
   }
   Two dw[kChunks][C::kTwos], kept[kKeep ? kChunks : 1][C::kTwos];
 #pragma unroll
@@ -950,8 +951,7 @@ int ebc_norm_grad(ebc_ctx* ctx, const void* d_dy, int64_t ld_dy, const void* d_h
           if (e != cudaSuccess) return e;
         }
         if constexpr (kStages > 0) {
-          const size_t ring = Ring<typename L::T, L::V, L::N, kStages>::bytes(threads) +
-                              (L::kShift && L::N == 2 ? 4 * L::N * L::V * threads : 0);
+          const size_t ring = Ring<typename L::T, L::V, L::N, kStages>::bytes(threads);
           constexpr int kMost = 226 * 1024;   // of an SM's 228 KB (each CTA has 1 KB of its own)
           if (ring > smem) smem = ring;
           if (each * (int64_t)(smem + 2048) > kMost) each = kMost / (int64_t)(smem + 2048);
