@@ -50,7 +50,7 @@ template <int N>
 struct Room {
   union {
     float c[32 * N + 32];
-    double d[32 * N];
+    int64_t k[32 * N];
   };
   // the candidates (a value and its expert each), then the best of them in their
   // order, and one that nobody reads
@@ -65,8 +65,14 @@ struct Room {
 // The sum of a softmax's exponentials.
 template <typename T>
 __device__ __noinline__ double exact_total(const T* row, int E, float most, int lane) {
-  double sum = 0.0;
-  for (int e = lane; e < E; e += 32) sum += exp((double)to_f32(row[e]) - (double)most);
+  double sum = 0.0, last = 0.0;
+  float l_last = CUDART_NAN_F;   // (like nothing)
+  for (int e = lane; e < E; e += 32) {
+    const float l = to_f32(row[e]);
+    if (l != l_last) last = exp((double)l - (double)most);
+    l_last = l;
+    sum += last;
+  }
   return warp_sum(sum);
 }
 // The choice's value of an expert.
@@ -75,6 +81,22 @@ __device__ __noinline__ double exact_value(const RouteArgs& a, const T* row, int
   const double l = (double)to_f32(row[e]);
   return (a.sigmoid ? 1.0 / (1.0 + exp(-l)) : exp(l - (double)most) / total) + (a.bias ? (double)a.bias[e] : 0.0);
 }
+
+// Numbers in their order as integers, NaN the largest: this chip has few units for
+// 64-bit floating point, and its comparisons are of them (8192 x 256 with a bias 11.6
+// -> 11.0 us, rows of equal scores 277 -> 49).
+__device__ __forceinline__ int64_t key_of(double v) {
+  const int64_t bits = __double_as_longlong(v), low = 0x7fffffffffffffffll;
+  if ((bits & low) == 0) return 0;   // (both zeros)
+  return (bits & low) > 0x7ff0000000000000ll ? low : bits ^ ((bits >> 63) & low);
+}
+__device__ __forceinline__ int64_t key_of(float v) {
+  const int32_t bits = __float_as_int(v), low = 0x7fffffff;
+  if ((bits & low) == 0) return 0;
+  return (bits & low) > 0x7f800000 ? low : bits ^ ((bits >> 31) & low);
+}
+__device__ __forceinline__ double of_key(int64_t k) { return __longlong_as_double(k ^ ((k >> 63) & 0x7fffffffffffffffll)); }
+constexpr int64_t kNone = -0x7ff0000000000001ll;   // of -infinity: below any other
 
 // The whole choice in 64 bits, for rows with a NaN and for ties of more values
 // than a warp has lanes: the same steps, written to be short.  A NaN is above
@@ -85,62 +107,66 @@ __device__ __noinline__ void choose_exactly(const RouteArgs& a, Room<N>& room, c
   const int size = a.E / a.groups;
   const double total = scored && !a.sigmoid ? exact_total(row, a.E, most, lane) : 1.0;
   __syncwarp();
+  // (a value like the lane's one before is not computed again: most where rows tie)
+  float l_last = 0.f, b_last = 0.f;
+  int64_t last = kNone;
+  bool any = false;
   for (int e = lane; e < a.E; e += 32) {
-    const float l = to_f32(row[e]);
-    room.d[e] = l == -CUDART_INF_F || (a.bias && a.bias[e] == -CUDART_INF_F) ? -CUDART_INF
-                : scored ? exact_value(a, row, e, most, total)
-                         : (double)l;
+    const float l = to_f32(row[e]), b = a.bias ? a.bias[e] : 0.f;
+    if (scored && !(any && l == l_last && b == b_last)) {
+      last = key_of(exact_value(a, row, e, most, total));
+      l_last = l;
+      b_last = b;
+      any = true;
+    }
+    room.k[e] = l == -CUDART_INF_F || b == -CUDART_INF_F ? kNone : scored ? last : key_of(l);
   }
   __syncwarp();
-  // x is better than y: larger, or a NaN
-  auto better = [](double x, double y) { return x > y || (x != x && y == y); };
   unsigned kept = kAll;
   if (a.groups > 1) {
-    double score = -CUDART_INF;
+    int64_t score = kNone;
     if (lane < a.groups) {
-      double first = -CUDART_INF, second = -CUDART_INF;
+      int64_t first = kNone, second = kNone;
       for (int i = 0; i < size; ++i) {
-        const double c = room.d[lane * size + i];
-        if (better(c, first)) {
-          second = first;
-          first = c;
-        } else if (better(c, second)) {
-          second = c;
-        }
+        const int64_t c = room.k[lane * size + i];
+        second = c > first ? first : c > second ? c : second;
+        first = c > first ? c : first;
       }
-      score = a.sums && second != -CUDART_INF ? first + second : first;
+      score = a.sums && second != kNone ? key_of(of_key(first) + of_key(second)) : first;
     }
     int rank = 0;
     for (int g = 0; g < a.groups; ++g) {
-      const double s = __shfl_sync(kAll, score, g);
-      rank += better(s, score) || (!better(score, s) && g < lane);
+      const int64_t s = __shfl_sync(kAll, score, g);
+      rank += s > score || (s == score && g < lane);
     }
     kept = __ballot_sync(kAll, lane < a.groups && rank < a.keep);
+    for (int e = lane; e < a.E; e += 32)
+      if (!(kept >> (e / size) & 1))
+        room.k[e] = kNone;
+      else if (scored && !a.bias && room.k[e] != kNone)   // without a bias it is the logits that are compared
+        room.k[e] = key_of(to_f32(row[e]));
+    __syncwarp();
   }
   for (int r = 0; r < a.top; ++r) {
-    double best = -CUDART_INF;
+    int64_t best = kNone;
     int at = INT32_MAX;
-    for (int e = lane; e < a.E; e += 32) {
-      if (a.groups > 1 && !(kept >> (e / size) & 1)) continue;
-      // without a bias it is the logits that are compared
-      const double c = room.d[e], v = c == -CUDART_INF || a.bias ? c : (double)to_f32(row[e]);
-      if (better(v, best)) {
-        best = v;
+    for (int e = lane; e < a.E; e += 32)
+      if (room.k[e] > best) {
+        best = room.k[e];
         at = e;
       }
-    }
 #pragma unroll 1
     for (int off = 16; off > 0; off >>= 1) {
-      const double v = __shfl_xor_sync(kAll, best, off);
+      const int64_t v = __shfl_xor_sync(kAll, best, off);
       const int o = __shfl_xor_sync(kAll, at, off);
-      if (better(v, best) || (!better(best, v) && o < at)) {
+      if (v > best || (v == best && o < at)) {
         best = v;
         at = o;
       }
     }
     if (lane == 0) {
       room.put(r, 0.f, at == INT32_MAX ? -1 : at);
-      if (at != INT32_MAX) room.d[at] = -CUDART_INF;
+      if (at != INT32_MAX) room.k[at] = kNone;
     }
     __syncwarp();
   }
@@ -203,22 +229,23 @@ __device__ __noinline__ int settle_groups(const RouteArgs& a, Room<N>& room, con
                                           bool near, float score, int log2, int lane) {
   const double total = a.sigmoid ? 1.0 : exact_total(row, a.E, most, lane);
   const int e = lane < found ? room.id(lane) : 0, g = lane >> log2;
-  const double value = exact_value(a, row, e, most, total);
+  const int64_t value = key_of(exact_value(a, row, e, most, total));
   const int eg = (int)((uint32_t)e * a.inverse >> 20);
-  double first = -CUDART_INF, second = -CUDART_INF;
+  int64_t first = kNone, second = kNone;
 #pragma unroll 1
   for (int i = 0; i < found; ++i) {
-    const double v = __shfl_sync(kAll, value, i);
+    const int64_t v = __shfl_sync(kAll, value, i);
     if (__shfl_sync(kAll, eg, i) == g) {
-      second = fmax(second, fmin(first, v));
-      first = fmax(first, v);
+      second = v > first ? first : v > second ? v : second;
+      first = v > first ? v : first;
     }
   }
-  const double sure = !near ? (double)score : a.sums && second > -CUDART_INF ? first + second : first;
+  const int64_t sure = !near ? key_of((double)score)
+                       : a.sums && second > kNone ? key_of(of_key(first) + of_key(second)) : first;
   int rank = 0;
 #pragma unroll 1
   for (int i = 0; i < a.groups; ++i) {
-    const double o = __shfl_sync(kAll, sure, i << log2);
+    const int64_t o = __shfl_sync(kAll, sure, i << log2);
     rank += o > sure || (o == sure && i < g);
   }
   return rank;
@@ -230,11 +257,11 @@ __device__ __noinline__ void settle_order(const RouteArgs& a, Room<N>& room, con
                                           int lane) {
   const double total = a.sigmoid ? 1.0 : exact_total(row, a.E, most, lane);
   const int e = lane < found ? room.id(lane) : -1;
-  const double value = e >= 0 ? exact_value(a, row, e, most, total) : -CUDART_INF;
+  const int64_t value = e >= 0 ? key_of(exact_value(a, row, e, most, total)) : kNone;
   int rank = 0;
 #pragma unroll 1
   for (int i = 0; i < found; ++i) {
-    const double u = __shfl_sync(kAll, value, i);
+    const int64_t u = __shfl_sync(kAll, value, i);
     const int n = __shfl_sync(kAll, e, i);
     rank += u > value || (u == value && n < e);
   }
@@ -260,8 +287,8 @@ __device__ __noinline__ void settle_order(const RouteArgs& a, Room<N>& room, con
 // a lane each; its whole row so took 30).
 //
 // Bound by issue: some 600 instructions a token, 300 more for the scores of a
-// bias, 350 more for groups.  8192 tokens x 256 experts, 8 chosen: 7.4 us by the
-// logits, 11.6 with a bias, 14.4 with both; x 64: 6.0.  A search a choice took 15.8,
+// bias, 350 more for groups.  8192 tokens x 256 experts, 8 chosen: 7.2 us by the
+// logits, 11.0 with a bias, 13.7 with both; x 64: 5.7.  A search a choice took 15.8,
 // 46 and 58.  A token alone takes 2.5 to 4 us of latency.
 template <typename T, int N, int kWarps>
 __global__ void __launch_bounds__(32 * kWarps, N <= 8 ? 8 : 4) k_moe_route(const __grid_constant__ RouteArgs a) {
@@ -418,7 +445,7 @@ __global__ void __launch_bounds__(32 * kWarps, N <= 8 ? 8 : 4) k_moe_route(const
       if (found > 32 && a.bias) {
         // many choices, or few lanes with what may be chosen: as many of the values
         // themselves, equal ones of a lane once (8 of two groups of 32: 369 -> 16 us of
-        // 8192 tokens, 24 of 256: 818 -> 24; what was left to choose_exactly)
+        // 8192 tokens, 24 of 256: 818 -> 24, in choose_exactly as it then was)
         left = top1;
 #pragma unroll 1
         for (int r = 0; r < a.top; ++r) {

@@ -196,6 +196,35 @@ def test_ties_go_to_the_lower_expert(ex, kind, bias):
 
 
 @pytest.mark.parametrize("kind", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("group_top", [1, 2])
+def test_rows_of_one_score(ex, kind, group_top):
+    """Every value ties, among them scores that are zero in 32 bits, rows but for one expert, and groups with one
+    expert left: the lower expert and the lower group, and two scores of a group are more than one."""
+    inf = float("inf")
+    l = torch.zeros(10, 256, device="cuda")
+    l[1] = -200.0
+    l[2], l[2, 100] = -200.0, -199.0
+    l[3, 200] = 1.0
+    l[4, :31] = -inf
+    l[5] = -200.0
+    l[5, :31] = -inf
+    l[6] = torch.finfo(torch.float32).min
+    l[7, 1::2] = torch.tensor(1.0).nextafter(torch.tensor(0.0)) * 1e-30
+    l[8, 3:] = -inf
+    l[9] = 90.0
+    for bias in (None, torch.zeros(256, device="cuda"), torch.full((256,), 0.25, device="cuda")):
+        for top in (1, 8, 32):
+            for dtype in (torch.float32, torch.bfloat16):
+                check(ex, l[[0, 3, 4, 8, 9]].to(dtype), top, kind=kind, bias=bias)
+                check(ex, l[[0, 3, 4, 8, 9]].to(dtype), top, kind=kind, bias=bias, groups=8, keep=4, group_top=group_top)
+            named = dict(bias=None if bias is None else bias.cpu().numpy(), kind=kind)
+            for how in (dict(), dict(groups=8, keep=4, group_top=group_top)):
+                ids, _ = ex.route(l, top, kind, bias, how.get("groups", 1), how.get("keep"), how.get("group_top", 1))
+                want = defined(l.cpu().numpy(), top, **named, **how)[0]
+                assert np.array_equal(ids.cpu().numpy(), want)
+
+
+@pytest.mark.parametrize("kind", ["softmax", "sigmoid"])
 def test_masks_that_leave_little_or_nothing(ex, kind):
     inf = float("inf")
     l = torch.full((6, 40), -inf, device="cuda")
