@@ -498,7 +498,7 @@ struct Ring {
 // without: 5.8 TB/s).  Weights stay in registers: read again each row, 2048 x 16384
 // bf16 took 74 us, so 48 (5.6 TB/s).  Rows off a boundary: 8192 x 4095 bf16 68 us,
 // 2048 x 16377 66, 8192 x 4095 fp32 103; one value an access, issue and latency (1531
-// x 1001 fp32 11.4 us).
+// x 1001 fp32 9.4 us).
 
 // (Rows off a boundary take a warp more; two CTAs an SM still.)
 constexpr int grad_threads(int lanes, int values, bool shift) {
@@ -920,10 +920,10 @@ int ebc_norm_grad(ebc_ctx* ctx, const void* d_dy, int64_t ld_dy, const void* d_h
     if (vals > vals_s) vals = vals_s;
     // Rows off the boundary in whole vectors where it takes less time: very wide ones,
     // and many of more than 512 values (us with dh, single values / so, bf16: 600 x
-    // 1001 7.9 / 8.6, 1024 x 1001 10.6 / 8.8, 128 x 4095 6.5 / 9.8, 512 x 4095 14.2 /
-    // 13.2, 64 x 8101 27.8 / 11.1, 16384 x 101 12.7 / 21.9; fp32: 2048 x 1001 13.5 /
-    // 12.7, 512 x 4095 13.9 / 15.2, 8192 x 4095 132 / 103, 64 x 8101 22.6 / 11.8).
-    const bool many = rows * width >= (b == 2 ? 3 << 18 : 1 << 22);
+    // 1001 7.9 / 8.4, 1531 x 1001 11.0 / 11.0, 8192 x 1001 48 / 23, 256 x 4095 8.8 / 10.6,
+    // 1024 x 4095 25.5 / 17.5, 64 x 8101 27.8 / 11.1, 16384 x 101 11.8 / 21.9; fp32: 2048 x
+    // 1001 11.5 / 12.7, 8192 x 1001 33 / 32, 2048 x 4095 38.6 / 34.0, 64 x 8101 22.6 / 11.8).
+    const bool many = rows * width >= (b == 2 ? 3 << 19 : 1 << 22);
     const bool shift = vals < 8 && at.shifts(width) && (width > 4096 || (width > 512 && many));
     e = with_type_of(type, [&](auto one) {
       using T = decltype(one);
@@ -938,9 +938,14 @@ int ebc_norm_grad(ebc_ctx* ctx, const void* d_dy, int64_t ld_dy, const void* d_h
         // Rows that take less than 256 threads: several in a CTA.
         const int lanes = L::kLanes ? L::kLanes : threads, groups = L::kLanes || threads <= 128 ? kRowThreads / lanes : 1;
         threads = groups * lanes;
-        // All CTAs at once, as many on each SM: as registers (at most 128 a thread),
-        // shared memory and the scratch's rows allow.
-        constexpr int kFit = L::N * L::V <= 8 ? 1024 : L::kLanes ? kFewThreads : grad_threads(0, L::N * L::V, L::kShift);
+        // All CTAs at once, as many on each SM as registers (16-bit vectors 63, fp32 ones
+        // 68, pairs 74, single values 101), shared memory and the scratch's rows allow (in
+        // two turns 1531 x 1001 fp32 with dh took 11.3 us, so 9.4; 131072 x 63 57 and 43).
+        constexpr bool kHalf = sizeof(typename L::T) == 2;
+        constexpr int kFit = L::N * L::V > 8 ? (L::kLanes ? kFewThreads : grad_threads(0, L::N * L::V, L::kShift))
+                             : L::V == 1 && (kHalf || !L::kLanes) ? 512
+                             : L::V == 8 && kHalf                 ? 1024
+                                                                  : 768;
         int64_t each = kFit / threads < 1 ? 1 : kFit / threads;
         // where the groups' sums are added up
         size_t smem = groups > 1 ? (size_t)4 * L::N * L::V * lanes : 0;
