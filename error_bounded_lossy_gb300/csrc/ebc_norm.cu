@@ -265,7 +265,7 @@ struct NormArgs {
 // and once to 8 bits.
 // Every input is read once and every output written once; bound by bandwidth:
 // 8192 x 4096 bf16 with a residual 42.5 us (6.3 TB/s), 16384 rows 81 us (6.6);
-// to 8 bits 41.5 and 78, both 48 and 93; off a boundary, x 4095, 51 us.  A row on
+// to 8 bits 41.7 and 78, both 48 and 93; off a boundary, x 4095, 53 us.  A row on
 // fewer threads with more values each takes fewer joins: 16384 x 1024 25.1 us with
 // eight values a thread, 22.1 with sixteen.
 // An SM has 1024 threads of 16 values: left to take 68 registers the first two took
