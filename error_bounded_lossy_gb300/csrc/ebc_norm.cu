@@ -811,7 +811,8 @@ struct Places {
   uintptr_t all = 0, first = 0, stride = 0;
   bool alike = true, any = false;
   int elem;
-  explicit Places(int elem) : elem(elem) {}
+  // (a row's last vector must not reach into what is beside it)
+  Places(int elem, int64_t width) : all((uintptr_t)(width * elem)), elem(elem) {}
   void add(const void* p, int64_t ld) {
     if (!p) return;
     const uintptr_t a = (uintptr_t)p, s = (uintptr_t)(ld * elem), unit = (uintptr_t)(8 * elem);
@@ -853,7 +854,7 @@ int ebc_norm(ebc_ctx* ctx, const void* d_x, int64_t ld_x, const void* d_residual
   if (rc || rows == 0) return rc;
   const NormArgs a{d_x, d_residual, d_weight, d_y, d_h, d_codes, d_scales, ld_x, ld_residual, rows,
                    (int)width, weight_type, eps};
-  Places at(b);
+  Places at(b, width);
   at.add(d_x, ld_x);
   at.add(d_residual, ld_residual);
   at.add(d_y, width);
@@ -909,7 +910,7 @@ int ebc_norm_grad(ebc_ctx* ctx, const void* d_dy, int64_t ld_dy, const void* d_h
              0, eps};
   cudaError_t e = cudaSuccess;
   if (rows > 0) {
-    Places at(b);
+    Places at(b, width);
     at.add(d_dy, ld_dy);
     at.add(d_h, ld_h);
     at.add(d_dh, ld_dh);

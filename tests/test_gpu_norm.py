@@ -128,6 +128,26 @@ def check_backward(dy, h, w, dh, dx, dw, eps=EPS):
 
 
 @pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("width,pad", [(511, 1), (1, 7), (7, 1), (30, 2), (33, 7), (509, 3), (1001, 7), (1001, 1), (4095, 1), (8191, 1), (8195, 5), (16383, 1)])
+def test_what_is_beside_the_rows_takes_no_part(ex, width, pad, dtype):
+    """Aligned rows of a wider buffer whose other values are NaN, of a width that is no multiple of a vector."""
+    rows = 20
+    t = list(batch(rows, width, dtype, width))
+    w = t.pop(2)
+    wide = [torch.full((rows, width + pad), float("nan"), device="cuda", dtype=dtype) for _ in t]
+    for a, b in zip(wide, t):
+        a[:, :width] = b
+    x, r, dy, dh = (a[:, :width] for a in wide)
+    check_forward(x, None, w, *ex.norm(x, w))
+    check_forward(x, r, w, *ex.norm(x, w, r))
+    for residual in (None, r):
+        check_8_bit(ex, ex.norm_mx8(x, w, residual)[0], x, residual, w)
+        check_8_bit(ex, ex.norm_mx8(x, w, residual, wide=True)[0], x, residual, w)
+    check_backward(dy, x, w, None, *ex.norm_grad(dy, x, w))
+    check_backward(dy, x, w, dh, *ex.norm_grad(dy, x, w, dh))
+
+
+@pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("rows,width", SIZES)
 def test_the_gradients(ex, rows, width, dtype):
     h, _, w, dy, dh = batch(rows, width, dtype, rows + width + 2)
