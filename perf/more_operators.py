@@ -333,8 +333,9 @@ def _run_own(s):
     q, _, h = ex.norm_mx8(s["x"], s["gain"], s["r"], EPS)
     ids, weights = ex.route(s["logits"], s["top"], s["score"], s["b"], s["groups"], s["keep"], s["best"], s["renorm"], s["scale"])
     plan = ex.plan(ids, s["experts"])
-    ys = ex.product(ex.dispatch(q, plan), w, plan.offsets, kind)
-    return {"ids": ids, "h": h, "y": ex.combine(ys, weights, plan)}
+    # (in 32 bits until the weighted sum is rounded)
+    ys = ex.product(ex.dispatch(q, plan), w, plan.offsets, torch.float32)
+    return {"ids": ids, "h": h, "y": ex.combine(ys, weights, plan).to(kind)}
 
 
 def run(state):
