@@ -223,7 +223,8 @@ __device__ __forceinline__ int gather(Room<N>& room, uint32_t bits, const float 
 }
 
 // The groups' ranks from sums in 64 bits of the `near` ones' largest values, which
-// are among the `found` of room.id, and from the others' as they are.
+// are among the `found` of room.id, and from the others' as they are (score: half of
+// a sum).
 template <typename T, int N>
 __device__ __noinline__ int settle_groups(const RouteArgs& a, Room<N>& room, const T* row, float most, int found,
                                           bool near, float score, int log2, int lane) {
@@ -240,7 +241,7 @@ __device__ __noinline__ int settle_groups(const RouteArgs& a, Room<N>& room, con
       first = v > first ? v : first;
     }
   }
-  const int64_t sure = !near ? key_of((double)score)
+  const int64_t sure = !near ? key_of(a.sums ? 2. * (double)score : (double)score)
                        : a.sums && second > kNone ? key_of(of_key(first) + of_key(second)) : first;
   int rank = 0;
 #pragma unroll 1
@@ -380,7 +381,9 @@ __global__ void __launch_bounds__(32 * kWarps, N <= 8 ? 8 : 4) k_moe_route(const
         second = fmaxf(fmaxf(second, s), fminf(first, f));
         first = fmaxf(first, f);
       }
-      const float score = a.sums && second > -CUDART_INF_F ? first + second : first;
+      // (half of the sum, which is exact but for numbers far below any `err`: two finite
+      // values may add up to more than fp32 holds)
+      const float score = !a.sums ? first : second > -CUDART_INF_F ? .5f * first + .5f * second : .5f * first;
       int rank = 0;
       for (int i = 0; i < a.groups; ++i) {
         const float s = __shfl_sync(kAll, score, i << log2);
@@ -390,9 +393,10 @@ __global__ void __launch_bounds__(32 * kWarps, N <= 8 ? 8 : 4) k_moe_route(const
       if (scored && a.keep < a.groups) {
         const unsigned in = __ballot_sync(kAll, one && rank == a.keep - 1), out = __ballot_sync(kAll, one && rank == a.keep);
         const float vi = __shfl_sync(kAll, score, __ffs(in) - 1), vo = __shfl_sync(kAll, score, __ffs(out) - 1);
-        if (vo > -CUDART_INF_F && vi - vo <= 6.f * err) {   // (two values and a rounding each)
+        const float reach = a.sums ? 3.f * err : 6.f * err;   // (two values and a rounding each, or half of them)
+        if (vo > -CUDART_INF_F && vi - vo <= reach) {
           // what decides: the largest of the groups that are that near
-          const bool near = score <= vi + 6.f * err && score >= vo - 6.f * err;
+          const bool near = score <= vi + reach && score >= vo - reach;
           const float from = near ? (a.sums && second > -CUDART_INF_F ? second : first) - 2.f * err : CUDART_INF_F;
           uint32_t bits = 0;
 #pragma unroll
