@@ -452,6 +452,12 @@ double real(PyObject* o) {
   return v;
 }
 
+bool truth(PyObject* o) {
+  const int v = PyObject_IsTrue(o);
+  if (v < 0) throw Raised{};
+  return v;
+}
+
 int small(PyObject* o) {   // an int argument of the C call, which refuses what is out of its range
   const int64_t v = integer(o);
   return (int)std::max<int64_t>(INT32_MIN, std::min<int64_t>(v, INT32_MAX));
@@ -478,7 +484,7 @@ PyObject* py_route(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const Parts all{w.empty({2 * pad16(4 * l.n * top)}, at::kByte)};
     at::Tensor ids = all.take(0, {l.n, top}, at::kInt), weights = all.take(pad16(4 * l.n * top), {l.n, top}, at::kFloat);
     checked(ebc_moe_route(w.ctx, l.t.data_ptr(), l.ld, l.type, l.n, (int)std::min<int64_t>(l.width, INT32_MAX), top,
-                          small(a[4]), bias, small(a[6]), small(a[7]), small(a[8]), PyObject_IsTrue(a[9]),
+                          small(a[4]), bias, small(a[6]), small(a[7]), small(a[8]), truth(a[9]),
                           (float)real(a[10]), (int32_t*)ids.data_ptr(), (float*)weights.data_ptr(), w.stream()),
             "ebc_moe_route");
     return tuple({ids, weights});
@@ -503,7 +509,7 @@ PyObject* py_route_grad(PyObject*, PyObject* const* a, Py_ssize_t n) {
     checked(ebc_moe_route_grad(w.ctx, (const float*)g.data_ptr(), l.t.data_ptr(), l.ld, l.type, l.n,
                                (int)std::min<int64_t>(l.width, INT32_MAX),
                                (int)std::min<int64_t>(g.size(1), INT32_MAX), (const int32_t*)ids.data_ptr(),
-                               small(a[5]), PyObject_IsTrue(a[6]), (float)real(a[7]), d.data_ptr(), w.stream()),
+                               small(a[5]), truth(a[6]), (float)real(a[7]), d.data_ptr(), w.stream()),
             "ebc_moe_route_grad");
     return wrap(d);
   });
@@ -570,7 +576,7 @@ PyObject* py_norm_mx8(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const Rows x = rows(w, a[2]);
     no_tangent(x.t);
     const at::Tensor& g = gain(w, a[3], x.width);
-    const bool more = a[4] != Py_None, wide = PyObject_IsTrue(a[6]);
+    const bool more = a[4] != Py_None, wide = truth(a[6]);
     const Rows r = more ? rows_like(w, a[4], x) : x;
     const int64_t each = pad32(x.n * x.width * (int64_t)x.t.element_size()), cb = x.n * code_bytes(8, x.width),
                   sb = pad32(x.n * EBC_MX8_SCALE_BYTES(x.width));
