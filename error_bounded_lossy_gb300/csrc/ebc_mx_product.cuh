@@ -72,15 +72,16 @@ struct Geom {
   static constexpr int kABytes = kM * kRowBytes;
   static constexpr int kBBytes = kBRows * kRowBytes;
   static constexpr int kScaleBytes = kWords * (1 + kScaleB) * kScaleTile; // per stage
-  // (256 rows a tile with 4 / 5 stages of codes: 329 / 320 us of 8192 x 8192, and
-  // more do not fit; 16 rows with 5 / 6 / 8 / 10: 12.9 / 12.6 / 13.1 / 13.5 us of a
-  // decode step)
+  // (4 bits: 256 rows a tile with 4 / 5 stages of codes 329 / 320 us of 8192 x 8192,
+  // and more do not fit; 16 rows with 5 / 6 / 8 / 10 12.9 / 12.6 / 13.1 / 13.5 us of a
+  // decode step.  8 bits take the same numbers, unmeasured: their scales are half as
+  // large, and six stages of 256 rows would fit.)
   static constexpr int kStages = kTN == 256 ? 5 : kTN == 64 ? 7 : 6;
   // A pair's scales have a ring of their own, a longer one: the second CTA's are
   // known to the first only some 3600 cycles after they were laid out (see
   // below).  The barriers on which stages are given back are as many, so that one
-  // instruction a stage gives back both.  8192 x 8192: 5 / 6 / 7 / 8 / 10 / 12 /
-  // 14 / 16 stages 483 / 426 / 396 / 360 / 342 / 328 / 325 / 322 us.
+  // instruction a stage gives back both.  8192 x 8192 in 4 bits: 5 / 6 / 7 / 8 / 10 /
+  // 12 / 14 / 16 stages 483 / 426 / 396 / 360 / 342 / 328 / 325 / 322 us.
   static constexpr int kScaleStages = kCtas == 2 ? 16 : kStages;
   static constexpr int kAcc = kTN == 256 ? 1 : 2;                         // accumulators
   static constexpr int kAccCols = kTN < 32 ? 32 : kTN;
@@ -537,7 +538,8 @@ __device__ __forceinline__ void product_begin(Shared<Geom<F, kTN, kCtas>>& sh) {
 // latency, from the first stage's arrival to the last result's store.  8 bits: one
 // expert, 16384 rows x 8192 x 8192: 680 us (3.2 PFLOP/s) at the board's power
 // limit, where the clock falls to 1.3 GHz and a stage takes 517 cycles of it (633 at
-// 2.07 GHz, with operands of zeros); 32 experts of 4096 x 4096: 203 us (2.7).
+// 2.07 GHz, with operands of zeros); 32 experts of 4096 x 4096: 203 us (2.7), of 2048 x
+// 2048: 66 (2.1), at 1.8 GHz, the accumulator's reading 3800 of some 12100 cycles a tile.
 template <typename F, int kTN, int kCtas>
 __device__ __forceinline__ void product_run(Shared<Geom<F, kTN, kCtas>>& sh, const CUtensorMap& wmap,
                                             const CUtensorMap& xmap, const Args& a) {

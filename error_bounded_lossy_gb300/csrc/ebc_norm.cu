@@ -262,14 +262,16 @@ struct NormArgs {
 
 // h = x + r, y = h / sqrt(mean(h^2) + eps) * w, in 32 bits: h is rounded once, to
 // be kept, and y is of the sum before that rounding, rounded once to its type
-// and once to 8 bits.
+// and once to 8 bits.  (A sum of squares past fp32's largest number gives a row of
+// zeros, as ebc.h says.)
 // Every input is read once and every output written once; bound by bandwidth:
 // 8192 x 4096 bf16 with a residual 42.5 us (6.3 TB/s), 16384 rows 81 us (6.6);
 // to 8 bits 41.7 and 78, both 48 and 93; off a boundary, x 4095, 53 us.  A row on
 // fewer threads with more values each takes fewer joins: 16384 x 1024 25.1 us with
 // eight values a thread, 22.1 with sixteen.
 // An SM has 1024 threads of 16 values: left to take 68 registers the first two took
-// 47.8 and 91 us.  Wide rows: 2048 x 16384 bf16 38.4 us (on 512 threads of 32 values
+// 47.8 and 91 us.  (Single 16-bit values of more than 4096 columns spill 84 bytes in
+// those 64, fp32 rows of 257 to 512 off a boundary 48.)  Wide rows: 2048 x 16384 bf16 38.4 us (on 512 threads of 32 values
 // 40.6), off a boundary 2731 x 12289 41.0 (45.5).
 // kAhead: without a residual there is room to load a row ahead (8192 x 4096 bf16 30.1
 // -> 24.8 us, x 4095 36.2 -> 27.2, 2048 x 16384 38.3 -> 26.1; in one kernel with the
@@ -498,7 +500,8 @@ struct Ring {
 // without: 5.8 TB/s).  Weights stay in registers: read again each row, 2048 x 16384
 // bf16 took 74 us, so 48 (5.6 TB/s).  Rows off a boundary: 8192 x 4095 bf16 68 us,
 // 2048 x 16377 66, 8192 x 4095 fp32 103; one value an access, issue and latency (1531
-// x 1001 fp32 9.4 us).
+// x 1001 fp32 9.4 us).  (Of 32 values a thread, single ones spill 72 to 80 bytes, rows
+// off a boundary 16 to 32.)
 
 // (Rows off a boundary take a warp more; two CTAs an SM still.)
 constexpr int grad_threads(int lanes, int values, bool shift) {
@@ -829,7 +832,9 @@ struct Places {
     return a < b ? a : b;
   }
   // Whether such rows can be taken in whole vectors all the same (with up to 7
-  // columns more, and a row's neighbours no nearer than a vector).
+  // columns more, and a row's neighbours no nearer than a vector).  Not so are rows
+  // of a padded buffer, whose outputs are dense and off by another distance: 8192 x
+  // 4095 bf16 of rows of 4096 take 173 us with a residual, of rows of 4095 53.
   bool shifts(int64_t width) const { return alike && width >= 8 && width + 7 <= EBC_MAX_NORM_WIDTH; }
 };
 

@@ -290,7 +290,11 @@ __device__ __noinline__ void settle_order(const RouteArgs& a, Room<N>& room, con
 // Bound by issue: some 600 instructions a token, 300 more for the scores of a
 // bias, 350 more for groups.  8192 tokens x 256 experts, 8 chosen: 7.2 us by the
 // logits, 11.0 with a bias, 13.7 with both; x 64: 5.7.  A search a choice took 15.8,
-// 46 and 58.  A token alone takes 2.5 to 4 us of latency.
+// 46 and 58.  A token alone takes 2.5 to 4 us of latency.  The registers of eight CTAs an
+// SM are 64, in which 65 to 256 experts spill 20 to 96 bytes; 257 to 512 have 128 (fp32
+// spills 36), more have 196 to 229 and eight warps an SM (8192 x 1024: 18.3, 34 and 41 us).
+// A finite mask in the bias (-1e9) makes `err` so large that every token goes to
+// choose_exactly: 118 us of 8192 x 256.
 template <typename T, int N, int kWarps>
 __global__ void __launch_bounds__(32 * kWarps, N <= 8 ? 8 : 4) k_moe_route(const __grid_constant__ RouteArgs a) {
   __shared__ Room<N> rooms[kWarps];

@@ -119,9 +119,11 @@ class Mx8:
 
 class Experts:
     """The expert-parallel, 4- and 8-bit, router and norm operators on one CUDA device.  Calls are
-    asynchronous on `stream` (None: the device's current stream), take no
-    scratch, and return new tensors of that stream; not thread safe, use one
-    per host thread.  A backward pass can be captured into a graph; as with
+    asynchronous on `stream` (None: the device's current stream) and return new
+    tensors of that stream (outputs of one call that are small, up to 64 KB, are
+    parts of one allocation; h of a norm without a residual is x itself).  They take no
+    scratch but norm_grad, which allocates up to 608 rows of fp32 for its call.  Not
+    thread safe, use one per host thread.  A backward pass can be captured into a graph; as with
     torch's own operations, outputs of eager passes over the same leaves are
     released before."""
 
@@ -180,7 +182,8 @@ class Experts:
 
     def norm(self, x, weight, residual=None, eps: float = 1e-6, stream=None):
         """(y, h): h = x + residual and y = h / sqrt(mean of h^2 over a row + eps) * weight, of x [..., width] and its
-        type.  y is of the sum before h is rounded; without a residual h is x.  weight [width] may be of another type."""
+        type.  y is of the sum before h is rounded; without a residual h is x itself.  weight [width] may be of another
+        type.  The mean is fp32's: a row whose squares add up past 3.4e38 has y = 0."""
         if stream is None:
             out = _calls.norm(self._h, self._index, x, weight, residual, eps)
             if out is not None:
@@ -234,8 +237,9 @@ class Experts:
         Scores are the softmax of a row or the sigmoid of each logit ("sigmoid").  bias (fp32 [n_experts]) is added to
         them for the choice alone.  With groups, experts are chosen from the keep_groups (None: all) groups whose best
         group_top (1 or 2) scores have the largest sum.  Weights are the scores without the bias, divided by their sum
-        over the choices with renormalize, times scale.  An expert whose logit or bias is -inf is not chosen; where a
-        token has too few, the rest are -1 (dropped, for plan) with weight 0."""
+        over the choices with renormalize, times scale.  An expert whose logit or bias is -inf is not chosen (a bias of
+        -1e9 is a value, with which the call takes ten times as long); where a token has too few, the rest are -1
+        (dropped, for plan) with weight 0."""
         kind = _SCORES.get(score)
         if kind is None:
             raise ValueError('score must be "softmax" or "sigmoid"')

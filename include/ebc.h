@@ -584,9 +584,12 @@ int ebc_moe_dispatch_mx(ebc_ctx* ctx, const uint8_t* d_codes, int64_t code_bytes
  * experts of the keep_groups best groups are chosen from.  d_ids[tokens][top] are
  * the experts of the largest c, the largest first, ties to the lower expert
  * (among groups: to the lower group); -1 (dropped, for ebc_moe_plan) where there
- * are not enough.  Two c are compared as they are, not as fp32 has them: where
- * that could not tell, they are computed in 64 bits.  A NaN counts as the largest
- * value.  Without a bias c orders as l does, and is compared so.
+ * are not enough.  Two c, and two groups' scores, are compared as 64-bit floating
+ * point has them: where fp32 could not tell, they are computed again.  (A sigmoid
+ * is 1 there for logits past 37, so with a bias, be it zero, those tie.)  A NaN
+ * counts as the largest value.  Without a bias c orders as l does, and is compared
+ * so.  A mask is -infinity; with a finite one in the bias (-1e9), which is a value,
+ * every token's c are compared in 64 bits, which takes ten times as long.
  *   d_weights[tokens][top], fp32: scale * s of the chosen, with `renormalize`
  * divided by the sum of s over the chosen; 0 for -1.
  * 1 <= top <= 32, 1 <= keep_groups <= groups <= 32, groups divides n_experts. */
@@ -610,7 +613,10 @@ int ebc_moe_route_grad(ebc_ctx* ctx, const float* d_dweights, const void* d_logi
 /* ---- The norm ahead of an expert layer ----
  *
  * h = x + residual (d_residual NULL: h = x), y = h / sqrt(mean(h^2) + eps) *
- * weight, in fp32 with y of the sum before h is rounded.  d_x and d_residual
+ * weight, in fp32 with y of the sum before h is rounded.  The squares' sum is fp32
+ * too: a row in which it is past 3.4e38 (one value above 1.8e19 is enough) has y = 0,
+ * and gradients to suit, and values below 1e-19 count with fewer bits (below 1e-23 as
+ * zeros), which shows where eps is not above their squares.  d_x and d_residual
  * [rows][width] of `type`, d_weight[width] of weight_type.  Written where not
  * NULL, dense: d_y and d_h of `type`; d_codes and d_scales, y in 8 bits.  One of
  * d_y and d_codes is asked for.  1 <= width <= EBC_MAX_NORM_WIDTH. */
@@ -621,7 +627,8 @@ int ebc_norm(ebc_ctx* ctx, const void* d_x, int64_t ld_x, const void* d_residual
 
 /* The gradients for the gradient d_dy of y, at the sum d_h that ebc_norm kept (x,
  * without a residual): d_dx[rows][width], that of x and of the residual alike,
- * with d_dh (NULL: none), what h has of other uses, added to it; and
+ * with d_dh (NULL: none), what h has of other uses, added to it (h is the kept one,
+ * rounded to `type`, where y was of the sum before that); and
  * d_dweight[width] of weight_type, its sums in fp32 and in the same order in every
  * run.  d_scratch: EBC_NORM_GRAD_SCRATCH(rows, width) bytes of the caller's,
  * 16-byte aligned, free again once the call's work is done; calls that may
